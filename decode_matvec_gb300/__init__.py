@@ -35,7 +35,8 @@ EXPORTED = [
     "qmoe_last_error", "qmoe_decode_dense", "rvq_decode_dense", "qmoe_set_phase_events",
     "qmoe_moe_layer_noalloc", "qmoe_pack_device_ws_size", "qmoe_pack_device", "rvq_pack_stages",
     "rvq_stage_allocation", "e8p_base_table", "e8p_pack", "e8p_nearest", "qmoe_offsets_compact",
-    "qmoe_moe_layer_kernels",
+    "qmoe_moe_layer_kernels", "kv4_block_tables", "qk_norm_rope", "kv4_append", "kv4_gather",
+    "kv4_attention_ws_size", "kv4_attention",
 ]
 
 
@@ -70,7 +71,13 @@ class CRvqSet(ctypes.Structure):
                 ("idx_base", ctypes.c_void_p), ("n_stages", ctypes.c_int), ("format", ctypes.c_int)]
 
 
+class CKv4Cache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
 _vp, _i, _sz, _d = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_double
+_i64, _f = ctypes.c_int64, ctypes.c_float
 _sig = {
     "qmoe_encode_dictionary": [_vp, _sz, _d, _vp, _vp],
     "qmoe_pack": [_vp, _i, _i, _i, _vp, _vp, _sz, _vp, _vp],
@@ -99,6 +106,12 @@ _sig = {
     "e8p_pack": [_vp, _i, _i, _vp, _vp, _vp, _vp],
     "e8p_nearest": [_vp, _sz, _vp],
     "qmoe_offsets_compact": [_vp, _i, _i, _vp, _vp],
+    "kv4_block_tables": [_vp, _vp, _i, _vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp],
+    "qk_norm_rope": [_vp, _i64, _i, _i, _i, _i, _vp, _vp, _f, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp],
+    "kv4_append": [_vp, _vp, _i64, _vp, _i64, _i, _vp, _vp],
+    "kv4_gather": [_vp, _vp, _i, _vp, _vp, _vp],
+    "kv4_attention_ws_size": [_i, _i, _i, _i, _i, _i, _i, _vp],
+    "kv4_attention": [_vp, _vp, _i, _i, _vp, _vp, _i, _vp, _i, _i, _i, _f, _i, _i, _vp, _vp, _sz, _vp],
 }
 for _name, _args in _sig.items():
     _f = getattr(_lib, _name)
@@ -477,3 +490,124 @@ def qmoe_set_phase_events(events) -> None:
         return
     arr = (ctypes.c_void_p * len(events))(*[int(e.cuda_event) for e in events])
     _check(_lib.qmoe_set_phase_events(arr, len(events)), "qmoe_set_phase_events")
+
+
+# ================================================================ attention over the 4-bit cache
+class Kv4Cache:
+    """One layer's keys and values in 4 bits: a handle on `pages`, a contiguous uint8 device tensor
+    [n_pages, page_bytes] (``kv4_cache`` in qmoe.h documents the layout)."""
+
+    def __init__(self, pages, page_size: int, n_kv_heads: int, head_dim: int):
+        import torch
+        nbytes = self.page_bytes(page_size, n_kv_heads, head_dim)
+        if pages.dtype != torch.uint8 or pages.dim() != 2 or pages.shape[1] != nbytes or not pages.is_contiguous():
+            raise ValueError(f"pages must be a contiguous uint8 tensor [n_pages, {nbytes}]")
+        self.pages, self.page_size, self.n_kv_heads, self.head_dim = pages, page_size, n_kv_heads, head_dim
+        self.n_pages = int(pages.shape[0])
+        self.c = CKv4Cache(_dptr(pages), self.n_pages, page_size, n_kv_heads, head_dim)
+        self.ref = ctypes.byref(self.c)
+
+    @staticmethod
+    def page_bytes(page_size: int, n_kv_heads: int, head_dim: int) -> int:
+        return n_kv_heads * page_size * (head_dim + 8)
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, device="cuda") -> "Kv4Cache":
+        import torch
+        pages = torch.zeros((n_pages, cls.page_bytes(page_size, n_kv_heads, head_dim)), dtype=torch.uint8, device=device)
+        return cls(pages, page_size, n_kv_heads, head_dim)
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _i32(t, n: int, name: str):
+    """Device pointer of a contiguous int32 tensor of at least n elements."""
+    _need(t.element_size() == 4 and t.is_contiguous() and t.numel() >= n, f"{name}: contiguous int32, {n} elements")
+    return t.data_ptr()
+
+
+def kv4_block_tables(cached, new_tokens, free_pages, n_free, page_size: int, table, q_start, kv_len, slots, positions,
+                     n_free_out, stream=None):
+    """Block tables and slot maps of a batch from its requests' lengths (all int32 device tensors): takes the
+    new pages from the stack free_pages[:n_free], writes their entries of table [B, max_blocks], and gives
+    q_start [B + 1], kv_len [B], and the slot and position of each new token."""
+    B, n = new_tokens.numel(), slots.numel()
+    _need(table.dim() == 2 and table.shape[0] == B, "table: [B, max_blocks]")
+    _check(_lib.kv4_block_tables(_i32(cached, B, "cached"), _i32(new_tokens, B, "new_tokens"), B,
+                                 _i32(free_pages, 0, "free_pages"), _i32(n_free, 1, "n_free"), page_size,
+                                 _i32(table, 0, "table"), table.shape[1], _i32(q_start, B + 1, "q_start"),
+                                 _i32(kv_len, B, "kv_len"), _i32(slots, n, "slots"), _i32(positions, n, "positions"),
+                                 n, _i32(n_free_out, 1, "n_free_out"), _stream_ptr(stream)), "kv4_block_tables")
+
+
+def qk_norm_rope(qkv, n_q_heads: int, n_kv_heads: int, head_dim: int, q_weight, k_weight, eps: float, cos_sin, positions,
+                 q_out, k_out=None, interleaved: bool = False, cache: Kv4Cache | None = None, slots=None, stream=None):
+    """Per-head RMS norms of queries and keys (weights None: no norm) and their rotation (cos_sin None: none) from
+    the rows of qkv [T, >= heads * head_dim] (bf16) into q_out [T, n_q_heads, head_dim] and k_out; with a cache,
+    keys and values are also written to it at slots."""
+    T = qkv.shape[0]
+    _need(qkv.dim() == 2 and qkv.element_size() == 2 and qkv.stride(1) == 1, "qkv: bf16 [T, heads * head_dim], rows contiguous")
+    _need(qkv.shape[1] >= (n_q_heads + n_kv_heads * (1 if cache is None else 2)) * head_dim, "qkv: too few columns")
+    _need(n_q_heads == 0 or (q_out.numel() == T * n_q_heads * head_dim and q_out.is_contiguous()), "q_out: contiguous [T, n_q_heads, head_dim]")
+    _need(k_out is None or (k_out.numel() == T * n_kv_heads * head_dim and k_out.is_contiguous()),
+          "k_out: contiguous [T, n_kv_heads, head_dim]")
+    n_pos = rot = 0
+    if cos_sin is not None:
+        n_pos, rot = cos_sin.shape
+        _need(cos_sin.element_size() == 4 and cos_sin.is_contiguous(), "cos_sin: contiguous fp32 [n_pos, rot_dim]")
+    for w in (q_weight, k_weight):
+        _need(w is None or (w.numel() == head_dim and w.element_size() == 2 and w.is_contiguous()), "weights: bf16 [head_dim]")
+    _check(_lib.qk_norm_rope(qkv.data_ptr(), qkv.stride(0), T, n_q_heads, n_kv_heads, head_dim, _dptr(q_weight),
+                             _dptr(k_weight), eps, _dptr(cos_sin), rot, int(interleaved), n_pos,
+                             None if cos_sin is None else _i32(positions, T, "positions"), _dptr(q_out), _dptr(k_out),
+                             None if cache is None else cache.ref, None if slots is None else _i32(slots, T, "slots"),
+                             _stream_ptr(stream)), "qk_norm_rope")
+    return q_out, k_out
+
+
+def kv4_append(cache: Kv4Cache, k, v, slots, stream=None):
+    """Quantise keys and values [T, n_kv_heads, head_dim] (bf16; any token stride) into the cache at slots."""
+    T, D = k.shape[0], cache.head_dim
+    for x in (k, v):
+        _need(x.dim() == 3 and x.shape == (T, cache.n_kv_heads, D) and x.element_size() == 2 and x.stride(2) == 1 and
+              (x.stride(1) == D or cache.n_kv_heads == 1), "k, v: bf16 [T, n_kv_heads, head_dim], a token's heads contiguous")
+    _check(_lib.kv4_append(cache.ref, k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), T, _i32(slots, T, "slots"),
+                           _stream_ptr(stream)), "kv4_append")
+
+
+def kv4_gather(cache: Kv4Cache, slots, k_out, v_out, stream=None):
+    """The keys and values that the cache holds at slots, as bf16 [n, n_kv_heads, head_dim]."""
+    n = slots.numel()
+    for x in (k_out, v_out):
+        _need(x.numel() == n * cache.n_kv_heads * cache.head_dim and x.element_size() == 2 and x.is_contiguous(),
+              "k_out, v_out: contiguous bf16 [n, n_kv_heads, head_dim]")
+    _check(_lib.kv4_gather(cache.ref, _i32(slots, n, "slots"), n, k_out.data_ptr(), v_out.data_ptr(),
+                           _stream_ptr(stream)), "kv4_gather")
+    return k_out, v_out
+
+
+def kv4_attention_ws_size(B: int, n_q_heads: int, n_kv_heads: int, head_dim: int, n_q_tokens: int, max_q: int,
+                          max_kv: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.kv4_attention_ws_size(B, n_q_heads, n_kv_heads, head_dim, n_q_tokens, max_q, max_kv, ctypes.byref(n)),
+           "kv4_attention_ws_size")
+    return n.value
+
+
+def kv4_attention(cache: Kv4Cache, q, q_start, kv_len, table, out, workspace, max_q: int, max_kv: int, scale: float,
+                  causal: bool = True, window: int = 0, stream=None):
+    """Softmax attention of a ragged batch over the cache: q, out [n_q_tokens, n_q_heads, head_dim] (bf16), request b's
+    queries being rows q_start[b] .. q_start[b + 1] - 1 and the last tokens of its kv_len[b]."""
+    n, hq, D = q.shape
+    B = kv_len.numel()
+    _need(q.element_size() == 2 and q.is_contiguous() and D == cache.head_dim, "q: contiguous bf16 [n, n_q_heads, head_dim]")
+    _need(out.shape == q.shape and out.element_size() == 2 and out.is_contiguous(), "out: as q")
+    _need(table.dim() == 2 and table.shape[0] == B, "table: [B, max_blocks]")
+    _check(_lib.kv4_attention(cache.ref, q.data_ptr(), n, hq, _i32(q_start, B + 1, "q_start"), _i32(kv_len, B, "kv_len"), B,
+                              _i32(table, 0, "table"), table.shape[1], max_q, max_kv, scale, int(causal), window,
+                              out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                              _stream_ptr(stream)), "kv4_attention")
+    return out

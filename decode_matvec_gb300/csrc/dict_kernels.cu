@@ -2173,11 +2173,15 @@ extern "C" int qmoe_check_status(void* stream) {
     const int a = qmoe::dict_take_error();
     const int b = qmoe::rvq_take_error();
     const int c = qmoe::pack_take_error();
-    if (a == QMOE_ECUDA || b == QMOE_ECUDA || c == QMOE_ECUDA)
+    const int d = qmoe::kv4_take_error();
+    const int f = qmoe::kv4_attention_take_error();
+    if (a == QMOE_ECUDA || b == QMOE_ECUDA || c == QMOE_ECUDA || d == QMOE_ECUDA || f == QMOE_ECUDA)
         return fail(QMOE_ECUDA, "qmoe_check_status: reading the error word failed");
     if (a) return fail(a, "device reported an error (dictionary kernels)");
     if (b) return fail(b, "device reported an error (RVQ kernels)");
     if (c) return fail(c, "device reported an error (device encoder)");
+    if (d) return fail(d, "device reported an error (key/value cache kernels)");
+    if (f) return fail(f, "device reported an error (attention kernels)");
     return QMOE_OK;
 }
 

@@ -1,0 +1,453 @@
+// What feeds attention over the 4-bit paged key/value cache: block tables and
+// slot maps, the norms and the rotation of queries and keys, and the cache's
+// writer and reader.  All are bound by memory (or, for a few tokens, by the
+// latency of a launch and one dependent chain of loads).
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "kv4_common.cuh"
+
+namespace {
+
+__device__ int g_kv4_error;
+
+__device__ __forceinline__ void kv4_set_error(int code) { atomicCAS(&g_kv4_error, 0, code); }
+
+// ---------------------------------------------------------------- block tables
+constexpr int kPlanThreads = 1024;
+
+struct TableArgs {
+    const int32_t* cached;
+    const int32_t* fresh;
+    const int32_t* free_pages;
+    const int32_t* n_free;
+    int32_t* table;
+    int32_t* q_start;
+    int32_t* kv_len;
+    int32_t* slots;
+    int32_t* positions;
+    int32_t* n_free_out;
+    int B, page_shift, max_blocks, n_tokens;
+};
+
+// Slot and position of new token t, whose request is the last one that starts
+// at or before it (binary search over q_start).
+__device__ __forceinline__ void map_token(const TableArgs& a, int t, int total) {
+    int slot = -1, pos = 0;
+    if (t < total) {
+        int lo = 0, hi = a.B;   // q_start[lo] <= t < q_start[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.q_start[mid] <= t)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        pos = max(a.cached[lo], 0) + t - a.q_start[lo];
+        const int blk = pos >> a.page_shift;
+        if (blk < a.max_blocks) {
+            const int page = a.table[(int64_t)lo * a.max_blocks + blk];
+            if (page >= 0)
+                slot = (page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+            else if (page != -1)
+                kv4_set_error(QMOE_EINVAL);
+        }
+    }
+    a.slots[t] = slot;
+    a.positions[t] = pos;
+}
+
+// One block: prefix sums of the new tokens and new pages over the requests,
+// the new table entries, and (kTokens) the tokens' slots as well.
+template <bool kTokens>
+__global__ void __launch_bounds__(kPlanThreads) block_tables_kernel(TableArgs a) {
+    __shared__ long long warp_tok[32];
+    __shared__ long long warp_page[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int P1 = (1 << a.page_shift) - 1;
+    const int n_free = max(*a.n_free, 0);
+    long long tok0 = 0;
+    long long page0 = 0;
+    bool bad = false;
+    for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        int c = 0, n = 0;
+        if (b < a.B) {
+            c = a.cached[b];
+            n = a.fresh[b];
+            bad |= c < 0 || n < 0 || (long long)c + n > 0x7FFFFFFF - 64;
+            c = max(c, 0);
+            n = min(max(n, 0), 0x7FFFFFFF - 64 - c);
+        }
+        const int have = (int)(((unsigned)c + P1) >> a.page_shift);
+        const int need = (int)(((unsigned)(c + n) + P1) >> a.page_shift) - have;
+        long long ts = n;
+        long long ps = need;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long to = __shfl_up_sync(QMOE_FULL_MASK, ts, d);
+            const long long po = __shfl_up_sync(QMOE_FULL_MASK, ps, d);
+            if (lane >= d) {
+                ts += to;
+                ps += po;
+            }
+        }
+        if (lane == 31) {
+            warp_tok[warp] = ts;
+            warp_page[warp] = ps;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            long long tw = warp_tok[lane];
+            long long pw = warp_page[lane];
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long to = __shfl_up_sync(QMOE_FULL_MASK, tw, d);
+                const long long po = __shfl_up_sync(QMOE_FULL_MASK, pw, d);
+                if (lane >= d) {
+                    tw += to;
+                    pw += po;
+                }
+            }
+            warp_tok[lane] = tw;
+            warp_page[lane] = pw;
+        }
+        __syncthreads();
+        const long long t_end = tok0 + ts + (warp ? warp_tok[warp - 1] : 0);
+        const long long p_first = page0 + ps - need + (warp ? warp_page[warp - 1] : 0);
+        if (b < a.B) {
+            a.q_start[b] = (int)min(t_end - n, (long long)a.n_tokens);
+            a.kv_len[b] = c + n;
+            if (have + need > a.max_blocks) bad = true;
+        }
+        // new entries: one request after another, its pages spread over the warp's lanes
+        for (int r = 0; r < 32; ++r) {
+            const int rn = __shfl_sync(QMOE_FULL_MASK, need, r);
+            if (rn == 0) continue;
+            const long long rf = __shfl_sync(QMOE_FULL_MASK, p_first, r);
+            const int rh = __shfl_sync(QMOE_FULL_MASK, have, r);
+            const int64_t row = (int64_t)(b - lane + r) * a.max_blocks;
+            for (int i = lane; i < rn && rh + i < a.max_blocks; i += 32) {
+                const long long at = n_free - 1 - rf - i;
+                a.table[row + rh + i] = at >= 0 ? a.free_pages[at] : -1;
+            }
+        }
+        tok0 += warp_tok[31];
+        page0 += warp_page[31];
+        __syncthreads();
+    }
+    if (__syncthreads_or(bad) && tid == 0) kv4_set_error(QMOE_EINVAL);
+    if (tid == 0) {
+        a.q_start[a.B] = (int)min(tok0, (long long)a.n_tokens);
+        *a.n_free_out = (int)max(n_free - page0, 0LL);
+        if (page0 > n_free || tok0 > a.n_tokens) kv4_set_error(QMOE_ECAPACITY);
+    }
+    if (kTokens) {
+        __syncthreads();   // table and q_start of this block are read below
+        const int total = (int)min(tok0, (long long)a.n_tokens);
+        for (int t = tid; t < a.n_tokens; t += kPlanThreads) map_token(a, t, total);
+    }
+}
+
+__global__ void __launch_bounds__(256) slot_map_kernel(TableArgs a) {
+    const int t = blockIdx.x * 256 + threadIdx.x;
+    if (t < a.n_tokens) map_token(a, t, a.q_start[a.B]);
+}
+
+// ---------------------------------------------------------------- norm, rotation, cache write
+struct RopeArgs {
+    const uint16_t *q, *k, *v;            // heads of one token contiguous
+    int64_t q_stride, k_stride, v_stride;  // elements from token to token
+    int T, n_q, n_kv, heads;               // heads: how many of a token's (q, k, v) heads are visited
+    const uint16_t *wq, *wk;               // norm weights or NULL
+    float eps;
+    const float* cos_sin;                  // NULL: no rotation
+    int rot, interleaved, n_pos;
+    const int32_t* positions;
+    uint16_t *q_out, *k_out;               // either may be NULL
+    const int32_t* slots;                  // NULL: no cache
+    kv4::CacheView cache;
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *(uint32_t*)&p;
+}
+
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int d = L / 2; d > 0; d >>= 1) v += __shfl_xor_sync(QMOE_FULL_MASK, v, d);
+    return v;
+}
+
+// Quantises the row held 8 values a lane by the L lanes of a group and stores
+// its codes (one word a lane) and its (s, z) pair.
+template <int L>
+__device__ __forceinline__ void store_row(const RopeArgs& a, const float (&x)[8], int slot, int head, int side, int gl) {
+    float y[8], lo, hi;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = x[i] == x[i] ? x[i] : 0.f;
+        y[i] = fminf(fmaxf(t, -32768.f), 32768.f);
+        lo = i ? fminf(lo, y[i]) : y[i];
+        hi = i ? fmaxf(hi, y[i]) : y[i];
+    }
+#pragma unroll
+    for (int d = L / 2; d > 0; d >>= 1) {
+        lo = fminf(lo, __shfl_xor_sync(QMOE_FULL_MASK, lo, d));
+        hi = fmaxf(hi, __shfl_xor_sync(QMOE_FULL_MASK, hi, d));
+    }
+    const __half zh = __float2half_rn(lo);
+    const float z = __half2float(zh);
+    const __half sh = __float2half_rn(__fdiv_rn(hi - z, 15.f));
+    const float s = __half2float(sh);
+    uint32_t word = 0;
+    if (s > 0.f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float u = fminf(fmaxf(rintf(__fdiv_rn(y[i] - z, s)), 0.f), 15.f);
+            word |= (uint32_t)u << (4 * (i >> 1) + 16 * (i & 1));
+        }
+    }
+    if (slot < 0) return;
+    const int P = 1 << a.cache.page_shift;
+    unsigned char* hp = kv4::head_ptr(a.cache, slot >> a.cache.page_shift, head);
+    const int in_page = slot & (P - 1);
+    const int row = side * P + in_page;
+    ((uint32_t*)hp)[row * L + gl] = word;
+    if (gl == 0)
+        ((uint32_t*)(hp + (size_t)2 * P * L * 4))[row] =
+            (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(zh) << 16);
+}
+
+// A group of L = head_dim / 8 lanes holds one head, 8 values a lane (16-byte loads and stores).
+template <int L>
+__global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
+    const int gl = threadIdx.x & (L - 1);
+    const long long n = (long long)a.T * a.heads;
+    const long long first = (long long)blockIdx.x * (256 / L);
+    const long long item = first + threadIdx.x / L;
+    if (first + ((threadIdx.x & ~31) / L) >= n) return;   // the whole warp is past the end
+    const bool live = item < n;
+    const int t = live ? (int)(item / a.heads) : a.T - 1;
+    const int h = live ? (int)(item - (long long)t * a.heads) : 0;
+    const int kind = h < a.n_q ? 0 : h < a.n_q + a.n_kv ? 1 : 2;   // query, key, value
+    const int hh = kind == 0 ? h : h - a.n_q - (kind == 2 ? a.n_kv : 0);
+    const uint16_t* src = kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride;
+    const uint4 raw = *(const uint4*)(src + hh * (L * 8) + gl * 8);
+    float x[8] = {bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y),
+                  bf16_lo(raw.z), bf16_hi(raw.z), bf16_lo(raw.w), bf16_hi(raw.w)};
+    const uint16_t* w = kind == 0 ? a.wq : kind == 1 ? a.wk : nullptr;
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+    ss = group_sum<L>(ss);
+    if (w) {
+        const uint4 wr = *(const uint4*)(w + gl * 8);
+        const float r = 1.f / sqrtf(ss / (L * 8) + a.eps);
+        const float wf[8] = {bf16_lo(wr.x), bf16_hi(wr.x), bf16_lo(wr.y), bf16_hi(wr.y),
+                             bf16_lo(wr.z), bf16_hi(wr.z), bf16_lo(wr.w), bf16_hi(wr.w)};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * wf[i];
+    }
+    if (a.cos_sin) {
+        const int half = a.rot >> 1, hl = half >> 3;     // values, lanes of half a rotation
+        const bool in = gl * 8 < a.rot;
+        const int partner = !in ? gl : gl < hl ? gl + hl : gl - hl;
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(QMOE_FULL_MASK, x[i], partner, L);
+        if (in && kind < 2) {
+            int pos = a.positions[t];
+            if (pos < 0 || pos >= a.n_pos) {
+                kv4_set_error(QMOE_EINVAL);
+                pos = pos < 0 ? 0 : a.n_pos - 1;
+            }
+            const float* cs = a.cos_sin + (int64_t)pos * a.rot;
+            if (a.interleaved) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const float c = cs[gl * 4 + i / 2], s = cs[half + gl * 4 + i / 2], u = x[i], v = x[i + 1];
+                    x[i] = u * c - v * s;
+                    x[i + 1] = v * c + u * s;
+                }
+            } else {
+                const float* cp = cs + (gl < hl ? gl : gl - hl) * 8;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float c = cp[i], s = cp[half + i];
+                    x[i] = x[i] * c + (gl < hl ? -y[i] : y[i]) * s;
+                }
+            }
+        }
+    }
+    const uint4 o = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    if (live && kind == 0) *(uint4*)(a.q_out + ((int64_t)t * a.n_q + hh) * (L * 8) + gl * 8) = o;
+    if (live && kind == 1 && a.k_out) *(uint4*)(a.k_out + ((int64_t)t * a.n_kv + hh) * (L * 8) + gl * 8) = o;
+    if (a.slots) {
+        // what the cache holds are the values as k_out holds them (rounded to bf16)
+        const float k8[8] = {bf16_lo(o.x), bf16_hi(o.x), bf16_lo(o.y), bf16_hi(o.y),
+                             bf16_lo(o.z), bf16_hi(o.z), bf16_lo(o.w), bf16_hi(o.w)};
+        int slot = live && kind > 0 ? a.slots[t] : -1;
+        if (slot < -1 || (slot >> a.cache.page_shift) >= a.cache.n_pages) {
+            kv4_set_error(QMOE_EINVAL);
+            slot = -1;
+        }
+        store_row<L>(a, k8, slot, hh, kind == 2, gl);
+    }
+}
+
+// ---------------------------------------------------------------- cache reader
+template <int L>
+__global__ void __launch_bounds__(256) gather_kernel(kv4::CacheView c, const int32_t* slots, int n, uint16_t* k_out,
+                                                     uint16_t* v_out) {
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (long long)n * c.n_kv_heads * 2 * L) return;
+    const int gl = (int)(i & (L - 1));
+    long long r = i / L;
+    const int h = (int)(r % c.n_kv_heads);
+    r /= c.n_kv_heads;
+    const int side = r >= n;
+    const int t = (int)(side ? r - n : r);
+    int slot = slots[t];
+    if (slot < -1 || (slot >> c.page_shift) >= c.n_pages) {
+        kv4_set_error(QMOE_EINVAL);
+        slot = -1;
+    }
+    uint4 o = make_uint4(0, 0, 0, 0);
+    if (slot >= 0) {
+        const int P = 1 << c.page_shift;
+        const unsigned char* hp = kv4::head_ptr(c, slot >> c.page_shift, h);
+        const int row = side * P + (slot & (P - 1));
+        const uint32_t w = ((const uint32_t*)hp)[row * L + gl];
+        const uint32_t sz = ((const uint32_t*)(hp + (size_t)2 * P * L * 4))[row];
+        const float s = f16_to_f32((uint16_t)sz), z = f16_to_f32((uint16_t)(sz >> 16));
+        float x[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = fmaf(s, (float)((w >> (4 * (q >> 1) + 16 * (q & 1))) & 15u), z);
+        o = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+    }
+    *(uint4*)((side ? v_out : k_out) + ((int64_t)t * c.n_kv_heads + h) * (L * 8) + gl * 8) = o;
+}
+
+int launch_rope(const RopeArgs& a, int head_dim, const char* who, cudaStream_t st) {
+    const long long items = (long long)a.T * a.heads;
+    if (items == 0) return QMOE_OK;
+    const int per = 256 / (head_dim / 8);
+    const long long blocks = (items + per - 1) / per;
+    if (blocks > 0x7FFFFFFFLL) return qmoe::fail(QMOE_EINVAL, std::string(who) + ": too many heads in one call");
+    if (head_dim == 128)
+        rope_kernel<16><<<(unsigned)blocks, 256, 0, st>>>(a);
+    else
+        rope_kernel<8><<<(unsigned)blocks, 256, 0, st>>>(a);
+    return qmoe::launch_check(who);
+}
+
+}  // namespace
+
+namespace qmoe {
+int kv4_take_error() {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_kv4_error, sizeof(int)) != cudaSuccess) return QMOE_ECUDA;
+    const int z = 0;
+    if (cudaMemcpyToSymbol(g_kv4_error, &z, sizeof(int)) != cudaSuccess) return QMOE_ECUDA;
+    return v;
+}
+}  // namespace qmoe
+
+extern "C" int kv4_block_tables(const int32_t* cached, const int32_t* new_tokens, int B, const int32_t* free_pages,
+                                const int32_t* n_free, int page_size, int32_t* table, int max_blocks,
+                                int32_t* q_start, int32_t* kv_len, int32_t* slots, int32_t* positions, int n_tokens,
+                                int32_t* n_free_out, void* stream) {
+    qmoe::clear_error();
+    if (page_size != 16 && page_size != 32 && page_size != 64)
+        return qmoe::fail(QMOE_EINVAL, "kv4_block_tables: page_size must be 16, 32 or 64");
+    if (B < 0 || n_tokens < 0 || max_blocks < 0) return qmoe::fail(QMOE_EINVAL, "kv4_block_tables: negative size");
+    if (!n_free || !n_free_out || !q_start || (B > 0 && (!cached || !new_tokens || !table || !kv_len || !free_pages)) ||
+        (n_tokens > 0 && (!slots || !positions)))
+        return qmoe::fail(QMOE_EINVAL, "kv4_block_tables: NULL pointer");
+    TableArgs a{cached, new_tokens, free_pages, n_free, table, q_start, kv_len, slots, positions, n_free_out,
+                B, page_size == 16 ? 4 : page_size == 32 ? 5 : 6, max_blocks, n_tokens};
+    cudaStream_t st = (cudaStream_t)stream;
+    block_tables_kernel<false><<<1, kPlanThreads, 0, st>>>(a);
+    if (n_tokens > 0) slot_map_kernel<<<(unsigned)((n_tokens + 255) / 256), 256, 0, st>>>(a);
+    return qmoe::launch_check("kv4_block_tables");
+}
+
+extern "C" int qk_norm_rope(const void* qkv, int64_t row_stride, int T, int n_q_heads, int n_kv_heads, int head_dim,
+                            const void* q_weight, const void* k_weight, float eps, const float* cos_sin, int rot_dim,
+                            int interleaved, int n_pos, const int32_t* positions, void* q_out, void* k_out,
+                            const kv4_cache* cache, const int32_t* slots, void* stream) {
+    qmoe::clear_error();
+    if (head_dim != 64 && head_dim != 128) return qmoe::fail(QMOE_EUNSUPPORTED, "qk_norm_rope: head_dim must be 64 or 128");
+    if (T < 0 || n_q_heads < 0 || n_kv_heads < 0 || n_q_heads > 65536 || n_kv_heads > 65536)
+        return qmoe::fail(QMOE_EINVAL, "qk_norm_rope: bad sizes");
+    if (!cos_sin != (rot_dim == 0) || rot_dim < 0 || rot_dim > head_dim || rot_dim % 16)
+        return qmoe::fail(QMOE_EINVAL, "qk_norm_rope: rot_dim must be a multiple of 16 up to head_dim, 0 without cos_sin");
+    if (cos_sin && (n_pos < 1 || (T > 0 && !positions)))
+        return qmoe::fail(QMOE_EINVAL, "qk_norm_rope: a rotation needs positions and n_pos >= 1");
+    if ((T > 0 && !qkv) || (T > 0 && n_q_heads > 0 && !q_out)) return qmoe::fail(QMOE_EINVAL, "qk_norm_rope: NULL pointer");
+    if (!cache != !slots && T > 0) return qmoe::fail(QMOE_EINVAL, "qk_norm_rope: cache and slots go together");
+    const int64_t width = (int64_t)(n_q_heads + (cache ? 2 : 1) * n_kv_heads) * head_dim;
+    if (row_stride % 8 || (T > 1 && row_stride < width))
+        return qmoe::fail(QMOE_EINVAL, "qk_norm_rope: row_stride must be a multiple of 8 and cover a token's heads");
+    if (!kv4::aligned16(qkv) || !kv4::aligned16(q_weight) || !kv4::aligned16(k_weight) || !kv4::aligned16(cos_sin) ||
+        !kv4::aligned16(q_out) || !kv4::aligned16(k_out))
+        return qmoe::fail(QMOE_EINVAL, "qk_norm_rope: pointer not 16-byte aligned");
+    RopeArgs a{};
+    if (cache) {
+        const int rc = kv4::view_of(cache, "qk_norm_rope", &a.cache);
+        if (rc) return rc;
+        if (cache->head_dim != head_dim || cache->n_kv_heads != n_kv_heads)
+            return qmoe::fail(QMOE_EINVAL, "qk_norm_rope: the cache has another head layout");
+    }
+    const uint16_t* base = (const uint16_t*)qkv;
+    a.q = base;
+    a.k = base + (int64_t)n_q_heads * head_dim;
+    a.v = a.k + (int64_t)n_kv_heads * head_dim;
+    a.q_stride = a.k_stride = a.v_stride = row_stride;
+    a.T = T, a.n_q = n_q_heads, a.n_kv = n_kv_heads, a.heads = n_q_heads + (cache ? 2 : 1) * n_kv_heads;
+    a.wq = (const uint16_t*)q_weight, a.wk = (const uint16_t*)k_weight, a.eps = eps;
+    a.cos_sin = cos_sin, a.rot = rot_dim, a.interleaved = interleaved ? 1 : 0, a.n_pos = n_pos, a.positions = positions;
+    a.q_out = (uint16_t*)q_out, a.k_out = (uint16_t*)k_out, a.slots = cache ? slots : nullptr;
+    if (!cache && !k_out) a.heads = n_q_heads;
+    return launch_rope(a, head_dim, "qk_norm_rope", (cudaStream_t)stream);
+}
+
+extern "C" int kv4_append(const kv4_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride, int T,
+                          const int32_t* slots, void* stream) {
+    qmoe::clear_error();
+    RopeArgs a{};
+    const int rc = kv4::view_of(cache, "kv4_append", &a.cache);
+    if (rc) return rc;
+    if (T < 0 || (T > 0 && (!k || !v || !slots))) return qmoe::fail(QMOE_EINVAL, "kv4_append: negative T or NULL pointer");
+    const int64_t width = (int64_t)cache->n_kv_heads * cache->head_dim;
+    if (k_stride % 8 || v_stride % 8 || (T > 1 && (k_stride < width || v_stride < width)) || !kv4::aligned16(k) ||
+        !kv4::aligned16(v))
+        return qmoe::fail(QMOE_EINVAL, "kv4_append: strides must be multiples of 8 that cover a token, pointers 16-byte aligned");
+    a.k = (const uint16_t*)k, a.v = (const uint16_t*)v, a.k_stride = k_stride, a.v_stride = v_stride;
+    a.T = T, a.n_kv = cache->n_kv_heads, a.heads = 2 * cache->n_kv_heads, a.slots = slots;
+    return launch_rope(a, cache->head_dim, "kv4_append", (cudaStream_t)stream);
+}
+
+extern "C" int kv4_gather(const kv4_cache* cache, const int32_t* slots, int n, void* k_out, void* v_out, void* stream) {
+    qmoe::clear_error();
+    kv4::CacheView c;
+    const int rc = kv4::view_of(cache, "kv4_gather", &c);
+    if (rc) return rc;
+    if (n < 0 || (n > 0 && (!slots || !k_out || !v_out))) return qmoe::fail(QMOE_EINVAL, "kv4_gather: negative n or NULL pointer");
+    if (!kv4::aligned16(k_out) || !kv4::aligned16(v_out)) return qmoe::fail(QMOE_EINVAL, "kv4_gather: pointer not 16-byte aligned");
+    if (n == 0) return QMOE_OK;
+    const long long items = (long long)n * c.n_kv_heads * 2 * (cache->head_dim / 8);
+    const long long blocks = (items + 255) / 256;
+    if (blocks > 0x7FFFFFFFLL) return qmoe::fail(QMOE_EINVAL, "kv4_gather: too many rows in one call");
+    if (cache->head_dim == 128)
+        gather_kernel<16><<<(unsigned)blocks, 256, 0, (cudaStream_t)stream>>>(c, slots, n, (uint16_t*)k_out, (uint16_t*)v_out);
+    else
+        gather_kernel<8><<<(unsigned)blocks, 256, 0, (cudaStream_t)stream>>>(c, slots, n, (uint16_t*)k_out, (uint16_t*)v_out);
+    return qmoe::launch_check("kv4_gather");
+}

@@ -500,6 +500,145 @@ int e8p_pack(const double* w, int rows, int cols, const int8_t* sign_out,
 int e8p_nearest(const double* u, size_t n, uint16_t* codes);
 
 /* ======================================================================
+ * Attention over a paged key/value cache held in 4 bits
+ *
+ * The attention half of a decoder layer whose feed-forward half is one of the
+ * MoE layers above.  Nothing here comes from the pages; the formulas are the
+ * usual ones and are given at each call.
+ * ====================================================================== */
+
+/*
+ * A cache of one layer's keys and values.  A row (the head_dim values of one
+ * token, kv head and side) is stored as unsigned 4-bit codes u with one fp16
+ * pair (s, z): value = s * u + z.  With x the row (NaN read as 0, magnitudes
+ * above 32768 clamped to it, so that everything stored is finite),
+ *   z = fp16(min x),  s = fp16((max x - z) / 15),
+ *   u = clamp(rint((x - z) / s), 0, 15)  (0 when s = 0),
+ * in fp32 with nearest-even rounding.
+ *  pages      device, 16-byte aligned: n_pages pages of
+ *             n_kv_heads * page_size * (head_dim + 8) bytes each.  A page
+ *             holds, for each kv head in turn:
+ *               codes of the keys    [page_size][head_dim / 2] bytes,
+ *               codes of the values  [page_size][head_dim / 2] bytes,
+ *               pairs of the keys    [page_size][2] fp16 (s, z),
+ *               pairs of the values  [page_size][2] fp16.
+ *             32-bit word w of a row holds values 8w .. 8w+7: value 8w + 2i in
+ *             bits 4i .. 4i+3 and value 8w + 2i + 1 in bits 16+4i .. 19+4i
+ *             (i < 4), so that two masks and a shift give adjacent pairs.
+ *  page_size  16, 32 or 64 tokens;  head_dim 64 or 128.
+ * n_pages * page_size must be below 2^31 (slots are int32); the cache itself
+ * may exceed 2^32 bytes.  Slot = page * page_size + token in the page.
+ */
+typedef struct {
+    void* pages;
+    int n_pages, page_size, n_kv_heads, head_dim;
+} kv4_cache;
+
+/*
+ * Block tables and slot maps from request lengths.  Request b has cached[b]
+ * tokens in the cache and gets new_tokens[b] more.  Its new pages
+ * (ceil((cached + new) / page_size) - ceil(cached / page_size) of them) are
+ * taken from the top of the stack of free pages: the i-th new page of the
+ * call, in request order, is free_pages[n_free - 1 - i].
+ *  cached, new_tokens  device int32 [B], >= 0.
+ *  free_pages  device int32 stack;  n_free device int32 [1].
+ *  table       device int32 [B][max_blocks], in/out: entries of pages that a
+ *              request has already are read, those of new pages written, the
+ *              others left as they are.
+ *  q_start     device out int32 [B + 1]: exclusive prefix sum of new_tokens.
+ *  kv_len      device out int32 [B]: cached + new_tokens.
+ *  slots, positions  device out int32 [n_tokens]: for each new token, in
+ *              request order, its cache slot and its position in the request.
+ *              n_tokens is the size of these arrays; entries past the sum of
+ *              new_tokens get slot -1 and position 0.
+ *  n_free_out  device out int32 [1]: free pages left (may be n_free itself).
+ * Tokens without a page get slot -1.  Errors on the host: EINVAL.  Errors
+ * found on the device go to qmoe_check_status(): ECAPACITY (not enough free
+ * pages: the missing table entries are -1; or more new tokens than n_tokens:
+ * the excess is dropped), EINVAL (a negative length, read as 0; more blocks
+ * than max_blocks; a negative page in the table).
+ */
+int kv4_block_tables(const int32_t* cached, const int32_t* new_tokens, int B,
+                     const int32_t* free_pages, const int32_t* n_free, int page_size,
+                     int32_t* table, int max_blocks, int32_t* q_start, int32_t* kv_len,
+                     int32_t* slots, int32_t* positions, int n_tokens,
+                     int32_t* n_free_out, void* stream);
+
+/*
+ * Norms of queries and keys for each head and the position rotation, in one
+ * pass; with a cache, the keys and values are written to it in the same pass.
+ *  qkv       device bf16: token t's row starts at qkv + t * row_stride and
+ *            holds n_q_heads query heads, then n_kv_heads key heads, then (read
+ *            only when cache is given) n_kv_heads value heads of head_dim.
+ *  q_weight, k_weight  device bf16 [head_dim], or NULL for no norm:
+ *            x <- x / sqrt(mean(x^2) + eps) * weight.
+ *  cos_sin   device fp32 [n_pos][rot_dim], cosines then sines of rot_dim / 2
+ *            angles, or NULL (rot_dim 0) for no rotation;  positions device
+ *            int32 [T].  The first rot_dim values of a head are rotated:
+ *            (a, b) <- (a cos - b sin, b cos + a sin) with the pairs
+ *            (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved.
+ *            rot_dim a multiple of 16, at most head_dim.
+ *  q_out     device bf16 [T][n_q_heads][head_dim].
+ *  k_out     device bf16 [T][n_kv_heads][head_dim], or NULL.
+ *  cache     NULL, or the cache that the keys (as k_out would hold them) and
+ *            the values are written to, at slots (device int32 [T]; -1 skips
+ *            the token; two tokens must not share a slot).
+ * fp32 arithmetic, one rounding to bf16 at the end.  Pointers 16-byte
+ * aligned, row_stride a multiple of 8.  q_out and k_out may not overlap qkv.
+ * Errors: EINVAL, EUNSUPPORTED (head_dim); on the device EINVAL (a position
+ * outside [0, n_pos): the nearest one is used; a slot outside the cache:
+ * skipped).
+ */
+int qk_norm_rope(const void* qkv, int64_t row_stride, int T, int n_q_heads, int n_kv_heads, int head_dim,
+                 const void* q_weight, const void* k_weight, float eps,
+                 const float* cos_sin, int rot_dim, int interleaved, int n_pos, const int32_t* positions,
+                 void* q_out, void* k_out, const kv4_cache* cache, const int32_t* slots, void* stream);
+
+/*
+ * Quantise T tokens' keys and values into the cache.  Token t's heads start
+ * at k + t * k_stride and v + t * v_stride (bf16, heads contiguous), and go
+ * to slots[t] as in qk_norm_rope.  Errors: EINVAL; on the device EINVAL (a
+ * slot outside the cache).
+ */
+int kv4_append(const kv4_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride, int T,
+               const int32_t* slots, void* stream);
+
+/*
+ * Read n tokens' keys and values back from the cache: k_out, v_out device
+ * bf16 [n][n_kv_heads][head_dim] (s * u + z in fp32, rounded once); zeros for
+ * slot -1.  Errors as kv4_append.
+ */
+int kv4_gather(const kv4_cache* cache, const int32_t* slots, int n, void* k_out, void* v_out, void* stream);
+
+/*
+ * Softmax attention over the cache, for a ragged batch of B requests:
+ *   out[i][h] = sum_j p_j v_j,  p = softmax_j(scale * q[i][h] . k_j)
+ * over the tokens j of the request that query i sees.  Request b's queries
+ * are rows q_start[b] .. q_start[b+1] - 1; they are its last tokens, so query
+ * n of q_len stands at position p = kv_len[b] - q_len + n.  It sees
+ * j < kv_len[b]; with causal, j <= p; with window > 0, j > p - window (without
+ * causal p = kv_len[b] - 1 for every query).  A query that sees nothing gets
+ * zeros.  Query head h reads kv head h / (n_q_heads / n_kv_heads).
+ *  q, out    device bf16 [n_q_tokens][n_q_heads][head_dim], 16-byte aligned.
+ *  q_start   device int32 [B + 1], non-decreasing within [0, n_q_tokens].
+ *  kv_len    device int32 [B];  table device int32 [B][max_blocks].
+ *  max_q, max_kv  host: at least the largest q_len and kv_len.  A request
+ *            that passes them is skipped (ECAPACITY in the error word).
+ *  workspace device, ws_bytes >= kv4_attention_ws_size(...), 16-byte aligned.
+ * Scores, softmax statistics and sums are fp32.  Rows of out that belong to no
+ * request are left as they are.
+ * Errors: EINVAL, EUNSUPPORTED (head_dim, more than 128 query heads per kv
+ * head), ECAPACITY (workspace); on the device EINVAL (a page outside the
+ * cache among the blocks of a request: its tokens are not seen; q_start out
+ * of order or a negative kv_len: such requests are skipped).
+ */
+int kv4_attention_ws_size(int B, int n_q_heads, int n_kv_heads, int head_dim, int n_q_tokens, int max_q, int max_kv,
+                          size_t* bytes);
+int kv4_attention(const kv4_cache* cache, const void* q, int n_q_tokens, int n_q_heads, const int32_t* q_start,
+                  const int32_t* kv_len, int B, const int32_t* table, int max_blocks, int max_q, int max_kv,
+                  float scale, int causal, int window, void* out, void* workspace, size_t ws_bytes, void* stream);
+
+/* ======================================================================
  * Status and test exports
  * ====================================================================== */
 
