@@ -578,6 +578,30 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
     }
 }
 
+// Four values (from d0) of row r of an item whose parts blocks c0 .. c1 left; the row is row `row` of the request's kv head.
+template <int D>
+__device__ __forceinline__ void join_parts(const AttnArgs& a, const float* parts, int c0, int c1, long long u0, long long chunk,
+                                           int part_rows, int r, int d0, int q0, int row, int kh) {
+    float mm = kNoMax, ll = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c <= c1; ++c) {
+        const float* p = part_of((float*)parts, c, u0 >= (long long)c * chunk ? 1 : 0, part_rows, D);
+        const float2 ml = *(const float2*)(p + (size_t)part_rows * D + 2 * r);
+        const float4 x = *(const float4*)(p + (size_t)r * D + d0);
+        const float m2 = fmaxf(mm, ml.x), fa = ex2(mm - m2), fb = ex2(ml.x - m2);
+        mm = m2;
+        ll = ll * fa + ml.y * fb;
+        acc.x = acc.x * fa + x.x * fb, acc.y = acc.y * fa + x.y * fb;
+        acc.z = acc.z * fa + x.z * fb, acc.w = acc.w * fa + x.w * fb;
+    }
+    const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);
+    const int n = row / a.group, h = kh * a.group + row - n * a.group;
+    uint2 w;
+    w.x = (uint32_t)f32_to_bf16(acc.x * inv) | ((uint32_t)f32_to_bf16(acc.y * inv) << 16);
+    w.y = (uint32_t)f32_to_bf16(acc.z * inv) | ((uint32_t)f32_to_bf16(acc.w * inv) << 16);
+    *(uint2*)(a.out + ((int64_t)(q0 + n) * a.n_q_heads + h) * D + d0) = w;
+}
+
 // Joins the parts of items that several blocks of decode_kernel shared.  One block per (request, kv head).
 constexpr int kCombineThreads = 128;
 
@@ -588,103 +612,739 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, in
     const Found f = scan_requests<kCombineThreads>(a, max_rows, b, true, n_ctas, 0, &chunk, false);
     int t0;
     const int n = tiles_of(a, b, max_rows, &t0, false);
+    asm volatile("griddepcontrol.wait;" ::: "memory");      // the parts are written by the kernel before
     if (n == 0) return;
     const long long u0 = f.before + (long long)kh * n, u1 = u0 + n;
     const int c0 = (int)(u0 / chunk), c1 = (int)((u1 - 1) / chunk);
     if (c0 == c1) return;
-    asm volatile("griddepcontrol.wait;" ::: "memory");      // the parts are written by the kernel before
     const int q0 = a.q_start[b], rows = (a.q_start[b + 1] - q0) * a.group;
     for (int i = threadIdx.x; i < rows * (D / 4); i += kCombineThreads) {
         const int r = i / (D / 4), d0 = (i - r * (D / 4)) * 4;
-        float mm = kNoMax, ll = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = c0; c <= c1; ++c) {
-            const float* p = part_of((float*)parts, c, u0 >= (long long)c * chunk ? 1 : 0, max_rows, D);
-            const float2 ml = *(const float2*)(p + (size_t)max_rows * D + 2 * r);
-            const float4 x = *(const float4*)(p + (size_t)r * D + d0);
-            const float m2 = fmaxf(mm, ml.x), fa = ex2(mm - m2), fb = ex2(ml.x - m2);
-            mm = m2;
-            ll = ll * fa + ml.y * fb;
-            acc.x = acc.x * fa + x.x * fb, acc.y = acc.y * fa + x.y * fb;
-            acc.z = acc.z * fa + x.z * fb, acc.w = acc.w * fa + x.w * fb;
-        }
-        const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);
-        const int n_ = r / a.group, h = kh * a.group + r - n_ * a.group;
-        uint2 w;
-        w.x = (uint32_t)f32_to_bf16(acc.x * inv) | ((uint32_t)f32_to_bf16(acc.y * inv) << 16);
-        w.y = (uint32_t)f32_to_bf16(acc.z * inv) | ((uint32_t)f32_to_bf16(acc.w * inv) << 16);
-        *(uint2*)(a.out + ((int64_t)(q0 + n_) * a.n_q_heads + h) * D + d0) = w;
+        join_parts<D>(a, parts, c0, c1, u0, chunk, max_rows, r, d0, q0, r, kh);
     }
 }
 
-// A warp per (query, head): a lane per key for the scores, head_dim / 32 values a lane for the sums.
-template <int D>
-__global__ void __launch_bounds__(128) attention_kernel(AttnArgs a, int max_rows) {
-    __shared__ float qs[4][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.x * 4 + warp;
-    const int b = blockIdx.z;
-    int q0, q_len, len;
-    if (!request(a, b, &q0, &q_len, &len, true) || q_len * a.group <= max_rows) return;
-    const int n = blockIdx.y;
-    if (n >= q_len || h >= a.n_q_heads) return;
-    const int pos = a.causal ? len - q_len + n : len - 1;
-    const int end = min(pos + 1, len);
-    const int begin = a.window ? max(0, pos - a.window + 1) : 0;
-    const int64_t row = ((int64_t)(q0 + n) * a.n_q_heads + h) * D;
-    for (int i = lane; i < D; i += 32) qs[warp][i] = bf16_to_f32(a.q[row + i]);
-    __syncwarp();
-    const int kh = h / a.group, P = 1 << a.cache.page_shift;
-    float m = -INFINITY, l = 0.f, o[D / 32] = {};
-    for (int j0 = begin; j0 < end; j0 += 32) {
-        const int j = j0 + lane;
-        float s = -INFINITY;
-        const unsigned char* hp = nullptr;
-        if (j < end) {
-            const int blk = j >> a.cache.page_shift;
-            const int page = blk < a.max_blocks ? a.table[(int64_t)b * a.max_blocks + blk] : -1;
-            if (page < 0 || page >= a.cache.n_pages) {
-                attn_set_error(QMOE_EINVAL);
-            } else {
-                hp = kv4::head_ptr(a.cache, page, kh);
-                const int r = j & (P - 1);
-                float dot = 0.f, sum = 0.f;
-                for (int w = 0; w < D / 8; ++w) {
-                    const uint32_t word = ((const uint32_t*)hp)[r * (D / 8) + w];
-                    for (int i = 0; i < 8; ++i) {
-                        const float qv = qs[warp][8 * w + i];
-                        dot += qv * (float)((word >> (4 * (i >> 1) + 16 * (i & 1))) & 15u);
-                        sum += qv;
-                    }
-                }
-                const uint32_t sz = ((const uint32_t*)(hp + P * D))[r];
-                s = (f16_to_f32((uint16_t)sz) * dot + f16_to_f32((uint16_t)(sz >> 16)) * sum) * a.scale;
-            }
+// ---------------------------------------------------------------- many query rows: tensor-core tiles
+//
+// A block takes 256 query rows of one (request, kv head) as two tiles of 128 and walks the keys 128 at
+// a time: S = Q K^T into tensor memory, P = 2^(S c - m) back into tensor memory as fp16 (over S), O += P V
+// (tcgen05, both products' accumulators fp32, P as the operand from tensor memory).  While one tile's
+// softmax runs, the tensor core works on the other.  The codes are expanded once per block to fp16 in
+// shared memory, k = s u + z rounded once to 11 bits (bf16 inputs and outputs have 8); P and the
+// values are fp16 too, statistics and sums fp32.  Queries carry a power of two per row (exact), so any
+// bf16 magnitude is inside fp16's range.  The running maximum moves, and O is rescaled, only when a
+// row passes it by 2^8; P carries 2^6, so that small weights stay above fp16's subnormals.
+//
+// Roles, one block per SM: 2 x 4 softmax warps (a thread per row), 4 warps that expand keys and values,
+// one warp that issues the products, one that copies pages.  What bounds it: at 256 rows the tensor
+// core needs about 2070 cycles for 128 keys (head_dim 128), shared memory about as many (the Q K^T
+// operands alone 1030), the softmax warps about 900 issue slots a scheduler and the expansion 550.
+//
+// Work is dealt out as in the few-row path: all (rows, kv head) items' key tiles in a row, in equal
+// runs; items that several blocks share are joined by tile_combine_kernel.
+constexpr int kKeys = 128;                       // keys of a tile
+constexpr int kRows = 256;                       // query rows of an item
+constexpr int kTileThreads = 512;
+constexpr int kExpandWarp = 8, kIssueWarp = 12, kCopyWarp = 13;
+constexpr int kRawStages = 2, kExpanded = 3, kInfo = 8;
+constexpr int kPlanTile = 1024;
+
+// Work list of the tile path, in the workspace: pairs (request, block of 256 rows) in order.
+struct TilePlan {
+    int32_t* pair_start;      // [B + 1]
+    long long* unit_start;    // [pairs + 1]: key tiles of all kv heads before the pair
+    int32_t* pair_b;          // [pairs]
+    int max_pairs;
+};
+
+// Key tiles [lo, hi) that rows [r0, r1) of a request see.
+__device__ __forceinline__ void key_tiles(const AttnArgs& a, int q_len, int kv_len, int r0, int r1, int* lo, int* hi) {
+    const int first = a.causal ? kv_len - q_len : kv_len - 1;
+    const int p0 = a.causal ? first + r0 / a.group : first, p1 = a.causal ? first + (r1 - 1) / a.group : first;
+    const int k1 = min(kv_len, p1 + 1), k0 = a.window ? max(0, p0 - a.window + 1) : 0;
+    *lo = k0 / kKeys;
+    *hi = k1 > k0 ? (k1 + kKeys - 1) / kKeys : *lo;
+}
+
+// Inclusive scan over the block's 1024 threads; *total gets the sum.
+__device__ __forceinline__ long long block_scan(long long v, long long* total) {
+    __shared__ long long sums[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(QMOE_FULL_MASK, v, d);
+        if (lane >= d) v += o;
+    }
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    long long before = 0, all = 0;
+    for (int w = 0; w < 32; ++w) {
+        if (w < warp) before += sums[w];
+        all += sums[w];
+    }
+    __syncthreads();
+    *total = all;
+    return v + before;
+}
+
+__global__ void __launch_bounds__(kPlanTile) tile_plan_kernel(AttnArgs a, TilePlan p, int min_rows) {
+    const int tid = threadIdx.x;
+    long long base = 0, total;
+    for (int b0 = 0; b0 < a.B; b0 += kPlanTile) {
+        const int b = b0 + tid;
+        int q0, q_len = 0, kv_len, pairs = 0;
+        if (b < a.B && request(a, b, &q0, &q_len, &kv_len, min_rows == 0) && q_len * a.group > min_rows)
+            pairs = (q_len * a.group + kRows - 1) / kRows;
+        const long long end = base + block_scan(pairs, &total);
+        if (b < a.B) {
+            p.pair_start[b] = (int)(end - pairs);
+            for (int i = 0; i < pairs; ++i)
+                if (end - pairs + i < p.max_pairs) p.pair_b[end - pairs + i] = b;
         }
-        float mx = s;
-        for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(QMOE_FULL_MASK, mx, d));
-        const float m2 = fmaxf(m, mx);
-        if (m2 == -INFINITY) continue;
-        const float f = expf(m - m2), p = expf(s - m2);
-        m = m2;
-        l = l * f + warp_sum(p);
-        for (int i = 0; i < D / 32; ++i) o[i] *= f;
-        for (int t = 0; t < min(32, end - j0); ++t) {
-            const float pt = __shfl_sync(QMOE_FULL_MASK, p, t);
-            const unsigned char* ht = (const unsigned char*)__shfl_sync(QMOE_FULL_MASK, (unsigned long long)hp, t);
-            if (!ht) continue;
-            const int r = P + ((j0 + t) & (P - 1));
-            const uint32_t sz = ((const uint32_t*)(ht + P * D))[r];
-            const float vs = f16_to_f32((uint16_t)sz), vz = f16_to_f32((uint16_t)(sz >> 16));
-            for (int i = 0; i < D / 32; ++i) {
-                const int d = lane + 32 * i;
-                const uint32_t word = ((const uint32_t*)ht)[r * (D / 8) + d / 8];
-                o[i] += pt * fmaf(vs, (float)((word >> (4 * ((d & 7) >> 1) + 16 * (d & 1))) & 15u), vz);
+        base += total;
+    }
+    const int n_pairs = (int)min(base, (long long)p.max_pairs);
+    if (tid == 0) p.pair_start[a.B] = n_pairs;
+    __syncthreads();
+    base = 0;
+    for (int i0 = 0; i0 < n_pairs; i0 += kPlanTile) {
+        const int i = i0 + tid;
+        int tiles = 0;
+        if (i < n_pairs) {
+            const int b = p.pair_b[i], q_len = a.q_start[b + 1] - a.q_start[b];
+            const int r0 = (i - p.pair_start[b]) * kRows;
+            int lo, hi;
+            key_tiles(a, q_len, a.kv_len[b], r0, min(r0 + kRows, q_len * a.group), &lo, &hi);
+            tiles = max(1, hi - lo);
+        }
+        const long long n = (long long)tiles * a.cache.n_kv_heads;
+        const long long end = base + block_scan(n, &total);
+        if (i < n_pairs) p.unit_start[i] = end - n;
+        base += total;
+    }
+    if (tid == 0) p.unit_start[n_pairs] = base;
+}
+
+struct TileCursor {
+    long long u, u1;             // next unit, end of the run
+    int pair, b, rb, kh, t0, t1, q0, q_len, kv_len, lo, more, whole;
+    int s[2], e[2];              // key tiles, in [t0, t1), that the two tiles of 128 rows see
+};
+
+template <int D>
+struct TileShared {
+    static constexpr int kQGroup = (D / 8) * 128;                // bytes of 8 rows of a Q or K tile
+    static constexpr int kVGroup = (kKeys / 8) * 128 + 16;       // of 8 head values of a V tile: the 16 spread the stores' banks
+    static constexpr int kBuf = (kKeys / 8) * kQGroup > (D / 8) * kVGroup ? (kKeys / 8) * kQGroup : (D / 8) * kVGroup;
+    alignas(1024) unsigned char q[2][16 * kQGroup];
+    alignas(128) unsigned char kv[kExpanded][(kBuf + 127) / 128 * 128];
+    alignas(128) unsigned char raw[kRawStages][kKeys * (D + 8)];
+    uint64_t raw_full[kRawStages], raw_empty[kRawStages], kv_full[kExpanded], kv_empty[kExpanded];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], fin;
+    uint32_t valid[kInfo];                                       // per tile: which groups of 16 tokens have a page
+    uint32_t tmem;
+    int dead;
+    TileCursor cur[kTileThreads / 32];
+};
+
+// The next item of the run, or false: rows block rb of request b, kv head kh, key tiles lo + [t0, t1).  Each warp keeps
+// its own in shared memory (the expanding and issuing warps have few registers); lane 0 moves it on.
+__device__ __forceinline__ bool next_item(const AttnArgs& a, const TilePlan& p, TileCursor* cur) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        TileCursor& c = *cur;
+        c.more = c.u < c.u1;
+        if (c.more) {
+            const long long pu = p.unit_start[c.pair];
+            const int n = (int)((p.unit_start[c.pair + 1] - pu) / a.cache.n_kv_heads);
+            c.b = p.pair_b[c.pair];
+            c.rb = c.pair - p.pair_start[c.b];
+            const long long off = c.u - pu;
+            c.kh = (int)(off / n);
+            c.t0 = (int)(off - (long long)c.kh * n);
+            c.t1 = (int)min((long long)n, c.t0 + (c.u1 - c.u));
+            c.q0 = a.q_start[c.b], c.q_len = a.q_start[c.b + 1] - c.q0, c.kv_len = a.kv_len[c.b];
+            int hi;
+            const int r0 = c.rb * kRows, rows = c.q_len * a.group;
+            key_tiles(a, c.q_len, c.kv_len, r0, min(r0 + kRows, rows), &c.lo, &hi);
+            for (int x = 0; x < 2; ++x) {
+                c.s[x] = c.e[x] = c.t0;
+                if (r0 + 128 * x >= rows) continue;
+                int lo;
+                key_tiles(a, c.q_len, c.kv_len, r0 + 128 * x, min(r0 + 128 * x + 128, rows), &lo, &hi);
+                const int s = max(lo - c.lo, c.t0), e = min(hi - c.lo, c.t1);
+                if (s < e) c.s[x] = s, c.e[x] = e;
             }
+            c.whole = c.t0 == 0 && c.t1 == n;
+            c.u += c.t1 - c.t0;
+            if (c.t1 == n && c.kh == a.cache.n_kv_heads - 1) ++c.pair;
         }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int i = 0; i < D / 32; ++i) a.out[row + lane + 32 * i] = f32_to_bf16(o[i] * inv);
+    __syncwarp();
+    return cur->more;
+}
+
+__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, int* dead) {
+    const uint32_t addr = qmoe_tc::smem_u32(bar);
+    for (uint32_t it = 0; it < kWaitLimit; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(addr), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((it & 63) == 63 && *(volatile int*)dead) return false;
+    }
+    *(volatile int*)dead = 1;
+    attn_set_error(QMOE_ETIMEOUT);
+    return false;
+}
+
+__device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// Ends the loads before it; naming the registers keeps their uses behind it.
+__device__ __forceinline__ void tmem_wait_load(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Two fp32 values in one 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float* lo, float* hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(p)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// One lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, P;\n}\n" : "=r"(p));
+    return p != 0;
+}
+
+// D += A B, the operands' descriptors as low words (plus off) and a high word: built at the instruction, so that they
+// are not all kept in registers across the loop.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t off,
+                                       uint32_t idesc, uint32_t accum) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b32 x, y;\n .reg .b64 A, B;\n setp.ne.b32 p, %7, 0;\n"
+        " add.u32 x, %1, %5;\n add.u32 y, %3, %5;\n mov.b64 A, {x, %2};\n mov.b64 B, {y, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], A, B, %6, p;\n}\n" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(off), "r"(idesc), "r"(accum)
+        : "memory");
+}
+
+// The same with A from tensor memory (fp16 pairs along K in 32-bit columns, from a + a_off).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t a_off, uint32_t b_lo, uint32_t b_hi, uint32_t off,
+                                       uint32_t idesc, uint32_t accum) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b32 x, y;\n .reg .b64 B;\n setp.ne.b32 p, %7, 0;\n"
+        " add.u32 x, %1, %2;\n add.u32 y, %3, %5;\n mov.b64 B, {y, %4};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [x], B, %6, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(a_off), "r"(b_lo), "r"(b_hi), "r"(off), "r"(idesc), "r"(accum)
+        : "memory");
+}
+
+// Four registers of a word of codes, (value 8w + 2i, value 8w + 2i + 1) each, as the integers 0..15 in fp16: 1024 + u
+// (1024 + 16 u one nibble up) is an or into fp16's pattern of 1024, and taking the 1024 off is exact.
+__device__ __forceinline__ void code_integers(uint32_t w, __half2 (&u)[4]) {
+    const uint32_t x[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x64006400u, ((w >> 8) & 0x000F000Fu) | 0x64006400u,
+                           ((w >> 8) & 0x00F000F0u) | 0x64006400u};
+    const __half2 one = __float2half2_rn(1024.f), off = __float2half2_rn(-64.f), sixteenth = __float2half2_rn(0.0625f);
+    u[0] = __hsub2(*(const __half2*)&x[0], one);
+    u[1] = __hfma2(*(const __half2*)&x[1], sixteenth, off);
+    u[2] = __hsub2(*(const __half2*)&x[2], one);
+    u[3] = __hfma2(*(const __half2*)&x[3], sixteenth, off);
+}
+
+__device__ __forceinline__ uint32_t h2(const __half2& h) { return *(const uint32_t*)&h; }
+
+// In key group (of 8) o of a V tile, place i holds key i ^ v_swap(o): the expanding lanes of four groups then read their
+// words from different banks, and the softmax packs its pairs in the same order.
+template <int D>
+__host__ __device__ constexpr int v_swap(int o) {
+    return D == 128 ? (o & 1) : (o & 3);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TilePlan plan, float* parts) {
+    using Sh = TileShared<D>;
+    extern __shared__ unsigned char smem_raw[];
+    Sh& sh = *(Sh*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int n_pairs = plan.pair_start[a.B];
+    const long long total = plan.unit_start[n_pairs];
+    const long long chunk = max(1LL, (total + gridDim.x - 1) / gridDim.x);
+    const long long first_unit = (long long)blockIdx.x * chunk, end_unit = min(first_unit + chunk, total);
+    if (first_unit >= end_unit) return;
+    if (tid == 0) {
+        for (int i = 0; i < kRawStages; ++i) qmoe_tc::mbar_init(&sh.raw_full[i], 1), qmoe_tc::mbar_init(&sh.raw_empty[i], 4);
+        for (int i = 0; i < kExpanded; ++i) qmoe_tc::mbar_init(&sh.kv_full[i], 128), qmoe_tc::mbar_init(&sh.kv_empty[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            qmoe_tc::mbar_init(&sh.q_full[i], 128);
+            qmoe_tc::mbar_init(&sh.s_full[i], 1);
+            qmoe_tc::mbar_init(&sh.p_full[i], 128);
+            qmoe_tc::mbar_init(&sh.o_full[i], 1);
+        }
+        qmoe_tc::mbar_init(&sh.fin, 1);
+        sh.dead = 0;
+        qmoe_tc::fence_mbar_init();
+    }
+    if (warp == kIssueWarp) qmoe_tc::tmem_alloc(&sh.tmem, 512);
+    if (warp == kCopyWarp) {
+        // last pair that starts at or before the run's first unit: 32 probes at a time
+        int lo = 0, hi = n_pairs;     // unit_start[lo] <= u < unit_start[hi]
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, at = min(lo + lane * step, hi);
+            const unsigned below = __ballot_sync(QMOE_FULL_MASK, plan.unit_start[at] <= first_unit);
+            const int k = 31 - __clz(below);      // bit 0 is always set
+            const int nlo = min(lo + k * step, hi);
+            hi = min(nlo + step, hi);
+            lo = nlo;
+        }
+        if (lane < kTileThreads / 32) sh.cur[lane].u = first_unit, sh.cur[lane].u1 = end_unit, sh.cur[lane].pair = lo;
+    }
+    __syncthreads();
+    qmoe_tc::tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    TileCursor& c = sh.cur[warp];
+
+    if (warp < kExpandWarp) {
+        // ---- softmax: a thread per query row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        const int x = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;           // 32 lanes a warp, lane index in bits 16..
+        const uint32_t ts = tmem + x * 128 + lanes, to = tmem + 256 + x * 128 + lanes;
+        uint32_t n_s = 0, n_items = 0;                               // phases of s_full, o_full passed
+        int tiles = 0;                                               // tiles of the run before the item
+        bool ok = true;
+        while (ok && next_item(a, plan, &c)) {
+            const int t_s = c.s[x], t_e = c.e[x], t0 = c.t0, lo = c.lo;
+            const int r = c.rb * kRows + x * 128 + row;
+            const bool live = r < c.q_len * a.group;
+            const int n = r / a.group, h = c.kh * a.group + r - n * a.group;
+            const int64_t base = ((int64_t)(c.q0 + n) * a.n_q_heads + h) * D;
+            float factor = 0.f, m = kNoMax, l = 0.f;
+            if (t_e > t_s) {
+                // the row into the tile, its largest magnitude scaled to [2^14, 2^15)
+                uint4 raw[D / 8];
+                float mx = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    raw[i] = live ? *(const uint4*)(a.q + base + 8 * i) : make_uint4(0, 0, 0, 0);
+                    mx = fmaxf(mx, fmaxf(fmaxf(fabsf(bf16_lo(raw[i].x)), fabsf(bf16_hi(raw[i].x))), fmaxf(fabsf(bf16_lo(raw[i].y)), fabsf(bf16_hi(raw[i].y)))));
+                    mx = fmaxf(mx, fmaxf(fmaxf(fabsf(bf16_lo(raw[i].z)), fabsf(bf16_hi(raw[i].z))), fmaxf(fabsf(bf16_lo(raw[i].w)), fabsf(bf16_hi(raw[i].w)))));
+                }
+                const int e = mx > 0.f ? min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 126) : 0;
+                const float up = a.scale < 0.f ? -pow2i(14 - e) : pow2i(14 - e);
+                // not 0, so that a masked score's -inf stays one
+                factor = fmaxf(fabsf(a.scale) * 1.4426950408889634f * pow2i(e - 14), 1.2e-38f);
+                unsigned char* dst = sh.q[x] + (row >> 3) * Sh::kQGroup + (row & 7) * 16;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    *(uint4*)(dst + i * 128) = make_uint4(half2_bits(bf16_lo(raw[i].x) * up, bf16_hi(raw[i].x) * up),
+                                                          half2_bits(bf16_lo(raw[i].y) * up, bf16_hi(raw[i].y) * up),
+                                                          half2_bits(bf16_lo(raw[i].z) * up, bf16_hi(raw[i].z) * up),
+                                                          half2_bits(bf16_lo(raw[i].w) * up, bf16_hi(raw[i].w) * up));
+                qmoe_tc::fence_async_shared();
+                mbar_arrive(&sh.q_full[x]);
+            }
+            const int first = a.causal ? c.kv_len - c.q_len : c.kv_len - 1;
+            const int pos = a.causal ? first + n : first;
+            const int k_hi = min(pos, c.kv_len - 1), k_lo = a.window ? pos - a.window + 1 : 0;    // keys seen: [k_lo, k_hi]
+            for (int t = t_s; t < t_e && ok; ++t) {
+                ok = tile_wait(&sh.s_full[x], n_s & 1, &sh.dead);
+                if (!__all_sync(QMOE_FULL_MASK, ok)) {
+                    ok = false;
+                    break;
+                }
+                ++n_s;
+                qmoe_tc::tc_fence_after();
+                uint32_t sr[kKeys];
+#pragma unroll
+                for (int i = 0; i < kKeys; i += 32) tmem_load32(ts + i, sr + i);
+#pragma unroll
+                for (int i = 0; i < kKeys; i += 32) tmem_wait_load(sr + i);
+                const int j0 = (lo + t) * kKeys;
+                const uint32_t valid = sh.valid[(tiles + t - t0) % kInfo];
+                if (j0 + kKeys - 1 > k_hi || j0 < k_lo || valid != 0xFFu) {
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i)
+                        if (j0 + i > k_hi || j0 + i < k_lo || !((valid >> (i >> 4)) & 1)) sr[i] = 0xFF800000u;
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < kKeys; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])));
+                mx *= factor;
+                if (__any_sync(QMOE_FULL_MASK, mx > m + kSlack)) {
+                    const float m2 = fmaxf(m, mx), f = ex2(m - m2);
+                    m = m2;
+                    l *= f;
+                    if (t > t_s) {
+#pragma unroll 1
+                        for (int i = 0; i < D; i += 16) {
+                            uint32_t orr[16];
+                            tmem_load16(to + i, orr);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) orr[j] = __float_as_uint(__uint_as_float(orr[j]) * f);
+                            tmem_store16(to + i, orr);
+                        }
+                    }
+                }
+                const float nb = 6.f - m;
+                // the fused product is not rounded before m is taken off: where m is so large that this shows, round first
+                float mul = factor;
+                if (__any_sync(QMOE_FULL_MASK, fabsf(m) > 65536.f && m != kNoMax)) {
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i) sr[i] = __float_as_uint(__uint_as_float(sr[i]) * factor);
+                    mul = 1.f;
+                }
+                const uint64_t mul2 = pair(mul, mul), nb2 = pair(nb, nb);
+                uint64_t l2[2] = {0, 0};
+#pragma unroll
+                for (int i = 0; i < kKeys; i += 2) {
+                    float e0, e1;
+                    unpair(fma2(pair(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), mul2, nb2), &e0, &e1);
+                    e0 = ex2(e0), e1 = ex2(e1);
+                    l2[(i >> 1) & 1] = add2(l2[(i >> 1) & 1], pair(e0, e1));
+                    sr[i] = __float_as_uint(e0), sr[i + 1] = __float_as_uint(e1);
+                }
+                {
+                    float e0, e1;
+                    unpair(add2(l2[0], l2[1]), &e0, &e1);
+                    l += e0 + e1;
+                }
+                uint32_t pr[kKeys / 2];
+#pragma unroll
+                for (int i = 0; i < kKeys / 2; ++i) {
+                    const int o = i >> 2, at = (2 * i) ^ v_swap<D>(o), at1 = (2 * i + 1) ^ v_swap<D>(o);
+                    pr[i] = half2_bits(__uint_as_float(sr[at]), __uint_as_float(sr[at1]));
+                }
+                tmem_store32(ts, pr);
+                tmem_store32(ts + 32, pr + 32);
+                tmem_wait_store();
+                qmoe_tc::tc_fence_before();
+                mbar_arrive(&sh.p_full[x]);
+            }
+            tiles += c.t1 - c.t0;
+            if (!ok) break;
+            const bool some = t_e > t_s;
+            if (some) {
+                ok = tile_wait(&sh.o_full[x], n_items & 1, &sh.dead);
+                if (!__all_sync(QMOE_FULL_MASK, ok)) break;
+                ++n_items;
+                qmoe_tc::tc_fence_after();
+            }
+            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+            float* part = part_of(parts, blockIdx.x, t0 == 0 ? 1 : 0, kRows, D) + (size_t)(x * 128 + row) * D;
+#pragma unroll
+            for (int i = 0; i < D; i += 32) {
+                uint32_t orr[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) orr[j] = 0;
+                if (some) {
+                    tmem_load32(to + i, orr);
+                    tmem_wait_load(orr);
+                }
+                if (live && c.whole) {
+                    uint4* dst = (uint4*)(a.out + base + i);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(orr[8 * j + 2 * k]) * inv, __uint_as_float(orr[8 * j + 2 * k + 1]) * inv);
+                            w[k] = *(const uint32_t*)&v;
+                        }
+                        dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else if (live) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) *(uint4*)(part + i + 4 * j) = make_uint4(orr[4 * j], orr[4 * j + 1], orr[4 * j + 2], orr[4 * j + 3]);
+                }
+            }
+            if (live && !c.whole)
+                *(float2*)(part_of(parts, blockIdx.x, t0 == 0 ? 1 : 0, kRows, D) + (size_t)kRows * D + 2 * (x * 128 + row)) = make_float2(m, l);
+            qmoe_tc::tc_fence_before();
+        }
+    } else if (warp < kIssueWarp) {
+        // ---- expand codes to fp16 tiles
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        const int i = tid - kExpandWarp * 32;
+        const int P = 1 << a.cache.page_shift, P1 = P - 1;
+        // keys: thread i holds key i; which 16-byte piece first differs with the row, so that eight rows read different banks
+        const uint32_t k_page = (uint32_t)(i >> a.cache.page_shift) * a.cache.head_bytes;
+        const uint32_t k_row = k_page + (uint32_t)(i & P1) * (D / 2), k_pair = k_page + (uint32_t)P * D + (i & P1) * 4;
+        constexpr int CH = D / 32, RP = 256 / D;
+        const int c0 = (i & 7) / RP;
+        const uint32_t k_dst = (uint32_t)(i >> 3) * Sh::kQGroup + (i & 7) * 16;
+        // values: lane (o4, p) of warp w holds keys 8 o .. 8 o + 7, o = 4 w + o4, and words p (and p + 8)
+        const int p = lane & 7, o4 = lane >> 3, o = 4 * (warp - kExpandWarp) + o4;
+        const uint32_t v_page = (uint32_t)((8 * o) >> a.cache.page_shift) * a.cache.head_bytes;
+        const int v_in = (8 * o) & P1;
+        const uint32_t v_row = v_page + (uint32_t)(P + v_in) * (D / 2), v_pair = v_page + (uint32_t)P * D + (P + v_in) * 4;
+        const int swap = v_swap<D>(o4);
+        uint32_t tile = 0, buf = 0, phase = 0;       // raw tiles done; next expanded buffer and its phase
+        bool ok = true;
+        while (ok && next_item(a, plan, &c)) {
+            for (int t = c.t0; t < c.t1; ++t, ++tile) {
+                const int st = tile % kRawStages;
+                ok = tile_wait(&sh.raw_full[st], (tile / kRawStages) & 1, &sh.dead);
+                if (ok && phase > 0) ok = tile_wait(&sh.kv_empty[buf], (phase - 1) & 1, &sh.dead);
+                if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
+                const unsigned char* raw = sh.raw[st];
+                const int j0 = (c.lo + t) * kKeys;
+                const uint32_t valid = sh.valid[tile % kInfo];
+                {
+                    uint32_t sz = *(const uint32_t*)(raw + k_pair);
+                    if (j0 + i >= c.kv_len || !((valid >> (i >> 4)) & 1)) sz = 0;
+                    const __half2 s2 = __half2half2(__ushort_as_half((uint16_t)sz)), z2 = __half2half2(__ushort_as_half((uint16_t)(sz >> 16)));
+                    unsigned char* dst = sh.kv[buf] + k_dst;
+#pragma unroll
+                    for (int s = 0; s < CH; ++s) {
+                        const int ch = (c0 + s) & (CH - 1);
+                        const uint4 w4 = *(const uint4*)(raw + k_row + ch * 16);
+                        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            __half2 u[4];
+                            code_integers(w[k], u);
+                            *(uint4*)(dst + (4 * ch + k) * 128) = make_uint4(h2(__hfma2(u[0], s2, z2)), h2(__hfma2(u[1], s2, z2)),
+                                                                            h2(__hfma2(u[2], s2, z2)), h2(__hfma2(u[3], s2, z2)));
+                        }
+                    }
+                }
+                qmoe_tc::fence_async_shared();
+                mbar_arrive(&sh.kv_full[buf]);
+                if (++buf == kExpanded) buf = 0, ++phase;
+                ok = phase == 0 || tile_wait(&sh.kv_empty[buf], (phase - 1) & 1, &sh.dead);
+                if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
+                {
+                    __half2 s2[4], z2[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t a0 = *(const uint32_t*)(raw + v_pair + ((2 * k) ^ swap) * 4), a1 = *(const uint32_t*)(raw + v_pair + ((2 * k + 1) ^ swap) * 4);
+                        const bool page_ok = (valid >> (o >> 1)) & 1;
+                        if (!page_ok || j0 + 8 * o + ((2 * k) ^ swap) >= c.kv_len) a0 = 0;
+                        if (!page_ok || j0 + 8 * o + ((2 * k + 1) ^ swap) >= c.kv_len) a1 = 0;
+                        const uint32_t ss = __byte_perm(a0, a1, 0x5410), zz = __byte_perm(a0, a1, 0x7632);
+                        s2[k] = *(const __half2*)&ss, z2[k] = *(const __half2*)&zz;
+                    }
+#pragma unroll
+                    for (int jj = 0; jj < D / 64; ++jj) {
+                        const int word = D == 128 ? p + 8 * (jj ^ (o4 >> 1)) : p;
+                        uint32_t w[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) w[k] = *(const uint32_t*)(raw + v_row + (k ^ swap) * (D / 2) + word * 4);
+                        unsigned char* dst = sh.kv[buf] + word * Sh::kVGroup + o * 128;
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            uint32_t r[4][4];      // [value 2 v + hh][pair of keys]
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                __half2 u[4];
+                                code_integers(__byte_perm(w[2 * k], w[2 * k + 1], hh ? 0x7632 : 0x5410), u);
+#pragma unroll
+                                for (int v = 0; v < 4; ++v) r[v][k] = h2(__hfma2(u[v], s2[k], z2[k]));
+                            }
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) *(uint4*)(dst + (2 * v + hh) * 16) = make_uint4(r[v][0], r[v][1], r[v][2], r[v][3]);
+                        }
+                    }
+                }
+                qmoe_tc::fence_async_shared();
+                mbar_arrive(&sh.kv_full[buf]);
+                if (++buf == kExpanded) buf = 0, ++phase;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.raw_empty[st]);
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == kIssueWarp) {
+            // ---- issue the products (the warp stays converged; one elected lane issues and commits)
+            constexpr uint32_t id_s = qmoe_tc::idesc_f16(128, kKeys, false, false), id_o = qmoe_tc::idesc_f16(128, D, false, false);
+            const uint64_t qd = qmoe_tc::umma_desc(qmoe_tc::smem_u32(sh.q[0]), 128, Sh::kQGroup);
+            const uint64_t kd = qmoe_tc::umma_desc(qmoe_tc::smem_u32(sh.kv[0]), 128, Sh::kQGroup);
+            const uint64_t vd = qmoe_tc::umma_desc(qmoe_tc::smem_u32(sh.kv[0]), 128, Sh::kVGroup);
+            constexpr uint32_t q_step = sizeof(sh.q[0]) / 16, kv_step = sizeof(sh.kv[0]) / 16;
+            uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
+            uint32_t kb = 0, kph = 0, vb = 0, vph = 0;      // buffers (and phases) of the next keys and of the values after them
+            bool ok = true;
+            while (ok && next_item(a, plan, &c)) {
+                const int s[2] = {c.s[0], c.s[1]}, e[2] = {c.e[0], c.e[1]}, t0 = c.t0, t1 = c.t1;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (e[x] > s[x]) ok = ok && tile_wait(&sh.q_full[x], n_q[x]++ & 1, &sh.dead);
+                // step t: S of tile t + 1 follows O of tile t
+                for (int t = t0 - 1; t < t1; ++t) {
+                    if (t >= t0) ok = ok && tile_wait(&sh.kv_full[vb], vph, &sh.dead);
+                    bool have_k = t + 1 >= t1;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (t >= s[x] && t < e[x]) {
+                            ok = ok && tile_wait(&sh.p_full[x], n_p[x]++ & 1, &sh.dead);
+                            if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
+                            qmoe_tc::tc_fence_after();
+                            if (elect_one()) {
+                                const uint32_t v = (uint32_t)vd + vb * kv_step;
+#pragma unroll
+                                for (int k = 0; k < kKeys / 16; ++k)
+                                    mma_ts(tmem + 256 + x * 128, tmem + x * 128, k * 8, v, (uint32_t)(vd >> 32), k * 16, id_o, k > 0 || t > s[x]);
+                                if (t + 1 == e[x]) qmoe_tc::mma_commit(&sh.o_full[x]);
+                            }
+                            __syncwarp();
+                        }
+                        if (!have_k) ok = ok && tile_wait(&sh.kv_full[kb], kph, &sh.dead);
+                        have_k = true;
+                        if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
+                        if (t + 1 >= s[x] && t + 1 < e[x]) {
+                            qmoe_tc::tc_fence_after();
+                            if (elect_one()) {
+                                const uint32_t q = (uint32_t)qd + x * q_step, kk = (uint32_t)kd + kb * kv_step;
+#pragma unroll
+                                for (int k = 0; k < D / 16; ++k) mma_ss(tmem + x * 128, q, (uint32_t)(qd >> 32), kk, (uint32_t)(kd >> 32), k * 16, id_s, k > 0);
+                                qmoe_tc::mma_commit(&sh.s_full[x]);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    if (!ok) break;
+                    if (elect_one()) {
+                        if (t >= t0) qmoe_tc::mma_commit(&sh.kv_empty[vb]);
+                        if (t + 1 < t1) qmoe_tc::mma_commit(&sh.kv_empty[kb]);
+                    }
+                    __syncwarp();
+                    if (t + 1 < t1) {       // the values of tile t + 1 follow its keys, the keys of t + 2 those
+                        vb = kb + 1, vph = kph;
+                        if (vb == kExpanded) vb = 0, vph ^= 1;
+                        kb = vb + 1, kph = vph;
+                        if (kb == kExpanded) kb = 0, kph ^= 1;
+                    }
+                }
+            }
+            // everything issued has ended before tensor memory is freed
+            __syncwarp();
+            if (elect_one()) qmoe_tc::mma_commit(&sh.fin);
+            qmoe_tc::mbar_wait(&sh.fin, 0, kWaitLimit);
+        } else if (warp == kCopyWarp) {
+            // ---- copy pages: lane i the tile's i-th
+            const int per_tile = kKeys >> a.cache.page_shift, per_page = (1 << a.cache.page_shift) / 16;
+            uint32_t tile = 0;
+            bool ok = true;
+            while (ok && next_item(a, plan, &c)) {
+                for (int t = c.t0; t < c.t1; ++t, ++tile) {
+                    const int st = tile % kRawStages;
+                    const int blk = (c.lo + t) * per_tile + lane;
+                    const bool mine = lane < per_tile && (blk << a.cache.page_shift) < c.kv_len;
+                    int page = -1;
+                    if (mine && blk < a.max_blocks) page = a.table[(int64_t)c.b * a.max_blocks + blk];
+                    const bool good = page >= 0 && page < a.cache.n_pages;
+                    if (mine && !good) attn_set_error(QMOE_EINVAL);
+                    const unsigned mask = __ballot_sync(QMOE_FULL_MASK, good);
+                    if (tile >= kRawStages) ok = tile_wait(&sh.raw_empty[st], (tile / kRawStages - 1) & 1, &sh.dead);
+                    ok = __all_sync(QMOE_FULL_MASK, ok);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        uint32_t v = 0;
+                        for (int i = 0; i < per_tile; ++i)
+                            if ((mask >> i) & 1) v |= ((1u << per_page) - 1) << (i * per_page);
+                        sh.valid[tile % kInfo] = v;
+                        mbar_expect(&sh.raw_full[st], (uint32_t)__popc(mask) * a.cache.head_bytes);
+                    }
+                    __syncwarp();
+                    if (good)
+                        bulk_copy(sh.raw[st] + lane * a.cache.head_bytes, kv4::head_ptr(a.cache, page, c.kh), a.cache.head_bytes, &sh.raw_full[st]);
+                }
+            }
+            // copies in flight land before the block's memory goes away
+            for (uint32_t i = tile > kRawStages ? tile - kRawStages : 0; i < tile; ++i)
+                qmoe_tc::mbar_wait(&sh.raw_full[i % kRawStages], (i / kRawStages) & 1, kWaitLimit);
+        }
+    }
+    qmoe_tc::tc_fence_before();
+    __syncthreads();
+    if (warp == kIssueWarp) {
+        __syncwarp();
+        qmoe_tc::tc_fence_after();
+        qmoe_tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the parts of items that several blocks of tile_kernel shared.  One block per (pair, kv head).
+template <int D>
+__global__ void __launch_bounds__(256) tile_combine_kernel(AttnArgs a, TilePlan plan, int n_ctas, const float* parts) {
+    const int pair = blockIdx.x / a.cache.n_kv_heads, kh = blockIdx.x - pair * a.cache.n_kv_heads;
+    const int n_pairs = plan.pair_start[a.B];
+    if (pair >= n_pairs) return;
+    const long long total = plan.unit_start[n_pairs], chunk = max(1LL, (total + n_ctas - 1) / n_ctas);
+    const long long pu = plan.unit_start[pair], n = (plan.unit_start[pair + 1] - pu) / a.cache.n_kv_heads;
+    const long long u0 = pu + kh * n, u1 = u0 + n;
+    const int c0 = (int)(u0 / chunk), c1 = (int)((u1 - 1) / chunk);
+    if (c0 == c1) return;
+    const int b = plan.pair_b[pair], rb = pair - plan.pair_start[b], q0 = a.q_start[b];
+    const int rows = min(kRows, (a.q_start[b + 1] - q0) * a.group - rb * kRows);
+    for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
+        const int r = i / (D / 4), d0 = (i - r * (D / 4)) * 4;
+        join_parts<D>(a, parts, c0, c1, u0, chunk, kRows, r, d0, q0, rb * kRows + r, kh);
+    }
 }
 
 // Query rows (a multiple of 8) that the few-row path takes per (request, kv head): the batch's largest where 32
@@ -728,6 +1388,48 @@ int launch_decode(const AttnArgs& a, float* parts, cudaStream_t st) {
                             "combine_kernel");
 }
 
+// Workspace of the tile path: the plan, then the blocks' parts.  max_pairs bounds the sum of ceil(rows / 256).
+struct TileWs {
+    TilePlan plan;
+    float* parts;
+    size_t bytes;
+};
+
+TileWs tile_ws(void* base, int B, int group, int head_dim, int n_q_tokens) {
+    TileWs w{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        void* p = base ? (void*)((char*)base + off) : nullptr;
+        off += (bytes + 255) & ~(size_t)255;
+        return p;
+    };
+    const long long pairs = (long long)n_q_tokens * group / kRows + B;
+    w.plan.max_pairs = (int)std::min(pairs, 0x7FFFFFFELL);
+    w.plan.pair_start = (int32_t*)take(sizeof(int32_t) * ((size_t)B + 1));
+    w.plan.unit_start = (long long*)take(sizeof(long long) * ((size_t)w.plan.max_pairs + 1));
+    w.plan.pair_b = (int32_t*)take(sizeof(int32_t) * (size_t)w.plan.max_pairs);
+    w.parts = (float*)take((size_t)qmoe::sm_count() * 2 * kRows * (head_dim + 2) * sizeof(float));
+    w.bytes = off;
+    return w;
+}
+
+template <int D>
+int launch_tiles(const AttnArgs& a, const TileWs& w, int min_rows, cudaStream_t st) {
+    const int smem = (int)sizeof(TileShared<D>) + 1024, blocks = qmoe::sm_count();
+    int rc = qmoe::smem_attr((const void*)tile_kernel<D>, smem, "attention attr");
+    if (rc) return rc;
+    const long long items = (long long)w.plan.max_pairs * a.cache.n_kv_heads;
+    if (items > 0x7FFFFFFFLL) return qmoe::fail(QMOE_EINVAL, "kv4_attention: batch too large");
+    tile_plan_kernel<<<1, kPlanTile, 0, st>>>(a, w.plan, min_rows);
+    tile_kernel<D><<<blocks, kTileThreads, smem, st>>>(a, w.plan, w.parts);
+    if ((rc = qmoe::launch_check("tile_kernel"))) return rc;
+    tile_combine_kernel<D><<<(unsigned)items, 256, 0, st>>>(a, w.plan, blocks, w.parts);
+    return qmoe::launch_check("tile_combine_kernel");
+}
+
+// Whether some request of the batch has more rows than the few-row path takes.
+bool has_tiles(int group, int max_q, int rows) { return (long long)group * max_q > rows; }
+
 int check_sizes(const char* who, int B, int n_q_heads, int n_kv_heads, int head_dim, int n_q_tokens, int max_q, int max_kv) {
     if (head_dim != 64 && head_dim != 128) return qmoe::fail(QMOE_EUNSUPPORTED, std::string(who) + ": head_dim must be 64 or 128");
     if (B < 0 || n_q_tokens < 0 || max_q < 0 || max_kv < 0 || n_kv_heads < 1 || n_q_heads < n_kv_heads ||
@@ -756,7 +1458,8 @@ extern "C" int kv4_attention_ws_size(int B, int n_q_heads, int n_kv_heads, int h
     if (!bytes) return qmoe::fail(QMOE_EINVAL, "kv4_attention_ws_size: NULL output");
     const int rc = check_sizes("kv4_attention_ws_size", B, n_q_heads, n_kv_heads, head_dim, n_q_tokens, max_q, max_kv);
     if (rc) return rc;
-    *bytes = decode_ws(decode_rows(n_q_heads / n_kv_heads, max_q), head_dim);
+    const int group = n_q_heads / n_kv_heads, rows = decode_rows(group, max_q);
+    *bytes = ((decode_ws(rows, head_dim) + 255) & ~(size_t)255) + (has_tiles(group, max_q, rows) ? tile_ws(nullptr, B, group, head_dim, n_q_tokens).bytes : 0);
     return QMOE_OK;
 }
 
@@ -779,19 +1482,16 @@ extern "C" int kv4_attention(const kv4_cache* cache, const void* q, int n_q_toke
     a.max_blocks = max_blocks, a.max_q = max_q, a.max_kv = max_kv, a.scale = scale, a.causal = causal ? 1 : 0, a.window = window;
     cudaStream_t st = (cudaStream_t)stream;
     const int rows = decode_rows(a.group, max_q), D = cache->head_dim;
-    if (ws_bytes < decode_ws(rows, D)) return qmoe::fail(QMOE_ECAPACITY, "kv4_attention: workspace too small");
-    if (rows > 0 && (!workspace || !kv4::aligned16(workspace)))
-        return qmoe::fail(QMOE_EINVAL, "kv4_attention: workspace NULL or not 16-byte aligned");
+    const bool tiles = has_tiles(a.group, max_q, rows);
+    const size_t few = (decode_ws(rows, D) + 255) & ~(size_t)255;
+    const TileWs tw = tiles ? tile_ws((char*)workspace + few, B, a.group, D, n_q_tokens) : TileWs{};
+    if (ws_bytes < few + tw.bytes) return qmoe::fail(QMOE_ECAPACITY, "kv4_attention: workspace too small");
+    if (!workspace || !kv4::aligned16(workspace)) return qmoe::fail(QMOE_EINVAL, "kv4_attention: workspace NULL or not 16-byte aligned");
     if ((long long)B * cache->n_kv_heads > 0x7FFFFFFFLL) return qmoe::fail(QMOE_EINVAL, "kv4_attention: batch too large");
     float* parts = (float*)workspace;
     if (rows == 8) rc = D == 128 ? launch_decode<128, 1>(a, parts, st) : launch_decode<64, 1>(a, parts, st);
     if (rows == 16) rc = D == 128 ? launch_decode<128, 2>(a, parts, st) : launch_decode<64, 2>(a, parts, st);
     if (rows == 32) rc = D == 128 ? launch_decode<128, 4>(a, parts, st) : launch_decode<64, 4>(a, parts, st);
-    if (rc || (long long)a.group * max_q <= rows) return rc;
-    const dim3 grid((n_q_heads + 3) / 4, max_q, B);
-    if (D == 128)
-        attention_kernel<128><<<grid, 128, 0, st>>>(a, rows);
-    else
-        attention_kernel<64><<<grid, 128, 0, st>>>(a, rows);
-    return qmoe::launch_check("kv4_attention");
+    if (rc || !tiles) return rc;
+    return D == 128 ? launch_tiles<128>(a, tw, rows, st) : launch_tiles<64>(a, tw, rows, st);
 }
