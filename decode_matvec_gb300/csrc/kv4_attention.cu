@@ -733,11 +733,12 @@ struct TileCursor {
 
 template <int D>
 struct TileShared {
-    static constexpr int kQGroup = (D / 8) * 128;                // bytes of 8 rows of a Q or K tile
-    static constexpr int kVGroup = (kKeys / 8) * 128 + 16;       // of 8 head values of a V tile: the 16 spread the stores' banks
-    static constexpr int kBuf = (kKeys / 8) * kQGroup > (D / 8) * kVGroup ? (kKeys / 8) * kQGroup : (D / 8) * kVGroup;
-    alignas(1024) unsigned char q[2][16 * kQGroup];
-    alignas(128) unsigned char kv[kExpanded][(kBuf + 127) / 128 * 128];
+    // operand tiles in the 128-byte-swizzled K-major layout: atoms of 64 columns, a row of an atom 128 bytes, the 16-byte
+    // piece i of row r at place i ^ (r % 8)
+    static constexpr int kQAtom = 128 * 128, kVAtom = D * 128;      // Q and K (rows: queries, keys), V (rows: head values)
+    static constexpr int kBuf = 128 * D * 2;
+    alignas(1024) unsigned char q[2][kBuf];
+    alignas(1024) unsigned char kv[kExpanded][kBuf];
     alignas(128) unsigned char raw[kRawStages][kKeys * (D + 8)];
     uint64_t raw_full[kRawStages], raw_empty[kRawStages], kv_full[kExpanded], kv_empty[kExpanded];
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2], fin;
@@ -834,6 +835,28 @@ __device__ __forceinline__ void tmem_wait_load(uint32_t* r) {
                  : "memory");
 }
 
+// 64 columns, complete.
+__device__ __forceinline__ void tmem_load64(uint32_t taddr, uint32_t* r) {
+    tmem_load32(taddr, r);
+    tmem_load32(taddr + 32, r + 32);
+    tmem_wait_load(r);
+    tmem_wait_load(r + 32);
+}
+
+// Scores of 64 keys outside [lo, hi], or in a group of 16 whose bit of `groups` is clear, become -inf.
+__device__ __forceinline__ void mask64(uint32_t* s, int lo, int hi, uint32_t groups) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int l = lo - 32 * h, u = hi - 32 * h;
+        uint32_t keep = u < 0 ? 0u : u >= 31 ? 0xFFFFFFFFu : (2u << u) - 1u;
+        keep &= l <= 0 ? 0xFFFFFFFFu : l > 31 ? 0u : 0xFFFFFFFFu << l;
+        keep &= ((groups >> (2 * h)) & 1 ? 0xFFFFu : 0u) | ((groups >> (2 * h + 1)) & 1 ? 0xFFFF0000u : 0u);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (!((keep >> i) & 1)) s[32 * h + i] = 0xFF800000u;
+    }
+}
+
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -872,11 +895,22 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return d;
 }
 
+// Arrival of a warp: one operation on the barrier, after all lanes.
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // One lane of a converged warp, always the same one.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, P;\n}\n" : "=r"(p));
     return p != 0;
+}
+
+// Descriptor of a 128-byte-swizzled K-major operand, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_sw128(const void* p) {
+    return (uint64_t)((qmoe_tc::smem_u32(p) & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
 }
 
 // D += A B, the operands' descriptors as low words (plus off) and a high word: built at the instruction, so that they
@@ -936,11 +970,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
     if (first_unit >= end_unit) return;
     if (tid == 0) {
         for (int i = 0; i < kRawStages; ++i) qmoe_tc::mbar_init(&sh.raw_full[i], 1), qmoe_tc::mbar_init(&sh.raw_empty[i], 4);
-        for (int i = 0; i < kExpanded; ++i) qmoe_tc::mbar_init(&sh.kv_full[i], 128), qmoe_tc::mbar_init(&sh.kv_empty[i], 1);
+        for (int i = 0; i < kExpanded; ++i) qmoe_tc::mbar_init(&sh.kv_full[i], 4), qmoe_tc::mbar_init(&sh.kv_empty[i], 1);
         for (int i = 0; i < 2; ++i) {
-            qmoe_tc::mbar_init(&sh.q_full[i], 128);
+            qmoe_tc::mbar_init(&sh.q_full[i], 4);
             qmoe_tc::mbar_init(&sh.s_full[i], 1);
-            qmoe_tc::mbar_init(&sh.p_full[i], 128);
+            qmoe_tc::mbar_init(&sh.p_full[i], 4);
             qmoe_tc::mbar_init(&sh.o_full[i], 1);
         }
         qmoe_tc::mbar_init(&sh.fin, 1);
@@ -968,7 +1002,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
 
     if (warp < kExpandWarp) {
         // ---- softmax: a thread per query row
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int x = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;           // 32 lanes a warp, lane index in bits 16..
         const uint32_t ts = tmem + x * 128 + lanes, to = tmem + 256 + x * 128 + lanes;
@@ -996,15 +1029,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                 const float up = a.scale < 0.f ? -pow2i(14 - e) : pow2i(14 - e);
                 // not 0, so that a masked score's -inf stays one
                 factor = fmaxf(fabsf(a.scale) * 1.4426950408889634f * pow2i(e - 14), 1.2e-38f);
-                unsigned char* dst = sh.q[x] + (row >> 3) * Sh::kQGroup + (row & 7) * 16;
+                unsigned char* dst = sh.q[x] + row * 128;
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i)
-                    *(uint4*)(dst + i * 128) = make_uint4(half2_bits(bf16_lo(raw[i].x) * up, bf16_hi(raw[i].x) * up),
+                    *(uint4*)(dst + (i >> 3) * Sh::kQAtom + (((i & 7) ^ (row & 7)) << 4)) =
+                                               make_uint4(half2_bits(bf16_lo(raw[i].x) * up, bf16_hi(raw[i].x) * up),
                                                           half2_bits(bf16_lo(raw[i].y) * up, bf16_hi(raw[i].y) * up),
                                                           half2_bits(bf16_lo(raw[i].z) * up, bf16_hi(raw[i].z) * up),
                                                           half2_bits(bf16_lo(raw[i].w) * up, bf16_hi(raw[i].w) * up));
                 qmoe_tc::fence_async_shared();
-                mbar_arrive(&sh.q_full[x]);
+                arrive_warp(&sh.q_full[x]);
             }
             const int first = a.causal ? c.kv_len - c.q_len : c.kv_len - 1;
             const int pos = a.causal ? first + n : first;
@@ -1017,21 +1051,25 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                 }
                 ++n_s;
                 qmoe_tc::tc_fence_after();
-                uint32_t sr[kKeys];
-#pragma unroll
-                for (int i = 0; i < kKeys; i += 32) tmem_load32(ts + i, sr + i);
-#pragma unroll
-                for (int i = 0; i < kKeys; i += 32) tmem_wait_load(sr + i);
                 const int j0 = (lo + t) * kKeys;
                 const uint32_t valid = sh.valid[(tiles + t - t0) % kInfo];
-                if (j0 + kKeys - 1 > k_hi || j0 < k_lo || valid != 0xFFu) {
-#pragma unroll
-                    for (int i = 0; i < kKeys; ++i)
-                        if (j0 + i > k_hi || j0 + i < k_lo || !((valid >> (i >> 4)) & 1)) sr[i] = 0xFF800000u;
-                }
+                const bool edge = j0 + kKeys - 1 > k_hi || j0 < k_lo || valid != 0xFFu;
+                // two passes over the row, 64 keys at a time: the loops stay small enough for the instruction caches, which a
+                // fully unrolled row (and the other roles' code) would not fit
                 float mx = -INFINITY;
+#pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t sr[64];
+                    tmem_load64(ts + 64 * hf, sr);
+                    if (edge) mask64(sr, k_lo - j0 - 64 * hf, k_hi - j0 - 64 * hf, valid >> (4 * hf));
+                    float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < kKeys; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])));
+                    for (int i = 0; i < 64; i += 4) {
+                        m0 = fmaxf(m0, fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])));
+                        m1 = fmaxf(m1, fmaxf(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])));
+                    }
+                    mx = fmaxf(mx, fmaxf(m0, m1));
+                }
                 mx *= factor;
                 if (__any_sync(QMOE_FULL_MASK, mx > m + kSlack)) {
                     const float m2 = fmaxf(m, mx), f = ex2(m - m2);
@@ -1050,38 +1088,39 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                 }
                 const float nb = 6.f - m;
                 // the fused product is not rounded before m is taken off: where m is so large that this shows, round first
-                float mul = factor;
-                if (__any_sync(QMOE_FULL_MASK, fabsf(m) > 65536.f && m != kNoMax)) {
-#pragma unroll
-                    for (int i = 0; i < kKeys; ++i) sr[i] = __float_as_uint(__uint_as_float(sr[i]) * factor);
-                    mul = 1.f;
-                }
-                const uint64_t mul2 = pair(mul, mul), nb2 = pair(nb, nb);
+                const bool far = __any_sync(QMOE_FULL_MASK, fabsf(m) > 65536.f && m != kNoMax);
+                const uint64_t nb2 = pair(nb, nb), mul2 = far ? pair(1.f, 1.f) : pair(factor, factor);
                 uint64_t l2[2] = {0, 0};
+#pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t sr[64], pr[32];
+                    tmem_load64(ts + 64 * hf, sr);
+                    if (edge) mask64(sr, k_lo - j0 - 64 * hf, k_hi - j0 - 64 * hf, valid >> (4 * hf));
+                    if (far) {
 #pragma unroll
-                for (int i = 0; i < kKeys; i += 2) {
-                    float e0, e1;
-                    unpair(fma2(pair(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), mul2, nb2), &e0, &e1);
-                    e0 = ex2(e0), e1 = ex2(e1);
-                    l2[(i >> 1) & 1] = add2(l2[(i >> 1) & 1], pair(e0, e1));
-                    sr[i] = __float_as_uint(e0), sr[i + 1] = __float_as_uint(e1);
+                        for (int i = 0; i < 64; ++i) sr[i] = __float_as_uint(__uint_as_float(sr[i]) * factor);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2) {
+                        float e0, e1;
+                        unpair(fma2(pair(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), mul2, nb2), &e0, &e1);
+                        e0 = ex2(e0), e1 = ex2(e1);
+                        l2[(i >> 1) & 1] = add2(l2[(i >> 1) & 1], pair(e0, e1));
+                        sr[i] = __float_as_uint(e0), sr[i + 1] = __float_as_uint(e1);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        pr[i] = half2_bits(__uint_as_float(sr[(2 * i) ^ v_swap<D>(i >> 2)]), __uint_as_float(sr[(2 * i + 1) ^ v_swap<D>(i >> 2)]));
+                    tmem_store32(ts + 32 * hf, pr);      // over scores that both passes are done with
                 }
                 {
                     float e0, e1;
                     unpair(add2(l2[0], l2[1]), &e0, &e1);
                     l += e0 + e1;
                 }
-                uint32_t pr[kKeys / 2];
-#pragma unroll
-                for (int i = 0; i < kKeys / 2; ++i) {
-                    const int o = i >> 2, at = (2 * i) ^ v_swap<D>(o), at1 = (2 * i + 1) ^ v_swap<D>(o);
-                    pr[i] = half2_bits(__uint_as_float(sr[at]), __uint_as_float(sr[at1]));
-                }
-                tmem_store32(ts, pr);
-                tmem_store32(ts + 32, pr + 32);
                 tmem_wait_store();
                 qmoe_tc::tc_fence_before();
-                mbar_arrive(&sh.p_full[x]);
+                arrive_warp(&sh.p_full[x]);
             }
             tiles += c.t1 - c.t0;
             if (!ok) break;
@@ -1094,7 +1133,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
             }
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
             float* part = part_of(parts, blockIdx.x, t0 == 0 ? 1 : 0, kRows, D) + (size_t)(x * 128 + row) * D;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < D; i += 32) {
                 uint32_t orr[32];
 #pragma unroll
@@ -1126,7 +1165,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
         }
     } else if (warp < kIssueWarp) {
         // ---- expand codes to fp16 tiles
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         const int i = tid - kExpandWarp * 32;
         const int P = 1 << a.cache.page_shift, P1 = P - 1;
         // keys: thread i holds key i; which 16-byte piece first differs with the row, so that eight rows read different banks
@@ -1134,13 +1172,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
         const uint32_t k_row = k_page + (uint32_t)(i & P1) * (D / 2), k_pair = k_page + (uint32_t)P * D + (i & P1) * 4;
         constexpr int CH = D / 32, RP = 256 / D;
         const int c0 = (i & 7) / RP;
-        const uint32_t k_dst = (uint32_t)(i >> 3) * Sh::kQGroup + (i & 7) * 16;
-        // values: lane (o4, p) of warp w holds keys 8 o .. 8 o + 7, o = 4 w + o4, and words p (and p + 8)
-        const int p = lane & 7, o4 = lane >> 3, o = 4 * (warp - kExpandWarp) + o4;
+        const uint32_t k_dst = (uint32_t)i * 128;
+        // values: a thread holds keys 8 o .. 8 o + 7 of its words (of 8 values each); the eight octets of a quarter-warp
+        // store to different banks, and the words (and the order of the keys, v_swap) differ from octet to octet so that
+        // the loads read different banks too
+        const int ol = lane & 7, o = ol + 8 * ((warp - kExpandWarp) >> 1), ws = (lane >> 3) + 4 * (warp & 1);
+        const int word0 = D == 128 ? 2 * ((ws + 2 * (ol >> 1)) & 7) : (ws + 4 * (ol >> 2)) & 7;
         const uint32_t v_page = (uint32_t)((8 * o) >> a.cache.page_shift) * a.cache.head_bytes;
         const int v_in = (8 * o) & P1;
         const uint32_t v_row = v_page + (uint32_t)(P + v_in) * (D / 2), v_pair = v_page + (uint32_t)P * D + (P + v_in) * 4;
-        const int swap = v_swap<D>(o4);
+        const int swap = v_swap<D>(o);
         uint32_t tile = 0, buf = 0, phase = 0;       // raw tiles done; next expanded buffer and its phase
         bool ok = true;
         while (ok && next_item(a, plan, &c)) {
@@ -1157,7 +1198,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                     if (j0 + i >= c.kv_len || !((valid >> (i >> 4)) & 1)) sz = 0;
                     const __half2 s2 = __half2half2(__ushort_as_half((uint16_t)sz)), z2 = __half2half2(__ushort_as_half((uint16_t)(sz >> 16)));
                     unsigned char* dst = sh.kv[buf] + k_dst;
-#pragma unroll
+#pragma unroll 1
                     for (int s = 0; s < CH; ++s) {
                         const int ch = (c0 + s) & (CH - 1);
                         const uint4 w4 = *(const uint4*)(raw + k_row + ch * 16);
@@ -1166,13 +1207,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                         for (int k = 0; k < 4; ++k) {
                             __half2 u[4];
                             code_integers(w[k], u);
-                            *(uint4*)(dst + (4 * ch + k) * 128) = make_uint4(h2(__hfma2(u[0], s2, z2)), h2(__hfma2(u[1], s2, z2)),
+                            const int piece = 4 * ch + k;
+                            *(uint4*)(dst + (piece >> 3) * Sh::kQAtom + (((piece & 7) ^ (i & 7)) << 4)) = make_uint4(h2(__hfma2(u[0], s2, z2)), h2(__hfma2(u[1], s2, z2)),
                                                                             h2(__hfma2(u[2], s2, z2)), h2(__hfma2(u[3], s2, z2)));
                         }
                     }
                 }
                 qmoe_tc::fence_async_shared();
-                mbar_arrive(&sh.kv_full[buf]);
+                arrive_warp(&sh.kv_full[buf]);
                 if (++buf == kExpanded) buf = 0, ++phase;
                 ok = phase == 0 || tile_wait(&sh.kv_empty[buf], (phase - 1) & 1, &sh.dead);
                 if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
@@ -1187,14 +1229,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                         const uint32_t ss = __byte_perm(a0, a1, 0x5410), zz = __byte_perm(a0, a1, 0x7632);
                         s2[k] = *(const __half2*)&ss, z2[k] = *(const __half2*)&zz;
                     }
-#pragma unroll
+                    unsigned char* dst0 = sh.kv[buf] + (o >> 3) * Sh::kVAtom;
+#pragma unroll 1
                     for (int jj = 0; jj < D / 64; ++jj) {
-                        const int word = D == 128 ? p + 8 * (jj ^ (o4 >> 1)) : p;
+                        const int word = word0 + (D == 128 ? jj ^ (lane >> 4) : 0);
                         uint32_t w[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) w[k] = *(const uint32_t*)(raw + v_row + (k ^ swap) * (D / 2) + word * 4);
-                        unsigned char* dst = sh.kv[buf] + word * Sh::kVGroup + o * 128;
-#pragma unroll
+#pragma unroll 1
                         for (int hh = 0; hh < 2; ++hh) {
                             uint32_t r[4][4];      // [value 2 v + hh][pair of keys]
 #pragma unroll
@@ -1204,26 +1246,24 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
 #pragma unroll
                                 for (int v = 0; v < 4; ++v) r[v][k] = h2(__hfma2(u[v], s2[k], z2[k]));
                             }
+                            unsigned char* dst = dst0 + word * 1024 + hh * 128;
 #pragma unroll
-                            for (int v = 0; v < 4; ++v) *(uint4*)(dst + (2 * v + hh) * 16) = make_uint4(r[v][0], r[v][1], r[v][2], r[v][3]);
+                            for (int v = 0; v < 4; ++v)
+                                *(uint4*)(dst + v * 256 + (((ol ^ hh) ^ (2 * v)) << 4)) = make_uint4(r[v][0], r[v][1], r[v][2], r[v][3]);
                         }
                     }
                 }
                 qmoe_tc::fence_async_shared();
-                mbar_arrive(&sh.kv_full[buf]);
+                arrive_warp(&sh.kv_full[buf]);
                 if (++buf == kExpanded) buf = 0, ++phase;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.raw_empty[st]);
+                arrive_warp(&sh.raw_empty[st]);
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == kIssueWarp) {
             // ---- issue the products (the warp stays converged; one elected lane issues and commits)
             constexpr uint32_t id_s = qmoe_tc::idesc_f16(128, kKeys, false, false), id_o = qmoe_tc::idesc_f16(128, D, false, false);
-            const uint64_t qd = qmoe_tc::umma_desc(qmoe_tc::smem_u32(sh.q[0]), 128, Sh::kQGroup);
-            const uint64_t kd = qmoe_tc::umma_desc(qmoe_tc::smem_u32(sh.kv[0]), 128, Sh::kQGroup);
-            const uint64_t vd = qmoe_tc::umma_desc(qmoe_tc::smem_u32(sh.kv[0]), 128, Sh::kVGroup);
+            const uint64_t qd = desc_sw128(sh.q[0]), kvd = desc_sw128(sh.kv[0]);
             constexpr uint32_t q_step = sizeof(sh.q[0]) / 16, kv_step = sizeof(sh.kv[0]) / 16;
             uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
             uint32_t kb = 0, kph = 0, vb = 0, vph = 0;      // buffers (and phases) of the next keys and of the values after them
@@ -1244,10 +1284,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                             if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
                             qmoe_tc::tc_fence_after();
                             if (elect_one()) {
-                                const uint32_t v = (uint32_t)vd + vb * kv_step;
+                                const uint32_t v = (uint32_t)kvd + vb * kv_step;
 #pragma unroll
                                 for (int k = 0; k < kKeys / 16; ++k)
-                                    mma_ts(tmem + 256 + x * 128, tmem + x * 128, k * 8, v, (uint32_t)(vd >> 32), k * 16, id_o, k > 0 || t > s[x]);
+                                    mma_ts(tmem + 256 + x * 128, tmem + x * 128, k * 8, v, (uint32_t)(kvd >> 32), (k >> 2) * (Sh::kVAtom / 16) + (k & 3) * 2, id_o, k > 0 || t > s[x]);
                                 if (t + 1 == e[x]) qmoe_tc::mma_commit(&sh.o_full[x]);
                             }
                             __syncwarp();
@@ -1258,9 +1298,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                         if (t + 1 >= s[x] && t + 1 < e[x]) {
                             qmoe_tc::tc_fence_after();
                             if (elect_one()) {
-                                const uint32_t q = (uint32_t)qd + x * q_step, kk = (uint32_t)kd + kb * kv_step;
+                                const uint32_t q = (uint32_t)qd + x * q_step, kk = (uint32_t)kvd + kb * kv_step;
 #pragma unroll
-                                for (int k = 0; k < D / 16; ++k) mma_ss(tmem + x * 128, q, (uint32_t)(qd >> 32), kk, (uint32_t)(kd >> 32), k * 16, id_s, k > 0);
+                                for (int k = 0; k < D / 16; ++k) mma_ss(tmem + x * 128, q, (uint32_t)(qd >> 32), kk, (uint32_t)(kvd >> 32), (k >> 2) * (Sh::kQAtom / 16) + (k & 3) * 2, id_s, k > 0);
                                 qmoe_tc::mma_commit(&sh.s_full[x]);
                             }
                             __syncwarp();
@@ -1328,7 +1368,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
     }
 }
 
-// Joins the parts of items that several blocks of tile_kernel shared.  One block per (pair, kv head).
+// Joins the parts of items that several blocks of tile_kernel shared.  A few blocks per (pair, kv head).
+constexpr int kCombineSlices = 16;
+
 template <int D>
 __global__ void __launch_bounds__(256) tile_combine_kernel(AttnArgs a, TilePlan plan, int n_ctas, const float* parts) {
     const int pair = blockIdx.x / a.cache.n_kv_heads, kh = blockIdx.x - pair * a.cache.n_kv_heads;
@@ -1341,7 +1383,7 @@ __global__ void __launch_bounds__(256) tile_combine_kernel(AttnArgs a, TilePlan 
     if (c0 == c1) return;
     const int b = plan.pair_b[pair], rb = pair - plan.pair_start[b], q0 = a.q_start[b];
     const int rows = min(kRows, (a.q_start[b + 1] - q0) * a.group - rb * kRows);
-    for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
+    for (int i = blockIdx.y * 256 + threadIdx.x; i < rows * (D / 4); i += 256 * kCombineSlices) {
         const int r = i / (D / 4), d0 = (i - r * (D / 4)) * 4;
         join_parts<D>(a, parts, c0, c1, u0, chunk, kRows, r, d0, q0, rb * kRows + r, kh);
     }
@@ -1423,7 +1465,7 @@ int launch_tiles(const AttnArgs& a, const TileWs& w, int min_rows, cudaStream_t 
     tile_plan_kernel<<<1, kPlanTile, 0, st>>>(a, w.plan, min_rows);
     tile_kernel<D><<<blocks, kTileThreads, smem, st>>>(a, w.plan, w.parts);
     if ((rc = qmoe::launch_check("tile_kernel"))) return rc;
-    tile_combine_kernel<D><<<(unsigned)items, 256, 0, st>>>(a, w.plan, blocks, w.parts);
+    tile_combine_kernel<D><<<dim3((unsigned)items, kCombineSlices), 256, 0, st>>>(a, w.plan, blocks, w.parts);
     return qmoe::launch_check("tile_combine_kernel");
 }
 
