@@ -203,8 +203,8 @@ __device__ __forceinline__ float* part_of(float* parts, long long cta, int which
 template <int D, int NT>
 __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
     decode_kernel(AttnArgs a, int max_rows, float* parts) {
-    extern __shared__ unsigned char smem_raw[];
-    DecodeShared<D, NT>& sh = *(DecodeShared<D, NT>*)(((uintptr_t)smem_raw + 127) & ~(uintptr_t)127);
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    DecodeShared<D, NT>& sh = *(DecodeShared<D, NT>*)smem_raw;
     constexpr int W = D / 32;              // words of a key row that a lane reads
     constexpr int VW = D / 64;             // words of a value row that a lane reads
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -642,7 +642,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, in
 //
 // Work is dealt out as in the few-row path: all (rows, kv head) items' key tiles in a row, in equal
 // runs; items that several blocks share are joined by tile_combine_kernel.
-constexpr int kKeys = 128;                       // keys of a tile
+constexpr int kKeys = 128;                       // keys of a tile (expanded at once)
+constexpr int kStep = 64;                        // keys of a softmax step
 constexpr int kRows = 256;                       // query rows of an item
 constexpr int kTileThreads = 512;
 constexpr int kExpandWarp = 8, kIssueWarp = 12, kCopyWarp = 13;
@@ -657,13 +658,13 @@ struct TilePlan {
     int max_pairs;
 };
 
-// Key tiles [lo, hi) that rows [r0, r1) of a request see.
-__device__ __forceinline__ void key_tiles(const AttnArgs& a, int q_len, int kv_len, int r0, int r1, int* lo, int* hi) {
+// Blocks of `step` keys, [lo, hi), that rows [r0, r1) of a request see.
+__device__ __forceinline__ void key_steps(const AttnArgs& a, int q_len, int kv_len, int r0, int r1, int step, int* lo, int* hi) {
     const int first = a.causal ? kv_len - q_len : kv_len - 1;
     const int p0 = a.causal ? first + r0 / a.group : first, p1 = a.causal ? first + (r1 - 1) / a.group : first;
     const int k1 = min(kv_len, p1 + 1), k0 = a.window ? max(0, p0 - a.window + 1) : 0;
-    *lo = k0 / kKeys;
-    *hi = k1 > k0 ? (k1 + kKeys - 1) / kKeys : *lo;
+    *lo = k0 / step;
+    *hi = k1 > k0 ? (k1 + step - 1) / step : *lo;
 }
 
 // Inclusive scan over the block's 1024 threads; *total gets the sum.
@@ -714,7 +715,7 @@ __global__ void __launch_bounds__(kPlanTile) tile_plan_kernel(AttnArgs a, TilePl
             const int b = p.pair_b[i], q_len = a.q_start[b + 1] - a.q_start[b];
             const int r0 = (i - p.pair_start[b]) * kRows;
             int lo, hi;
-            key_tiles(a, q_len, a.kv_len[b], r0, min(r0 + kRows, q_len * a.group), &lo, &hi);
+            key_steps(a, q_len, a.kv_len[b], r0, min(r0 + kRows, q_len * a.group), kKeys, &lo, &hi);
             tiles = max(1, hi - lo);
         }
         const long long n = (long long)tiles * a.cache.n_kv_heads;
@@ -728,31 +729,30 @@ __global__ void __launch_bounds__(kPlanTile) tile_plan_kernel(AttnArgs a, TilePl
 struct TileCursor {
     long long u, u1;             // next unit, end of the run
     int pair, b, rb, kh, t0, t1, q0, q_len, kv_len, lo, more, whole;
-    int s[2], e[2];              // key tiles, in [t0, t1), that the two tiles of 128 rows see
+    int s[2], e[2];              // steps, in [2 t0, 2 t1), that the two tiles of 128 rows see
 };
 
 template <int D>
 struct TileShared {
     // operand tiles in the 128-byte-swizzled K-major layout: atoms of 64 columns, a row of an atom 128 bytes, the 16-byte
     // piece i of row r at place i ^ (r % 8)
+    // (a step's 64 keys: half the rows of K's atoms, one atom of V)
     static constexpr int kQAtom = 128 * 128, kVAtom = D * 128;      // Q and K (rows: queries, keys), V (rows: head values)
     static constexpr int kBuf = 128 * D * 2;
     alignas(1024) unsigned char q[2][kBuf];
     alignas(1024) unsigned char kv[kExpanded][kBuf];
     alignas(128) unsigned char raw[kRawStages][kKeys * (D + 8)];
     uint64_t raw_full[kRawStages], raw_empty[kRawStages], kv_full[kExpanded], kv_empty[kExpanded];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], fin;
+    uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2], fin[2];      // [tile of rows][step parity]
     uint32_t valid[kInfo];                                       // per tile: which groups of 16 tokens have a page
     uint32_t tmem;
-    int dead;
     TileCursor cur[kTileThreads / 32];
 };
 
 // The next item of the run, or false: rows block rb of request b, kv head kh, key tiles lo + [t0, t1).  Each warp keeps
 // its own in shared memory (the expanding and issuing warps have few registers); lane 0 moves it on.
-__device__ __forceinline__ bool next_item(const AttnArgs& a, const TilePlan& p, TileCursor* cur) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) {
+__device__ __forceinline__ bool next_item_alone(const AttnArgs& a, const TilePlan& p, TileCursor* cur) {
+    {
         TileCursor& c = *cur;
         c.more = c.u < c.u1;
         if (c.more) {
@@ -767,13 +767,13 @@ __device__ __forceinline__ bool next_item(const AttnArgs& a, const TilePlan& p, 
             c.q0 = a.q_start[c.b], c.q_len = a.q_start[c.b + 1] - c.q0, c.kv_len = a.kv_len[c.b];
             int hi;
             const int r0 = c.rb * kRows, rows = c.q_len * a.group;
-            key_tiles(a, c.q_len, c.kv_len, r0, min(r0 + kRows, rows), &c.lo, &hi);
+            key_steps(a, c.q_len, c.kv_len, r0, min(r0 + kRows, rows), kKeys, &c.lo, &hi);
             for (int x = 0; x < 2; ++x) {
-                c.s[x] = c.e[x] = c.t0;
+                c.s[x] = c.e[x] = 2 * c.t0;
                 if (r0 + 128 * x >= rows) continue;
                 int lo;
-                key_tiles(a, c.q_len, c.kv_len, r0 + 128 * x, min(r0 + 128 * x + 128, rows), &lo, &hi);
-                const int s = max(lo - c.lo, c.t0), e = min(hi - c.lo, c.t1);
+                key_steps(a, c.q_len, c.kv_len, r0 + 128 * x, min(r0 + 128 * x + 128, rows), kStep, &lo, &hi);
+                const int s = max(lo - 2 * c.lo, 2 * c.t0), e = min(hi - 2 * c.lo, 2 * c.t1);
                 if (s < e) c.s[x] = s, c.e[x] = e;
             }
             c.whole = c.t0 == 0 && c.t1 == n;
@@ -781,25 +781,30 @@ __device__ __forceinline__ bool next_item(const AttnArgs& a, const TilePlan& p, 
             if (c.t1 == n && c.kh == a.cache.n_kv_heads - 1) ++c.pair;
         }
     }
+    return cur->more;
+}
+
+__device__ __forceinline__ bool next_item(const AttnArgs& a, const TilePlan& p, TileCursor* cur) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) next_item_alone(a, p, cur);
     __syncwarp();
     return cur->more;
 }
 
-__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, int* dead) {
-    const uint32_t addr = qmoe_tc::smem_u32(bar);
-    for (uint32_t it = 0; it < kWaitLimit; ++it) {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
-            : "r"(addr), "r"(parity)
-            : "memory");
-        if (ok) return true;
-        if ((it & 63) == 63 && *(volatile int*)dead) return false;
-    }
-    *(volatile int*)dead = 1;
-    attn_set_error(QMOE_ETIMEOUT);
-    return false;
+// Bounded wait; false when the tries ran out.  A few instructions, as every role's loop holds some of these and the
+// roles' code shares the instruction caches; the hardware suspends the thread for part of each try.
+constexpr uint32_t kTries = 1u << 21;
+__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b32 n;\n mov.b32 n, %3;\n"
+        "AGAIN:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
+        " sub.u32 n, n, 1;\n setp.ne.u32 p, n, 0;\n @p bra AGAIN;\n setp.eq.u32 p, n, 1;\n"
+        "DONE:\n selp.b32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(qmoe_tc::smem_u32(bar)), "r"(parity), "n"(kTries)
+        : "memory");
+    return ok != 0;
 }
 
 __device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t* r) {
@@ -835,12 +840,26 @@ __device__ __forceinline__ void tmem_wait_load(uint32_t* r) {
                  : "memory");
 }
 
-// 64 columns, complete.
-__device__ __forceinline__ void tmem_load64(uint32_t taddr, uint32_t* r) {
-    tmem_load32(taddr, r);
-    tmem_load32(taddr + 32, r + 32);
-    tmem_wait_load(r);
-    tmem_wait_load(r + 32);
+// 64 columns, complete: the wait is in the same statement, so that the registers are used in place.
+__device__ __forceinline__ void tmem_load64(uint32_t taddr, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
+        "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, "
+        "%42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, "
+        "%62, %63 "
+        "}, [%64];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr)
+        : "memory");
 }
 
 // Scores of 64 keys outside [lo, hi], or in a group of 16 whose bit of `groups` is clear, become -inf.
@@ -960,8 +979,8 @@ __host__ __device__ constexpr int v_swap(int o) {
 template <int D>
 __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TilePlan plan, float* parts) {
     using Sh = TileShared<D>;
-    extern __shared__ unsigned char smem_raw[];
-    Sh& sh = *(Sh*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    Sh& sh = *(Sh*)smem_raw;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n_pairs = plan.pair_start[a.B];
     const long long total = plan.unit_start[n_pairs];
@@ -970,15 +989,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
     if (first_unit >= end_unit) return;
     if (tid == 0) {
         for (int i = 0; i < kRawStages; ++i) qmoe_tc::mbar_init(&sh.raw_full[i], 1), qmoe_tc::mbar_init(&sh.raw_empty[i], 4);
-        for (int i = 0; i < kExpanded; ++i) qmoe_tc::mbar_init(&sh.kv_full[i], 4), qmoe_tc::mbar_init(&sh.kv_empty[i], 1);
+        for (int i = 0; i < kExpanded; ++i) qmoe_tc::mbar_init(&sh.kv_full[i], 4), qmoe_tc::mbar_init(&sh.kv_empty[i], 2);
         for (int i = 0; i < 2; ++i) {
             qmoe_tc::mbar_init(&sh.q_full[i], 4);
-            qmoe_tc::mbar_init(&sh.s_full[i], 1);
-            qmoe_tc::mbar_init(&sh.p_full[i], 4);
-            qmoe_tc::mbar_init(&sh.o_full[i], 1);
+            for (int j = 0; j < 2; ++j) {
+                qmoe_tc::mbar_init(&sh.s_full[i][j], 1);
+                qmoe_tc::mbar_init(&sh.p_full[i][j], 4);
+                qmoe_tc::mbar_init(&sh.o_full[i][j], 1);
+            }
         }
-        qmoe_tc::mbar_init(&sh.fin, 1);
-        sh.dead = 0;
+        for (int i = 0; i < 2; ++i) qmoe_tc::mbar_init(&sh.fin[i], 1);
         qmoe_tc::fence_mbar_init();
     }
     if (warp == kIssueWarp) qmoe_tc::tmem_alloc(&sh.tmem, 512);
@@ -997,17 +1017,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
     }
     __syncthreads();
     qmoe_tc::tc_fence_after();
-    const uint32_t tmem = sh.tmem;
+    // all 512 columns were taken, so they begin at column 0
+    constexpr uint32_t tmem = 0;
     TileCursor& c = sh.cur[warp];
 
+    bool ok = true;
     if (warp < kExpandWarp) {
         // ---- softmax: a thread per query row
         const int x = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;           // 32 lanes a warp, lane index in bits 16..
         const uint32_t ts = tmem + x * 128 + lanes, to = tmem + 256 + x * 128 + lanes;
-        uint32_t n_s = 0, n_items = 0;                               // phases of s_full, o_full passed
+        uint32_t n_s = 0;                                            // steps done (the step barriers take turns)
         int tiles = 0;                                               // tiles of the run before the item
-        bool ok = true;
         while (ok && next_item(a, plan, &c)) {
             const int t_s = c.s[x], t_e = c.e[x], t0 = c.t0, lo = c.lo;
             const int r = c.rb * kRows + x * 128 + row;
@@ -1044,38 +1065,34 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
             const int pos = a.causal ? first + n : first;
             const int k_hi = min(pos, c.kv_len - 1), k_lo = a.window ? pos - a.window + 1 : 0;    // keys seen: [k_lo, k_hi]
             for (int t = t_s; t < t_e && ok; ++t) {
-                ok = tile_wait(&sh.s_full[x], n_s & 1, &sh.dead);
-                if (!__all_sync(QMOE_FULL_MASK, ok)) {
-                    ok = false;
-                    break;
-                }
-                ++n_s;
+                const uint32_t tb = ts + (n_s & 1) * kStep;
+                ok = tile_wait(&sh.s_full[x][n_s & 1], (n_s >> 1) & 1);
+                if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
                 qmoe_tc::tc_fence_after();
-                const int j0 = (lo + t) * kKeys;
-                const uint32_t valid = sh.valid[(tiles + t - t0) % kInfo];
-                const bool edge = j0 + kKeys - 1 > k_hi || j0 < k_lo || valid != 0xFFu;
-                // two passes over the row, 64 keys at a time: the loops stay small enough for the instruction caches, which a
-                // fully unrolled row (and the other roles' code) would not fit
-                float mx = -INFINITY;
-#pragma unroll 1
-                for (int hf = 0; hf < 2; ++hf) {
-                    uint32_t sr[64];
-                    tmem_load64(ts + 64 * hf, sr);
-                    if (edge) mask64(sr, k_lo - j0 - 64 * hf, k_hi - j0 - 64 * hf, valid >> (4 * hf));
-                    float m0 = -INFINITY, m1 = -INFINITY;
+                uint32_t sr[kStep];
+                tmem_load64(tb, sr);
+                const int j0 = lo * kKeys + t * kStep;
+                const uint32_t valid = sh.valid[(tiles + (t >> 1) - t0) % kInfo] >> (4 * (t & 1)) & 15u;
+                if (__builtin_expect(j0 + kStep - 1 > k_hi || j0 < k_lo || valid != 15u, 0)) mask64(sr, k_lo - j0, k_hi - j0, valid);
+                float mx, m1 = -INFINITY;
+                {
+                    float m0 = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 64; i += 4) {
+                    for (int i = 0; i < kStep; i += 4) {
                         m0 = fmaxf(m0, fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])));
                         m1 = fmaxf(m1, fmaxf(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])));
                     }
-                    mx = fmaxf(mx, fmaxf(m0, m1));
+                    mx = fmaxf(m0, m1) * factor;
                 }
-                mx *= factor;
-                if (__any_sync(QMOE_FULL_MASK, mx > m + kSlack)) {
+                if (__builtin_expect(__any_sync(QMOE_FULL_MASK, mx > m + kSlack), 0)) {
                     const float m2 = fmaxf(m, mx), f = ex2(m - m2);
                     m = m2;
                     l *= f;
                     if (t > t_s) {
+                        // O as the step before left it
+                        ok = tile_wait(&sh.o_full[x][(n_s - 1) & 1], ((n_s - 1) >> 1) & 1);
+                        if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
+                        qmoe_tc::tc_fence_after();
 #pragma unroll 1
                         for (int i = 0; i < D; i += 16) {
                             uint32_t orr[16];
@@ -1091,28 +1108,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                 const bool far = __any_sync(QMOE_FULL_MASK, fabsf(m) > 65536.f && m != kNoMax);
                 const uint64_t nb2 = pair(nb, nb), mul2 = far ? pair(1.f, 1.f) : pair(factor, factor);
                 uint64_t l2[2] = {0, 0};
-#pragma unroll 1
-                for (int hf = 0; hf < 2; ++hf) {
-                    uint32_t sr[64], pr[32];
-                    tmem_load64(ts + 64 * hf, sr);
-                    if (edge) mask64(sr, k_lo - j0 - 64 * hf, k_hi - j0 - 64 * hf, valid >> (4 * hf));
-                    if (far) {
+                if (__builtin_expect(far, 0)) {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) sr[i] = __float_as_uint(__uint_as_float(sr[i]) * factor);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 64; i += 2) {
-                        float e0, e1;
-                        unpair(fma2(pair(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), mul2, nb2), &e0, &e1);
-                        e0 = ex2(e0), e1 = ex2(e1);
-                        l2[(i >> 1) & 1] = add2(l2[(i >> 1) & 1], pair(e0, e1));
-                        sr[i] = __float_as_uint(e0), sr[i + 1] = __float_as_uint(e1);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        pr[i] = half2_bits(__uint_as_float(sr[(2 * i) ^ v_swap<D>(i >> 2)]), __uint_as_float(sr[(2 * i + 1) ^ v_swap<D>(i >> 2)]));
-                    tmem_store32(ts + 32 * hf, pr);      // over scores that both passes are done with
+                    for (int i = 0; i < kStep; ++i) sr[i] = __float_as_uint(__uint_as_float(sr[i]) * factor);
                 }
+                uint32_t pr[kStep / 2];
+#pragma unroll
+                for (int i = 0; i < kStep; i += 2) {
+                    float e0, e1;
+                    unpair(fma2(pair(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), mul2, nb2), &e0, &e1);
+                    e0 = ex2(e0), e1 = ex2(e1);
+                    l2[(i >> 1) & 1] = add2(l2[(i >> 1) & 1], pair(e0, e1));
+                    sr[i] = __float_as_uint(e0), sr[i + 1] = __float_as_uint(e1);
+                }
+#pragma unroll
+                for (int i = 0; i < kStep / 2; ++i)
+                    pr[i] = half2_bits(__uint_as_float(sr[(2 * i) ^ v_swap<D>(i >> 2)]), __uint_as_float(sr[(2 * i + 1) ^ v_swap<D>(i >> 2)]));
+                tmem_store32(tb, pr);      // over the scores
                 {
                     float e0, e1;
                     unpair(add2(l2[0], l2[1]), &e0, &e1);
@@ -1120,15 +1132,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                 }
                 tmem_wait_store();
                 qmoe_tc::tc_fence_before();
-                arrive_warp(&sh.p_full[x]);
+                arrive_warp(&sh.p_full[x][n_s & 1]);
+                ++n_s;
             }
             tiles += c.t1 - c.t0;
             if (!ok) break;
             const bool some = t_e > t_s;
             if (some) {
-                ok = tile_wait(&sh.o_full[x], n_items & 1, &sh.dead);
-                if (!__all_sync(QMOE_FULL_MASK, ok)) break;
-                ++n_items;
+                ok = tile_wait(&sh.o_full[x][(n_s - 1) & 1], ((n_s - 1) >> 1) & 1);
+                if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
                 qmoe_tc::tc_fence_after();
             }
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
@@ -1183,12 +1195,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
         const uint32_t v_row = v_page + (uint32_t)(P + v_in) * (D / 2), v_pair = v_page + (uint32_t)P * D + (P + v_in) * 4;
         const int swap = v_swap<D>(o);
         uint32_t tile = 0, buf = 0, phase = 0;       // raw tiles done; next expanded buffer and its phase
-        bool ok = true;
         while (ok && next_item(a, plan, &c)) {
             for (int t = c.t0; t < c.t1; ++t, ++tile) {
                 const int st = tile % kRawStages;
-                ok = tile_wait(&sh.raw_full[st], (tile / kRawStages) & 1, &sh.dead);
-                if (ok && phase > 0) ok = tile_wait(&sh.kv_empty[buf], (phase - 1) & 1, &sh.dead);
+                ok = tile_wait(&sh.raw_full[st], (tile / kRawStages) & 1);
+                if (ok && phase > 0) ok = tile_wait(&sh.kv_empty[buf], (phase - 1) & 1);
                 if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
                 const unsigned char* raw = sh.raw[st];
                 const int j0 = (c.lo + t) * kKeys;
@@ -1216,7 +1227,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                 qmoe_tc::fence_async_shared();
                 arrive_warp(&sh.kv_full[buf]);
                 if (++buf == kExpanded) buf = 0, ++phase;
-                ok = phase == 0 || tile_wait(&sh.kv_empty[buf], (phase - 1) & 1, &sh.dead);
+                ok = phase == 0 || tile_wait(&sh.kv_empty[buf], (phase - 1) & 1);
                 if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
                 {
                     __half2 s2[4], z2[4];
@@ -1260,76 +1271,69 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
             }
         }
     } else {
-        if (warp == kIssueWarp) {
-            // ---- issue the products (the warp stays converged; one elected lane issues and commits)
-            constexpr uint32_t id_s = qmoe_tc::idesc_f16(128, kKeys, false, false), id_o = qmoe_tc::idesc_f16(128, D, false, false);
-            const uint64_t qd = desc_sw128(sh.q[0]), kvd = desc_sw128(sh.kv[0]);
-            constexpr uint32_t q_step = sizeof(sh.q[0]) / 16, kv_step = sizeof(sh.kv[0]) / 16;
-            uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0};
-            uint32_t kb = 0, kph = 0, vb = 0, vph = 0;      // buffers (and phases) of the next keys and of the values after them
-            bool ok = true;
-            while (ok && next_item(a, plan, &c)) {
-                const int s[2] = {c.s[0], c.s[1]}, e[2] = {c.e[0], c.e[1]}, t0 = c.t0, t1 = c.t1;
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    if (e[x] > s[x]) ok = ok && tile_wait(&sh.q_full[x], n_q[x]++ & 1, &sh.dead);
-                // step t: S of tile t + 1 follows O of tile t
-                for (int t = t0 - 1; t < t1; ++t) {
-                    if (t >= t0) ok = ok && tile_wait(&sh.kv_full[vb], vph, &sh.dead);
-                    bool have_k = t + 1 >= t1;
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        if (t >= s[x] && t < e[x]) {
-                            ok = ok && tile_wait(&sh.p_full[x], n_p[x]++ & 1, &sh.dead);
-                            if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
-                            qmoe_tc::tc_fence_after();
-                            if (elect_one()) {
-                                const uint32_t v = (uint32_t)kvd + vb * kv_step;
-#pragma unroll
-                                for (int k = 0; k < kKeys / 16; ++k)
-                                    mma_ts(tmem + 256 + x * 128, tmem + x * 128, k * 8, v, (uint32_t)(kvd >> 32), (k >> 2) * (Sh::kVAtom / 16) + (k & 3) * 2, id_o, k > 0 || t > s[x]);
-                                if (t + 1 == e[x]) qmoe_tc::mma_commit(&sh.o_full[x]);
-                            }
-                            __syncwarp();
+        if (warp == kIssueWarp || warp == kIssueWarp + 2) {
+            // ---- issue the products of one tile of rows, by one elected thread
+            const int x = (warp - kIssueWarp) >> 1;
+            if (elect_one()) {
+                constexpr uint32_t id_s = qmoe_tc::idesc_f16(128, kStep, false, false), id_o = qmoe_tc::idesc_f16(128, D, false, false);
+                const uint64_t qd = desc_sw128(sh.q[x]), kvd = desc_sw128(sh.kv[0]);
+                constexpr uint32_t kv_step = sizeof(sh.kv[0]) / 16;
+                uint32_t n_q = 0, n_s = 0, n_p = 0;             // items, steps of scores and of values done
+                uint32_t kb = 0, kph = 0, vb = 0, vph = 0;      // buffers and phases: keys, values
+                while (ok && next_item_alone(a, plan, &c)) {
+                    const int t0 = 2 * c.t0, t1 = 2 * c.t1, s = c.s[x], e = c.e[x];
+                    // scores of step t + 1 go ahead of the values of step t, so that the softmax finds its next scores ready
+#pragma unroll 1
+                    for (int t = t0 - 1; t < t1 && ok; ++t) {
+                        const uint32_t half = t & 1;            // of the values; the scores' is the other
+                        if (half) {
+                            if (t + 1 < t1) ok = tile_wait(&sh.kv_full[kb], kph);
+                        } else {
+                            vb = kb + 1, vph = kph;
+                            if (vb == kExpanded) vb = 0, vph ^= 1;
+                            ok = tile_wait(&sh.kv_full[vb], vph);
                         }
-                        if (!have_k) ok = ok && tile_wait(&sh.kv_full[kb], kph, &sh.dead);
-                        have_k = true;
-                        if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
-                        if (t + 1 >= s[x] && t + 1 < e[x]) {
+                        if (t + 1 >= s && t + 1 < e) {
+                            if (t + 1 == s && ok) ok = tile_wait(&sh.q_full[x], n_q++ & 1);
+                            if (!ok) break;
                             qmoe_tc::tc_fence_after();
-                            if (elect_one()) {
-                                const uint32_t q = (uint32_t)qd + x * q_step, kk = (uint32_t)kvd + kb * kv_step;
+                            const uint32_t k_lo = (uint32_t)kvd + kb * kv_step + (half ^ 1) * (kStep * 128 / 16), at = x * 128 + (n_s & 1) * kStep;
 #pragma unroll
-                                for (int k = 0; k < D / 16; ++k) mma_ss(tmem + x * 128, q, (uint32_t)(qd >> 32), kk, (uint32_t)(kvd >> 32), (k >> 2) * (Sh::kQAtom / 16) + (k & 3) * 2, id_s, k > 0);
-                                qmoe_tc::mma_commit(&sh.s_full[x]);
-                            }
-                            __syncwarp();
+                            for (int k = 0; k < D / 16; ++k)
+                                mma_ss(at, (uint32_t)qd, (uint32_t)(qd >> 32), k_lo, (uint32_t)(kvd >> 32), (k >> 2) * (Sh::kQAtom / 16) + (k & 3) * 2, id_s, k > 0);
+                            qmoe_tc::mma_commit(&sh.s_full[x][n_s & 1]);
+                            ++n_s;
                         }
-                    }
-                    if (!ok) break;
-                    if (elect_one()) {
-                        if (t >= t0) qmoe_tc::mma_commit(&sh.kv_empty[vb]);
-                        if (t + 1 < t1) qmoe_tc::mma_commit(&sh.kv_empty[kb]);
-                    }
-                    __syncwarp();
-                    if (t + 1 < t1) {       // the values of tile t + 1 follow its keys, the keys of t + 2 those
-                        vb = kb + 1, vph = kph;
-                        if (vb == kExpanded) vb = 0, vph ^= 1;
-                        kb = vb + 1, kph = vph;
-                        if (kb == kExpanded) kb = 0, kph ^= 1;
+                        if (t >= s && t < e) {
+                            ok = ok && tile_wait(&sh.p_full[x][n_p & 1], (n_p >> 1) & 1);
+                            if (!ok) break;
+                            qmoe_tc::tc_fence_after();
+                            const uint32_t v_lo = (uint32_t)kvd + vb * kv_step + half * (Sh::kVAtom / 16), at = x * 128 + (n_p & 1) * kStep;
+#pragma unroll
+                            for (int k = 0; k < kStep / 16; ++k)
+                                mma_ts(256 + x * 128, at, k * 8, v_lo, (uint32_t)(kvd >> 32), k * 2, id_o, k > 0 || t > s);
+                            qmoe_tc::mma_commit(&sh.o_full[x][n_p & 1]);
+                            ++n_p;
+                        }
+                        // a tile's keys are done with after its second step's scores, its values after the second step's
+                        if (t >= t0) {
+                            qmoe_tc::mma_commit(&sh.kv_empty[half ? vb : kb]);
+                            if (!half) {
+                                kb = vb + 1, kph = vph;
+                                if (kb == kExpanded) kb = 0, kph ^= 1;
+                            }
+                        }
                     }
                 }
+                // everything issued has ended before tensor memory is freed
+                qmoe_tc::mma_commit(&sh.fin[x]);
+                tile_wait(&sh.fin[x], 0);
             }
-            // everything issued has ended before tensor memory is freed
-            __syncwarp();
-            if (elect_one()) qmoe_tc::mma_commit(&sh.fin);
-            qmoe_tc::mbar_wait(&sh.fin, 0, kWaitLimit);
         } else if (warp == kCopyWarp) {
             // ---- copy pages: lane i the tile's i-th
             const int per_tile = kKeys >> a.cache.page_shift, per_page = (1 << a.cache.page_shift) / 16;
             uint32_t tile = 0;
-            bool ok = true;
-            while (ok && next_item(a, plan, &c)) {
+                while (ok && next_item(a, plan, &c)) {
                 for (int t = c.t0; t < c.t1; ++t, ++tile) {
                     const int st = tile % kRawStages;
                     const int blk = (c.lo + t) * per_tile + lane;
@@ -1339,7 +1343,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                     const bool good = page >= 0 && page < a.cache.n_pages;
                     if (mine && !good) attn_set_error(QMOE_EINVAL);
                     const unsigned mask = __ballot_sync(QMOE_FULL_MASK, good);
-                    if (tile >= kRawStages) ok = tile_wait(&sh.raw_empty[st], (tile / kRawStages - 1) & 1, &sh.dead);
+                    if (tile >= kRawStages) ok = tile_wait(&sh.raw_empty[st], (tile / kRawStages - 1) & 1);
                     ok = __all_sync(QMOE_FULL_MASK, ok);
                     if (!ok) break;
                     if (lane == 0) {
@@ -1359,6 +1363,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                 qmoe_tc::mbar_wait(&sh.raw_full[i % kRawStages], (i / kRawStages) & 1, kWaitLimit);
         }
     }
+    if (!ok) attn_set_error(QMOE_ETIMEOUT);
     qmoe_tc::tc_fence_before();
     __syncthreads();
     if (warp == kIssueWarp) {
@@ -1411,7 +1416,7 @@ size_t decode_ws(int rows, int head_dim) {
 
 template <int D, int NT>
 int launch_decode(const AttnArgs& a, float* parts, cudaStream_t st) {
-    const int smem = (int)sizeof(DecodeShared<D, NT>) + 128;
+    const int smem = (int)sizeof(DecodeShared<D, NT>);
     int rc = qmoe::smem_attr((const void*)decode_kernel<D, NT>, smem, "attention attr");
     if (rc) return rc;
     const long long blocks = decode_blocks(8 * NT, a.B, a.cache.n_kv_heads, a.max_kv);
@@ -1457,7 +1462,7 @@ TileWs tile_ws(void* base, int B, int group, int head_dim, int n_q_tokens) {
 
 template <int D>
 int launch_tiles(const AttnArgs& a, const TileWs& w, int min_rows, cudaStream_t st) {
-    const int smem = (int)sizeof(TileShared<D>) + 1024, blocks = qmoe::sm_count();
+    const int smem = (int)sizeof(TileShared<D>), blocks = qmoe::sm_count();
     int rc = qmoe::smem_attr((const void*)tile_kernel<D>, smem, "attention attr");
     if (rc) return rc;
     const long long items = (long long)w.plan.max_pairs * a.cache.n_kv_heads;
