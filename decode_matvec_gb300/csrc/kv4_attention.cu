@@ -60,7 +60,7 @@ __device__ __forceinline__ bool request(const AttnArgs& a, int b, int* q0, int* 
 // out to the blocks in equal runs, whatever the lengths.  A producer warp copies whole pages of one
 // head (contiguous in the layout) into a ring of stages with bulk copies; four warps take 16 tokens of
 // each 64.  An item that several blocks share leaves its parts (unnormalised sums, maximum, sum of
-// weights) in the workspace for combine_kernel.
+// weights) in the workspace for join_kernel.
 constexpr int kTile = 64;
 constexpr int kStages = 4;
 constexpr int kConsumers = 4;                        // warps that compute
@@ -80,16 +80,15 @@ __device__ __forceinline__ int tiles_of(const AttnArgs& a, int b, int max_rows, 
     return max(1, (kv_len + kTile - 1) / kTile - *t0);
 }
 
-// Block-wide: units (tiles of all items) before request `want`'s first and in all, by a scan over the
-// requests; or, with find >= 0, the request that holds unit `find`.  Every thread gets the results.
+// Block-wide: the units (tiles of all items) in all, the run of each block, and the request that holds this block's first
+// unit with the units before it.  A scan over the requests; every thread gets the results.
 struct Found {
     long long total, before;
     int b;
 };
 
 template <int THREADS>
-__device__ __forceinline__ Found scan_requests(const AttnArgs& a, int max_rows, long long want, bool by_request, int n_ctas,
-                                               int cta, long long* chunk, bool report) {
+__device__ __forceinline__ Found scan_requests(const AttnArgs& a, int max_rows, long long* chunk) {
     __shared__ long long warp_sum_s[THREADS / 32];
     __shared__ Found found;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -97,7 +96,7 @@ __device__ __forceinline__ Found scan_requests(const AttnArgs& a, int max_rows, 
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
     long long mine = 0;
     int t0;
-    for (int b = b0; b < b1; ++b) mine += tiles_of(a, b, max_rows, &t0, report);
+    for (int b = b0; b < b1; ++b) mine += tiles_of(a, b, max_rows, &t0, blockIdx.x == 0);
     mine *= a.cache.n_kv_heads;
     long long incl = mine;
 #pragma unroll
@@ -106,7 +105,6 @@ __device__ __forceinline__ Found scan_requests(const AttnArgs& a, int max_rows, 
         if (lane >= d) incl += o;
     }
     if (lane == 31) warp_sum_s[warp] = incl;
-    if (tid == 0) found.b = -1;
     __syncthreads();
     long long total = 0, before = incl - mine;
 #pragma unroll
@@ -114,19 +112,17 @@ __device__ __forceinline__ Found scan_requests(const AttnArgs& a, int max_rows, 
         if (w < warp) before += warp_sum_s[w];
         total += warp_sum_s[w];
     }
-    *chunk = max(1LL, (total + n_ctas - 1) / n_ctas);
-    const long long target = by_request ? 0 : (long long)cta * *chunk;
-    const bool here = by_request ? want >= b0 && want < b1 : target >= before && target < before + mine;
-    if (here) {
-        long long at = before;
+    *chunk = max(1LL, (total + gridDim.x - 1) / gridDim.x);
+    const long long target = (long long)blockIdx.x * *chunk;
+    if (target >= before && target < before + mine) {
         for (int b = b0; b < b1; ++b) {
             const long long n = (long long)tiles_of(a, b, max_rows, &t0, false) * a.cache.n_kv_heads;
-            if (by_request ? b == want : target < at + n) {
+            if (target < before + n) {
                 found.b = b;
-                found.before = at;
+                found.before = before;
                 break;
             }
-            at += n;
+            before += n;
         }
     }
     __syncthreads();
@@ -200,9 +196,18 @@ __device__ __forceinline__ float* part_of(float* parts, long long cta, int which
     return parts + ((size_t)cta * 2 + which) * (size_t)(rows * (D + 2));
 }
 
+// An item that a block began and left unfinished, and the last block that works on it (-1: none).
+struct SplitItem {
+    int b, kh, rb, last;
+};
+
+// Programmatic dependent launch: the kernels of a call overlap each other's launches.
+__device__ __forceinline__ void depend_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void depend_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
-    decode_kernel(AttnArgs a, int max_rows, float* parts) {
+    decode_kernel(AttnArgs a, int max_rows, SplitItem* items, float* parts) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     DecodeShared<D, NT>& sh = *(DecodeShared<D, NT>*)smem_raw;
     constexpr int W = D / 32;              // words of a key row that a lane reads
@@ -216,8 +221,10 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
         qmoe_tc::fence_mbar_init();
     }
     long long chunk;
-    const Found f = scan_requests<kDecodeThreads>(a, max_rows, 0, false, gridDim.x, blockIdx.x, &chunk, blockIdx.x == 0);
+    const Found f = scan_requests<kDecodeThreads>(a, max_rows, &chunk);
+    depend_launch();
     const long long u0 = (long long)blockIdx.x * chunk, u1 = min(u0 + chunk, f.total);
+    if (tid == 32 * kConsumers) items[blockIdx.x] = SplitItem{0, 0, 0, -1};
     if (u0 >= u1) return;
     const int n_units = (int)(u1 - u0);
 
@@ -251,6 +258,8 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
                 if (u >= tile) flags |= kWholeStart;            // the item's first tile is in this run
                 if (u + (n - 1 - tile) < n_units) flags |= kWholeEnd;
                 sh.info[st] = StageInfo{b, kh, t0 + tile, flags};
+                if ((flags & (kLast | kWholeStart | kWholeEnd)) == (kLast | kWholeStart))
+                    items[blockIdx.x] = SplitItem{b, kh, 0, (int)((u0 + u - tile + n - 1) / chunk)};
                 mbar_expect(&sh.full[st], (uint32_t)__popc(mask) * page_copy);
             }
             __syncwarp();
@@ -578,49 +587,65 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
     }
 }
 
-// Four values (from d0) of row r of an item whose parts blocks c0 .. c1 left; the row is row `row` of the request's kv head.
-template <int D>
-__device__ __forceinline__ void join_parts(const AttnArgs& a, const float* parts, int c0, int c1, long long u0, long long chunk,
-                                           int part_rows, int r, int d0, int q0, int row, int kh) {
-    float mm = kNoMax, ll = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; ++c) {
-        const float* p = part_of((float*)parts, c, u0 >= (long long)c * chunk ? 1 : 0, part_rows, D);
-        const float2 ml = *(const float2*)(p + (size_t)part_rows * D + 2 * r);
-        const float4 x = *(const float4*)(p + (size_t)r * D + d0);
-        const float m2 = fmaxf(mm, ml.x), fa = ex2(mm - m2), fb = ex2(ml.x - m2);
-        mm = m2;
-        ll = ll * fa + ml.y * fb;
-        acc.x = acc.x * fa + x.x * fb, acc.y = acc.y * fa + x.y * fb;
-        acc.z = acc.z * fa + x.z * fb, acc.w = acc.w * fa + x.w * fb;
-    }
-    const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);
-    const int n = row / a.group, h = kh * a.group + row - n * a.group;
-    uint2 w;
-    w.x = (uint32_t)f32_to_bf16(acc.x * inv) | ((uint32_t)f32_to_bf16(acc.y * inv) << 16);
-    w.y = (uint32_t)f32_to_bf16(acc.z * inv) | ((uint32_t)f32_to_bf16(acc.w * inv) << 16);
-    *(uint2*)(a.out + ((int64_t)(q0 + n) * a.n_q_heads + h) * D + d0) = w;
-}
-
-// Joins the parts of items that several blocks of decode_kernel shared.  One block per (request, kv head).
-constexpr int kCombineThreads = 128;
+// Joins the parts of items that several blocks shared: block (c, slice) those of the item that block c began and left
+// unfinished.  Its parts are slot 1 of block c and slot 0 of blocks c + 1 .. rec.last; a group of head_dim / 4 lanes
+// adds up a row's parts, or every group some of them where there are many.
+constexpr int kJoinThreads = 128;
 
 template <int D>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, int max_rows, int n_ctas, const float* parts) {
-    const int b = blockIdx.x / a.cache.n_kv_heads, kh = blockIdx.x - b * a.cache.n_kv_heads;
-    long long chunk;
-    const Found f = scan_requests<kCombineThreads>(a, max_rows, b, true, n_ctas, 0, &chunk, false);
-    int t0;
-    const int n = tiles_of(a, b, max_rows, &t0, false);
-    asm volatile("griddepcontrol.wait;" ::: "memory");      // the parts are written by the kernel before
-    if (n == 0) return;
-    const long long u0 = f.before + (long long)kh * n, u1 = u0 + n;
-    const int c0 = (int)(u0 / chunk), c1 = (int)((u1 - 1) / chunk);
-    if (c0 == c1) return;
-    const int q0 = a.q_start[b], rows = (a.q_start[b + 1] - q0) * a.group;
-    for (int i = threadIdx.x; i < rows * (D / 4); i += kCombineThreads) {
-        const int r = i / (D / 4), d0 = (i - r * (D / 4)) * 4;
-        join_parts<D>(a, parts, c0, c1, u0, chunk, max_rows, r, d0, q0, r, kh);
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, const SplitItem* items, const float* parts, int part_rows) {
+    constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES;
+    __shared__ float4 acc_s[GROUPS][LANES];
+    __shared__ float2 ml_s[GROUPS];
+    depend_wait();
+    const SplitItem it = items[blockIdx.x];
+    const int n_parts = it.last - (int)blockIdx.x + 1;
+    if (n_parts < 2) return;
+    depend_launch();
+    const int q0 = a.q_start[it.b], rows = min(part_rows, (a.q_start[it.b + 1] - q0) * a.group - it.rb * part_rows);
+    const int grp = threadIdx.x / LANES, ln = threadIdx.x - grp * LANES;
+    const bool wide = n_parts > 4;
+    for (int r0 = blockIdx.y * (wide ? 1 : GROUPS); r0 < rows; r0 += gridDim.y * (wide ? 1 : GROUPS)) {
+        const int r = wide ? r0 : min(r0 + grp, rows - 1);
+        float mm = kNoMax, ll = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = wide ? grp : 0; i < n_parts; i += wide ? GROUPS : 1) {
+            const float* p = part_of((float*)parts, blockIdx.x + i, i == 0, part_rows, D);
+            const float2 ml = *(const float2*)(p + (size_t)part_rows * D + 2 * r);
+            const float4 x = *(const float4*)(p + (size_t)r * D + 4 * ln);
+            const float m2 = fmaxf(mm, ml.x), fa = ex2(mm - m2), fb = ex2(ml.x - m2);
+            mm = m2;
+            ll = ll * fa + ml.y * fb;
+            acc.x = acc.x * fa + x.x * fb, acc.y = acc.y * fa + x.y * fb;
+            acc.z = acc.z * fa + x.z * fb, acc.w = acc.w * fa + x.w * fb;
+        }
+        if (wide) {
+            acc_s[grp][ln] = acc;
+            if (ln == 0) ml_s[grp] = make_float2(mm, ll);
+            __syncthreads();
+            if (grp == 0) {
+#pragma unroll
+                for (int g = 1; g < GROUPS; ++g) {
+                    const float2 ml = ml_s[g];
+                    const float4 x = acc_s[g][ln];
+                    const float m2 = fmaxf(mm, ml.x), fa = ex2(mm - m2), fb = ex2(ml.x - m2);
+                    mm = m2;
+                    ll = ll * fa + ml.y * fb;
+                    acc.x = acc.x * fa + x.x * fb, acc.y = acc.y * fa + x.y * fb;
+                    acc.z = acc.z * fa + x.z * fb, acc.w = acc.w * fa + x.w * fb;
+                }
+            }
+            __syncthreads();
+        }
+        if (wide ? grp == 0 : r0 + grp < rows) {
+            const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);
+            const int row = it.rb * part_rows + r, n = row / a.group, h = it.kh * a.group + row - n * a.group;
+            uint2 w;
+            w.x = (uint32_t)f32_to_bf16(acc.x * inv) | ((uint32_t)f32_to_bf16(acc.y * inv) << 16);
+            w.y = (uint32_t)f32_to_bf16(acc.z * inv) | ((uint32_t)f32_to_bf16(acc.w * inv) << 16);
+            *(uint2*)(a.out + ((int64_t)(q0 + n) * a.n_q_heads + h) * D + 4 * ln) = w;
+        }
     }
 }
 
@@ -641,7 +666,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, in
 // operands alone 1030), the softmax warps about 900 issue slots a scheduler and the expansion 550.
 //
 // Work is dealt out as in the few-row path: all (rows, kv head) items' key tiles in a row, in equal
-// runs; items that several blocks share are joined by tile_combine_kernel.
+// runs; items that several blocks share are joined by join_kernel.
 constexpr int kKeys = 128;                       // keys of a tile (expanded at once)
 constexpr int kStep = 64;                        // keys of a softmax step
 constexpr int kRows = 256;                       // query rows of an item
@@ -651,10 +676,21 @@ constexpr int kRawStages = 2, kExpanded = 3, kInfo = 8;
 constexpr int kPlanTile = 1024;
 
 // Work list of the tile path, in the workspace: pairs (request, block of 256 rows) in order.
+struct alignas(16) PairInfo {
+    long long unit;              // key tiles of all kv heads before the pair
+    int n;                       // key tiles of one kv head, lo .. lo + n - 1
+    int b, rb, q0, q_len, kv_len, lo;
+    int s[2], e[2];              // steps, from 2 lo, that the two tiles of 128 rows see
+    int pad[3];
+};
+static_assert(sizeof(PairInfo) == 64, "read as sixteen words");
+
 struct TilePlan {
-    int32_t* pair_start;      // [B + 1]
-    long long* unit_start;    // [pairs + 1]: key tiles of all kv heads before the pair
-    int32_t* pair_b;          // [pairs]
+    int32_t* pair_start;         // [B + 1]
+    int32_t* pair_b;             // [pairs]
+    PairInfo* pairs;
+    long long* total;            // units of the batch
+    SplitItem* items;            // [blocks]
     int max_pairs;
 };
 
@@ -690,6 +726,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* total) {
 
 __global__ void __launch_bounds__(kPlanTile) tile_plan_kernel(AttnArgs a, TilePlan p, int min_rows) {
     const int tid = threadIdx.x;
+    depend_launch();
     long long base = 0, total;
     for (int b0 = 0; b0 < a.B; b0 += kPlanTile) {
         const int b = b0 + tid;
@@ -710,26 +747,38 @@ __global__ void __launch_bounds__(kPlanTile) tile_plan_kernel(AttnArgs a, TilePl
     base = 0;
     for (int i0 = 0; i0 < n_pairs; i0 += kPlanTile) {
         const int i = i0 + tid;
-        int tiles = 0;
+        PairInfo w{};
         if (i < n_pairs) {
-            const int b = p.pair_b[i], q_len = a.q_start[b + 1] - a.q_start[b];
-            const int r0 = (i - p.pair_start[b]) * kRows;
-            int lo, hi;
-            key_steps(a, q_len, a.kv_len[b], r0, min(r0 + kRows, q_len * a.group), kKeys, &lo, &hi);
-            tiles = max(1, hi - lo);
+            w.b = p.pair_b[i], w.q0 = a.q_start[w.b], w.q_len = a.q_start[w.b + 1] - w.q0, w.kv_len = a.kv_len[w.b];
+            w.rb = i - p.pair_start[w.b];
+            const int r0 = w.rb * kRows, rows = w.q_len * a.group;
+            int hi;
+            key_steps(a, w.q_len, w.kv_len, r0, min(r0 + kRows, rows), kKeys, &w.lo, &hi);
+            w.n = max(1, hi - w.lo);
+            for (int x = 0; x < 2; ++x) {
+                if (r0 + 128 * x >= rows) continue;
+                int lo;
+                key_steps(a, w.q_len, w.kv_len, r0 + 128 * x, min(r0 + 128 * x + 128, rows), kStep, &lo, &hi);
+                w.s[x] = lo - 2 * w.lo, w.e[x] = hi - 2 * w.lo;
+            }
         }
-        const long long n = (long long)tiles * a.cache.n_kv_heads;
+        const long long n = (long long)w.n * a.cache.n_kv_heads;
         const long long end = base + block_scan(n, &total);
-        if (i < n_pairs) p.unit_start[i] = end - n;
+        if (i < n_pairs) {
+            w.unit = end - n;
+            p.pairs[i] = w;
+        }
         base += total;
     }
-    if (tid == 0) p.unit_start[n_pairs] = base;
+    if (tid == 0) *p.total = base;
+    depend_wait();      // nothing before is read, but whoever waits for this kernel waits for those
 }
 
 struct TileCursor {
+    PairInfo w;                  // the pair
     long long u, u1;             // next unit, end of the run
-    int pair, b, rb, kh, t0, t1, q0, q_len, kv_len, lo, more, whole;
-    int s[2], e[2];              // steps, in [2 t0, 2 t1), that the two tiles of 128 rows see
+    int pair, kh, t0, t1, whole;
+    int s[2], e[2];              // the tiles' steps inside [2 t0, 2 t1)
 };
 
 template <int D>
@@ -749,46 +798,62 @@ struct TileShared {
     TileCursor cur[kTileThreads / 32];
 };
 
-// The next item of the run, or false: rows block rb of request b, kv head kh, key tiles lo + [t0, t1).  Each warp keeps
-// its own in shared memory (the expanding and issuing warps have few registers); lane 0 moves it on.
-__device__ __forceinline__ bool next_item_alone(const AttnArgs& a, const TilePlan& p, TileCursor* cur) {
-    {
-        TileCursor& c = *cur;
-        c.more = c.u < c.u1;
-        if (c.more) {
-            const long long pu = p.unit_start[c.pair];
-            const int n = (int)((p.unit_start[c.pair + 1] - pu) / a.cache.n_kv_heads);
-            c.b = p.pair_b[c.pair];
-            c.rb = c.pair - p.pair_start[c.b];
-            const long long off = c.u - pu;
-            c.kh = (int)(off / n);
-            c.t0 = (int)(off - (long long)c.kh * n);
-            c.t1 = (int)min((long long)n, c.t0 + (c.u1 - c.u));
-            c.q0 = a.q_start[c.b], c.q_len = a.q_start[c.b + 1] - c.q0, c.kv_len = a.kv_len[c.b];
-            int hi;
-            const int r0 = c.rb * kRows, rows = c.q_len * a.group;
-            key_steps(a, c.q_len, c.kv_len, r0, min(r0 + kRows, rows), kKeys, &c.lo, &hi);
-            for (int x = 0; x < 2; ++x) {
-                c.s[x] = c.e[x] = 2 * c.t0;
-                if (r0 + 128 * x >= rows) continue;
-                int lo;
-                key_steps(a, c.q_len, c.kv_len, r0 + 128 * x, min(r0 + 128 * x + 128, rows), kStep, &lo, &hi);
-                const int s = max(lo - 2 * c.lo, 2 * c.t0), e = min(hi - 2 * c.lo, 2 * c.t1);
-                if (s < e) c.s[x] = s, c.e[x] = e;
-            }
-            c.whole = c.t0 == 0 && c.t1 == n;
-            c.u += c.t1 - c.t0;
-            if (c.t1 == n && c.kh == a.cache.n_kv_heads - 1) ++c.pair;
-        }
+// The next item of the run, or false: the pair's rows, kv head kh, key tiles w.lo + [t0, t1).  Each warp keeps its own
+// cursor in shared memory.  first: the run's first item, which may begin inside a pair.
+__device__ __forceinline__ void place_item(const AttnArgs& a, TileCursor& c, bool first) {
+    if (first) {
+        const long long off = c.u - c.w.unit;
+        c.kh = (int)(off / c.w.n);
+        c.t0 = (int)(off - (long long)c.kh * c.w.n);
+    } else {
+        c.t0 = 0;
     }
-    return cur->more;
+    c.t1 = (int)min((long long)c.w.n, c.t0 + (c.u1 - c.u));
+    c.whole = c.t0 == 0 && c.t1 == c.w.n;
+    for (int x = 0; x < 2; ++x) {
+        const int s = max(c.w.s[x], 2 * c.t0), e = min(c.w.e[x], 2 * c.t1);
+        c.s[x] = s < e ? s : 0, c.e[x] = s < e ? e : 0;
+    }
+    c.u += c.t1 - c.t0;
 }
 
-__device__ __forceinline__ bool next_item(const AttnArgs& a, const TilePlan& p, TileCursor* cur) {
+// By one thread.
+__device__ __forceinline__ bool next_item_alone(const AttnArgs& a, const TilePlan& p, TileCursor& c, bool first) {
+    if (c.u >= c.u1) return false;
+    if (first || ++c.kh == a.cache.n_kv_heads) {
+        c.kh = 0;
+        if (!first) ++c.pair;
+        const uint4* src = (const uint4*)(p.pairs + c.pair);
+        const uint4 v[4] = {src[0], src[1], src[2], src[3]};
+        for (int i = 0; i < 4; ++i) ((uint4*)&c.w)[i] = v[i];
+    }
+    place_item(a, c, first);
+    return true;
+}
+
+// By a warp; ahead holds the pair after this one (a word a lane), loaded while this one is worked on.
+__device__ __forceinline__ bool next_item(const AttnArgs& a, const TilePlan& p, int n_pairs, TileCursor& c, bool first, uint32_t& ahead) {
+    const int lane = threadIdx.x & 31;
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) next_item_alone(a, p, cur);
+    if (c.u >= c.u1) return false;
+    const bool load = first || c.kh + 1 == a.cache.n_kv_heads;
+    const int pair = c.pair + (first ? 0 : 1);
     __syncwarp();
-    return cur->more;
+    if (load) {
+        if (first && lane < 16) ahead = ((const uint32_t*)(p.pairs + pair))[lane];
+        if (lane < 16) ((uint32_t*)&c.w)[lane] = ahead;
+        if (lane < 16 && pair + 1 < n_pairs) ahead = ((const uint32_t*)(p.pairs + pair + 1))[lane];
+        __syncwarp();
+    }
+    if (lane == 0) {
+        if (load)
+            c.kh = 0, c.pair = pair;
+        else
+            ++c.kh;
+        place_item(a, c, first);
+    }
+    __syncwarp();
+    return true;
 }
 
 // Bounded wait; false when the tries ran out.  A few instructions, as every role's loop holds some of these and the
@@ -976,15 +1041,34 @@ __host__ __device__ constexpr int v_swap(int o) {
     return D == 128 ? (o & 1) : (o & 3);
 }
 
+// Where row r of the item's rows is in q and out, and the row itself (zeros past the request's rows).
+template <int D>
+__device__ __forceinline__ int64_t row_at(const AttnArgs& a, const TileCursor& c, int r) {
+    const int n = r / a.group;
+    return ((int64_t)(c.w.q0 + n) * a.n_q_heads + c.kh * a.group + r - n * a.group) * D;
+}
+
+template <int D>
+__device__ __forceinline__ void load_row(const AttnArgs& a, const TileCursor& c, int x, int row, uint4 (&raw)[D / 8]) {
+    const int r = c.w.rb * kRows + x * 128 + row;
+    const bool live = r < c.w.q_len * a.group && c.e[x] > c.s[x];
+    const uint4* src = (const uint4*)(a.q + row_at<D>(a, c, r));
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) raw[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TilePlan plan, float* parts) {
     using Sh = TileShared<D>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     Sh& sh = *(Sh*)smem_raw;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    depend_launch();
+    depend_wait();
     const int n_pairs = plan.pair_start[a.B];
-    const long long total = plan.unit_start[n_pairs];
+    const long long total = *plan.total;
     const long long chunk = max(1LL, (total + gridDim.x - 1) / gridDim.x);
+    if (tid == 32 * kCopyWarp) plan.items[blockIdx.x] = SplitItem{0, 0, 0, -1};
     const long long first_unit = (long long)blockIdx.x * chunk, end_unit = min(first_unit + chunk, total);
     if (first_unit >= end_unit) return;
     if (tid == 0) {
@@ -1004,10 +1088,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
     if (warp == kIssueWarp) qmoe_tc::tmem_alloc(&sh.tmem, 512);
     if (warp == kCopyWarp) {
         // last pair that starts at or before the run's first unit: 32 probes at a time
-        int lo = 0, hi = n_pairs;     // unit_start[lo] <= u < unit_start[hi]
+        int lo = 0, hi = n_pairs;     // the pair is in [lo, hi)
         while (hi - lo > 1) {
-            const int step = (hi - lo + 31) / 32, at = min(lo + lane * step, hi);
-            const unsigned below = __ballot_sync(QMOE_FULL_MASK, plan.unit_start[at] <= first_unit);
+            const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+            const unsigned below = __ballot_sync(QMOE_FULL_MASK, at < hi && plan.pairs[at].unit <= first_unit);
             const int k = 31 - __clz(below);      // bit 0 is always set
             const int nlo = min(lo + k * step, hi);
             hi = min(nlo + step, hi);
@@ -1020,29 +1104,33 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
     // all 512 columns were taken, so they begin at column 0
     constexpr uint32_t tmem = 0;
     TileCursor& c = sh.cur[warp];
+    uint32_t ahead = 0;
 
     bool ok = true;
     if (warp < kExpandWarp) {
-        // ---- softmax: a thread per query row
+        // ---- softmax: a thread per query row.  2 x 128 threads of 184 registers and 256 of 72: what the block was launched with
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int x = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;           // 32 lanes a warp, lane index in bits 16..
         const uint32_t ts = tmem + x * 128 + lanes, to = tmem + 256 + x * 128 + lanes;
         uint32_t n_s = 0;                                            // steps done (the step barriers take turns)
         int tiles = 0;                                               // tiles of the run before the item
-        while (ok && next_item(a, plan, &c)) {
-            const int t_s = c.s[x], t_e = c.e[x], t0 = c.t0, lo = c.lo;
-            const int r = c.rb * kRows + x * 128 + row;
-            const bool live = r < c.q_len * a.group;
-            const int n = r / a.group, h = c.kh * a.group + r - n * a.group;
-            const int64_t base = ((int64_t)(c.q0 + n) * a.n_q_heads + h) * D;
+        uint4 raw[D / 8];                                            // this thread's query row
+        bool more = next_item(a, plan, n_pairs, c, true, ahead);
+        if (more) load_row<D>(a, c, x, row, raw);
+        while (more) {
+            const int t_s = c.s[x], t_e = c.e[x], t0 = c.t0, lo = c.w.lo;
+            const bool whole = c.whole, some = t_e > t_s;
+            const int r = c.w.rb * kRows + x * 128 + row;
+            const bool live = r < c.w.q_len * a.group;
+            const int n = r / a.group;
+            const int64_t base = row_at<D>(a, c, r);
             float factor = 0.f, m = kNoMax, l = 0.f;
-            if (t_e > t_s) {
+            if (some) {
                 // the row into the tile, its largest magnitude scaled to [2^14, 2^15)
-                uint4 raw[D / 8];
                 float mx = 0.f;
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i) {
-                    raw[i] = live ? *(const uint4*)(a.q + base + 8 * i) : make_uint4(0, 0, 0, 0);
                     mx = fmaxf(mx, fmaxf(fmaxf(fabsf(bf16_lo(raw[i].x)), fabsf(bf16_hi(raw[i].x))), fmaxf(fabsf(bf16_lo(raw[i].y)), fabsf(bf16_hi(raw[i].y)))));
                     mx = fmaxf(mx, fmaxf(fmaxf(fabsf(bf16_lo(raw[i].z)), fabsf(bf16_hi(raw[i].z))), fmaxf(fabsf(bf16_lo(raw[i].w)), fabsf(bf16_hi(raw[i].w)))));
                 }
@@ -1054,16 +1142,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
 #pragma unroll
                 for (int i = 0; i < D / 8; ++i)
                     *(uint4*)(dst + (i >> 3) * Sh::kQAtom + (((i & 7) ^ (row & 7)) << 4)) =
-                                               make_uint4(half2_bits(bf16_lo(raw[i].x) * up, bf16_hi(raw[i].x) * up),
-                                                          half2_bits(bf16_lo(raw[i].y) * up, bf16_hi(raw[i].y) * up),
-                                                          half2_bits(bf16_lo(raw[i].z) * up, bf16_hi(raw[i].z) * up),
-                                                          half2_bits(bf16_lo(raw[i].w) * up, bf16_hi(raw[i].w) * up));
+                        make_uint4(half2_bits(bf16_lo(raw[i].x) * up, bf16_hi(raw[i].x) * up), half2_bits(bf16_lo(raw[i].y) * up, bf16_hi(raw[i].y) * up),
+                                   half2_bits(bf16_lo(raw[i].z) * up, bf16_hi(raw[i].z) * up), half2_bits(bf16_lo(raw[i].w) * up, bf16_hi(raw[i].w) * up));
                 qmoe_tc::fence_async_shared();
                 arrive_warp(&sh.q_full[x]);
             }
-            const int first = a.causal ? c.kv_len - c.q_len : c.kv_len - 1;
+            const int first = a.causal ? c.w.kv_len - c.w.q_len : c.w.kv_len - 1;
             const int pos = a.causal ? first + n : first;
-            const int k_hi = min(pos, c.kv_len - 1), k_lo = a.window ? pos - a.window + 1 : 0;    // keys seen: [k_lo, k_hi]
+            const int k_hi = min(pos, c.w.kv_len - 1), k_lo = a.window ? pos - a.window + 1 : 0;    // keys seen: [k_lo, k_hi]
             for (int t = t_s; t < t_e && ok; ++t) {
                 const uint32_t tb = ts + (n_s & 1) * kStep;
                 ok = tile_wait(&sh.s_full[x][n_s & 1], (n_s >> 1) & 1);
@@ -1135,9 +1221,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                 arrive_warp(&sh.p_full[x][n_s & 1]);
                 ++n_s;
             }
-            tiles += c.t1 - c.t0;
             if (!ok) break;
-            const bool some = t_e > t_s;
+            tiles += c.t1 - t0;
+            // the next item's row is on its way while this one's sums are written
+            more = next_item(a, plan, n_pairs, c, false, ahead);
+            if (more) load_row<D>(a, c, x, row, raw);
             if (some) {
                 ok = tile_wait(&sh.o_full[x][(n_s - 1) & 1], ((n_s - 1) >> 1) & 1);
                 if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
@@ -1154,7 +1242,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                     tmem_load32(to + i, orr);
                     tmem_wait_load(orr);
                 }
-                if (live && c.whole) {
+                if (live && whole) {
                     uint4* dst = (uint4*)(a.out + base + i);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -1171,12 +1259,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                     for (int j = 0; j < 8; ++j) *(uint4*)(part + i + 4 * j) = make_uint4(orr[4 * j], orr[4 * j + 1], orr[4 * j + 2], orr[4 * j + 3]);
                 }
             }
-            if (live && !c.whole)
+            if (live && !whole)
                 *(float2*)(part_of(parts, blockIdx.x, t0 == 0 ? 1 : 0, kRows, D) + (size_t)kRows * D + 2 * (x * 128 + row)) = make_float2(m, l);
             qmoe_tc::tc_fence_before();
         }
     } else if (warp < kIssueWarp) {
         // ---- expand codes to fp16 tiles
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const int i = tid - kExpandWarp * 32;
         const int P = 1 << a.cache.page_shift, P1 = P - 1;
         // keys: thread i holds key i; which 16-byte piece first differs with the row, so that eight rows read different banks
@@ -1195,18 +1284,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
         const uint32_t v_row = v_page + (uint32_t)(P + v_in) * (D / 2), v_pair = v_page + (uint32_t)P * D + (P + v_in) * 4;
         const int swap = v_swap<D>(o);
         uint32_t tile = 0, buf = 0, phase = 0;       // raw tiles done; next expanded buffer and its phase
-        while (ok && next_item(a, plan, &c)) {
+        for (bool first = true; ok && next_item(a, plan, n_pairs, c, first, ahead); first = false) {
             for (int t = c.t0; t < c.t1; ++t, ++tile) {
                 const int st = tile % kRawStages;
                 ok = tile_wait(&sh.raw_full[st], (tile / kRawStages) & 1);
                 if (ok && phase > 0) ok = tile_wait(&sh.kv_empty[buf], (phase - 1) & 1);
                 if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
                 const unsigned char* raw = sh.raw[st];
-                const int j0 = (c.lo + t) * kKeys;
+                const int j0 = (c.w.lo + t) * kKeys;
                 const uint32_t valid = sh.valid[tile % kInfo];
                 {
                     uint32_t sz = *(const uint32_t*)(raw + k_pair);
-                    if (j0 + i >= c.kv_len || !((valid >> (i >> 4)) & 1)) sz = 0;
+                    if (j0 + i >= c.w.kv_len || !((valid >> (i >> 4)) & 1)) sz = 0;
                     const __half2 s2 = __half2half2(__ushort_as_half((uint16_t)sz)), z2 = __half2half2(__ushort_as_half((uint16_t)(sz >> 16)));
                     unsigned char* dst = sh.kv[buf] + k_dst;
 #pragma unroll 1
@@ -1235,8 +1324,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                     for (int k = 0; k < 4; ++k) {
                         uint32_t a0 = *(const uint32_t*)(raw + v_pair + ((2 * k) ^ swap) * 4), a1 = *(const uint32_t*)(raw + v_pair + ((2 * k + 1) ^ swap) * 4);
                         const bool page_ok = (valid >> (o >> 1)) & 1;
-                        if (!page_ok || j0 + 8 * o + ((2 * k) ^ swap) >= c.kv_len) a0 = 0;
-                        if (!page_ok || j0 + 8 * o + ((2 * k + 1) ^ swap) >= c.kv_len) a1 = 0;
+                        if (!page_ok || j0 + 8 * o + ((2 * k) ^ swap) >= c.w.kv_len) a0 = 0;
+                        if (!page_ok || j0 + 8 * o + ((2 * k + 1) ^ swap) >= c.w.kv_len) a1 = 0;
                         const uint32_t ss = __byte_perm(a0, a1, 0x5410), zz = __byte_perm(a0, a1, 0x7632);
                         s2[k] = *(const __half2*)&ss, z2[k] = *(const __half2*)&zz;
                     }
@@ -1271,6 +1360,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
             }
         }
     } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == kIssueWarp || warp == kIssueWarp + 2) {
             // ---- issue the products of one tile of rows, by one elected thread
             const int x = (warp - kIssueWarp) >> 1;
@@ -1280,7 +1370,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                 constexpr uint32_t kv_step = sizeof(sh.kv[0]) / 16;
                 uint32_t n_q = 0, n_s = 0, n_p = 0;             // items, steps of scores and of values done
                 uint32_t kb = 0, kph = 0, vb = 0, vph = 0;      // buffers and phases: keys, values
-                while (ok && next_item_alone(a, plan, &c)) {
+                for (bool first = true; ok && next_item_alone(a, plan, c, first); first = false) {
                     const int t0 = 2 * c.t0, t1 = 2 * c.t1, s = c.s[x], e = c.e[x];
                     // scores of step t + 1 go ahead of the values of step t, so that the softmax finds its next scores ready
 #pragma unroll 1
@@ -1333,13 +1423,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
             // ---- copy pages: lane i the tile's i-th
             const int per_tile = kKeys >> a.cache.page_shift, per_page = (1 << a.cache.page_shift) / 16;
             uint32_t tile = 0;
-                while (ok && next_item(a, plan, &c)) {
+                for (bool first = true; ok && next_item(a, plan, n_pairs, c, first, ahead); first = false) {
+                if (lane == 0 && c.t0 == 0 && !c.whole)
+                    plan.items[blockIdx.x] = SplitItem{c.w.b, c.kh, c.w.rb, (int)((first_unit + tile + c.w.n - 1) / chunk)};
                 for (int t = c.t0; t < c.t1; ++t, ++tile) {
                     const int st = tile % kRawStages;
-                    const int blk = (c.lo + t) * per_tile + lane;
-                    const bool mine = lane < per_tile && (blk << a.cache.page_shift) < c.kv_len;
+                    const int blk = (c.w.lo + t) * per_tile + lane;
+                    const bool mine = lane < per_tile && (blk << a.cache.page_shift) < c.w.kv_len;
                     int page = -1;
-                    if (mine && blk < a.max_blocks) page = a.table[(int64_t)c.b * a.max_blocks + blk];
+                    if (mine && blk < a.max_blocks) page = a.table[(int64_t)c.w.b * a.max_blocks + blk];
                     const bool good = page >= 0 && page < a.cache.n_pages;
                     if (mine && !good) attn_set_error(QMOE_EINVAL);
                     const unsigned mask = __ballot_sync(QMOE_FULL_MASK, good);
@@ -1373,27 +1465,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
     }
 }
 
-// Joins the parts of items that several blocks of tile_kernel shared.  A few blocks per (pair, kv head).
-constexpr int kCombineSlices = 16;
-
-template <int D>
-__global__ void __launch_bounds__(256) tile_combine_kernel(AttnArgs a, TilePlan plan, int n_ctas, const float* parts) {
-    const int pair = blockIdx.x / a.cache.n_kv_heads, kh = blockIdx.x - pair * a.cache.n_kv_heads;
-    const int n_pairs = plan.pair_start[a.B];
-    if (pair >= n_pairs) return;
-    const long long total = plan.unit_start[n_pairs], chunk = max(1LL, (total + n_ctas - 1) / n_ctas);
-    const long long pu = plan.unit_start[pair], n = (plan.unit_start[pair + 1] - pu) / a.cache.n_kv_heads;
-    const long long u0 = pu + kh * n, u1 = u0 + n;
-    const int c0 = (int)(u0 / chunk), c1 = (int)((u1 - 1) / chunk);
-    if (c0 == c1) return;
-    const int b = plan.pair_b[pair], rb = pair - plan.pair_start[b], q0 = a.q_start[b];
-    const int rows = min(kRows, (a.q_start[b + 1] - q0) * a.group - rb * kRows);
-    for (int i = blockIdx.y * 256 + threadIdx.x; i < rows * (D / 4); i += 256 * kCombineSlices) {
-        const int r = i / (D / 4), d0 = (i - r * (D / 4)) * 4;
-        join_parts<D>(a, parts, c0, c1, u0, chunk, kRows, r, d0, q0, rb * kRows + r, kh);
-    }
-}
-
 // Query rows (a multiple of 8) that the few-row path takes per (request, kv head): the batch's largest where 32
 // hold it, else enough for a single query (requests with more go to the tiles); 0 for groups above 32.
 int decode_rows(int group, int max_q) {
@@ -1402,37 +1473,55 @@ int decode_rows(int group, int max_q) {
     return rows == 0 ? 0 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
 }
 
+// Blocks of the few-row path that are on the device together.
+size_t decode_fit(int rows) { return (size_t)qmoe::sm_count() * (rows <= 8 ? 4 : rows <= 16 ? 3 : 2); }
+
 // Blocks of the few-row path: as many as fit on the device, no more than tiles.
 long long decode_blocks(int rows, int B, int n_kv_heads, int max_kv) {
-    const long long fit = (long long)qmoe::sm_count() * (rows <= 8 ? 4 : rows <= 16 ? 3 : 2);
+    const long long fit = (long long)decode_fit(rows);
     return std::min(fit, (long long)B * n_kv_heads * std::max(1, (max_kv + kTile - 1) / kTile));
 }
 
+size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
+
+// Workspace of the few-row path: a record for each block, then the blocks' parts.
 size_t decode_ws(int rows, int head_dim) {
-    if (rows == 0) return 0;
-    const size_t fit = (size_t)qmoe::sm_count() * (rows <= 8 ? 4 : rows <= 16 ? 3 : 2);
-    return fit * 2 * rows * (head_dim + 2) * sizeof(float);
+    return rows == 0 ? 0 : align256(decode_fit(rows) * sizeof(SplitItem)) + align256(decode_fit(rows) * 2 * rows * (head_dim + 2) * sizeof(float));
 }
 
-template <int D, int NT>
-int launch_decode(const AttnArgs& a, float* parts, cudaStream_t st) {
-    const int smem = (int)sizeof(DecodeShared<D, NT>);
-    int rc = qmoe::smem_attr((const void*)decode_kernel<D, NT>, smem, "attention attr");
-    if (rc) return rc;
-    const long long blocks = decode_blocks(8 * NT, a.B, a.cache.n_kv_heads, a.max_kv);
-    decode_kernel<D, NT><<<(unsigned)blocks, kDecodeThreads, smem, st>>>(a, 8 * NT, parts);
-    if ((rc = qmoe::launch_check("decode_kernel"))) return rc;
+template <typename T>
+struct Same {
+    using type = T;
+};
+
+// Launches a kernel that may start while the one before it in the stream still runs (it waits itself, by depend_wait).
+template <typename... Args>
+int launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t st, const char* who, typename Same<Args>::type... args) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)(a.B * a.cache.n_kv_heads));
-    cfg.blockDim = dim3(kCombineThreads);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return qmoe::cuda_check(cudaLaunchKernelEx(&cfg, combine_kernel<D>, a, 8 * NT, (int)blocks, (const float*)parts),
-                            "combine_kernel");
+    return qmoe::cuda_check(cudaLaunchKernelEx(&cfg, kernel, args...), who);
+}
+
+template <int D, int NT>
+int launch_decode(const AttnArgs& a, void* ws, cudaStream_t st) {
+    constexpr int rows = 8 * NT;
+    const int smem = (int)sizeof(DecodeShared<D, NT>);
+    int rc = qmoe::smem_attr((const void*)decode_kernel<D, NT>, smem, "attention attr");
+    if (rc) return rc;
+    const unsigned blocks = (unsigned)decode_blocks(rows, a.B, a.cache.n_kv_heads, a.max_kv);
+    SplitItem* items = (SplitItem*)ws;
+    float* parts = (float*)((char*)ws + align256(decode_fit(rows) * sizeof(SplitItem)));
+    decode_kernel<D, NT><<<blocks, kDecodeThreads, smem, st>>>(a, rows, items, parts);
+    if ((rc = qmoe::launch_check("decode_kernel"))) return rc;
+    return launch_dependent(join_kernel<D>, dim3(blocks, NT == 1 ? 8 : 16), kJoinThreads, 0, st, "join_kernel", a, items, parts, rows);
 }
 
 // Workspace of the tile path: the plan, then the blocks' parts.  max_pairs bounds the sum of ceil(rows / 256).
@@ -1447,14 +1536,15 @@ TileWs tile_ws(void* base, int B, int group, int head_dim, int n_q_tokens) {
     size_t off = 0;
     auto take = [&](size_t bytes) {
         void* p = base ? (void*)((char*)base + off) : nullptr;
-        off += (bytes + 255) & ~(size_t)255;
+        off += align256(bytes);
         return p;
     };
-    const long long pairs = (long long)n_q_tokens * group / kRows + B;
-    w.plan.max_pairs = (int)std::min(pairs, 0x7FFFFFFELL);
+    w.plan.max_pairs = (int)((long long)n_q_tokens * group / kRows + B);
     w.plan.pair_start = (int32_t*)take(sizeof(int32_t) * ((size_t)B + 1));
-    w.plan.unit_start = (long long*)take(sizeof(long long) * ((size_t)w.plan.max_pairs + 1));
     w.plan.pair_b = (int32_t*)take(sizeof(int32_t) * (size_t)w.plan.max_pairs);
+    w.plan.pairs = (PairInfo*)take(sizeof(PairInfo) * (size_t)w.plan.max_pairs);
+    w.plan.total = (long long*)take(sizeof(long long));
+    w.plan.items = (SplitItem*)take(sizeof(SplitItem) * (size_t)qmoe::sm_count());
     w.parts = (float*)take((size_t)qmoe::sm_count() * 2 * kRows * (head_dim + 2) * sizeof(float));
     w.bytes = off;
     return w;
@@ -1465,13 +1555,13 @@ int launch_tiles(const AttnArgs& a, const TileWs& w, int min_rows, cudaStream_t 
     const int smem = (int)sizeof(TileShared<D>), blocks = qmoe::sm_count();
     int rc = qmoe::smem_attr((const void*)tile_kernel<D>, smem, "attention attr");
     if (rc) return rc;
-    const long long items = (long long)w.plan.max_pairs * a.cache.n_kv_heads;
-    if (items > 0x7FFFFFFFLL) return qmoe::fail(QMOE_EINVAL, "kv4_attention: batch too large");
-    tile_plan_kernel<<<1, kPlanTile, 0, st>>>(a, w.plan, min_rows);
-    tile_kernel<D><<<blocks, kTileThreads, smem, st>>>(a, w.plan, w.parts);
-    if ((rc = qmoe::launch_check("tile_kernel"))) return rc;
-    tile_combine_kernel<D><<<dim3((unsigned)items, kCombineSlices), 256, 0, st>>>(a, w.plan, blocks, w.parts);
-    return qmoe::launch_check("tile_combine_kernel");
+    if (min_rows == 0)      // the call's first kernel
+        tile_plan_kernel<<<1, kPlanTile, 0, st>>>(a, w.plan, min_rows);
+    else
+        rc = launch_dependent(tile_plan_kernel, dim3(1), kPlanTile, 0, st, "tile_plan_kernel", a, w.plan, min_rows);
+    if (rc || (rc = qmoe::launch_check("tile_plan_kernel"))) return rc;
+    if ((rc = launch_dependent(tile_kernel<D>, dim3(blocks), kTileThreads, smem, st, "tile_kernel", a, w.plan, w.parts))) return rc;
+    return launch_dependent(join_kernel<D>, dim3(blocks, 32), kJoinThreads, 0, st, "join_kernel", a, w.plan.items, w.parts, kRows);
 }
 
 // Whether some request of the batch has more rows than the few-row path takes.
@@ -1482,6 +1572,8 @@ int check_sizes(const char* who, int B, int n_q_heads, int n_kv_heads, int head_
     if (B < 0 || n_q_tokens < 0 || max_q < 0 || max_kv < 0 || n_kv_heads < 1 || n_q_heads < n_kv_heads ||
         n_q_heads % n_kv_heads)
         return qmoe::fail(QMOE_EINVAL, std::string(who) + ": bad sizes (n_q_heads must be a multiple of n_kv_heads)");
+    if ((long long)n_q_tokens * (n_q_heads / n_kv_heads) + (long long)kRows * B > 0x7FFFFFFFLL)
+        return qmoe::fail(QMOE_EINVAL, std::string(who) + ": too many query rows in one call");
     if (n_q_heads / n_kv_heads > 128)
         return qmoe::fail(QMOE_EUNSUPPORTED, std::string(who) + ": more than 128 query heads per kv head");
     return QMOE_OK;
@@ -1506,7 +1598,7 @@ extern "C" int kv4_attention_ws_size(int B, int n_q_heads, int n_kv_heads, int h
     const int rc = check_sizes("kv4_attention_ws_size", B, n_q_heads, n_kv_heads, head_dim, n_q_tokens, max_q, max_kv);
     if (rc) return rc;
     const int group = n_q_heads / n_kv_heads, rows = decode_rows(group, max_q);
-    *bytes = ((decode_ws(rows, head_dim) + 255) & ~(size_t)255) + (has_tiles(group, max_q, rows) ? tile_ws(nullptr, B, group, head_dim, n_q_tokens).bytes : 0);
+    *bytes = decode_ws(rows, head_dim) + (has_tiles(group, max_q, rows) ? tile_ws(nullptr, B, group, head_dim, n_q_tokens).bytes : 0);
     return QMOE_OK;
 }
 
@@ -1530,15 +1622,14 @@ extern "C" int kv4_attention(const kv4_cache* cache, const void* q, int n_q_toke
     cudaStream_t st = (cudaStream_t)stream;
     const int rows = decode_rows(a.group, max_q), D = cache->head_dim;
     const bool tiles = has_tiles(a.group, max_q, rows);
-    const size_t few = (decode_ws(rows, D) + 255) & ~(size_t)255;
+    const size_t few = decode_ws(rows, D);
     const TileWs tw = tiles ? tile_ws((char*)workspace + few, B, a.group, D, n_q_tokens) : TileWs{};
     if (ws_bytes < few + tw.bytes) return qmoe::fail(QMOE_ECAPACITY, "kv4_attention: workspace too small");
     if (!workspace || !kv4::aligned16(workspace)) return qmoe::fail(QMOE_EINVAL, "kv4_attention: workspace NULL or not 16-byte aligned");
     if ((long long)B * cache->n_kv_heads > 0x7FFFFFFFLL) return qmoe::fail(QMOE_EINVAL, "kv4_attention: batch too large");
-    float* parts = (float*)workspace;
-    if (rows == 8) rc = D == 128 ? launch_decode<128, 1>(a, parts, st) : launch_decode<64, 1>(a, parts, st);
-    if (rows == 16) rc = D == 128 ? launch_decode<128, 2>(a, parts, st) : launch_decode<64, 2>(a, parts, st);
-    if (rows == 32) rc = D == 128 ? launch_decode<128, 4>(a, parts, st) : launch_decode<64, 4>(a, parts, st);
+    if (rows == 8) rc = D == 128 ? launch_decode<128, 1>(a, workspace, st) : launch_decode<64, 1>(a, workspace, st);
+    if (rows == 16) rc = D == 128 ? launch_decode<128, 2>(a, workspace, st) : launch_decode<64, 2>(a, workspace, st);
+    if (rows == 32) rc = D == 128 ? launch_decode<128, 4>(a, workspace, st) : launch_decode<64, 4>(a, workspace, st);
     if (rc || !tiles) return rc;
     return D == 128 ? launch_tiles<128>(a, tw, rows, st) : launch_tiles<64>(a, tw, rows, st);
 }
