@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, const Sp
 // shared memory, k = s u + z rounded once to 11 bits (bf16 inputs and outputs have 8); P and the
 // values are fp16 too, statistics and sums fp32.  Queries carry a power of two per row (exact), so any
 // bf16 magnitude is inside fp16's range.  The running maximum moves, and O is rescaled, only when a
-// row passes it by 2^8; P carries 2^6, so that small weights stay above fp16's subnormals.
+// row's weights by it pass 2^14; P carries 2^6, so that small weights stay above fp16's subnormals.
 //
 // Roles, one block per SM: 2 x 4 softmax warps (a thread per row), 4 warps that expand keys and values,
 // one warp that issues the products, one that copies pages.  What bounds it: at 256 rows the tensor
@@ -1108,8 +1108,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
 
     bool ok = true;
     if (warp < kExpandWarp) {
-        // ---- softmax: a thread per query row.  2 x 128 threads of 184 registers and 256 of 72: what the block was launched with
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        // ---- softmax: a thread per query row.  2 x 128 threads of 160 registers and 256 of 96: what the block was launched with
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
         const int x = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;           // 32 lanes a warp, lane index in bits 16..
         const uint32_t ts = tmem + x * 128 + lanes, to = tmem + 256 + x * 128 + lanes;
@@ -1150,28 +1150,45 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
             const int first = a.causal ? c.w.kv_len - c.w.q_len : c.w.kv_len - 1;
             const int pos = a.causal ? first + n : first;
             const int k_hi = min(pos, c.w.kv_len - 1), k_lo = a.window ? pos - a.window + 1 : 0;    // keys seen: [k_lo, k_hi]
+            bool far = false;
+            uint64_t mul2 = pair(factor, factor), nb2 = pair(6.f - m, 6.f - m);
             for (int t = t_s; t < t_e && ok; ++t) {
                 const uint32_t tb = ts + (n_s & 1) * kStep;
                 ok = tile_wait(&sh.s_full[x][n_s & 1], (n_s >> 1) & 1);
                 if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
                 qmoe_tc::tc_fence_after();
-                uint32_t sr[kStep];
-                tmem_load64(tb, sr);
                 const int j0 = lo * kKeys + t * kStep;
                 const uint32_t valid = sh.valid[(tiles + (t >> 1) - t0) % kInfo] >> (4 * (t & 1)) & 15u;
-                if (__builtin_expect(j0 + kStep - 1 > k_hi || j0 < k_lo || valid != 15u, 0)) mask64(sr, k_lo - j0, k_hi - j0, valid);
-                float mx, m1 = -INFINITY;
-                {
-                    float m0 = -INFINITY;
+                const bool edge = j0 + kStep - 1 > k_hi || j0 < k_lo || valid != 15u;
+                // The weights are taken with the maximum as it stands; only when a row's sum shows that it has grown too
+                // far (or there is none yet) the scores are read again, for their maximum and for the weights by it.
+                uint32_t sr[kStep];
+                float e0, e1;
+#pragma unroll 1
+                for (bool again = false;; again = true) {
+                    tmem_load64(tb, sr);
+                    if (__builtin_expect(edge, 0)) mask64(sr, k_lo - j0, k_hi - j0, valid);
+                    if (__builtin_expect(far, 0)) {
 #pragma unroll
-                    for (int i = 0; i < kStep; i += 4) {
-                        m0 = fmaxf(m0, fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])));
-                        m1 = fmaxf(m1, fmaxf(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])));
+                        for (int i = 0; i < kStep; ++i) sr[i] = __float_as_uint(__uint_as_float(sr[i]) * factor);
                     }
-                    mx = fmaxf(m0, m1) * factor;
-                }
-                if (__builtin_expect(__any_sync(QMOE_FULL_MASK, mx > m + kSlack), 0)) {
-                    const float m2 = fmaxf(m, mx), f = ex2(m - m2);
+                    uint64_t l2[2] = {0, 0};
+#pragma unroll
+                    for (int i = 0; i < kStep; i += 2) {
+                        unpair(fma2(pair(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), mul2, nb2), &e0, &e1);
+                        e0 = ex2(e0), e1 = ex2(e1);
+                        l2[(i >> 1) & 1] = add2(l2[(i >> 1) & 1], pair(e0, e1));
+                        sr[i] = __float_as_uint(e0), sr[i + 1] = __float_as_uint(e1);
+                    }
+                    unpair(add2(l2[0], l2[1]), &e0, &e1);
+                    e0 += e1;
+                    if (again || !__any_sync(QMOE_FULL_MASK, !(e0 < 16384.f))) break;
+                    tmem_load64(tb, sr);
+                    if (edge) mask64(sr, k_lo - j0, k_hi - j0, valid);
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < kStep; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])));
+                    const float m2 = fmaxf(m, mx * factor), f = ex2(m - m2);
                     m = m2;
                     l *= f;
                     if (t > t_s) {
@@ -1188,34 +1205,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                             tmem_store16(to + i, orr);
                         }
                     }
+                    // the fused product is not rounded before m is taken off: where m is so large that this shows, round first
+                    far = __any_sync(QMOE_FULL_MASK, fabsf(m) > 65536.f && m != kNoMax);
+                    mul2 = far ? pair(1.f, 1.f) : pair(factor, factor), nb2 = pair(6.f - m, 6.f - m);
                 }
-                const float nb = 6.f - m;
-                // the fused product is not rounded before m is taken off: where m is so large that this shows, round first
-                const bool far = __any_sync(QMOE_FULL_MASK, fabsf(m) > 65536.f && m != kNoMax);
-                const uint64_t nb2 = pair(nb, nb), mul2 = far ? pair(1.f, 1.f) : pair(factor, factor);
-                uint64_t l2[2] = {0, 0};
-                if (__builtin_expect(far, 0)) {
-#pragma unroll
-                    for (int i = 0; i < kStep; ++i) sr[i] = __float_as_uint(__uint_as_float(sr[i]) * factor);
-                }
+                if (!ok) break;
+                l += e0;
                 uint32_t pr[kStep / 2];
-#pragma unroll
-                for (int i = 0; i < kStep; i += 2) {
-                    float e0, e1;
-                    unpair(fma2(pair(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), mul2, nb2), &e0, &e1);
-                    e0 = ex2(e0), e1 = ex2(e1);
-                    l2[(i >> 1) & 1] = add2(l2[(i >> 1) & 1], pair(e0, e1));
-                    sr[i] = __float_as_uint(e0), sr[i + 1] = __float_as_uint(e1);
-                }
 #pragma unroll
                 for (int i = 0; i < kStep / 2; ++i)
                     pr[i] = half2_bits(__uint_as_float(sr[(2 * i) ^ v_swap<D>(i >> 2)]), __uint_as_float(sr[(2 * i + 1) ^ v_swap<D>(i >> 2)]));
                 tmem_store32(tb, pr);      // over the scores
-                {
-                    float e0, e1;
-                    unpair(add2(l2[0], l2[1]), &e0, &e1);
-                    l += e0 + e1;
-                }
                 tmem_wait_store();
                 qmoe_tc::tc_fence_before();
                 arrive_warp(&sh.p_full[x][n_s & 1]);
@@ -1265,7 +1265,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
         }
     } else if (warp < kIssueWarp) {
         // ---- expand codes to fp16 tiles
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         const int i = tid - kExpandWarp * 32;
         const int P = 1 << a.cache.page_shift, P1 = P - 1;
         // keys: thread i holds key i; which 16-byte piece first differs with the row, so that eight rows read different banks
@@ -1336,7 +1336,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                         uint32_t w[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) w[k] = *(const uint32_t*)(raw + v_row + (k ^ swap) * (D / 2) + word * 4);
-#pragma unroll 1
+#pragma unroll
                         for (int hh = 0; hh < 2; ++hh) {
                             uint32_t r[4][4];      // [value 2 v + hh][pair of keys]
 #pragma unroll
@@ -1360,7 +1360,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
             }
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         if (warp == kIssueWarp || warp == kIssueWarp + 2) {
             // ---- issue the products of one tile of rows, by one elected thread
             const int x = (warp - kIssueWarp) >> 1;
