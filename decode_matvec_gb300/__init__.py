@@ -129,11 +129,19 @@ def _np_ptr(a: np.ndarray) -> int:
     return a.ctypes.data if a is not None else None
 
 
+_raw_stream = None      # (device index of the current device, its current stream's handle), looked up on first use
+
+
 def _stream_ptr(stream) -> int:
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return int(stream.cuda_stream)
+    if stream is not None:
+        return int(stream.cuda_stream)
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.init()
+        _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    device, current = _raw_stream
+    return current(device())
 
 
 def _dptr(t) -> int | None:
@@ -518,14 +526,23 @@ class Kv4Cache:
         return cls(pages, page_size, n_kv_heads, head_dim)
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+def _refuse(what: str):
+    raise ValueError(what)
 
 
-def _i32(t, n: int, name: str):
-    """Device pointer of a contiguous int32 tensor of at least n elements."""
-    _need(t.element_size() == 4 and t.is_contiguous() and t.numel() >= n, f"{name}: contiguous int32, {n} elements")
+# The calls below are made once per layer and decode step: each tensor is looked at once (layout, then pointer), in
+# as few Python calls as that takes.
+def _i32(t, n: int, name: str) -> int:
+    """Device pointer of a contiguous 32-bit tensor of at least n elements."""
+    if t.itemsize != 4 or not t.is_contiguous() or t.numel() < n:
+        _refuse(f"{name}: a contiguous int32 tensor of {n} elements or more")
+    return t.data_ptr()
+
+
+def _b16(t, n: int, name: str) -> int:
+    """Device pointer of a contiguous 16-bit tensor of n elements."""
+    if t.itemsize != 2 or not t.is_contiguous() or t.numel() != n:
+        _refuse(f"{name}: a contiguous bf16 tensor of {n} elements")
     return t.data_ptr()
 
 
@@ -535,12 +552,16 @@ def kv4_block_tables(cached, new_tokens, free_pages, n_free, page_size: int, tab
     new pages from the stack free_pages[:n_free], writes their entries of table [B, max_blocks], and gives
     q_start [B + 1], kv_len [B], and the slot and position of each new token."""
     B, n = new_tokens.numel(), slots.numel()
-    _need(table.dim() == 2 and table.shape[0] == B, "table: [B, max_blocks]")
-    _check(_lib.kv4_block_tables(_i32(cached, B, "cached"), _i32(new_tokens, B, "new_tokens"), B,
-                                 _i32(free_pages, 0, "free_pages"), _i32(n_free, 1, "n_free"), page_size,
-                                 _i32(table, 0, "table"), table.shape[1], _i32(q_start, B + 1, "q_start"),
-                                 _i32(kv_len, B, "kv_len"), _i32(slots, n, "slots"), _i32(positions, n, "positions"),
-                                 n, _i32(n_free_out, 1, "n_free_out"), _stream_ptr(stream)), "kv4_block_tables")
+    rows, width = table.shape
+    if rows != B:
+        _refuse("table: [B, max_blocks]")
+    st = _lib.kv4_block_tables(_i32(cached, B, "cached"), _i32(new_tokens, B, "new_tokens"), B,
+                               _i32(free_pages, 0, "free_pages"), _i32(n_free, 1, "n_free"), page_size,
+                               _i32(table, 0, "table"), width, _i32(q_start, B + 1, "q_start"),
+                               _i32(kv_len, B, "kv_len"), _i32(slots, n, "slots"), _i32(positions, n, "positions"),
+                               n, _i32(n_free_out, 1, "n_free_out"), _stream_ptr(stream))
+    if st:
+        _check(st, "kv4_block_tables")
 
 
 def qk_norm_rope(qkv, n_q_heads: int, n_kv_heads: int, head_dim: int, q_weight, k_weight, eps: float, cos_sin, positions,
@@ -548,44 +569,52 @@ def qk_norm_rope(qkv, n_q_heads: int, n_kv_heads: int, head_dim: int, q_weight, 
     """Per-head RMS norms of queries and keys (weights None: no norm) and their rotation (cos_sin None: none) from
     the rows of qkv [T, >= heads * head_dim] (bf16) into q_out [T, n_q_heads, head_dim] and k_out; with a cache,
     keys and values are also written to it at slots."""
-    T = qkv.shape[0]
-    _need(qkv.dim() == 2 and qkv.element_size() == 2 and qkv.stride(1) == 1, "qkv: bf16 [T, heads * head_dim], rows contiguous")
-    _need(qkv.shape[1] >= (n_q_heads + n_kv_heads * (1 if cache is None else 2)) * head_dim, "qkv: too few columns")
-    _need(n_q_heads == 0 or (q_out.numel() == T * n_q_heads * head_dim and q_out.is_contiguous()), "q_out: contiguous [T, n_q_heads, head_dim]")
-    _need(k_out is None or (k_out.numel() == T * n_kv_heads * head_dim and k_out.is_contiguous()),
-          "k_out: contiguous [T, n_kv_heads, head_dim]")
-    n_pos = rot = 0
+    T, width = qkv.shape
+    row, one = qkv.stride()
+    if one != 1 or qkv.itemsize != 2 or width < (n_q_heads + n_kv_heads * (1 if cache is None else 2)) * head_dim:
+        _refuse("qkv: bf16 [T, heads * head_dim], rows contiguous")
+    n_pos = rot = cs = pos = None
     if cos_sin is not None:
         n_pos, rot = cos_sin.shape
-        _need(cos_sin.element_size() == 4 and cos_sin.is_contiguous(), "cos_sin: contiguous fp32 [n_pos, rot_dim]")
-    for w in (q_weight, k_weight):
-        _need(w is None or (w.numel() == head_dim and w.element_size() == 2 and w.is_contiguous()), "weights: bf16 [head_dim]")
-    _check(_lib.qk_norm_rope(qkv.data_ptr(), qkv.stride(0), T, n_q_heads, n_kv_heads, head_dim, _dptr(q_weight),
-                             _dptr(k_weight), eps, _dptr(cos_sin), rot, int(interleaved), n_pos,
-                             None if cos_sin is None else _i32(positions, T, "positions"), _dptr(q_out), _dptr(k_out),
-                             None if cache is None else cache.ref, None if slots is None else _i32(slots, T, "slots"),
-                             _stream_ptr(stream)), "qk_norm_rope")
+        cs, pos = _i32(cos_sin, 0, "cos_sin"), _i32(positions, T, "positions")
+    st = _lib.qk_norm_rope(qkv.data_ptr(), row, T, n_q_heads, n_kv_heads, head_dim,
+                           None if q_weight is None else _b16(q_weight, head_dim, "q_weight"),
+                           None if k_weight is None else _b16(k_weight, head_dim, "k_weight"), eps, cs, rot or 0,
+                           interleaved, n_pos or 0, pos,
+                           _b16(q_out, T * n_q_heads * head_dim, "q_out") if n_q_heads else None,
+                           None if k_out is None else _b16(k_out, T * n_kv_heads * head_dim, "k_out"),
+                           None if cache is None else cache.ref, None if slots is None else _i32(slots, T, "slots"),
+                           _stream_ptr(stream))
+    if st:
+        _check(st, "qk_norm_rope")
     return q_out, k_out
+
+
+def _heads(x, T: int, cache: Kv4Cache) -> int:
+    """Token stride of x [T, n_kv_heads, head_dim] (16-bit, a token's heads contiguous)."""
+    s0, s1, s2 = x.stride()
+    if x.shape != (T, cache.n_kv_heads, cache.head_dim) or x.itemsize != 2 or s2 != 1 or (s1 != cache.head_dim and cache.n_kv_heads > 1):
+        _refuse("k, v: bf16 [T, n_kv_heads, head_dim], a token's heads contiguous")
+    return s0
 
 
 def kv4_append(cache: Kv4Cache, k, v, slots, stream=None):
     """Quantise keys and values [T, n_kv_heads, head_dim] (bf16; any token stride) into the cache at slots."""
-    T, D = k.shape[0], cache.head_dim
-    for x in (k, v):
-        _need(x.dim() == 3 and x.shape == (T, cache.n_kv_heads, D) and x.element_size() == 2 and x.stride(2) == 1 and
-              (x.stride(1) == D or cache.n_kv_heads == 1), "k, v: bf16 [T, n_kv_heads, head_dim], a token's heads contiguous")
-    _check(_lib.kv4_append(cache.ref, k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0), T, _i32(slots, T, "slots"),
-                           _stream_ptr(stream)), "kv4_append")
+    T = k.shape[0]
+    st = _lib.kv4_append(cache.ref, k.data_ptr(), _heads(k, T, cache), v.data_ptr(), _heads(v, T, cache), T,
+                         _i32(slots, T, "slots"), _stream_ptr(stream))
+    if st:
+        _check(st, "kv4_append")
 
 
 def kv4_gather(cache: Kv4Cache, slots, k_out, v_out, stream=None):
     """The keys and values that the cache holds at slots, as bf16 [n, n_kv_heads, head_dim]."""
     n = slots.numel()
-    for x in (k_out, v_out):
-        _need(x.numel() == n * cache.n_kv_heads * cache.head_dim and x.element_size() == 2 and x.is_contiguous(),
-              "k_out, v_out: contiguous bf16 [n, n_kv_heads, head_dim]")
-    _check(_lib.kv4_gather(cache.ref, _i32(slots, n, "slots"), n, k_out.data_ptr(), v_out.data_ptr(),
-                           _stream_ptr(stream)), "kv4_gather")
+    size = n * cache.n_kv_heads * cache.head_dim
+    st = _lib.kv4_gather(cache.ref, _i32(slots, n, "slots"), n, _b16(k_out, size, "k_out"), _b16(v_out, size, "v_out"),
+                         _stream_ptr(stream))
+    if st:
+        _check(st, "kv4_gather")
     return k_out, v_out
 
 
@@ -602,12 +631,14 @@ def kv4_attention(cache: Kv4Cache, q, q_start, kv_len, table, out, workspace, ma
     """Softmax attention of a ragged batch over the cache: q, out [n_q_tokens, n_q_heads, head_dim] (bf16), request b's
     queries being rows q_start[b] .. q_start[b + 1] - 1 and the last tokens of its kv_len[b]."""
     n, hq, D = q.shape
+    rows, width = table.shape
     B = kv_len.numel()
-    _need(q.element_size() == 2 and q.is_contiguous() and D == cache.head_dim, "q: contiguous bf16 [n, n_q_heads, head_dim]")
-    _need(out.shape == q.shape and out.element_size() == 2 and out.is_contiguous(), "out: as q")
-    _need(table.dim() == 2 and table.shape[0] == B, "table: [B, max_blocks]")
-    _check(_lib.kv4_attention(cache.ref, q.data_ptr(), n, hq, _i32(q_start, B + 1, "q_start"), _i32(kv_len, B, "kv_len"), B,
-                              _i32(table, 0, "table"), table.shape[1], max_q, max_kv, scale, int(causal), window,
-                              out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                              _stream_ptr(stream)), "kv4_attention")
+    if D != cache.head_dim or rows != B:
+        _refuse("q: [n, n_q_heads, head_dim] of the cache's head_dim; table: [B, max_blocks]")
+    st = _lib.kv4_attention(cache.ref, _b16(q, n * hq * D, "q"), n, hq, _i32(q_start, B + 1, "q_start"),
+                            _i32(kv_len, B, "kv_len"), B, _i32(table, 0, "table"), width, max_q, max_kv, scale, causal,
+                            window, _b16(out, n * hq * D, "out"), workspace.data_ptr(), workspace.nbytes,
+                            _stream_ptr(stream))
+    if st:
+        _check(st, "kv4_attention")
     return out

@@ -1489,27 +1489,6 @@ size_t decode_ws(int rows, int head_dim) {
     return rows == 0 ? 0 : align256(decode_fit(rows) * sizeof(SplitItem)) + align256(decode_fit(rows) * 2 * rows * (head_dim + 2) * sizeof(float));
 }
 
-template <typename T>
-struct Same {
-    using type = T;
-};
-
-// Launches a kernel that may start while the one before it in the stream still runs (it waits itself, by depend_wait).
-template <typename... Args>
-int launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t st, const char* who, typename Same<Args>::type... args) {
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return qmoe::cuda_check(cudaLaunchKernelEx(&cfg, kernel, args...), who);
-}
-
 template <int D, int NT>
 int launch_decode(const AttnArgs& a, void* ws, cudaStream_t st) {
     constexpr int rows = 8 * NT;
@@ -1521,7 +1500,7 @@ int launch_decode(const AttnArgs& a, void* ws, cudaStream_t st) {
     float* parts = (float*)((char*)ws + align256(decode_fit(rows) * sizeof(SplitItem)));
     decode_kernel<D, NT><<<blocks, kDecodeThreads, smem, st>>>(a, rows, items, parts);
     if ((rc = qmoe::launch_check("decode_kernel"))) return rc;
-    return launch_dependent(join_kernel<D>, dim3(blocks, NT == 1 ? 8 : 16), kJoinThreads, 0, st, "join_kernel", a, items, parts, rows);
+    return kv4::launch_dependent(join_kernel<D>, dim3(blocks, NT == 1 ? 8 : 16), kJoinThreads, 0, st, "join_kernel", a, items, parts, rows);
 }
 
 // Workspace of the tile path: the plan, then the blocks' parts.  max_pairs bounds the sum of ceil(rows / 256).
@@ -1558,10 +1537,10 @@ int launch_tiles(const AttnArgs& a, const TileWs& w, int min_rows, cudaStream_t 
     if (min_rows == 0)      // the call's first kernel
         tile_plan_kernel<<<1, kPlanTile, 0, st>>>(a, w.plan, min_rows);
     else
-        rc = launch_dependent(tile_plan_kernel, dim3(1), kPlanTile, 0, st, "tile_plan_kernel", a, w.plan, min_rows);
+        rc = kv4::launch_dependent(tile_plan_kernel, dim3(1), kPlanTile, 0, st, "tile_plan_kernel", a, w.plan, min_rows);
     if (rc || (rc = qmoe::launch_check("tile_plan_kernel"))) return rc;
-    if ((rc = launch_dependent(tile_kernel<D>, dim3(blocks), kTileThreads, smem, st, "tile_kernel", a, w.plan, w.parts))) return rc;
-    return launch_dependent(join_kernel<D>, dim3(blocks, 32), kJoinThreads, 0, st, "join_kernel", a, w.plan.items, w.parts, kRows);
+    if ((rc = kv4::launch_dependent(tile_kernel<D>, dim3(blocks), kTileThreads, smem, st, "tile_kernel", a, w.plan, w.parts))) return rc;
+    return kv4::launch_dependent(join_kernel<D>, dim3(blocks, 32), kJoinThreads, 0, st, "join_kernel", a, w.plan.items, w.parts, kRows);
 }
 
 // Whether some request of the batch has more rows than the few-row path takes.

@@ -47,4 +47,25 @@ inline int view_of(const kv4_cache* c, const char* who, CacheView* v) {
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
+template <typename T>
+struct Same {
+    using type = T;
+};
+
+// Launches a kernel that may start while the one before it in the stream still runs (it waits itself, by depend_wait).
+template <typename... Args>
+inline int launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t st, const char* who, typename Same<Args>::type... args) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return qmoe::cuda_check(cudaLaunchKernelEx(&cfg, kernel, args...), who);
+}
+
 }  // namespace kv4

@@ -31,46 +31,49 @@ struct TableArgs {
     int32_t* positions;
     int32_t* n_free_out;
     int B, page_shift, max_blocks, n_tokens;
+    int vector4;      // slots and positions are 16-byte aligned
 };
 
-// Slot and position of new token t, whose request is the last one that starts
-// at or before it (binary search over q_start).
-__device__ __forceinline__ void map_token(const TableArgs& a, int t, int total) {
-    int slot = -1, pos = 0;
-    if (t < total) {
-        int lo = 0, hi = a.B;   // q_start[lo] <= t < q_start[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.q_start[mid] <= t)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        pos = max(a.cached[lo], 0) + t - a.q_start[lo];
-        const int blk = pos >> a.page_shift;
-        if (blk < a.max_blocks) {
-            const int page = a.table[(int64_t)lo * a.max_blocks + blk];
-            if (page >= 0)
-                slot = (page << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-            else if (page != -1)
-                kv4_set_error(QMOE_EINVAL);
-        }
+// Slot and position of new token t of request b (t in [q_start[b], q_start[b + 1])).
+__device__ __forceinline__ void map_token(const TableArgs& a, int t, int b, int start, int* slot, int* pos) {
+    *pos = max(a.cached[b], 0) + t - start;
+    *slot = -1;
+    const int blk = *pos >> a.page_shift;
+    if (blk < a.max_blocks) {
+        const int page = a.table[(int64_t)b * a.max_blocks + blk];
+        if (page >= 0)
+            *slot = (page << a.page_shift) + (*pos & ((1 << a.page_shift) - 1));
+        else if (page != -1)
+            kv4_set_error(QMOE_EINVAL);
     }
-    a.slots[t] = slot;
-    a.positions[t] = pos;
 }
 
-// One block: prefix sums of the new tokens and new pages over the requests,
-// the new table entries, and (kTokens) the tokens' slots as well.
+// Last i of [0, n) with start[i] <= t (start[0] <= t).
+template <typename T>
+__device__ __forceinline__ int last_start(const T* start, int n, T t) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= t)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// One block: prefix sums of the new tokens and new pages over the requests (1024 at a time), the new table entries (a
+// thread a page, so that the loads from the stack do not wait for one another), and with kTokens the tokens' slots too
+// (few tokens: one launch costs less than two).
 template <bool kTokens>
 __global__ void __launch_bounds__(kPlanThreads) block_tables_kernel(TableArgs a) {
-    __shared__ long long warp_tok[32];
-    __shared__ long long warp_page[32];
+    __shared__ long long warp_tok[32], warp_page[32];
+    __shared__ long long page_at[kPlanThreads];
+    __shared__ int have_s[kPlanThreads];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P1 = (1 << a.page_shift) - 1;
     const int n_free = max(*a.n_free, 0);
-    long long tok0 = 0;
-    long long page0 = 0;
+    long long tok0 = 0, page0 = 0;
     bool bad = false;
     for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
         const int b = b0 + tid;
@@ -84,12 +87,10 @@ __global__ void __launch_bounds__(kPlanThreads) block_tables_kernel(TableArgs a)
         }
         const int have = (int)(((unsigned)c + P1) >> a.page_shift);
         const int need = (int)(((unsigned)(c + n) + P1) >> a.page_shift) - have;
-        long long ts = n;
-        long long ps = need;
+        long long ts = n, ps = need;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const long long to = __shfl_up_sync(QMOE_FULL_MASK, ts, d);
-            const long long po = __shfl_up_sync(QMOE_FULL_MASK, ps, d);
+            const long long to = __shfl_up_sync(QMOE_FULL_MASK, ts, d), po = __shfl_up_sync(QMOE_FULL_MASK, ps, d);
             if (lane >= d) {
                 ts += to;
                 ps += po;
@@ -101,12 +102,10 @@ __global__ void __launch_bounds__(kPlanThreads) block_tables_kernel(TableArgs a)
         }
         __syncthreads();
         if (warp == 0) {
-            long long tw = warp_tok[lane];
-            long long pw = warp_page[lane];
+            long long tw = warp_tok[lane], pw = warp_page[lane];
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const long long to = __shfl_up_sync(QMOE_FULL_MASK, tw, d);
-                const long long po = __shfl_up_sync(QMOE_FULL_MASK, pw, d);
+                const long long to = __shfl_up_sync(QMOE_FULL_MASK, tw, d), po = __shfl_up_sync(QMOE_FULL_MASK, pw, d);
                 if (lane >= d) {
                     tw += to;
                     pw += po;
@@ -117,44 +116,80 @@ __global__ void __launch_bounds__(kPlanThreads) block_tables_kernel(TableArgs a)
         }
         __syncthreads();
         const long long t_end = tok0 + ts + (warp ? warp_tok[warp - 1] : 0);
-        const long long p_first = page0 + ps - need + (warp ? warp_page[warp - 1] : 0);
+        page_at[tid] = ps - need + (warp ? warp_page[warp - 1] : 0);
+        have_s[tid] = have;
         if (b < a.B) {
             a.q_start[b] = (int)min(t_end - n, (long long)a.n_tokens);
             a.kv_len[b] = c + n;
             if (have + need > a.max_blocks) bad = true;
         }
-        // new entries: one request after another, its pages spread over the warp's lanes
-        for (int r = 0; r < 32; ++r) {
-            const int rn = __shfl_sync(QMOE_FULL_MASK, need, r);
-            if (rn == 0) continue;
-            const long long rf = __shfl_sync(QMOE_FULL_MASK, p_first, r);
-            const int rh = __shfl_sync(QMOE_FULL_MASK, have, r);
-            const int64_t row = (int64_t)(b - lane + r) * a.max_blocks;
-            for (int i = lane; i < rn && rh + i < a.max_blocks; i += 32) {
-                const long long at = n_free - 1 - rf - i;
-                a.table[row + rh + i] = at >= 0 ? a.free_pages[at] : -1;
-            }
+        __syncthreads();
+        const long long pages = warp_page[31];
+        for (long long i = tid; i < pages; i += kPlanThreads) {
+            // requests without new pages begin where the next one does: the last of equals is the one that has the page
+            const int r = last_start(page_at, min(kPlanThreads, a.B - b0), i);
+            const long long entry = have_s[r] + i - page_at[r], at = n_free - 1 - page0 - i;
+            if (entry < a.max_blocks) a.table[(int64_t)(b0 + r) * a.max_blocks + entry] = at >= 0 ? a.free_pages[at] : -1;
         }
         tok0 += warp_tok[31];
-        page0 += warp_page[31];
+        page0 += pages;
         __syncthreads();
     }
     if (__syncthreads_or(bad) && tid == 0) kv4_set_error(QMOE_EINVAL);
+    const int total = (int)min(tok0, (long long)a.n_tokens);
     if (tid == 0) {
-        a.q_start[a.B] = (int)min(tok0, (long long)a.n_tokens);
+        a.q_start[a.B] = total;
         *a.n_free_out = (int)max(n_free - page0, 0LL);
         if (page0 > n_free || tok0 > a.n_tokens) kv4_set_error(QMOE_ECAPACITY);
     }
     if (kTokens) {
-        __syncthreads();   // table and q_start of this block are read below
-        const int total = (int)min(tok0, (long long)a.n_tokens);
-        for (int t = tid; t < a.n_tokens; t += kPlanThreads) map_token(a, t, total);
+        __syncthreads();   // the table and q_start, which this block wrote, are read below
+        for (int t = tid; t < a.n_tokens; t += kPlanThreads) {
+            int slot = -1, pos = 0;
+            if (t < total) {
+                const int b = last_start((const int32_t*)a.q_start, a.B, t);
+                map_token(a, t, b, a.q_start[b], &slot, &pos);
+            }
+            a.slots[t] = slot;
+            a.positions[t] = pos;
+        }
     }
 }
 
-__global__ void __launch_bounds__(256) slot_map_kernel(TableArgs a) {
-    const int t = blockIdx.x * 256 + threadIdx.x;
-    if (t < a.n_tokens) map_token(a, t, a.q_start[a.B]);
+// Many tokens: a block maps 1024, four neighbours a thread.  Where they fit, the requests' starts are searched in
+// shared memory (a search in global memory is a chain of about ten cache accesses).
+constexpr int kMapTokens = 1024, kMapStarts = 4096;
+
+__global__ void __launch_bounds__(kMapTokens / 4) slot_map_kernel(TableArgs a) {
+    __shared__ int start_s[kMapStarts];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int total = a.q_start[a.B], t0 = blockIdx.x * kMapTokens + threadIdx.x * 4;
+    const bool in_smem = a.B <= kMapStarts;
+    if (in_smem) {
+        for (int i = threadIdx.x; i < a.B; i += kMapTokens / 4) start_s[i] = a.q_start[i];
+        __syncthreads();
+    }
+    if (t0 >= a.n_tokens) return;
+    const int32_t* start = in_smem ? start_s : a.q_start;
+    int slot[4], pos[4];
+    int b = t0 < total ? last_start(start, a.B, t0) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = t0 + i;
+        slot[i] = -1, pos[i] = 0;
+        if (t < total) {
+            while (b + 1 < a.B && start[b + 1] <= t) ++b;
+            map_token(a, t, b, start[b], &slot[i], &pos[i]);
+        }
+    }
+    if (t0 + 3 < a.n_tokens && a.vector4) {
+        *(int4*)(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        *(int4*)(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (t0 + i < a.n_tokens) a.slots[t0 + i] = slot[i], a.positions[t0 + i] = pos[i];
+    }
 }
 
 // ---------------------------------------------------------------- norm, rotation, cache write
@@ -207,10 +242,14 @@ __device__ __forceinline__ void store_row(const RopeArgs& a, const float (&x)[8]
     const float s = __half2float(sh);
     uint32_t word = 0;
     if (s > 0.f) {
+        // rint of the quotient: the product with 1 / s is within 3e-6 of it, which decides unless it is that near a half
+        const float r = __fdiv_rn(1.f, s);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float u = fminf(fmaxf(rintf(__fdiv_rn(y[i] - z, s)), 0.f), 15.f);
-            word |= (uint32_t)u << (4 * (i >> 1) + 16 * (i & 1));
+            const float d = y[i] - z, q = d * r;
+            float u = rintf(q);
+            if (__builtin_expect(fabsf(fabsf(q - u) - 0.5f) < 1e-5f, 0)) u = rintf(__fdiv_rn(d, s));
+            word |= (uint32_t)fminf(fmaxf(u, 0.f), 15.f) << (4 * (i >> 1) + 16 * (i & 1));
         }
     }
     if (slot < 0) return;
@@ -224,127 +263,174 @@ __device__ __forceinline__ void store_row(const RopeArgs& a, const float (&x)[8]
             (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(zh) << 16);
 }
 
-// A group of L = head_dim / 8 lanes holds one head, 8 values a lane (16-byte loads and stores).
-template <int L>
-__global__ void __launch_bounds__(256) rope_kernel(RopeArgs a) {
-    const int gl = threadIdx.x & (L - 1);
-    const long long n = (long long)a.T * a.heads;
-    const long long first = (long long)blockIdx.x * (256 / L);
-    const long long item = first + threadIdx.x / L;
-    if (first + ((threadIdx.x & ~31) / L) >= n) return;   // the whole warp is past the end
-    const bool live = item < n;
-    const int t = live ? (int)(item / a.heads) : a.T - 1;
-    const int h = live ? (int)(item - (long long)t * a.heads) : 0;
-    const int kind = h < a.n_q ? 0 : h < a.n_q + a.n_kv ? 1 : 2;   // query, key, value
-    const int hh = kind == 0 ? h : h - a.n_q - (kind == 2 ? a.n_kv : 0);
-    const uint16_t* src = kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride;
-    const uint4 raw = *(const uint4*)(src + hh * (L * 8) + gl * 8);
-    float x[8] = {bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y),
-                  bf16_lo(raw.z), bf16_hi(raw.z), bf16_lo(raw.w), bf16_hi(raw.w)};
-    const uint16_t* w = kind == 0 ? a.wq : kind == 1 ? a.wk : nullptr;
-    float ss = 0.f;
+// A group of L = head_dim / 8 lanes holds one head, 8 values a lane (16-byte loads and stores); a warp takes HB heads a
+// group of one token, all loaded before the first is used, with the token's angles in registers.
+template <int L, int HB>
+__global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, unsigned per_token) {
+    constexpr int G = 32 / L;
+    const int lane = threadIdx.x & 31, gl = lane & (L - 1), g = lane / L;
+    const unsigned long long w = (unsigned long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (w >= (unsigned long long)a.T * per_token) return;
+    const int t = w >> 32 ? (int)(w / per_token) : (int)((unsigned)w / per_token);
+    const int h0 = (int)(w - (unsigned long long)t * per_token) * (HB * G) + g;
+    uint4 raw[HB];
+    int slot = a.slots ? a.slots[t] : -1;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
-    ss = group_sum<L>(ss);
-    if (w) {
-        const uint4 wr = *(const uint4*)(w + gl * 8);
-        const float r = 1.f / sqrtf(ss / (L * 8) + a.eps);
-        const float wf[8] = {bf16_lo(wr.x), bf16_hi(wr.x), bf16_lo(wr.y), bf16_hi(wr.y),
-                             bf16_lo(wr.z), bf16_hi(wr.z), bf16_lo(wr.w), bf16_hi(wr.w)};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * wf[i];
+    for (int k = 0; k < HB; ++k) {
+        const int h = h0 + k * G;
+        raw[k] = make_uint4(0, 0, 0, 0);
+        if (h < a.heads) {
+            const uint16_t* src = h < a.n_q ? a.q + t * a.q_stride + h * (L * 8)
+                                  : h < a.n_q + a.n_kv ? a.k + t * a.k_stride + (h - a.n_q) * (L * 8)
+                                                       : a.v + t * a.v_stride + (h - a.n_q - a.n_kv) * (L * 8);
+            raw[k] = *(const uint4*)(src + gl * 8);
+        }
     }
-    if (a.cos_sin) {
-        const int half = a.rot >> 1, hl = half >> 3;     // values, lanes of half a rotation
-        const bool in = gl * 8 < a.rot;
-        const int partner = !in ? gl : gl < hl ? gl + hl : gl - hl;
-        float y[8];
+    // the rotation of this lane's values: angles, the partner's lane and the sign of its part
+    const int half = a.rot >> 1, hl = half >> 3;
+    const bool turns = a.cos_sin && gl * 8 < a.rot;
+    float cs[8], sn[8];
+    if (turns) {
+        int pos = a.positions[t];
+        if (pos < 0 || pos >= a.n_pos) {
+            kv4_set_error(QMOE_EINVAL);
+            pos = pos < 0 ? 0 : a.n_pos - 1;
+        }
+        const float* row = a.cos_sin + (int64_t)pos * a.rot + (a.interleaved ? gl * 4 : (gl < hl ? gl : gl - hl) * 8);
+        *(float4*)cs = *(const float4*)row, *(float4*)sn = *(const float4*)(row + half);
+        if (!a.interleaved) *(float4*)(cs + 4) = *(const float4*)(row + 4), *(float4*)(sn + 4) = *(const float4*)(row + half + 4);
+    }
+    if (slot < -1 || (slot >> a.cache.page_shift) >= a.cache.n_pages) {
+        if (a.slots) kv4_set_error(QMOE_EINVAL);
+        slot = -1;
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(QMOE_FULL_MASK, x[i], partner, L);
-        if (in && kind < 2) {
-            int pos = a.positions[t];
-            if (pos < 0 || pos >= a.n_pos) {
-                kv4_set_error(QMOE_EINVAL);
-                pos = pos < 0 ? 0 : a.n_pos - 1;
+    for (int k = 0; k < HB; ++k) {
+        const int h = h0 + k * G;
+        const int kind = h >= a.heads ? 3 : h < a.n_q ? 0 : h < a.n_q + a.n_kv ? 1 : 2;   // query, key, value, none
+        const int hh = kind == 0 ? h : h - a.n_q - (kind == 2 ? a.n_kv : 0);
+        float x[8] = {bf16_lo(raw[k].x), bf16_hi(raw[k].x), bf16_lo(raw[k].y), bf16_hi(raw[k].y),
+                      bf16_lo(raw[k].z), bf16_hi(raw[k].z), bf16_lo(raw[k].w), bf16_hi(raw[k].w)};
+        if (a.wq || a.wk) {
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+            ss = group_sum<L>(ss);
+            const uint16_t* wt = kind == 0 ? a.wq : kind == 1 ? a.wk : nullptr;
+            if (wt) {
+                const uint4 wr = *(const uint4*)(wt + gl * 8);
+                const float r = 1.f / sqrtf(ss / (L * 8) + a.eps);
+                const float wf[8] = {bf16_lo(wr.x), bf16_hi(wr.x), bf16_lo(wr.y), bf16_hi(wr.y),
+                                     bf16_lo(wr.z), bf16_hi(wr.z), bf16_lo(wr.w), bf16_hi(wr.w)};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = x[i] * r * wf[i];
             }
-            const float* cs = a.cos_sin + (int64_t)pos * a.rot;
+        }
+        if (a.cos_sin) {
             if (a.interleaved) {
+                if (turns && kind < 2) {
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    const float c = cs[gl * 4 + i / 2], s = cs[half + gl * 4 + i / 2], u = x[i], v = x[i + 1];
-                    x[i] = u * c - v * s;
-                    x[i + 1] = v * c + u * s;
+                    for (int i = 0; i < 4; ++i) {
+                        const float u = x[2 * i], v = x[2 * i + 1];
+                        x[2 * i] = u * cs[i] - v * sn[i];
+                        x[2 * i + 1] = v * cs[i] + u * sn[i];
+                    }
                 }
             } else {
-                const float* cp = cs + (gl < hl ? gl : gl - hl) * 8;
+                const int partner = !turns ? gl : gl < hl ? gl + hl : gl - hl;
+                float y[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float c = cp[i], s = cp[half + i];
-                    x[i] = x[i] * c + (gl < hl ? -y[i] : y[i]) * s;
+                for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(QMOE_FULL_MASK, x[i], partner, L);
+                if (turns && kind < 2) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = x[i] * cs[i] + (gl < hl ? -y[i] : y[i]) * sn[i];
                 }
             }
         }
-    }
-    const uint4 o = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-    if (live && kind == 0) *(uint4*)(a.q_out + ((int64_t)t * a.n_q + hh) * (L * 8) + gl * 8) = o;
-    if (live && kind == 1 && a.k_out) *(uint4*)(a.k_out + ((int64_t)t * a.n_kv + hh) * (L * 8) + gl * 8) = o;
-    if (a.slots) {
-        // what the cache holds are the values as k_out holds them (rounded to bf16)
-        const float k8[8] = {bf16_lo(o.x), bf16_hi(o.x), bf16_lo(o.y), bf16_hi(o.y),
-                             bf16_lo(o.z), bf16_hi(o.z), bf16_lo(o.w), bf16_hi(o.w)};
-        int slot = live && kind > 0 ? a.slots[t] : -1;
-        if (slot < -1 || (slot >> a.cache.page_shift) >= a.cache.n_pages) {
-            kv4_set_error(QMOE_EINVAL);
-            slot = -1;
+        const uint4 o = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        if (kind == 0) *(uint4*)(a.q_out + ((int64_t)t * a.n_q + hh) * (L * 8) + gl * 8) = o;
+        if (kind == 1 && a.k_out) *(uint4*)(a.k_out + ((int64_t)t * a.n_kv + hh) * (L * 8) + gl * 8) = o;
+        if (a.slots && __any_sync(QMOE_FULL_MASK, kind == 1 || kind == 2)) {
+            // what the cache holds are the values as k_out holds them (rounded to bf16)
+            const float k8[8] = {bf16_lo(o.x), bf16_hi(o.x), bf16_lo(o.y), bf16_hi(o.y),
+                                 bf16_lo(o.z), bf16_hi(o.z), bf16_lo(o.w), bf16_hi(o.w)};
+            store_row<L>(a, k8, kind == 1 || kind == 2 ? slot : -1, hh, kind == 2, gl);
         }
-        store_row<L>(a, k8, slot, hh, kind == 2, gl);
     }
 }
 
 // ---------------------------------------------------------------- cache reader
-template <int L>
-__global__ void __launch_bounds__(256) gather_kernel(kv4::CacheView c, const int32_t* slots, int n, uint16_t* k_out,
+// As the writer: a group a row (token, side, head), HB rows a group, a word a lane.
+template <int L, int HB>
+__global__ void __launch_bounds__(256) gather_kernel(kv4::CacheView c, const int32_t* slots, int n, unsigned per_token, uint16_t* k_out,
                                                      uint16_t* v_out) {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (long long)n * c.n_kv_heads * 2 * L) return;
-    const int gl = (int)(i & (L - 1));
-    long long r = i / L;
-    const int h = (int)(r % c.n_kv_heads);
-    r /= c.n_kv_heads;
-    const int side = r >= n;
-    const int t = (int)(side ? r - n : r);
+    constexpr int G = 32 / L;
+    const int lane = threadIdx.x & 31, gl = lane & (L - 1), g = lane / L;
+    const unsigned long long w = (unsigned long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (w >= (unsigned long long)n * per_token) return;
+    const int t = w >> 32 ? (int)(w / per_token) : (int)((unsigned)w / per_token);
+    const int r0 = (int)(w - (unsigned long long)t * per_token) * (HB * G) + g;
     int slot = slots[t];
     if (slot < -1 || (slot >> c.page_shift) >= c.n_pages) {
         kv4_set_error(QMOE_EINVAL);
         slot = -1;
     }
-    uint4 o = make_uint4(0, 0, 0, 0);
-    if (slot >= 0) {
-        const int P = 1 << c.page_shift;
-        const unsigned char* hp = kv4::head_ptr(c, slot >> c.page_shift, h);
-        const int row = side * P + (slot & (P - 1));
-        const uint32_t w = ((const uint32_t*)hp)[row * L + gl];
-        const uint32_t sz = ((const uint32_t*)(hp + (size_t)2 * P * L * 4))[row];
-        const float s = f16_to_f32((uint16_t)sz), z = f16_to_f32((uint16_t)(sz >> 16));
+    const int P = 1 << c.page_shift;
+    uint32_t word[HB], sz[HB];
+#pragma unroll
+    for (int k = 0; k < HB; ++k) {
+        const int r = r0 + k * G;
+        word[k] = sz[k] = 0;
+        if (r < 2 * c.n_kv_heads && slot >= 0) {
+            const int side = r >= c.n_kv_heads, h = side ? r - c.n_kv_heads : r;
+            const unsigned char* hp = kv4::head_ptr(c, slot >> c.page_shift, h);
+            const int row = side * P + (slot & (P - 1));
+            word[k] = ((const uint32_t*)hp)[row * L + gl];
+            sz[k] = ((const uint32_t*)(hp + (size_t)2 * P * L * 4))[row];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < HB; ++k) {
+        const int r = r0 + k * G;
+        if (r >= 2 * c.n_kv_heads) break;
+        const int side = r >= c.n_kv_heads, h = side ? r - c.n_kv_heads : r;
+        const float s = f16_to_f32((uint16_t)sz[k]), z = f16_to_f32((uint16_t)(sz[k] >> 16));
         float x[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) x[q] = fmaf(s, (float)((w >> (4 * (q >> 1) + 16 * (q & 1))) & 15u), z);
-        o = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        for (int q = 0; q < 8; ++q) x[q] = fmaf(s, (float)((word[k] >> (4 * (q >> 1) + 16 * (q & 1))) & 15u), z);
+        *(uint4*)((side ? v_out : k_out) + ((int64_t)t * c.n_kv_heads + h) * (L * 8) + gl * 8) =
+            make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
     }
-    *(uint4*)((side ? v_out : k_out) + ((int64_t)t * c.n_kv_heads + h) * (L * 8) + gl * 8) = o;
+}
+
+// Heads a group of lanes takes: four where that still gives every scheduler of the device some eight warps, else one.
+template <int L>
+bool four_heads(long long T, int heads) {
+    return T * ((heads + 4 * (32 / L) - 1) / (4 * (32 / L))) >= (long long)qmoe::sm_count() * 32;
+}
+
+template <int L, int HB>
+int launch_rope_as(const RopeArgs& a, const char* who, cudaStream_t st) {
+    const unsigned per_token = (unsigned)((a.heads + HB * (32 / L) - 1) / (HB * (32 / L)));
+    const long long blocks = ((long long)a.T * per_token + 7) / 8;
+    if (blocks > 0x7FFFFFFFLL) return qmoe::fail(QMOE_EINVAL, std::string(who) + ": too many heads in one call");
+    rope_kernel<L, HB><<<(unsigned)blocks, 256, 0, st>>>(a, per_token);
+    return qmoe::launch_check(who);
 }
 
 int launch_rope(const RopeArgs& a, int head_dim, const char* who, cudaStream_t st) {
-    const long long items = (long long)a.T * a.heads;
-    if (items == 0) return QMOE_OK;
-    const int per = 256 / (head_dim / 8);
-    const long long blocks = (items + per - 1) / per;
-    if (blocks > 0x7FFFFFFFLL) return qmoe::fail(QMOE_EINVAL, std::string(who) + ": too many heads in one call");
-    if (head_dim == 128)
-        rope_kernel<16><<<(unsigned)blocks, 256, 0, st>>>(a);
-    else
-        rope_kernel<8><<<(unsigned)blocks, 256, 0, st>>>(a);
-    return qmoe::launch_check(who);
+    if (a.T == 0 || a.heads == 0) return QMOE_OK;
+    if (head_dim == 128) return four_heads<16>(a.T, a.heads) ? launch_rope_as<16, 4>(a, who, st) : launch_rope_as<16, 1>(a, who, st);
+    return four_heads<8>(a.T, a.heads) ? launch_rope_as<8, 4>(a, who, st) : launch_rope_as<8, 1>(a, who, st);
+}
+
+template <int L, int HB>
+int launch_gather(const kv4::CacheView& c, const int32_t* slots, int n, void* k_out, void* v_out, cudaStream_t st) {
+    const unsigned per_token = (unsigned)((2 * c.n_kv_heads + HB * (32 / L) - 1) / (HB * (32 / L)));
+    const long long blocks = ((long long)n * per_token + 7) / 8;
+    if (blocks > 0x7FFFFFFFLL) return qmoe::fail(QMOE_EINVAL, "kv4_gather: too many rows in one call");
+    gather_kernel<L, HB><<<(unsigned)blocks, 256, 0, st>>>(c, slots, n, per_token, (uint16_t*)k_out, (uint16_t*)v_out);
+    return qmoe::launch_check("kv4_gather");
 }
 
 }  // namespace
@@ -371,11 +457,19 @@ extern "C" int kv4_block_tables(const int32_t* cached, const int32_t* new_tokens
         (n_tokens > 0 && (!slots || !positions)))
         return qmoe::fail(QMOE_EINVAL, "kv4_block_tables: NULL pointer");
     TableArgs a{cached, new_tokens, free_pages, n_free, table, q_start, kv_len, slots, positions, n_free_out,
-                B, page_size == 16 ? 4 : page_size == 32 ? 5 : 6, max_blocks, n_tokens};
+                B, page_size == 16 ? 4 : page_size == 32 ? 5 : 6, max_blocks, n_tokens,
+                kv4::aligned16(slots) && kv4::aligned16(positions)};
     cudaStream_t st = (cudaStream_t)stream;
+    // up to four tokens a thread: one launch
+    if (n_tokens <= 4 * kPlanThreads) {
+        block_tables_kernel<true><<<1, kPlanThreads, 0, st>>>(a);
+        return qmoe::launch_check("kv4_block_tables");
+    }
     block_tables_kernel<false><<<1, kPlanThreads, 0, st>>>(a);
-    if (n_tokens > 0) slot_map_kernel<<<(unsigned)((n_tokens + 255) / 256), 256, 0, st>>>(a);
-    return qmoe::launch_check("kv4_block_tables");
+    const int rc = qmoe::launch_check("kv4_block_tables");
+    if (rc) return rc;
+    return kv4::launch_dependent(slot_map_kernel, dim3((unsigned)((n_tokens + kMapTokens - 1) / kMapTokens)), kMapTokens / 4, 0, st,
+                                 "kv4_block_tables", a);
 }
 
 extern "C" int qk_norm_rope(const void* qkv, int64_t row_stride, int T, int n_q_heads, int n_kv_heads, int head_dim,
@@ -442,12 +536,8 @@ extern "C" int kv4_gather(const kv4_cache* cache, const int32_t* slots, int n, v
     if (n < 0 || (n > 0 && (!slots || !k_out || !v_out))) return qmoe::fail(QMOE_EINVAL, "kv4_gather: negative n or NULL pointer");
     if (!kv4::aligned16(k_out) || !kv4::aligned16(v_out)) return qmoe::fail(QMOE_EINVAL, "kv4_gather: pointer not 16-byte aligned");
     if (n == 0) return QMOE_OK;
-    const long long items = (long long)n * c.n_kv_heads * 2 * (cache->head_dim / 8);
-    const long long blocks = (items + 255) / 256;
-    if (blocks > 0x7FFFFFFFLL) return qmoe::fail(QMOE_EINVAL, "kv4_gather: too many rows in one call");
+    cudaStream_t st = (cudaStream_t)stream;
     if (cache->head_dim == 128)
-        gather_kernel<16><<<(unsigned)blocks, 256, 0, (cudaStream_t)stream>>>(c, slots, n, (uint16_t*)k_out, (uint16_t*)v_out);
-    else
-        gather_kernel<8><<<(unsigned)blocks, 256, 0, (cudaStream_t)stream>>>(c, slots, n, (uint16_t*)k_out, (uint16_t*)v_out);
-    return qmoe::launch_check("kv4_gather");
+        return four_heads<16>(n, 2 * c.n_kv_heads) ? launch_gather<16, 4>(c, slots, n, k_out, v_out, st) : launch_gather<16, 1>(c, slots, n, k_out, v_out, st);
+    return four_heads<8>(n, 2 * c.n_kv_heads) ? launch_gather<8, 4>(c, slots, n, k_out, v_out, st) : launch_gather<8, 1>(c, slots, n, k_out, v_out, st);
 }
