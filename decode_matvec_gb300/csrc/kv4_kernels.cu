@@ -219,22 +219,59 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-// Quantises the row held 8 values a lane by the L lanes of a group and stores
-// its codes (one word a lane) and its (s, z) pair.
-template <int L>
-__device__ __forceinline__ void store_row(const RopeArgs& a, const float (&x)[8], int slot, int head, int side, int gl) {
-    float y[8], lo, hi;
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmin2(*(__nv_bfloat162*)&a, *(__nv_bfloat162*)&b);
+    return *(const uint32_t*)&r;
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmax2(*(__nv_bfloat162*)&a, *(__nv_bfloat162*)&b);
+    return *(const uint32_t*)&r;
+}
+
+// The code word of 8 values y by (s, z): u = clamp(rint((y - z) / s), 0, 15), the quotient rounded as the format defines it.
+__device__ __forceinline__ uint32_t code_word(const float (&y)[8], float s, float z) {
+    uint32_t word = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float t = x[i] == x[i] ? x[i] : 0.f;
-        y[i] = fminf(fmaxf(t, -32768.f), 32768.f);
-        lo = i ? fminf(lo, y[i]) : y[i];
-        hi = i ? fmaxf(hi, y[i]) : y[i];
+        const float u = fminf(fmaxf(rintf(__fdiv_rn(y[i] - z, s)), 0.f), 15.f);
+        word |= (uint32_t)u << (4 * (i >> 1) + 16 * (i & 1));
     }
+    return word;
+}
+
+// Quantises the row held as 8 bf16 values a lane by the L lanes of a group and stores its codes (one word a lane) and its
+// (s, z) pair.  All lanes of the warp take part.
+//
+// Dividing 8 values a lane exactly would cost several times what the row's bytes do, so the quotient is taken as
+// 15 saturate((y - z) (1 / (15 s))), within 1e-5 of it: its rounding is the same unless it lies that near a half, and a row
+// with such a value, or with a NaN or a magnitude of 32768 or more, is done again with divisions.
+template <int L>
+__device__ __forceinline__ void store_row(const RopeArgs& a, uint4 o, int slot, int head, int side, int gl) {
+    const uint32_t w4[4] = {o.x, o.y, o.z, o.w};
+    uint32_t lo2 = min2(min2(o.x, o.y), min2(o.z, o.w)), hi2 = max2(max2(o.x, o.y), max2(o.z, o.w)), big = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) big |= (w4[i] & 0x7FFF7FFFu) + 0x39003900u;      // a half's top bit: magnitude >= 0x4700, 32768
 #pragma unroll
     for (int d = L / 2; d > 0; d >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(QMOE_FULL_MASK, lo, d));
-        hi = fmaxf(hi, __shfl_xor_sync(QMOE_FULL_MASK, hi, d));
+        lo2 = min2(lo2, __shfl_xor_sync(QMOE_FULL_MASK, lo2, d));
+        hi2 = max2(hi2, __shfl_xor_sync(QMOE_FULL_MASK, hi2, d));
+    }
+    float y[8], lo = fminf(bf16_lo(lo2), bf16_hi(lo2)), hi = fmaxf(bf16_lo(hi2), bf16_hi(hi2));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[2 * i] = bf16_lo(w4[i]), y[2 * i + 1] = bf16_hi(w4[i]);
+    const bool odd = __any_sync(QMOE_FULL_MASK, (big & 0x80008000u) != 0);
+    if (__builtin_expect(odd, 0)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            y[i] = fminf(fmaxf(y[i] == y[i] ? y[i] : 0.f, -32768.f), 32768.f);
+            lo = i ? fminf(lo, y[i]) : y[i];
+            hi = i ? fmaxf(hi, y[i]) : y[i];
+        }
+#pragma unroll
+        for (int d = L / 2; d > 0; d >>= 1) {
+            lo = fminf(lo, __shfl_xor_sync(QMOE_FULL_MASK, lo, d));
+            hi = fmaxf(hi, __shfl_xor_sync(QMOE_FULL_MASK, hi, d));
+        }
     }
     const __half zh = __float2half_rn(lo);
     const float z = __half2float(zh);
@@ -242,21 +279,22 @@ __device__ __forceinline__ void store_row(const RopeArgs& a, const float (&x)[8]
     const float s = __half2float(sh);
     uint32_t word = 0;
     if (s > 0.f) {
-        // rint of the quotient: the product with 1 / s is within 3e-6 of it, which decides unless it is that near a half
-        const float r = __fdiv_rn(1.f, s);
+        constexpr float kMagic = 12582912.f;       // 1.5 * 2^23: adding it leaves the nearest integer in the low bits
+        constexpr uint32_t kBits = 0x4B400000u;
+        const float r = __fdividef(1.f / 15.f, s);
+        float worst = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float d = y[i] - z, q = d * r;
-            float u = rintf(q);
-            if (__builtin_expect(fabsf(fabsf(q - u) - 0.5f) < 1e-5f, 0)) u = rintf(__fdiv_rn(d, s));
-            word |= (uint32_t)fminf(fmaxf(u, 0.f), 15.f) << (4 * (i >> 1) + 16 * (i & 1));
+            const float q = __saturatef((y[i] - z) * r), v = fmaf(q, 15.f, kMagic);
+            worst = fmaxf(worst, fabsf(fmaf(q, 15.f, kMagic - v)));
+            word += (__float_as_uint(v) - kBits) << (4 * (i >> 1) + 16 * (i & 1));
         }
+        if (__builtin_expect(worst > 0.49999f || odd, 0)) word = code_word(y, s, z);
     }
     if (slot < 0) return;
     const int P = 1 << a.cache.page_shift;
     unsigned char* hp = kv4::head_ptr(a.cache, slot >> a.cache.page_shift, head);
-    const int in_page = slot & (P - 1);
-    const int row = side * P + in_page;
+    const int row = side * P + (slot & (P - 1));
     ((uint32_t*)hp)[row * L + gl] = word;
     if (gl == 0)
         ((uint32_t*)(hp + (size_t)2 * P * L * 4))[row] =
@@ -266,7 +304,7 @@ __device__ __forceinline__ void store_row(const RopeArgs& a, const float (&x)[8]
 // A group of L = head_dim / 8 lanes holds one head, 8 values a lane (16-byte loads and stores); a warp takes HB heads a
 // group of one token, all loaded before the first is used, with the token's angles in registers.
 template <int L, int HB>
-__global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, unsigned per_token) {
+__global__ void __launch_bounds__(256, 4) rope_kernel(RopeArgs a, unsigned per_token) {
     constexpr int G = 32 / L;
     const int lane = threadIdx.x & 31, gl = lane & (L - 1), g = lane / L;
     const unsigned long long w = (unsigned long long)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -286,9 +324,10 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, unsigned per_toke
             raw[k] = *(const uint4*)(src + gl * 8);
         }
     }
-    // the rotation of this lane's values: angles, the partner's lane and the sign of its part
+    // the rotation of this lane's values: angles (the sines with the sign of the partner's part), the partner's lane
     const int half = a.rot >> 1, hl = half >> 3;
     const bool turns = a.cos_sin && gl * 8 < a.rot;
+    const int partner = !turns ? gl : gl < hl ? gl + hl : gl - hl;
     float cs[8], sn[8];
     if (turns) {
         int pos = a.positions[t];
@@ -298,8 +337,15 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, unsigned per_toke
         }
         const float* row = a.cos_sin + (int64_t)pos * a.rot + (a.interleaved ? gl * 4 : (gl < hl ? gl : gl - hl) * 8);
         *(float4*)cs = *(const float4*)row, *(float4*)sn = *(const float4*)(row + half);
-        if (!a.interleaved) *(float4*)(cs + 4) = *(const float4*)(row + 4), *(float4*)(sn + 4) = *(const float4*)(row + half + 4);
+        if (!a.interleaved) {
+            *(float4*)(cs + 4) = *(const float4*)(row + 4), *(float4*)(sn + 4) = *(const float4*)(row + half + 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sn[i] = gl < hl ? -sn[i] : sn[i];
+        }
     }
+    uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
+    if (a.wq) wq = *(const uint4*)(a.wq + gl * 8);
+    if (a.wk) wk = *(const uint4*)(a.wk + gl * 8);
     if (slot < -1 || (slot >> a.cache.page_shift) >= a.cache.n_pages) {
         if (a.slots) kv4_set_error(QMOE_EINVAL);
         slot = -1;
@@ -316,12 +362,11 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, unsigned per_toke
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
             ss = group_sum<L>(ss);
-            const uint16_t* wt = kind == 0 ? a.wq : kind == 1 ? a.wk : nullptr;
-            if (wt) {
-                const uint4 wr = *(const uint4*)(wt + gl * 8);
-                const float r = 1.f / sqrtf(ss / (L * 8) + a.eps);
-                const float wf[8] = {bf16_lo(wr.x), bf16_hi(wr.x), bf16_lo(wr.y), bf16_hi(wr.y),
-                                     bf16_lo(wr.z), bf16_hi(wr.z), bf16_lo(wr.w), bf16_hi(wr.w)};
+            if ((kind == 0 && a.wq) || (kind == 1 && a.wk)) {
+                const uint4 w4 = kind == 0 ? wq : wk;
+                const float r = rsqrtf(ss * (1.f / (L * 8)) + a.eps);      // 2 ulp of fp32, before a rounding to 8 bits
+                const float wf[8] = {bf16_lo(w4.x), bf16_hi(w4.x), bf16_lo(w4.y), bf16_hi(w4.y),
+                                     bf16_lo(w4.z), bf16_hi(w4.z), bf16_lo(w4.w), bf16_hi(w4.w)};
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = x[i] * r * wf[i];
             }
@@ -337,13 +382,12 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, unsigned per_toke
                     }
                 }
             } else {
-                const int partner = !turns ? gl : gl < hl ? gl + hl : gl - hl;
                 float y[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(QMOE_FULL_MASK, x[i], partner, L);
                 if (turns && kind < 2) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = x[i] * cs[i] + (gl < hl ? -y[i] : y[i]) * sn[i];
+                    for (int i = 0; i < 8; ++i) x[i] = fmaf(y[i], sn[i], x[i] * cs[i]);
                 }
             }
         }
@@ -352,9 +396,7 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, unsigned per_toke
         if (kind == 1 && a.k_out) *(uint4*)(a.k_out + ((int64_t)t * a.n_kv + hh) * (L * 8) + gl * 8) = o;
         if (a.slots && __any_sync(QMOE_FULL_MASK, kind == 1 || kind == 2)) {
             // what the cache holds are the values as k_out holds them (rounded to bf16)
-            const float k8[8] = {bf16_lo(o.x), bf16_hi(o.x), bf16_lo(o.y), bf16_hi(o.y),
-                                 bf16_lo(o.z), bf16_hi(o.z), bf16_lo(o.w), bf16_hi(o.w)};
-            store_row<L>(a, k8, kind == 1 || kind == 2 ? slot : -1, hh, kind == 2, gl);
+            store_row<L>(a, o, kind == 1 || kind == 2 ? slot : -1, hh, kind == 2, gl);
         }
     }
 }
