@@ -275,7 +275,11 @@ __device__ __forceinline__ void store_row(const RopeArgs& a, uint4 o, int slot, 
     }
     const __half zh = __float2half_rn(lo);
     const float z = __half2float(zh);
-    const __half sh = __float2half_rn(__fdiv_rn(hi - z, 15.f));
+    // fp16 of (hi - z) / 15: the product with 1 / 15 is within 2 units of the quotient's last place, which decides unless
+    // that is next to the middle of two fp16 values (or fp16 has no 11 bits there)
+    float d15 = (hi - z) * (1.f / 15.f);
+    if (__builtin_expect(((__float_as_uint(d15) + 2u) & 0x1FFFu) - 0x1000u <= 4u || d15 < 6.2e-5f, 0)) d15 = __fdiv_rn(hi - z, 15.f);
+    const __half sh = __float2half_rn(d15);
     const float s = __half2float(sh);
     uint32_t word = 0;
     if (s > 0.f) {
@@ -301,79 +305,82 @@ __device__ __forceinline__ void store_row(const RopeArgs& a, uint4 o, int slot, 
             (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(zh) << 16);
 }
 
-// A group of L = head_dim / 8 lanes holds one head, 8 values a lane (16-byte loads and stores); a warp takes HB heads a
-// group of one token, all loaded before the first is used, with the token's angles in registers.
-template <int L, int HB>
-__global__ void __launch_bounds__(256, 4) rope_kernel(RopeArgs a, unsigned per_token) {
+// A group of L = head_dim / 8 lanes holds one head, 8 values a lane (16-byte loads and stores); a warp takes `rounds`
+// heads a group of one token, one after another (a loop, not unrolled: its code has to stay in the instruction caches),
+// with the next head's load ahead of the present one's work and the token's angles in registers.
+// kTurn: norm and rotation; kCache: keys and values go to the cache.
+template <int L, bool kTurn, bool kCache>
+__global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, unsigned per_token, int rounds) {
     constexpr int G = 32 / L;
     const int lane = threadIdx.x & 31, gl = lane & (L - 1), g = lane / L;
     const unsigned long long w = (unsigned long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (w >= (unsigned long long)a.T * per_token) return;
     const int t = w >> 32 ? (int)(w / per_token) : (int)((unsigned)w / per_token);
-    const int h0 = (int)(w - (unsigned long long)t * per_token) * (HB * G) + g;
-    uint4 raw[HB];
-    int slot = a.slots ? a.slots[t] : -1;
-#pragma unroll
-    for (int k = 0; k < HB; ++k) {
-        const int h = h0 + k * G;
-        raw[k] = make_uint4(0, 0, 0, 0);
-        if (h < a.heads) {
-            const uint16_t* src = h < a.n_q ? a.q + t * a.q_stride + h * (L * 8)
-                                  : h < a.n_q + a.n_kv ? a.k + t * a.k_stride + (h - a.n_q) * (L * 8)
-                                                       : a.v + t * a.v_stride + (h - a.n_q - a.n_kv) * (L * 8);
-            raw[k] = *(const uint4*)(src + gl * 8);
+    int h = (int)(w - (unsigned long long)t * per_token) * (rounds * G) + g;
+    const int n_qk = a.n_q + a.n_kv;
+    auto load = [&](int head) {
+        if (head >= a.heads) return make_uint4(0, 0, 0, 0);
+        const uint16_t* src = head < a.n_q ? a.q + t * a.q_stride + head * (L * 8)
+                              : head < n_qk ? a.k + t * a.k_stride + (head - a.n_q) * (L * 8)
+                                            : a.v + t * a.v_stride + (head - n_qk) * (L * 8);
+        return *(const uint4*)(src + gl * 8);
+    };
+    uint4 next = load(h);
+    int slot = -1;
+    if (kCache) {
+        slot = a.slots[t];
+        if (slot < -1 || (slot >> a.cache.page_shift) >= a.cache.n_pages) {
+            kv4_set_error(QMOE_EINVAL);
+            slot = -1;
         }
     }
     // the rotation of this lane's values: angles (the sines with the sign of the partner's part), the partner's lane
     const int half = a.rot >> 1, hl = half >> 3;
-    const bool turns = a.cos_sin && gl * 8 < a.rot;
+    const bool turns = kTurn && a.cos_sin && gl * 8 < a.rot;
     const int partner = !turns ? gl : gl < hl ? gl + hl : gl - hl;
     float cs[8], sn[8];
-    if (turns) {
-        int pos = a.positions[t];
-        if (pos < 0 || pos >= a.n_pos) {
-            kv4_set_error(QMOE_EINVAL);
-            pos = pos < 0 ? 0 : a.n_pos - 1;
-        }
-        const float* row = a.cos_sin + (int64_t)pos * a.rot + (a.interleaved ? gl * 4 : (gl < hl ? gl : gl - hl) * 8);
-        *(float4*)cs = *(const float4*)row, *(float4*)sn = *(const float4*)(row + half);
-        if (!a.interleaved) {
-            *(float4*)(cs + 4) = *(const float4*)(row + 4), *(float4*)(sn + 4) = *(const float4*)(row + half + 4);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sn[i] = gl < hl ? -sn[i] : sn[i];
-        }
-    }
     uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-    if (a.wq) wq = *(const uint4*)(a.wq + gl * 8);
-    if (a.wk) wk = *(const uint4*)(a.wk + gl * 8);
-    if (slot < -1 || (slot >> a.cache.page_shift) >= a.cache.n_pages) {
-        if (a.slots) kv4_set_error(QMOE_EINVAL);
-        slot = -1;
-    }
+    if (kTurn) {
+        if (turns) {
+            int pos = a.positions[t];
+            if (pos < 0 || pos >= a.n_pos) {
+                kv4_set_error(QMOE_EINVAL);
+                pos = pos < 0 ? 0 : a.n_pos - 1;
+            }
+            const float* row = a.cos_sin + (int64_t)pos * a.rot + (a.interleaved ? gl * 4 : (gl < hl ? gl : gl - hl) * 8);
+            *(float4*)cs = *(const float4*)row, *(float4*)sn = *(const float4*)(row + half);
+            if (!a.interleaved) {
+                *(float4*)(cs + 4) = *(const float4*)(row + 4), *(float4*)(sn + 4) = *(const float4*)(row + half + 4);
 #pragma unroll
-    for (int k = 0; k < HB; ++k) {
-        const int h = h0 + k * G;
-        const int kind = h >= a.heads ? 3 : h < a.n_q ? 0 : h < a.n_q + a.n_kv ? 1 : 2;   // query, key, value, none
-        const int hh = kind == 0 ? h : h - a.n_q - (kind == 2 ? a.n_kv : 0);
-        float x[8] = {bf16_lo(raw[k].x), bf16_hi(raw[k].x), bf16_lo(raw[k].y), bf16_hi(raw[k].y),
-                      bf16_lo(raw[k].z), bf16_hi(raw[k].z), bf16_lo(raw[k].w), bf16_hi(raw[k].w)};
-        if (a.wq || a.wk) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
-            ss = group_sum<L>(ss);
-            if ((kind == 0 && a.wq) || (kind == 1 && a.wk)) {
-                const uint4 w4 = kind == 0 ? wq : wk;
-                const float r = rsqrtf(ss * (1.f / (L * 8)) + a.eps);      // 2 ulp of fp32, before a rounding to 8 bits
-                const float wf[8] = {bf16_lo(w4.x), bf16_hi(w4.x), bf16_lo(w4.y), bf16_hi(w4.y),
-                                     bf16_lo(w4.z), bf16_hi(w4.z), bf16_lo(w4.w), bf16_hi(w4.w)};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = x[i] * r * wf[i];
+                for (int i = 0; i < 8; ++i) sn[i] = gl < hl ? -sn[i] : sn[i];
             }
         }
-        if (a.cos_sin) {
-            if (a.interleaved) {
-                if (turns && kind < 2) {
+        if (a.wq) wq = *(const uint4*)(a.wq + gl * 8);
+        if (a.wk) wk = *(const uint4*)(a.wk + gl * 8);
+    }
+#pragma unroll 1
+    for (int k = 0; k < rounds; ++k, h += G) {
+        uint4 o = next;
+        if (k + 1 < rounds) next = load(h + G);
+        const int kind = h >= a.heads ? 3 : h < a.n_q ? 0 : h < n_qk ? 1 : 2;   // query, key, value, none
+        if (kTurn && __any_sync(QMOE_FULL_MASK, kind < 2)) {
+            float x[8] = {bf16_lo(o.x), bf16_hi(o.x), bf16_lo(o.y), bf16_hi(o.y), bf16_lo(o.z), bf16_hi(o.z), bf16_lo(o.w), bf16_hi(o.w)};
+            if (a.wq || a.wk) {
+                float ss = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+                ss = group_sum<L>(ss);
+                if ((kind == 0 && a.wq) || (kind == 1 && a.wk)) {
+                    const uint4 w4 = kind == 0 ? wq : wk;
+                    const float r = rsqrtf(ss * (1.f / (L * 8)) + a.eps);      // 2 ulp of fp32, before a rounding to 8 bits
+                    const float wf[8] = {bf16_lo(w4.x), bf16_hi(w4.x), bf16_lo(w4.y), bf16_hi(w4.y),
+                                         bf16_lo(w4.z), bf16_hi(w4.z), bf16_lo(w4.w), bf16_hi(w4.w)};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * wf[i];
+                }
+            }
+            if (a.cos_sin && a.interleaved) {
+                if (turns) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float u = x[2 * i], v = x[2 * i + 1];
@@ -381,23 +388,24 @@ __global__ void __launch_bounds__(256, 4) rope_kernel(RopeArgs a, unsigned per_t
                         x[2 * i + 1] = v * cs[i] + u * sn[i];
                     }
                 }
-            } else {
+            } else if (a.cos_sin) {
                 float y[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(QMOE_FULL_MASK, x[i], partner, L);
-                if (turns && kind < 2) {
+                if (turns) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[i] = fmaf(y[i], sn[i], x[i] * cs[i]);
                 }
             }
+            if (kind < 2) {
+                o = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+                uint16_t* out = kind == 0 ? a.q_out + ((int64_t)t * a.n_q + h) * (L * 8) : a.k_out + ((int64_t)t * a.n_kv + h - a.n_q) * (L * 8);
+                if (kind == 0 || a.k_out) *(uint4*)(out + gl * 8) = o;
+            }
         }
-        const uint4 o = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-        if (kind == 0) *(uint4*)(a.q_out + ((int64_t)t * a.n_q + hh) * (L * 8) + gl * 8) = o;
-        if (kind == 1 && a.k_out) *(uint4*)(a.k_out + ((int64_t)t * a.n_kv + hh) * (L * 8) + gl * 8) = o;
-        if (a.slots && __any_sync(QMOE_FULL_MASK, kind == 1 || kind == 2)) {
-            // what the cache holds are the values as k_out holds them (rounded to bf16)
-            store_row<L>(a, o, kind == 1 || kind == 2 ? slot : -1, hh, kind == 2, gl);
-        }
+        // what the cache holds are the values as k_out holds them (rounded to bf16)
+        if (kCache && __any_sync(QMOE_FULL_MASK, kind == 1 || kind == 2))
+            store_row<L>(a, o, kind == 1 || kind == 2 ? slot : -1, kind == 2 ? h - n_qk : h - a.n_q, kind == 2, gl);
     }
 }
 
@@ -451,19 +459,21 @@ bool four_heads(long long T, int heads) {
     return T * ((heads + 4 * (32 / L) - 1) / (4 * (32 / L))) >= (long long)qmoe::sm_count() * 32;
 }
 
-template <int L, int HB>
-int launch_rope_as(const RopeArgs& a, const char* who, cudaStream_t st) {
-    const unsigned per_token = (unsigned)((a.heads + HB * (32 / L) - 1) / (HB * (32 / L)));
+// turn: norm and rotation (false: the rows as they are, for the cache alone).
+template <int L>
+int launch_rope(const RopeArgs& a, bool turn, const char* who, cudaStream_t st) {
+    if (a.T == 0 || a.heads == 0) return QMOE_OK;
+    const int rounds = four_heads<L>(a.T, a.heads) ? 4 : 1;
+    const unsigned per_token = (unsigned)((a.heads + rounds * (32 / L) - 1) / (rounds * (32 / L)));
     const long long blocks = ((long long)a.T * per_token + 7) / 8;
     if (blocks > 0x7FFFFFFFLL) return qmoe::fail(QMOE_EINVAL, std::string(who) + ": too many heads in one call");
-    rope_kernel<L, HB><<<(unsigned)blocks, 256, 0, st>>>(a, per_token);
+    if (!turn)
+        rope_kernel<L, false, true><<<(unsigned)blocks, 256, 0, st>>>(a, per_token, rounds);
+    else if (a.slots)
+        rope_kernel<L, true, true><<<(unsigned)blocks, 256, 0, st>>>(a, per_token, rounds);
+    else
+        rope_kernel<L, true, false><<<(unsigned)blocks, 256, 0, st>>>(a, per_token, rounds);
     return qmoe::launch_check(who);
-}
-
-int launch_rope(const RopeArgs& a, int head_dim, const char* who, cudaStream_t st) {
-    if (a.T == 0 || a.heads == 0) return QMOE_OK;
-    if (head_dim == 128) return four_heads<16>(a.T, a.heads) ? launch_rope_as<16, 4>(a, who, st) : launch_rope_as<16, 1>(a, who, st);
-    return four_heads<8>(a.T, a.heads) ? launch_rope_as<8, 4>(a, who, st) : launch_rope_as<8, 1>(a, who, st);
 }
 
 template <int L, int HB>
@@ -551,7 +561,7 @@ extern "C" int qk_norm_rope(const void* qkv, int64_t row_stride, int T, int n_q_
     a.cos_sin = cos_sin, a.rot = rot_dim, a.interleaved = interleaved ? 1 : 0, a.n_pos = n_pos, a.positions = positions;
     a.q_out = (uint16_t*)q_out, a.k_out = (uint16_t*)k_out, a.slots = cache ? slots : nullptr;
     if (!cache && !k_out) a.heads = n_q_heads;
-    return launch_rope(a, head_dim, "qk_norm_rope", (cudaStream_t)stream);
+    return head_dim == 128 ? launch_rope<16>(a, true, "qk_norm_rope", (cudaStream_t)stream) : launch_rope<8>(a, true, "qk_norm_rope", (cudaStream_t)stream);
 }
 
 extern "C" int kv4_append(const kv4_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride, int T,
@@ -567,7 +577,7 @@ extern "C" int kv4_append(const kv4_cache* cache, const void* k, int64_t k_strid
         return qmoe::fail(QMOE_EINVAL, "kv4_append: strides must be multiples of 8 that cover a token, pointers 16-byte aligned");
     a.k = (const uint16_t*)k, a.v = (const uint16_t*)v, a.k_stride = k_stride, a.v_stride = v_stride;
     a.T = T, a.n_kv = cache->n_kv_heads, a.heads = 2 * cache->n_kv_heads, a.slots = slots;
-    return launch_rope(a, cache->head_dim, "kv4_append", (cudaStream_t)stream);
+    return cache->head_dim == 128 ? launch_rope<16>(a, false, "kv4_append", (cudaStream_t)stream) : launch_rope<8>(a, false, "kv4_append", (cudaStream_t)stream);
 }
 
 extern "C" int kv4_gather(const kv4_cache* cache, const int32_t* slots, int n, void* k_out, void* v_out, void* stream) {
