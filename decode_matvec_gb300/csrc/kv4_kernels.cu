@@ -197,6 +197,7 @@ struct RopeArgs {
     const uint16_t *q, *k, *v;            // heads of one token contiguous
     int64_t q_stride, k_stride, v_stride;  // elements from token to token
     int T, n_q, n_kv, heads;               // heads: how many of a token's (q, k, v) heads are visited
+    int q_blocks, kv_blocks;               // a warp's blocks of heads of one kind
     const uint16_t *wq, *wk;               // norm weights or NULL
     float eps;
     const float* cos_sin;                  // NULL: no rotation
@@ -305,107 +306,106 @@ __device__ __forceinline__ void store_row(const RopeArgs& a, uint4 o, int slot, 
             (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(zh) << 16);
 }
 
-// A group of L = head_dim / 8 lanes holds one head, 8 values a lane (16-byte loads and stores); a warp takes `rounds`
-// heads a group of one token, one after another (a loop, not unrolled: its code has to stay in the instruction caches),
-// with the next head's load ahead of the present one's work and the token's angles in registers.
+// A group of L = head_dim / 8 lanes holds one head, 8 values a lane (16-byte loads and stores); a warp takes up to
+// `rounds` heads a group of one token and one kind (queries, keys or values), one after another (a loop, not unrolled:
+// its code has to stay in the instruction caches), with the next head's load ahead of the present one's work.
+//
+// Norm and rotation are one linear map of the head, r (x_i w_i c_i + x_j w_j s_i) with j the value that i is paired with
+// and r = 1 / sqrt(mean(x^2) + eps): w c and w s are made once a token, and the pair's values come from the partner's
+// lane (or the same word, when pairs are neighbours) as they were loaded.
 // kTurn: norm and rotation; kCache: keys and values go to the cache.
 template <int L, bool kTurn, bool kCache>
 __global__ void __launch_bounds__(256) rope_kernel(RopeArgs a, unsigned per_token, int rounds) {
-    constexpr int G = 32 / L;
+    constexpr int G = 32 / L, D = L * 8;
     const int lane = threadIdx.x & 31, gl = lane & (L - 1), g = lane / L;
     const unsigned long long w = (unsigned long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     if (w >= (unsigned long long)a.T * per_token) return;
     const int t = w >> 32 ? (int)(w / per_token) : (int)((unsigned)w / per_token);
-    int h = (int)(w - (unsigned long long)t * per_token) * (rounds * G) + g;
-    const int n_qk = a.n_q + a.n_kv;
-    auto load = [&](int head) {
-        if (head >= a.heads) return make_uint4(0, 0, 0, 0);
-        const uint16_t* src = head < a.n_q ? a.q + t * a.q_stride + head * (L * 8)
-                              : head < n_qk ? a.k + t * a.k_stride + (head - a.n_q) * (L * 8)
-                                            : a.v + t * a.v_stride + (head - n_qk) * (L * 8);
-        return *(const uint4*)(src + gl * 8);
-    };
-    uint4 next = load(h);
+    int block = (int)(w - (unsigned long long)t * per_token), kind = 0;      // queries, keys, values in turn
+    if (block >= a.q_blocks) {
+        kind = block - a.q_blocks >= a.kv_blocks ? 2 : 1;
+        block -= a.q_blocks + (kind == 2 ? a.kv_blocks : 0);
+    }
+    const int n = kind == 0 ? a.n_q : a.n_kv;
+    int h = block * (rounds * G) + g;
+    const uint16_t* src = (kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride) + h * D + gl * 8;
+    uint4 next = h < n ? *(const uint4*)src : make_uint4(0, 0, 0, 0);
+    uint16_t* dst = !kTurn || kind == 2 ? nullptr : kind == 0 ? a.q_out : a.k_out;
+    if (dst) dst += ((int64_t)t * n + h) * D + gl * 8;
     int slot = -1;
-    if (kCache) {
+    if (kCache && kind > 0) {
         slot = a.slots[t];
         if (slot < -1 || (slot >> a.cache.page_shift) >= a.cache.n_pages) {
             kv4_set_error(QMOE_EINVAL);
             slot = -1;
         }
     }
-    // the rotation of this lane's values: angles (the sines with the sign of the partner's part), the partner's lane
-    const int half = a.rot >> 1, hl = half >> 3;
-    const bool turns = kTurn && a.cos_sin && gl * 8 < a.rot;
-    const int partner = !turns ? gl : gl < hl ? gl + hl : gl - hl;
-    float cs[8], sn[8];
-    uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
+    const uint16_t* wt = kind == 0 ? a.wq : kind == 1 ? a.wk : nullptr;
+    const int hl = a.rot >> 4;                                   // lanes of half a rotation
+    const bool turns = kTurn && gl * 8 < a.rot && kind < 2;
+    const int partner = !turns || a.interleaved ? gl : gl < hl ? gl + hl : gl - hl;
+    float wc[8], ws[8];
     if (kTurn) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wc[i] = 1.f, ws[i] = 0.f;
         if (turns) {
             int pos = a.positions[t];
             if (pos < 0 || pos >= a.n_pos) {
                 kv4_set_error(QMOE_EINVAL);
                 pos = pos < 0 ? 0 : a.n_pos - 1;
             }
-            const float* row = a.cos_sin + (int64_t)pos * a.rot + (a.interleaved ? gl * 4 : (gl < hl ? gl : gl - hl) * 8);
-            *(float4*)cs = *(const float4*)row, *(float4*)sn = *(const float4*)(row + half);
-            if (!a.interleaved) {
-                *(float4*)(cs + 4) = *(const float4*)(row + 4), *(float4*)(sn + 4) = *(const float4*)(row + half + 4);
+            const float* row = a.cos_sin + (int64_t)pos * a.rot;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sn[i] = gl < hl ? -sn[i] : sn[i];
+            for (int i = 0; i < 8; ++i) {
+                const int at = a.interleaved ? gl * 4 + i / 2 : (gl < hl ? gl : gl - hl) * 8 + i;
+                const float s = row[(a.rot >> 1) + at];
+                wc[i] = row[at];
+                ws[i] = (a.interleaved ? (i & 1) == 0 : gl < hl) ? -s : s;
             }
         }
-        if (a.wq) wq = *(const uint4*)(a.wq + gl * 8);
-        if (a.wk) wk = *(const uint4*)(a.wk + gl * 8);
+        if (wt) {
+            const uint4 w4 = *(const uint4*)(wt + gl * 8), p4 = *(const uint4*)(wt + partner * 8);
+            const uint32_t wo[4] = {w4.x, w4.y, w4.z, w4.w}, wp[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                wc[2 * i] *= bf16_lo(wo[i]), wc[2 * i + 1] *= bf16_hi(wo[i]);
+                ws[2 * i] *= a.interleaved ? bf16_hi(wp[i]) : bf16_lo(wp[i]), ws[2 * i + 1] *= a.interleaved ? bf16_lo(wp[i]) : bf16_hi(wp[i]);
+            }
+        }
     }
 #pragma unroll 1
-    for (int k = 0; k < rounds; ++k, h += G) {
+    for (int k = 0; k < rounds; ++k) {
         uint4 o = next;
-        if (k + 1 < rounds) next = load(h + G);
-        const int kind = h >= a.heads ? 3 : h < a.n_q ? 0 : h < n_qk ? 1 : 2;   // query, key, value, none
-        if (kTurn && __any_sync(QMOE_FULL_MASK, kind < 2)) {
-            float x[8] = {bf16_lo(o.x), bf16_hi(o.x), bf16_lo(o.y), bf16_hi(o.y), bf16_lo(o.z), bf16_hi(o.z), bf16_lo(o.w), bf16_hi(o.w)};
-            if (a.wq || a.wk) {
+        const int at = h;
+        h += G, src += G * D;
+        if (k + 1 < rounds && h < n) next = *(const uint4*)src;
+        if (kTurn && kind < 2) {
+            uint32_t xw[4] = {o.x, o.y, o.z, o.w}, yw[4];
+            float r = 1.f;
+            if (wt) {
                 float ss = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+                for (int i = 0; i < 4; ++i) ss = fmaf(bf16_lo(xw[i]), bf16_lo(xw[i]), fmaf(bf16_hi(xw[i]), bf16_hi(xw[i]), ss));
                 ss = group_sum<L>(ss);
-                if ((kind == 0 && a.wq) || (kind == 1 && a.wk)) {
-                    const uint4 w4 = kind == 0 ? wq : wk;
-                    const float r = rsqrtf(ss * (1.f / (L * 8)) + a.eps);      // 2 ulp of fp32, before a rounding to 8 bits
-                    const float wf[8] = {bf16_lo(w4.x), bf16_hi(w4.x), bf16_lo(w4.y), bf16_hi(w4.y),
-                                         bf16_lo(w4.z), bf16_hi(w4.z), bf16_lo(w4.w), bf16_hi(w4.w)};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * wf[i];
-                }
+                r = rsqrtf(ss * (1.f / D) + a.eps);      // 2 ulp of fp32, before a rounding to 8 bits
             }
-            if (a.cos_sin && a.interleaved) {
-                if (turns) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float u = x[2 * i], v = x[2 * i + 1];
-                        x[2 * i] = u * cs[i] - v * sn[i];
-                        x[2 * i + 1] = v * cs[i] + u * sn[i];
-                    }
-                }
-            } else if (a.cos_sin) {
-                float y[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(QMOE_FULL_MASK, x[i], partner, L);
-                if (turns) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = fmaf(y[i], sn[i], x[i] * cs[i]);
-                }
+            for (int i = 0; i < 4; ++i) {
+                yw[i] = a.interleaved ? __byte_perm(xw[i], 0, 0x1032) : __shfl_sync(QMOE_FULL_MASK, xw[i], partner, L);
+                if (!turns) yw[i] = 0;
             }
-            if (kind < 2) {
-                o = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-                uint16_t* out = kind == 0 ? a.q_out + ((int64_t)t * a.n_q + h) * (L * 8) : a.k_out + ((int64_t)t * a.n_kv + h - a.n_q) * (L * 8);
-                if (kind == 0 || a.k_out) *(uint4*)(out + gl * 8) = o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                xw[i] = pack_bf16(fmaf(bf16_lo(yw[i]), ws[2 * i], bf16_lo(xw[i]) * wc[2 * i]) * r,
+                                  fmaf(bf16_hi(yw[i]), ws[2 * i + 1], bf16_hi(xw[i]) * wc[2 * i + 1]) * r);
+            o = make_uint4(xw[0], xw[1], xw[2], xw[3]);
+            if (dst) {
+                if (at < n) *(uint4*)dst = o;
+                dst += G * D;
             }
         }
         // what the cache holds are the values as k_out holds them (rounded to bf16)
-        if (kCache && __any_sync(QMOE_FULL_MASK, kind == 1 || kind == 2))
-            store_row<L>(a, o, kind == 1 || kind == 2 ? slot : -1, kind == 2 ? h - n_qk : h - a.n_q, kind == 2, gl);
+        if (kCache && kind > 0) store_row<L>(a, o, at < n ? slot : -1, at, kind == 2, gl);
     }
 }
 
@@ -461,10 +461,12 @@ bool four_heads(long long T, int heads) {
 
 // turn: norm and rotation (false: the rows as they are, for the cache alone).
 template <int L>
-int launch_rope(const RopeArgs& a, bool turn, const char* who, cudaStream_t st) {
+int launch_rope(RopeArgs a, bool turn, const char* who, cudaStream_t st) {
     if (a.T == 0 || a.heads == 0) return QMOE_OK;
-    const int rounds = four_heads<L>(a.T, a.heads) ? 4 : 1;
-    const unsigned per_token = (unsigned)((a.heads + rounds * (32 / L) - 1) / (rounds * (32 / L)));
+    const int rounds = four_heads<L>(a.T, a.heads) ? 4 : 1, span = rounds * (32 / L);
+    a.q_blocks = (a.n_q + span - 1) / span, a.kv_blocks = (a.n_kv + span - 1) / span;
+    const unsigned per_token = (unsigned)(a.q_blocks + (a.heads - a.n_q) / std::max(a.n_kv, 1) * a.kv_blocks);
+    if (per_token == 0) return QMOE_OK;
     const long long blocks = ((long long)a.T * per_token + 7) / 8;
     if (blocks > 0x7FFFFFFFLL) return qmoe::fail(QMOE_EINVAL, std::string(who) + ": too many heads in one call");
     if (!turn)
