@@ -54,15 +54,15 @@ __device__ __forceinline__ bool request(const AttnArgs& a, int b, int* q0, int* 
 // The products are S^T = U_k Q^T and O^T = U_v^T P^T (m16n8k16, keys or head values as the 16 rows, 8
 // query rows as the 8 columns), so that one to eight rows fill the instruction; tcgen05's 128 rows
 // would be idle and its operands would have to be expanded through shared memory.  The running maximum
-// moves only when a score passes it by 2^8 (a vote per 16 tokens instead of a reduction).
+// moves only when a score passes it by 2^8 (a vote instead of a reduction).
 //
 // Work is cut into tiles of kTile tokens; the tiles of all (request, kv head) items in a row are dealt
 // out to the blocks in equal runs, whatever the lengths.  A producer warp copies whole pages of one
-// head (contiguous in the layout) into a ring of stages with bulk copies; four warps take 16 tokens of
-// each 64.  An item that several blocks share leaves its parts (unnormalised sums, maximum, sum of
+// head (contiguous in the layout) into a ring of stages with bulk copies; four warps take 32 tokens of
+// a tile each.  An item that several blocks share leaves its parts (unnormalised sums, maximum, sum of
 // weights) in the workspace for join_kernel.
-constexpr int kTile = 64;
-constexpr int kStages = 4;
+constexpr int kTile = 128;
+constexpr int kStages = 2;
 constexpr int kConsumers = 4;                        // warps that compute
 constexpr int kDecodeThreads = 32 * (kConsumers + 1);
 constexpr float kNoMax = -3.0e38f;                   // running maximum before any score
@@ -177,7 +177,7 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
 struct StageInfo {
     int b, kh, tile, flags;
 };
-constexpr int kFirst = 1, kLast = 2, kWholeStart = 4, kWholeEnd = 8, kValid = 16;   // kValid << page of the tile
+constexpr int kFirst = 1, kLast = 2, kWholeStart = 4, kWholeEnd = 8, kEdge = 16, kValid = 32;   // kValid << page of the tile; kEdge: some row does not see all of it
 
 template <int D, int NT>
 struct DecodeShared {
@@ -229,21 +229,33 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
     const int n_units = (int)(u1 - u0);
 
     if (warp == kConsumers) {
-        // ---- producer: a warp, lane i copies the tile's i-th page
+        // ---- producer: a warp, lane i copies the tile's i-th page; 32 entries of the block table are read at a time
         const int per_tile = kTile >> a.cache.page_shift;
         const uint32_t page_copy = a.cache.head_bytes;
         int b = f.b, t0, n = tiles_of(a, b, max_rows, &t0, false);
         int kh = (int)((u0 - f.before) / n), tile = (int)((u0 - f.before) % n);
-        int kv_len = a.kv_len[b];
-        bool ok = true;
+        int kv_len = 0, seen_lo = 0, seen_hi = 0;       // every row sees tokens [seen_lo, seen_hi)
+        int held = 0, entry = -1;                       // lane i holds the entry of block held + i
+        bool ok = true, fresh = true;
         int issued = 0;
         for (int u = 0; u < n_units && ok; ++u) {
             const int st = u % kStages;
-            const int blk = (t0 + tile) * per_tile + lane;
-            const bool mine = lane < per_tile && (blk << a.cache.page_shift) < kv_len;
-            int page = -1;
-            if (mine && blk < a.max_blocks) page = a.table[(int64_t)b * a.max_blocks + blk];
-            const bool good = page >= 0 && page < a.cache.n_pages;
+            const int blk0 = (t0 + tile) * per_tile;
+            if (fresh) {
+                const int q_len = a.q_start[b + 1] - a.q_start[b];
+                kv_len = a.kv_len[b];
+                seen_hi = a.causal ? kv_len - q_len + 1 : kv_len;
+                seen_lo = a.window ? max(0, kv_len - a.window) : 0;
+            }
+            if (fresh || blk0 + per_tile > held + 32) {
+                held = blk0;
+                const int blk = blk0 + lane;
+                entry = blk < a.max_blocks && ((long long)blk << a.cache.page_shift) < kv_len ? a.table[(int64_t)b * a.max_blocks + blk] : -1;
+                fresh = false;
+            }
+            const int page = __shfl_sync(QMOE_FULL_MASK, entry, (blk0 - held + lane) & 31);
+            const bool mine = lane < per_tile && ((blk0 + lane) << a.cache.page_shift) < kv_len;
+            const bool good = mine && page >= 0 && page < a.cache.n_pages;
             if (mine && !good) attn_set_error(QMOE_EINVAL);
             const unsigned mask = __ballot_sync(QMOE_FULL_MASK, good);
             if (u >= kStages) ok = qmoe_tc::mbar_wait(&sh.empty[st], (uint32_t)((u / kStages - 1) & 1), kWaitLimit);
@@ -257,6 +269,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
                 if (u == n_units - 1 || tile == n - 1) flags |= kLast;
                 if (u >= tile) flags |= kWholeStart;            // the item's first tile is in this run
                 if (u + (n - 1 - tile) < n_units) flags |= kWholeEnd;
+                if ((t0 + tile) * kTile < seen_lo || (t0 + tile + 1) * kTile > seen_hi || (int)mask != (1 << per_tile) - 1) flags |= kEdge;
                 sh.info[st] = StageInfo{b, kh, t0 + tile, flags};
                 if ((flags & (kLast | kWholeStart | kWholeEnd)) == (kLast | kWholeStart))
                     items[blockIdx.x] = SplitItem{b, kh, 0, (int)((u0 + u - tile + n - 1) / chunk)};
@@ -267,12 +280,12 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
             issued = u + 1;
             if (++tile == n) {
                 tile = 0;
+                fresh = true;
                 if (++kh == a.cache.n_kv_heads) {
                     kh = 0;
                     if (u + 1 < n_units) {
                         do n = tiles_of(a, ++b, max_rows, &t0, false);
                         while (n == 0 && b + 1 < a.B);
-                        kv_len = a.kv_len[b];
                     }
                 }
             }
@@ -289,8 +302,8 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
     // ---- consumers
     const int g = lane >> 2, t = lane & 3;
     const int P = 1 << a.cache.page_shift;
-    // this warp's 16 tokens of a tile: page of the tile and token in the page
-    const int tok0 = warp * 16, pg = tok0 >> a.cache.page_shift, in0 = tok0 & (P - 1);
+    // this warp's 32 tokens of a tile, in two halves of 16: page of the tile and token in the page
+    const int tok0 = warp * 32, pg = tok0 >> a.cache.page_shift, in0 = tok0 & (P - 1);
     const uint32_t page_off = (uint32_t)pg * a.cache.head_bytes;
     // row kappa of the product is token (kappa & 8) + ((kappa & 7) >> 1) + 4 (kappa & 1): the value operand's
     // lanes t then read four neighbouring rows
@@ -299,6 +312,8 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
     const uint32_t v_off = page_off + (uint32_t)(P + in0 + t) * (D / 2) + g * (VW * 4);
     const uint32_t kp_off = page_off + (uint32_t)P * D + kt * 4;
     const uint32_t vp_off = kp_off + (uint32_t)P * 4;
+    // from one half to the other: the next 16 rows, or the next page where a page has 16
+    const uint32_t row_step = P == 16 ? a.cache.head_bytes : 16 * (D / 2), pair_step = P == 16 ? a.cache.head_bytes : 64;
 
     uint2 qr[W][2];                // query operand of 8 rows: [word][nibble parity]
     float c1[NT][2], cz[NT][2];    // per row: factor of s (q . u), and factor times sum(q), in log2 units
@@ -378,148 +393,167 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
             __syncwarp();
         }
         const unsigned char* stg = sh.stage[st];
-        // ---- scores of 16 tokens
-        uint32_t kw[2][W];
+        // With 8 rows both halves go through each phase together (two chains to overlap, one vote); with more, whose sums
+        // take the registers, one after the other.
+        constexpr int J = NT == 1 ? 2 : 1;
+#pragma unroll 1
+        for (int half = 0; half < 2; half += J) {
+            float s[J][NT][4], sv[J][2], zv[J][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            if constexpr (W == 4) {
-                const uint4 x = *(const uint4*)(stg + k_off + r * 8 * (D / 2));
-                kw[r][0] = x.x, kw[r][1] = x.y, kw[r][2] = x.z, kw[r][3] = x.w;
-            } else {
-                const uint2 x = *(const uint2*)(stg + k_off + r * 8 * (D / 2));
-                kw[r][0] = x.x, kw[r][1] = x.y;
-            }
-        }
-        float s[NT][4];
+            for (int j = 0; j < J; ++j) {
+                // ---- scores of 16 tokens
+                const unsigned char* kb = stg + k_off + (half + j) * row_step;
+                uint32_t kw[2][W];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[nt][j] = 0.f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const uint32_t x0 = kw[0][w], x1 = kw[1][w], y0 = x0 >> 8, y1 = x1 >> 8;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                uint2 qa, qb;
-                if constexpr (NT == 1)
-                    qa = qr[w][0], qb = qr[w][1];
-                else
-                    qa = sh.qf[nt][w][0][lane], qb = sh.qf[nt][w][1][lane];
-                mma_16816(s[nt], x0 & 0x000F000Fu, x1 & 0x000F000Fu, y0 & 0x000F000Fu, y1 & 0x000F000Fu, qa.x, qa.y);
-                mma_16816(s[nt], x0 & 0x00F000F0u, x1 & 0x00F000F0u, y0 & 0x00F000F0u, y1 & 0x00F000F0u, qb.x, qb.y);
-            }
-        }
-        float sk[2], zk[2], sv[2], zv[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float2 kp = __half22float2(*(const __half2*)(stg + kp_off + r * 32));
-            const float2 vp = __half22float2(*(const __half2*)(stg + vp_off + r * 32));
-            sk[r] = kp.x, zk[r] = kp.y, sv[r] = vp.x, zv[r] = vp.y;
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    s[nt][2 * r + i] = fmaf(c1[nt][i], sk[r] * s[nt][2 * r + i], cz[nt][i] * zk[r]);
-        // ---- tokens that some row does not see
-        const int j0 = in.tile * kTile;
-        const int first = a.causal ? kv_len - q_len : kv_len - 1;
-        const int edge_lo = a.window ? max(0, (a.causal ? kv_len - 1 : first) - a.window + 1) : 0;
-        if (j0 + kTile > first + 1 || j0 + kTile > kv_len || j0 < edge_lo ||
-            (in.flags / kValid) != (1 << (kTile >> a.cache.page_shift)) - 1) {
-            const bool page_ok = (in.flags / kValid >> pg) & 1;
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int j = j0 + tok0 + (g >> 1) + 4 * (g & 1) + 8 * r;
-                const bool there = page_ok && j < kv_len;
-                if (!there) sv[r] = 0.f, zv[r] = 0.f;
+                for (int r = 0; r < 2; ++r) {
+                    if constexpr (W == 4) {
+                        const uint4 x = *(const uint4*)(kb + r * 8 * (D / 2));
+                        kw[r][0] = x.x, kw[r][1] = x.y, kw[r][2] = x.z, kw[r][3] = x.w;
+                    } else {
+                        const uint2 x = *(const uint2*)(kb + r * 8 * (D / 2));
+                        kw[r][0] = x.x, kw[r][1] = x.y;
+                    }
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int pos = a.causal ? first + (nt * 8 + 2 * t + i) / a.group : first;
-                        if (!there || j > pos || (a.window && j <= pos - a.window)) s[nt][2 * r + i] = -INFINITY;
+                    for (int i = 0; i < 4; ++i) s[j][nt][i] = 0.f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const uint32_t x0 = kw[0][w], x1 = kw[1][w], y0 = x0 >> 8, y1 = x1 >> 8;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint2 qa, qb;
+                        if constexpr (NT == 1)
+                            qa = qr[w][0], qb = qr[w][1];
+                        else
+                            qa = sh.qf[nt][w][0][lane], qb = sh.qf[nt][w][1][lane];
+                        mma_16816(s[j][nt], x0 & 0x000F000Fu, x1 & 0x000F000Fu, y0 & 0x000F000Fu, y1 & 0x000F000Fu, qa.x, qa.y);
+                        mma_16816(s[j][nt], x0 & 0x00F000F0u, x1 & 0x00F000F0u, y0 & 0x00F000F0u, y1 & 0x00F000F0u, qb.x, qb.y);
                     }
-            }
-        }
-        // ---- move the maximum or the values' scale, rarely
-        bool move = fmaxf(fabsf(sv[0]), fabsf(sv[1])) >= vlim;
+                }
+                float sk[2], zk[2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) move |= fmaxf(s[nt][i], s[nt][2 + i]) > m[nt][i] + kSlack;
-        if (__any_sync(QMOE_FULL_MASK, move)) {
-            float v = fmaxf(fmaxf(fabsf(sv[0]), fabsf(sv[1])), vlim * 0.5f);
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(QMOE_FULL_MASK, v, d));
-            float fo = 1.f;
-            if (v >= vlim) {
-                const int k = (int)(__float_as_uint(v) >> 23) - 127;       // v in [2^k, 2^(k+1))
-                const float nvs = pow2i(6 - k);
-                fo = nvs / vs;
-                vs = nvs;
-                vlim = pow2i(k + 1);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float fr[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float mx = fmaxf(s[nt][i], s[nt][2 + i]);
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(QMOE_FULL_MASK, mx, d));
-                    const float m2 = fmaxf(m[nt][i], mx), fm = ex2(m[nt][i] - m2);
-                    m[nt][i] = m2;
-                    l[nt][i] *= fm, pz[nt][i] *= fm;
-                    fr[i] = fm * fo;
+                for (int r = 0; r < 2; ++r) {
+                    const float2 kp = __half22float2(*(const __half2*)(stg + kp_off + (half + j) * pair_step + r * 32));
+                    const float2 vp = __half22float2(*(const __half2*)(stg + vp_off + (half + j) * pair_step + r * 32));
+                    sk[r] = kp.x, zk[r] = kp.y, sv[j][r] = vp.x, zv[j][r] = vp.y;
                 }
 #pragma unroll
-                for (int i = 0; i < 4 * VW; ++i)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) o[nt][i][j] *= fr[j & 1];
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            s[j][nt][2 * r + i] = fmaf(c1[nt][i], sk[r] * s[j][nt][2 * r + i], cz[nt][i] * zk[r]);
+                // ---- tokens that some row does not see
+                if (__builtin_expect(in.flags & kEdge, 0)) {
+                    const int first = a.causal ? kv_len - q_len : kv_len - 1;
+                    const bool page_ok = (in.flags / kValid >> ((tok0 + 16 * (half + j)) >> a.cache.page_shift)) & 1;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int tok = in.tile * kTile + tok0 + 16 * (half + j) + (g >> 1) + 4 * (g & 1) + 8 * r;
+                        const bool there = page_ok && tok < kv_len;
+                        if (!there) sv[j][r] = 0.f, zv[j][r] = 0.f;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int pos = a.causal ? first + (nt * 8 + 2 * t + i) / a.group : first;
+                                if (!there || tok > pos || (a.window && tok <= pos - a.window)) s[j][nt][2 * r + i] = -INFINITY;
+                            }
+                    }
+                }
             }
-        }
-        // ---- probabilities, as the value product's operand
-        uint32_t pf[NT][2];
-        const float w0 = sv[0] * vs, w1 = sv[1] * vs;
+            // ---- move the maximum or the values' scale, rarely
+            float vmax = 0.f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float p[4];
+            for (int j = 0; j < J; ++j) vmax = fmaxf(vmax, fmaxf(fabsf(sv[j][0]), fabsf(sv[j][1])));
+            bool move = vmax >= vlim;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) p[j] = ex2(s[nt][j] - m[nt][j & 1]);
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                l[nt][i] += p[i] + p[2 + i];
-                pz[nt][i] = fmaf(p[i], zv[0], fmaf(p[2 + i], zv[1], pz[nt][i]));
+                for (int i = 0; i < 2; ++i) {
+                    float mx = fmaxf(s[0][nt][i], s[0][nt][2 + i]);
+                    if (J == 2) mx = fmaxf(mx, fmaxf(s[J - 1][nt][i], s[J - 1][nt][2 + i]));
+                    move |= mx > m[nt][i] + kSlack;
+                }
+            if (__builtin_expect(__any_sync(QMOE_FULL_MASK, move), 0)) {
+                float v = fmaxf(vmax, vlim * 0.5f);
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(QMOE_FULL_MASK, v, d));
+                float fo = 1.f;
+                if (v >= vlim) {
+                    const int k = (int)(__float_as_uint(v) >> 23) - 127;       // v in [2^k, 2^(k+1))
+                    const float nvs = pow2i(6 - k);
+                    fo = nvs / vs;
+                    vs = nvs;
+                    vlim = pow2i(k + 1);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float fr[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float mx = fmaxf(s[0][nt][i], s[0][nt][2 + i]);
+                        if (J == 2) mx = fmaxf(mx, fmaxf(s[J - 1][nt][i], s[J - 1][nt][2 + i]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(QMOE_FULL_MASK, mx, d));
+                        const float m2 = fmaxf(m[nt][i], mx), fm = ex2(m[nt][i] - m2);
+                        m[nt][i] = m2;
+                        l[nt][i] *= fm, pz[nt][i] *= fm;
+                        fr[i] = fm * fo;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4 * VW; ++i)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) o[nt][i][q] *= fr[q & 1];
+                }
             }
-            pf[nt][0] = movmatrix(half2_bits(p[0] * w0, p[1] * w0));
-            pf[nt][1] = movmatrix(half2_bits(p[2] * w1, p[3] * w1));
-        }
-        // ---- values: words of tokens t, t + 4, t + 8, t + 12 of this warp's 16
-        uint32_t vw[4][VW];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            if constexpr (VW == 2) {
-                const uint2 x = *(const uint2*)(stg + v_off + r * 4 * (D / 2));
-                vw[r][0] = x.x, vw[r][1] = x.y;
-            } else {
-                vw[r][0] = *(const uint32_t*)(stg + v_off + r * 4 * (D / 2));
-            }
-        }
+            for (int j = 0; j < J; ++j) {
+                // ---- probabilities, as the value product's operand
+                uint32_t pf[NT][2];
+                const float w0 = sv[j][0] * vs, w1 = sv[j][1] * vs;
 #pragma unroll
-        for (int w = 0; w < VW; ++w) {
-            // pairs of tokens: (t, t + 4) and (t + 8, t + 12); even values in the low halves, odd ones in the high
-            const uint32_t e0 = __byte_perm(vw[0][w], vw[1][w], 0x5410), d0 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
-            const uint32_t e1 = __byte_perm(vw[2][w], vw[3][w], 0x5410), d1 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
-            const uint32_t e0s = e0 >> 8, d0s = d0 >> 8, e1s = e1 >> 8, d1s = d1 >> 8;
+                for (int nt = 0; nt < NT; ++nt) {
+                    float p[4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                mma_16816(o[nt][4 * w], e0 & 0x000F000Fu, d0 & 0x000F000Fu, e1 & 0x000F000Fu, d1 & 0x000F000Fu, pf[nt][0], pf[nt][1]);
-                mma_16816(o[nt][4 * w + 1], e0 & 0x00F000F0u, d0 & 0x00F000F0u, e1 & 0x00F000F0u, d1 & 0x00F000F0u, pf[nt][0], pf[nt][1]);
-                mma_16816(o[nt][4 * w + 2], e0s & 0x000F000Fu, d0s & 0x000F000Fu, e1s & 0x000F000Fu, d1s & 0x000F000Fu, pf[nt][0], pf[nt][1]);
-                mma_16816(o[nt][4 * w + 3], e0s & 0x00F000F0u, d0s & 0x00F000F0u, e1s & 0x00F000F0u, d1s & 0x00F000F0u, pf[nt][0], pf[nt][1]);
+                    for (int i = 0; i < 4; ++i) p[i] = ex2(s[j][nt][i] - m[nt][i & 1]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        l[nt][i] += p[i] + p[2 + i];
+                        pz[nt][i] = fmaf(p[i], zv[j][0], fmaf(p[2 + i], zv[j][1], pz[nt][i]));
+                    }
+                    pf[nt][0] = movmatrix(half2_bits(p[0] * w0, p[1] * w0));
+                    pf[nt][1] = movmatrix(half2_bits(p[2] * w1, p[3] * w1));
+                }
+                // ---- values: words of tokens t, t + 4, t + 8, t + 12 of the 16
+                const unsigned char* vb = stg + v_off + (half + j) * row_step;
+                uint32_t vw[4][VW];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    if constexpr (VW == 2) {
+                        const uint2 x = *(const uint2*)(vb + r * 4 * (D / 2));
+                        vw[r][0] = x.x, vw[r][1] = x.y;
+                    } else {
+                        vw[r][0] = *(const uint32_t*)(vb + r * 4 * (D / 2));
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < VW; ++w) {
+                    // pairs of tokens: (t, t + 4) and (t + 8, t + 12); even values in the low halves, odd ones in the high
+                    const uint32_t e0 = __byte_perm(vw[0][w], vw[1][w], 0x5410), d0 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
+                    const uint32_t e1 = __byte_perm(vw[2][w], vw[3][w], 0x5410), d1 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
+                    const uint32_t e0s = e0 >> 8, d0s = d0 >> 8, e1s = e1 >> 8, d1s = d1 >> 8;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_16816(o[nt][4 * w], e0 & 0x000F000Fu, d0 & 0x000F000Fu, e1 & 0x000F000Fu, d1 & 0x000F000Fu, pf[nt][0], pf[nt][1]);
+                        mma_16816(o[nt][4 * w + 1], e0 & 0x00F000F0u, d0 & 0x00F000F0u, e1 & 0x00F000F0u, d1 & 0x00F000F0u, pf[nt][0], pf[nt][1]);
+                        mma_16816(o[nt][4 * w + 2], e0s & 0x000F000Fu, d0s & 0x000F000Fu, e1s & 0x000F000Fu, d1s & 0x000F000Fu, pf[nt][0], pf[nt][1]);
+                        mma_16816(o[nt][4 * w + 3], e0s & 0x00F000F0u, d0s & 0x00F000F0u, e1s & 0x00F000F0u, d1s & 0x00F000F0u, pf[nt][0], pf[nt][1]);
+                    }
+                }
             }
         }
         __syncwarp();
