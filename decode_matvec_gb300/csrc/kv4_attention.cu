@@ -62,7 +62,8 @@ __device__ __forceinline__ bool request(const AttnArgs& a, int b, int* q0, int* 
 // a tile each.  An item that several blocks share leaves its parts (unnormalised sums, maximum, sum of
 // weights) in the workspace for join_kernel.
 constexpr int kTile = 128;
-constexpr int kStages = 2;
+constexpr int kItemCost = 3;                         // what beginning and ending an item costs, in tiles
+constexpr int kStages = 3;
 constexpr int kConsumers = 4;                        // warps that compute
 constexpr int kDecodeThreads = 32 * (kConsumers + 1);
 constexpr float kNoMax = -3.0e38f;                   // running maximum before any score
@@ -80,7 +81,7 @@ __device__ __forceinline__ int tiles_of(const AttnArgs& a, int b, int max_rows, 
     return max(1, (kv_len + kTile - 1) / kTile - *t0);
 }
 
-// Block-wide: the units (tiles of all items) in all, the run of each block, and the request that holds this block's first
+// Block-wide: the units (tiles of all items, and kItemCost for each item after its tiles) in all, the run of each block, and the request that holds this block's first
 // unit with the units before it.  A scan over the requests; every thread gets the results.
 struct Found {
     long long total, before;
@@ -96,7 +97,10 @@ __device__ __forceinline__ Found scan_requests(const AttnArgs& a, int max_rows, 
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
     long long mine = 0;
     int t0;
-    for (int b = b0; b < b1; ++b) mine += tiles_of(a, b, max_rows, &t0, blockIdx.x == 0);
+    for (int b = b0; b < b1; ++b) {
+        const int n = tiles_of(a, b, max_rows, &t0, blockIdx.x == 0);
+        if (n) mine += n + kItemCost;
+    }
     mine *= a.cache.n_kv_heads;
     long long incl = mine;
 #pragma unroll
@@ -116,7 +120,8 @@ __device__ __forceinline__ Found scan_requests(const AttnArgs& a, int max_rows, 
     const long long target = (long long)blockIdx.x * *chunk;
     if (target >= before && target < before + mine) {
         for (int b = b0; b < b1; ++b) {
-            const long long n = (long long)tiles_of(a, b, max_rows, &t0, false) * a.cache.n_kv_heads;
+            const int tiles = tiles_of(a, b, max_rows, &t0, false);
+            const long long n = tiles ? (long long)(tiles + kItemCost) * a.cache.n_kv_heads : 0;
             if (target < before + n) {
                 found.b = b;
                 found.before = before;
@@ -177,7 +182,8 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
 struct StageInfo {
     int b, kh, tile, flags;
 };
-constexpr int kFirst = 1, kLast = 2, kWholeStart = 4, kWholeEnd = 8, kEdge = 16, kValid = 32;   // kValid << page of the tile; kEdge: some row does not see all of it
+constexpr int kFirst = 1, kLast = 2, kWholeStart = 4, kWholeEnd = 8, kEdge = 16, kEnd = 32, kValid = 64;   // kValid << page of the tile; kEdge: some row does not see all of it;
+                                                                                                   // kEnd: nothing, the run is over
 
 template <int D, int NT>
 struct DecodeShared {
@@ -206,7 +212,7 @@ __device__ __forceinline__ void depend_launch() { asm volatile("griddepcontrol.l
 __device__ __forceinline__ void depend_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
+__global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
     decode_kernel(AttnArgs a, int max_rows, SplitItem* items, float* parts) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     DecodeShared<D, NT>& sh = *(DecodeShared<D, NT>*)smem_raw;
@@ -226,20 +232,43 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
     const long long u0 = (long long)blockIdx.x * chunk, u1 = min(u0 + chunk, f.total);
     if (tid == 32 * kConsumers) items[blockIdx.x] = SplitItem{0, 0, 0, -1};
     if (u0 >= u1) return;
-    const int n_units = (int)(u1 - u0);
 
     if (warp == kConsumers) {
         // ---- producer: a warp, lane i copies the tile's i-th page; 32 entries of the block table are read at a time
         const int per_tile = kTile >> a.cache.page_shift;
         const uint32_t page_copy = a.cache.head_bytes;
         int b = f.b, t0, n = tiles_of(a, b, max_rows, &t0, false);
-        int kh = (int)((u0 - f.before) / n), tile = (int)((u0 - f.before) % n);
+        int kh = (int)((u0 - f.before) / (n + kItemCost));
+        long long begin = f.before + (long long)kh * (n + kItemCost);       // the item's first unit
+        int tile = (int)(u0 - begin);
         int kv_len = 0, seen_lo = 0, seen_hi = 0;       // every row sees tokens [seen_lo, seen_hi)
         int held = 0, entry = -1;                       // lane i holds the entry of block held + i
         bool ok = true, fresh = true;
         int issued = 0;
-        for (int u = 0; u < n_units && ok; ++u) {
+        for (int u = 0; ok; ++u) {
             const int st = u % kStages;
+            // the next tile of the run: past an item's last one comes the next item's first
+            bool over = begin + tile >= u1;
+            while (!over && tile >= n) {
+                begin += n + kItemCost;
+                tile = 0;
+                fresh = true;
+                over = begin >= u1;
+                if (!over && ++kh == a.cache.n_kv_heads) {
+                    kh = 0;
+                    do n = tiles_of(a, ++b, max_rows, &t0, false);
+                    while (n == 0 && b + 1 < a.B);
+                }
+            }
+            if (over) {
+                if (u >= kStages) ok = qmoe_tc::mbar_wait(&sh.empty[st], (uint32_t)((u / kStages - 1) & 1), kWaitLimit);
+                if (ok && lane == 0) {
+                    sh.info[st].flags = kEnd;
+                    mbar_arrive(&sh.full[st]);
+                }
+                break;
+            }
+            const int end = (int)min((long long)n, u1 - begin);      // of the item's tiles in this run
             const int blk0 = (t0 + tile) * per_tile;
             if (fresh) {
                 const int q_len = a.q_start[b + 1] - a.q_start[b];
@@ -251,7 +280,6 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
                 held = blk0;
                 const int blk = blk0 + lane;
                 entry = blk < a.max_blocks && ((long long)blk << a.cache.page_shift) < kv_len ? a.table[(int64_t)b * a.max_blocks + blk] : -1;
-                fresh = false;
             }
             const int page = __shfl_sync(QMOE_FULL_MASK, entry, (blk0 - held + lane) & 31);
             const bool mine = lane < per_tile && ((blk0 + lane) << a.cache.page_shift) < kv_len;
@@ -265,30 +293,21 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
             }
             if (lane == 0) {
                 int flags = (int)mask * kValid;
-                if (u == 0 || tile == 0) flags |= kFirst;
-                if (u == n_units - 1 || tile == n - 1) flags |= kLast;
-                if (u >= tile) flags |= kWholeStart;            // the item's first tile is in this run
-                if (u + (n - 1 - tile) < n_units) flags |= kWholeEnd;
+                if (fresh) flags |= kFirst;
+                if (tile == end - 1) flags |= kLast;
+                if (begin >= u0) flags |= kWholeStart;          // the item's first tile is in this run
+                if (end == n) flags |= kWholeEnd;
                 if ((t0 + tile) * kTile < seen_lo || (t0 + tile + 1) * kTile > seen_hi || (int)mask != (1 << per_tile) - 1) flags |= kEdge;
                 sh.info[st] = StageInfo{b, kh, t0 + tile, flags};
                 if ((flags & (kLast | kWholeStart | kWholeEnd)) == (kLast | kWholeStart))
-                    items[blockIdx.x] = SplitItem{b, kh, 0, (int)((u0 + u - tile + n - 1) / chunk)};
+                    items[blockIdx.x] = SplitItem{b, kh, 0, (int)((begin + n - 1) / chunk)};
                 mbar_expect(&sh.full[st], (uint32_t)__popc(mask) * page_copy);
             }
             __syncwarp();
             if (good) bulk_copy(sh.stage[st] + lane * page_copy, kv4::head_ptr(a.cache, page, kh), page_copy, &sh.full[st]);
             issued = u + 1;
-            if (++tile == n) {
-                tile = 0;
-                fresh = true;
-                if (++kh == a.cache.n_kv_heads) {
-                    kh = 0;
-                    if (u + 1 < n_units) {
-                        do n = tiles_of(a, ++b, max_rows, &t0, false);
-                        while (n == 0 && b + 1 < a.B);
-                    }
-                }
-            }
+            fresh = false;
+            ++tile;
         }
         if (!ok) {
             // give up: report, and let the copies in flight land before the block's memory goes away
@@ -322,13 +341,14 @@ __global__ void __launch_bounds__(kDecodeThreads, NT == 1 ? 4 : NT == 2 ? 3 : 2)
     float vs = 1.f, vlim = 1e-9f;  // probabilities carry vs (a power of two); a value scale >= vlim moves it
     int q0 = 0, q_len = 0, kv_len = 0;
 
-    for (int u = 0; u < n_units; ++u) {
+    for (int u = 0;; ++u) {
         const int st = u % kStages;
         if (!qmoe_tc::mbar_wait(&sh.full[st], (uint32_t)((u / kStages) & 1), kWaitLimit)) {
             if (lane == 0) attn_set_error(QMOE_ETIMEOUT);
             return;
         }
         const StageInfo in = sh.info[st];
+        if (in.flags & kEnd) return;
         if (in.flags & kFirst) {
             q0 = a.q_start[in.b], q_len = a.q_start[in.b + 1] - q0, kv_len = a.kv_len[in.b];
             const int rows = q_len * a.group;
@@ -703,6 +723,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, const Sp
 // runs; items that several blocks share are joined by join_kernel.
 constexpr int kKeys = 128;                       // keys of a tile (expanded at once)
 constexpr int kStep = 64;                        // keys of a softmax step
+constexpr int kTileItemCost = 3;                 // what beginning and ending an item costs, in tiles
 constexpr int kRows = 256;                       // query rows of an item
 constexpr int kTileThreads = 512;
 constexpr int kExpandWarp = 8, kIssueWarp = 12, kCopyWarp = 13;
@@ -711,7 +732,7 @@ constexpr int kPlanTile = 1024;
 
 // Work list of the tile path, in the workspace: pairs (request, block of 256 rows) in order.
 struct alignas(16) PairInfo {
-    long long unit;              // key tiles of all kv heads before the pair
+    long long unit;              // units before the pair: its kv heads' key tiles, and kTileItemCost for each item
     int n;                       // key tiles of one kv head, lo .. lo + n - 1
     int b, rb, q0, q_len, kv_len, lo;
     int s[2], e[2];              // steps, from 2 lo, that the two tiles of 128 rows see
@@ -796,7 +817,7 @@ __global__ void __launch_bounds__(kPlanTile) tile_plan_kernel(AttnArgs a, TilePl
                 w.s[x] = lo - 2 * w.lo, w.e[x] = hi - 2 * w.lo;
             }
         }
-        const long long n = (long long)w.n * a.cache.n_kv_heads;
+        const long long n = w.n ? (long long)(w.n + kTileItemCost) * a.cache.n_kv_heads : 0;
         const long long end = base + block_scan(n, &total);
         if (i < n_pairs) {
             w.unit = end - n;
@@ -833,61 +854,66 @@ struct TileShared {
 };
 
 // The next item of the run, or false: the pair's rows, kv head kh, key tiles w.lo + [t0, t1).  Each warp keeps its own
-// cursor in shared memory.  first: the run's first item, which may begin inside a pair.
-__device__ __forceinline__ void place_item(const AttnArgs& a, TileCursor& c, bool first) {
+// cursor in shared memory.  Returns whether the place holds tiles (a run may begin or end in an item's extra units).
+__device__ __forceinline__ bool place_item(const AttnArgs& a, TileCursor& c, bool first) {
+    long long off = 0;
     if (first) {
-        const long long off = c.u - c.w.unit;
-        c.kh = (int)(off / c.w.n);
-        c.t0 = (int)(off - (long long)c.kh * c.w.n);
-    } else {
-        c.t0 = 0;
+        off = c.u - c.w.unit;
+        c.kh = (int)(off / (c.w.n + kTileItemCost));
+        off -= (long long)c.kh * (c.w.n + kTileItemCost);
     }
-    c.t1 = (int)min((long long)c.w.n, c.t0 + (c.u1 - c.u));
+    const long long span = min(c.w.n + kTileItemCost - off, c.u1 - c.u);
+    c.t0 = (int)min(off, (long long)c.w.n);
+    c.t1 = (int)min(off + span, (long long)c.w.n);
     c.whole = c.t0 == 0 && c.t1 == c.w.n;
     for (int x = 0; x < 2; ++x) {
         const int s = max(c.w.s[x], 2 * c.t0), e = min(c.w.e[x], 2 * c.t1);
         c.s[x] = s < e ? s : 0, c.e[x] = s < e ? e : 0;
     }
-    c.u += c.t1 - c.t0;
+    c.u += span;
+    return c.t0 < c.t1;
 }
 
 // By one thread.
 __device__ __forceinline__ bool next_item_alone(const AttnArgs& a, const TilePlan& p, TileCursor& c, bool first) {
-    if (c.u >= c.u1) return false;
-    if (first || ++c.kh == a.cache.n_kv_heads) {
-        c.kh = 0;
-        if (!first) ++c.pair;
-        const uint4* src = (const uint4*)(p.pairs + c.pair);
-        const uint4 v[4] = {src[0], src[1], src[2], src[3]};
-        for (int i = 0; i < 4; ++i) ((uint4*)&c.w)[i] = v[i];
+    for (;; first = false) {
+        if (c.u >= c.u1) return false;
+        if (first || ++c.kh == a.cache.n_kv_heads) {
+            c.kh = 0;
+            if (!first) ++c.pair;
+            const uint4* src = (const uint4*)(p.pairs + c.pair);
+            const uint4 v[4] = {src[0], src[1], src[2], src[3]};
+            for (int i = 0; i < 4; ++i) ((uint4*)&c.w)[i] = v[i];
+        }
+        if (place_item(a, c, first)) return true;
     }
-    place_item(a, c, first);
-    return true;
 }
 
 // By a warp; ahead holds the pair after this one (a word a lane), loaded while this one is worked on.
 __device__ __forceinline__ bool next_item(const AttnArgs& a, const TilePlan& p, int n_pairs, TileCursor& c, bool first, uint32_t& ahead) {
     const int lane = threadIdx.x & 31;
-    __syncwarp();
-    if (c.u >= c.u1) return false;
-    const bool load = first || c.kh + 1 == a.cache.n_kv_heads;
-    const int pair = c.pair + (first ? 0 : 1);
-    __syncwarp();
-    if (load) {
-        if (first && lane < 16) ahead = ((const uint32_t*)(p.pairs + pair))[lane];
-        if (lane < 16) ((uint32_t*)&c.w)[lane] = ahead;
-        if (lane < 16 && pair + 1 < n_pairs) ahead = ((const uint32_t*)(p.pairs + pair + 1))[lane];
+    for (;; first = false) {
         __syncwarp();
+        if (c.u >= c.u1) return false;
+        const bool load = first || c.kh + 1 == a.cache.n_kv_heads;
+        const int pair = c.pair + (first ? 0 : 1);
+        __syncwarp();
+        if (load) {
+            if (first && lane < 16) ahead = ((const uint32_t*)(p.pairs + pair))[lane];
+            if (lane < 16) ((uint32_t*)&c.w)[lane] = ahead;
+            if (lane < 16 && pair + 1 < n_pairs) ahead = ((const uint32_t*)(p.pairs + pair + 1))[lane];
+            __syncwarp();
+        }
+        bool some = false;
+        if (lane == 0) {
+            if (load)
+                c.kh = 0, c.pair = pair;
+            else
+                ++c.kh;
+            some = place_item(a, c, first);
+        }
+        if (__shfl_sync(QMOE_FULL_MASK, (int)some, 0)) return true;
     }
-    if (lane == 0) {
-        if (load)
-            c.kh = 0, c.pair = pair;
-        else
-            ++c.kh;
-        place_item(a, c, first);
-    }
-    __syncwarp();
-    return true;
 }
 
 // Bounded wait; false when the tries ran out.  A few instructions, as every role's loop holds some of these and the
@@ -1459,7 +1485,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
             uint32_t tile = 0;
                 for (bool first = true; ok && next_item(a, plan, n_pairs, c, first, ahead); first = false) {
                 if (lane == 0 && c.t0 == 0 && !c.whole)
-                    plan.items[blockIdx.x] = SplitItem{c.w.b, c.kh, c.w.rb, (int)((first_unit + tile + c.w.n - 1) / chunk)};
+                    plan.items[blockIdx.x] = SplitItem{c.w.b, c.kh, c.w.rb, (int)((c.w.unit + (long long)c.kh * (c.w.n + kTileItemCost) + c.w.n - 1) / chunk)};
                 for (int t = c.t0; t < c.t1; ++t, ++tile) {
                     const int st = tile % kRawStages;
                     const int blk = (c.w.lo + t) * per_tile + lane;
@@ -1508,7 +1534,7 @@ int decode_rows(int group, int max_q) {
 }
 
 // Blocks of the few-row path that are on the device together.
-size_t decode_fit(int rows) { return (size_t)qmoe::sm_count() * (rows <= 8 ? 4 : rows <= 16 ? 3 : 2); }
+size_t decode_fit(int rows) { return (size_t)qmoe::sm_count() * (rows <= 16 ? 3 : 2); }
 
 // Blocks of the few-row path: as many as fit on the device, no more than tiles.
 long long decode_blocks(int rows, int B, int n_kv_heads, int max_kv) {
