@@ -1530,7 +1530,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
 int decode_rows(int group, int max_q) {
     const long long all = (long long)group * max_q;
     const int rows = all <= 32 ? (int)all : group <= 32 ? group : 0;
-    return rows == 0 ? 0 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    return (rows + 7) / 8 * 8;
 }
 
 // Blocks of the few-row path that are on the device together.
@@ -1668,6 +1668,7 @@ extern "C" int kv4_attention(const kv4_cache* cache, const void* q, int n_q_toke
     if ((long long)B * cache->n_kv_heads > 0x7FFFFFFFLL) return qmoe::fail(QMOE_EINVAL, "kv4_attention: batch too large");
     if (rows == 8) rc = D == 128 ? launch_decode<128, 1>(a, workspace, st) : launch_decode<64, 1>(a, workspace, st);
     if (rows == 16) rc = D == 128 ? launch_decode<128, 2>(a, workspace, st) : launch_decode<64, 2>(a, workspace, st);
+    if (rows == 24) rc = D == 128 ? launch_decode<128, 3>(a, workspace, st) : launch_decode<64, 3>(a, workspace, st);
     if (rows == 32) rc = D == 128 ? launch_decode<128, 4>(a, workspace, st) : launch_decode<64, 4>(a, workspace, st);
     if (rc || !tiles) return rc;
     return D == 128 ? launch_tiles<128>(a, tw, rows, st) : launch_tiles<64>(a, tw, rows, st);
