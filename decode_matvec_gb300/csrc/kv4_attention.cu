@@ -846,6 +846,7 @@ struct TileShared {
     alignas(1024) unsigned char q[2][kBuf];
     alignas(1024) unsigned char kv[kExpanded][kBuf];
     alignas(128) unsigned char raw[kRawStages][kKeys * (D + 8)];
+    alignas(16) unsigned char rows[8][32 * 80];                  // a softmax warp's 64 bytes a row, on their way out
     uint64_t raw_full[kRawStages], raw_empty[kRawStages], kv_full[kExpanded], kv_empty[kExpanded];
     uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2], fin[2];      // [tile of rows][step parity]
     uint32_t valid[kInfo];                                       // per tile: which groups of 16 tokens have a page
@@ -1101,20 +1102,69 @@ __host__ __device__ constexpr int v_swap(int o) {
     return D == 128 ? (o & 1) : (o & 3);
 }
 
-// Where row r of the item's rows is in q and out, and the row itself (zeros past the request's rows).
+// Where row r of the item's rows is in q and out; -1 past the request's rows.
 template <int D>
 __device__ __forceinline__ int64_t row_at(const AttnArgs& a, const TileCursor& c, int r) {
+    if (r >= c.w.q_len * a.group) return -1;
     const int n = r / a.group;
     return ((int64_t)(c.w.q0 + n) * a.n_q_heads + c.kh * a.group + r - n * a.group) * D;
 }
 
+// A warp's 32 query rows into the query tile, D / 8 lanes a row (a thread a row would touch 32 cache lines a load), each
+// row's largest magnitude scaled to [2^14, 2^15).  Returns the factor that takes the thread's own row's scores to log2
+// units.  Rows past the request's are zeros.
 template <int D>
-__device__ __forceinline__ void load_row(const AttnArgs& a, const TileCursor& c, int x, int row, uint4 (&raw)[D / 8]) {
-    const int r = c.w.rb * kRows + x * 128 + row;
-    const bool live = r < c.w.q_len * a.group && c.e[x] > c.s[x];
-    const uint4* src = (const uint4*)(a.q + row_at<D>(a, c, r));
+__device__ __forceinline__ float put_rows(const AttnArgs& a, const TileCursor& c, int x, TileShared<D>& sh) {
+    if (c.e[x] <= c.s[x]) return 0.f;
+    constexpr int LANES = D / 8, PER = 32 / LANES, LOADS = 32 / PER;      // lanes of a row, rows of a load, loads
+    const int lane = threadIdx.x & 31, row0 = ((threadIdx.x >> 5) & 3) * 32, sub = lane / LANES, piece = lane % LANES;
+    const int64_t mine = row_at<D>(a, c, c.w.rb * kRows + x * 128 + row0 + lane);
+    int e_mine = 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < LOADS; i0 += 8) {
+        uint4 raw[8];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) raw[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 8; ++i) {
+            const int64_t at = __shfl_sync(QMOE_FULL_MASK, mine, (i0 + i) * PER + sub);
+            raw[i] = at >= 0 ? *(const uint4*)(a.q + at + piece * 8) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint4 v = raw[i];
+            float mx = fmaxf(fmaxf(fmaxf(fabsf(bf16_lo(v.x)), fabsf(bf16_hi(v.x))), fmaxf(fabsf(bf16_lo(v.y)), fabsf(bf16_hi(v.y)))),
+                             fmaxf(fmaxf(fabsf(bf16_lo(v.z)), fabsf(bf16_hi(v.z))), fmaxf(fabsf(bf16_lo(v.w)), fabsf(bf16_hi(v.w)))));
+#pragma unroll
+            for (int d = LANES / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(QMOE_FULL_MASK, mx, d));
+            const int e = mx > 0.f ? min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 126) : 0;
+            const float up = a.scale < 0.f ? -pow2i(14 - e) : pow2i(14 - e);
+            const int r = row0 + (i0 + i) * PER + sub;
+            *(uint4*)(sh.q[x] + r * 128 + (piece >> 3) * TileShared<D>::kQAtom + (((piece & 7) ^ (r & 7)) << 4)) =
+                make_uint4(half2_bits(bf16_lo(v.x) * up, bf16_hi(v.x) * up), half2_bits(bf16_lo(v.y) * up, bf16_hi(v.y) * up),
+                           half2_bits(bf16_lo(v.z) * up, bf16_hi(v.z) * up), half2_bits(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+            const int of = __shfl_sync(QMOE_FULL_MASK, e, (lane % PER) * LANES);
+            if (lane / PER == i0 + i) e_mine = of;
+        }
+    }
+    qmoe_tc::fence_async_shared();
+    arrive_warp(&sh.q_full[x]);
+    // not 0, so that a masked score's -inf stays one
+    return fmaxf(fabsf(a.scale) * 1.4426950408889634f * pow2i(e_mine - 14), 1.2e-38f);
+}
+
+// 64 bytes of each of a warp's 32 rows to where the rows go (dst: the thread's own row's place, or NULL), four lanes a row.
+__device__ __forceinline__ void rows_out(unsigned char* stage, const uint4 (&v)[4], unsigned char* dst) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *(uint4*)(stage + lane * 80 + 16 * j) = v[j];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        unsigned char* to = (unsigned char*)__shfl_sync(QMOE_FULL_MASK, (unsigned long long)dst, r);
+        const uint4 x = *(const uint4*)(stage + r * 80 + (lane & 3) * 16);
+        if (to) *(uint4*)(to + (lane & 3) * 16) = x;
+    }
+    __syncwarp();
 }
 
 template <int D>
@@ -1175,38 +1225,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
         const uint32_t ts = tmem + x * 128 + lanes, to = tmem + 256 + x * 128 + lanes;
         uint32_t n_s = 0;                                            // steps done (the step barriers take turns)
         int tiles = 0;                                               // tiles of the run before the item
-        uint4 raw[D / 8];                                            // this thread's query row
+        float factor = 0.f;                                          // of the item's scores, in log2 units
         bool more = next_item(a, plan, n_pairs, c, true, ahead);
-        if (more) load_row<D>(a, c, x, row, raw);
+        if (more) factor = put_rows<D>(a, c, x, sh);
         while (more) {
             const int t_s = c.s[x], t_e = c.e[x], t0 = c.t0, lo = c.w.lo;
             const bool whole = c.whole, some = t_e > t_s;
             const int r = c.w.rb * kRows + x * 128 + row;
-            const bool live = r < c.w.q_len * a.group;
             const int n = r / a.group;
             const int64_t base = row_at<D>(a, c, r);
-            float factor = 0.f, m = kNoMax, l = 0.f;
-            if (some) {
-                // the row into the tile, its largest magnitude scaled to [2^14, 2^15)
-                float mx = 0.f;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    mx = fmaxf(mx, fmaxf(fmaxf(fabsf(bf16_lo(raw[i].x)), fabsf(bf16_hi(raw[i].x))), fmaxf(fabsf(bf16_lo(raw[i].y)), fabsf(bf16_hi(raw[i].y)))));
-                    mx = fmaxf(mx, fmaxf(fmaxf(fabsf(bf16_lo(raw[i].z)), fabsf(bf16_hi(raw[i].z))), fmaxf(fabsf(bf16_lo(raw[i].w)), fabsf(bf16_hi(raw[i].w)))));
-                }
-                const int e = mx > 0.f ? min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 126) : 0;
-                const float up = a.scale < 0.f ? -pow2i(14 - e) : pow2i(14 - e);
-                // not 0, so that a masked score's -inf stays one
-                factor = fmaxf(fabsf(a.scale) * 1.4426950408889634f * pow2i(e - 14), 1.2e-38f);
-                unsigned char* dst = sh.q[x] + row * 128;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i)
-                    *(uint4*)(dst + (i >> 3) * Sh::kQAtom + (((i & 7) ^ (row & 7)) << 4)) =
-                        make_uint4(half2_bits(bf16_lo(raw[i].x) * up, bf16_hi(raw[i].x) * up), half2_bits(bf16_lo(raw[i].y) * up, bf16_hi(raw[i].y) * up),
-                                   half2_bits(bf16_lo(raw[i].z) * up, bf16_hi(raw[i].z) * up), half2_bits(bf16_lo(raw[i].w) * up, bf16_hi(raw[i].w) * up));
-                qmoe_tc::fence_async_shared();
-                arrive_warp(&sh.q_full[x]);
-            }
+            const bool live = base >= 0;
+            float m = kNoMax, l = 0.f;
             const int first = a.causal ? c.w.kv_len - c.w.q_len : c.w.kv_len - 1;
             const int pos = a.causal ? first + n : first;
             const int k_hi = min(pos, c.w.kv_len - 1), k_lo = a.window ? pos - a.window + 1 : 0;    // keys seen: [k_lo, k_hi]
@@ -1283,14 +1312,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
             }
             if (!ok) break;
             tiles += c.t1 - t0;
-            // the next item's row is on its way while this one's sums are written
+            // the next item's rows go into place first (this item's scores are done with them), so that its first products
+            // run while this one's sums are written
             more = next_item(a, plan, n_pairs, c, false, ahead);
-            if (more) load_row<D>(a, c, x, row, raw);
-            if (some) {
-                ok = tile_wait(&sh.o_full[x][(n_s - 1) & 1], ((n_s - 1) >> 1) & 1);
-                if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
-                qmoe_tc::tc_fence_after();
-            }
+            if (more) factor = put_rows<D>(a, c, x, sh);
+            if (some) ok = tile_wait(&sh.o_full[x][(n_s - 1) & 1], ((n_s - 1) >> 1) & 1);
+            if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
+            qmoe_tc::tc_fence_after();
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
             float* part = part_of(parts, blockIdx.x, t0 == 0 ? 1 : 0, kRows, D) + (size_t)(x * 128 + row) * D;
 #pragma unroll 1
@@ -1302,21 +1330,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                     tmem_load32(to + i, orr);
                     tmem_wait_load(orr);
                 }
-                if (live && whole) {
-                    uint4* dst = (uint4*)(a.out + base + i);
+                uint4 v[4];
+                if (whole) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint32_t w[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(orr[8 * j + 2 * k]) * inv, __uint_as_float(orr[8 * j + 2 * k + 1]) * inv);
-                            w[k] = *(const uint32_t*)&v;
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(orr[8 * j + 2 * k]) * inv, __uint_as_float(orr[8 * j + 2 * k + 1]) * inv);
+                            w[k] = *(const uint32_t*)&b2;
                         }
-                        dst[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                        v[j] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                } else if (live) {
+                    rows_out(sh.rows[warp], v, live ? (unsigned char*)(a.out + base + i) : nullptr);
+                } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) *(uint4*)(part + i + 4 * j) = make_uint4(orr[4 * j], orr[4 * j + 1], orr[4 * j + 2], orr[4 * j + 3]);
+                    for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] = make_uint4(orr[16 * hf + 4 * j], orr[16 * hf + 4 * j + 1], orr[16 * hf + 4 * j + 2], orr[16 * hf + 4 * j + 3]);
+                        rows_out(sh.rows[warp], v, live ? (unsigned char*)(part + i + 16 * hf) : nullptr);
+                    }
                 }
             }
             if (live && !whole)
