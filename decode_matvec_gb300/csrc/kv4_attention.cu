@@ -213,7 +213,7 @@ __device__ __forceinline__ void depend_wait() { asm volatile("griddepcontrol.wai
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
-    decode_kernel(AttnArgs a, int max_rows, SplitItem* items, float* parts) {
+    decode_kernel(AttnArgs a, int max_rows, int direct, SplitItem* items, float* parts) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     DecodeShared<D, NT>& sh = *(DecodeShared<D, NT>*)smem_raw;
     constexpr int W = D / 32;              // words of a key row that a lane reads
@@ -226,12 +226,25 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
         }
         qmoe_tc::fence_mbar_init();
     }
-    long long chunk;
-    const Found f = scan_requests<kDecodeThreads>(a, max_rows, &chunk);
+    long long chunk = 1, u0, u1;
+    Found f;
     depend_launch();
-    const long long u0 = (long long)blockIdx.x * chunk, u1 = min(u0 + chunk, f.total);
-    if (tid == 32 * kConsumers) items[blockIdx.x] = SplitItem{0, 0, 0, -1};
-    if (u0 >= u1) return;
+    if (direct) {
+        // a block an item: few tiles each, and nothing to join
+        f.b = blockIdx.x / a.cache.n_kv_heads;
+        int t0;
+        const int n = tiles_of(a, f.b, max_rows, &t0, blockIdx.x == f.b * a.cache.n_kv_heads);
+        if (n == 0) return;
+        f.before = 0;
+        u0 = (long long)(blockIdx.x - f.b * a.cache.n_kv_heads) * (n + kItemCost);
+        u1 = u0 + n;
+        __syncthreads();
+    } else {
+        f = scan_requests<kDecodeThreads>(a, max_rows, &chunk);
+        u0 = (long long)blockIdx.x * chunk, u1 = min(u0 + chunk, f.total);
+        if (tid == 32 * kConsumers) items[blockIdx.x] = SplitItem{0, 0, 0, -1};
+        if (u0 >= u1) return;
+    }
 
     if (warp == kConsumers) {
         // ---- producer: a warp, lane i copies the tile's i-th page; 32 entries of the block table are read at a time
@@ -644,7 +657,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
 // Joins the parts of items that several blocks shared: block (c, slice) those of the item that block c began and left
 // unfinished.  Its parts are slot 1 of block c and slot 0 of blocks c + 1 .. rec.last; a group of head_dim / 4 lanes
 // adds up a row's parts, or every group some of them where there are many.
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, const SplitItem* items, const float* parts, int part_rows) {
@@ -1569,12 +1582,6 @@ int decode_rows(int group, int max_q) {
 // Blocks of the few-row path that are on the device together.
 size_t decode_fit(int rows) { return (size_t)qmoe::sm_count() * (rows <= 16 ? 3 : 2); }
 
-// Blocks of the few-row path: as many as fit on the device, no more than tiles.
-long long decode_blocks(int rows, int B, int n_kv_heads, int max_kv) {
-    const long long fit = (long long)decode_fit(rows);
-    return std::min(fit, (long long)B * n_kv_heads * std::max(1, (max_kv + kTile - 1) / kTile));
-}
-
 size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 // Workspace of the few-row path: a record for each block, then the blocks' parts.
@@ -1588,10 +1595,18 @@ int launch_decode(const AttnArgs& a, void* ws, cudaStream_t st) {
     const int smem = (int)sizeof(DecodeShared<D, NT>);
     int rc = qmoe::smem_attr((const void*)decode_kernel<D, NT>, smem, "attention attr");
     if (rc) return rc;
-    const unsigned blocks = (unsigned)decode_blocks(rows, a.B, a.cache.n_kv_heads, a.max_kv);
+    const long long n_items = (long long)a.B * a.cache.n_kv_heads;
+    const int tiles = a.window ? std::min((a.max_kv + kTile - 1) / kTile, (a.window + a.max_q + kTile - 1) / kTile + 1) : (a.max_kv + kTile - 1) / kTile;
+    // Four tiles take a block about 3 us (16 heads, 511 tokens: 7 us a call from the host); spread over blocks they would
+    // take one, but need the second kernel (10 us).
+    if (tiles <= 4 && n_items <= (long long)decode_fit(rows)) {
+        decode_kernel<D, NT><<<(unsigned)n_items, kDecodeThreads, smem, st>>>(a, rows, 1, nullptr, nullptr);
+        return qmoe::launch_check("decode_kernel");
+    }
+    const unsigned blocks = (unsigned)std::min((long long)decode_fit(rows), n_items * std::max(1, tiles));
     SplitItem* items = (SplitItem*)ws;
     float* parts = (float*)((char*)ws + align256(decode_fit(rows) * sizeof(SplitItem)));
-    decode_kernel<D, NT><<<blocks, kDecodeThreads, smem, st>>>(a, rows, items, parts);
+    decode_kernel<D, NT><<<blocks, kDecodeThreads, smem, st>>>(a, rows, 0, items, parts);
     if ((rc = qmoe::launch_check("decode_kernel"))) return rc;
     return kv4::launch_dependent(join_kernel<D>, dim3(blocks, NT == 1 ? 8 : 16), kJoinThreads, 0, st, "join_kernel", a, items, parts, rows);
 }
