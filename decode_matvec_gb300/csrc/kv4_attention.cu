@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
 // Joins the parts of items that several blocks shared: block (c, slice) those of the item that block c began and left
 // unfinished.  Its parts are slot 1 of block c and slot 0 of blocks c + 1 .. rec.last; a group of head_dim / 4 lanes
 // adds up a row's parts, or every group some of them where there are many.
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, const SplitItem* items, const float* parts, int part_rows) {
@@ -1648,7 +1648,7 @@ int launch_tiles(const AttnArgs& a, const TileWs& w, int min_rows, cudaStream_t 
         rc = kv4::launch_dependent(tile_plan_kernel, dim3(1), kPlanTile, 0, st, "tile_plan_kernel", a, w.plan, min_rows);
     if (rc || (rc = qmoe::launch_check("tile_plan_kernel"))) return rc;
     if ((rc = kv4::launch_dependent(tile_kernel<D>, dim3(blocks), kTileThreads, smem, st, "tile_kernel", a, w.plan, w.parts))) return rc;
-    return kv4::launch_dependent(join_kernel<D>, dim3(blocks, 32), kJoinThreads, 0, st, "join_kernel", a, w.plan.items, w.parts, kRows);
+    return kv4::launch_dependent(join_kernel<D>, dim3(blocks, 16), kJoinThreads, 0, st, "join_kernel", a, w.plan.items, w.parts, kRows);
 }
 
 // Whether some request of the batch has more rows than the few-row path takes.

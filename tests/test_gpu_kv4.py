@@ -438,3 +438,126 @@ def test_refusals():
     with pytest.raises(ValueError):
         Q.Kv4Cache(torch.zeros((2, 7), dtype=torch.uint8, device="cuda"), 16, 1, 64)
     ok()
+
+
+# ------------------------------------------------------------------ more of attention's edges
+@pytest.mark.parametrize("B,kv_hi,ql,hq,hkv,D,P,window", [
+    (300, 200, 1, 4, 2, 64, 16, 0),        # more items than blocks, a few tokens each
+    (40, 700, 1, 4, 4, 128, 16, 130),      # window shorter than the contexts
+    (9, 900, 6, 4, 1, 128, 32, 0),         # 24 rows
+    (9, 500, 8, 4, 1, 64, 64, 70),         # 32 rows
+    (2, 5000, 1, 2, 1, 128, 64, 0)])       # one item over many blocks
+def test_attention_few_rows_many_shapes(B, kv_hi, ql, hq, hkv, D, P, window):
+    r = np.random.RandomState(B + kv_hi)
+    kv = r.randint(0, kv_hi + 1, B).tolist()
+    kv[0] = kv_hi
+    lens = [ql] + r.randint(0, ql + 1, B - 1).tolist()
+    pages, table, ks, vs, q, qs = make_batch(r, kv, lens, hq, hkv, D, P)
+    out = attend(pages, table, q, qs, kv, hq, hkv, D, P, D ** -0.5, True, window)
+    ok()
+    ref, spread = K.attention(synth.bf16_to_f64(q), qs, ks, vs, D ** -0.5, True, window)
+    check(out, ref, spread)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.125, 1.0])
+@pytest.mark.parametrize("ql", [[1, 2], [70, 50]])
+def test_attention_scale_of_any_sign(scale, ql):
+    kv, hq, hkv, D, P = [140, 60], 4, 2, 64, 16
+    r = np.random.RandomState(21)
+    pages, table, ks, vs, q, qs = make_batch(r, kv, ql, hq, hkv, D, P)
+    out = attend(pages, table, q, qs, kv, hq, hkv, D, P, scale)
+    ok()
+    ref, spread = K.attention(synth.bf16_to_f64(q), qs, ks, vs, scale)
+    spread[..., 0] = abs(scale) * K.attention(synth.bf16_to_f64(q), qs, ks, vs, 1.0)[1][..., 0]
+    check(out, ref, spread, norm=False)
+
+
+@pytest.mark.parametrize("ql", [[3], [60]])
+def test_attention_keeps_a_bad_query_to_itself(ql):
+    kv, hq, hkv, D, P = [200], 2, 1, 128, 16
+    r = np.random.RandomState(22)
+    pages, table, ks, vs, q, qs = make_batch(r, kv, ql, hq, hkv, D, P)
+    good = attend(pages, table, q, qs, kv, hq, hkv, D, P, 0.1)
+    bad = q.copy()
+    bad[1, 0, 5], bad[2, 1, 7] = 0x7FC0, 0x7F80                   # NaN, infinity
+    out = attend(pages, table, bad, qs, kv, hq, hkv, D, P, 0.1)
+    same = np.ones(good.shape[:2], bool)
+    same[1, 0] = same[2, 1] = False
+    assert np.isfinite(out[same]).all() and np.isnan(out[1, 0]).all()
+    assert np.abs(out[same] - good[same]).max() <= UBF * np.abs(good).max()      # (a neighbour may rescale at another time)
+
+
+def test_attention_tiles_skip_a_bad_page():
+    kv, ql, hq, hkv, D, P = [300], [80], 2, 1, 64, 16
+    r = np.random.RandomState(23)
+    pages, table, ks, vs, q, qs = make_batch(r, kv, ql, hq, hkv, D, P)
+    bad = table.copy()
+    bad[0, 4] = -7
+    out = attend(pages, bad, q, qs, kv, hq, hkv, D, P, 0.125)
+    assert Q.qmoe_check_status() == Q.QMOE_EINVAL
+    keep = np.r_[0:64, 80:300]
+    ref, spread = np.zeros_like(out), np.zeros(out.shape[:2] + (2,))
+    qf = synth.bf16_to_f64(q)
+    for i in range(80):
+        n = int((keep <= 220 + i).sum())
+        o, s = K.attention(qf[i:i + 1], [0, 1], [ks[0][:, keep[:n]]], [vs[0][:, keep[:n]]], 0.125)
+        ref[i], spread[i] = o[0], s[0]
+    check(out, ref, spread)
+
+
+def test_calls_replay_from_a_graph():
+    """A decode step captured once and replayed as the sequence grows: lengths, pages and the cache live on the device."""
+    B, hq, hkv, D, P, steps = 3, 4, 2, 64, 16, 20
+    r = np.random.RandomState(24)
+    start = np.array([14, 0, 31])
+    cap = start + steps
+    blocks = -(-cap // P)
+    cache = Q.Kv4Cache.empty(int(blocks.sum()), P, hkv, D)
+    table = np.full((B, int(blocks.max())), -1, np.int64)
+    perm = r.permutation(cache.n_pages)
+    have = -(-start // P)
+    at = np.concatenate([[0], np.cumsum(have)])
+    for b in range(B):
+        table[b, :have[b]] = perm[at[b]:at[b + 1]]
+    table_d, lens, one, nf = ints(table), ints(start), ints(np.ones(B)), ints([cache.n_pages - at[-1]])
+    free = ints(perm[at[-1]:])
+    qs, kl, sl, po = ints(np.zeros(B + 1)), ints(np.zeros(B)), ints(np.zeros(B)), ints(np.zeros(B))
+    hist = r.randn(int(start.sum()), 2, hkv, D)
+    slots = np.concatenate([table[b][np.arange(start[b]) // P] * P + np.arange(start[b]) % P for b in range(B)])
+    ht = bf16_tensor(bits(hist).reshape(len(hist), -1)).view(-1, 2, hkv, D)
+    Q.kv4_append(cache, ht[:, 0], ht[:, 1], ints(slots))
+    k_all = [list(x) for x in np.split(K.bf16_round(hist), np.cumsum(start)[:-1])]
+    x = torch.zeros((B, (hq + 2 * hkv) * D), dtype=torch.bfloat16, device="cuda")
+    q, out = (torch.zeros((B, hq, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    mk = int(cap.max())
+    ws = torch.empty(Q.kv4_attention_ws_size(B, hq, hkv, D, B, 1, mk) + 1, dtype=torch.uint8, device="cuda")
+
+    def step():
+        Q.kv4_block_tables(lens, one, free, nf, P, table_d, qs, kl, sl, po, nf)
+        Q.qk_norm_rope(x, hq, hkv, D, None, None, 0.0, None, None, q, None, cache=cache, slots=sl)
+        Q.kv4_attention(cache, q, qs, kl, table_d, out, ws, 1, mk, D ** -0.5)
+        lens.copy_(kl)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(g, stream=side):
+            step()
+    for i in range(steps):
+        xs = bits(r.randn(B, hq + 2 * hkv, D))
+        x.copy_(bf16_tensor(xs.reshape(B, -1)).view(torch.bfloat16))
+        g.replay()
+        xf = synth.bf16_to_f64(xs)
+        ks, vs = [], []
+        for b in range(B):
+            k_all[b].append(np.stack([xf[b, hq:hq + hkv], xf[b, hq + hkv:]]))
+            u, s, z = K.quantise(np.array(k_all[b]))
+            d = K.dequantise(u, s, z)
+            ks.append(d[:, 0].transpose(1, 0, 2))
+            vs.append(d[:, 1].transpose(1, 0, 2))
+        if i % 6 == 5 or i == steps - 1:
+            ref, spread = K.attention(xf[:, :hq], [0, 1, 2, 3], ks, vs, D ** -0.5)
+            check(out.double().cpu().numpy(), ref, spread)
+    ok()
+    assert lens.cpu().numpy().tolist() == cap.tolist()
