@@ -61,6 +61,11 @@ __device__ __forceinline__ bool request(const AttnArgs& a, int b, int* q0, int* 
 // head (contiguous in the layout) into a ring of stages with bulk copies; four warps take 32 tokens of
 // a tile each.  An item that several blocks share leaves its parts (unnormalised sums, maximum, sum of
 // weights) in the workspace for join_kernel.
+//
+// Measured (one GB300): 64 requests of 1 to 16384 tokens, 32 query heads on 8 key heads of 128, 105 us =
+// 5.5 TB/s of codes and pairs, 81 % of the copy rate.  What it took: 32 tokens a warp and stage
+// instead of 16 (141 -> 127 us: fewer instructions beside the products), three stages and blocks a
+// multiprocessor instead of two and four (120), runs that count an item's beginning and end (105).
 constexpr int kTile = 128;
 constexpr int kItemCost = 3;                         // what beginning and ending an item costs, in tiles
 constexpr int kStages = 3;
@@ -182,12 +187,13 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
 struct StageInfo {
     int b, kh, tile, flags;
 };
-constexpr int kFirst = 1, kLast = 2, kWholeStart = 4, kWholeEnd = 8, kEdge = 16, kEnd = 32, kValid = 64;   // kValid << page of the tile; kEdge: some row does not see all of it;
-                                                                                                   // kEnd: nothing, the run is over
+constexpr int kFirst = 1, kLast = 2, kWholeStart = 4, kWholeEnd = 8, kEdge = 16, kEnd = 32, kValid = 64;
+// kWholeStart, kWholeEnd: the item begins, ends in this run; kEdge: some row does not see all of the tile; kEnd: the run is
+// over; kValid << page of the tile: the page is there
 
 template <int D, int NT>
 struct DecodeShared {
-    // query operand of 16 or 32 rows (with 8 it is held in registers); every warp writes the same values
+    // query operand of 16 to 32 rows (with 8 it is held in registers); every warp writes the same values
     alignas(16) uint2 qf[NT == 1 ? 1 : NT][D / 32][2][32];
     alignas(128) unsigned char stage[kStages][kTile * (D + 8)];
     alignas(16) float red[kConsumers][8][D + 4];
@@ -727,10 +733,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, const Sp
 // bf16 magnitude is inside fp16's range.  The running maximum moves, and O is rescaled, only when a
 // row's weights by it pass 2^14; P carries 2^6, so that small weights stay above fp16's subnormals.
 //
+// Measured: 2048 query tokens behind 30011 cached ones, 32 query heads on 4 key heads of 128, 840 us = 1.24
+// PFLOP/s, 66 % of cuBLAS's bf16 rate.  Leaving parts out in turn (no expansion -12 %, no exponentials -2 %,
+// one product of eight -5 %) shows no single limit: the four roles share the schedulers' issue slots (59 %
+// used) and the instruction caches, which is why every loop is short.  A 64-key step has two score buffers a
+// tile of rows, so that a softmax finds its next scores ready; with 128-key steps and one buffer 951 us.
+//
 // Roles, one block per SM: 2 x 4 softmax warps (a thread per row), 4 warps that expand keys and values,
-// one warp that issues the products, one that copies pages.  What bounds it: at 256 rows the tensor
-// core needs about 2070 cycles for 128 keys (head_dim 128), shared memory about as many (the Q K^T
-// operands alone 1030), the softmax warps about 900 issue slots a scheduler and the expansion 550.
+// a warp for each tile of rows that issues its products, one that copies pages.  For 128 keys at 256 rows
+// and head_dim 128 the tensor core needs about 2500 cycles (its 64-column products run at 45 cycles instead
+// of 32), the exponentials 1030 of a scheduler's; a step of the walk takes 3900.
 //
 // Work is dealt out as in the few-row path: all (rows, kv head) items' key tiles in a row, in equal
 // runs; items that several blocks share are joined by join_kernel.
@@ -1705,7 +1717,8 @@ extern "C" int kv4_attention(const kv4_cache* cache, const void* q, int n_q_toke
     if (!kv4::aligned16(q) || !kv4::aligned16(out)) return qmoe::fail(QMOE_EINVAL, "kv4_attention: pointer not 16-byte aligned");
     a.q = (const uint16_t*)q, a.out = (uint16_t*)out, a.q_start = q_start, a.kv_len = kv_len, a.table = table;
     a.B = B, a.n_q_tokens = n_q_tokens, a.n_q_heads = n_q_heads, a.group = n_q_heads / cache->n_kv_heads;
-    a.max_blocks = max_blocks, a.max_q = max_q, a.max_kv = max_kv, a.scale = scale, a.causal = causal ? 1 : 0, a.window = window;
+    a.max_blocks = max_blocks, a.max_q = max_q, a.max_kv = max_kv, a.scale = scale, a.causal = causal ? 1 : 0;
+    a.window = window >= max_kv ? 0 : window;      // as long as any request: it hides nothing
     cudaStream_t st = (cudaStream_t)stream;
     const int rows = decode_rows(a.group, max_q), D = cache->head_dim;
     const bool tiles = has_tiles(a.group, max_q, rows);

@@ -1,7 +1,11 @@
 // What feeds attention over the 4-bit paged key/value cache: block tables and
 // slot maps, the norms and the rotation of queries and keys, and the cache's
-// writer and reader.  All are bound by memory (or, for a few tokens, by the
-// latency of a launch and one dependent chain of loads).
+// writer and reader.  For a few tokens all are bound by a launch and one
+// dependent chain of loads (2 to 4 us in a graph); for many the norm and the
+// writer by instruction issue, the reader by memory.  Measured (one GB300):
+// norm and rotation of 16383 tokens, 32 + 8 heads of 128, 72 us (4.8 TB/s of
+// 6.8); writing 16384 tokens of 16 heads of 128 59 us, reading them back 30;
+// tables, slots and positions of 257 requests with 260 thousand new tokens 9.5 us.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
