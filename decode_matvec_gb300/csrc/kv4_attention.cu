@@ -1015,6 +1015,7 @@ __device__ __forceinline__ void tmem_load64(uint32_t taddr, uint32_t (&r)[64]) {
 
 // Scores of 64 keys outside [lo, hi], or in a group of 16 whose bit of `groups` is clear, become -inf.
 __device__ __forceinline__ void mask64(uint32_t* s, int lo, int hi, uint32_t groups) {
+    asm volatile("" : "+r"(lo), "+r"(hi), "+r"(groups));      // nothing of this is made ahead of the branch to it
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int l = lo - 32 * h, u = hi - 32 * h;
@@ -1108,9 +1109,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t a_off, u
 
 // Four registers of a word of codes, (value 8w + 2i, value 8w + 2i + 1) each, as the integers 0..15 in fp16: 1024 + u
 // (1024 + 16 u one nibble up) is an or into fp16's pattern of 1024, and taking the 1024 off is exact.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
+    uint32_t d;      // one instruction; the compiler makes two of the same in C
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(bits));
+    return d;
+}
+
 __device__ __forceinline__ void code_integers(uint32_t w, __half2 (&u)[4]) {
-    const uint32_t x[4] = {(w & 0x000F000Fu) | 0x64006400u, (w & 0x00F000F0u) | 0x64006400u, ((w >> 8) & 0x000F000Fu) | 0x64006400u,
-                           ((w >> 8) & 0x00F000F0u) | 0x64006400u};
+    const uint32_t h = w >> 8, magic = 0x64006400u;
+    const uint32_t x[4] = {and_or(w, 0x000F000Fu, magic), and_or(w, 0x00F000F0u, magic), and_or(h, 0x000F000Fu, magic),
+                           and_or(h, 0x00F000F0u, magic)};
     const __half2 one = __float2half2_rn(1024.f), off = __float2half2_rn(-64.f), sixteenth = __float2half2_rn(0.0625f);
     u[0] = __hsub2(*(const __half2*)&x[0], one);
     u[1] = __hfma2(*(const __half2*)&x[1], sixteenth, off);
@@ -1273,7 +1281,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                 qmoe_tc::tc_fence_after();
                 const int j0 = lo * kKeys + t * kStep;
                 const uint32_t valid = sh.valid[(tiles + (t >> 1) - t0) % kInfo] >> (4 * (t & 1)) & 15u;
-                const bool edge = j0 + kStep - 1 > k_hi || j0 < k_lo || valid != 15u;
+                // (by a vote, so that it is a branch: predicated, the 64 tests would be issued in every step)
+                const bool edge = __any_sync(QMOE_FULL_MASK, j0 + kStep - 1 > k_hi || j0 < k_lo || valid != 15u);
                 // The weights are taken with the maximum as it stands; only when a row's sum shows that it has grown too
                 // far (or there is none yet) the scores are read again, for their maximum and for the weights by it.
                 uint32_t sr[kStep];
@@ -1421,13 +1430,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                         const int ch = (c0 + s) & (CH - 1);
                         const uint4 w4 = *(const uint4*)(raw + k_row + ch * 16);
                         const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+                        // piece 4 ch + k of the row, at place (4 (ch & 1) + k) ^ (row % 8): the k only flips bits of the address
+                        const uint32_t at = (ch >> 1) * Sh::kQAtom + (((4 * (ch & 1)) ^ (i & 7)) << 4);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             __half2 u[4];
                             code_integers(w[k], u);
-                            const int piece = 4 * ch + k;
-                            *(uint4*)(dst + (piece >> 3) * Sh::kQAtom + (((piece & 7) ^ (i & 7)) << 4)) = make_uint4(h2(__hfma2(u[0], s2, z2)), h2(__hfma2(u[1], s2, z2)),
-                                                                            h2(__hfma2(u[2], s2, z2)), h2(__hfma2(u[3], s2, z2)));
+                            *(uint4*)(dst + (at ^ (k << 4))) = make_uint4(h2(__hfma2(u[0], s2, z2)), h2(__hfma2(u[1], s2, z2)),
+                                                                        h2(__hfma2(u[2], s2, z2)), h2(__hfma2(u[3], s2, z2)));
                         }
                     }
                 }
@@ -1438,13 +1448,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
                 if (!(ok = __all_sync(QMOE_FULL_MASK, ok))) break;
                 {
                     __half2 s2[4], z2[4];
+                    uint32_t pr[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) pr[k] = *(const uint32_t*)(raw + v_pair + (k ^ swap) * 4);
+                    if (__builtin_expect(j0 + kKeys > c.w.kv_len || valid != 0xFFu, 0)) {
+                        const bool page_ok = (valid >> (o >> 1)) & 1;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (!page_ok || j0 + 8 * o + (k ^ swap) >= c.w.kv_len) pr[k] = 0;
+                    }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        uint32_t a0 = *(const uint32_t*)(raw + v_pair + ((2 * k) ^ swap) * 4), a1 = *(const uint32_t*)(raw + v_pair + ((2 * k + 1) ^ swap) * 4);
-                        const bool page_ok = (valid >> (o >> 1)) & 1;
-                        if (!page_ok || j0 + 8 * o + ((2 * k) ^ swap) >= c.w.kv_len) a0 = 0;
-                        if (!page_ok || j0 + 8 * o + ((2 * k + 1) ^ swap) >= c.w.kv_len) a1 = 0;
-                        const uint32_t ss = __byte_perm(a0, a1, 0x5410), zz = __byte_perm(a0, a1, 0x7632);
+                        const uint32_t ss = __byte_perm(pr[2 * k], pr[2 * k + 1], 0x5410), zz = __byte_perm(pr[2 * k], pr[2 * k + 1], 0x7632);
                         s2[k] = *(const __half2*)&ss, z2[k] = *(const __half2*)&zz;
                     }
                     unsigned char* dst0 = sh.kv[buf] + (o >> 3) * Sh::kVAtom;
