@@ -487,7 +487,8 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
                             s[j][nt][2 * r + i] = fmaf(c1[nt][i], sk[r] * s[j][nt][2 * r + i], cz[nt][i] * zk[r]);
                 // ---- tokens that some row does not see
                 if (__builtin_expect(in.flags & kEdge, 0)) {
-                    const int first = a.causal ? kv_len - q_len : kv_len - 1;
+                    int first = a.causal ? kv_len - q_len : kv_len - 1;
+                    asm volatile("" : "+r"(first));      // nothing of this is made ahead of the branch to it
                     const bool page_ok = (in.flags / kValid >> ((tok0 + 16 * (half + j)) >> a.cache.page_shift)) & 1;
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
