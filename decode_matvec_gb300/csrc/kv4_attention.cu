@@ -62,8 +62,8 @@ __device__ __forceinline__ bool request(const AttnArgs& a, int b, int* q0, int* 
 // a tile each.  An item that several blocks share leaves its parts (unnormalised sums, maximum, sum of
 // weights) in the workspace for join_kernel.
 //
-// Measured (one GB300): 64 requests of 1 to 16384 tokens, 32 query heads on 8 key heads of 128, 105 us =
-// 5.5 TB/s of codes and pairs, 81 % of the copy rate.  What it took: 32 tokens a warp and stage
+// Measured (one GB300): 64 requests of 1 to 16384 tokens, 32 query heads on 8 key heads of 128, 104 us =
+// 5.5 TB/s of codes and pairs, 82 % of the copy rate.  What it took: 32 tokens a warp and stage
 // instead of 16 (141 -> 127 us: fewer instructions beside the products), three stages and blocks a
 // multiprocessor instead of two and four (120), runs that count an item's beginning and end (105).
 constexpr int kTile = 128;
@@ -734,16 +734,16 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, const Sp
 // bf16 magnitude is inside fp16's range.  The running maximum moves, and O is rescaled, only when a
 // row's weights by it pass 2^14; P carries 2^6, so that small weights stay above fp16's subnormals.
 //
-// Measured: 2048 query tokens behind 30011 cached ones, 32 query heads on 4 key heads of 128, 840 us = 1.24
-// PFLOP/s, 66 % of cuBLAS's bf16 rate.  Leaving parts out in turn (no expansion -12 %, no exponentials -2 %,
-// one product of eight -5 %) shows no single limit: the four roles share the schedulers' issue slots (59 %
-// used) and the instruction caches, which is why every loop is short.  A 64-key step has two score buffers a
-// tile of rows, so that a softmax finds its next scores ready; with 128-key steps and one buffer 951 us.
+// Measured: 2048 query tokens behind 30011 cached ones, 32 query heads on 4 key heads of 128, 730 us = 1.43
+// PFLOP/s, 76 % of cuBLAS's bf16 rate.  Leaving parts out in turn (no exponentials -5 %, one product of
+// eight -1 %) shows no single limit: the four roles share the schedulers' issue slots (about 60 % used) and
+// the instruction caches, which is why every loop is short.  A 64-key step has two score buffers a tile of
+// rows, so that a softmax finds its next scores ready (128-key steps with one buffer: 951 us then, 895 with).
 //
 // Roles, one block per SM: 2 x 4 softmax warps (a thread per row), 4 warps that expand keys and values,
 // a warp for each tile of rows that issues its products, one that copies pages.  For 128 keys at 256 rows
 // and head_dim 128 the tensor core needs about 2500 cycles (its 64-column products run at 45 cycles instead
-// of 32), the exponentials 1030 of a scheduler's; a step of the walk takes 3900.
+// of 32), the exponentials 1030 of a scheduler's; the walk takes 3400.
 //
 // Work is dealt out as in the few-row path: all (rows, kv head) items' key tiles in a row, in equal
 // runs; items that several blocks share are joined by join_kernel.
