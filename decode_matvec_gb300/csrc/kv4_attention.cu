@@ -199,7 +199,7 @@ struct DecodeShared {
     alignas(16) float red[kConsumers][8][D + 4];
     float m[kConsumers][8], l[kConsumers][8];
     StageInfo info[kStages];
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kStages], empty[kStages], joint;
 };
 
 // fp32 parts of split items: slot 2 * block for an item that began before the block's run, 2 * block + 1
@@ -217,6 +217,16 @@ struct SplitItem {
 __device__ __forceinline__ void depend_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void depend_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The computing warps wait for each other; false (and reported) when one of them has given up.
+__device__ __forceinline__ bool meet(uint64_t* bar, uint32_t& met) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+    const bool ok = qmoe_tc::mbar_wait(bar, met & 1, kWaitLimit);
+    ++met;
+    if (!ok) attn_set_error(QMOE_ETIMEOUT);
+    return ok;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
     decode_kernel(AttnArgs a, int max_rows, int direct, SplitItem* items, float* parts) {
@@ -230,6 +240,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
             qmoe_tc::mbar_init(&sh.full[i], 1);
             qmoe_tc::mbar_init(&sh.empty[i], kConsumers);
         }
+        qmoe_tc::mbar_init(&sh.joint, kConsumers);
         qmoe_tc::fence_mbar_init();
     }
     long long chunk = 1, u0, u1;
@@ -357,6 +368,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
     float c1[NT][2], cz[NT][2];    // per row: factor of s (q . u), and factor times sum(q), in log2 units
     float m[NT][2], l[NT][2], pz[NT][2];
     float o[NT][4 * VW][4];
+    uint32_t met = 0;              // times the computing warps have met
     float vs = 1.f, vlim = 1e-9f;  // probabilities carry vs (a power of two); a value scale >= vlim moves it
     int q0 = 0, q_len = 0, kv_len = 0;
 
@@ -625,7 +637,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
                             make_float2(fmaf(o[nt][x][i], un, ps), fmaf(o[nt][x][2 + i], un, ps));
                     }
                 }
-                asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
+                if (!meet(&sh.joint, met)) return;
                 {
                     const int row = tid >> 4, d0 = (tid & 15) * (D / 16), r = nt * 8 + row;
                     float mm = sh.m[0][row];
@@ -655,7 +667,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
                         }
                     }
                 }
-                asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
+                if (!meet(&sh.joint, met)) return;
             }
         }
     }
