@@ -951,6 +951,7 @@ __device__ __forceinline__ bool next_item(const AttnArgs& a, const TilePlan& p, 
                 ++c.kh;
             some = place_item(a, c, first);
         }
+        __syncwarp();      // all lanes read what lane 0 wrote (the shuffle orders no memory)
         if (__shfl_sync(QMOE_FULL_MASK, (int)some, 0)) return true;
     }
 }

@@ -1,0 +1,35 @@
+"""GPU parity of attention over the 4-bit cache where it can go wrong beside the shapes of test_gpu_kv4: long runs of short
+items, values of very different sizes, saturated scores, host-side bounds, shared pages, streams."""
+import numpy as np
+import pytest
+
+import synth
+from oracle import kv4 as K
+
+from helpers import bf16_tensor
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+Q = pytest.importorskip("decode_matvec_gb300")
+
+from test_gpu_kv4 import attend, bits, check, ints, make_batch, ok  # noqa: E402
+
+
+@pytest.mark.parametrize("B,q_hi,kv_hi,hq,hkv,D,P,window", [
+    (70, 70, 200, 32, 8, 128, 16, 0),       # several items a block, one or two tiles of keys each
+    (70, 70, 200, 32, 8, 128, 32, 40),      # the same behind a window, single tokens among them
+    (230, 9, 300, 34, 1, 64, 64, 0),        # groups that only the tiles take
+])
+def test_tiles_many_short_items(B, q_hi, kv_hi, hq, hkv, D, P, window):
+    """A block goes through several items of the tile path one after another, and takes up each where the last one ended."""
+    r = np.random.RandomState(B + D + window)
+    ql = r.randint(1, q_hi + 1, B)
+    ql[::5] = 1
+    kv = (ql + r.randint(0, kv_hi - q_hi, B)).tolist()
+    ql = ql.tolist()
+    assert sum(-(-n * (hq // hkv) // 256) for n in ql if n * (hq // hkv) > 32 or hq // hkv > 32) * hkv > 152
+    pages, table, ks, vs, q, qs = make_batch(r, kv, ql, hq, hkv, D, P)
+    out = attend(pages, table, q, qs, kv, hq, hkv, D, P, D ** -0.5, True, window)
+    ok()
+    ref, spread = K.attention(synth.bf16_to_f64(q), qs, ks, vs, D ** -0.5, True, window)
+    check(out, ref, spread)
