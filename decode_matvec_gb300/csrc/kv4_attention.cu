@@ -1621,13 +1621,17 @@ int decode_rows(int group, int max_q) {
 }
 
 // Blocks of the few-row path that are on the device together.
-size_t decode_fit(int rows) { return (size_t)qmoe::sm_count() * (rows <= 16 ? 3 : 2); }
+constexpr int kMaxFit = 3;
+size_t decode_fit(int rows) { return (size_t)qmoe::sm_count() * (rows <= 16 ? kMaxFit : 2); }
 
 size_t align256(size_t b) { return (b + 255) & ~(size_t)255; }
 
-// Workspace of the few-row path: a record for each block, then the blocks' parts.
+// Workspace of the few-row path: a record for each block (room for as many blocks as any row count has: what a longer
+// draft needs then covers a shorter one), then the blocks' parts.
+size_t decode_records() { return align256((size_t)qmoe::sm_count() * kMaxFit * sizeof(SplitItem)); }
+
 size_t decode_ws(int rows, int head_dim) {
-    return rows == 0 ? 0 : align256(decode_fit(rows) * sizeof(SplitItem)) + align256(decode_fit(rows) * 2 * rows * (head_dim + 2) * sizeof(float));
+    return rows == 0 ? 0 : decode_records() + align256(decode_fit(rows) * 2 * rows * (head_dim + 2) * sizeof(float));
 }
 
 template <int D, int NT>
@@ -1646,7 +1650,7 @@ int launch_decode(const AttnArgs& a, void* ws, cudaStream_t st) {
     }
     const unsigned blocks = (unsigned)std::min((long long)decode_fit(rows), n_items * std::max(1, tiles));
     SplitItem* items = (SplitItem*)ws;
-    float* parts = (float*)((char*)ws + align256(decode_fit(rows) * sizeof(SplitItem)));
+    float* parts = (float*)((char*)ws + decode_records());
     decode_kernel<D, NT><<<blocks, kDecodeThreads, smem, st>>>(a, rows, 0, items, parts);
     if ((rc = qmoe::launch_check("decode_kernel"))) return rc;
     return kv4::launch_dependent(join_kernel<D>, dim3(blocks, NT == 1 ? 8 : 16), kJoinThreads, 0, st, "join_kernel", a, items, parts, rows);

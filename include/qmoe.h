@@ -625,6 +625,8 @@ int kv4_gather(const kv4_cache* cache, const int32_t* slots, int n, void* k_out,
  *  max_q, max_kv  host: at least the largest q_len and kv_len.  A request
  *            that passes them is skipped (ECAPACITY in the error word).
  *  workspace device, ws_bytes >= kv4_attention_ws_size(...), 16-byte aligned.
+ *            The size does not fall when B, n_q_tokens, max_q or max_kv grow, so
+ *            one sized for a program's largest call serves its others too.
  * Scores, softmax statistics and sums are fp32.  Rows of out that belong to no
  * request are left as they are.
  * Errors: EINVAL, EUNSUPPORTED (head_dim, more than 128 query heads per kv
