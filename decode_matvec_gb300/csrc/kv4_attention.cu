@@ -1641,14 +1641,16 @@ int launch_decode(const AttnArgs& a, void* ws, cudaStream_t st) {
     int rc = qmoe::smem_attr((const void*)decode_kernel<D, NT>, smem, "attention attr");
     if (rc) return rc;
     const long long n_items = (long long)a.B * a.cache.n_kv_heads;
-    const int tiles = a.window ? std::min((a.max_kv + kTile - 1) / kTile, (a.window + a.max_q + kTile - 1) / kTile + 1) : (a.max_kv + kTile - 1) / kTile;
+    // tiles of the longest item (64 bits: the bounds may be the largest int32)
+    long long tiles = ((long long)a.max_kv + kTile - 1) / kTile;
+    if (a.window) tiles = std::min(tiles, ((long long)a.window + a.max_q + kTile - 1) / kTile + 1);
     // Four tiles take a block about 3 us (16 heads, 511 tokens: 7 us a call from the host); spread over blocks they would
     // take one, but need the second kernel (10 us).
     if (tiles <= 4 && n_items <= (long long)decode_fit(rows)) {
         decode_kernel<D, NT><<<(unsigned)n_items, kDecodeThreads, smem, st>>>(a, rows, 1, nullptr, nullptr);
         return qmoe::launch_check("decode_kernel");
     }
-    const unsigned blocks = (unsigned)std::min((long long)decode_fit(rows), n_items * std::max(1, tiles));
+    const unsigned blocks = (unsigned)std::min((long long)decode_fit(rows), n_items * std::max(1LL, tiles));
     SplitItem* items = (SplitItem*)ws;
     float* parts = (float*)((char*)ws + decode_records());
     decode_kernel<D, NT><<<blocks, kDecodeThreads, smem, st>>>(a, rows, 0, items, parts);

@@ -33,3 +33,17 @@ def test_tiles_many_short_items(B, q_hi, kv_hi, hq, hkv, D, P, window):
     ok()
     ref, spread = K.attention(synth.bf16_to_f64(q), qs, ks, vs, D ** -0.5, True, window)
     check(out, ref, spread)
+
+
+@pytest.mark.parametrize("window", [0, 2 ** 31 - 200])
+def test_bounds_at_the_end_of_int32_choose_as_any_large_bound_does(window):
+    """max_kv is a bound, not a length: one that says "no bound" gives the same blocks, hence the same bits, as one that is large."""
+    kv, ql, hq, hkv, D, P = [5000, 3000], [1, 1], 4, 2, 128, 64
+    r = np.random.RandomState(31)
+    pages, table, ks, vs, q, qs = make_batch(r, kv, ql, hq, hkv, D, P)
+    large = attend(pages, table, q, qs, kv, hq, hkv, D, P, D ** -0.5, max_kv=2 ** 31 - 128)
+    out = attend(pages, table, q, qs, kv, hq, hkv, D, P, D ** -0.5, window=window, max_kv=2 ** 31 - 1)
+    ok()
+    assert np.array_equal(out, large)
+    ref, spread = K.attention(synth.bf16_to_f64(q), qs, ks, vs, D ** -0.5)
+    check(out, ref, spread)
