@@ -24,11 +24,14 @@ struct AttnArgs {
     int causal, window;
 };
 
+// Longest request: its keys, rounded up to a tile of either path, stay in int32.
+constexpr int kMaxKv = 0x7FFFFFFF - 127;
+
 // Whether request b can be run; what is wrong with it goes to the error word.
 __device__ __forceinline__ bool request(const AttnArgs& a, int b, int* q0, int* q_len, int* kv_len, bool report) {
     const int s = a.q_start[b], e = a.q_start[b + 1], n = a.kv_len[b];
     *q0 = s, *q_len = e - s, *kv_len = n;
-    if (s < 0 || e < s || e > a.n_q_tokens || n < 0) {
+    if (s < 0 || e < s || e > a.n_q_tokens || n < 0 || n > kMaxKv) {
         if (report) attn_set_error(QMOE_EINVAL);
         return false;
     }

@@ -623,7 +623,8 @@ int kv4_gather(const kv4_cache* cache, const int32_t* slots, int n, void* k_out,
  *  q_start   device int32 [B + 1], non-decreasing within [0, n_q_tokens].
  *  kv_len    device int32 [B];  table device int32 [B][max_blocks].
  *  max_q, max_kv  host: at least the largest q_len and kv_len.  A request
- *            that passes them is skipped (ECAPACITY in the error word).
+ *            that passes them is skipped (ECAPACITY in the error word).  A
+ *            kv_len above 2^31 - 128 is out of range (EINVAL in the error word).
  *  workspace device, ws_bytes >= kv4_attention_ws_size(...), 16-byte aligned.
  *            The size does not fall when B, n_q_tokens, max_q or max_kv grow, so
  *            one sized for a program's largest call serves its others too.
@@ -632,7 +633,8 @@ int kv4_gather(const kv4_cache* cache, const int32_t* slots, int n, void* k_out,
  * Errors: EINVAL, EUNSUPPORTED (head_dim, more than 128 query heads per kv
  * head), ECAPACITY (workspace); on the device EINVAL (a page outside the
  * cache among the blocks of a request: its tokens are not seen; q_start out
- * of order or a negative kv_len: such requests are skipped).
+ * of order, or a kv_len that is negative or above 2^31 - 128: such requests
+ * are skipped).
  */
 int kv4_attention_ws_size(int B, int n_q_heads, int n_kv_heads, int head_dim, int n_q_tokens, int max_q, int max_kv,
                           size_t* bytes);

@@ -47,3 +47,16 @@ def test_bounds_at_the_end_of_int32_choose_as_any_large_bound_does(window):
     assert np.array_equal(out, large)
     ref, spread = K.attention(synth.bf16_to_f64(q), qs, ks, vs, D ** -0.5)
     check(out, ref, spread)
+
+
+@pytest.mark.parametrize("ql", [[1, 1], [1, 40]])
+def test_lengths_past_the_last_whole_tile_of_int32_are_reported(ql):
+    """2^31 - 1 tokens, which no table here can hold, are an error and not one tile of them."""
+    kv, hq, hkv, D, P = [50, 60], 2, 1, 64, 16
+    r = np.random.RandomState(32)
+    pages, table, ks, vs, q, qs = make_batch(r, kv, ql, hq, hkv, D, P)
+    out = attend(pages, table, q, qs, [50, 2 ** 31 - 1], hq, hkv, D, P, 0.125, max_kv=2 ** 31 - 1, fill=7.0)
+    assert Q.qmoe_check_status() == Q.QMOE_EINVAL
+    ref, spread = K.attention(synth.bf16_to_f64(q[:1]), [0, 1], ks[:1], vs[:1], 0.125)
+    check(out[:1], ref, spread)
+    assert (out[1:] == 7).all()
