@@ -129,18 +129,22 @@ def _np_ptr(a: np.ndarray) -> int:
     return a.ctypes.data if a is not None else None
 
 
-_raw_stream = None      # (device index of the current device, its current stream's handle), looked up on first use
+_raw_stream = None      # (index of the current device, handle of a device's current stream), looked up on first use
 
 
-def _stream_ptr(stream) -> int:
-    if stream is not None:
-        return int(stream.cuda_stream)
+def _raw():
     global _raw_stream
     if _raw_stream is None:
         import torch
         torch.cuda.init()
         _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-    device, current = _raw_stream
+    return _raw_stream
+
+
+def _stream_ptr(stream) -> int:
+    if stream is not None:
+        return int(stream.cuda_stream)
+    device, current = _raw_stream or _raw()
     return current(device())
 
 
@@ -510,7 +514,10 @@ class Kv4Cache:
         nbytes = self.page_bytes(page_size, n_kv_heads, head_dim)
         if pages.dtype != torch.uint8 or pages.dim() != 2 or pages.shape[1] != nbytes or not pages.is_contiguous():
             raise ValueError(f"pages must be a contiguous uint8 tensor [n_pages, {nbytes}]")
+        if not pages.is_cuda:
+            raise ValueError("pages must be on a CUDA device")
         self.pages, self.page_size, self.n_kv_heads, self.head_dim = pages, page_size, n_kv_heads, head_dim
+        self.device = pages.get_device()
         self.n_pages = int(pages.shape[0])
         self.c = CKv4Cache(_dptr(pages), self.n_pages, page_size, n_kv_heads, head_dim)
         self.ref = ctypes.byref(self.c)
@@ -530,19 +537,39 @@ def _refuse(what: str):
     raise ValueError(what)
 
 
-# The calls below are made once per layer and decode step: each tensor is looked at once (layout, then pointer), in
-# as few Python calls as that takes.
-def _i32(t, n: int, name: str) -> int:
-    """Device pointer of a contiguous 32-bit tensor of at least n elements."""
-    if t.itemsize != 4 or not t.is_contiguous() or t.numel() < n:
-        _refuse(f"{name}: a contiguous int32 tensor of {n} elements or more")
+# The calls below are made once per layer and decode step: each tensor is looked at once (type, device, layout, then
+# pointer), in as few Python calls as that takes.
+_int32 = _f32 = None
+_bits16 = ()         # bf16, and its bits as 16-bit integers
+
+
+def _call_on(t, name: str, stream):
+    """(device index, stream handle) of a call: the current device, which t has to be on (and the other tensors where t
+    is), and its current stream where none is given."""
+    global _int32, _f32, _bits16
+    if not _bits16:
+        import torch
+        _int32, _f32, _bits16 = torch.int32, torch.float32, (torch.bfloat16, torch.int16, torch.uint16)
+    dev = t.get_device()
+    if dev < 0:
+        _refuse(f"{name}: a tensor on the current CUDA device")
+    device, current = _raw_stream or _raw()
+    if dev != device():
+        _refuse(f"{name}: a tensor on the current CUDA device")
+    return dev, current(dev) if stream is None else int(stream.cuda_stream)
+
+
+def _i32(t, n: int, name: str, dev: int) -> int:
+    """Device pointer of a contiguous int32 tensor of at least n elements."""
+    if t.dtype is not _int32 or t.get_device() != dev or not t.is_contiguous() or t.numel() < n:
+        _refuse(f"{name}: a contiguous int32 tensor of {n} elements or more on cuda:{dev}")
     return t.data_ptr()
 
 
-def _b16(t, n: int, name: str) -> int:
-    """Device pointer of a contiguous 16-bit tensor of n elements."""
-    if t.itemsize != 2 or not t.is_contiguous() or t.numel() != n:
-        _refuse(f"{name}: a contiguous bf16 tensor of {n} elements")
+def _b16(t, n: int, name: str, dev: int) -> int:
+    """Device pointer of a contiguous bf16 tensor of n elements."""
+    if t.dtype not in _bits16 or t.get_device() != dev or not t.is_contiguous() or t.numel() != n:
+        _refuse(f"{name}: a contiguous bf16 tensor of {n} elements on cuda:{dev}")
     return t.data_ptr()
 
 
@@ -555,11 +582,13 @@ def kv4_block_tables(cached, new_tokens, free_pages, n_free, page_size: int, tab
     rows, width = table.shape
     if rows != B:
         _refuse("table: [B, max_blocks]")
-    st = _lib.kv4_block_tables(_i32(cached, B, "cached"), _i32(new_tokens, B, "new_tokens"), B,
-                               _i32(free_pages, 0, "free_pages"), _i32(n_free, 1, "n_free"), page_size,
-                               _i32(table, 0, "table"), width, _i32(q_start, B + 1, "q_start"),
-                               _i32(kv_len, B, "kv_len"), _i32(slots, n, "slots"), _i32(positions, n, "positions"),
-                               n, _i32(n_free_out, 1, "n_free_out"), _stream_ptr(stream))
+    dev, handle = _call_on(new_tokens, "new_tokens", stream)
+    st = _lib.kv4_block_tables(_i32(cached, B, "cached", dev), _i32(new_tokens, B, "new_tokens", dev), B,
+                               _i32(free_pages, 0, "free_pages", dev), _i32(n_free, 1, "n_free", dev), page_size,
+                               _i32(table, 0, "table", dev), width, _i32(q_start, B + 1, "q_start", dev),
+                               _i32(kv_len, B, "kv_len", dev), _i32(slots, n, "slots", dev),
+                               _i32(positions, n, "positions", dev), n, _i32(n_free_out, 1, "n_free_out", dev),
+                               handle)
     if st:
         _check(st, "kv4_block_tables")
 
@@ -571,38 +600,44 @@ def qk_norm_rope(qkv, n_q_heads: int, n_kv_heads: int, head_dim: int, q_weight, 
     keys and values are also written to it at slots."""
     T, width = qkv.shape
     row, one = qkv.stride()
-    if one != 1 or qkv.itemsize != 2 or width < (n_q_heads + n_kv_heads * (1 if cache is None else 2)) * head_dim:
+    dev, handle = _call_on(qkv, "qkv", stream)
+    if one != 1 or qkv.dtype not in _bits16 or width < (n_q_heads + n_kv_heads * (1 if cache is None else 2)) * head_dim:
         _refuse("qkv: bf16 [T, heads * head_dim], rows contiguous")
     n_pos = rot = cs = pos = None
     if cos_sin is not None:
         n_pos, rot = cos_sin.shape
-        cs, pos = _i32(cos_sin, 0, "cos_sin"), _i32(positions, T, "positions")
+        if cos_sin.dtype is not _f32 or cos_sin.get_device() != dev or not cos_sin.is_contiguous():
+            _refuse(f"cos_sin: a contiguous float32 tensor [n_pos, rot_dim] on cuda:{dev}")
+        cs, pos = cos_sin.data_ptr(), _i32(positions, T, "positions", dev)
+    if cache is not None and cache.device != dev:
+        _refuse(f"cache: on cuda:{dev}")
     st = _lib.qk_norm_rope(qkv.data_ptr(), row, T, n_q_heads, n_kv_heads, head_dim,
-                           None if q_weight is None else _b16(q_weight, head_dim, "q_weight"),
-                           None if k_weight is None else _b16(k_weight, head_dim, "k_weight"), eps, cs, rot or 0,
+                           None if q_weight is None else _b16(q_weight, head_dim, "q_weight", dev),
+                           None if k_weight is None else _b16(k_weight, head_dim, "k_weight", dev), eps, cs, rot or 0,
                            interleaved, n_pos or 0, pos,
-                           _b16(q_out, T * n_q_heads * head_dim, "q_out") if n_q_heads else None,
-                           None if k_out is None else _b16(k_out, T * n_kv_heads * head_dim, "k_out"),
-                           None if cache is None else cache.ref, None if slots is None else _i32(slots, T, "slots"),
-                           _stream_ptr(stream))
+                           _b16(q_out, T * n_q_heads * head_dim, "q_out", dev) if n_q_heads else None,
+                           None if k_out is None else _b16(k_out, T * n_kv_heads * head_dim, "k_out", dev),
+                           None if cache is None else cache.ref, None if slots is None else _i32(slots, T, "slots", dev),
+                           handle)
     if st:
         _check(st, "qk_norm_rope")
     return q_out, k_out
 
 
 def _heads(x, T: int, cache: Kv4Cache) -> int:
-    """Token stride of x [T, n_kv_heads, head_dim] (16-bit, a token's heads contiguous)."""
+    """Token stride of x [T, n_kv_heads, head_dim] (bf16, a token's heads contiguous)."""
     s0, s1, s2 = x.stride()
-    if x.shape != (T, cache.n_kv_heads, cache.head_dim) or x.itemsize != 2 or s2 != 1 or (s1 != cache.head_dim and cache.n_kv_heads > 1):
-        _refuse("k, v: bf16 [T, n_kv_heads, head_dim], a token's heads contiguous")
+    if x.shape != (T, cache.n_kv_heads, cache.head_dim) or x.dtype not in _bits16 or x.get_device() != cache.device or s2 != 1 or (s1 != cache.head_dim and cache.n_kv_heads > 1):
+        _refuse("k, v: bf16 [T, n_kv_heads, head_dim] where the cache is, a token's heads contiguous")
     return s0
 
 
 def kv4_append(cache: Kv4Cache, k, v, slots, stream=None):
     """Quantise keys and values [T, n_kv_heads, head_dim] (bf16; any token stride) into the cache at slots."""
     T = k.shape[0]
+    dev, handle = _call_on(cache.pages, "cache", stream)
     st = _lib.kv4_append(cache.ref, k.data_ptr(), _heads(k, T, cache), v.data_ptr(), _heads(v, T, cache), T,
-                         _i32(slots, T, "slots"), _stream_ptr(stream))
+                         _i32(slots, T, "slots", dev), handle)
     if st:
         _check(st, "kv4_append")
 
@@ -611,8 +646,9 @@ def kv4_gather(cache: Kv4Cache, slots, k_out, v_out, stream=None):
     """The keys and values that the cache holds at slots, as bf16 [n, n_kv_heads, head_dim]."""
     n = slots.numel()
     size = n * cache.n_kv_heads * cache.head_dim
-    st = _lib.kv4_gather(cache.ref, _i32(slots, n, "slots"), n, _b16(k_out, size, "k_out"), _b16(v_out, size, "v_out"),
-                         _stream_ptr(stream))
+    dev, handle = _call_on(cache.pages, "cache", stream)
+    st = _lib.kv4_gather(cache.ref, _i32(slots, n, "slots", dev), n, _b16(k_out, size, "k_out", dev),
+                         _b16(v_out, size, "v_out", dev), handle)
     if st:
         _check(st, "kv4_gather")
     return k_out, v_out
@@ -635,10 +671,13 @@ def kv4_attention(cache: Kv4Cache, q, q_start, kv_len, table, out, workspace, ma
     B = kv_len.numel()
     if D != cache.head_dim or rows != B:
         _refuse("q: [n, n_q_heads, head_dim] of the cache's head_dim; table: [B, max_blocks]")
-    st = _lib.kv4_attention(cache.ref, _b16(q, n * hq * D, "q"), n, hq, _i32(q_start, B + 1, "q_start"),
-                            _i32(kv_len, B, "kv_len"), B, _i32(table, 0, "table"), width, max_q, max_kv, scale, causal,
-                            window, _b16(out, n * hq * D, "out"), workspace.data_ptr(), workspace.nbytes,
-                            _stream_ptr(stream))
+    dev, handle = _call_on(cache.pages, "cache", stream)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(f"workspace: a contiguous tensor on cuda:{dev}")
+    st = _lib.kv4_attention(cache.ref, _b16(q, n * hq * D, "q", dev), n, hq, _i32(q_start, B + 1, "q_start", dev),
+                            _i32(kv_len, B, "kv_len", dev), B, _i32(table, 0, "table", dev), width, max_q, max_kv, scale,
+                            causal, window, _b16(out, n * hq * D, "out", dev), workspace.data_ptr(), workspace.nbytes,
+                            handle)
     if st:
         _check(st, "kv4_attention")
     return out
