@@ -36,7 +36,7 @@ EXPORTED = [
     "qmoe_moe_layer_noalloc", "qmoe_pack_device_ws_size", "qmoe_pack_device", "rvq_pack_stages",
     "rvq_stage_allocation", "e8p_base_table", "e8p_pack", "e8p_nearest", "qmoe_offsets_compact",
     "qmoe_moe_layer_kernels", "kv4_block_tables", "qk_norm_rope", "kv4_append", "kv4_gather",
-    "kv4_attention_ws_size", "kv4_attention",
+    "kv4_attention_ws_size", "kv4_attention", "kv4_block_tables_bounded",
 ]
 
 
@@ -107,6 +107,7 @@ _sig = {
     "e8p_nearest": [_vp, _sz, _vp],
     "qmoe_offsets_compact": [_vp, _i, _i, _vp, _vp],
     "kv4_block_tables": [_vp, _vp, _i, _vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp],
+    "kv4_block_tables_bounded": [_vp, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp],
     "qk_norm_rope": [_vp, _i64, _i, _i, _i, _i, _vp, _vp, _f, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp],
     "kv4_append": [_vp, _vp, _i64, _vp, _i64, _i, _vp, _vp],
     "kv4_gather": [_vp, _vp, _i, _vp, _vp, _vp],
@@ -576,19 +577,19 @@ def _b16(t, n: int, name: str, dev: int) -> int:
 def kv4_block_tables(cached, new_tokens, free_pages, n_free, page_size: int, table, q_start, kv_len, slots, positions,
                      n_free_out, stream=None):
     """Block tables and slot maps of a batch from its requests' lengths (all int32 device tensors): takes the
-    new pages from the stack free_pages[:n_free], writes their entries of table [B, max_blocks], and gives
+    new pages from the stack free_pages[:n_free] (an n_free past free_pages is an error on the device), writes their entries of table [B, max_blocks], and gives
     q_start [B + 1], kv_len [B], and the slot and position of each new token."""
     B, n = new_tokens.numel(), slots.numel()
     rows, width = table.shape
     if rows != B:
         _refuse("table: [B, max_blocks]")
     dev, handle = _call_on(new_tokens, "new_tokens", stream)
-    st = _lib.kv4_block_tables(_i32(cached, B, "cached", dev), _i32(new_tokens, B, "new_tokens", dev), B,
-                               _i32(free_pages, 0, "free_pages", dev), _i32(n_free, 1, "n_free", dev), page_size,
-                               _i32(table, 0, "table", dev), width, _i32(q_start, B + 1, "q_start", dev),
-                               _i32(kv_len, B, "kv_len", dev), _i32(slots, n, "slots", dev),
-                               _i32(positions, n, "positions", dev), n, _i32(n_free_out, 1, "n_free_out", dev),
-                               handle)
+    st = _lib.kv4_block_tables_bounded(_i32(cached, B, "cached", dev), _i32(new_tokens, B, "new_tokens", dev), B,
+                                       _i32(free_pages, 0, "free_pages", dev), free_pages.numel(),
+                                       _i32(n_free, 1, "n_free", dev), page_size, _i32(table, 0, "table", dev), width,
+                                       _i32(q_start, B + 1, "q_start", dev), _i32(kv_len, B, "kv_len", dev),
+                                       _i32(slots, n, "slots", dev), _i32(positions, n, "positions", dev), n,
+                                       _i32(n_free_out, 1, "n_free_out", dev), handle)
     if st:
         _check(st, "kv4_block_tables")
 

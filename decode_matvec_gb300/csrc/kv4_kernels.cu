@@ -35,6 +35,7 @@ struct TableArgs {
     int32_t* positions;
     int32_t* n_free_out;
     int B, page_shift, max_blocks, n_tokens;
+    int max_free;     // places of the stack
     int vector4;      // slots and positions are 16-byte aligned
 };
 
@@ -76,9 +77,9 @@ __global__ void __launch_bounds__(kPlanThreads) block_tables_kernel(TableArgs a)
     __shared__ int have_s[kPlanThreads];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P1 = (1 << a.page_shift) - 1;
-    const int n_free = max(*a.n_free, 0);
+    const int said = *a.n_free, n_free = min(max(said, 0), a.max_free);
     long long tok0 = 0, page0 = 0;
-    bool bad = false;
+    bool bad = said > a.max_free;
     for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
         const int b = b0 + tid;
         int c = 0, n = 0;
@@ -503,19 +504,19 @@ int kv4_take_error() {
 }
 }  // namespace qmoe
 
-extern "C" int kv4_block_tables(const int32_t* cached, const int32_t* new_tokens, int B, const int32_t* free_pages,
-                                const int32_t* n_free, int page_size, int32_t* table, int max_blocks,
-                                int32_t* q_start, int32_t* kv_len, int32_t* slots, int32_t* positions, int n_tokens,
-                                int32_t* n_free_out, void* stream) {
+extern "C" int kv4_block_tables_bounded(const int32_t* cached, const int32_t* new_tokens, int B, const int32_t* free_pages,
+                                        int max_free, const int32_t* n_free, int page_size, int32_t* table, int max_blocks,
+                                        int32_t* q_start, int32_t* kv_len, int32_t* slots, int32_t* positions, int n_tokens,
+                                        int32_t* n_free_out, void* stream) {
     qmoe::clear_error();
     if (page_size != 16 && page_size != 32 && page_size != 64)
         return qmoe::fail(QMOE_EINVAL, "kv4_block_tables: page_size must be 16, 32 or 64");
-    if (B < 0 || n_tokens < 0 || max_blocks < 0) return qmoe::fail(QMOE_EINVAL, "kv4_block_tables: negative size");
+    if (B < 0 || n_tokens < 0 || max_blocks < 0 || max_free < 0) return qmoe::fail(QMOE_EINVAL, "kv4_block_tables: negative size");
     if (!n_free || !n_free_out || !q_start || (B > 0 && (!cached || !new_tokens || !table || !kv_len || !free_pages)) ||
         (n_tokens > 0 && (!slots || !positions)))
         return qmoe::fail(QMOE_EINVAL, "kv4_block_tables: NULL pointer");
     TableArgs a{cached, new_tokens, free_pages, n_free, table, q_start, kv_len, slots, positions, n_free_out,
-                B, page_size == 16 ? 4 : page_size == 32 ? 5 : 6, max_blocks, n_tokens,
+                B, page_size == 16 ? 4 : page_size == 32 ? 5 : 6, max_blocks, n_tokens, max_free,
                 kv4::aligned16(slots) && kv4::aligned16(positions)};
     cudaStream_t st = (cudaStream_t)stream;
     // up to four tokens a thread: one launch
@@ -528,6 +529,14 @@ extern "C" int kv4_block_tables(const int32_t* cached, const int32_t* new_tokens
     if (rc) return rc;
     return kv4::launch_dependent(slot_map_kernel, dim3((unsigned)((n_tokens + kMapTokens - 1) / kMapTokens)), kMapTokens / 4, 0, st,
                                  "kv4_block_tables", a);
+}
+
+extern "C" int kv4_block_tables(const int32_t* cached, const int32_t* new_tokens, int B, const int32_t* free_pages,
+                                const int32_t* n_free, int page_size, int32_t* table, int max_blocks,
+                                int32_t* q_start, int32_t* kv_len, int32_t* slots, int32_t* positions, int n_tokens,
+                                int32_t* n_free_out, void* stream) {
+    return kv4_block_tables_bounded(cached, new_tokens, B, free_pages, 0x7FFFFFFF, n_free, page_size, table, max_blocks, q_start,
+                                    kv_len, slots, positions, n_tokens, n_free_out, stream);
 }
 
 extern "C" int qk_norm_rope(const void* qkv, int64_t row_stride, int T, int n_q_heads, int n_kv_heads, int head_dim,

@@ -541,7 +541,8 @@ typedef struct {
  * taken from the top of the stack of free pages: the i-th new page of the
  * call, in request order, is free_pages[n_free - 1 - i].
  *  cached, new_tokens  device int32 [B], >= 0.
- *  free_pages  device int32 stack;  n_free device int32 [1].
+ *  free_pages  device int32 stack;  n_free device int32 [1], at most the
+ *              stack's places (kv4_block_tables_bounded checks that).
  *  table       device int32 [B][max_blocks], in/out: entries of pages that a
  *              request has already are read, those of new pages written, the
  *              others left as they are.
@@ -563,6 +564,17 @@ int kv4_block_tables(const int32_t* cached, const int32_t* new_tokens, int B,
                      int32_t* table, int max_blocks, int32_t* q_start, int32_t* kv_len,
                      int32_t* slots, int32_t* positions, int n_tokens,
                      int32_t* n_free_out, void* stream);
+
+/*
+ * kv4_block_tables with the stack's size, max_free places, from the host: an
+ * n_free above it is EINVAL in the error word and read as max_free, so that
+ * nothing past the stack is read.
+ */
+int kv4_block_tables_bounded(const int32_t* cached, const int32_t* new_tokens, int B,
+                             const int32_t* free_pages, int max_free, const int32_t* n_free, int page_size,
+                             int32_t* table, int max_blocks, int32_t* q_start, int32_t* kv_len,
+                             int32_t* slots, int32_t* positions, int n_tokens,
+                             int32_t* n_free_out, void* stream);
 
 /*
  * Norms of queries and keys for each head and the position rotation, in one

@@ -60,3 +60,21 @@ def test_lengths_past_the_last_whole_tile_of_int32_are_reported(ql):
     ref, spread = K.attention(synth.bf16_to_f64(q[:1]), [0, 1], ks[:1], vs[:1], 0.125)
     check(out[:1], ref, spread)
     assert (out[1:] == 7).all()
+
+
+@pytest.mark.parametrize("tokens", [20, 5000])
+def test_block_tables_do_not_read_past_the_stack(tokens):
+    """A count of free pages above the stack's places: an error, and the pages are those that the stack has."""
+    P, n = 16, -(-tokens // 16)
+    stack = np.arange(100, 100 + n + 3)
+    memory = ints(np.concatenate([stack, np.full(50, 7)]))         # what lies behind the stack is not a page of it
+    cached, new, nf, out = ints([0]), ints([tokens]), ints([len(stack) + 40]), ints([0])
+    table, qs, kl = ints(np.full((1, n), -1)), ints([0, 0]), ints([0])
+    sl, po = ints(np.zeros(tokens)), ints(np.zeros(tokens))
+    Q.kv4_block_tables(cached, new, memory[:len(stack)], nf, P, table, qs, kl, sl, po, out)
+    assert Q.qmoe_check_status() == Q.QMOE_EINVAL
+    assert table.cpu().numpy()[0].tolist() == stack[::-1][:n].tolist() and out.item() == len(stack) - n
+    assert np.array_equal(sl.cpu().numpy(), table.cpu().numpy()[0][np.arange(tokens) // P] * P + np.arange(tokens) % P)
+    nf.fill_(len(stack))
+    Q.kv4_block_tables(cached, new, memory[:len(stack)], nf, P, table, qs, kl, sl, po, out)
+    ok()

@@ -64,7 +64,7 @@ def call(monkeypatch):
     """Makes a call on the named tensors (device 0 is current); returns whether it got as far as the library."""
     reached = []
     monkeypatch.setattr(Q, "_raw_stream", (lambda: 0, lambda device: 0))
-    for name in TENSORS:
+    for name in [*TENSORS, "kv4_block_tables_bounded"]:
         monkeypatch.setattr(Q._lib, name, lambda *a: reached.append(a) or 0)
     pages = OnDevice(torch.zeros((4, Q.Kv4Cache.page_bytes(16, 2, 64)), dtype=torch.uint8))
 
@@ -73,7 +73,7 @@ def call(monkeypatch):
         del reached[:]
         getattr(Q, name)(**cache, **NUMBERS[name], **{k: OnDevice(v) for k, v in TENSORS[name].items()} | other)
         return bool(reached)
-    run.reached = reached
+    run.reached, run.undo = reached, monkeypatch.undo
     return run
 
 
@@ -109,3 +109,12 @@ def test_caches_elsewhere_are_refused(call, name):
         with pytest.raises(ValueError):
             call(name, pages=p)
         assert not call.reached
+
+
+def test_block_tables_hand_the_library_the_size_of_the_stack(call):
+    call("kv4_block_tables")
+    assert call.reached[0][4] == TENSORS["kv4_block_tables"]["free_pages"].numel()
+    L, ptr = Q.lib(), 0x10000      # (never read: refused on the host)
+    tab = [ptr, ptr, 2, ptr, -1, ptr, 16, ptr, 4, ptr, ptr, ptr, ptr, 3, ptr, None]
+    call.undo()
+    assert L.kv4_block_tables_bounded(*tab) == Q.QMOE_EINVAL
