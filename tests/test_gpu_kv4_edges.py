@@ -12,7 +12,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 Q = pytest.importorskip("decode_matvec_gb300")
 
-from test_gpu_kv4 import attend, bits, check, ints, make_batch, ok  # noqa: E402
+from test_gpu_kv4 import U16, UBF, attend, bits, check, ints, make_batch, ok  # noqa: E402
 
 
 @pytest.mark.parametrize("B,q_hi,kv_hi,hq,hkv,D,P,window", [
@@ -78,3 +78,142 @@ def test_block_tables_do_not_read_past_the_stack(tokens):
     nf.fill_(len(stack))
     Q.kv4_block_tables(cached, new, memory[:len(stack)], nf, P, table, qs, kl, sl, po, out)
     ok()
+
+
+# ------------------------------------------------------------------ one token has all of the weight
+def cache_of(r, rows, P):
+    """Pages and table that hold the given rows (float [2, hkv, n, D] for each request), and what they are after 4 bits:
+    (pages, table, keys, values), float64, and the value rows' range 15 s."""
+    hkv, D = rows[0].shape[1], rows[0].shape[3]
+    blocks = [-(-x.shape[2] // P) for x in rows]
+    pages = np.full((sum(blocks), hkv, P * (D + 8)), 0xFF, np.uint8)      # NaN pairs where there is no token
+    perm, at = r.permutation(len(pages)), 0
+    table = np.full((len(rows), max(blocks)), -1, np.int64)
+    ks, vs, ranges = [], [], []
+    for b, x in enumerate(rows):
+        table[b, :blocks[b]] = perm[at:at + blocks[b]]
+        at += blocks[b]
+        u, s, z = K.quantise(x)
+        words = (u.reshape(*u.shape[:3], -1, 8).astype(np.uint32) << K.BITS).sum(-1, dtype=np.uint32)
+        for i in range(x.shape[2]):
+            pg = pages[table[b, i // P]]
+            for h in range(hkv):
+                for side in range(2):
+                    row = side * P + i % P
+                    pg[h, row * D // 2:(row + 1) * D // 2] = words[side, h, i].view(np.uint8)
+                    pg[h, P * D + 4 * row:P * D + 4 * row + 4] = np.stack([s[side, h, i], z[side, h, i]]).view(np.uint8)
+        d = K.dequantise(u, s, z)
+        ks.append(d[0])
+        vs.append(d[1])
+        ranges.append(15 * s[1].astype(np.float64))
+    return pages.reshape(len(pages), -1), table, ks, vs, ranges
+
+
+def one_hot_batch(r, kv, ql, hq, hkv, D, qscale, kscale):
+    """Keys of random signs, and queries that have the signs of one token that they see each (their target); the token
+    behind a query, hidden from it, has its first head's target's signs twice as large.  (rows of ones for the values,
+    queries float, targets)"""
+    g, rows, qs, targets = hq // hkv, [], [], []
+    for n, m in zip(kv, ql):
+        k = np.where(r.rand(hkv, n, D) < 0.5, -1.0, 1.0)
+        q, t = np.zeros((m, hq, D)), np.zeros((m, hq), int)
+        before = [r.permutation(n - m + 1) for _ in range(hkv)]   # the tokens before the call's, and its first one
+        for i in range(m):
+            for h in range(hq):                                   # (the first heads' own ones are shadowed, so no one else's)
+                t[i, h] = before[h // g][i if h % g == 0 else r.randint(m, n - m + 1)]
+                q[i, h] = k[h // g, t[i, h]] * r.uniform(0.75, 1.25, D)
+        for i in range(m - 1):
+            for h in range(hkv):
+                k[h, n - m + i + 1] = 2 * k[h, t[i, h * g]]
+        rows.append(np.stack([k * kscale, np.ones_like(k)]))
+        qs.append(q * qscale)
+        targets.append(t)
+    return rows, np.concatenate(qs), targets
+
+
+def lead_of(q, q_start, ks, targets, scale, causal=True):
+    """How far the targets' scores are above all others that the query sees, in log2 units, at least; and what the queries
+    should give: one target each."""
+    least = np.inf
+    for b, k in enumerate(ks):
+        n, g = q_start[b + 1] - q_start[b], q.shape[1] // k.shape[0]
+        for i in range(n):
+            last = k.shape[1] - n + i + 1
+            for h in range(q.shape[1]):
+                s = k[h // g, :last] @ q[q_start[b] + i, h] * scale * np.log2(np.e)
+                t = targets[b][i, h]
+                least = min(least, s[t] - np.delete(s, t).max())
+    return least
+
+
+def one_hot_reference(q_shape, q_start, vs, ranges, targets):
+    """The targets' value rows, and each row's range and largest magnitude [..., 2]."""
+    ref, size = np.zeros(q_shape), np.zeros(q_shape[:2] + (2,))
+    for b, v in enumerate(vs):
+        g = q_shape[1] // v.shape[0]
+        for i in range(q_start[b + 1] - q_start[b]):
+            for h in range(q_shape[1]):
+                t = targets[b][i, h]
+                ref[q_start[b] + i, h] = v[h // g, t]
+                size[q_start[b] + i, h] = ranges[b][h // g, t], np.abs(v[h // g, t]).max()
+    return ref, size
+
+
+def check_one_hot(out, ref, size):
+    """One rounding to bf16; the value product's operands rounded to fp16 once each, the weight (times the row's scale, or
+    alone) and the value: U16 of the row's range and twice U16 of the value; fp32 2^-20 of the row.  No error of the score
+    is allowed: the other weights are nothing.  Zeros and the opposite signs are no answers within that."""
+    tol = UBF * np.abs(ref) * 1.01 + U16 * size[..., :1] + 2.02 * U16 * np.abs(ref) + 2.0 ** -20 * size[..., 1:]
+    assert np.isfinite(out).all()
+    assert (np.abs(out - ref) <= tol).all(), float((np.abs(out - ref) / tol).max())
+    for wrong in (0 * ref, -ref):
+        assert (np.abs(wrong - ref) <= tol).mean() < 0.01
+
+
+SATURATED = [(40.0, 1.0), (1e30, 1e-3), (1.5, 1000.0), (1.5, 20000.0), (300.0, 20.0)]
+
+
+@pytest.mark.parametrize("kv,ql,hq,hkv,D,P", [
+    ([150, 90], [1, 1], 4, 2, 128, 16), ([700], [5], 4, 1, 64, 32), ([150, 210], [60, 70], 4, 2, 128, 16), ([300], [130], 3, 1, 64, 64)])
+@pytest.mark.parametrize("qscale,kscale", SATURATED)
+def test_attention_saturated_scores(kv, ql, hq, hkv, D, P, qscale, kscale):
+    """Where one token leads by far more than scores are off by, the answer is its value row, however large the scores."""
+    r = np.random.RandomState(D + len(ql))
+    rows, q, targets = one_hot_batch(r, kv, ql, hq, hkv, D, qscale, kscale)
+    for x in rows:
+        x[1] = r.randn(*x[1].shape) * np.exp(r.randn(*x[1].shape[:2], 1))
+    pages, table, ks, vs, ranges = cache_of(r, rows, P)
+    qb, qs = bits(q), np.concatenate([[0], np.cumsum(ql)]).astype(int)
+    # scores are off by fp32's 2^-22 and, with keys in fp16, 2^-11 of their size, which is below the sum of 128 |q k|
+    size = 2 * 1.25 * qscale * kscale * D * D ** -0.5 * np.log2(np.e)
+    assert lead_of(synth.bf16_to_f64(qb), qs, ks, targets, D ** -0.5) > 40 + 2.0 ** -9 * size
+    out = attend(pages, table, qb, qs, kv, hq, hkv, D, P, D ** -0.5)
+    ok()
+    check_one_hot(out, *one_hot_reference(out.shape, qs, vs, ranges, targets))
+
+
+@pytest.mark.parametrize("kv,ql,hq,hkv,D,P,window", [
+    ([400], [1], 1, 1, 64, 16, 0), ([400], [1], 4, 1, 128, 32, 390), ([150, 210], [4, 5], 4, 2, 128, 16, 0),
+    ([900], [8], 4, 1, 64, 64, 0), ([150, 210], [60, 70], 4, 2, 128, 16, 0), ([400], [70], 2, 1, 64, 16, 0)])
+@pytest.mark.parametrize("small", [2.0 ** -10, 2.0 ** -16])
+def test_attention_small_values_of_the_token_that_counts(kv, ql, hq, hkv, D, P, window, small):
+    """The targets' value rows are 2^10 or 2^16 times smaller than the other tokens', which have no weight, and the request's
+    last and first tokens, hidden from the earlier queries or behind the window, are 256 times larger still: the answer keeps
+    the precision of the targets' own rows."""
+    r = np.random.RandomState(D + len(ql) + window)
+    rows, q, targets = one_hot_batch(r, kv, ql, hq, hkv, D, 40.0, 2.0)
+    for x, t in zip(rows, targets):
+        x[1] = r.randn(*x[1].shape)
+        x[1][:, [0, 1, -1]] *= 256
+        for i, h in np.ndindex(*t.shape):
+            if t[i, h] > 10:
+                x[1][h // (hq // hkv), t[i, h]] = small * r.randn(D)
+    pages, table, ks, vs, ranges = cache_of(r, rows, P)
+    qb, qs = bits(q), np.concatenate([[0], np.cumsum(ql)]).astype(int)
+    assert lead_of(synth.bf16_to_f64(qb), qs, ks, targets, D ** -0.5) > 60
+    out = attend(pages, table, qb, qs, kv, hq, hkv, D, P, D ** -0.5, True, window)
+    ok()
+    keep = np.concatenate([(t > 10).reshape(-1) for t in targets]).reshape(out.shape[:2])
+    ref, size = one_hot_reference(out.shape, qs, vs, ranges, targets)
+    assert keep.mean() > 0.8
+    check_one_hot(out[keep], ref[keep], size[keep])
