@@ -50,14 +50,16 @@ __device__ __forceinline__ bool request(const AttnArgs& a, int b, int* q0, int* 
 // the 4-bit codes are matrix operands as they are: a code in the low mantissa bits of an fp16 pattern
 // is the subnormal u 2^-24 (u 2^-20 one nibble up), so two masks and a shift turn a 32-bit word into
 // four operand registers, and scale and offset enter on the few scores.  Queries are scaled by a power
-// of two per row into fp16's range (exact: bf16 has fewer significant bits), probabilities by the
-// largest row scale seen, also a power of two, so that p s_v keeps fp16's 11 bits whatever the values'
-// magnitude.  Statistics and sums are fp32.
+// of two per row into fp16's range (exact: bf16 has fewer significant bits).  What is rounded to fp16
+// (11 bits) is a weight times its value row's scale, p s_v: with p = 2^(score - m) each row's m follows
+// its largest score + log2(s_v) so that its largest product stands between 2^6 and 2^14, and products
+// down to 2^-20 of that keep all bits whatever the values' magnitudes are, also those of tokens that the
+// row does not see.  Statistics and sums are fp32.
 //
 // The products are S^T = U_k Q^T and O^T = U_v^T P^T (m16n8k16, keys or head values as the 16 rows, 8
 // query rows as the 8 columns), so that one to eight rows fill the instruction; tcgen05's 128 rows
-// would be idle and its operands would have to be expanded through shared memory.  The running maximum
-// moves only when a score passes it by 2^8 (a vote instead of a reduction).
+// would be idle and its operands would have to be expanded through shared memory.  A row's m moves only
+// when a product would pass 2^14 (a vote instead of a reduction).
 //
 // Work is cut into tiles of kTile tokens; the tiles of all (request, kv head) items in a row are dealt
 // out to the blocks in equal runs, whatever the lengths.  A producer warp copies whole pages of one
@@ -75,7 +77,8 @@ constexpr int kStages = 3;
 constexpr int kConsumers = 4;                        // warps that compute
 constexpr int kDecodeThreads = 32 * (kConsumers + 1);
 constexpr float kNoMax = -3.0e38f;                   // running maximum before any score
-constexpr float kSlack = 8.f;                        // scores may pass the running maximum by 2^8
+constexpr float kTop = 6.f, kSlack = 14.f;           // few rows: the largest product is 2^6 when m moves, and 2^14 at most
+constexpr float kLeastScale = 5.9604645e-8f;         // fp16's smallest scale but 0, 2^-24
 constexpr uint32_t kWaitLimit = 1u << 22;
 
 // Tiles of request b for this path (0: not its request), and the first one.
@@ -163,6 +166,12 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
     __half2 h = __floats2half2_rn(lo, hi);
     return *(uint32_t*)&h;
@@ -198,6 +207,7 @@ template <int D, int NT>
 struct DecodeShared {
     // query operand of 16 to 32 rows (with 8 it is held in registers); every warp writes the same values
     alignas(16) uint2 qf[NT == 1 ? 1 : NT][D / 32][2][32];
+    alignas(16) float4 qc[NT][4];          // and the factors of rows 2 t, 2 t + 1: of s (q . u), then of z
     alignas(128) unsigned char stage[kStages][kTile * (D + 8)];
     alignas(16) float red[kConsumers][8][D + 4];
     float m[kConsumers][8], l[kConsumers][8];
@@ -219,6 +229,14 @@ struct SplitItem {
 // Programmatic dependent launch: the kernels of a call overlap each other's launches.
 __device__ __forceinline__ void depend_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void depend_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Read where it stands: volatile, so that it is not read once for all tokens and kept.
+__device__ __forceinline__ void load_factors(const float4* src, float (&c1)[2], float (&cz)[2]) {
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(c1[0]), "=f"(c1[1]), "=f"(cz[0]), "=f"(cz[1])
+                 : "r"(qmoe_tc::smem_u32(src))
+                 : "memory");
+}
 
 // The computing warps wait for each other; false (and reported) when one of them has given up.
 __device__ __forceinline__ bool meet(uint64_t* bar, uint32_t& met) {
@@ -368,11 +386,10 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
     const uint32_t row_step = P == 16 ? a.cache.head_bytes : 16 * (D / 2), pair_step = P == 16 ? a.cache.head_bytes : 64;
 
     uint2 qr[W][2];                // query operand of 8 rows: [word][nibble parity]
-    float c1[NT][2], cz[NT][2];    // per row: factor of s (q . u), and factor times sum(q), in log2 units
+    float c1[2], cz[2];            // of 8 rows, per row: factor of s (q . u), and factor times sum(q), in log2 units
     float m[NT][2], l[NT][2], pz[NT][2];
     float o[NT][4 * VW][4];
     uint32_t met = 0;              // times the computing warps have met
-    float vs = 1.f, vlim = 1e-9f;  // probabilities carry vs (a power of two); a value scale >= vlim moves it
     int q0 = 0, q_len = 0, kv_len = 0;
 
     for (int u = 0;; ++u) {
@@ -434,16 +451,16 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
                 const float fa = f1 * 16777216.f, fb = f1 * sum;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    c1[nt][i] = __shfl_sync(QMOE_FULL_MASK, fa, 8 * t + 4 * i);
-                    cz[nt][i] = __shfl_sync(QMOE_FULL_MASK, fb, 8 * t + 4 * i);
+                    c1[i] = __shfl_sync(QMOE_FULL_MASK, fa, 8 * t + 4 * i);
+                    cz[i] = __shfl_sync(QMOE_FULL_MASK, fb, 8 * t + 4 * i);
                     m[nt][i] = kNoMax, l[nt][i] = 0.f, pz[nt][i] = 0.f;
                 }
+                if (NT > 1) sh.qc[nt][t] = make_float4(c1[0], c1[1], cz[0], cz[1]);
 #pragma unroll
                 for (int i = 0; i < 4 * VW; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
             }
-            vs = 1.f, vlim = 1e-9f;
             __syncwarp();
         }
         const unsigned char* stg = sh.stage[st];
@@ -494,12 +511,15 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
                     sk[r] = kp.x, zk[r] = kp.y, sv[j][r] = vp.x, zv[j][r] = vp.y;
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
+                    // (with more rows they would cost the registers that the sums need)
+                    if (NT > 1) load_factors(&sh.qc[nt][t], c1, cz);
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
-                            s[j][nt][2 * r + i] = fmaf(c1[nt][i], sk[r] * s[j][nt][2 * r + i], cz[nt][i] * zk[r]);
+                            s[j][nt][2 * r + i] = fmaf(c1[i], sk[r] * s[j][nt][2 * r + i], cz[i] * zk[r]);
+                }
                 // ---- tokens that some row does not see
                 if (__builtin_expect(in.flags & kEdge, 0)) {
                     int first = a.causal ? kv_len - q_len : kv_len - 1;
@@ -520,44 +540,34 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
                     }
                 }
             }
-            // ---- move the maximum or the values' scale, rarely
-            float vmax = 0.f;
+            // ---- move a row's m, rarely (a row of values without a scale, all z, counts as one with the least scale)
+            float ls[J][2];
 #pragma unroll
-            for (int j = 0; j < J; ++j) vmax = fmaxf(vmax, fmaxf(fabsf(sv[j][0]), fabsf(sv[j][1])));
-            bool move = vmax >= vlim;
+            for (int j = 0; j < J; ++j) ls[j][0] = lg2(fmaxf(sv[j][0], kLeastScale)), ls[j][1] = lg2(fmaxf(sv[j][1], kLeastScale));
+            bool move = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float mx = fmaxf(s[0][nt][i], s[0][nt][2 + i]);
-                    if (J == 2) mx = fmaxf(mx, fmaxf(s[J - 1][nt][i], s[J - 1][nt][2 + i]));
-                    move |= mx > m[nt][i] + kSlack;
+                    float mx = fmaxf(s[0][nt][i] + ls[0][0], s[0][nt][2 + i] + ls[0][1]);
+                    if (J == 2) mx = fmaxf(mx, fmaxf(s[J - 1][nt][i] + ls[J - 1][0], s[J - 1][nt][2 + i] + ls[J - 1][1]));
+                    // (scores above 2^24, whose last place is worth more than the slack, are always looked at)
+                    move |= mx > fmaf(fabsf(m[nt][i]), -0x1p-21f, m[nt][i] + kSlack);
                 }
             if (__builtin_expect(__any_sync(QMOE_FULL_MASK, move), 0)) {
-                float v = fmaxf(vmax, vlim * 0.5f);
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) v = fmaxf(v, __shfl_xor_sync(QMOE_FULL_MASK, v, d));
-                float fo = 1.f;
-                if (v >= vlim) {
-                    const int k = (int)(__float_as_uint(v) >> 23) - 127;       // v in [2^k, 2^(k+1))
-                    const float nvs = pow2i(6 - k);
-                    fo = nvs / vs;
-                    vs = nvs;
-                    vlim = pow2i(k + 1);
-                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float fr[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float mx = fmaxf(s[0][nt][i], s[0][nt][2 + i]);
-                        if (J == 2) mx = fmaxf(mx, fmaxf(s[J - 1][nt][i], s[J - 1][nt][2 + i]));
+                        float mx = fmaxf(s[0][nt][i] + ls[0][0], s[0][nt][2 + i] + ls[0][1]);
+                        if (J == 2) mx = fmaxf(mx, fmaxf(s[J - 1][nt][i] + ls[J - 1][0], s[J - 1][nt][2 + i] + ls[J - 1][1]));
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(QMOE_FULL_MASK, mx, d));
-                        const float m2 = fmaxf(m[nt][i], mx), fm = ex2(m[nt][i] - m2);
+                        const float m2 = fmaxf(m[nt][i], mx - kTop);
+                        fr[i] = ex2(m[nt][i] - m2);
                         m[nt][i] = m2;
-                        l[nt][i] *= fm, pz[nt][i] *= fm;
-                        fr[i] = fm * fo;
+                        l[nt][i] *= fr[i], pz[nt][i] *= fr[i];
                     }
 #pragma unroll
                     for (int i = 0; i < 4 * VW; ++i)
@@ -569,7 +579,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
             for (int j = 0; j < J; ++j) {
                 // ---- probabilities, as the value product's operand
                 uint32_t pf[NT][2];
-                const float w0 = sv[j][0] * vs, w1 = sv[j][1] * vs;
+                const float w0 = sv[j][0], w1 = sv[j][1];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float p[4];
@@ -618,7 +628,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
             const int rows = q_len * a.group;
             const bool whole = (in.flags & kWholeStart) && (in.flags & kWholeEnd);
             float* part = part_of(parts, blockIdx.x, (in.flags & kWholeStart) ? 1 : 0, 8 * NT, D);
-            const float unit = 16777216.f / vs;
+            constexpr float unit = 16777216.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 if (nt * 8 >= rows) break;
