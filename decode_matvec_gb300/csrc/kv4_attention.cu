@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
             // ---- move a row's m, rarely (a row of values without a scale, all z, counts as one with the least scale)
             float ls[J][2];
 #pragma unroll
-            for (int j = 0; j < J; ++j) ls[j][0] = lg2(fmaxf(sv[j][0], kLeastScale)), ls[j][1] = lg2(fmaxf(sv[j][1], kLeastScale));
+            for (int j = 0; j < J; ++j) ls[j][0] = lg2(fmaxf(fabsf(sv[j][0]), kLeastScale)), ls[j][1] = lg2(fmaxf(fabsf(sv[j][1]), kLeastScale));
             bool move = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)

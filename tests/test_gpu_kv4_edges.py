@@ -266,3 +266,23 @@ def test_attention_equal_scores_of_any_size(ql, qscale, kscale):
         # as check_one_hot, on the average; fp32's sums of values that cancel, 2^-20 of the largest
         tol = UBF * np.abs(ref) * 1.01 + U16 * size.mean() + 2.02 * U16 * np.abs(v).mean(0) + 2.0 ** -20 * np.abs(v).max()
         assert np.isfinite(out[i]).all() and (np.abs(out[i] - ref) <= tol).all(), float((np.abs(out[i] - ref) / tol).max())
+
+
+@pytest.mark.parametrize("ql", [[1], [5], [80]])
+def test_attention_reads_scales_of_either_sign(ql):
+    """The writer stores scales of 0 and above; a cache filled elsewhere may hold value rows upside down, s u + z with s < 0."""
+    kv, hq, hkv, D, P = [200], 4, 1, 64, 16
+    r = np.random.RandomState(43)
+    pages, table, ks, vs, ranges = cache_of(r, [np.stack([r.randn(1, 200, D), r.randn(1, 200, D) * np.exp2(r.randint(-4, 12, (1, 200, 1)))])], P)
+    heads = pages.reshape(len(pages), P * (D + 8))
+    for b, i in np.ndindex(len(pages), P):
+        sz = heads[b, P * D + 4 * (P + i):][:4].view(np.float16)
+        if np.isfinite(sz).all() and i % 3:
+            sz[:] = -sz[0], -sz[1]                                  # every third row as it was
+    q, qs = bits(r.randn(ql[0], hq, D)), [0, ql[0]]
+    k, v = K.unpack(pages, table[0], 200, P, hkv, D)
+    assert (v == np.where(np.arange(200)[:, None] % P % 3, -vs[0][0], vs[0][0])).all()
+    out = attend(pages, table, q, qs, kv, hq, hkv, D, P, D ** -0.5)
+    ok()
+    ref, spread = K.attention(synth.bf16_to_f64(q), qs, [k], [v], D ** -0.5)
+    check(out, ref, spread)
