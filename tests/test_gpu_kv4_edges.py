@@ -286,3 +286,48 @@ def test_attention_reads_scales_of_either_sign(ql):
     ok()
     ref, spread = K.attention(synth.bf16_to_f64(q), qs, [k], [v], D ** -0.5)
     check(out, ref, spread)
+
+
+# ------------------------------------------------------------------ pages of several requests, calls in flight together
+@pytest.mark.parametrize("ql", [[1, 1, 1], [3, 1, 70], [60, 70, 50]])
+def test_requests_that_share_pages(ql):
+    """A common prefix is held once: the tables of several requests name the same pages."""
+    common, own, hq, hkv, D, P = 160, [41, 70, 77], 4, 2, 128, 16
+    r = np.random.RandomState(51)
+    pages, table, ks, vs, _ = cache_of(r, [r.randn(2, hkv, n, D) for n in [common] + own], P)
+    rows = np.full((3, common // P + table.shape[1]), -1)
+    for b in range(3):
+        n = -(-own[b] // P)
+        rows[b, :common // P], rows[b, common // P:common // P + n] = table[0, :common // P], table[b + 1, :n]
+    kv = [common + n for n in own]
+    q, qs = bits(r.randn(sum(ql), hq, D)), np.concatenate([[0], np.cumsum(ql)]).astype(int)
+    out = attend(pages, rows, q, qs, kv, hq, hkv, D, P, D ** -0.5)
+    ok()
+    ref, spread = K.attention(synth.bf16_to_f64(q), qs, *([np.concatenate([x[0], x[b + 1]], 1) for b in range(3)] for x in (ks, vs)),
+                              D ** -0.5)
+    check(out, ref, spread)
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams, each with its own workspace, give the bits that they give alone."""
+    hq, hkv, D, P = 8, 2, 128, 16
+    calls = []
+    for seed, kv, ql in ((61, [900, 70, 2000, 1] * 8, [1, 1, 3, 1] * 8), (62, [300, 500, 40] * 4, [200, 1, 40] * 4)):
+        r = np.random.RandomState(seed)
+        pages, table, _, _, q, qs = make_batch(r, kv, ql, hq, hkv, D, P)
+        cache, mq, mk = Q.Kv4Cache(torch.from_numpy(pages).cuda(), P, hkv, D), max(ql), max(kv)
+        qt = bf16_tensor(q).view(torch.bfloat16).view(-1, hq, D)
+        ws = torch.empty(Q.kv4_attention_ws_size(len(kv), hq, hkv, D, qt.shape[0], mq, mk), dtype=torch.uint8, device="cuda")
+        args = (cache, qt, ints(qs), ints(kv), ints(table))
+        calls.append((torch.cuda.Stream(), lambda out, args=args, ws=ws, mq=mq, mk=mk: Q.kv4_attention(*args, out, ws, mq, mk, D ** -0.5), qt))
+    alone = [call(torch.empty_like(qt)) for _, call, qt in calls]
+    outs = [[torch.full_like(qt, float("nan")) for _ in range(20)] for _, _, qt in calls]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for (stream, call, _), out in zip(calls, outs):
+            with torch.cuda.stream(stream):
+                call(out[i])
+    torch.cuda.synchronize()
+    ok()
+    for first, out in zip(alone, outs):
+        assert bool(first.isfinite().all()) and all(torch.equal(first, o) for o in out)
