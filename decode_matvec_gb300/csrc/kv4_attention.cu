@@ -67,10 +67,12 @@ __device__ __forceinline__ bool request(const AttnArgs& a, int b, int* q0, int* 
 // a tile each.  An item that several blocks share leaves its parts (unnormalised sums, maximum, sum of
 // weights) in the workspace for join_kernel.
 //
-// Measured (one GB300): 64 requests of 1 to 16384 tokens, 32 query heads on 8 key heads of 128, 104 us =
-// 5.5 TB/s of codes and pairs, 82 % of the copy rate.  What it took: 32 tokens a warp and stage
-// instead of 16 (141 -> 127 us: fewer instructions beside the products), three stages and blocks a
-// multiprocessor instead of two and four (120), runs that count an item's beginning and end (105).
+// Measured (one GB300): 64 requests of 1 to 16384 tokens, 32 query heads on 8 key heads of 128, 106 us in
+// a graph = 5.5 TB/s of codes and pairs, 81 % of the copy rate (109 to 112 in a stream of calls from
+// Python); issue slots 52 % used, tensor pipe 29 %.  What it took: 32 tokens a warp and stage instead of
+// 16 (141 -> 127 us: fewer instructions beside the products), three stages and blocks a multiprocessor
+// instead of two and four (120), runs that count an item's beginning and end (105).  The instances for 16
+// and 32 rows of 128 spill 8 and 528 bytes of loads a thread; the others none.
 constexpr int kTile = 128;
 constexpr int kItemCost = 3;                         // what beginning and ending an item costs, in tiles
 constexpr int kStages = 3;
@@ -759,8 +761,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, const Sp
 // bf16 magnitude is inside fp16's range.  The running maximum moves, and O is rescaled, only when a
 // row's weights by it pass 2^14; P carries 2^6, so that small weights stay above fp16's subnormals.
 //
-// Measured: 2048 query tokens behind 30011 cached ones, 32 query heads on 4 key heads of 128, 730 us = 1.43
-// PFLOP/s, 76 % of cuBLAS's bf16 rate.  Leaving parts out in turn (no exponentials -5 %, one product of
+// Measured: 2048 query tokens behind 30011 cached ones, 32 query heads on 4 key heads of 128, 772 us = 1.35
+// PFLOP/s, 72 % of cuBLAS's bf16 rate (690 to 775 by machine).  Leaving parts out in turn (no exponentials -5 %, one product of
 // eight -1 %) shows no single limit: the four roles share the schedulers' issue slots (about 60 % used) and
 // the instruction caches, which is why every loop is short.  A 64-key step has two score buffers a tile of
 // rows, so that a softmax finds its next scores ready (128-key steps with one buffer: 951 us then, 895 with).
@@ -1657,8 +1659,10 @@ int launch_decode(const AttnArgs& a, void* ws, cudaStream_t st) {
     // tiles of the longest item (64 bits: the bounds may be the largest int32)
     long long tiles = ((long long)a.max_kv + kTile - 1) / kTile;
     if (a.window) tiles = std::min(tiles, ((long long)a.window + a.max_q + kTile - 1) / kTile + 1);
-    // Four tiles take a block about 3 us (16 heads, 511 tokens: 7 us a call from the host); spread over blocks they would
-    // take one, but need the second kernel (10 us).
+    // One block an item, or tiles spread over blocks and joined by a second kernel.  One request, 16/16 heads of 128, us in
+    // a graph, one block / spread: 2 tiles 6.0 / 9.0, 4 7.8 / 9.0, 5 8.6 / 8.8, 6 9.4 / 9.1, 8 11.0 / 9.3; 16/1 heads of 64:
+    // 4 8.7 / 9.2, 5 9.5 / 9.0.  More items cross later (8 requests of 32/8 heads: 6 9.6 / 10.6, 8 11.2 / 10.9; 32 of them:
+    // 16 21.0 / 23.3), which is not counted on: the bound is the longest request's, and the others may be short.
     if (tiles <= 4 && n_items <= (long long)decode_fit(rows)) {
         decode_kernel<D, NT><<<(unsigned)n_items, kDecodeThreads, smem, st>>>(a, rows, 1, nullptr, nullptr);
         return qmoe::launch_check("decode_kernel");

@@ -3,9 +3,10 @@
 // writer and reader.  For a few tokens all are bound by a launch and one
 // dependent chain of loads (2 to 4 us in a graph); for many the norm and the
 // writer by instruction issue, the reader by memory.  Measured (one GB300):
-// norm and rotation of 16383 tokens, 32 + 8 heads of 128, 72 us (4.8 TB/s of
-// 6.8); writing 16384 tokens of 16 heads of 128 59 us, reading them back 30;
-// tables, slots and positions of 257 requests with 260 thousand new tokens 9.5 us.
+// norm and rotation of 16383 tokens, 32 + 8 heads of 128, 73 us (4.7 TB/s of
+// 6.8; 206 instructions for two heads, issue slots 79 % used), with the cache
+// write 110; writing 16384 tokens of 16 heads of 128 59 us, reading them back 30;
+// tables, slots and positions of 257 requests with 260 thousand new tokens 10 us.
 
 #include <cuda_runtime.h>
 #include <stdint.h>

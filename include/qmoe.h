@@ -640,8 +640,17 @@ int kv4_gather(const kv4_cache* cache, const int32_t* slots, int n, void* k_out,
  *  workspace device, ws_bytes >= kv4_attention_ws_size(...), 16-byte aligned.
  *            The size does not fall when B, n_q_tokens, max_q or max_kv grow, so
  *            one sized for a program's largest call serves its others too.
- * Scores, softmax statistics and sums are fp32.  Rows of out that belong to no
- * request are left as they are.
+ * Scores, softmax statistics and sums are fp32; out is rounded once to bf16.
+ * Operands of the matrix products are fp16 (11 bits), queries as they are (to
+ * 2^-24 of the row's largest element).  Requests with few query rows (q_len *
+ * heads per kv head): codes exact, each weight times its value row's scale
+ * rounded, all 11 bits down to 2^-20 of the row's largest such product.  Requests
+ * with more: keys and values (s * u + z) and weights rounded; weights lose bits
+ * below 2^-20 of the largest and are none below 2^-31.  Which form a request takes goes by its rows and max_q: few means up to
+ * 32 rows where max_q tokens have no more than that, else up to the heads per kv
+ * head rounded up to 8 (none above 32).  So its last bits may change when a
+ * longer request joins the batch; the same call gives the same bits every time.
+ * Rows of out that belong to no request are left as they are.
  * Errors: EINVAL, EUNSUPPORTED (head_dim, more than 128 query heads per kv
  * head), ECAPACITY (workspace); on the device EINVAL (a page outside the
  * cache among the blocks of a request: its tokens are not seen; q_start out
