@@ -1914,6 +1914,7 @@ void phase_event(int i, cudaStream_t st) {
 int dict_take_error() {
     int v = 0;
     if (cudaMemcpyFromSymbol(&v, g_dict_error, sizeof(int)) != cudaSuccess) return QMOE_ECUDA;
+    if (v == 0) return 0;      // nothing to clear
     const int z = 0;
     if (cudaMemcpyToSymbol(g_dict_error, &z, sizeof(int)) != cudaSuccess) return QMOE_ECUDA;
     return v;

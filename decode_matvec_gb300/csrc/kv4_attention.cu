@@ -1736,6 +1736,7 @@ namespace qmoe {
 int kv4_attention_take_error() {
     int v = 0;
     if (cudaMemcpyFromSymbol(&v, g_kv4_attention_error, sizeof(int)) != cudaSuccess) return QMOE_ECUDA;
+    if (v == 0) return 0;      // nothing to clear
     const int z = 0;
     if (cudaMemcpyToSymbol(g_kv4_attention_error, &z, sizeof(int)) != cudaSuccess) return QMOE_ECUDA;
     return v;

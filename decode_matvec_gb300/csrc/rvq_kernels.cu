@@ -1460,6 +1460,7 @@ namespace qmoe {
 int rvq_take_error() {
     int v = 0;
     if (cudaMemcpyFromSymbol(&v, g_rvq_error, sizeof(int)) != cudaSuccess) return QMOE_ECUDA;
+    if (v == 0) return 0;      // nothing to clear
     const int z = 0;
     if (cudaMemcpyToSymbol(g_rvq_error, &z, sizeof(int)) != cudaSuccess) return QMOE_ECUDA;
     return v;

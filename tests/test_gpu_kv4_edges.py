@@ -331,3 +331,15 @@ def test_two_streams_at_once():
     ok()
     for first, out in zip(alone, outs):
         assert bool(first.isfinite().all()) and all(torch.equal(first, o) for o in out)
+
+
+def test_errors_of_two_kinds_are_each_cleared():
+    """The status call gives one error, clears all words that hold one, and then says that all is well."""
+    cache = Q.Kv4Cache.empty(2, 16, 1, 64)
+    k = torch.zeros((1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    for _ in range(2):
+        Q.kv4_append(cache, k, k, ints([99]))                                                       # EINVAL, cache kernels
+        ws = torch.empty(Q.kv4_attention_ws_size(1, 1, 1, 64, 1, 1, 5), dtype=torch.uint8, device="cuda")
+        Q.kv4_attention(cache, k, ints([0, 1]), ints([9]), ints([[0]]), k.clone(), ws, 1, 5, 1.0)   # ECAPACITY, attention
+        assert Q.qmoe_check_status() == Q.QMOE_EINVAL
+        ok()
