@@ -42,6 +42,9 @@ __device__ __forceinline__ bool request(const AttnArgs& a, int b, int* q0, int* 
     return true;
 }
 
+// First token that a query at position pos sees (pos may be below 0: then it sees none, and pos - window would overflow).
+__device__ __forceinline__ int first_seen(const AttnArgs& a, int pos) { return a.window && pos >= a.window ? pos - a.window + 1 : 0; }
+
 // ---------------------------------------------------------------- few query rows: one pass over the codes
 //
 // A request's rows of one kv head (query n, head g of the group: row n * group + g) are few, so the
@@ -89,8 +92,7 @@ __device__ __forceinline__ int tiles_of(const AttnArgs& a, int b, int max_rows, 
     *t0 = 0;
     if (!request(a, b, &q0, &q_len, &kv_len, report) || q_len == 0 || q_len * a.group > max_rows) return 0;
     const int first = a.causal ? kv_len - q_len : kv_len - 1;    // position of the first query
-    const int lo = a.window ? max(0, first - a.window + 1) : 0;
-    *t0 = lo / kTile;
+    *t0 = first_seen(a, first) / kTile;
     return max(1, (kv_len + kTile - 1) / kTile - *t0);
 }
 
@@ -537,7 +539,8 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const int pos = a.causal ? first + (nt * 8 + 2 * t + i) / a.group : first;
-                                if (!there || tok > pos || (a.window && tok <= pos - a.window)) s[j][nt][2 * r + i] = -INFINITY;
+                                // (below position 0 nothing is seen, wherever pos - window wraps to)
+                                if (!there || tok > pos || (a.window && tok <= (int)((unsigned)pos - (unsigned)a.window))) s[j][nt][2 * r + i] = -INFINITY;
                             }
                     }
                 }
@@ -806,7 +809,7 @@ struct TilePlan {
 __device__ __forceinline__ void key_steps(const AttnArgs& a, int q_len, int kv_len, int r0, int r1, int step, int* lo, int* hi) {
     const int first = a.causal ? kv_len - q_len : kv_len - 1;
     const int p0 = a.causal ? first + r0 / a.group : first, p1 = a.causal ? first + (r1 - 1) / a.group : first;
-    const int k1 = min(kv_len, p1 + 1), k0 = a.window ? max(0, p0 - a.window + 1) : 0;
+    const int k1 = min(kv_len, p1 + 1), k0 = first_seen(a, p0);
     *lo = k0 / step;
     *hi = k1 > k0 ? (k1 + step - 1) / step : *lo;
 }
@@ -1300,7 +1303,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
             float m = kNoMax, l = 0.f;
             const int first = a.causal ? c.w.kv_len - c.w.q_len : c.w.kv_len - 1;
             const int pos = a.causal ? first + n : first;
-            const int k_hi = min(pos, c.w.kv_len - 1), k_lo = a.window ? pos - a.window + 1 : 0;    // keys seen: [k_lo, k_hi]
+            const int k_hi = min(pos, c.w.kv_len - 1), k_lo = first_seen(a, pos);    // keys seen: [k_lo, k_hi]
             bool far = false;
             uint64_t mul2 = pair(factor, factor), nb2 = pair(6.f - m, 6.f - m);
             for (int t = t_s; t < t_e && ok; ++t) {

@@ -343,3 +343,16 @@ def test_errors_of_two_kinds_are_each_cleared():
         Q.kv4_attention(cache, k, ints([0, 1]), ints([9]), ints([[0]]), k.clone(), ws, 1, 5, 1.0)   # ECAPACITY, attention
         assert Q.qmoe_check_status() == Q.QMOE_EINVAL
         ok()
+
+
+@pytest.mark.parametrize("ql", [[12, 2], [90, 5]])
+def test_widest_window_with_queries_before_the_first_token(ql):
+    """A window one below the largest bound, and queries that stand before the first token: these see nothing, the others all."""
+    kv, hq, hkv, D, P = [4, 70], 4, 2, 64, 16
+    r = np.random.RandomState(71)
+    pages, table, ks, vs, q, qs = make_batch(r, kv, ql, hq, hkv, D, P)
+    out = attend(pages, table, q, qs, kv, hq, hkv, D, P, 0.125, window=2 ** 31 - 2, max_kv=2 ** 31 - 1)
+    ok()
+    ref, spread = K.attention(synth.bf16_to_f64(q), qs, ks, vs, 0.125)
+    check(out, ref, spread)
+    assert not out[:ql[0] - 4].any()
