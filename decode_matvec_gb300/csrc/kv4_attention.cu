@@ -297,6 +297,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
         long long begin = f.before + (long long)kh * (n + kItemCost);       // the item's first unit
         int tile = (int)(u0 - begin);
         int kv_len = 0, seen_lo = 0, seen_hi = 0;       // every row sees tokens [seen_lo, seen_hi)
+        int blk_lo = 0;                                 // first block that some row sees: those before may have no page
         int held = 0, entry = -1;                       // lane i holds the entry of block held + i
         bool ok = true, fresh = true;
         int issued = 0;
@@ -330,6 +331,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
                 kv_len = a.kv_len[b];
                 seen_hi = a.causal ? kv_len - q_len + 1 : kv_len;
                 seen_lo = a.window ? max(0, kv_len - a.window) : 0;
+                blk_lo = first_seen(a, a.causal ? kv_len - q_len : kv_len - 1) >> a.cache.page_shift;
             }
             if (fresh || blk0 + per_tile > held + 32) {
                 held = blk0;
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
                 entry = blk < a.max_blocks && ((long long)blk << a.cache.page_shift) < kv_len ? a.table[(int64_t)b * a.max_blocks + blk] : -1;
             }
             const int page = __shfl_sync(QMOE_FULL_MASK, entry, (blk0 - held + lane) & 31);
-            const bool mine = lane < per_tile && ((blk0 + lane) << a.cache.page_shift) < kv_len;
+            const bool mine = lane < per_tile && blk0 + lane >= blk_lo && ((blk0 + lane) << a.cache.page_shift) < kv_len;
             const bool good = mine && page >= 0 && page < a.cache.n_pages;
             if (mine && !good) attn_set_error(QMOE_EINVAL);
             const unsigned mask = __ballot_sync(QMOE_FULL_MASK, good);
@@ -1588,13 +1590,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) tile_kernel(AttnArgs a, TileP
             // ---- copy pages: lane i the tile's i-th
             const int per_tile = kKeys >> a.cache.page_shift, per_page = (1 << a.cache.page_shift) / 16;
             uint32_t tile = 0;
-                for (bool first = true; ok && next_item(a, plan, n_pairs, c, first, ahead); first = false) {
+            for (bool first = true; ok && next_item(a, plan, n_pairs, c, first, ahead); first = false) {
                 if (lane == 0 && c.t0 == 0 && !c.whole)
                     plan.items[blockIdx.x] = SplitItem{c.w.b, c.kh, c.w.rb, (int)((c.w.unit + (long long)c.kh * (c.w.n + kTileItemCost) + c.w.n - 1) / chunk)};
+                // the first block that a query of the request sees: those before may have no page
+                const int blk_lo = first_seen(a, c.w.kv_len - (a.causal ? c.w.q_len : 1)) >> a.cache.page_shift;
                 for (int t = c.t0; t < c.t1; ++t, ++tile) {
                     const int st = tile % kRawStages;
                     const int blk = (c.w.lo + t) * per_tile + lane;
-                    const bool mine = lane < per_tile && (blk << a.cache.page_shift) < c.w.kv_len;
+                    const bool mine = lane < per_tile && blk >= blk_lo && (blk << a.cache.page_shift) < c.w.kv_len;
                     int page = -1;
                     if (mine && blk < a.max_blocks) page = a.table[(int64_t)c.w.b * a.max_blocks + blk];
                     const bool good = page >= 0 && page < a.cache.n_pages;

@@ -653,7 +653,8 @@ int kv4_gather(const kv4_cache* cache, const int32_t* slots, int n, void* k_out,
  * Rows of out that belong to no request are left as they are.
  * Errors: EINVAL, EUNSUPPORTED (head_dim, more than 128 query heads per kv
  * head), ECAPACITY (workspace); on the device EINVAL (a page outside the
- * cache among the blocks of a request: its tokens are not seen; q_start out
+ * cache among the blocks that a request's queries see: its tokens are not
+ * seen; blocks behind the first query's window need no page; q_start out
  * of order, or a kv_len that is negative or above 2^31 - 128: such requests
  * are skipped).
  */

@@ -356,3 +356,27 @@ def test_widest_window_with_queries_before_the_first_token(ql):
     ref, spread = K.attention(synth.bf16_to_f64(q), qs, ks, vs, 0.125)
     check(out, ref, spread)
     assert not out[:ql[0] - 4].any()
+
+
+@pytest.mark.parametrize("kv,ql,P,window,gone", [
+    ([700, 90], [1, 1], 16, 300, -1), ([700, 390], [3, 2], 16, 300, 10 ** 6), ([500], [1], 32, 100, -1), ([900, 300], [70, 80], 16, 200, -1),
+    ([900], [100], 64, 130, -1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_pages_behind_the_window_may_be_gone(kv, ql, P, window, gone, causal):
+    """Blocks that no query of the request sees any more need no page: neither an error nor a change."""
+    hq, hkv, D = 4, 2, 128
+    r = np.random.RandomState(81)
+    pages, table, ks, vs, q, qs = make_batch(r, kv, ql, hq, hkv, D, P)
+    dropped = 0
+    for b, (n, m) in enumerate(zip(kv, ql)):
+        first = K.visible(n, m, 0, causal, window)[0]
+        table[b, :first // P] = gone
+        dropped += first // P
+    assert dropped
+    out = attend(pages, table, q, qs, kv, hq, hkv, D, P, D ** -0.5, causal, window)
+    ok()
+    ref, spread = K.attention(synth.bf16_to_f64(q), qs, ks, vs, D ** -0.5, causal, window)
+    check(out, ref, spread)
+    table[0, kv[0] // P - 1] = -1                       # one that is seen is still missed
+    attend(pages, table, q, qs, kv, hq, hkv, D, P, D ** -0.5, causal, window)
+    assert Q.qmoe_check_status() == Q.QMOE_EINVAL
