@@ -71,7 +71,7 @@ __device__ __forceinline__ int first_seen(const AttnArgs& a, int pos) { return a
 // weights) in the workspace for join_kernel.
 //
 // Measured (one GB300): 64 requests of 1 to 16384 tokens, 32 query heads on 8 key heads of 128, 106 us in
-// a graph = 5.5 TB/s of codes and pairs, 81 % of the copy rate (109 to 112 in a stream of calls from
+// a graph = 5.5 TB/s of codes and pairs, 81 % of the copy rate (109 to 113 in a stream of calls from
 // Python); issue slots 52 % used, tensor pipe 29 %.  What it took: 32 tokens a warp and stage instead of
 // 16 (141 -> 127 us: fewer instructions beside the products), three stages and blocks a multiprocessor
 // instead of two and four (120), runs that count an item's beginning and end (105).  The instances for 16
