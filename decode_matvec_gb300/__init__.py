@@ -36,7 +36,9 @@ EXPORTED = [
     "qmoe_moe_layer_noalloc", "qmoe_pack_device_ws_size", "qmoe_pack_device", "rvq_pack_stages",
     "rvq_stage_allocation", "e8p_base_table", "e8p_pack", "e8p_nearest", "qmoe_offsets_compact",
     "qmoe_moe_layer_kernels", "kv4_block_tables", "qk_norm_rope", "kv4_append", "kv4_gather",
-    "kv4_attention_ws_size", "kv4_attention", "kv4_block_tables_bounded",
+    "kv4_attention_ws_size", "kv4_attention", "kv4_block_tables_bounded", "add_rms_norm", "qmoe_route_scored",
+    "kv4_block_bounds", "kv4_select_blocks_ws_size", "kv4_select_blocks", "kv4_attention_blocks_ws_size",
+    "kv4_attention_blocks",
 ]
 
 
@@ -76,6 +78,11 @@ class CKv4Cache(ctypes.Structure):
                 ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
 
 
+class CKv4Bounds(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("steps", ctypes.c_void_p), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
 _vp, _i, _sz, _d = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_double
 _i64, _f = ctypes.c_int64, ctypes.c_float
 _sig = {
@@ -113,6 +120,13 @@ _sig = {
     "kv4_gather": [_vp, _vp, _i, _vp, _vp, _vp],
     "kv4_attention_ws_size": [_i, _i, _i, _i, _i, _i, _i, _vp],
     "kv4_attention": [_vp, _vp, _i, _i, _vp, _vp, _i, _vp, _i, _i, _i, _f, _i, _i, _vp, _vp, _sz, _vp],
+    "add_rms_norm": [_vp, _i, _i64, _vp, _i64, _vp, _i64, _vp, _i, _i, _f, _vp, _i64, _vp, _vp, _i, _vp],
+    "qmoe_route_scored": [_vp, _i, _i64, _i, _i, _i, _i, _vp, _i, _i, _i, _i, _f, _vp, _vp, _vp],
+    "kv4_block_bounds": [_vp, _vp, _vp, _i, _vp],
+    "kv4_select_blocks_ws_size": [_i, _i, _i, _i, _vp],
+    "kv4_select_blocks": [_vp, _vp, _i, _i, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _vp, _vp, _sz, _vp],
+    "kv4_attention_blocks_ws_size": [_i, _i, _i, _i, _i, _i, _vp],
+    "kv4_attention_blocks": [_vp, _vp, _i, _i, _vp, _vp, _i, _vp, _i, _vp, _i, _f, _vp, _vp, _sz, _vp],
 }
 for _name, _args in _sig.items():
     _f = getattr(_lib, _name)
@@ -682,4 +696,177 @@ def kv4_attention(cache: Kv4Cache, q, q_start, kv_len, table, out, workspace, ma
                             handle)
     if st:
         _check(st, "kv4_attention")
+    return out
+
+
+# ================================================================ around attention and experts
+def _rows(t, T: int, n: int, types, name: str, dev: int) -> int:
+    """Row stride of t [T, n] (values of a row contiguous)."""
+    if t.shape != (T, n) or t.dtype not in types or t.get_device() != dev:
+        _refuse(f"{name}: [{T}, {n}] of {' or '.join(str(x) for x in types)} on cuda:{dev}")
+    s0, s1 = t.stride()
+    if s1 != 1 and n > 1:
+        _refuse(f"{name}: the values of a row contiguous")
+    return s0
+
+
+_bits8 = ()          # e4m3, and its bits as 8-bit integers
+
+
+def add_rms_norm(x, weight, eps: float, y=None, residual=None, residual_out=None, codes=None, scales=None, stream=None):
+    """y = norm(x + residual) * weight for rows of x [T, n] (bf16 or float32; any row stride); residual_out (bf16; None:
+    residual itself) gets x + residual.  codes [T, n] (float8_e4m3fn or uint8) get y / scale with scales [T, 1] (a scale a
+    row) or [T, ceil(n / 128)] (one for each 128 values)."""
+    global _bits8
+    T, n = x.shape
+    dev, handle = _call_on(x, "x", stream)
+    f32 = x.dtype is _f32
+    xs = _rows(x, T, n, _bits16 if not f32 else (_f32,), "x", dev)
+    rs = ros = ys = 0
+    rp = rop = yp = cp = sp = None
+    group = 0
+    if residual is not None:
+        rs, rp = _rows(residual, T, n, _bits16, "residual", dev), residual.data_ptr()
+        if residual_out is None:
+            ros, rop = rs, rp
+        else:
+            ros, rop = _rows(residual_out, T, n, _bits16, "residual_out", dev), residual_out.data_ptr()
+    elif residual_out is not None:
+        _refuse("residual_out: needs a residual")
+    if y is not None:
+        ys, yp = _rows(y, T, n, _bits16, "y", dev), y.data_ptr()
+    if codes is not None:
+        if not _bits8:
+            import torch
+            _bits8 = (torch.float8_e4m3fn, torch.uint8)
+        if codes.dtype not in _bits8 or codes.shape != (T, n) or codes.get_device() != dev or not codes.is_contiguous():
+            _refuse(f"codes: a contiguous float8_e4m3fn tensor [{T}, {n}] on cuda:{dev}")
+        groups = (n + 127) >> 7
+        if (scales is None or scales.dtype is not _f32 or scales.get_device() != dev or not scales.is_contiguous()
+                or scales.dim() != 2 or scales.shape[0] != T or scales.shape[1] not in (1, groups)):
+            _refuse(f"scales: a contiguous float32 tensor [{T}, 1] or [{T}, {groups}] on cuda:{dev}")
+        group = 0 if scales.shape[1] == 1 else 128
+        cp, sp = codes.data_ptr(), scales.data_ptr()
+    elif scales is not None:
+        _refuse("scales: need codes")
+    st = _lib.add_rms_norm(x.data_ptr(), f32, xs, rp, rs, rop, ros, None if weight is None else _b16(weight, n, "weight", dev), T, n,
+                           eps, yp, ys, cp, sp, group, handle)
+    if st:
+        _check(st, "add_rms_norm")
+    return y
+
+
+def qmoe_route_scored(logits, k: int, ids, gates, sigmoid: bool = False, bias=None, n_groups: int = 1, top_groups: int = 1,
+                      group_best: int = 1, renormalise: bool = False, scale: float = 1.0, stream=None):
+    """Experts ids [T, k] (int32) and gates [T, k] (float32) from logits [T, E] (float32 or bf16; any row stride): softmax or
+    sigmoid scores, chosen by score + bias (float32 [E]) among the top_groups best of n_groups groups."""
+    T, E = logits.shape
+    dev, handle = _call_on(logits, "logits", stream)
+    f32 = logits.dtype is _f32
+    stride = _rows(logits, T, E, _bits16 if not f32 else (_f32,), "logits", dev)
+    bp = None
+    if bias is not None:
+        if bias.dtype is not _f32 or bias.get_device() != dev or not bias.is_contiguous() or bias.numel() != E:
+            _refuse(f"bias: a contiguous float32 tensor of {E} elements on cuda:{dev}")
+        bp = bias.data_ptr()
+    if gates.dtype is not _f32 or gates.get_device() != dev or not gates.is_contiguous() or gates.numel() != T * k:
+        _refuse(f"gates: a contiguous float32 tensor [{T}, {k}] on cuda:{dev}")
+    if ids.numel() != T * k:
+        _refuse(f"ids: a contiguous int32 tensor [{T}, {k}] on cuda:{dev}")
+    st = _lib.qmoe_route_scored(logits.data_ptr(), f32, stride, T, E, k, sigmoid, bp, n_groups, top_groups, group_best, renormalise,
+                                scale, _i32(ids, T * k, "ids", dev), gates.data_ptr(), handle)
+    if st:
+        _check(st, "qmoe_route_scored")
+    return ids, gates
+
+
+# ================================================================ attention over chosen blocks
+class Kv4Bounds:
+    """Bounds of each block's keys beside a Kv4Cache: codes int8 [n_pages, n_kv_heads, 2, head_dim] and steps float32
+    [n_pages, n_kv_heads] (``kv4_bounds`` in qmoe.h)."""
+
+    def __init__(self, codes, steps, page_size: int):
+        import torch
+        if codes.dtype != torch.int8 or codes.dim() != 4 or codes.shape[2] != 2 or not codes.is_contiguous():
+            raise ValueError("codes must be a contiguous int8 tensor [n_pages, n_kv_heads, 2, head_dim]")
+        if steps.dtype != torch.float32 or steps.shape != codes.shape[:2] or not steps.is_contiguous():
+            raise ValueError("steps must be a contiguous float32 tensor [n_pages, n_kv_heads]")
+        if not codes.is_cuda or steps.get_device() != codes.get_device():
+            raise ValueError("codes and steps must be on one CUDA device")
+        self.codes, self.steps, self.page_size = codes, steps, page_size
+        self.n_pages, self.n_kv_heads, _, self.head_dim = codes.shape
+        self.device = codes.get_device()
+        self.c = CKv4Bounds(_dptr(codes), _dptr(steps), self.n_pages, page_size, self.n_kv_heads, self.head_dim)
+        self.ref = ctypes.byref(self.c)
+
+    @classmethod
+    def empty(cls, cache: Kv4Cache) -> "Kv4Bounds":
+        import torch
+        where = cache.pages.device
+        return cls(torch.zeros((cache.n_pages, cache.n_kv_heads, 2, cache.head_dim), dtype=torch.int8, device=where),
+                   torch.zeros((cache.n_pages, cache.n_kv_heads), dtype=torch.float32, device=where), cache.page_size)
+
+
+def kv4_block_bounds(cache: Kv4Cache, bounds: Kv4Bounds, slots, stream=None):
+    """Bring the bounds of the blocks that tokens were written to at slots (int32) up to date."""
+    dev, handle = _call_on(cache.pages, "cache", stream)
+    if bounds.device != dev:
+        _refuse(f"bounds: on cuda:{dev}")
+    n = slots.numel()
+    st = _lib.kv4_block_bounds(cache.ref, bounds.ref, _i32(slots, n, "slots", dev), n, handle)
+    if st:
+        _check(st, "kv4_block_bounds")
+
+
+def kv4_select_blocks_ws_size(n_q_tokens: int, n_kv_heads: int, page_size: int, max_kv: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.kv4_select_blocks_ws_size(n_q_tokens, n_kv_heads, page_size, max_kv, ctypes.byref(n)), "kv4_select_blocks_ws_size")
+    return n.value
+
+
+def kv4_select_blocks(bounds: Kv4Bounds, q, q_start, kv_len, table, sel, workspace, max_kv: int, first: int = 1, last: int = 1,
+                      stream=None):
+    """Fill sel [n_q_tokens, n_kv_heads, top] (int32) with the blocks that each query of q [n_q_tokens, n_q_heads, head_dim]
+    (bf16) attends to: the first and last ones and those whose bounds give the largest scores, ascending, then -1."""
+    n, hq, D = q.shape
+    rows, width = table.shape
+    B = kv_len.numel()
+    n_sel, heads, top = sel.shape
+    if D != bounds.head_dim or rows != B or n_sel != n or heads != bounds.n_kv_heads:
+        _refuse("q: [n, n_q_heads, head_dim] of the bounds' head_dim; table: [B, max_blocks]; sel: [n, n_kv_heads, top]")
+    dev, handle = _call_on(bounds.codes, "bounds", stream)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(f"workspace: a contiguous tensor on cuda:{dev}")
+    st = _lib.kv4_select_blocks(bounds.ref, _b16(q, n * hq * D, "q", dev), n, hq, _i32(q_start, B + 1, "q_start", dev),
+                                _i32(kv_len, B, "kv_len", dev), B, _i32(table, 0, "table", dev), width, max_kv, top, first, last,
+                                _i32(sel, 0, "sel", dev), workspace.data_ptr(), workspace.nbytes, handle)
+    if st:
+        _check(st, "kv4_select_blocks")
+    return sel
+
+
+def kv4_attention_blocks_ws_size(n_q_tokens: int, n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, top: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.kv4_attention_blocks_ws_size(n_q_tokens, n_q_heads, n_kv_heads, head_dim, page_size, top, ctypes.byref(n)),
+           "kv4_attention_blocks_ws_size")
+    return n.value
+
+
+def kv4_attention_blocks(cache: Kv4Cache, q, q_start, kv_len, table, sel, out, workspace, scale: float, stream=None):
+    """kv4_attention (causal) where each query token and kv head sees the blocks of its list sel [n_q_tokens, n_kv_heads,
+    top] only."""
+    n, hq, D = q.shape
+    rows, width = table.shape
+    B = kv_len.numel()
+    n_sel, heads, top = sel.shape
+    if D != cache.head_dim or rows != B or n_sel != n or heads != cache.n_kv_heads:
+        _refuse("q: [n, n_q_heads, head_dim] of the cache's head_dim; table: [B, max_blocks]; sel: [n, n_kv_heads, top]")
+    dev, handle = _call_on(cache.pages, "cache", stream)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(f"workspace: a contiguous tensor on cuda:{dev}")
+    st = _lib.kv4_attention_blocks(cache.ref, _b16(q, n * hq * D, "q", dev), n, hq, _i32(q_start, B + 1, "q_start", dev),
+                                   _i32(kv_len, B, "kv_len", dev), B, _i32(table, 0, "table", dev), width, _i32(sel, 0, "sel", dev), top,
+                                   scale, _b16(out, n * hq * D, "out", dev), workspace.data_ptr(), workspace.nbytes, handle)
+    if st:
+        _check(st, "kv4_attention_blocks")
     return out

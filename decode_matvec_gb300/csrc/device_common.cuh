@@ -44,6 +44,7 @@ int rvq_take_error();
 int pack_take_error();
 int kv4_take_error();
 int kv4_attention_take_error();
+int kv4_blocks_take_error();
 
 // Unit of work of the expert kernels: one expert matrix applied to up to
 // `n_tok` tokens whose slots are slots[slot_begin .. slot_begin + n_tok).

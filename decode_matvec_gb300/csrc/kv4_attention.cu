@@ -22,6 +22,8 @@ struct AttnArgs {
     int B, n_q_tokens, n_q_heads, group, max_blocks, max_q, max_kv;
     float scale;
     int causal, window;
+    const int32_t* sel;      // lists of chosen blocks [query token][kv head][top], or NULL
+    int top;
 };
 
 // Longest request: its keys, rounded up to a tile of either path, stay in int32.
@@ -44,6 +46,23 @@ __device__ __forceinline__ bool request(const AttnArgs& a, int b, int* q0, int* 
 
 // First token that a query at position pos sees (pos may be below 0: then it sees none, and pos - window would overflow).
 __device__ __forceinline__ int first_seen(const AttnArgs& a, int pos) { return a.window && pos >= a.window ? pos - a.window + 1 : 0; }
+
+// ---- with lists of chosen blocks every query token is a request of its own, with its list's blocks as its keys
+
+// Whether query token t can be run: its request, its position, and the blocks that it sees.
+__device__ __forceinline__ bool chosen_token(const AttnArgs& a, int t, int* b, int* pos, int* seen, bool report) {
+    *b = kv4::request_of(a.q_start, a.B, t);
+    if (*b < 0) return false;
+    const int n = a.kv_len[*b];
+    if (n < 0 || n > kMaxKv) {
+        if (report) attn_set_error(QMOE_EINVAL);
+        return false;
+    }
+    const long long p = (long long)n - ((long long)a.q_start[*b + 1] - t);      // (below 0 where q_start runs past kv_len)
+    *pos = p < 0 ? -1 : (int)p;
+    *seen = p < 0 ? 0 : (int)(p >> a.cache.page_shift) + 1;
+    return true;
+}
 
 // ---------------------------------------------------------------- few query rows: one pass over the codes
 //
@@ -87,9 +106,15 @@ constexpr float kLeastScale = 5.9604645e-8f;         // fp16's smallest scale bu
 constexpr uint32_t kWaitLimit = 1u << 22;
 
 // Tiles of request b for this path (0: not its request), and the first one.
+template <bool kSel>
 __device__ __forceinline__ int tiles_of(const AttnArgs& a, int b, int max_rows, int* t0, bool report) {
     int q0, q_len, kv_len;
     *t0 = 0;
+    if constexpr (kSel) {
+        int r, pos, seen;
+        if (!chosen_token(a, b, &r, &pos, &seen, report)) return 0;
+        return max(1, (int)((((long long)min(seen, a.top) << a.cache.page_shift) + kTile - 1) / kTile));
+    }
     if (!request(a, b, &q0, &q_len, &kv_len, report) || q_len == 0 || q_len * a.group > max_rows) return 0;
     const int first = a.causal ? kv_len - q_len : kv_len - 1;    // position of the first query
     *t0 = first_seen(a, first) / kTile;
@@ -103,17 +128,17 @@ struct Found {
     int b;
 };
 
-template <int THREADS>
+template <int THREADS, bool kSel>
 __device__ __forceinline__ Found scan_requests(const AttnArgs& a, int max_rows, long long* chunk) {
     __shared__ long long warp_sum_s[THREADS / 32];
     __shared__ Found found;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (a.B + THREADS - 1) / THREADS;
-    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    const int all = kSel ? a.n_q_tokens : a.B, per = (all + THREADS - 1) / THREADS;
+    const int b0 = min(tid * per, all), b1 = min(b0 + per, all);
     long long mine = 0;
     int t0;
     for (int b = b0; b < b1; ++b) {
-        const int n = tiles_of(a, b, max_rows, &t0, blockIdx.x == 0);
+        const int n = tiles_of<kSel>(a, b, max_rows, &t0, blockIdx.x == 0);
         if (n) mine += n + kItemCost;
     }
     mine *= a.cache.n_kv_heads;
@@ -135,7 +160,7 @@ __device__ __forceinline__ Found scan_requests(const AttnArgs& a, int max_rows, 
     const long long target = (long long)blockIdx.x * *chunk;
     if (target >= before && target < before + mine) {
         for (int b = b0; b < b1; ++b) {
-            const int tiles = tiles_of(a, b, max_rows, &t0, false);
+            const int tiles = tiles_of<kSel>(a, b, max_rows, &t0, false);
             const long long n = tiles ? (long long)(tiles + kItemCost) * a.cache.n_kv_heads : 0;
             if (target < before + n) {
                 found.b = b;
@@ -203,9 +228,9 @@ __device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
 struct StageInfo {
     int b, kh, tile, flags;
 };
-constexpr int kFirst = 1, kLast = 2, kWholeStart = 4, kWholeEnd = 8, kEdge = 16, kEnd = 32, kValid = 64;
+constexpr int kFirst = 1, kLast = 2, kWholeStart = 4, kWholeEnd = 8, kEdge = 16, kEnd = 32, kValid = 64, kPartial = 1 << 16;
 // kWholeStart, kWholeEnd: the item begins, ends in this run; kEdge: some row does not see all of the tile; kEnd: the run is
-// over; kValid << page of the tile: the page is there
+// over; kValid << page of the tile: the page is there; with chosen blocks, kPartial << page: the query sees its first tokens only
 
 template <int D, int NT>
 struct DecodeShared {
@@ -252,7 +277,7 @@ __device__ __forceinline__ bool meet(uint64_t* bar, uint32_t& met) {
     return ok;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kSel>
 __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
     decode_kernel(AttnArgs a, int max_rows, int direct, SplitItem* items, float* parts) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -275,14 +300,14 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
         // a block an item: few tiles each, and nothing to join
         f.b = blockIdx.x / a.cache.n_kv_heads;
         int t0;
-        const int n = tiles_of(a, f.b, max_rows, &t0, blockIdx.x == f.b * a.cache.n_kv_heads);
+        const int n = tiles_of<kSel>(a, f.b, max_rows, &t0, blockIdx.x == f.b * a.cache.n_kv_heads);
         if (n == 0) return;
         f.before = 0;
         u0 = (long long)(blockIdx.x - f.b * a.cache.n_kv_heads) * (n + kItemCost);
         u1 = u0 + n;
         __syncthreads();
     } else {
-        f = scan_requests<kDecodeThreads>(a, max_rows, &chunk);
+        f = scan_requests<kDecodeThreads, kSel>(a, max_rows, &chunk);
         u0 = (long long)blockIdx.x * chunk, u1 = min(u0 + chunk, f.total);
         if (tid == 32 * kConsumers) items[blockIdx.x] = SplitItem{0, 0, 0, -1};
         if (u0 >= u1) return;
@@ -292,13 +317,15 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
         // ---- producer: a warp, lane i copies the tile's i-th page; 32 entries of the block table are read at a time
         const int per_tile = kTile >> a.cache.page_shift;
         const uint32_t page_copy = a.cache.head_bytes;
-        int b = f.b, t0, n = tiles_of(a, b, max_rows, &t0, false);
+        int b = f.b, t0, n = tiles_of<kSel>(a, b, max_rows, &t0, false);
         int kh = (int)((u0 - f.before) / (n + kItemCost));
         long long begin = f.before + (long long)kh * (n + kItemCost);       // the item's first unit
         int tile = (int)(u0 - begin);
         int kv_len = 0, seen_lo = 0, seen_hi = 0;       // every row sees tokens [seen_lo, seen_hi)
         int blk_lo = 0;                                 // first block that some row sees: those before may have no page
         int held = 0, entry = -1;                       // lane i holds the entry of block held + i
+        int listed = 0, own_blk = -1, in_own = 0, req = 0;   // chosen blocks: entries read, the query's own block, what it sees of that, its request
+        int chosen = -1;                                // and the block that entry belongs to
         bool ok = true, fresh = true;
         int issued = 0;
         for (int u = 0; ok; ++u) {
@@ -312,8 +339,8 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
                 over = begin >= u1;
                 if (!over && ++kh == a.cache.n_kv_heads) {
                     kh = 0;
-                    do n = tiles_of(a, ++b, max_rows, &t0, false);
-                    while (n == 0 && b + 1 < a.B);
+                    do n = tiles_of<kSel>(a, ++b, max_rows, &t0, false);
+                    while (n == 0 && b + 1 < (kSel ? a.n_q_tokens : a.B));
                 }
             }
             if (over) {
@@ -326,7 +353,12 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
             }
             const int end = (int)min((long long)n, u1 - begin);      // of the item's tiles in this run
             const int blk0 = (t0 + tile) * per_tile;
-            if (fresh) {
+            if (kSel && fresh) {
+                int pos = -1, seen = 0;
+                chosen_token(a, b, &req, &pos, &seen, false);
+                listed = min(seen, a.top);
+                own_blk = seen - 1, in_own = pos - (own_blk << a.cache.page_shift) + 1;
+            } else if (fresh) {
                 const int q_len = a.q_start[b + 1] - a.q_start[b];
                 kv_len = a.kv_len[b];
                 seen_hi = a.causal ? kv_len - q_len + 1 : kv_len;
@@ -336,10 +368,21 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
             if (fresh || blk0 + per_tile > held + 32) {
                 held = blk0;
                 const int blk = blk0 + lane;
+                if (kSel) {
+                    chosen = blk < listed ? a.sel[((int64_t)b * a.cache.n_kv_heads + kh) * a.top + blk] : -1;
+                    if (chosen < -1) attn_set_error(QMOE_EINVAL);
+                    entry = chosen >= 0 && chosen <= own_blk && chosen < a.max_blocks ? a.table[(int64_t)req * a.max_blocks + chosen] : -1;
+                } else
                 entry = blk < a.max_blocks && ((long long)blk << a.cache.page_shift) < kv_len ? a.table[(int64_t)b * a.max_blocks + blk] : -1;
             }
             const int page = __shfl_sync(QMOE_FULL_MASK, entry, (blk0 - held + lane) & 31);
-            const bool mine = lane < per_tile && blk0 + lane >= blk_lo && ((blk0 + lane) << a.cache.page_shift) < kv_len;
+            bool mine = lane < per_tile && blk0 + lane >= blk_lo && ((blk0 + lane) << a.cache.page_shift) < kv_len;
+            unsigned partial = 0;
+            if (kSel) {
+                const int blk = __shfl_sync(QMOE_FULL_MASK, chosen, (blk0 - held + lane) & 31);
+                mine = lane < per_tile && blk0 + lane < listed && blk >= 0 && blk <= own_blk;
+                partial = __ballot_sync(QMOE_FULL_MASK, mine && blk == own_blk && in_own < 1 << a.cache.page_shift);
+            }
             const bool good = mine && page >= 0 && page < a.cache.n_pages;
             if (mine && !good) attn_set_error(QMOE_EINVAL);
             const unsigned mask = __ballot_sync(QMOE_FULL_MASK, good);
@@ -354,8 +397,10 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
                 if (tile == end - 1) flags |= kLast;
                 if (begin >= u0) flags |= kWholeStart;          // the item's first tile is in this run
                 if (end == n) flags |= kWholeEnd;
-                if ((t0 + tile) * kTile < seen_lo || (t0 + tile + 1) * kTile > seen_hi || (int)mask != (1 << per_tile) - 1) flags |= kEdge;
-                sh.info[st] = StageInfo{b, kh, t0 + tile, flags};
+                if (kSel) {
+                    if ((int)mask != (1 << per_tile) - 1 || partial) flags |= kEdge | (int)partial * kPartial;
+                } else if ((t0 + tile) * kTile < seen_lo || (t0 + tile + 1) * kTile > seen_hi || (int)mask != (1 << per_tile) - 1) flags |= kEdge;
+                sh.info[st] = StageInfo{b, kh, kSel ? in_own : t0 + tile, flags};
                 if ((flags & (kLast | kWholeStart | kWholeEnd)) == (kLast | kWholeStart))
                     items[blockIdx.x] = SplitItem{b, kh, 0, (int)((begin + n - 1) / chunk)};
                 mbar_expect(&sh.full[st], (uint32_t)__popc(mask) * page_copy);
@@ -407,7 +452,8 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
         const StageInfo in = sh.info[st];
         if (in.flags & kEnd) return;
         if (in.flags & kFirst) {
-            q0 = a.q_start[in.b], q_len = a.q_start[in.b + 1] - q0, kv_len = a.kv_len[in.b];
+            if (kSel) q0 = in.b, q_len = 1;
+            else q0 = a.q_start[in.b], q_len = a.q_start[in.b + 1] - q0, kv_len = a.kv_len[in.b];
             const int rows = q_len * a.group;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -527,7 +573,21 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
                             s[j][nt][2 * r + i] = fmaf(c1[i], sk[r] * s[j][nt][2 * r + i], cz[i] * zk[r]);
                 }
                 // ---- tokens that some row does not see
-                if (__builtin_expect(in.flags & kEdge, 0)) {
+                if (kSel && __builtin_expect(in.flags & kEdge, 0)) {
+                    const int page = (tok0 + 16 * (half + j)) >> a.cache.page_shift;
+                    const bool page_ok = (in.flags / kValid >> page) & 1;
+                    const int sees = (in.flags / kPartial >> page) & 1 ? in.tile : P;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int tok = ((tok0 + 16 * (half + j)) & (P - 1)) + (g >> 1) + 4 * (g & 1) + 8 * r;
+                        if (page_ok && tok < sees) continue;
+                        sv[j][r] = 0.f, zv[j][r] = 0.f;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) s[j][nt][2 * r + i] = -INFINITY;
+                    }
+                } else if (!kSel && __builtin_expect(in.flags & kEdge, 0)) {
                     int first = a.causal ? kv_len - q_len : kv_len - 1;
                     asm volatile("" : "+r"(first));      // nothing of this is made ahead of the branch to it
                     const bool page_ok = (in.flags / kValid >> ((tok0 + 16 * (half + j)) >> a.cache.page_shift)) & 1;
@@ -698,7 +758,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
 // adds up a row's parts, or every group some of them where there are many.
 constexpr int kJoinThreads = 128;
 
-template <int D>
+template <int D, bool kSel>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, const SplitItem* items, const float* parts, int part_rows) {
     constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES;
     __shared__ float4 acc_s[GROUPS][LANES];
@@ -708,7 +768,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttnArgs a, const Sp
     const int n_parts = it.last - (int)blockIdx.x + 1;
     if (n_parts < 2) return;
     depend_launch();
-    const int q0 = a.q_start[it.b], rows = min(part_rows, (a.q_start[it.b + 1] - q0) * a.group - it.rb * part_rows);
+    const int q0 = kSel ? it.b : a.q_start[it.b];
+    const int rows = kSel ? a.group : min(part_rows, (a.q_start[it.b + 1] - q0) * a.group - it.rb * part_rows);
     const int grp = threadIdx.x / LANES, ln = threadIdx.x - grp * LANES;
     const bool wide = n_parts > 4;
     for (int r0 = blockIdx.y * (wide ? 1 : GROUPS); r0 < rows; r0 += gridDim.y * (wide ? 1 : GROUPS)) {
@@ -1656,30 +1717,31 @@ size_t decode_ws(int rows, int head_dim) {
     return rows == 0 ? 0 : decode_records() + align256(decode_fit(rows) * 2 * rows * (head_dim + 2) * sizeof(float));
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kSel = false>
 int launch_decode(const AttnArgs& a, void* ws, cudaStream_t st) {
     constexpr int rows = 8 * NT;
     const int smem = (int)sizeof(DecodeShared<D, NT>);
-    int rc = qmoe::smem_attr((const void*)decode_kernel<D, NT>, smem, "attention attr");
+    int rc = qmoe::smem_attr((const void*)decode_kernel<D, NT, kSel>, smem, "attention attr");
     if (rc) return rc;
-    const long long n_items = (long long)a.B * a.cache.n_kv_heads;
+    const long long n_items = (long long)(kSel ? a.n_q_tokens : a.B) * a.cache.n_kv_heads;
     // tiles of the longest item (64 bits: the bounds may be the largest int32)
     long long tiles = ((long long)a.max_kv + kTile - 1) / kTile;
+    if (kSel) tiles = (((long long)a.top << a.cache.page_shift) + kTile - 1) / kTile;
     if (a.window) tiles = std::min(tiles, ((long long)a.window + a.max_q + kTile - 1) / kTile + 1);
     // One block an item, or tiles spread over blocks and joined by a second kernel.  One request, 16/16 heads of 128, us in
     // a graph, one block / spread: 2 tiles 6.0 / 9.0, 4 7.8 / 9.0, 5 8.6 / 8.8, 6 9.4 / 9.1, 8 11.0 / 9.3; 16/1 heads of 64:
     // 4 8.7 / 9.2, 5 9.5 / 9.0.  More items cross later (8 requests of 32/8 heads: 6 9.6 / 10.6, 8 11.2 / 10.9; 32 of them:
     // 16 21.0 / 23.3), which is not counted on: the bound is the longest request's, and the others may be short.
     if (tiles <= 4 && n_items <= (long long)decode_fit(rows)) {
-        decode_kernel<D, NT><<<(unsigned)n_items, kDecodeThreads, smem, st>>>(a, rows, 1, nullptr, nullptr);
+        decode_kernel<D, NT, kSel><<<(unsigned)n_items, kDecodeThreads, smem, st>>>(a, rows, 1, nullptr, nullptr);
         return qmoe::launch_check("decode_kernel");
     }
     const unsigned blocks = (unsigned)std::min((long long)decode_fit(rows), n_items * std::max(1LL, tiles));
     SplitItem* items = (SplitItem*)ws;
     float* parts = (float*)((char*)ws + decode_records());
-    decode_kernel<D, NT><<<blocks, kDecodeThreads, smem, st>>>(a, rows, 0, items, parts);
+    decode_kernel<D, NT, kSel><<<blocks, kDecodeThreads, smem, st>>>(a, rows, 0, items, parts);
     if ((rc = qmoe::launch_check("decode_kernel"))) return rc;
-    return kv4::launch_dependent(join_kernel<D>, dim3(blocks, NT == 1 ? 8 : 16), kJoinThreads, 0, st, "join_kernel", a, items, parts, rows);
+    return kv4::launch_dependent(join_kernel<D, kSel>, dim3(blocks, NT == 1 ? 8 : 16), kJoinThreads, 0, st, "join_kernel", a, items, parts, rows);
 }
 
 // Workspace of the tile path: the plan, then the blocks' parts.  max_pairs bounds the sum of ceil(rows / 256).
@@ -1719,7 +1781,7 @@ int launch_tiles(const AttnArgs& a, const TileWs& w, int min_rows, cudaStream_t 
         rc = kv4::launch_dependent(tile_plan_kernel, dim3(1), kPlanTile, 0, st, "tile_plan_kernel", a, w.plan, min_rows);
     if (rc || (rc = qmoe::launch_check("tile_plan_kernel"))) return rc;
     if ((rc = kv4::launch_dependent(tile_kernel<D>, dim3(blocks), kTileThreads, smem, st, "tile_kernel", a, w.plan, w.parts))) return rc;
-    return kv4::launch_dependent(join_kernel<D>, dim3(blocks, 16), kJoinThreads, 0, st, "join_kernel", a, w.plan.items, w.parts, kRows);
+    return kv4::launch_dependent(join_kernel<D, false>, dim3(blocks, 16), kJoinThreads, 0, st, "join_kernel", a, w.plan.items, w.parts, kRows);
 }
 
 // Whether some request of the batch has more rows than the few-row path takes.
@@ -1734,6 +1796,15 @@ int check_sizes(const char* who, int B, int n_q_heads, int n_kv_heads, int head_
         return qmoe::fail(QMOE_EINVAL, std::string(who) + ": too many query rows in one call");
     if (n_q_heads / n_kv_heads > 128)
         return qmoe::fail(QMOE_EUNSUPPORTED, std::string(who) + ": more than 128 query heads per kv head");
+    return QMOE_OK;
+}
+
+int check_chosen(const char* who, int n_q_tokens, int n_q_heads, int n_kv_heads, int head_dim, int top) {
+    const int rc = check_sizes(who, 0, n_q_heads, n_kv_heads, head_dim, n_q_tokens, 0, 0);
+    if (rc) return rc;
+    if (n_q_heads / n_kv_heads > 32) return qmoe::fail(QMOE_EUNSUPPORTED, std::string(who) + ": more than 32 query heads per kv head");
+    if (top < 1 || top > 65536) return qmoe::fail(QMOE_EINVAL, std::string(who) + ": need 1 <= top <= 65536");
+    if ((long long)n_q_tokens * n_kv_heads > 0x7FFFFFFFLL) return qmoe::fail(QMOE_EINVAL, std::string(who) + ": too many query tokens in one call");
     return QMOE_OK;
 }
 
@@ -1793,4 +1864,42 @@ extern "C" int kv4_attention(const kv4_cache* cache, const void* q, int n_q_toke
     if (rows == 32) rc = D == 128 ? launch_decode<128, 4>(a, workspace, st) : launch_decode<64, 4>(a, workspace, st);
     if (rc || !tiles) return rc;
     return D == 128 ? launch_tiles<128>(a, tw, rows, st) : launch_tiles<64>(a, tw, rows, st);
+}
+
+extern "C" int kv4_attention_blocks_ws_size(int n_q_tokens, int n_q_heads, int n_kv_heads, int head_dim, int page_size, int top,
+                                            size_t* bytes) {
+    qmoe::clear_error();
+    if (!bytes) return qmoe::fail(QMOE_EINVAL, "kv4_attention_blocks_ws_size: NULL output");
+    const int rc = check_chosen("kv4_attention_blocks_ws_size", n_q_tokens, n_q_heads, n_kv_heads, head_dim, top);
+    if (rc) return rc;
+    if (page_size != 16 && page_size != 32 && page_size != 64)
+        return qmoe::fail(QMOE_EINVAL, "kv4_attention_blocks_ws_size: page_size must be 16, 32 or 64");
+    *bytes = decode_ws(decode_rows(n_q_heads / n_kv_heads, 1), head_dim);
+    return QMOE_OK;
+}
+
+extern "C" int kv4_attention_blocks(const kv4_cache* cache, const void* q, int n_q_tokens, int n_q_heads, const int32_t* q_start,
+                                    const int32_t* kv_len, int B, const int32_t* table, int max_blocks, const int32_t* sel, int top,
+                                    float scale, void* out, void* workspace, size_t ws_bytes, void* stream) {
+    qmoe::clear_error();
+    AttnArgs a{};
+    int rc = kv4::view_of(cache, "kv4_attention_blocks", &a.cache);
+    if (rc) return rc;
+    if ((rc = check_chosen("kv4_attention_blocks", n_q_tokens, n_q_heads, cache->n_kv_heads, cache->head_dim, top))) return rc;
+    if (B < 0 || max_blocks < 0) return qmoe::fail(QMOE_EINVAL, "kv4_attention_blocks: negative B or max_blocks");
+    if (B == 0 || n_q_tokens == 0) return QMOE_OK;
+    if (!q || !out || !q_start || !kv_len || !sel || (max_blocks > 0 && !table))
+        return qmoe::fail(QMOE_EINVAL, "kv4_attention_blocks: NULL pointer");
+    if (!kv4::aligned16(q) || !kv4::aligned16(out)) return qmoe::fail(QMOE_EINVAL, "kv4_attention_blocks: pointer not 16-byte aligned");
+    a.q = (const uint16_t*)q, a.out = (uint16_t*)out, a.q_start = q_start, a.kv_len = kv_len, a.table = table, a.sel = sel;
+    a.B = B, a.n_q_tokens = n_q_tokens, a.n_q_heads = n_q_heads, a.group = n_q_heads / cache->n_kv_heads;
+    a.max_blocks = max_blocks, a.max_q = 1, a.scale = scale, a.causal = 1, a.top = top;
+    const int rows = decode_rows(a.group, 1), D = cache->head_dim;
+    if (ws_bytes < decode_ws(rows, D)) return qmoe::fail(QMOE_ECAPACITY, "kv4_attention_blocks: workspace too small");
+    if (!workspace || !kv4::aligned16(workspace)) return qmoe::fail(QMOE_EINVAL, "kv4_attention_blocks: workspace NULL or not 16-byte aligned");
+    cudaStream_t st = (cudaStream_t)stream;
+    if (rows == 8) return D == 128 ? launch_decode<128, 1, true>(a, workspace, st) : launch_decode<64, 1, true>(a, workspace, st);
+    if (rows == 16) return D == 128 ? launch_decode<128, 2, true>(a, workspace, st) : launch_decode<64, 2, true>(a, workspace, st);
+    if (rows == 24) return D == 128 ? launch_decode<128, 3, true>(a, workspace, st) : launch_decode<64, 3, true>(a, workspace, st);
+    return D == 128 ? launch_decode<128, 4, true>(a, workspace, st) : launch_decode<64, 4, true>(a, workspace, st);
 }

@@ -25,6 +25,18 @@ __device__ __forceinline__ unsigned char* head_ptr(const CacheView& c, int page,
     return c.pages + (uint64_t)page * c.page_bytes + (uint64_t)h * c.head_bytes;
 }
 
+// The request that query token t belongs to (q_start[b] <= t < q_start[b + 1]), or -1.  In a decode step it is t itself.
+__device__ __forceinline__ int request_of(const int32_t* q_start, int B, int t) {
+    if (t < B && q_start[t] == t && q_start[t + 1] == t + 1) return t;
+    int lo = 0, hi = B;         // the last b with q_start[b] <= t is in [lo - 1, hi - 1]
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (q_start[mid] <= t) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo > 0 && t < q_start[lo] ? lo - 1 : -1;
+}
+
 // Checks a descriptor and fills the view; `who` names the call in the message.
 inline int view_of(const kv4_cache* c, const char* who, CacheView* v) {
     if (!c || !c->pages) return qmoe::fail(QMOE_EINVAL, std::string(who) + ": NULL cache");

@@ -258,6 +258,34 @@ int qmoe_route(const float* logits, int T, int E, int k, int32_t* ids,
                float* gates, void* stream);
 
 /*
+ * Router with the scores and the choice that later expert layers use.  For each token
+ *   s = softmax(l) or 1 / (1 + e^-l)  over its logits l,   c = s + bias  (what is chosen by),
+ * a group's value is the sum of its group_best largest c, experts outside the top_groups best
+ * groups are left out, and the k experts of largest c are chosen, largest first.  Equal values go
+ * to the lower index (of the group, of the expert).
+ *   gate = s of the chosen, over the sum of the chosen s when renormalise, times scale.
+ *  logits  device fp32 or bf16 [T][E], rows row_stride elements apart.  NaN is read as -infinity
+ *          (score 0), +infinity as the largest finite value.
+ *  score   QMOE_SCORE_SOFTMAX or QMOE_SCORE_SIGMOID.
+ *  bias    device fp32 [E], or NULL.  A value that is NaN counts as -infinity.
+ *  n_groups  groups of E / n_groups neighbouring experts (1: no groups), at most 32;
+ *  group_best  1 or 2 (ignored with one group).
+ *  ids     device out int32 [T][k];  gates device out fp32 [T][k].
+ * Values are compared as 64-bit floats made in 64 bits (without a bias experts are in the order of
+ * their logits, and with group_best 1 groups in that of their largest): fp32 decides where its error
+ * leaves no doubt, and the other rows are decided again.  Gates are fp32; a row without a finite
+ * logit has gates 0; renormalised gates keep their ratios when the scores themselves are below
+ * fp32's range.
+ * Errors: EINVAL (sizes as qmoe_route; E not a multiple of n_groups, fewer than k experts in the
+ * kept groups), EUNSUPPORTED (groups with E > 1024), ECUDA.
+ */
+#define QMOE_SCORE_SOFTMAX 0
+#define QMOE_SCORE_SIGMOID 1
+int qmoe_route_scored(const void* logits, int logits_are_f32, int64_t row_stride, int T, int E, int k, int score,
+                      const float* bias, int n_groups, int top_groups, int group_best, int renormalise, float scale,
+                      int32_t* ids, float* gates, void* stream);
+
+/*
  * Bucketiser (step a2): stable counting sort of the flat slots t*k + j by
  * expert ids[t][j].  counts[E], offsets[E+1] (exclusive prefix sum) and
  * perm[T*k] (slots of expert e, increasing, at perm[offsets[e]..]) are
@@ -607,6 +635,32 @@ int qk_norm_rope(const void* qkv, int64_t row_stride, int T, int n_q_heads, int 
                  void* q_out, void* k_out, const kv4_cache* cache, const int32_t* slots, void* stream);
 
 /*
+ * Norm of whole rows, with the residual's addition before it:
+ *   h = x + residual,  residual_out = bf16(h),  y = h / sqrt(mean(h^2) + eps) * weight,
+ * in fp32 (the norm is that of the unrounded h), each output rounded once.  In 8 bits: codes are
+ * e4m3 values of y / s (y before its rounding to bf16), nearest even, with s = max |y| / 448 over the
+ * row or over each 128 values of it (the last run of a row may be shorter); s is 0 and the codes 0
+ * where all y are 0.
+ *  x         device fp32 or bf16: T rows of n values, x_stride elements apart.
+ *  residual  device bf16 rows, or NULL;  residual_out  device out bf16 rows (may be residual itself,
+ *            with its stride; NULL without a residual).
+ *  weight    device bf16 [n], or NULL for 1.
+ *  y         device out bf16 rows, or NULL when codes are given; may be x (bf16, the same stride).
+ *  codes     device out uint8 [T][n], or NULL;  scales device out fp32 [T] when scale_group is 0,
+ *            [T][ceil(n / 128)] when it is 128.
+ *  n         1 .. 32768;  eps positive.
+ * Other overlaps between outputs and inputs are not allowed.  A row with a NaN or an infinity gives
+ * what the formula gives (NaN, or 0 for its finite values beside an infinity); squares are fp32, so rows
+ * with values of 1e19 and more overflow to that too.  Rows whose width, strides and
+ * addresses allow 16-byte accesses take fewer instructions; the others are as exact.
+ * Errors: EINVAL (sizes, strides below n, NULL, alignment to the type), EUNSUPPORTED (codes with n
+ * or a stride that is no multiple of 8, or pointers not 16-byte aligned (codes 8); another scale_group).
+ */
+int add_rms_norm(const void* x, int x_is_f32, int64_t x_stride, const void* residual, int64_t residual_stride,
+                 void* residual_out, int64_t residual_out_stride, const void* weight, int T, int n, float eps, void* y,
+                 int64_t y_stride, void* codes, float* scales, int scale_group, void* stream);
+
+/*
  * Quantise T tokens' keys and values into the cache.  Token t's heads start
  * at k + t * k_stride and v + t * v_stride (bf16, heads contiguous), and go
  * to slots[t] as in qk_norm_rope.  Errors: EINVAL; on the device EINVAL (a
@@ -663,6 +717,79 @@ int kv4_attention_ws_size(int B, int n_q_heads, int n_kv_heads, int head_dim, in
 int kv4_attention(const kv4_cache* cache, const void* q, int n_q_tokens, int n_q_heads, const int32_t* q_start,
                   const int32_t* kv_len, int B, const int32_t* table, int max_blocks, int max_q, int max_kv,
                   float scale, int causal, int window, void* out, void* workspace, size_t ws_bytes, void* stream);
+
+/* ----------------------------------------------------------------------
+ * Attention over chosen blocks.  For long contexts a query attends to the blocks (pages) of its
+ * request whose keys may give it the largest scores, instead of all: bounds of each block's keys are
+ * kept beside the cache, every query and kv head chooses its blocks by them, and attention reads those.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Bounds of the keys of each block and kv head: per channel d the largest and the smallest key,
+ *   hi_d = ceil(max_j k_jd / step),  lo_d = floor(min_j k_jd / step),
+ * k being the values that the 4-bit cache stands for (s u + z rounded to fp32) and step the smallest
+ * power of two with which all of them are within -127 .. 127 (0, with codes 0, when all keys are 0).
+ *  codes  device int8 [n_pages][n_kv_heads][2][head_dim]: hi, then lo; 16-byte aligned.
+ *  steps  device fp32 [n_pages][n_kv_heads].
+ */
+typedef struct {
+    void* codes;
+    float* steps;
+    int n_pages, page_size, n_kv_heads, head_dim;
+} kv4_bounds;
+
+/*
+ * Bring the bounds up to date after tokens were written to the cache at slots (device int32 [n], -1
+ * skips): the bounds of each page among them, over its tokens up to the last written one, are made
+ * from the cache.  slots as kv4_block_tables gives them: the tokens of a page next to each other and
+ * in order.  Errors: EINVAL (other sizes than the cache's); on the device EINVAL (a slot outside the
+ * cache: skipped).
+ */
+int kv4_block_bounds(const kv4_cache* cache, const kv4_bounds* bounds, const int32_t* slots, int n, void* stream);
+
+/*
+ * Choose the blocks that each query token and kv head attends to.  A query at position p of its
+ * request (positions as in kv4_attention with causal) sees blocks 0 .. p / page_size.  Of these, the
+ * first `first` and the last `last` are taken, and then those with the largest
+ *   score = step * sum_d (hi_d * sum_g max(q_gd, 0) + lo_d * sum_g min(q_gd, 0)),
+ * an upper bound of the sum over the group's query heads g of q_g . k for any key of the block (up to
+ * q's rounding), to `top` blocks in all; equal scores go to the lower block.  q enters as whole numbers: q_gd
+ * times the power of two that brings the group's largest magnitude into [2^(b-1), 2^b), rounded
+ * (nearest even) and kept within +-(2^b - 1), with b = 15 - ceil(log2(heads per kv head)); NaN is read as 0, an infinity as the largest
+ * finite value.  The sum is exact; it is rounded once to fp32, and so is its product with step.
+ *  q, q_start, kv_len, table, max_kv  as in kv4_attention.
+ *  sel     device out int32 [n_q_tokens][n_kv_heads][top]: block numbers, ascending, then -1.  A query
+ *          that sees top blocks or fewer has them all.
+ *  top     1 .. 65536;  first, last >= 0, first + last <= top.
+ *  workspace  device, ws_bytes >= kv4_select_blocks_ws_size(...), 16-byte aligned (no smaller for larger
+ *          n_q_tokens or max_kv).
+ * Rows of sel that belong to no request are left as they are.  A block without a page in the cache has
+ * score -infinity (EINVAL in the error word).  A request whose kv_len is negative (EINVAL) or above
+ * max_kv (ECAPACITY) gets lists of -1.
+ * Errors: EINVAL, EUNSUPPORTED (more than 128 query heads per kv head), ECAPACITY (workspace).
+ */
+int kv4_select_blocks_ws_size(int n_q_tokens, int n_kv_heads, int page_size, int max_kv, size_t* bytes);
+int kv4_select_blocks(const kv4_bounds* bounds, const void* q, int n_q_tokens, int n_q_heads, const int32_t* q_start,
+                      const int32_t* kv_len, int B, const int32_t* table, int max_blocks, int max_kv, int top, int first,
+                      int last, int32_t* sel, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * kv4_attention where each query token and kv head sees the tokens of its own list of blocks only (and,
+ * of those, the ones up to its position):
+ *  sel     device int32 [n_q_tokens][n_kv_heads][top], as kv4_select_blocks writes it.  Of a query that
+ *          sees nb blocks the first min(top, nb) entries are read; -1, and a block that the query does not
+ *          see, name no tokens.  A block listed twice counts twice.
+ *  workspace  device, ws_bytes >= kv4_attention_blocks_ws_size(...), 16-byte aligned.
+ * The other arguments, the arithmetic (that of requests with few query rows) and the rows that are left as they are: as in
+ * kv4_attention with causal.
+ * Errors: EINVAL, EUNSUPPORTED (head_dim, more than 32 query heads per kv head), ECAPACITY; on the
+ * device EINVAL (a listed block without a page in the cache: its tokens are not seen; an entry below -1; a
+ * kv_len that is negative or above 2^31 - 128: its rows are skipped).
+ */
+int kv4_attention_blocks_ws_size(int n_q_tokens, int n_q_heads, int n_kv_heads, int head_dim, int page_size, int top, size_t* bytes);
+int kv4_attention_blocks(const kv4_cache* cache, const void* q, int n_q_tokens, int n_q_heads, const int32_t* q_start,
+                         const int32_t* kv_len, int B, const int32_t* table, int max_blocks, const int32_t* sel, int top,
+                         float scale, void* out, void* workspace, size_t ws_bytes, void* stream);
 
 /* ======================================================================
  * Status and test exports
