@@ -229,12 +229,15 @@ int launch_norm(const NormArgs& a, cudaStream_t st) {
 // c; the k best experts by c of the best groups; gates s, or s over the sum of the chosen, times a factor.
 //
 // The order is that of the values in 64 bits, equal ones to the lower index.  Without a bias an expert's order is its
-// logit's, exactly.  Else the values are made in fp32 with a bound on their error, and a row in which two neighbours in
-// the order are nearer than their bounds (and are not the same logit with the same bias) is decided again in fp64.
+// logit's, exactly.  Else the values are made in fp32 with a bound on their error (the approximate exponential and reciprocal
+// are enough), and where two neighbours in the order are nearer than their bounds, and are not the same logit with the
+// same bias, those are made in fp64: of the experts in question (fp64 runs at a 64th of fp32's rate here), of the groups' best
+// ones, or of a whole row where more of its experts are in question than the list of the chosen holds.
 //
-// A lane holds R neighbouring experts, so that among lanes with equal values the lowest has the lowest index: a round of
-// the choice is a reduction of the lanes' best keys (one instruction) and a ballot.  A warp takes a token; above 1024 experts a
-// block of 8 warps does, each warp's best k + 1 being merged by the first.
+// A lane holds R neighbouring experts as integer keys, and the 8 best of them sorted; among lanes with equal keys the
+// lowest has the lowest index.  A round of the choice is a reduction of the lanes' heads (one instruction), a ballot, and the
+// winner's list moving up.  Which expert a key was is looked up at the end, for all the chosen at once.  A warp takes a
+// token; above 1024 experts a block of 8 warps does, each warp's best being merged by the first.
 struct RouteArgs {
     const void* logits;
     const float* bias;
@@ -242,17 +245,19 @@ struct RouteArgs {
     float* gates;
     int64_t stride;
     int T, E, k, sigmoid, groups, top_groups, best, renorm;
+    int vec, vec_bias;      // rows (the bias) allow loads of 16 bytes, or of all of a lane's values where those are fewer
     float scale;
 };
 
 constexpr int kRouteWarps = 8;
 constexpr float kUlp = 5.9604645e-8f;       // 2^-24
 constexpr float kLargest = 3.402823466e38f;
+constexpr float kLog2e = 1.4426950408889634f;
 
-// fp32 -> integer of the same order (NaN is read as -infinity, -0 as 0); 0 stands for no value.
+// fp32 -> integer of the same order (-0 as 0); 0 stands for no value.
 __device__ __forceinline__ uint32_t key_of(float v) {
     const uint32_t u = __float_as_uint(v + 0.f);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
@@ -263,21 +268,165 @@ __device__ __forceinline__ unsigned long long key_of(double v) {
 }
 
 // A logit as it is read: NaN as -infinity, +infinity as the largest finite value.
+__device__ __forceinline__ float clean(float v) { return fminf(fmaxf(v, -INFINITY), kLargest); }
 template <typename X>
 __device__ __forceinline__ float logit(const X* row, int e) {
-    const float v = sizeof(X) == 2 ? bf16_to_f32(((const uint16_t*)row)[e]) : ((const float*)row)[e];
-    return v == v ? fminf(v, kLargest) : -INFINITY;
+    return clean(sizeof(X) == 2 ? bf16_to_f32(((const uint16_t*)row)[e]) : ((const float*)row)[e]);
 }
 
-// A value of the choice: NaN (an infinite bias of the other sign) as -infinity.
-__device__ __forceinline__ float plain_value(float c) { return c == c ? c : -INFINITY; }
+// R values from p[e0] on, `none` past E.
+template <typename X, int R>
+__device__ __forceinline__ void load_values(const X* p, int e0, int E, int vec, float none, float (&v)[R]) {
+    constexpr int W = R * (int)sizeof(X) < 16 ? R : 16 / (int)sizeof(X);      // values of a wide load
+#pragma unroll
+    for (int i = 0; i < R; ++i) v[i] = none;
+    if (vec) {
+#pragma unroll
+        for (int c = 0; c < R; c += W) {
+            if (e0 + c >= E) break;      // (E is a multiple of W)
+            uint32_t w[W * sizeof(X) >= 4 ? W * sizeof(X) / 4 : 1];
+            if constexpr (W * sizeof(X) == 16) {
+                const uint4 x = *(const uint4*)(p + e0 + c);
+                w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+            } else if constexpr (W * sizeof(X) == 8) {
+                const uint2 x = *(const uint2*)(p + e0 + c);
+                w[0] = x.x, w[1] = x.y;
+            } else if constexpr (W * sizeof(X) == 4) {
+                w[0] = *(const uint32_t*)(p + e0 + c);
+            } else {
+                w[0] = *(const uint16_t*)(p + e0 + c);
+            }
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                v[c + i] = sizeof(X) == 4 ? __uint_as_float(w[sizeof(X) == 4 ? i : 0]) : i & 1 ? bf16_hi(w[sizeof(X) == 4 ? 0 : i / 2]) : bf16_lo(w[sizeof(X) == 4 ? 0 : i / 2]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (e0 + i < E) v[i] = sizeof(X) == 2 ? bf16_to_f32(((const uint16_t*)p)[e0 + i]) : ((const float*)p)[e0 + i];
+    }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Within 6 2^-24: (1.5 |l| + 4) 2^-24 of the exponential, which the score's slope s (1 - s) makes 1.4, and 3 of the rest.
+__device__ __forceinline__ float sigmoid_near(float l) { return rcp(1.f + ex2(-kLog2e * l)); }
+
+// ---- sorted lists of keys, the largest first
+__device__ __forceinline__ void order(uint32_t& a, uint32_t& b) {
+    const uint32_t hi = max(a, b);
+    b = min(a, b), a = hi;
+}
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t* v) {
+    if constexpr (N == 2) {
+        order(v[0], v[1]);
+    } else if constexpr (N == 4) {
+        order(v[0], v[1]), order(v[2], v[3]), order(v[0], v[2]), order(v[1], v[3]), order(v[1], v[2]);
+    } else if constexpr (N == 8) {
+        // Batcher's odd-even merge sort
+        sort_keys<4>(v), sort_keys<4>(v + 4);
+        order(v[0], v[4]), order(v[1], v[5]), order(v[2], v[6]), order(v[3], v[7]);
+        order(v[2], v[4]), order(v[3], v[5]);
+        order(v[1], v[2]), order(v[3], v[4]), order(v[5], v[6]);
+    }
+}
+template <int R>
+constexpr int kDepth = R < 8 ? R : 8;
+
+// The best kDepth<R> of R keys.
+template <int R>
+__device__ __forceinline__ void best_keys(const uint32_t (&key)[R], uint32_t (&list)[kDepth<R>]) {
+#pragma unroll
+    for (int i = 0; i < kDepth<R>; ++i) list[i] = key[i];
+    sort_keys<kDepth<R>>(list);
+#pragma unroll
+    for (int c = 8; c < R; c += 8) {
+        uint32_t more[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) more[i] = key[c + i];
+        sort_keys<8>(more);
+        // the larger halves of a bitonic sequence, then its merge
+#pragma unroll
+        for (int i = 0; i < kDepth<R>; ++i) list[i] = max(list[i], more[7 - i]);
+#pragma unroll
+        for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+            for (int i = 0; i < kDepth<R>; ++i)
+                if (!(i & d)) order(list[i], list[(i + d) & 7]);
+    }
+}
+
+// The `rounds` best of all lanes' lists: lane j gets the j-th one's key and the lane that held it.  False when a lane of
+// more than 8 keys gave away all that its list held.
+template <int R>
+__device__ __forceinline__ bool choose(uint32_t (&list)[kDepth<R>], int rounds, int lane, uint32_t* my_key, int* my_lane) {
+    *my_key = 0, *my_lane = 0;
+    int given = 0;
+    for (int j = 0; j < rounds; ++j) {
+        const uint32_t m = __reduce_max_sync(QMOE_FULL_MASK, list[0]);
+        const int w = __ffs(__ballot_sync(QMOE_FULL_MASK, list[0] == m)) - 1;
+        if (lane == j) *my_key = m, *my_lane = w;
+        const bool mine = lane == w;
+        if (R > 8) given += mine && m;
+#pragma unroll
+        for (int i = 0; i + 1 < kDepth<R>; ++i) list[i] = mine ? list[i + 1] : list[i];
+        list[kDepth<R> - 1] = mine ? 0u : list[kDepth<R> - 1];
+    }
+    return R <= 8 || !__any_sync(QMOE_FULL_MASK, given >= 8);
+}
+
+// Which of its lane's experts the key of lane j's choice was: the first with that key, or the one after where the same
+// lane gave the same key the round before.
+template <int R>
+__device__ __forceinline__ int which(const uint32_t (&key)[R], uint32_t my_key, int my_lane, int lane) {
+    const uint32_t before = __shfl_up_sync(QMOE_FULL_MASK, my_key, 1);
+    const int from = __shfl_up_sync(QMOE_FULL_MASK, my_lane, 1);
+    const unsigned starts = __ballot_sync(QMOE_FULL_MASK, lane == 0 || before != my_key || from != my_lane);
+    int skip = lane - (31 - __clz((int)(starts & (0xFFFFFFFFu >> (31 - lane)))));
+    int at = R - 1;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const bool hit = __shfl_sync(QMOE_FULL_MASK, key[i], my_lane) == my_key;
+        if (hit && skip == 0) at = i;
+        skip -= hit;
+    }
+    return my_lane * R + at;
+}
+
+// As choose and which, from the keys themselves (any number of a lane's), which it takes out; the slow way.  The remaining
+// keys' largest is returned.
+template <int R>
+__device__ __noinline__ uint32_t choose_slow(uint32_t* key, int rounds, int lane, uint32_t* my_key, int* my_at) {
+    *my_key = 0, *my_at = -1;
+    uint32_t best = 0;
+    int at = 0;
+    for (int j = 0; j <= rounds; ++j) {
+        best = 0;
+        for (int i = 0; i < R; ++i)
+            if (key[i] > best) best = key[i], at = i;
+        const uint32_t m = __reduce_max_sync(QMOE_FULL_MASK, best);
+        if (j == rounds) break;
+        const int w = __ffs(__ballot_sync(QMOE_FULL_MASK, best == m)) - 1;
+        const int tag = __shfl_sync(QMOE_FULL_MASK, lane * R + at, w);
+        if (lane == j) *my_key = m, *my_at = m ? tag : -1;
+        if (lane == w) key[at] = 0;
+    }
+    return best;
+}
 
 struct Pair {
-    float a, b;      // the best and the second best
+    uint32_t a, b;      // keys of the best and the second best
 };
-__device__ __forceinline__ Pair merge(Pair x, Pair y) {
-    return Pair{fmaxf(x.a, y.a), fmaxf(fminf(x.a, y.a), fmaxf(x.b, y.b))};
-}
+__device__ __forceinline__ Pair merge(Pair x, Pair y) { return Pair{max(x.a, y.a), max(min(x.a, y.a), max(x.b, y.b))}; }
 
 // Which groups are kept (bit g of the result), from values that lane g holds for g < groups.
 template <typename F>
@@ -290,16 +439,11 @@ __device__ __forceinline__ uint32_t best_groups(F v, int groups, int top, int la
     return __ballot_sync(QMOE_FULL_MASK, lane < groups && rank < top);
 }
 
+// ---- in 64 bits
 __device__ __forceinline__ unsigned long long warp_max64(unsigned long long v) {
     const uint32_t hi = __reduce_max_sync(QMOE_FULL_MASK, (uint32_t)(v >> 32));
     const uint32_t lo = __reduce_max_sync(QMOE_FULL_MASK, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
     return (unsigned long long)hi << 32 | lo;
-}
-
-__device__ __forceinline__ double warp_sum_d(double v) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(QMOE_FULL_MASK, v, d);
-    return v;
 }
 
 struct ResolveShared {
@@ -307,73 +451,76 @@ struct ResolveShared {
     unsigned long long key[kRouteWarps];
 };
 
-// The choice in 64 bits, by NW warps: lane j of the first gets the j-th expert.  `cand`: bit i is set where expert e0 + i may be
-// among the chosen (all of them where the groups are to be decided too).
+// Sum of the row's exponentials, by NW warps that hold R experts a lane from e0 on (1 for sigmoid scores).
 template <typename X, int NW>
-__device__ __noinline__ int resolve(const RouteArgs& a, const X* row, int e0, int R, float top, uint32_t cand, bool groups_too,
-                                    ResolveShared* sh) {
-    const int lane = threadIdx.x & 31, warp = NW == 1 ? 0 : threadIdx.x >> 5;
-    double c[32], z = 1.0;
-    if (!a.sigmoid) {
-        double mine = 0.0;
+__device__ __noinline__ double exact_sum(const RouteArgs& a, const X* row, int e0, int R, float top, ResolveShared* sh) {
+    if (a.sigmoid) return 1.0;
+    double z = 0.0;
+    for (int i = 0; i < R && e0 + i < a.E; ++i) {
+        const float l = logit(row, e0 + i);
+        if (l > -INFINITY) z += exp((double)l - (double)top);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(QMOE_FULL_MASK, z, d);
+    if (NW > 1) {
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) sh->sum[threadIdx.x >> 5] = z;
+        __syncthreads();
+        z = 0.0;
+        for (int w = 0; w < NW; ++w) z += sh->sum[w];
+    }
+    return z > 0.0 ? z : 1.0;
+}
+
+// Value c of expert e.
+template <typename X>
+__device__ __noinline__ double exact_value(const RouteArgs& a, const X* row, int e, float top, double z) {
+    const double l = logit(row, e);
+    double s = l > -INFINITY ? a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / z : 0.0;
+    if (a.bias) s += (double)a.bias[e];
+    return s == s ? s : -INFINITY;
+}
+
+// Values of the groups in `which`, to lane g for group g, from the experts that each lane names (bit i of `cand`: e0 + i).
+template <typename X>
+__device__ __noinline__ double exact_groups(const RouteArgs& a, const X* row, int e0, int R, float top, uint32_t cand, uint32_t which_groups) {
+    const int lane = threadIdx.x & 31, size = a.E / a.groups;
+    const double z = exact_sum<X, 1>(a, row, e0, R, top, nullptr);
+    double c[32], mine = 0.0;
+    for (int i = 0; i < R; ++i) c[i] = (cand >> i) & 1 ? exact_value(a, row, e0 + i, top, z) : -INFINITY;
+    for (uint32_t todo = which_groups; todo; todo &= todo - 1) {
+        const int g = __ffs(todo) - 1;
+        double b0 = -INFINITY, b1 = -INFINITY;
         for (int i = 0; i < R; ++i) {
-            const float l = e0 + i < a.E ? logit(row, e0 + i) : -INFINITY;
-            if (l > -INFINITY) mine += exp((double)l - (double)top);
+            if (e0 + i < g * size || e0 + i >= (g + 1) * size) continue;
+            b1 = fmax(b1, fmin(b0, c[i]));
+            b0 = fmax(b0, c[i]);
         }
-        z = warp_sum_d(mine);
-        if (NW > 1) {
-            if (lane == 0) sh->sum[warp] = z;
-            __syncthreads();
-            z = 0.0;
-            for (int w = 0; w < NW; ++w) z += sh->sum[w];
+        for (int d = 16; d > 0; d >>= 1) {
+            const double o0 = __shfl_xor_sync(QMOE_FULL_MASK, b0, d), o1 = __shfl_xor_sync(QMOE_FULL_MASK, b1, d);
+            b1 = fmax(fmin(b0, o0), fmax(b1, o1));
+            b0 = fmax(b0, o0);
         }
+        double v = a.best == 2 ? b0 + b1 : b0;
+        if (v != v) v = -INFINITY;
+        if (lane == g) mine = v;
     }
-    for (int i = 0; i < R; ++i) {
-        c[i] = -INFINITY;
-        if (!((cand >> i) & 1)) continue;
-        const double l = logit(row, e0 + i);
-        double s = 0.0;
-        if (l > -INFINITY) s = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / z;
-        if (a.bias) s += (double)a.bias[e0 + i];
-        c[i] = s == s ? s : -INFINITY;
-    }
-    if (groups_too) {
-        const int size = a.E / a.groups;
-        double mine = 0.0;
-        for (int g = 0; g < a.groups; ++g) {
-            double b0 = -INFINITY, b1 = -INFINITY;
-            for (int i = 0; i < R; ++i) {
-                const int e = e0 + i;
-                if (e < g * size || e >= (g + 1) * size) continue;
-                b1 = fmax(b1, fmin(b0, c[i]));
-                b0 = fmax(b0, c[i]);
-            }
-            for (int d = 16; d > 0; d >>= 1) {
-                const double o0 = __shfl_xor_sync(QMOE_FULL_MASK, b0, d), o1 = __shfl_xor_sync(QMOE_FULL_MASK, b1, d);
-                b1 = fmax(fmin(b0, o0), fmax(b1, o1));
-                b0 = fmax(b0, o0);
-            }
-            double v = a.best == 2 ? b0 + b1 : b0;
-            if (v != v) v = -INFINITY;
-            if (lane == g) mine = v;
-        }
-        const uint32_t kept = best_groups(mine, a.groups, a.top_groups, lane);
-        for (int i = 0; i < R; ++i)
-            if (e0 + i < a.E && !((kept >> ((e0 + i) / size)) & 1)) cand &= ~(1u << i);
-    }
-    // (without a bias the order is the logits'; sums of scores have decided the groups)
-    if (!a.bias)
-        for (int i = 0; i < R; ++i)
-            if ((cand >> i) & 1) c[i] = logit(row, e0 + i);
+    return mine;
+}
+
+// The choice among the experts that each lane names, by NW warps: lane j of each gets the j-th expert.
+template <typename X, int NW>
+__device__ __noinline__ int exact_choice(const RouteArgs& a, const X* row, int e0, int R, float top, uint32_t cand, ResolveShared* sh) {
+    const int lane = threadIdx.x & 31, warp = NW == 1 ? 0 : threadIdx.x >> 5;
+    const double z = exact_sum<X, NW>(a, row, e0, R, top, sh);
+    unsigned long long c[32];
+    for (int i = 0; i < R; ++i) c[i] = (cand >> i) & 1 ? key_of(exact_value(a, row, e0 + i, top, z)) : 0ull;
     int got = 0;
     for (int j = 0; j < a.k; ++j) {
         unsigned long long best = 0;
         int at = 0;
         for (int i = 0; i < R; ++i)
-            if ((cand >> i) & 1) {
-                const unsigned long long key = key_of(c[i]);
-                if (key > best) best = key, at = i;
-            }
+            if (c[i] > best) best = c[i], at = i;
         unsigned long long m = warp_max64(best);
         bool here = true;
         if (NW > 1) {
@@ -392,7 +539,7 @@ __device__ __noinline__ int resolve(const RouteArgs& a, const X* row, int e0, in
         if (who) {
             const int w = __ffs(who) - 1;
             e = __shfl_sync(QMOE_FULL_MASK, e0 + at, w);
-            if (lane == w) cand &= ~(1u << at);
+            if (lane == w) c[at] = 0;
         }
         if (NW > 1) {
             __syncthreads();
@@ -405,56 +552,51 @@ __device__ __noinline__ int resolve(const RouteArgs& a, const X* row, int e0, in
     return got;
 }
 
-// The k + 1 best of the values that the lanes hold (R each, keys; 0: none): lane j gets the j-th one's key and tag, and
-// the last round's go to every lane.  Keys are taken out of `key`.
-template <int R>
-__device__ __forceinline__ void choose(uint32_t (&key)[R], int rounds, int lane, uint32_t* my_key, int* my_at) {
-    uint32_t best = 0;
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-        if (key[i] > best) best = key[i], at = i;
-    *my_key = 0, *my_at = -1;
-    for (int j = 0; j < rounds; ++j) {
-        const uint32_t m = __reduce_max_sync(QMOE_FULL_MASK, best);
-        const int w = __ffs(__ballot_sync(QMOE_FULL_MASK, best == m)) - 1;
-        const int tag = __shfl_sync(QMOE_FULL_MASK, lane * R + at, w);
-        if (lane == j) *my_key = m, *my_at = m ? tag : -1;
-        if (lane == w) {
-            best = 0;
-            const int gone = at;
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-                if (i == gone) key[i] = 0;
-                if (key[i] > best) best = key[i], at = i;
-            }
-        }
+// The list of lanes 0 .. n - 1 in the order of its values, those of lanes with `near` in 64 bits.
+template <typename X>
+__device__ __noinline__ int exact_order(const RouteArgs& a, const X* row, int n, float value, int at, bool near, float top, double z) {
+    const int lane = threadIdx.x & 31;
+    const double c = near ? exact_value(a, row, at, top, z) : (double)value;
+    int rank = 0, got = at;
+    for (int j = 0; j < n; ++j) {
+        const double o = __shfl_sync(QMOE_FULL_MASK, c, j);
+        const int e = __shfl_sync(QMOE_FULL_MASK, at, j);
+        rank += o > c || (o == c && e < at);
     }
+    for (int j = 0; j < n; ++j) {
+        const int r = __shfl_sync(QMOE_FULL_MASK, rank, j), e = __shfl_sync(QMOE_FULL_MASK, at, j);
+        if (r == lane) got = e;
+    }
+    return got;
 }
 
-// Gates of the experts that lanes 0 .. k - 1 hold, and the outputs of token t.  Renormalised weights are taken relative to the
-// largest, so that scores below fp32's range keep their ratios.
-template <typename X>
-__device__ __forceinline__ void write_route(const RouteArgs& a, const X* row, int64_t t, int id, float top, float z, int lane) {
+// Gates of the experts that lanes 0 .. k - 1 hold (l: their logits), and the outputs of token t.  Renormalised weights are taken
+// relative to the largest, so that scores below fp32's range keep their ratios.
+__device__ __forceinline__ void write_route(const RouteArgs& a, int64_t t, int id, float l, float top, float z, int lane) {
     const bool on = lane < a.k;
-    const float l = on ? logit(row, id) : -INFINITY;
+    if (!on) l = -INFINITY;
     float g = 0.f;
     if (a.renorm) {
         float big = l;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor_sync(QMOE_FULL_MASK, big, d));
         if (l > -INFINITY) {
-            if (!a.sigmoid)
+            if (!a.sigmoid) {
                 g = expf(l - big);
-            else if (l >= 0.f)
-                g = 1.f / (1.f + expf(-l));
-            else
-                g = expf(l - fminf(big, 0.f)) / (1.f + expf(l));
+            } else {
+                const float e = expf(-fabsf(l));      // 1 / (1 + e^-l) = e^l / (1 + e^l)
+                g = (l >= 0.f ? 1.f : big >= 0.f ? e : expf(l - big)) / (1.f + e);
+            }
         }
         const float sum = warp_sum(g);
         g = sum > 0.f ? g / sum : 0.f;
     } else if (l > -INFINITY) {
-        g = a.sigmoid ? (l >= 0.f ? 1.f / (1.f + expf(-l)) : expf(l) / (1.f + expf(l))) : expf(l - top) / z;
+        if (a.sigmoid) {
+            const float e = expf(-fabsf(l));
+            g = (l >= 0.f ? 1.f : e) / (1.f + e);
+        } else {
+            g = expf(l - top) / z;
+        }
     }
     if (on) {
         a.ids[t * a.k + lane] = id;
@@ -470,27 +612,30 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
     __shared__ uint32_t key_s[NW > 1 ? kRouteWarps * 32 : 1];
     __shared__ int id_s[NW > 1 ? kRouteWarps * 32 : 1];
     __shared__ float2 bound_s;
+    __shared__ uint32_t left_s[kRouteWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = NW == 1 ? (int64_t)blockIdx.x * kRouteWarps + warp : blockIdx.x;
     if (t >= a.T) return;
     const X* row = (const X*)a.logits + t * a.stride;
     const int e0 = (NW == 1 ? lane : (int)threadIdx.x) * R;
-    float l[R];
+    float c[R];
+    load_values<X, R>(row, e0, a.E, a.vec, -INFINITY, c);
 #pragma unroll
-    for (int i = 0; i < R; ++i) l[i] = e0 + i < a.E ? logit(row, e0 + i) : -INFINITY;
-    // ---- softmax: largest logit and sum of exponentials
+    for (int i = 0; i < R; ++i) c[i] = clean(c[i]);
+    // ---- softmax: largest logit and sum of exponentials, where they are needed
+    const bool by_logit = !a.bias, sums = a.groups > 1 && a.best == 2;
     float top = 0.f, z = 1.f;
-    if (!a.sigmoid) {
-        top = l[0];
+    if (!a.sigmoid && !(by_logit && a.renorm && !sums)) {
+        top = c[0];
 #pragma unroll
-        for (int i = 1; i < R; ++i) top = fmaxf(top, l[i]);
+        for (int i = 1; i < R; ++i) top = fmaxf(top, c[i]);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(QMOE_FULL_MASK, top, d));
         const float m = top > -INFINITY ? top : 0.f;
-        z = 0.f;
+        float part[4] = {};
 #pragma unroll
-        for (int i = 0; i < R; ++i) z += expf(l[i] - m);
-        z = warp_sum(z);
+        for (int i = 0; i < R; ++i) part[i & 3] += ex2(kLog2e * (c[i] - m));
+        z = warp_sum((part[0] + part[1]) + (part[2] + part[3]));
         if (NW > 1) {
             if (lane == 0) part_s[warp] = make_float2(top, z);
             __syncthreads();
@@ -498,149 +643,188 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
             top = p.x;
 #pragma unroll
             for (int d = NW / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(QMOE_FULL_MASK, top, d));
-            z = p.x > -INFINITY ? p.y * expf(p.x - top) : 0.f;
+            z = p.x > -INFINITY ? p.y * ex2(kLog2e * (p.x - top)) : 0.f;
 #pragma unroll
             for (int d = NW / 2; d > 0; d >>= 1) z += __shfl_xor_sync(QMOE_FULL_MASK, z, d);
         }
         if (!(top > -INFINITY)) top = 0.f, z = 1.f;      // nothing in the row: scores 0
     }
-    // ---- values, and the bound on their error besides the last addition's: a score has at most (|x| + 3) 2^-24 of itself
-    // from its exponential (x = l - top), the sum that and an addition's for each term; a sigmoid score 6 2^-24
-    const bool by_logit = !a.bias;
-    float c[R];
-    const float slack = by_logit ? 0.f : fmaf(a.sigmoid ? 6.f : (float)(2 * R + 48) / z, kUlp, 1e-37f);
+    // ---- values, and the bound on a score's error: sigmoid_near's; or, with x = l - top, (2.5 |x| + 4) 2^-24 of itself from an
+    // exponential (|x| e^x <= 0.37), the same of the sum (|x| weighed by the scores is at most ln E) and R / 4 + 17 additions, and a
+    // quotient's 3
+    const float score_err = fmaf(a.sigmoid ? 6.f : (float)(R / 4 + 64) / z, kUlp, 1e-37f);
+    const float inv_z = 1.f / z;
+    auto score_near = [&](float l) { return a.sigmoid ? sigmoid_near(l) : ex2(kLog2e * (l - top)) * inv_z; };
+    if (!by_logit) {
+        float bias[R];
+        load_values<float, R>(a.bias, e0, a.E, a.vec_bias, 0.f, bias);
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        c[i] = l[i];
-        if (!by_logit || (a.groups > 1 && a.best == 2)) {
-            float s = a.sigmoid ? 1.f / (1.f + expf(-l[i])) : expf(l[i] - top) / z;
-            if (a.bias) s = plain_value(s + (e0 + i < a.E ? a.bias[e0 + i] : 0.f));
-            c[i] = s;
-        }
+        for (int i = 0; i < R; ++i) c[i] = fmaxf(score_near(c[i]) + bias[i], -INFINITY);      // (an infinite bias may give NaN)
     }
-    bool again = false, groups_too = false;
-    uint32_t in = 0;      // experts that may be chosen
+    uint32_t key[R], list[kDepth<R>];
 #pragma unroll
-    for (int i = 0; i < R; ++i) in |= e0 + i < a.E ? 1u << i : 0u;
-    const uint32_t all = in;
+    for (int i = 0; i < R; ++i) key[i] = e0 + i < a.E ? key_of(c[i]) : 0u;
+    const float slack = by_logit ? 0.f : score_err;
+    best_keys<R>(key, list);
     if constexpr (NW == 1) {
         if (a.groups > 1) {
             // ---- groups
             const int size = a.E / a.groups, lanes = size / R;
-            Pair mine{-INFINITY, -INFINITY};
-            if (size % R == 0 && (lanes & (lanes - 1)) == 0) {
-                // a group is a power of two of whole lanes
-                Pair p{-INFINITY, -INFINITY};
-#pragma unroll
-                for (int i = 0; i < R; ++i) p = merge(p, Pair{(all >> i) & 1 ? c[i] : -INFINITY, -INFINITY});
+            const bool whole = size % R == 0 && (lanes & (lanes - 1)) == 0;      // a group is a power of two of whole lanes
+            Pair mine{0, 0};
+            if (whole) {
+                Pair p{list[0], R > 1 ? list[R > 1 ? 1 : 0] : 0u};
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1)
                     if (d < lanes) p = merge(p, Pair{__shfl_xor_sync(QMOE_FULL_MASK, p.a, d), __shfl_xor_sync(QMOE_FULL_MASK, p.b, d)});
                 mine = Pair{__shfl_sync(QMOE_FULL_MASK, p.a, lane * lanes & 31), __shfl_sync(QMOE_FULL_MASK, p.b, lane * lanes & 31)};
             } else {
                 for (int g = 0; g < a.groups; ++g) {
-                    Pair p{-INFINITY, -INFINITY};
+                    Pair p{0, 0};
 #pragma unroll
                     for (int i = 0; i < R; ++i)
-                        if (e0 + i >= g * size && e0 + i < (g + 1) * size) p = merge(p, Pair{c[i], -INFINITY});
+                        if (e0 + i >= g * size && e0 + i < (g + 1) * size) p = merge(p, Pair{key[i], 0});
 #pragma unroll
                     for (int d = 16; d > 0; d >>= 1) p = merge(p, Pair{__shfl_xor_sync(QMOE_FULL_MASK, p.a, d), __shfl_xor_sync(QMOE_FULL_MASK, p.b, d)});
                     if (lane == g) mine = p;
                 }
             }
-            const float v = plain_value(a.best == 2 ? mine.a + mine.b : mine.a);
-            const uint32_t kept = best_groups(v, a.groups, a.top_groups, lane);
-            if (!(by_logit && a.best == 1) && a.top_groups < a.groups) {
-                // the last one kept and the best one dropped
-                const float one = fmaf(a.sigmoid ? 6.f : (float)(2 * R + 48) / z, kUlp, 1e-37f);
-                const float mag = fabsf(mine.a) + fabsf(mine.b);
-                const float err = 2.f * one + (mag < kLargest ? 2.f * kUlp * mag : 0.f);
-                const bool is = (kept >> lane) & 1;
-                const float low = value_of(~__reduce_max_sync(QMOE_FULL_MASK, is ? ~key_of(v) : 0u));
-                const uint32_t hk = __reduce_max_sync(QMOE_FULL_MASK, lane < a.groups && !is ? key_of(v) : 0u);
-                const float gap = low - value_of(hk);
-                const float err_all = __uint_as_float(__reduce_max_sync(QMOE_FULL_MASK, lane < a.groups ? __float_as_uint(err) : 0u));
-                // (two groups of nothing but -infinity: a NaN, decided by the index as in 64 bits)
-                again = groups_too = gap <= 2.f * err_all;
-            }
+            uint32_t kept;
+            if (by_logit && a.best == 1) {
+                kept = best_groups(mine.a, a.groups, a.top_groups, lane);
+            } else {
+                float va = value_of(mine.a), vb = a.best == 2 ? value_of(mine.b) : 0.f;
+                if (by_logit) va = score_near(va), vb = score_near(vb);      // (sums of scores)
+                const bool on = lane < a.groups;
+                const float v = on ? fmaxf(va + vb, -INFINITY) : -INFINITY;
+                kept = best_groups(v, a.groups, a.top_groups, lane);
+                if (a.top_groups < a.groups) {
+                    // the last one kept and the best one dropped
+                    const float mag = fabsf(va) + fabsf(vb);
+                    const float err = on ? 2.f * score_err + (mag < kLargest ? 2.f * kUlp * mag : 0.f) : 0.f;
+                    const bool is = (kept >> lane) & 1;
+                    const float low = value_of(~__reduce_max_sync(QMOE_FULL_MASK, is ? ~key_of(v) : 0u));
+                    const float high = value_of(__reduce_max_sync(QMOE_FULL_MASK, on && !is ? key_of(v) : 0u));
+                    const float err2 = 2.f * __uint_as_float(__reduce_max_sync(QMOE_FULL_MASK, __float_as_uint(err)));
+                    // (infinite ones are equal or not, whatever the bits: NaN here)
+                    if (__builtin_expect(low - high <= err2, 0)) {
+                        const uint32_t doubt = __ballot_sync(QMOE_FULL_MASK, on && v >= high - err2 && v <= low + err2);
+                        // the experts that may be among the best of those groups
+                        uint32_t cand = 0;
+                        for (uint32_t todo = doubt; todo; todo &= todo - 1) {
+                            const int g = __ffs(todo) - 1;
+                            const uint32_t least = __shfl_sync(QMOE_FULL_MASK, a.best == 2 ? mine.b : mine.a, g);
+                            const float from = value_of(least) - (2.f * slack + 2.f * kUlp * fminf(fabsf(value_of(least)), kLargest));
 #pragma unroll
-            for (int i = 0; i < R; ++i)
-                if (((all >> i) & 1) && !((kept >> ((e0 + i) / size)) & 1)) in &= ~(1u << i);
+                            for (int i = 0; i < R; ++i)
+                                if (e0 + i >= g * size && e0 + i < (g + 1) * size && (by_logit ? key[i] >= least : value_of(key[i]) >= from)) cand |= 1u << i;
+                        }
+                        const double exact = exact_groups(a, row, e0, R, top, cand, doubt);
+                        kept = best_groups((doubt >> lane) & 1 ? exact : (double)v, a.groups, a.top_groups, lane);
+                    }
+                }
+            }
+            if (whole) {
+                const bool off = e0 < a.E && !((kept >> (e0 / size)) & 1);
+#pragma unroll
+                for (int i = 0; i < R; ++i) key[i] = off ? 0u : key[i];
+#pragma unroll
+                for (int i = 0; i < kDepth<R>; ++i) list[i] = off ? 0u : list[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    if (e0 + i < a.E && !((kept >> ((e0 + i) / size)) & 1)) key[i] = 0u;
+                best_keys<R>(key, list);
+            }
         }
     }
-    // ---- the k best, and the next one
-    uint32_t key[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) key[i] = (in >> i) & 1 ? key_of(by_logit ? l[i] : c[i]) : 0u;
+    // ---- the k best, and the next one where the values are not exact
     const int rounds = min(a.k + (by_logit ? 0 : 1), 32);
-    uint32_t mk;
+    uint32_t mk, left;      // left: the largest key that was not taken
     int at;
-    choose<R>(key, rounds, lane, &mk, &at);
+    {
+        int from;
+        if (__builtin_expect(choose<R>(list, rounds, lane, &mk, &from), 1)) {
+            at = which<R>(key, mk, from, lane);
+            left = list[0];
+        } else {
+            uint32_t all[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i) all[i] = key[i];
+            left = choose_slow<R>(all, rounds, lane, &mk, &at);
+        }
+    }
     if constexpr (NW > 1) {
         key_s[warp * 32 + lane] = lane < rounds ? mk : 0u;
         id_s[warp * 32 + lane] = lane < rounds && mk ? warp * 32 * R + at : 0;
+        left = __reduce_max_sync(QMOE_FULL_MASK, left);
+        if (lane == 0) left_s[warp] = left;
         __syncthreads();
         if (warp == 0) {
-            // the warps' lists one behind the other, kRouteWarps of them a lane's worth at a time: lower lanes hold lower experts
-            // among equal keys
-            uint32_t mkeys[kRouteWarps];
+            // the warps' lists one behind the other, eight entries a lane: lower lanes hold lower experts among equal keys
+            uint32_t keys[8], lists[8];
 #pragma unroll
-            for (int i = 0; i < kRouteWarps; ++i) mkeys[i] = key_s[lane * kRouteWarps + i];
-            choose<kRouteWarps>(mkeys, rounds, lane, &mk, &at);
-            at = mk ? id_s[at] : -1;
+            for (int i = 0; i < 8; ++i) keys[i] = key_s[lane * 8 + i];
+            best_keys<8>(keys, lists);
+            int from;
+            choose<8>(lists, rounds, lane, &mk, &from);
+            at = id_s[which<8>(keys, mk, from, lane)];
+            left = max(lists[0], left_s[lane & (kRouteWarps - 1)]);
         }
     }
-    if (!by_logit && (NW == 1 || warp == 0)) {
-        // ---- neighbours that are too near to tell (with k = 32 the 33rd is not known: then the last gap counts as too small)
-        const uint32_t nk = __shfl_down_sync(QMOE_FULL_MASK, mk, 1);
-        const int nat = __shfl_down_sync(QMOE_FULL_MASK, at, 1);
-        bool near = false;
-        if (lane < a.k && mk) {
-            if (lane == 31) {
-                near = a.k < a.E;
-            } else if (nk) {
-                const float v = value_of(mk), nv = value_of(nk);
-                const float err = 2.f * slack + kUlp * (fabsf(v) + fabsf(nv));
-                if (v > -INFINITY && v < INFINITY && nv > -INFINITY)
-                    near = v - nv <= err;
-                else
-                    near = v == nv;
-                if (near) near = !(logit(row, at) == logit(row, nat) && a.bias[at] == a.bias[nat]);
-            }
-        }
-        again |= __any_sync(QMOE_FULL_MASK, near);
-    }
-    if constexpr (NW == 1) {
-        if (__builtin_expect(again, 0)) {
-            // what may be among the chosen: values down to the k-th's less the errors
-            const float last = value_of(__shfl_sync(QMOE_FULL_MASK, mk, a.k - 1));
-            uint32_t cand = groups_too ? all : 0u;
-            if (!groups_too) {
-#pragma unroll
-                for (int i = 0; i < R; ++i)
-                    if (((in >> i) & 1) && !(c[i] < last - (2.f * slack + 2.f * kUlp * fmaxf(fabsf(last), fabsf(c[i]))))) cand |= 1u << i;
-            }
-            at = resolve<X, 1>(a, row, e0, R, top, cand, groups_too, &rs);
-        }
-        write_route<X>(a, row, t, at < 0 ? 0 : at, top, z, lane);
-    } else {
+    // ---- the chosen ones' logits, and neighbours that are too near to tell
+    bool again = false;       // ... among more experts than the list holds
+    float l = -INFINITY, last = 0.f;
+    if (NW == 1 || warp == 0) {
+        const bool in_list = lane < rounds && mk;
+        if (!in_list) at = 0;
+        if (in_list) l = logit(row, at);
         if (!by_logit) {
-            if (warp == 0) {
-                const float last = value_of(__shfl_sync(QMOE_FULL_MASK, mk, a.k - 1));
-                if (lane == 0) bound_s = make_float2(again ? 1.f : 0.f, last);
+            const float v = value_of(mk);
+            const uint32_t nk = __shfl_down_sync(QMOE_FULL_MASK, mk, 1);
+            const int nat = __shfl_down_sync(QMOE_FULL_MASK, at, 1);
+            const float nl = __shfl_down_sync(QMOE_FULL_MASK, l, 1);
+            bool near = false, doubt = false;
+            if (lane < a.k && lane < 31 && mk && nk) {
+                const float nv = value_of(nk);
+                near = fabsf(v) < INFINITY && nv > -INFINITY ? v - nv <= 2.f * slack + kUlp * (fabsf(v) + fabsf(nv)) : v == nv;
+                if (near) doubt = !(l == nl && a.bias[at] == a.bias[nat]);
             }
-            __syncthreads();
-            if (__builtin_expect(bound_s.x != 0.f, 0)) {
-                const float last = bound_s.y;
-                uint32_t cand = 0u;
-#pragma unroll
-                for (int i = 0; i < R; ++i)
-                    if (((in >> i) & 1) && !(c[i] < last - (2.f * slack + 2.f * kUlp * fmaxf(fabsf(last), fabsf(c[i]))))) cand |= 1u << i;
-                at = resolve<X, NW>(a, row, e0, R, top, cand, false, &rs);
+            const bool doubts = __any_sync(QMOE_FULL_MASK, doubt);
+            if (__builtin_expect(doubts || a.k == 32, 0)) {
+                last = value_of(__shfl_sync(QMOE_FULL_MASK, mk, a.k - 1));
+                const float from = last - (2.f * slack + 4.f * kUlp * fminf(fabsf(last), kLargest));
+                // experts outside the list that may belong into it
+                again = __any_sync(QMOE_FULL_MASK, left && !(value_of(left) < from));
+                if (!again && doubts) {
+                    if (NW == 1) {
+                        const unsigned pairs = __ballot_sync(QMOE_FULL_MASK, near);      // (equal ones with them)
+                        const double z64 = exact_sum<X, 1>(a, row, e0, R, top, nullptr);
+                        at = exact_order(a, row, __popc(__ballot_sync(QMOE_FULL_MASK, in_list)), v, at, ((pairs | pairs << 1) >> lane) & 1, top, z64);
+                        if (in_list) l = logit(row, at);
+                    } else {
+                        again = true;
+                    }
+                }
             }
         }
-        if (warp == 0) write_route<X>(a, row, t, at < 0 ? 0 : at, top, z, lane);
     }
+    if (NW > 1 && !by_logit) {
+        if (warp == 0 && lane == 0) bound_s = make_float2(again ? 1.f : 0.f, last);
+        __syncthreads();
+        again = bound_s.x != 0.f, last = bound_s.y;
+    }
+    if (__builtin_expect(again, 0)) {
+        // what may be among the chosen: values down to the k-th's less the errors
+        const float from = last - (2.f * slack + 4.f * kUlp * fminf(fabsf(last), kLargest));
+        uint32_t cand = 0u;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (key[i] && !(value_of(key[i]) < from)) cand |= 1u << i;
+        at = exact_choice<X, NW>(a, row, e0, R, top, cand, &rs);
+        if (lane < a.k) l = logit(row, at);
+    }
+    if (NW == 1 || warp == 0) write_route(a, t, at, l, top, z, lane);
 }
 
 template <typename X>
@@ -714,7 +898,11 @@ extern "C" int qmoe_route_scored(const void* logits, int logits_are_f32, int64_t
     if (T > 1 && row_stride < E) return qmoe::fail(QMOE_EINVAL, "qmoe_route_scored: the row stride is smaller than a row");
     if (!aligned(logits, logits_are_f32 ? 4 : 2) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(gates, 4))
         return qmoe::fail(QMOE_EINVAL, "qmoe_route_scored: pointer not aligned to its type");
+    // experts a lane holds (launch_route), and what its loads have to be multiples of
+    const int R = E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : E <= 256 || (E > 1024 && E <= 2048) ? 8 : 16, size = logits_are_f32 ? 4 : 2;
+    const int wide = std::min(16, R * size), wide_bias = std::min(16, R * 4);
     RouteArgs a{logits, bias, ids, gates, row_stride, T, E, k, score == QMOE_SCORE_SIGMOID, n_groups, top_groups, group_best,
-                renormalise ? 1 : 0, scale};
+                renormalise ? 1 : 0, aligned(logits, wide) && (T == 1 || row_stride * size % wide == 0) && E * size % wide == 0,
+                aligned(bias, wide_bias) && E * 4 % wide_bias == 0, scale};
     return logits_are_f32 ? launch_route<float>(a, (cudaStream_t)stream) : launch_route<uint16_t>(a, (cudaStream_t)stream);
 }
