@@ -255,9 +255,8 @@ struct SplitItem {
     int b, kh, rb, last;
 };
 
-// Programmatic dependent launch: the kernels of a call overlap each other's launches.
-__device__ __forceinline__ void depend_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void depend_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+using kv4::depend_launch;
+using kv4::depend_wait;
 
 // Read where it stands: volatile, so that it is not read once for all tokens and kept.
 __device__ __forceinline__ void load_factors(const float4* src, float (&c1)[2], float (&cz)[2]) {

@@ -23,72 +23,99 @@ struct BoundsArgs {
     int n;
 };
 
-// A warp takes the tokens of one kv head that stand `span` from t0 on and bounds the block of each that is the last new one
-// of its block: L = head_dim / 8 lanes a row of codes (a word, 8 channels, a lane), 32 / L rows at a time.
+// A thread block takes `span` tokens of one kv head and bounds the block of each that is the last new one of its block.
+// L = head_dim / 8 lanes hold a row of codes (a word, 8 channels, a lane); the rows of a block are dealt out over the four
+// warps, all of a lane's loads in flight together, and joined in shared memory, where a thread takes a channel.
+constexpr int kBoundsThreads = 128;
+
 template <int L>
-__global__ void __launch_bounds__(128) bounds_kernel(BoundsArgs a, int span) {
-    constexpr int G = 32 / L, D = L * 8;
-    const int lane = threadIdx.x & 31, gl = lane & (L - 1), g = lane / L;
-    const int h = blockIdx.y;
-    const int64_t t0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * span;
-    if (t0 >= a.n) return;
-    const int shift = a.cache.page_shift, P = 1 << shift;
-    int slot = -1;
-    bool last = false;
-    if (lane < span && t0 + lane < a.n) {
-        slot = a.slots[t0 + lane];
+__global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(BoundsArgs a, int span) {
+    constexpr int D = L * 8, ROWS = kBoundsThreads / L, STEPS = 64 / ROWS, WARPS = kBoundsThreads / 32;
+    __shared__ float lo_s[WARPS][D], hi_s[WARPS][D], big_s[WARPS];
+    __shared__ int ends[kBoundsThreads], n_ends;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gl = lane & (L - 1), row = tid / L;
+    const int h = blockIdx.y, shift = a.cache.page_shift, P = 1 << shift;
+    const int64_t t = (int64_t)blockIdx.x * span + tid;
+    if (tid == 0) n_ends = 0;
+    __syncthreads();
+    if (tid < span && t < a.n) {
+        int slot = a.slots[t];
         if (slot < -1 || (slot >> shift) >= a.cache.n_pages) {
             blocks_set_error(QMOE_EINVAL);
             slot = -1;
         }
-        const int next = t0 + lane + 1 < a.n ? a.slots[t0 + lane + 1] : -1;
-        last = slot >= 0 && (next != slot + 1 || (next & (P - 1)) == 0);
+        const int next = t + 1 < a.n ? a.slots[t + 1] : -1;
+        if (slot >= 0 && (next != slot + 1 || (next & (P - 1)) == 0)) ends[atomicAdd(&n_ends, 1)] = slot;
     }
-    for (unsigned todo = __ballot_sync(QMOE_FULL_MASK, last); todo; todo &= todo - 1) {
-        const int s = __shfl_sync(QMOE_FULL_MASK, slot, __ffs(todo) - 1), page = s >> shift, count = (s & (P - 1)) + 1;
+    __syncthreads();
+    const int n = n_ends;
+    for (int i = 0; i < n; ++i) {
+        const int s = ends[i], page = s >> shift, count = (s & (P - 1)) + 1;
         const unsigned char* hp = kv4::head_ptr(a.cache, page, h);
         const uint32_t* words = (const uint32_t*)hp;
         const __half2* pairs = (const __half2*)(hp + (size_t)P * D);
+        uint32_t w[STEPS];
+        __half2 sz[STEPS];
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+            const int r = row + k * ROWS;
+            if (r < count) w[k] = words[r * L + gl], sz[k] = pairs[r];
+        }
         float lo[8], hi[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) lo[i] = INFINITY, hi[i] = -INFINITY;
-#pragma unroll 4
-        for (int r = g; r < count; r += G) {
-            const uint32_t w = words[r * L + gl];
-            const float2 sz = __half22float2(pairs[r]);
+        for (int c = 0; c < 8; ++c) lo[c] = INFINITY, hi[c] = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float v = fmaf(sz.x, (float)((w >> (4 * (i >> 1) + 16 * (i & 1))) & 15u), sz.y);
-                lo[i] = fminf(lo[i], v), hi[i] = fmaxf(hi[i], v);
+        for (int k = 0; k < STEPS; ++k) {
+            if (row + k * ROWS < count) {
+                const float2 p = __half22float2(sz[k]);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    // the code as the low bits of 2^23: one mask instead of a conversion
+                    const float u = __uint_as_float((w[k] >> (4 * (c >> 1) + 16 * (c & 1)) & 15u) | 0x4B000000u) - 8388608.f;
+                    const float v = fmaf(p.x, u, p.y);
+                    lo[c] = fminf(lo[c], v), hi[c] = fmaxf(hi[c], v);
+                }
             }
         }
-        float big = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int c = 0; c < 8; ++c) {
 #pragma unroll
             for (int d = L; d < 32; d <<= 1) {
-                lo[i] = fminf(lo[i], __shfl_xor_sync(QMOE_FULL_MASK, lo[i], d));
-                hi[i] = fmaxf(hi[i], __shfl_xor_sync(QMOE_FULL_MASK, hi[i], d));
+                lo[c] = fminf(lo[c], __shfl_xor_sync(QMOE_FULL_MASK, lo[c], d));
+                hi[c] = fmaxf(hi[c], __shfl_xor_sync(QMOE_FULL_MASK, hi[c], d));
             }
-            big = fmaxf(big, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
         }
+        if (lane < L) {
 #pragma unroll
-        for (int d = L / 2; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor_sync(QMOE_FULL_MASK, big, d));
-        // big = m 2^e with m in [64, 127], or [63.5, 64) one power up; the quotients by a power of two are exact
+            for (int c = 0; c < 8; c += 4) {
+                *(float4*)&lo_s[warp][gl * 8 + c] = make_float4(lo[c], lo[c + 1], lo[c + 2], lo[c + 3]);
+                *(float4*)&hi_s[warp][gl * 8 + c] = make_float4(hi[c], hi[c + 1], hi[c + 2], hi[c + 3]);
+            }
+        }
+        __syncthreads();
+        float l = 0.f, u = 0.f;
+        if (tid < D) {
+            l = lo_s[0][tid], u = hi_s[0][tid];
+#pragma unroll
+            for (int x = 1; x < WARPS; ++x) l = fminf(l, lo_s[x][tid]), u = fmaxf(u, hi_s[x][tid]);
+        }
+        float big = fmaxf(fabsf(l), fabsf(u));
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor_sync(QMOE_FULL_MASK, big, d));
+        if (lane == 0) big_s[warp] = big;
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < WARPS; ++x) big = fmaxf(big, big_s[x]);
+        // big = m 2^e with m in [64, 127], or (63.5, 64) one power up; the quotients by a power of two are exact
         int e = (int)(__float_as_uint(big) >> 23) - 127 - 6;
         if (big > 127.f * __int_as_float((e + 127) << 23)) ++e;
         const float step = big > 0.f ? __int_as_float((e + 127) << 23) : 0.f, inv = big > 0.f ? __int_as_float((127 - e) << 23) : 0.f;
         const int64_t rec = (int64_t)page * a.cache.n_kv_heads + h;
-        if (g < 2) {
-            uint32_t w[2] = {0, 0};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int q = g == 0 ? __float2int_ru(hi[i] * inv) : __float2int_rd(lo[i] * inv);
-                w[i >> 2] |= (uint32_t)(min(max(q, -127), 127) & 255) << (8 * (i & 3));
-            }
-            *(uint2*)(a.codes + (rec * 2 + g) * D + gl * 8) = make_uint2(w[0], w[1]);
+        if (tid < D) {
+            a.codes[rec * (2 * D) + tid] = (int8_t)min(max(__float2int_ru(u * inv), -127), 127);
+            a.codes[rec * (2 * D) + D + tid] = (int8_t)min(max(__float2int_rd(l * inv), -127), 127);
         }
-        if (lane == 0) a.steps[rec] = step;
+        if (tid == 0) a.steps[rec] = step;
     }
 }
 
@@ -122,7 +149,7 @@ __device__ __forceinline__ int dot4(uint32_t c, uint32_t q0, uint32_t q1, int ac
     return __dp2a_hi((int)q1, (int)c, acc);
 }
 
-constexpr int kScoreThreads = 256, kScoreBlocks = 64;     // blocks of the cache that a thread block scores
+constexpr int kScoreThreads = 256;
 
 // q as bf16, NaN as 0, infinities as the largest finite value
 __device__ __forceinline__ float query_value(uint32_t bits) {
@@ -130,26 +157,57 @@ __device__ __forceinline__ float query_value(uint32_t bits) {
     return v == v ? fminf(fmaxf(v, -3.3895313892515355e38f), 3.3895313892515355e38f) : 0.f;
 }
 
-// A thread block scores kScoreBlocks blocks of one query token for every kv head.  L = 2 D / 16 lanes take a record (hi and lo
-// codes), 16 codes a lane, against the group's summed queries, which a lane keeps in registers for one kv head.
+// Lanes that take a record (hi and lo codes, 16 a lane), and records of one kv head that they take at once.
+template <int D>
+constexpr int kRecordLanes = D / 8;
+
+// Blocks of the cache that a thread block scores for every kv head.
+inline int score_chunk(int head_dim, int n_kv) {
+    const int lanes = head_dim / 8, groups = kScoreThreads / lanes;
+    return std::max(1, groups / n_kv) * lanes;
+}
+
+// A thread block scores `chunk` blocks of one query token for every kv head.  L lanes take L records of one kv head: lane i
+// looks up the i-th one's page and step, all of them load their 16 codes of every record (L loads of 16 bytes in flight), multiply
+// them with the group's summed queries, which a lane keeps in registers, and the L x L partial sums are added up crosswise, so
+// that lane i ends with the i-th record's.
 template <int D>
 __global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int chunks) {
-    constexpr int L = D / 8, SLOTS = kScoreThreads / L;     // groups of lanes
-    const int t = blockIdx.x / chunks, chunk = blockIdx.x - t * chunks;
+    constexpr int L = kRecordLanes<D>, GROUPS = kScoreThreads / L;
+    kv4::depend_launch();
+    const int t = blockIdx.x / chunks, c = blockIdx.x - t * chunks;
     int b;
-    const int seen = blocks_seen(a, t, &b, chunk == 0 && threadIdx.x == 0);
-    const int j0 = chunk * kScoreBlocks, j1 = min(j0 + kScoreBlocks, seen);
-    if (seen <= a.top || j0 >= j1) return;      // few blocks are all taken
-    const int sl = threadIdx.x / L, gl = threadIdx.x - sl * L;
-    const int parts = max(1, SLOTS / a.n_kv);
-    if (sl >= a.n_kv * parts) return;           // (whole groups of lanes: the shuffles below stay within a group)
-    const unsigned mask = (L == 16 ? 0xFFFFu : 0xFFu) << (threadIdx.x & 31 & ~(L - 1));
-    for (int h = sl % a.n_kv; h < a.n_kv; h += SLOTS) {
-        // this lane's 16 channels: hi of 16 gl .., or lo
+    const int seen = blocks_seen(a, t, &b, c == 0 && threadIdx.x == 0);
+    const int grp = threadIdx.x / L, gl = threadIdx.x & (L - 1);
+    const int parts = max(1, GROUPS / a.n_kv);
+    // few blocks are all taken
+    if (seen <= a.top || c * parts * L >= seen || grp >= a.n_kv * parts) return;      // (whole groups of lanes leave)
+    const int j = (c * parts + grp / a.n_kv) * L + gl;                                // the block that this lane looks up
+    const int base = threadIdx.x & 31 & ~(L - 1);
+    const unsigned mask = (L == 16 ? 0xFFFFu : 0xFFu) << base;
+    int page = -1;
+    if (j < seen) {
+        page = j < a.max_blocks ? a.table[(int64_t)b * a.max_blocks + j] : -1;
+        if (page < 0 || page >= a.n_pages) {
+            if (grp % a.n_kv == 0) blocks_set_error(QMOE_EINVAL);
+            page = -1;
+        }
+    }
+    for (int h = grp % a.n_kv; h < a.n_kv; h += GROUPS) {
+        const float step = page >= 0 ? a.steps[(int64_t)page * a.n_kv + h] : 0.f;
+        uint4 code[L];
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const int pg = __shfl_sync(mask, page, i, L);
+            code[i] = make_uint4(0, 0, 0, 0);
+            if (pg >= 0) code[i] = *(const uint4*)(a.codes + ((int64_t)pg * a.n_kv + h) * (2 * D) + gl * 16);
+        }
+        // this lane's 16 channels of the queries: of hi the positive parts, of lo the negative ones
         const int d0 = (gl * 16) % D;
         const bool low = gl * 16 >= D;
         const uint16_t* q = a.q + ((int64_t)t * a.n_kv + h) * a.group * D + d0;
         float big = 0.f;
+#pragma unroll 4
         for (int g = 0; g < a.group; ++g) {
             const uint4 x[2] = {((const uint4*)(q + g * D))[0], ((const uint4*)(q + g * D))[1]};
             const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
@@ -159,11 +217,12 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int 
 #pragma unroll
         for (int d = L / 2; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor_sync(mask, big, d));
         // largest magnitude to [2^(bits-1), 2^bits): times 2^(bits - 1 - exponent), in two factors of normal size
-        const int up = a.bits - 1 - (ilogbf(big > 0.f ? big : 1.f)), limit = (1 << a.bits) - 1;
+        const int up = a.bits - 1 - ilogbf(big > 0.f ? big : 1.f), limit = (1 << a.bits) - 1;
         const float f1 = __int_as_float((min(up, 100) + 127) << 23), f2 = __int_as_float((max(up - 100, 0) + 127) << 23);
         int sum[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum[i] = 0;
+#pragma unroll 2
         for (int g = 0; g < a.group; ++g) {
             const uint4 x[2] = {((const uint4*)(q + g * D))[0], ((const uint4*)(q + g * D))[1]};
             const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
@@ -177,37 +236,50 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int 
         uint32_t pk[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) pk[i] = __byte_perm((uint32_t)sum[2 * i], (uint32_t)sum[2 * i + 1], 0x5410);
-        float* out = a.scores + ((int64_t)t * a.n_kv + h) * a.max_seen;
-#pragma unroll 4
-        for (int j = j0 + sl / a.n_kv; j < j1; j += parts) {
-            const int page = j < a.max_blocks ? a.table[(int64_t)b * a.max_blocks + j] : -1;
-            float score = -INFINITY;
-            if (page >= 0 && page < a.n_pages) {
-                const int64_t rec = (int64_t)page * a.n_kv + h;
-                const uint4 c = *(const uint4*)(a.codes + rec * (2 * D) + gl * 16);
-                int acc = dot4(c.x, pk[0], pk[1], 0);
-                acc = dot4(c.y, pk[2], pk[3], acc);
-                acc = dot4(c.z, pk[4], pk[5], acc);
-                acc = dot4(c.w, pk[6], pk[7], acc);
+        int acc[L];
 #pragma unroll
-                for (int d = L / 2; d > 0; d >>= 1) acc += __shfl_xor_sync(mask, acc, d);
-                score = __fmul_rn((float)acc, a.steps[rec]);
-            } else if (gl == 0 && h == 0) {
-                blocks_set_error(QMOE_EINVAL);
+        for (int i = 0; i < L; ++i)
+            acc[i] = dot4(code[i].w, pk[6], pk[7], dot4(code[i].z, pk[4], pk[5], dot4(code[i].y, pk[2], pk[3], dot4(code[i].x, pk[0], pk[1], 0))));
+        // lane i keeps the records whose number has the lane's upper bits, and gives the others away
+#pragma unroll
+        for (int d = L / 2; d > 0; d >>= 1) {
+            const bool upper = gl & d;
+#pragma unroll
+            for (int i = 0; i < d; ++i) {
+                const int give = upper ? acc[i] : acc[i + d], keep = upper ? acc[i + d] : acc[i];
+                acc[i] = keep + __shfl_xor_sync(mask, give, d);
             }
-            if (gl == 0) out[j] = score;
         }
+        // (a step that is NaN, which kv4_block_bounds never writes, gives a score like a missing page's)
+        if (j < seen) a.scores[((int64_t)t * a.n_kv + h) * a.max_seen + j] = page >= 0 ? fmaxf(__fmul_rn((float)acc[0], step), -INFINITY) : -INFINITY;
     }
 }
 
 // ---------------------------------------------------------------- the best blocks
-constexpr int kPickThreads = 256;
+//
+// A thread block writes the list of one (token, kv head).  Its scores are kept in registers, warp w those of the w-th equal run.
+// A histogram over the scores' range finds the bin that the last taken score falls into, and the few scores of that bin are
+// ranked against each other (a bin with too many, and rows longer than the registers hold, are settled by bisection); then
+// every warp writes the blocks of its run that lie above that score, and the first ones at it.
+constexpr int kBins = 1024, kRankMost = 256;
 
+// fp32 -> integer of the same order (-0 as 0); no key is 0.
 __device__ __forceinline__ uint32_t score_key(float v) {
     const uint32_t u = __float_as_uint(v + 0.f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+template <int THREADS>
+struct PickShared {
+    int count[THREADS / 32], above[THREADS / 32], equal[THREADS / 32];
+    float lo[THREADS / 32], hi[THREADS / 32];
+    int bins[kBins];
+    uint32_t rank_key[kRankMost];
+    int n_rank, bin, need;
+    uint32_t key;
+};
+
+template <int THREADS>
 __device__ __forceinline__ int block_sum(int v, int* buf) {
     v = warp_sum_int(v);
     __syncthreads();
@@ -215,61 +287,143 @@ __device__ __forceinline__ int block_sum(int v, int* buf) {
     __syncthreads();
     int s = 0;
 #pragma unroll
-    for (int w = 0; w < kPickThreads / 32; ++w) s += buf[w];
+    for (int w = 0; w < THREADS / 32; ++w) s += buf[w];
     return s;
 }
 
-// A thread block writes the list of one (token, kv head): the key of the last block taken by bisection, then the blocks above
-// it and the first ones at it, in order (each warp those of an equal run of the blocks).
-__global__ void __launch_bounds__(kPickThreads) pick_kernel(SelectArgs a) {
-    __shared__ int buf[kPickThreads / 32], above_s[kPickThreads / 32], equal_s[kPickThreads / 32];
-    const int t = blockIdx.x / a.n_kv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// R scores a thread in registers; R = 0: any number, read again each time.
+template <int THREADS, int R>
+__global__ void __launch_bounds__(THREADS) pick_kernel(SelectArgs a) {
+    __shared__ PickShared<THREADS> sh;
+    constexpr int WARPS = THREADS / 32;
+    const int t = blockIdx.x / a.n_kv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int b;
-    const int seen = blocks_seen(a, t, &b, false);
+    const int seen = blocks_seen(a, t, &b, a.max_seen <= a.top && tid == 0 && blockIdx.x == t * a.n_kv);
+    kv4::depend_wait();        // (before any return: what follows the call waits for this kernel alone)
     if (seen < 0) return;
     int32_t* sel = a.sel + (int64_t)blockIdx.x * a.top;
     if (seen <= a.top) {
-        for (int i = threadIdx.x; i < a.top; i += kPickThreads) sel[i] = i < seen ? i : -1;
+        for (int i = tid; i < a.top; i += THREADS) sel[i] = i < seen ? i : -1;
         return;
     }
     const float* scores = a.scores + (int64_t)blockIdx.x * a.max_seen;
     const int lo = a.first, hi = seen - a.last, want = a.top - a.first - a.last;
-    for (int i = threadIdx.x; i < a.first; i += kPickThreads) sel[i] = i;
-    for (int i = threadIdx.x; i < a.last; i += kPickThreads) sel[a.top - a.last + i] = hi + i;
+    for (int i = tid; i < a.first; i += THREADS) sel[i] = i;
+    for (int i = tid; i < a.last; i += THREADS) sel[a.top - a.last + i] = hi + i;
     if (want == 0) return;
-    // largest key k with at least `want` keys >= k
-    uint32_t key = 0;
-    for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t probe = key | 1u << bit;
-        int c = 0;
-        for (int j = lo + threadIdx.x; j < hi; j += kPickThreads) c += score_key(scores[j]) >= probe;
-        if (block_sum(c, buf) >= want) key = probe;
-    }
-    const int per = ((hi - lo + kPickThreads / 32 - 1) / (kPickThreads / 32) + 31) & ~31;
+    const int per = R ? R * 32 : ((hi - lo + WARPS - 1) / WARPS + 31) & ~31;
     const int w0 = min(lo + warp * per, hi), w1 = min(w0 + per, hi);
-    int above = 0, equal = 0;
-    for (int j = w0 + lane; j < w1; j += 32) {
-        const uint32_t k = score_key(scores[j]);
-        above += k > key, equal += k == key;
+    uint32_t cut = 0;          // key of the last score taken
+    bool found = false;
+    uint32_t key[R ? R : 1];
+    if constexpr (R > 0) {
+        float v[R], least = INFINITY, most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int j = w0 + 32 * i + lane;
+            v[i] = j < w1 ? scores[j] : -INFINITY;
+            key[i] = j < w1 ? score_key(v[i]) : 0u;
+            if (v[i] > -INFINITY) least = fminf(least, v[i]);
+            most = fmaxf(most, v[i]);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            least = fminf(least, __shfl_xor_sync(QMOE_FULL_MASK, least, d));
+            most = fmaxf(most, __shfl_xor_sync(QMOE_FULL_MASK, most, d));
+        }
+        if (lane == 0) sh.lo[warp] = least, sh.hi[warp] = most;
+        for (int i = tid; i < kBins; i += THREADS) sh.bins[i] = 0;
+        if (tid == 0) sh.n_rank = 0;
+        __syncthreads();
+        least = sh.lo[lane % WARPS], most = sh.hi[lane % WARPS];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            least = fminf(least, __shfl_xor_sync(QMOE_FULL_MASK, least, d));
+            most = fmaxf(most, __shfl_xor_sync(QMOE_FULL_MASK, most, d));
+        }
+        // bins from the largest score down; -infinity stands in the last one.  The map does not rise with the score, whatever
+        // it rounds, so that bins are in the scores' order
+        const float per_bin = (float)(kBins - 2) / (most - least);
+        if (most > least && per_bin < INFINITY) {
+            auto bin_of = [&](float x) { return x > -INFINITY ? min((int)((most - x) * per_bin), kBins - 2) : kBins - 1; };
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                if (key[i]) atomicAdd(&sh.bins[bin_of(v[i])], 1);
+            __syncthreads();
+            // the bin of the want-th score: a scan by the first warp, 32 bins a lane
+            if (warp == 0) {
+                int mine = 0;
+#pragma unroll 8
+                for (int i = 0; i < kBins / 32; ++i) mine += sh.bins[lane * (kBins / 32) + ((i + lane) & (kBins / 32 - 1))];      // (skewed: no bank conflicts)
+                const int before = warp_incl_scan(mine, lane) - mine;
+                if (before < want && before + mine >= want) {
+                    int at = lane * (kBins / 32), sum = before;
+                    while (sum + sh.bins[at] < want) sum += sh.bins[at++];
+                    sh.bin = at, sh.need = want - sum;
+                }
+            }
+            __syncthreads();
+            const int bin = sh.bin, need = sh.need, many = sh.bins[bin];
+            if (many <= kRankMost) {
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    if (key[i] && bin_of(v[i]) == bin) sh.rank_key[atomicAdd(&sh.n_rank, 1)] = key[i];
+                __syncthreads();
+                for (int i = tid; i < many; i += THREADS) {
+                    const uint32_t mine = sh.rank_key[i];
+                    int over = 0, same = 0;
+                    for (int k = 0; k < many; ++k) over += sh.rank_key[k] > mine, same += sh.rank_key[k] == mine;
+                    if (over < need && over + same >= need) sh.key = mine;      // (equal ones write the same)
+                }
+                __syncthreads();
+                cut = sh.key;
+                found = true;
+            }
+        }
     }
-    above = warp_sum_int(above), equal = warp_sum_int(equal);
-    if (lane == 0) above_s[warp] = above, equal_s[warp] = equal;
+    if (!found) {
+        // largest key with at least `want` keys >= it
+        for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t probe = cut | 1u << bit;
+            int c = 0;
+            if constexpr (R > 0) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) c += key[i] >= probe;
+            } else {
+                for (int j = w0 + lane; j < w1; j += 32) c += score_key(scores[j]) >= probe;
+            }
+            if (block_sum<THREADS>(c, sh.count) >= want) cut = probe;
+        }
+    }
+    auto key_at = [&](int i, int j) {
+        if constexpr (R > 0) return key[i];
+        else return j < w1 ? score_key(scores[j]) : 0u;
+    };
+    const int steps = R ? R : (w1 - w0 + 31) / 32;
+    int above = 0, equal = 0;
+#pragma unroll
+    for (int i = 0; i < (R ? R : steps); ++i) {
+        const uint32_t k = key_at(i, w0 + 32 * i + lane);
+        above += __popc(__ballot_sync(QMOE_FULL_MASK, k > cut)), equal += __popc(__ballot_sync(QMOE_FULL_MASK, k == cut));
+    }
+    if (lane == 0) sh.above[warp] = above, sh.equal[warp] = equal;
     __syncthreads();
     int all_above = 0, above_before = 0, equal_before = 0;
 #pragma unroll
-    for (int w = 0; w < kPickThreads / 32; ++w) {
-        all_above += above_s[w];
-        if (w < warp) above_before += above_s[w], equal_before += equal_s[w];
+    for (int w = 0; w < WARPS; ++w) {
+        const int x = sh.above[w], y = sh.equal[w];
+        all_above += x;
+        if (w < warp) above_before += x, equal_before += y;
     }
     const int room = want - all_above;          // of the equal ones
-    for (int j0 = w0; j0 < w1; j0 += 32) {
-        const int j = j0 + lane;
-        const uint32_t k = j < w1 ? score_key(scores[j]) : 0u;
-        const unsigned over = __ballot_sync(QMOE_FULL_MASK, j < w1 && k > key), same = __ballot_sync(QMOE_FULL_MASK, j < w1 && k == key);
-        const unsigned before = (1u << lane) - 1;
-        const int n_same = equal_before + __popc(same & before);
-        const int at = above_before + __popc(over & before) + min(n_same, room);
-        if (((over >> lane) & 1) || (((same >> lane) & 1) && n_same < room)) sel[a.first + at] = j;
+    const unsigned below = (1u << lane) - 1;
+#pragma unroll
+    for (int i = 0; i < (R ? R : steps); ++i) {
+        const int j = w0 + 32 * i + lane;
+        const uint32_t k = key_at(i, j);
+        const unsigned over = __ballot_sync(QMOE_FULL_MASK, k > cut), same = __ballot_sync(QMOE_FULL_MASK, k == cut);
+        const int n_same = equal_before + __popc(same & below);
+        if (k > cut || (k == cut && n_same < room)) sel[a.first + above_before + __popc(over & below) + min(n_same, room)] = j;
         above_before += __popc(over), equal_before += __popc(same);
     }
 }
@@ -314,11 +468,12 @@ extern "C" int kv4_block_bounds(const kv4_cache* cache, const kv4_bounds* bounds
     if (n < 0 || (n > 0 && !slots)) return qmoe::fail(QMOE_EINVAL, "kv4_block_bounds: negative n or NULL slots");
     if (n == 0) return QMOE_OK;
     a.codes = (int8_t*)bounds->codes, a.steps = bounds->steps, a.slots = slots, a.n = n;
-    // few tokens: a warp each, so that blocks are bounded side by side; many: a warp a run of 32
-    const int span = (int64_t)n * cache->n_kv_heads <= (int64_t)qmoe::sm_count() * 64 ? 1 : 32;
-    const dim3 grid((unsigned)(((int64_t)n + 4 * span - 1) / (4 * span)), (unsigned)cache->n_kv_heads);
-    if (cache->head_dim == 128) bounds_kernel<16><<<grid, 128, 0, (cudaStream_t)stream>>>(a, span);
-    else bounds_kernel<8><<<grid, 128, 0, (cudaStream_t)stream>>>(a, span);
+    // few tokens: a thread block each, so that their blocks are bounded side by side; many: a page's worth of them
+    const int64_t share = (int64_t)n * cache->n_kv_heads / ((int64_t)qmoe::sm_count() * 16);
+    const int span = (int)std::min<int64_t>(std::max<int64_t>(share, 1), cache->page_size);
+    const dim3 grid((unsigned)(((int64_t)n + span - 1) / span), (unsigned)cache->n_kv_heads);
+    if (cache->head_dim == 128) bounds_kernel<16><<<grid, kBoundsThreads, 0, (cudaStream_t)stream>>>(a, span);
+    else bounds_kernel<8><<<grid, kBoundsThreads, 0, (cudaStream_t)stream>>>(a, span);
     return qmoe::launch_check("kv4_block_bounds");
 }
 
@@ -356,15 +511,23 @@ extern "C" int kv4_select_blocks(const kv4_bounds* bounds, const void* q, int n_
     a.bits = 15;
     while ((1 << (15 - a.bits)) < a.group) --a.bits;
     cudaStream_t st = (cudaStream_t)stream;
-    const int64_t chunks = (row + kScoreBlocks - 1) / kScoreBlocks, blocks = chunks * n_q_tokens;
+    const int chunk = score_chunk(bounds->head_dim, n_kv);
+    const int64_t chunks = (row + chunk - 1) / chunk, blocks = chunks * n_q_tokens;
     if (blocks > 0x7FFFFFFFLL || (int64_t)n_q_tokens * n_kv > 0x7FFFFFFFLL)
         return qmoe::fail(QMOE_EINVAL, "kv4_select_blocks: too many query tokens in one call");
-    if (row > top) {
-        if (!workspace || !kv4::aligned16(workspace)) return qmoe::fail(QMOE_EINVAL, "kv4_select_blocks: workspace NULL or not 16-byte aligned");
-        if (bounds->head_dim == 128) score_kernel<128><<<(unsigned)blocks, kScoreThreads, 0, st>>>(a, (int)chunks);
-        else score_kernel<64><<<(unsigned)blocks, kScoreThreads, 0, st>>>(a, (int)chunks);
-        if ((rc = qmoe::launch_check("kv4_select_blocks"))) return rc;
+    const unsigned lists = (unsigned)(n_q_tokens * n_kv);
+    if (row <= top) {
+        pick_kernel<128, 0><<<lists, 128, 0, st>>>(a);      // every block that is there
+        return qmoe::launch_check("kv4_select_blocks");
     }
-    pick_kernel<<<(unsigned)(n_q_tokens * n_kv), kPickThreads, 0, st>>>(a);
-    return qmoe::launch_check("kv4_select_blocks");
+    if (!workspace || !kv4::aligned16(workspace)) return qmoe::fail(QMOE_EINVAL, "kv4_select_blocks: workspace NULL or not 16-byte aligned");
+    if (bounds->head_dim == 128) score_kernel<128><<<(unsigned)blocks, kScoreThreads, 0, st>>>(a, (int)chunks);
+    else score_kernel<64><<<(unsigned)blocks, kScoreThreads, 0, st>>>(a, (int)chunks);
+    if ((rc = qmoe::launch_check("kv4_select_blocks"))) return rc;
+    const char* who = "kv4_select_blocks";
+    if (row <= 512) return kv4::launch_dependent(pick_kernel<128, 4>, dim3(lists), 128, 0, st, who, a);
+    if (row <= 2048) return kv4::launch_dependent(pick_kernel<256, 8>, dim3(lists), 256, 0, st, who, a);
+    if (row <= 8192) return kv4::launch_dependent(pick_kernel<512, 16>, dim3(lists), 512, 0, st, who, a);
+    if (row <= 16384) return kv4::launch_dependent(pick_kernel<1024, 16>, dim3(lists), 1024, 0, st, who, a);
+    return kv4::launch_dependent(pick_kernel<1024, 0>, dim3(lists), 1024, 0, st, who, a);
 }

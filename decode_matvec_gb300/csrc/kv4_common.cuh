@@ -57,6 +57,10 @@ inline int view_of(const kv4_cache* c, const char* who, CacheView* v) {
     return QMOE_OK;
 }
 
+// Programmatic dependent launch: the kernels of a call overlap each other's launches.
+__device__ __forceinline__ void depend_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void depend_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 template <typename T>
