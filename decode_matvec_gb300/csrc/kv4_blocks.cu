@@ -14,6 +14,20 @@ __device__ int g_kv4_blocks_error;
 
 __device__ __forceinline__ void blocks_set_error(int code) { atomicCAS(&g_kv4_blocks_error, 0, code); }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(*(unsigned long long*)&r) : "l"(*(unsigned long long*)&a), "l"(*(unsigned long long*)&b));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(*(unsigned long long*)&r)
+        : "l"(*(unsigned long long*)&a), "l"(*(unsigned long long*)&b), "l"(*(unsigned long long*)&c));
+    return r;
+}
+
 // ---------------------------------------------------------------- bounds of a block's keys
 struct BoundsArgs {
     kv4::CacheView cache;
@@ -58,24 +72,36 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(BoundsArgs a, in
         __half2 sz[STEPS];
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
-            const int r = row + k * ROWS;
-            if (r < count) w[k] = words[r * L + gl], sz[k] = pairs[r];
+            if ((k & ~1) * ROWS < P) {
+                const int r = min(row + k * ROWS, count - 1);
+                w[k] = words[r * L + gl], sz[k] = pairs[r];
+            }
         }
+        // Rows past the block's end repeat a row of it.  A code is a float's low bits above 2^23, where it stands in its
+        // half of the word: 16^i u, which a scale of s 16^-i makes the same product, exactly.
         float lo[8], hi[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) lo[c] = INFINITY, hi[c] = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < STEPS; ++k) {
-            if (row + k * ROWS < count) {
-                const float2 p = __half22float2(sz[k]);
+        for (int k = 0; k < STEPS; k += 2) {
+            if (k * ROWS >= P) break;
+            float v[2][8];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    // the code as the low bits of 2^23: one mask instead of a conversion
-                    const float u = __uint_as_float((w[k] >> (4 * (c >> 1) + 16 * (c & 1)) & 15u) | 0x4B000000u) - 8388608.f;
-                    const float v = fmaf(p.x, u, p.y);
-                    lo[c] = fminf(lo[c], v), hi[c] = fmaxf(hi[c], v);
+            for (int x = 0; x < 2; ++x) {
+                const float2 p = __half22float2(sz[k + x]);
+                const float2 z = make_float2(p.y, p.y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float one = p.x * (1.f / (float)(1 << 4 * i));
+                    const float2 u = add2(make_float2(__uint_as_float((w[k + x] & 15u << 4 * i) | 0x4B000000u),
+                                                      __uint_as_float((w[k + x] >> 16 & 15u << 4 * i) | 0x4B000000u)),
+                                          make_float2(-8388608.f, -8388608.f));
+                    const float2 r = fma2(make_float2(one, one), u, z);
+                    v[x][2 * i] = r.x, v[x][2 * i + 1] = r.y;
                 }
             }
+#pragma unroll
+            for (int c = 0; c < 8; ++c) lo[c] = fminf(fminf(lo[c], v[0][c]), v[1][c]), hi[c] = fmaxf(fmaxf(hi[c], v[0][c]), v[1][c]);
         }
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -127,6 +153,7 @@ struct SelectArgs {
     const int32_t *q_start, *kv_len, *table;
     int32_t* sel;
     float* scores;         // [token][kv head][max_seen]
+    uint16_t* whole;       // [token][kv head][2 D]: sums of the group's queries as whole numbers
     int B, n, n_kv, group, n_pages, max_blocks, page_shift, max_kv, max_seen, top, first, last, bits;
 };
 
@@ -157,6 +184,61 @@ __device__ __forceinline__ float query_value(uint32_t bits) {
     return v == v ? fminf(fmaxf(v, -3.3895313892515355e38f), 3.3895313892515355e38f) : 0.f;
 }
 
+// The queries of one token and kv head as whole numbers: sums over the group of the positive parts, then of the negative
+// ones, 16 bits each.  A warp takes a (token, kv head), a lane D / 32 channels.
+constexpr int kWholeThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kWholeThreads) whole_kernel(SelectArgs a) {
+    constexpr int V = D / 32;
+    kv4::depend_launch();
+    const int64_t i = (int64_t)blockIdx.x * (kWholeThreads / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (i >= (int64_t)a.n * a.n_kv) return;
+    const uint16_t* q = a.q + i * a.group * D + lane * V;
+    auto load = [&](int g, uint32_t (&w)[V / 2]) {
+        if constexpr (V == 4) {
+            const uint2 x = *(const uint2*)(q + g * D);
+            w[0] = x.x, w[1] = x.y;
+        } else {
+            w[0] = *(const uint32_t*)(q + g * D);
+        }
+    };
+    float big = 0.f;
+#pragma unroll 8
+    for (int g = 0; g < a.group; ++g) {
+        uint32_t w[V / 2];
+        load(g, w);
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) big = fmaxf(big, fmaxf(fabsf(query_value(w[k] & 0xFFFFu)), fabsf(query_value(w[k] >> 16))));
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor_sync(QMOE_FULL_MASK, big, d));
+    // largest magnitude to [2^(bits-1), 2^bits): times 2^(bits - 1 - exponent), in two factors of normal size
+    const int up = a.bits - 1 - ilogbf(big > 0.f ? big : 1.f), limit = (1 << a.bits) - 1;
+    const float f1 = __int_as_float((min(up, 100) + 127) << 23), f2 = __int_as_float((max(up - 100, 0) + 127) << 23);
+    int pos[V], neg[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) pos[k] = neg[k] = 0;
+#pragma unroll 8
+    for (int g = 0; g < a.group; ++g) {
+        uint32_t w[V / 2];
+        load(g, w);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const float v = query_value(k & 1 ? w[k >> 1] >> 16 : w[k >> 1] & 0xFFFFu);
+            const int r = min(max(__float2int_rn(v * f1 * f2), -limit), limit);
+            pos[k] += max(r, 0), neg[k] += min(r, 0);
+        }
+    }
+    uint32_t* out = (uint32_t*)(a.whole + i * (2 * D)) + lane * (V / 2);
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+        out[k] = __byte_perm((uint32_t)pos[2 * k], (uint32_t)pos[2 * k + 1], 0x5410);
+        out[D / 2 + k] = __byte_perm((uint32_t)neg[2 * k], (uint32_t)neg[2 * k + 1], 0x5410);
+    }
+}
+
 // Lanes that take a record (hi and lo codes, 16 a lane), and records of one kv head that they take at once.
 template <int D>
 constexpr int kRecordLanes = D / 8;
@@ -169,8 +251,8 @@ inline int score_chunk(int head_dim, int n_kv) {
 
 // A thread block scores `chunk` blocks of one query token for every kv head.  L lanes take L records of one kv head: lane i
 // looks up the i-th one's page and step, all of them load their 16 codes of every record (L loads of 16 bytes in flight), multiply
-// them with the group's summed queries, which a lane keeps in registers, and the L x L partial sums are added up crosswise, so
-// that lane i ends with the i-th record's.
+// them with the group's summed queries, and the L x L partial sums are added up crosswise, so that lane i ends with the i-th
+// record's.  What does not depend on the queries goes ahead of the wait for them.
 template <int D>
 __global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int chunks) {
     constexpr int L = kRecordLanes<D>, GROUPS = kScoreThreads / L;
@@ -181,10 +263,12 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int 
     const int grp = threadIdx.x / L, gl = threadIdx.x & (L - 1);
     const int parts = max(1, GROUPS / a.n_kv);
     // few blocks are all taken
-    if (seen <= a.top || c * parts * L >= seen || grp >= a.n_kv * parts) return;      // (whole groups of lanes leave)
-    const int j = (c * parts + grp / a.n_kv) * L + gl;                                // the block that this lane looks up
-    const int base = threadIdx.x & 31 & ~(L - 1);
-    const unsigned mask = (L == 16 ? 0xFFFFu : 0xFFu) << base;
+    if (seen <= a.top || c * parts * L >= seen || grp >= a.n_kv * parts) {      // (whole groups of lanes leave)
+        kv4::depend_wait();
+        return;
+    }
+    const int j = (c * parts + grp / a.n_kv) * L + gl;                          // the block that this lane looks up
+    const unsigned mask = (L == 16 ? 0xFFFFu : 0xFFu) << (threadIdx.x & 31 & ~(L - 1));
     int page = -1;
     if (j < seen) {
         page = j < a.max_blocks ? a.table[(int64_t)b * a.max_blocks + j] : -1;
@@ -193,6 +277,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int 
             page = -1;
         }
     }
+    bool waited = false;
     for (int h = grp % a.n_kv; h < a.n_kv; h += GROUPS) {
         const float step = page >= 0 ? a.steps[(int64_t)page * a.n_kv + h] : 0.f;
         uint4 code[L];
@@ -202,44 +287,14 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int 
             code[i] = make_uint4(0, 0, 0, 0);
             if (pg >= 0) code[i] = *(const uint4*)(a.codes + ((int64_t)pg * a.n_kv + h) * (2 * D) + gl * 16);
         }
-        // this lane's 16 channels of the queries: of hi the positive parts, of lo the negative ones
-        const int d0 = (gl * 16) % D;
-        const bool low = gl * 16 >= D;
-        const uint16_t* q = a.q + ((int64_t)t * a.n_kv + h) * a.group * D + d0;
-        float big = 0.f;
-#pragma unroll 4
-        for (int g = 0; g < a.group; ++g) {
-            const uint4 x[2] = {((const uint4*)(q + g * D))[0], ((const uint4*)(q + g * D))[1]};
-            const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) big = fmaxf(big, fmaxf(fabsf(query_value(w[i] & 0xFFFFu)), fabsf(query_value(w[i] >> 16))));
-        }
-#pragma unroll
-        for (int d = L / 2; d > 0; d >>= 1) big = fmaxf(big, __shfl_xor_sync(mask, big, d));
-        // largest magnitude to [2^(bits-1), 2^bits): times 2^(bits - 1 - exponent), in two factors of normal size
-        const int up = a.bits - 1 - ilogbf(big > 0.f ? big : 1.f), limit = (1 << a.bits) - 1;
-        const float f1 = __int_as_float((min(up, 100) + 127) << 23), f2 = __int_as_float((max(up - 100, 0) + 127) << 23);
-        int sum[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum[i] = 0;
-#pragma unroll 2
-        for (int g = 0; g < a.group; ++g) {
-            const uint4 x[2] = {((const uint4*)(q + g * D))[0], ((const uint4*)(q + g * D))[1]};
-            const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float v = query_value(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu);
-                const int r = min(max(__float2int_rn(v * f1 * f2), -limit), limit);
-                sum[i] += low ? min(r, 0) : max(r, 0);
-            }
-        }
-        uint32_t pk[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) pk[i] = __byte_perm((uint32_t)sum[2 * i], (uint32_t)sum[2 * i + 1], 0x5410);
+        if (!waited) kv4::depend_wait();
+        waited = true;
+        const uint4* q = (const uint4*)(a.whole + ((int64_t)t * a.n_kv + h) * (2 * D) + gl * 16);
+        const uint4 p0 = q[0], p1 = q[1];
         int acc[L];
 #pragma unroll
         for (int i = 0; i < L; ++i)
-            acc[i] = dot4(code[i].w, pk[6], pk[7], dot4(code[i].z, pk[4], pk[5], dot4(code[i].y, pk[2], pk[3], dot4(code[i].x, pk[0], pk[1], 0))));
+            acc[i] = dot4(code[i].w, p1.z, p1.w, dot4(code[i].z, p1.x, p1.y, dot4(code[i].y, p0.z, p0.w, dot4(code[i].x, p0.x, p0.y, 0))));
         // lane i keeps the records whose number has the lane's upper bits, and gives the others away
 #pragma unroll
         for (int d = L / 2; d > 0; d >>= 1) {
@@ -353,14 +408,14 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(SelectArgs a) {
             // the bin of the want-th score: a scan by the first warp, 32 bins a lane
             if (warp == 0) {
                 int mine = 0;
-#pragma unroll 8
+#pragma unroll
                 for (int i = 0; i < kBins / 32; ++i) mine += sh.bins[lane * (kBins / 32) + ((i + lane) & (kBins / 32 - 1))];      // (skewed: no bank conflicts)
-                const int before = warp_incl_scan(mine, lane) - mine;
-                if (before < want && before + mine >= want) {
-                    int at = lane * (kBins / 32), sum = before;
-                    while (sum + sh.bins[at] < want) sum += sh.bins[at++];
-                    sh.bin = at, sh.need = want - sum;
-                }
+                const int sum = warp_incl_scan(mine, lane);
+                const int row = __ffs(__ballot_sync(QMOE_FULL_MASK, sum >= want)) - 1;        // the 32 bins that hold it
+                const int before = __shfl_sync(QMOE_FULL_MASK, sum - mine, row);
+                const int one = sh.bins[row * (kBins / 32) + lane], upto = before + warp_incl_scan(one, lane);
+                const int at = __ffs(__ballot_sync(QMOE_FULL_MASK, upto >= want)) - 1;
+                if (lane == at) sh.bin = row * (kBins / 32) + at, sh.need = want - (upto - one);
             }
             __syncthreads();
             const int bin = sh.bin, need = sh.need, many = sh.bins[bin];
@@ -404,8 +459,9 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(SelectArgs a) {
 #pragma unroll
     for (int i = 0; i < (R ? R : steps); ++i) {
         const uint32_t k = key_at(i, w0 + 32 * i + lane);
-        above += __popc(__ballot_sync(QMOE_FULL_MASK, k > cut)), equal += __popc(__ballot_sync(QMOE_FULL_MASK, k == cut));
+        above += k > cut, equal += k == cut;
     }
+    above = (int)__reduce_add_sync(QMOE_FULL_MASK, (unsigned)above), equal = (int)__reduce_add_sync(QMOE_FULL_MASK, (unsigned)equal);
     if (lane == 0) sh.above[warp] = above, sh.equal[warp] = equal;
     __syncthreads();
     int all_above = 0, above_before = 0, equal_before = 0;
@@ -421,7 +477,9 @@ __global__ void __launch_bounds__(THREADS) pick_kernel(SelectArgs a) {
     for (int i = 0; i < (R ? R : steps); ++i) {
         const int j = w0 + 32 * i + lane;
         const uint32_t k = key_at(i, j);
-        const unsigned over = __ballot_sync(QMOE_FULL_MASK, k > cut), same = __ballot_sync(QMOE_FULL_MASK, k == cut);
+        const unsigned hit = __ballot_sync(QMOE_FULL_MASK, k >= cut);
+        if (hit == 0) continue;
+        const unsigned over = __ballot_sync(QMOE_FULL_MASK, k > cut), same = hit & ~over;
         const int n_same = equal_before + __popc(same & below);
         if (k > cut || (k == cut && n_same < room)) sel[a.first + above_before + __popc(over & below) + min(n_same, room)] = j;
         above_before += __popc(over), equal_before += __popc(same);
@@ -440,6 +498,9 @@ int check_bounds(const kv4_bounds* b, const char* who) {
 }
 
 int shift_of(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : 6; }
+
+// Workspace: the queries as whole numbers (room for the larger head_dim), then the scores.
+size_t whole_bytes(int n_q_tokens, int n_kv_heads) { return (size_t)n_q_tokens * n_kv_heads * (2 * 128) * sizeof(uint16_t); }
 
 // Scores of a (token, kv head), rounded up to 16 bytes.
 int64_t score_row(int page_size, int max_kv) { return (((int64_t)max_kv + page_size - 1) / page_size + 3) & ~(int64_t)3; }
@@ -482,7 +543,7 @@ extern "C" int kv4_select_blocks_ws_size(int n_q_tokens, int n_kv_heads, int pag
     if (!bytes) return qmoe::fail(QMOE_EINVAL, "kv4_select_blocks_ws_size: NULL output");
     if (n_q_tokens < 0 || n_kv_heads < 1 || max_kv < 0 || (page_size != 16 && page_size != 32 && page_size != 64))
         return qmoe::fail(QMOE_EINVAL, "kv4_select_blocks_ws_size: bad sizes (page_size 16, 32 or 64)");
-    *bytes = (size_t)n_q_tokens * n_kv_heads * (size_t)score_row(page_size, max_kv) * sizeof(float);
+    *bytes = whole_bytes(n_q_tokens, n_kv_heads) + (size_t)n_q_tokens * n_kv_heads * (size_t)score_row(page_size, max_kv) * sizeof(float);
     return QMOE_OK;
 }
 
@@ -503,9 +564,11 @@ extern "C" int kv4_select_blocks(const kv4_bounds* bounds, const void* q, int n_
     if (!kv4::aligned16(q)) return qmoe::fail(QMOE_EINVAL, "kv4_select_blocks: q not 16-byte aligned");
     SelectArgs a{};
     const int64_t row = score_row(bounds->page_size, max_kv);
-    if (ws_bytes < (size_t)n_q_tokens * n_kv * (size_t)row * sizeof(float)) return qmoe::fail(QMOE_ECAPACITY, "kv4_select_blocks: workspace too small");
+    const size_t whole = whole_bytes(n_q_tokens, n_kv);
+    if (ws_bytes < whole + (size_t)n_q_tokens * n_kv * (size_t)row * sizeof(float)) return qmoe::fail(QMOE_ECAPACITY, "kv4_select_blocks: workspace too small");
     a.codes = (const int8_t*)bounds->codes, a.steps = bounds->steps, a.q = (const uint16_t*)q;
-    a.q_start = q_start, a.kv_len = kv_len, a.table = table, a.sel = sel, a.scores = (float*)workspace;
+    a.q_start = q_start, a.kv_len = kv_len, a.table = table, a.sel = sel;
+    a.whole = (uint16_t*)workspace, a.scores = (float*)((char*)workspace + whole);
     a.B = B, a.n = n_q_tokens, a.n_kv = n_kv, a.group = n_q_heads / n_kv, a.n_pages = bounds->n_pages, a.max_blocks = max_blocks;
     a.page_shift = shift_of(bounds->page_size), a.max_kv = max_kv, a.max_seen = (int)row, a.top = top, a.first = first, a.last = last;
     a.bits = 15;
@@ -521,10 +584,13 @@ extern "C" int kv4_select_blocks(const kv4_bounds* bounds, const void* q, int n_
         return qmoe::launch_check("kv4_select_blocks");
     }
     if (!workspace || !kv4::aligned16(workspace)) return qmoe::fail(QMOE_EINVAL, "kv4_select_blocks: workspace NULL or not 16-byte aligned");
-    if (bounds->head_dim == 128) score_kernel<128><<<(unsigned)blocks, kScoreThreads, 0, st>>>(a, (int)chunks);
-    else score_kernel<64><<<(unsigned)blocks, kScoreThreads, 0, st>>>(a, (int)chunks);
-    if ((rc = qmoe::launch_check("kv4_select_blocks"))) return rc;
     const char* who = "kv4_select_blocks";
+    const unsigned whole_blocks = (lists + kWholeThreads / 32 - 1) / (kWholeThreads / 32);
+    const bool d128 = bounds->head_dim == 128;
+    if (d128) whole_kernel<128><<<whole_blocks, kWholeThreads, 0, st>>>(a);
+    else whole_kernel<64><<<whole_blocks, kWholeThreads, 0, st>>>(a);
+    if ((rc = qmoe::launch_check(who))) return rc;
+    if ((rc = kv4::launch_dependent(d128 ? score_kernel<128> : score_kernel<64>, dim3((unsigned)blocks), kScoreThreads, 0, st, who, a, (int)chunks))) return rc;
     if (row <= 512) return kv4::launch_dependent(pick_kernel<128, 4>, dim3(lists), 128, 0, st, who, a);
     if (row <= 2048) return kv4::launch_dependent(pick_kernel<256, 8>, dim3(lists), 256, 0, st, who, a);
     if (row <= 8192) return kv4::launch_dependent(pick_kernel<512, 16>, dim3(lists), 512, 0, st, who, a);

@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.cuh"
 
@@ -234,7 +235,7 @@ int launch_norm(const NormArgs& a, cudaStream_t st) {
 // same bias, those are made in fp64: of the experts in question (fp64 runs at a 64th of fp32's rate here), of the groups' best
 // ones, or of a whole row where more of its experts are in question than the list of the chosen holds.
 //
-// A lane holds R neighbouring experts as integer keys, and the 8 best of them sorted; among lanes with equal keys the
+// A lane holds R neighbouring experts as integer keys, and the 4 best of them sorted; among lanes with equal keys the
 // lowest has the lowest index.  A round of the choice is a reduction of the lanes' heads (one instruction), a ballot, and the
 // winner's list moving up.  Which expert a key was is looked up at the end, for all the chosen at once.  A warp takes a
 // token; above 1024 experts a block of 8 warps does, each warp's best being merged by the first.
@@ -331,16 +332,12 @@ __device__ __forceinline__ void sort_keys(uint32_t* v) {
         order(v[0], v[1]);
     } else if constexpr (N == 4) {
         order(v[0], v[1]), order(v[2], v[3]), order(v[0], v[2]), order(v[1], v[3]), order(v[1], v[2]);
-    } else if constexpr (N == 8) {
-        // Batcher's odd-even merge sort
-        sort_keys<4>(v), sort_keys<4>(v + 4);
-        order(v[0], v[4]), order(v[1], v[5]), order(v[2], v[6]), order(v[3], v[7]);
-        order(v[2], v[4]), order(v[3], v[5]);
-        order(v[1], v[2]), order(v[3], v[4]), order(v[5], v[6]);
     }
 }
+// The keys that a lane keeps sorted.  Four: a lane of the 32 rarely holds more of the chosen (then choose_slow goes through all
+// of them), and a round moves the list up by one.
 template <int R>
-constexpr int kDepth = R < 8 ? R : 8;
+constexpr int kDepth = R < 4 ? R : 4;
 
 // The best kDepth<R> of R keys.
 template <int R>
@@ -349,39 +346,44 @@ __device__ __forceinline__ void best_keys(const uint32_t (&key)[R], uint32_t (&l
     for (int i = 0; i < kDepth<R>; ++i) list[i] = key[i];
     sort_keys<kDepth<R>>(list);
 #pragma unroll
-    for (int c = 8; c < R; c += 8) {
-        uint32_t more[8];
+    for (int c = 4; c < R; c += 4) {
+        uint32_t more[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) more[i] = key[c + i];
-        sort_keys<8>(more);
+        for (int i = 0; i < 4; ++i) more[i] = key[c + i];
+        sort_keys<4>(more);
         // the larger halves of a bitonic sequence, then its merge
 #pragma unroll
-        for (int i = 0; i < kDepth<R>; ++i) list[i] = max(list[i], more[7 - i]);
-#pragma unroll
-        for (int d = 4; d > 0; d >>= 1)
-#pragma unroll
-            for (int i = 0; i < kDepth<R>; ++i)
-                if (!(i & d)) order(list[i], list[(i + d) & 7]);
+        for (int i = 0; i < kDepth<R>; ++i) list[i] = max(list[i], more[3 - i]);
+        if constexpr (R > 4) order(list[0], list[2]), order(list[1], list[3]), order(list[0], list[1]), order(list[2], list[3]);
     }
 }
 
-// The `rounds` best of all lanes' lists: lane j gets the j-th one's key and the lane that held it.  False when a lane of
-// more than 8 keys gave away all that its list held.
-template <int R>
-__device__ __forceinline__ bool choose(uint32_t (&list)[kDepth<R>], int rounds, int lane, uint32_t* my_key, int* my_lane) {
+// The `rounds` best of all lanes' lists: lane j gets the j-th one's key and the lane that held it.
+template <int N>
+__device__ __forceinline__ void choose(uint32_t (&list)[N], int rounds, int lane, uint32_t* my_key, int* my_lane) {
     *my_key = 0, *my_lane = 0;
-    int given = 0;
     for (int j = 0; j < rounds; ++j) {
         const uint32_t m = __reduce_max_sync(QMOE_FULL_MASK, list[0]);
         const int w = __ffs(__ballot_sync(QMOE_FULL_MASK, list[0] == m)) - 1;
         if (lane == j) *my_key = m, *my_lane = w;
         const bool mine = lane == w;
-        if (R > 8) given += mine && m;
 #pragma unroll
-        for (int i = 0; i + 1 < kDepth<R>; ++i) list[i] = mine ? list[i + 1] : list[i];
-        list[kDepth<R> - 1] = mine ? 0u : list[kDepth<R> - 1];
+        for (int i = 0; i + 1 < N; ++i) list[i] = mine ? list[i + 1] : list[i];
+        list[N - 1] = mine ? 0u : list[N - 1];
     }
-    return R <= 8 || !__any_sync(QMOE_FULL_MASK, given >= 8);
+}
+
+// Whether a lane's list (`had`: it was not empty) ran out while it held another of the `rounds` best.
+template <int R>
+__device__ __forceinline__ bool ran_out(const uint32_t (&key)[R], const uint32_t (&list)[kDepth<R>], bool had, int rounds, uint32_t my_key) {
+    if (R <= kDepth<R>) return false;
+    const bool empty = had && list[0] == 0;
+    if (!__any_sync(QMOE_FULL_MASK, empty)) return false;
+    const uint32_t last = __shfl_sync(QMOE_FULL_MASK, my_key, rounds - 1);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) n += key[i] && key[i] >= last;
+    return __any_sync(QMOE_FULL_MASK, empty && n > kDepth<R>);
 }
 
 // Which of its lane's experts the key of lane j's choice was: the first with that key, or the one after where the same
@@ -402,25 +404,21 @@ __device__ __forceinline__ int which(const uint32_t (&key)[R], uint32_t my_key, 
     return my_lane * R + at;
 }
 
-// As choose and which, from the keys themselves (any number of a lane's), which it takes out; the slow way.  The remaining
-// keys' largest is returned.
+// As choose and which, from the keys themselves (any number of a lane's), which it takes out; the slow way.
 template <int R>
-__device__ __noinline__ uint32_t choose_slow(uint32_t* key, int rounds, int lane, uint32_t* my_key, int* my_at) {
+__device__ __noinline__ void choose_slow(uint32_t* key, int rounds, int lane, uint32_t* my_key, int* my_at) {
     *my_key = 0, *my_at = -1;
-    uint32_t best = 0;
-    int at = 0;
-    for (int j = 0; j <= rounds; ++j) {
-        best = 0;
+    for (int j = 0; j < rounds; ++j) {
+        uint32_t best = 0;
+        int at = 0;
         for (int i = 0; i < R; ++i)
             if (key[i] > best) best = key[i], at = i;
         const uint32_t m = __reduce_max_sync(QMOE_FULL_MASK, best);
-        if (j == rounds) break;
         const int w = __ffs(__ballot_sync(QMOE_FULL_MASK, best == m)) - 1;
         const int tag = __shfl_sync(QMOE_FULL_MASK, lane * R + at, w);
         if (lane == j) *my_key = m, *my_at = m ? tag : -1;
         if (lane == w) key[at] = 0;
     }
-    return best;
 }
 
 struct Pair {
@@ -487,7 +485,9 @@ __device__ __noinline__ double exact_groups(const RouteArgs& a, const X* row, in
     const int lane = threadIdx.x & 31, size = a.E / a.groups;
     const double z = exact_sum<X, 1>(a, row, e0, R, top, nullptr);
     double c[32], mine = 0.0;
-    for (int i = 0; i < R; ++i) c[i] = (cand >> i) & 1 ? exact_value(a, row, e0 + i, top, z) : -INFINITY;
+    for (int i = 0; i < R; ++i) c[i] = -INFINITY;
+    for (uint32_t todo = cand; todo; todo &= todo - 1) c[__ffs(todo) - 1] = exact_value(a, row, e0 + __ffs(todo) - 1, top, z);
+    __syncwarp();
     for (uint32_t todo = which_groups; todo; todo &= todo - 1) {
         const int g = __ffs(todo) - 1;
         double b0 = -INFINITY, b1 = -INFINITY;
@@ -509,12 +509,18 @@ __device__ __noinline__ double exact_groups(const RouteArgs& a, const X* row, in
 }
 
 // The choice among the experts that each lane names, by NW warps: lane j of each gets the j-th expert.
-template <typename X, int NW>
-__device__ __noinline__ int exact_choice(const RouteArgs& a, const X* row, int e0, int R, float top, uint32_t cand, ResolveShared* sh) {
+template <typename X, int NW, typename Bits>
+__device__ __noinline__ int exact_choice(const RouteArgs& a, const X* row, int e0, int R, float top, Bits cand, ResolveShared* sh) {
+    constexpr int MOST = 8 * sizeof(Bits);
     const int lane = threadIdx.x & 31, warp = NW == 1 ? 0 : threadIdx.x >> 5;
     const double z = exact_sum<X, NW>(a, row, e0, R, top, sh);
-    unsigned long long c[32];
-    for (int i = 0; i < R; ++i) c[i] = (cand >> i) & 1 ? key_of(exact_value(a, row, e0 + i, top, z)) : 0ull;
+    unsigned long long c[MOST];
+    for (int i = 0; i < R; ++i) c[i] = 0ull;
+    for (Bits todo = cand; todo; todo &= todo - 1) {
+        const int i = sizeof(Bits) == 8 ? __ffsll((long long)todo) - 1 : __ffs((int)todo) - 1;
+        c[i] = key_of(exact_value(a, row, e0 + i, top, z));
+    }
+    __syncwarp();
     int got = 0;
     for (int j = 0; j < a.k; ++j) {
         unsigned long long best = 0;
@@ -585,15 +591,15 @@ __device__ __forceinline__ void write_route(const RouteArgs& a, int64_t t, int i
                 g = expf(l - big);
             } else {
                 const float e = expf(-fabsf(l));      // 1 / (1 + e^-l) = e^l / (1 + e^l)
-                g = (l >= 0.f ? 1.f : big >= 0.f ? e : expf(l - big)) / (1.f + e);
+                g = (l >= 0.f ? 1.f : big >= 0.f ? e : expf(l - big)) * rcp(1.f + e);
             }
         }
         const float sum = warp_sum(g);
-        g = sum > 0.f ? g / sum : 0.f;
+        g = sum > 0.f ? __fdividef(g, sum) : 0.f;      // (a sum of at most 32 terms up to 1)
     } else if (l > -INFINITY) {
         if (a.sigmoid) {
             const float e = expf(-fabsf(l));
-            g = (l >= 0.f ? 1.f : e) / (1.f + e);
+            g = (l >= 0.f ? 1.f : e) * rcp(1.f + e);
         } else {
             g = expf(l - top) / z;
         }
@@ -606,13 +612,12 @@ __device__ __forceinline__ void write_route(const RouteArgs& a, int64_t t, int i
 
 // R experts a lane; NW warps a token (1: kRouteWarps tokens a block).
 template <typename X, int R, int NW>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(kRouteWarps * 32, R <= 8 ? 4 : 2) route_kernel(RouteArgs a) {
     __shared__ ResolveShared rs;
     __shared__ float2 part_s[kRouteWarps];
     __shared__ uint32_t key_s[NW > 1 ? kRouteWarps * 32 : 1];
     __shared__ int id_s[NW > 1 ? kRouteWarps * 32 : 1];
     __shared__ float2 bound_s;
-    __shared__ uint32_t left_s[kRouteWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = NW == 1 ? (int64_t)blockIdx.x * kRouteWarps + warp : blockIdx.x;
     if (t >= a.T) return;
@@ -666,7 +671,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
     for (int i = 0; i < R; ++i) key[i] = e0 + i < a.E ? key_of(c[i]) : 0u;
     const float slack = by_logit ? 0.f : score_err;
     best_keys<R>(key, list);
-    if constexpr (NW == 1) {
+    if constexpr (NW == 1 && R <= 32) {
         if (a.groups > 1) {
             // ---- groups
             const int size = a.E / a.groups, lanes = size / R;
@@ -740,36 +745,30 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
     }
     // ---- the k best, and the next one where the values are not exact
     const int rounds = min(a.k + (by_logit ? 0 : 1), 32);
-    uint32_t mk, left;      // left: the largest key that was not taken
+    uint32_t mk;
     int at;
-    {
-        int from;
-        if (__builtin_expect(choose<R>(list, rounds, lane, &mk, &from), 1)) {
-            at = which<R>(key, mk, from, lane);
-            left = list[0];
-        } else {
-            uint32_t all[R];
+    int from;
+    const bool had = list[0] != 0;
+    choose(list, rounds, lane, &mk, &from);
+    if (__builtin_expect(ran_out<R>(key, list, had, rounds, mk), 0)) {
+        uint32_t all[R];
 #pragma unroll
-            for (int i = 0; i < R; ++i) all[i] = key[i];
-            left = choose_slow<R>(all, rounds, lane, &mk, &at);
-        }
+        for (int i = 0; i < R; ++i) all[i] = key[i];
+        choose_slow<R>(all, rounds, lane, &mk, &at);
+    } else {
+        at = which<R>(key, mk, from, lane);
     }
     if constexpr (NW > 1) {
         key_s[warp * 32 + lane] = lane < rounds ? mk : 0u;
         id_s[warp * 32 + lane] = lane < rounds && mk ? warp * 32 * R + at : 0;
-        left = __reduce_max_sync(QMOE_FULL_MASK, left);
-        if (lane == 0) left_s[warp] = left;
         __syncthreads();
         if (warp == 0) {
             // the warps' lists one behind the other, eight entries a lane: lower lanes hold lower experts among equal keys
-            uint32_t keys[8], lists[8];
+            uint32_t keys[8], sorted[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) keys[i] = key_s[lane * 8 + i];
-            best_keys<8>(keys, lists);
-            int from;
-            choose<8>(lists, rounds, lane, &mk, &from);
+            for (int i = 0; i < 8; ++i) sorted[i] = keys[i] = key_s[lane * 8 + i];      // (a part of a warp's list: in order already)
+            choose(sorted, rounds, lane, &mk, &from);
             at = id_s[which<8>(keys, mk, from, lane)];
-            left = max(lists[0], left_s[lane & (kRouteWarps - 1)]);
         }
     }
     // ---- the chosen ones' logits, and neighbours that are too near to tell
@@ -793,17 +792,19 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
             const bool doubts = __any_sync(QMOE_FULL_MASK, doubt);
             if (__builtin_expect(doubts || a.k == 32, 0)) {
                 last = value_of(__shfl_sync(QMOE_FULL_MASK, mk, a.k - 1));
-                const float from = last - (2.f * slack + 4.f * kUlp * fminf(fabsf(last), kLargest));
-                // experts outside the list that may belong into it
-                again = __any_sync(QMOE_FULL_MASK, left && !(value_of(left) < from));
-                if (!again && doubts) {
-                    if (NW == 1) {
+                const float least = last - (2.f * slack + 4.f * kUlp * fminf(fabsf(last), kLargest));
+                // experts outside the list that may belong into it: a block decides all of its doubts together
+                again = NW > 1;
+                if (NW == 1) {
+                    int may = 0;
+#pragma unroll
+                    for (int i = 0; i < R; ++i) may += key[i] && !(value_of(key[i]) < least);
+                    again = warp_sum_int(may) > __popc(__ballot_sync(QMOE_FULL_MASK, in_list && !(v < least)));
+                    if (!again && doubts) {
                         const unsigned pairs = __ballot_sync(QMOE_FULL_MASK, near);      // (equal ones with them)
                         const double z64 = exact_sum<X, 1>(a, row, e0, R, top, nullptr);
                         at = exact_order(a, row, __popc(__ballot_sync(QMOE_FULL_MASK, in_list)), v, at, ((pairs | pairs << 1) >> lane) & 1, top, z64);
                         if (in_list) l = logit(row, at);
-                    } else {
-                        again = true;
                     }
                 }
             }
@@ -816,12 +817,13 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
     }
     if (__builtin_expect(again, 0)) {
         // what may be among the chosen: values down to the k-th's less the errors
-        const float from = last - (2.f * slack + 4.f * kUlp * fminf(fabsf(last), kLargest));
-        uint32_t cand = 0u;
+        const float least = last - (2.f * slack + 4.f * kUlp * fminf(fabsf(last), kLargest));
+        using Bits = std::conditional_t<(R > 32), unsigned long long, uint32_t>;
+        Bits cand = 0;
 #pragma unroll
         for (int i = 0; i < R; ++i)
-            if (key[i] && !(value_of(key[i]) < from)) cand |= 1u << i;
-        at = exact_choice<X, NW>(a, row, e0, R, top, cand, &rs);
+            if (key[i] && !(value_of(key[i]) < least)) cand |= (Bits)1 << i;
+        at = exact_choice<X, NW, Bits>(a, row, e0, R, top, cand, &rs);
         if (lane < a.k) l = logit(row, at);
     }
     if (NW == 1 || warp == 0) write_route(a, t, at, l, top, z, lane);
@@ -837,6 +839,7 @@ int launch_route(const RouteArgs& a, cudaStream_t st) {
     else if (a.E <= 256) route_kernel<X, 8, 1><<<per_warp, threads, 0, st>>>(a);
     else if (a.E <= 512) route_kernel<X, 16, 1><<<per_warp, threads, 0, st>>>(a);
     else if (a.E <= 1024) route_kernel<X, 32, 1><<<per_warp, threads, 0, st>>>(a);
+    else if (a.E <= 2048 && a.T >= 8 * qmoe::sm_count()) route_kernel<X, 64, 1><<<per_warp, threads, 0, st>>>(a);
     else if (a.E <= 2048) route_kernel<X, 8, kRouteWarps><<<(unsigned)a.T, threads, 0, st>>>(a);
     else if (a.E <= 4096) route_kernel<X, 16, kRouteWarps><<<(unsigned)a.T, threads, 0, st>>>(a);
     else route_kernel<X, 32, kRouteWarps><<<(unsigned)a.T, threads, 0, st>>>(a);
