@@ -43,40 +43,91 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(*(unsigned long long*)&r) : "l"(*(unsigned long long*)&a), "l"(*(unsigned long long*)&b));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(*(unsigned long long*)&r) : "l"(*(unsigned long long*)&a), "l"(*(unsigned long long*)&b));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(*(unsigned long long*)&r)
+        : "l"(*(unsigned long long*)&a), "l"(*(unsigned long long*)&b), "l"(*(unsigned long long*)&c));
+    return r;
+}
+
+// A lane's values of a step: eight as four pairs (16-byte accesses), or one (any width, stride and alignment).
 template <int V>
-__device__ __forceinline__ void load_bf16(const uint16_t* p, float (&v)[V]) {
+struct Values {
+    float2 p[4];
+    __device__ __forceinline__ void add(const Values& o) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = add2(p[i], o.p[i]);
+    }
+    __device__ __forceinline__ void times(const Values& o) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = mul2(p[i], o.p[i]);
+    }
+    __device__ __forceinline__ void times(float f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = mul2(p[i], make_float2(f, f));
+    }
+    __device__ __forceinline__ float2 squares(float2 sum) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum = fma2(p[i], p[i], sum);
+        return sum;
+    }
+};
+template <>
+struct Values<1> {
+    float v;
+    __device__ __forceinline__ void add(const Values& o) { v += o.v; }
+    __device__ __forceinline__ void times(const Values& o) { v *= o.v; }
+    __device__ __forceinline__ void times(float f) { v *= f; }
+    __device__ __forceinline__ float2 squares(float2 sum) const { return make_float2(fmaf(v, v, sum.x), sum.y); }
+};
+
+template <int V>
+__device__ __forceinline__ Values<V> load_bf16(const uint16_t* p) {
+    Values<V> v;
     if constexpr (V == 8) {
         const uint4 w = *(const uint4*)p;
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(u[i]), v[2 * i + 1] = bf16_hi(u[i]);
+        for (int i = 0; i < 4; ++i) v.p[i] = make_float2(bf16_lo(u[i]), bf16_hi(u[i]));
     } else {
-        v[0] = bf16_to_f32(*p);
+        v.v = bf16_to_f32(*p);
     }
+    return v;
 }
 
 template <int V>
-__device__ __forceinline__ void store_bf16(uint16_t* p, const float (&v)[V]) {
-    if constexpr (V == 8) {
-        *(uint4*)p = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    } else {
-        *p = (uint16_t)pack_bf16(v[0], v[0]);
-    }
+__device__ __forceinline__ void store_bf16(uint16_t* p, const Values<V>& v) {
+    if constexpr (V == 8)
+        *(uint4*)p = make_uint4(pack_bf16(v.p[0].x, v.p[0].y), pack_bf16(v.p[1].x, v.p[1].y), pack_bf16(v.p[2].x, v.p[2].y), pack_bf16(v.p[3].x, v.p[3].y));
+    else
+        *p = (uint16_t)pack_bf16(v.v, 0.f);
 }
 
 template <typename X, int V>
-__device__ __forceinline__ void load_x(const X* p, float (&v)[V]) {
+__device__ __forceinline__ Values<V> load_x(const X* p) {
     if constexpr (sizeof(X) == 2) {
-        load_bf16<V>((const uint16_t*)p, v);
+        return load_bf16<V>((const uint16_t*)p);
     } else if constexpr (V == 8) {
         const float4 a = ((const float4*)p)[0], b = ((const float4*)p)[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        return Values<V>{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
     } else {
-        v[0] = *p;
+        return Values<V>{*(const float*)p};
     }
 }
 
-// Reduction over the W warps of a row (slot: this row's place in shared memory).
+// Reduction over the W warps of a row (slot: this row's places in shared memory).
 template <bool kMax>
 __device__ __forceinline__ float row_reduce(float v, int W, float* slot, int warp_in_row, int lane) {
 #pragma unroll
@@ -87,101 +138,100 @@ __device__ __forceinline__ float row_reduce(float v, int W, float* slot, int war
     if (W == 1) return v;
     if (lane == 0) slot[warp_in_row] = v;
     __syncthreads();
-    v = slot[lane & (W - 1)];
+    v = lane < W ? slot[lane] : 0.f;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
-        if (d < W) {
-            const float o = __shfl_xor_sync(QMOE_FULL_MASK, v, d);
-            v = kMax ? max_nan(v, o) : v + o;
-        }
+        const float o = __shfl_xor_sync(QMOE_FULL_MASK, v, d);
+        v = kMax ? max_nan(v, o) : v + o;
     }
     return v;
 }
 
-// 8 codes of y / s.  A reciprocal is within a step of the quotient's last place, before a rounding to 4 bits; it
-// overflows for scales near fp32's smallest, which divide.
-template <int V>
-__device__ __forceinline__ void store_codes(uint8_t* dst, const float (&y)[V], float s) {
-    static_assert(V == 8, "codes are written eight at a time");
-    float q[V];
-    if (s >= 1e-37f) {
-        const float inv = 1.f / s;
+__device__ __forceinline__ float largest(const Values<8>& v) {
+    float m = 0.f;
 #pragma unroll
-        for (int j = 0; j < V; ++j) q[j] = y[j] * inv;
+    for (int i = 0; i < 4; ++i) asm("max.NaN.abs.f32 %0, %1, %2, %0;" : "+f"(m) : "f"(v.p[i].x), "f"(v.p[i].y));
+    return m;
+}
+
+// 8 codes of y / s for s = m / 448, which is returned.  448 / m is within two steps of the quotient's last place, before a
+// rounding to 4 bits; where it or m leaves fp32's middle range, every code is a division.
+__device__ __forceinline__ float store_codes(uint8_t* dst, const Values<8>& y, float m) {
+    const float s = m * (1.f / 448.f);
+    float2 q[4];
+    if (m >= 1e-30f && m <= 1e30f) {
+        const float inv = __fdividef(448.f, m);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = mul2(y.p[i], make_float2(inv, inv));
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) q[j] = s > 0.f ? __fdiv_rn(y[j], s) : 0.f;      // (a NaN scale: codes 0)
+        for (int i = 0; i < 4; ++i)      // (0 and NaN: codes 0)
+            q[i] = s > 0.f ? make_float2(__fdiv_rn(y.p[i].x, s), __fdiv_rn(y.p[i].y, s)) : make_float2(0.f, 0.f);
     }
     uint32_t w[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-        w[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[4 * j], q[4 * j + 1]), __NV_SATFINITE, __NV_E4M3) |
-               (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[4 * j + 2], q[4 * j + 3]), __NV_SATFINITE, __NV_E4M3) << 16;
+        w[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(q[2 * j], __NV_SATFINITE, __NV_E4M3) |
+               (uint32_t)__nv_cvt_float2_to_fp8x2(q[2 * j + 1], __NV_SATFINITE, __NV_E4M3) << 16;
     *(uint2*)dst = make_uint2(w[0], w[1]);
+    return s;
 }
 
-// V values a lane and step (8: 16-byte accesses; 1: any width, stride and alignment), K steps, W warps a row.
+// K steps of V values a lane, W warps a row.
 template <typename X, int V, int K>
-__global__ void __launch_bounds__(V == 8 ? 1024 : 1024) norm_kernel(NormArgs a, int W) {
+__global__ void __launch_bounds__(1024) norm_kernel(NormArgs a, int W) {
     __shared__ float sum_s[32], max_s[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, in_row = warp & (W - 1), first = warp - in_row;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = W == 1 ? warp : warp / W, in_row = warp - row * W;
     const int rows = (blockDim.x >> 5) / W;
-    const int64_t t = (int64_t)blockIdx.x * rows + warp / W;
+    const int64_t t = (int64_t)blockIdx.x * rows + row;
     const bool on = t < a.T;
     const int c0 = in_row * 32 + lane, step = W * 32, chunks = on ? a.n / V : 0;
     const X* x = (const X*)a.x + t * a.x_stride;
-    float h[K][V];
+    Values<V> h[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) h[k][j] = 0.f;
-        if (c0 + k * step < chunks) load_x<X, V>(x + (int64_t)(c0 + k * step) * V, h[k]);
+        h[k] = Values<V>{};
+        if (c0 + k * step < chunks) h[k] = load_x<X, V>(x + (c0 + k * step) * V);
     }
     if (a.residual) {
         const uint16_t* r = a.residual + t * a.res_stride;
         uint16_t* ro = a.residual_out + t * a.res_out_stride;
+        Values<V> v[K];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (c0 + k * step < chunks) v[k] = load_bf16<V>(r + (c0 + k * step) * V);
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (c0 + k * step < chunks) {
-                float v[V];
-                load_bf16<V>(r + (int64_t)(c0 + k * step) * V, v);
-#pragma unroll
-                for (int j = 0; j < V; ++j) h[k][j] += v[j];
-                store_bf16<V>(ro + (int64_t)(c0 + k * step) * V, h[k]);
+                h[k].add(v[k]);
+                store_bf16<V>(ro + (c0 + k * step) * V, h[k]);
             }
     }
-    float ss = 0.f;
+    float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int j = 0; j < V; ++j) ss = fmaf(h[k][j], h[k][j], ss);
-    ss = row_reduce<false>(ss, W, sum_s + first, in_row, lane);
-    const float r = rsqrtf(ss / (float)a.n + a.eps);
+    for (int k = 0; k < K; ++k) ss = h[k].squares(ss);
+    const float sum = row_reduce<false>(ss.x + ss.y, W, sum_s + row * W, in_row, lane);
+    const float r = rsqrtf(__fdividef(sum, (float)a.n) + a.eps);
     float big = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int c = c0 + k * step;
         if (c < chunks) {
-            float w[V];
-            if (a.weight) load_bf16<V>(a.weight + (int64_t)c * V, w);
-#pragma unroll
-            for (int j = 0; j < V; ++j) h[k][j] = h[k][j] * r * (a.weight ? w[j] : 1.f);
-            if (a.y) store_bf16<V>(a.y + t * a.y_stride + (int64_t)c * V, h[k]);
+            h[k].times(r);
+            if (a.weight) h[k].times(load_bf16<V>(a.weight + c * V));
+            if (a.y) store_bf16<V>(a.y + t * a.y_stride + c * V, h[k]);
         }
         if constexpr (V == 8) {
             if (a.codes) {
-                float m = 0.f;
-#pragma unroll
-                for (int j = 0; j < V; ++j) m = max_nan(m, fabsf(h[k][j]));
+                float m = largest(h[k]);
                 if (a.row_scale) {
                     big = max_nan(big, m);
                 } else {       // 16 lanes hold 128 values
 #pragma unroll
                     for (int d = 8; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(QMOE_FULL_MASK, m, d));
                     if (c < chunks) {
-                        const float s = __fdiv_rn(m, 448.f);
+                        const float s = store_codes(a.codes + t * a.n + c * V, h[k], m);
                         if ((lane & 15) == 0) a.scales[t * ((a.n + 127) >> 7) + (c >> 4)] = s;
-                        store_codes<V>(a.codes + t * a.n + (int64_t)c * V, h[k], s);
                     }
                 }
             }
@@ -189,12 +239,11 @@ __global__ void __launch_bounds__(V == 8 ? 1024 : 1024) norm_kernel(NormArgs a, 
     }
     if constexpr (V == 8) {
         if (a.codes && a.row_scale) {
-            big = row_reduce<true>(big, W, max_s + first, in_row, lane);
-            const float s = __fdiv_rn(big, 448.f);
-            if (on && c0 == 0) a.scales[t] = s;
+            big = row_reduce<true>(big, W, max_s + row * W, in_row, lane);
+            if (on && c0 == 0) a.scales[t] = big * (1.f / 448.f);
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (c0 + k * step < chunks) store_codes<V>(a.codes + t * a.n + (int64_t)(c0 + k * step) * V, h[k], s);
+                if (c0 + k * step < chunks) store_codes(a.codes + t * a.n + (c0 + k * step) * V, h[k], big);
         }
     }
 }
@@ -203,23 +252,20 @@ constexpr int kNormMaxWidth = 32768;
 
 template <typename X, int V>
 int launch_norm(const NormArgs& a, cudaStream_t st) {
-    const int chunks = (a.n + V - 1) / V;
-    constexpr int kMost = V == 8 ? 4 : 32;      // steps that a thread's registers hold
-    // many rows: a few steps a thread; few rows: as many threads as a row has chunks
-    int W = 1;
-    while (W < 32 && W * 32 * (V == 8 ? 2 : 8) < chunks) W *= 2;
-    if (a.T < 2 * qmoe::sm_count())
-        while (W < 32 && W * 32 < chunks) W *= 2;
-    const int need = (chunks + 32 * W - 1) / (32 * W), rows = std::max(1, 8 / W);
-    const unsigned blocks = (unsigned)((a.T + rows - 1) / rows);
+    // as many threads as a row has steps, up to 512 (more steps a thread then), and rows side by side in a block of 256
+    const int chunks = a.n / V, most = V == 8 ? 4 : 32;
+    int K = 1;
+    while (K < most && (chunks + K - 1) / K > 512) K *= 2;
+    const int W = (chunks + 32 * K - 1) / (32 * K), rows = std::max(1, 8 / W);
+    const unsigned blocks = (unsigned)(((int64_t)a.T + rows - 1) / rows);
     const int threads = rows * W * 32;
-    if constexpr (V == 8) {
-        if (need <= 1) norm_kernel<X, V, 1><<<blocks, threads, 0, st>>>(a, W);
-        else if (need <= 2) norm_kernel<X, V, 2><<<blocks, threads, 0, st>>>(a, W);
-        else norm_kernel<X, V, kMost><<<blocks, threads, 0, st>>>(a, W);
-    } else {
-        if (need <= 8) norm_kernel<X, V, 8><<<blocks, threads, 0, st>>>(a, W);
-        else norm_kernel<X, V, kMost><<<blocks, threads, 0, st>>>(a, W);
+    if (K == 1) norm_kernel<X, V, 1><<<blocks, threads, 0, st>>>(a, W);
+    else if (K == 2) norm_kernel<X, V, 2><<<blocks, threads, 0, st>>>(a, W);
+    else if (K == 4) norm_kernel<X, V, 4><<<blocks, threads, 0, st>>>(a, W);
+    if constexpr (V == 1) {
+        if (K == 8) norm_kernel<X, V, 8><<<blocks, threads, 0, st>>>(a, W);
+        else if (K == 16) norm_kernel<X, V, 16><<<blocks, threads, 0, st>>>(a, W);
+        else if (K == 32) norm_kernel<X, V, 32><<<blocks, threads, 0, st>>>(a, W);
     }
     return qmoe::launch_check("add_rms_norm");
 }
@@ -246,11 +292,13 @@ struct RouteArgs {
     float* gates;
     int64_t stride;
     int T, E, k, sigmoid, groups, top_groups, best, renorm;
+    int group_size, group_lanes;      // experts of a group; lanes, where a group is a power of two of whole ones (else 0)
     int vec, vec_bias;      // rows (the bias) allow loads of 16 bytes, or of all of a lane's values where those are fewer
     float scale;
 };
 
-constexpr int kRouteWarps = 8;
+constexpr int kRouteWarps = 8;              // of a block that works on one token
+constexpr int kTokenWarps = 4;              // of a block whose warps take a token each (small blocks end and begin evenly)
 constexpr float kUlp = 5.9604645e-8f;       // 2^-24
 constexpr float kLargest = 3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -266,6 +314,10 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 __device__ __forceinline__ unsigned long long key_of(double v) {
     const unsigned long long u = (unsigned long long)__double_as_longlong(v + 0.0);
     return u >> 63 ? ~u : u | 0x8000000000000000ull;
+}
+
+__device__ __forceinline__ double value_of(unsigned long long key) {
+    return __longlong_as_double((long long)(key >> 63 ? key & 0x7FFFFFFFFFFFFFFFull : ~key));
 }
 
 // A logit as it is read: NaN as -infinity, +infinity as the largest finite value.
@@ -484,41 +536,45 @@ template <typename X>
 __device__ __noinline__ double exact_groups(const RouteArgs& a, const X* row, int e0, int R, float top, uint32_t cand, uint32_t which_groups) {
     const int lane = threadIdx.x & 31, size = a.E / a.groups;
     const double z = exact_sum<X, 1>(a, row, e0, R, top, nullptr);
-    double c[32], mine = 0.0;
-    for (int i = 0; i < R; ++i) c[i] = -INFINITY;
-    for (uint32_t todo = cand; todo; todo &= todo - 1) c[__ffs(todo) - 1] = exact_value(a, row, e0 + __ffs(todo) - 1, top, z);
+    unsigned long long c[32];
+    for (uint32_t todo = cand; todo; todo &= todo - 1) c[__ffs(todo) - 1] = key_of(exact_value(a, row, e0 + __ffs(todo) - 1, top, z));
     __syncwarp();
+    double mine = 0.0;
     for (uint32_t todo = which_groups; todo; todo &= todo - 1) {
         const int g = __ffs(todo) - 1;
-        double b0 = -INFINITY, b1 = -INFINITY;
-        for (int i = 0; i < R; ++i) {
-            if (e0 + i < g * size || e0 + i >= (g + 1) * size) continue;
-            b1 = fmax(b1, fmin(b0, c[i]));
-            b0 = fmax(b0, c[i]);
+        unsigned long long b0 = 0, b1 = 0;
+        for (uint32_t left = cand; left; left &= left - 1) {
+            const int i = __ffs(left) - 1, e = e0 + i;
+            if (e < g * size || e >= (g + 1) * size) continue;
+            b1 = max(b1, min(b0, c[i]));
+            b0 = max(b0, c[i]);
         }
-        for (int d = 16; d > 0; d >>= 1) {
-            const double o0 = __shfl_xor_sync(QMOE_FULL_MASK, b0, d), o1 = __shfl_xor_sync(QMOE_FULL_MASK, b1, d);
-            b1 = fmax(fmin(b0, o0), fmax(b1, o1));
-            b0 = fmax(b0, o0);
+        __syncwarp();
+        const unsigned long long best = warp_max64(b0);
+        double v = value_of(best);
+        if (a.best == 2) {
+            // the second best: the next of the lane that held the best, or another lane's best
+            const int w = __ffs(__ballot_sync(QMOE_FULL_MASK, b0 == best)) - 1;
+            v += value_of(warp_max64(lane == w ? b1 : b0));
         }
-        double v = a.best == 2 ? b0 + b1 : b0;
         if (v != v) v = -INFINITY;
         if (lane == g) mine = v;
     }
     return mine;
 }
 
-// The choice among the experts that each lane names, by NW warps: lane j of each gets the j-th expert.
+// The choice among the experts that each lane names, by NW warps: lane j of each gets the j-th expert.  (Without a bias: by
+// the logits themselves.)
 template <typename X, int NW, typename Bits>
 __device__ __noinline__ int exact_choice(const RouteArgs& a, const X* row, int e0, int R, float top, Bits cand, ResolveShared* sh) {
     constexpr int MOST = 8 * sizeof(Bits);
     const int lane = threadIdx.x & 31, warp = NW == 1 ? 0 : threadIdx.x >> 5;
-    const double z = exact_sum<X, NW>(a, row, e0, R, top, sh);
+    const double z = a.bias ? exact_sum<X, NW>(a, row, e0, R, top, sh) : 1.0;
     unsigned long long c[MOST];
     for (int i = 0; i < R; ++i) c[i] = 0ull;
     for (Bits todo = cand; todo; todo &= todo - 1) {
         const int i = sizeof(Bits) == 8 ? __ffsll((long long)todo) - 1 : __ffs((int)todo) - 1;
-        c[i] = key_of(exact_value(a, row, e0 + i, top, z));
+        c[i] = key_of(a.bias ? exact_value(a, row, e0 + i, top, z) : (double)logit(row, e0 + i));
     }
     __syncwarp();
     int got = 0;
@@ -562,10 +618,10 @@ __device__ __noinline__ int exact_choice(const RouteArgs& a, const X* row, int e
 template <typename X>
 __device__ __noinline__ int exact_order(const RouteArgs& a, const X* row, int n, float value, int at, bool near, float top, double z) {
     const int lane = threadIdx.x & 31;
-    const double c = near ? exact_value(a, row, at, top, z) : (double)value;
+    const unsigned long long c = key_of(near ? exact_value(a, row, at, top, z) : (double)value);
     int rank = 0, got = at;
     for (int j = 0; j < n; ++j) {
-        const double o = __shfl_sync(QMOE_FULL_MASK, c, j);
+        const unsigned long long o = __shfl_sync(QMOE_FULL_MASK, c, j);
         const int e = __shfl_sync(QMOE_FULL_MASK, at, j);
         rank += o > c || (o == c && e < at);
     }
@@ -610,16 +666,45 @@ __device__ __forceinline__ void write_route(const RouteArgs& a, int64_t t, int i
     }
 }
 
-// R experts a lane; NW warps a token (1: kRouteWarps tokens a block).
+// Which of the list that the lanes hold, largest first, are too near to tell apart (key mk of expert at, whose logit is l; one
+// entry more than are chosen, where there is one).
+struct Doubts {
+    bool any;        // some two neighbours
+    bool mine;       // this lane's entry is one of such a pair, or equal to one that is
+    float last;      // value of the last one chosen
+    float least;     // what is below that for certain
+};
+__device__ __forceinline__ Doubts doubts_of(const RouteArgs& a, uint32_t mk, int at, float l, float slack, int lane) {
+    const float v = value_of(mk);
+    const uint32_t nk = __shfl_down_sync(QMOE_FULL_MASK, mk, 1);
+    const int nat = __shfl_down_sync(QMOE_FULL_MASK, at, 1);
+    const float nl = __shfl_down_sync(QMOE_FULL_MASK, l, 1);
+    bool near = false, doubt = false;
+    if (lane < a.k && lane < 31 && mk && nk) {
+        const float nv = value_of(nk);
+        near = fabsf(v) < INFINITY && nv > -INFINITY ? v - nv <= 2.f * slack + kUlp * (fabsf(v) + fabsf(nv)) : v == nv;
+        if (near) doubt = !(l == nl && a.bias[at] == a.bias[nat]);
+    }
+    Doubts d{__any_sync(QMOE_FULL_MASK, doubt) != 0, false, 0.f, 0.f};
+    if (d.any || a.k == 32) {
+        const unsigned pairs = __ballot_sync(QMOE_FULL_MASK, near);
+        d.mine = ((pairs | pairs << 1) >> lane & 1) != 0;
+        d.last = value_of(__shfl_sync(QMOE_FULL_MASK, mk, a.k - 1));
+        d.least = d.last - (2.f * slack + 4.f * kUlp * fminf(fabsf(d.last), kLargest));
+    }
+    return d;
+}
+
+// R experts a lane; NW warps a token (1: kTokenWarps tokens a block).
 template <typename X, int R, int NW>
-__global__ void __launch_bounds__(kRouteWarps * 32, R <= 8 ? 4 : 2) route_kernel(RouteArgs a) {
+__global__ void __launch_bounds__((NW == 1 ? kTokenWarps : kRouteWarps) * 32, NW == 1 ? (R <= 8 ? 8 : 4) : 2) route_kernel(RouteArgs a) {
     __shared__ ResolveShared rs;
     __shared__ float2 part_s[kRouteWarps];
     __shared__ uint32_t key_s[NW > 1 ? kRouteWarps * 32 : 1];
     __shared__ int id_s[NW > 1 ? kRouteWarps * 32 : 1];
     __shared__ float2 bound_s;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = NW == 1 ? (int64_t)blockIdx.x * kRouteWarps + warp : blockIdx.x;
+    const int64_t t = NW == 1 ? (int64_t)blockIdx.x * kTokenWarps + warp : blockIdx.x;
     if (t >= a.T) return;
     const X* row = (const X*)a.logits + t * a.stride;
     const int e0 = (NW == 1 ? lane : (int)threadIdx.x) * R;
@@ -657,8 +742,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32, R <= 8 ? 4 : 2) route_kernel
     // ---- values, and the bound on a score's error: sigmoid_near's; or, with x = l - top, (2.5 |x| + 4) 2^-24 of itself from an
     // exponential (|x| e^x <= 0.37), the same of the sum (|x| weighed by the scores is at most ln E) and R / 4 + 17 additions, and a
     // quotient's 3
-    const float score_err = fmaf(a.sigmoid ? 6.f : (float)(R / 4 + 64) / z, kUlp, 1e-37f);
-    const float inv_z = 1.f / z;
+    const float inv_z = rcp(z);
+    const float score_err = fmaf(a.sigmoid ? 6.f : (float)(R / 4 + 64) * inv_z, kUlp, 1e-37f);
     auto score_near = [&](float l) { return a.sigmoid ? sigmoid_near(l) : ex2(kLog2e * (l - top)) * inv_z; };
     if (!by_logit) {
         float bias[R];
@@ -668,14 +753,19 @@ __global__ void __launch_bounds__(kRouteWarps * 32, R <= 8 ? 4 : 2) route_kernel
     }
     uint32_t key[R], list[kDepth<R>];
 #pragma unroll
-    for (int i = 0; i < R; ++i) key[i] = e0 + i < a.E ? key_of(c[i]) : 0u;
+    for (int i = 0; i < R; ++i) key[i] = key_of(c[i]);
+    if (e0 + R > a.E) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (e0 + i >= a.E) key[i] = 0u;
+    }
     const float slack = by_logit ? 0.f : score_err;
     best_keys<R>(key, list);
     if constexpr (NW == 1 && R <= 32) {
         if (a.groups > 1) {
             // ---- groups
-            const int size = a.E / a.groups, lanes = size / R;
-            const bool whole = size % R == 0 && (lanes & (lanes - 1)) == 0;      // a group is a power of two of whole lanes
+            const int size = a.group_size, lanes = a.group_lanes;
+            const bool whole = lanes > 0;
             Pair mine{0, 0};
             if (whole) {
                 Pair p{list[0], R > 1 ? list[R > 1 ? 1 : 0] : 0u};
@@ -730,7 +820,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, R <= 8 ? 4 : 2) route_kernel
                 }
             }
             if (whole) {
-                const bool off = e0 < a.E && !((kept >> (e0 / size)) & 1);
+                const bool off = !((kept >> (lane >> (31 - __clz(lanes)))) & 1);      // (lanes past the last group hold nothing)
 #pragma unroll
                 for (int i = 0; i < R; ++i) key[i] = off ? 0u : key[i];
 #pragma unroll
@@ -779,31 +869,19 @@ __global__ void __launch_bounds__(kRouteWarps * 32, R <= 8 ? 4 : 2) route_kernel
         if (!in_list) at = 0;
         if (in_list) l = logit(row, at);
         if (!by_logit) {
-            const float v = value_of(mk);
-            const uint32_t nk = __shfl_down_sync(QMOE_FULL_MASK, mk, 1);
-            const int nat = __shfl_down_sync(QMOE_FULL_MASK, at, 1);
-            const float nl = __shfl_down_sync(QMOE_FULL_MASK, l, 1);
-            bool near = false, doubt = false;
-            if (lane < a.k && lane < 31 && mk && nk) {
-                const float nv = value_of(nk);
-                near = fabsf(v) < INFINITY && nv > -INFINITY ? v - nv <= 2.f * slack + kUlp * (fabsf(v) + fabsf(nv)) : v == nv;
-                if (near) doubt = !(l == nl && a.bias[at] == a.bias[nat]);
-            }
-            const bool doubts = __any_sync(QMOE_FULL_MASK, doubt);
-            if (__builtin_expect(doubts || a.k == 32, 0)) {
-                last = value_of(__shfl_sync(QMOE_FULL_MASK, mk, a.k - 1));
-                const float least = last - (2.f * slack + 4.f * kUlp * fminf(fabsf(last), kLargest));
+            const Doubts d = doubts_of(a, mk, at, l, slack, lane);
+            if (__builtin_expect(d.any || a.k == 32, 0)) {
+                last = d.last;
                 // experts outside the list that may belong into it: a block decides all of its doubts together
                 again = NW > 1;
                 if (NW == 1) {
                     int may = 0;
 #pragma unroll
-                    for (int i = 0; i < R; ++i) may += key[i] && !(value_of(key[i]) < least);
-                    again = warp_sum_int(may) > __popc(__ballot_sync(QMOE_FULL_MASK, in_list && !(v < least)));
-                    if (!again && doubts) {
-                        const unsigned pairs = __ballot_sync(QMOE_FULL_MASK, near);      // (equal ones with them)
+                    for (int i = 0; i < R; ++i) may += key[i] && !(value_of(key[i]) < d.least);
+                    again = warp_sum_int(may) > __popc(__ballot_sync(QMOE_FULL_MASK, in_list && !(value_of(mk) < d.least)));
+                    if (!again && d.any) {
                         const double z64 = exact_sum<X, 1>(a, row, e0, R, top, nullptr);
-                        at = exact_order(a, row, __popc(__ballot_sync(QMOE_FULL_MASK, in_list)), v, at, ((pairs | pairs << 1) >> lane) & 1, top, z64);
+                        at = exact_order(a, row, __popc(__ballot_sync(QMOE_FULL_MASK, in_list)), value_of(mk), at, d.mine, top, z64);
                         if (in_list) l = logit(row, at);
                     }
                 }
@@ -829,20 +907,181 @@ __global__ void __launch_bounds__(kRouteWarps * 32, R <= 8 ? 4 : 2) route_kernel
     if (NW == 1 || warp == 0) write_route(a, t, at, l, top, z, lane);
 }
 
+// Many experts without groups: a warp a token, 32 R experts in loads that stand side by side.  The `rounds`-th largest of the
+// lanes' maxima bounds the values to look at from below; the few that reach it are put side by side in shared memory, and
+// the rounds go over those, by key and index.
+constexpr int kWideMost = 256;      // values put side by side; rows with more (many equal ones) take exact_choice
+
+template <typename X, int R>
+__global__ void __launch_bounds__(kTokenWarps * 32, R <= 16 ? 8 : R <= 32 ? 6 : 4) wide_route_kernel(RouteArgs a) {
+    constexpr int V = 16 / (int)sizeof(X);
+    __shared__ uint32_t key_s[kTokenWarps][kWideMost];
+    __shared__ int id_s[kTokenWarps][kWideMost];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * kTokenWarps + warp;
+    if (t >= a.T) return;
+    const X* row = (const X*)a.logits + t * a.stride;
+    // expert of value i
+    auto expert = [&](int i) { return a.vec ? (i / V) * (32 * V) + lane * V + i % V : i * 32 + lane; };
+    float c[R];
+    if (a.vec) {
+#pragma unroll
+        for (int i = 0; i < R; i += V) {
+            float v[V];
+            load_values<X, V>(row, i * 32 + lane * V, a.E, 1, -INFINITY, v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) c[i + j] = clean(v[j]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i) c[i] = i * 32 + lane < a.E ? logit(row, i * 32 + lane) : -INFINITY;
+    }
+    const bool by_logit = !a.bias;
+    float top = 0.f, z = 1.f, inv_z = 1.f, slack = 0.f;
+    if (!a.sigmoid && !(by_logit && a.renorm)) {
+        top = c[0];
+#pragma unroll
+        for (int i = 1; i < R; ++i) top = fmaxf(top, c[i]);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(QMOE_FULL_MASK, top, d));
+        if (!(top > -INFINITY)) top = 0.f;       // nothing in the row: scores 0
+        float part[4] = {};
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const float e = ex2(kLog2e * (c[i] - top));
+            part[i & 3] += e;
+            if (!by_logit) c[i] = e;
+        }
+        z = warp_sum((part[0] + part[1]) + (part[2] + part[3]));
+        if (!(z > 0.f)) z = 1.f;
+        inv_z = rcp(z);
+    }
+    if (!by_logit) {
+        slack = fmaf(a.sigmoid ? 6.f : (float)(R / 4 + 64) * inv_z, kUlp, 1e-37f);      // (as in route_kernel)
+#pragma unroll
+        for (int i = 0; i < R; i += V) {
+            float bias[V];
+            if (a.vec && a.vec_bias) {
+                load_values<float, V>(a.bias, i * 32 + lane * V, a.E, 1, 0.f, bias);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) bias[j] = expert(i + j) < a.E ? a.bias[expert(i + j)] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float s = a.sigmoid ? sigmoid_near(c[i + j]) : c[i + j] * inv_z;
+                c[i + j] = expert(i + j) < a.E ? fmaxf(s + bias[j], -INFINITY) : -INFINITY;
+            }
+        }
+    }
+    // ---- the lanes' largest values, and the `rounds`-th of them
+    constexpr int CHUNK = R < 8 ? R : 8;
+    float chunk[R / CHUNK], mine = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < R / CHUNK; ++i) {
+        chunk[i] = c[i * CHUNK];
+#pragma unroll
+        for (int j = 1; j < CHUNK; ++j) chunk[i] = fmaxf(chunk[i], c[i * CHUNK + j]);
+        mine = fmaxf(mine, chunk[i]);
+    }
+    const int rounds = min(a.k + (by_logit ? 0 : 1), 32);
+    uint32_t head = key_of(mine), bound = 0;
+    for (int j = 0; j < rounds; ++j) {
+        bound = __reduce_max_sync(QMOE_FULL_MASK, head);
+        const int w = __ffs(__ballot_sync(QMOE_FULL_MASK, head == bound)) - 1;
+        if (lane == w) head = 0;
+    }
+    const float from = value_of(bound);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < R / CHUNK; ++i) {
+        if (!__any_sync(QMOE_FULL_MASK, chunk[i] >= from)) continue;
+#pragma unroll
+        for (int j = 0; j < CHUNK; ++j) {
+            const int e = expert(i * CHUNK + j);
+            const bool in = c[i * CHUNK + j] >= from && e < a.E;
+            const unsigned who = __ballot_sync(QMOE_FULL_MASK, in);
+            if (who == 0) continue;
+            const int at = n + __popc(who & ((1u << lane) - 1));
+            if (in && at < kWideMost) key_s[warp][at] = key_of(c[i * CHUNK + j]), id_s[warp][at] = e;
+            n += __popc(who);
+        }
+    }
+    __syncwarp();
+    bool again = n > kWideMost;
+    uint32_t mk = 0;
+    int at = 0;
+    float l = -INFINITY;
+    if (!again) {
+        constexpr int MOST = kWideMost / 32;
+        uint32_t key[MOST];
+        int id[MOST];
+        const int mine_n = (n + 31) / 32;
+#pragma unroll
+        for (int i = 0; i < MOST; ++i) {
+            key[i] = 0, id[i] = 0;
+            if (i * 32 + lane < n) key[i] = key_s[warp][i * 32 + lane], id[i] = id_s[warp][i * 32 + lane];
+        }
+        for (int j = 0; j < rounds; ++j) {
+            uint32_t best = key[0];
+            int e = id[0];
+            if (mine_n > 1) {
+#pragma unroll
+                for (int i = 1; i < MOST; ++i)
+                    if (key[i] > best || (key[i] == best && id[i] < e)) best = key[i], e = id[i];
+            }
+            const uint32_t m = __reduce_max_sync(QMOE_FULL_MASK, best);
+            const int first = (int)__reduce_min_sync(QMOE_FULL_MASK, best == m ? (unsigned)e : 0xFFFFFFFFu);
+            if (lane == j) mk = m, at = first;
+#pragma unroll
+            for (int i = 0; i < MOST; ++i) {
+                if (i > 0 && mine_n == 1) break;
+                if (key[i] == m && id[i] == first) key[i] = 0;
+            }
+        }
+        const bool in_list = lane < rounds && mk;
+        if (!in_list) at = 0;
+        if (in_list) l = logit(row, at);
+        if (!by_logit) {
+            const Doubts d = doubts_of(a, mk, at, l, slack, lane);
+            if (__builtin_expect(d.any || a.k == 32, 0)) {
+                int may = 0;
+#pragma unroll
+                for (int i = 0; i < R; ++i) may += expert(i) < a.E && !(c[i] < d.least);
+                again = warp_sum_int(may) > __popc(__ballot_sync(QMOE_FULL_MASK, in_list && !(value_of(mk) < d.least)));
+                if (!again && d.any) {
+                    const double z64 = exact_sum<X, 1>(a, row, lane * R, R, top, nullptr);
+                    at = exact_order(a, row, __popc(__ballot_sync(QMOE_FULL_MASK, in_list)), value_of(mk), at, d.mine, top, z64);
+                    if (in_list) l = logit(row, at);
+                }
+            }
+        }
+    }
+    if (__builtin_expect(again, 0)) {
+        using Bits = std::conditional_t<(R > 32), unsigned long long, uint32_t>;
+        const int have = min(max(a.E - lane * R, 0), R);      // all of the row, R neighbouring experts a lane
+        const Bits cand = have == 0 ? 0 : ~(Bits)0 >> (8 * sizeof(Bits) - have);
+        at = exact_choice<X, 1, Bits>(a, row, lane * R, R, top, cand, nullptr);
+        if (lane < a.k) l = logit(row, at);
+    }
+    write_route(a, t, at, l, top, z, lane);
+}
+
 template <typename X>
 int launch_route(const RouteArgs& a, cudaStream_t st) {
-    const unsigned per_warp = (unsigned)((a.T + kRouteWarps - 1) / kRouteWarps);
-    constexpr int threads = kRouteWarps * 32;
+    const unsigned per_warp = (unsigned)((a.T + kTokenWarps - 1) / kTokenWarps);
+    constexpr int threads = kTokenWarps * 32;
     if (a.E <= 32) route_kernel<X, 1, 1><<<per_warp, threads, 0, st>>>(a);
     else if (a.E <= 64) route_kernel<X, 2, 1><<<per_warp, threads, 0, st>>>(a);
     else if (a.E <= 128) route_kernel<X, 4, 1><<<per_warp, threads, 0, st>>>(a);
     else if (a.E <= 256) route_kernel<X, 8, 1><<<per_warp, threads, 0, st>>>(a);
-    else if (a.E <= 512) route_kernel<X, 16, 1><<<per_warp, threads, 0, st>>>(a);
-    else if (a.E <= 1024) route_kernel<X, 32, 1><<<per_warp, threads, 0, st>>>(a);
-    else if (a.E <= 2048 && a.T >= 8 * qmoe::sm_count()) route_kernel<X, 64, 1><<<per_warp, threads, 0, st>>>(a);
-    else if (a.E <= 2048) route_kernel<X, 8, kRouteWarps><<<(unsigned)a.T, threads, 0, st>>>(a);
-    else if (a.E <= 4096) route_kernel<X, 16, kRouteWarps><<<(unsigned)a.T, threads, 0, st>>>(a);
-    else route_kernel<X, 32, kRouteWarps><<<(unsigned)a.T, threads, 0, st>>>(a);
+    else if (a.groups > 1 && a.E <= 512) route_kernel<X, 16, 1><<<per_warp, threads, 0, st>>>(a);
+    else if (a.groups > 1) route_kernel<X, 32, 1><<<per_warp, threads, 0, st>>>(a);
+    else if (a.E <= 512) wide_route_kernel<X, 16><<<per_warp, threads, 0, st>>>(a);
+    else if (a.E <= 1024) wide_route_kernel<X, 32><<<per_warp, threads, 0, st>>>(a);
+    else if (a.E <= 2048) wide_route_kernel<X, 64><<<per_warp, threads, 0, st>>>(a);
+    else if (a.E <= 4096) route_kernel<X, 16, kRouteWarps><<<(unsigned)a.T, kRouteWarps * 32, 0, st>>>(a);
+    else route_kernel<X, 32, kRouteWarps><<<(unsigned)a.T, kRouteWarps * 32, 0, st>>>(a);
     return qmoe::launch_check("qmoe_route_scored");
 }
 
@@ -901,11 +1140,16 @@ extern "C" int qmoe_route_scored(const void* logits, int logits_are_f32, int64_t
     if (T > 1 && row_stride < E) return qmoe::fail(QMOE_EINVAL, "qmoe_route_scored: the row stride is smaller than a row");
     if (!aligned(logits, logits_are_f32 ? 4 : 2) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(gates, 4))
         return qmoe::fail(QMOE_EINVAL, "qmoe_route_scored: pointer not aligned to its type");
-    // experts a lane holds (launch_route), and what its loads have to be multiples of
-    const int R = E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : E <= 256 || (E > 1024 && E <= 2048) ? 8 : 16, size = logits_are_f32 ? 4 : 2;
+    // neighbouring experts of a lane (launch_route; 16 stands for more), and what its loads have to be multiples of
+    const int R = E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : E <= 256 ? 8 : 16, size = logits_are_f32 ? 4 : 2;
     const int wide = std::min(16, R * size), wide_bias = std::min(16, R * 4);
-    RouteArgs a{logits, bias, ids, gates, row_stride, T, E, k, score == QMOE_SCORE_SIGMOID, n_groups, top_groups, group_best,
-                renormalise ? 1 : 0, aligned(logits, wide) && (T == 1 || row_stride * size % wide == 0) && E * size % wide == 0,
-                aligned(bias, wide_bias) && E * 4 % wide_bias == 0, scale};
+    const int per_lane = E > 512 && E <= 1024 ? 32 : R, group = E / n_groups, lanes = group / per_lane;
+    RouteArgs a{};
+    a.logits = logits, a.bias = bias, a.ids = ids, a.gates = gates, a.stride = row_stride;
+    a.T = T, a.E = E, a.k = k, a.sigmoid = score == QMOE_SCORE_SIGMOID, a.groups = n_groups, a.top_groups = top_groups;
+    a.best = group_best, a.renorm = renormalise ? 1 : 0, a.scale = scale;
+    a.group_size = group, a.group_lanes = group % per_lane == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    a.vec = aligned(logits, wide) && (T == 1 || row_stride * size % wide == 0) && E * size % wide == 0;
+    a.vec_bias = aligned(bias, wide_bias) && E * 4 % wide_bias == 0;
     return logits_are_f32 ? launch_route<float>(a, (cudaStream_t)stream) : launch_route<uint16_t>(a, (cudaStream_t)stream);
 }
