@@ -51,14 +51,14 @@ __device__ __forceinline__ int first_seen(const AttnArgs& a, int pos) { return a
 
 // Whether query token t can be run: its request, its position, and the blocks that it sees.
 __device__ __forceinline__ bool chosen_token(const AttnArgs& a, int t, int* b, int* pos, int* seen, bool report) {
-    *b = kv4::request_of(a.q_start, a.B, t);
+    int end, n;
+    *b = kv4::request_of(a.q_start, a.kv_len, a.B, t, &end, &n);
     if (*b < 0) return false;
-    const int n = a.kv_len[*b];
     if (n < 0 || n > kMaxKv) {
         if (report) attn_set_error(QMOE_EINVAL);
         return false;
     }
-    const long long p = (long long)n - ((long long)a.q_start[*b + 1] - t);      // (below 0 where q_start runs past kv_len)
+    const long long p = (long long)n - ((long long)end - t);      // (below 0 where q_start runs past kv_len)
     *pos = p < 0 ? -1 : (int)p;
     *seen = p < 0 ? 0 : (int)(p >> a.cache.page_shift) + 1;
     return true;

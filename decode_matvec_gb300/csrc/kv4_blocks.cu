@@ -159,14 +159,14 @@ struct SelectArgs {
 
 // Blocks that query token t sees (-1: the token belongs to no request), and its request.
 __device__ __forceinline__ int blocks_seen(const SelectArgs& a, int t, int* b, bool report) {
-    *b = kv4::request_of(a.q_start, a.B, t);
+    int end, kv;
+    *b = kv4::request_of(a.q_start, a.kv_len, a.B, t, &end, &kv);
     if (*b < 0) return -1;
-    const int kv = a.kv_len[*b];
     if (kv < 0 || kv > a.max_kv) {
         if (report) blocks_set_error(kv < 0 ? QMOE_EINVAL : QMOE_ECAPACITY);
         return 0;
     }
-    const int64_t pos = (int64_t)kv - ((int64_t)a.q_start[*b + 1] - t);
+    const int64_t pos = (int64_t)kv - ((int64_t)end - t);
     return pos < 0 ? 0 : (int)(pos >> a.page_shift) + 1;
 }
 
@@ -258,20 +258,22 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int 
     constexpr int L = kRecordLanes<D>, GROUPS = kScoreThreads / L;
     kv4::depend_launch();
     const int t = blockIdx.x / chunks, c = blockIdx.x - t * chunks;
-    int b;
-    const int seen = blocks_seen(a, t, &b, c == 0 && threadIdx.x == 0);
     const int grp = threadIdx.x / L, gl = threadIdx.x & (L - 1);
     const int parts = max(1, GROUPS / a.n_kv);
+    const int j = (c * parts + grp / a.n_kv) * L + gl;                          // the block that this lane looks up
+    // (in a decode step token t is request t: its table entry is loaded beside the lengths that say so)
+    const int likely = t < a.B && j < a.max_blocks ? a.table[(int64_t)t * a.max_blocks + j] : -1;
+    int b;
+    const int seen = blocks_seen(a, t, &b, c == 0 && threadIdx.x == 0);
     // few blocks are all taken
     if (seen <= a.top || c * parts * L >= seen || grp >= a.n_kv * parts) {      // (whole groups of lanes leave)
         kv4::depend_wait();
         return;
     }
-    const int j = (c * parts + grp / a.n_kv) * L + gl;                          // the block that this lane looks up
     const unsigned mask = (L == 16 ? 0xFFFFu : 0xFFu) << (threadIdx.x & 31 & ~(L - 1));
     int page = -1;
     if (j < seen) {
-        page = j < a.max_blocks ? a.table[(int64_t)b * a.max_blocks + j] : -1;
+        page = b == t ? likely : j < a.max_blocks ? a.table[(int64_t)b * a.max_blocks + j] : -1;
         if (page < 0 || page >= a.n_pages) {
             if (grp % a.n_kv == 0) blocks_set_error(QMOE_EINVAL);
             page = -1;
@@ -312,176 +314,140 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int 
 
 // ---------------------------------------------------------------- the best blocks
 //
-// A thread block writes the list of one (token, kv head).  Its scores are kept in registers, warp w those of the w-th equal run.
-// A histogram over the scores' range finds the bin that the last taken score falls into, and the few scores of that bin are
-// ranked against each other (a bin with too many, and rows longer than the registers hold, are settled by bisection); then
-// every warp writes the blocks of its run that lie above that score, and the first ones at it.
-constexpr int kBins = 1024, kRankMost = 256;
+// The list of one (token, kv head) is made by a warp (up to 1024 blocks to choose from) or a thread block.  Scores are kept in
+// registers as integer keys, warp w those of the w-th equal run.  The key of the last one taken is found between the
+// smallest and the largest by trying three keys at a time (a count each, all three in one word), until as many are above
+// one of them as are wanted or nothing is left between; then every warp writes the blocks of its run that are above it, and the
+// first ones at it.
+constexpr int kMostBlocks = 1 << 20;      // of a request
+constexpr int kPickThreads = 128;        // of a block whose warps make a list each
 
 // fp32 -> integer of the same order (-0 as 0); no key is 0.
 __device__ __forceinline__ uint32_t score_key(float v) {
     const uint32_t u = __float_as_uint(v + 0.f);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 
-template <int THREADS>
-struct PickShared {
-    int count[THREADS / 32], above[THREADS / 32], equal[THREADS / 32];
-    float lo[THREADS / 32], hi[THREADS / 32];
-    int bins[kBins];
-    uint32_t rank_key[kRankMost];
-    int n_rank, bin, need;
-    uint32_t key;
-};
-
-template <int THREADS>
-__device__ __forceinline__ int block_sum(int v, int* buf) {
-    v = warp_sum_int(v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int s = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) s += buf[w];
-    return s;
-}
-
-// R scores a thread in registers; R = 0: any number, read again each time.
-template <int THREADS, int R>
-__global__ void __launch_bounds__(THREADS) pick_kernel(SelectArgs a) {
-    __shared__ PickShared<THREADS> sh;
-    constexpr int WARPS = THREADS / 32;
-    const int t = blockIdx.x / a.n_kv, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int b;
-    const int seen = blocks_seen(a, t, &b, a.max_seen <= a.top && tid == 0 && blockIdx.x == t * a.n_kv);
+// WARPS a list (1: a block makes several), R scores a lane in registers; R = 0: any number, read again each time.
+template <int WARPS, int R>
+__global__ void __launch_bounds__(WARPS == 1 ? kPickThreads : WARPS * 32) pick_kernel(SelectArgs a) {
+    __shared__ uint2 part_s[2][WARPS];
+    __shared__ unsigned long long count_s[2][WARPS];
+    const int lane = threadIdx.x & 31, warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
+    const int64_t list = WARPS == 1 ? (int64_t)blockIdx.x * (kPickThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
+    const int tid = warp * 32 + lane;
+    constexpr int THREADS = WARPS * 32;
+    const int t = (int)(list / a.n_kv);
+    int b, seen = -1;
+    if (t < a.n) seen = blocks_seen(a, t, &b, a.max_seen <= a.top && tid == 0 && list == (int64_t)t * a.n_kv);
     kv4::depend_wait();        // (before any return: what follows the call waits for this kernel alone)
     if (seen < 0) return;
-    int32_t* sel = a.sel + (int64_t)blockIdx.x * a.top;
+    int32_t* sel = a.sel + list * a.top;
     if (seen <= a.top) {
         for (int i = tid; i < a.top; i += THREADS) sel[i] = i < seen ? i : -1;
         return;
     }
-    const float* scores = a.scores + (int64_t)blockIdx.x * a.max_seen;
+    const float* scores = a.scores + list * a.max_seen;
     const int lo = a.first, hi = seen - a.last, want = a.top - a.first - a.last;
     for (int i = tid; i < a.first; i += THREADS) sel[i] = i;
     for (int i = tid; i < a.last; i += THREADS) sel[a.top - a.last + i] = hi + i;
     if (want == 0) return;
     const int per = R ? R * 32 : ((hi - lo + WARPS - 1) / WARPS + 31) & ~31;
-    const int w0 = min(lo + warp * per, hi), w1 = min(w0 + per, hi);
-    uint32_t cut = 0;          // key of the last score taken
-    bool found = false;
+    const int w0 = min(lo + warp * per, hi), w1 = min(w0 + per, hi), steps = R ? R : (w1 - w0 + 31) / 32;
     uint32_t key[R ? R : 1];
     if constexpr (R > 0) {
-        float v[R], least = INFINITY, most = -INFINITY;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int j = w0 + 32 * i + lane;
-            v[i] = j < w1 ? scores[j] : -INFINITY;
-            key[i] = j < w1 ? score_key(v[i]) : 0u;
-            if (v[i] > -INFINITY) least = fminf(least, v[i]);
-            most = fmaxf(most, v[i]);
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) {
-            least = fminf(least, __shfl_xor_sync(QMOE_FULL_MASK, least, d));
-            most = fmaxf(most, __shfl_xor_sync(QMOE_FULL_MASK, most, d));
-        }
-        if (lane == 0) sh.lo[warp] = least, sh.hi[warp] = most;
-        for (int i = tid; i < kBins; i += THREADS) sh.bins[i] = 0;
-        if (tid == 0) sh.n_rank = 0;
-        __syncthreads();
-        least = sh.lo[lane % WARPS], most = sh.hi[lane % WARPS];
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) {
-            least = fminf(least, __shfl_xor_sync(QMOE_FULL_MASK, least, d));
-            most = fmaxf(most, __shfl_xor_sync(QMOE_FULL_MASK, most, d));
-        }
-        // bins from the largest score down; -infinity stands in the last one.  The map does not rise with the score, whatever
-        // it rounds, so that bins are in the scores' order
-        const float per_bin = (float)(kBins - 2) / (most - least);
-        if (most > least && per_bin < INFINITY) {
-            auto bin_of = [&](float x) { return x > -INFINITY ? min((int)((most - x) * per_bin), kBins - 2) : kBins - 1; };
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-                if (key[i]) atomicAdd(&sh.bins[bin_of(v[i])], 1);
-            __syncthreads();
-            // the bin of the want-th score: a scan by the first warp, 32 bins a lane
-            if (warp == 0) {
-                int mine = 0;
-#pragma unroll
-                for (int i = 0; i < kBins / 32; ++i) mine += sh.bins[lane * (kBins / 32) + ((i + lane) & (kBins / 32 - 1))];      // (skewed: no bank conflicts)
-                const int sum = warp_incl_scan(mine, lane);
-                const int row = __ffs(__ballot_sync(QMOE_FULL_MASK, sum >= want)) - 1;        // the 32 bins that hold it
-                const int before = __shfl_sync(QMOE_FULL_MASK, sum - mine, row);
-                const int one = sh.bins[row * (kBins / 32) + lane], upto = before + warp_incl_scan(one, lane);
-                const int at = __ffs(__ballot_sync(QMOE_FULL_MASK, upto >= want)) - 1;
-                if (lane == at) sh.bin = row * (kBins / 32) + at, sh.need = want - (upto - one);
-            }
-            __syncthreads();
-            const int bin = sh.bin, need = sh.need, many = sh.bins[bin];
-            if (many <= kRankMost) {
-#pragma unroll
-                for (int i = 0; i < R; ++i)
-                    if (key[i] && bin_of(v[i]) == bin) sh.rank_key[atomicAdd(&sh.n_rank, 1)] = key[i];
-                __syncthreads();
-                for (int i = tid; i < many; i += THREADS) {
-                    const uint32_t mine = sh.rank_key[i];
-                    int over = 0, same = 0;
-                    for (int k = 0; k < many; ++k) over += sh.rank_key[k] > mine, same += sh.rank_key[k] == mine;
-                    if (over < need && over + same >= need) sh.key = mine;      // (equal ones write the same)
-                }
-                __syncthreads();
-                cut = sh.key;
-                found = true;
-            }
+            key[i] = j < w1 ? score_key(scores[j]) : 0u;
         }
     }
-    if (!found) {
-        // largest key with at least `want` keys >= it
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t probe = cut | 1u << bit;
-            int c = 0;
-            if constexpr (R > 0) {
-#pragma unroll
-                for (int i = 0; i < R; ++i) c += key[i] >= probe;
-            } else {
-                for (int j = w0 + lane; j < w1; j += 32) c += score_key(scores[j]) >= probe;
-            }
-            if (block_sum<THREADS>(c, sh.count) >= want) cut = probe;
+    auto key_at = [&](int i) {
+        if constexpr (R > 0) {
+            return key[i];
+        } else {
+            const int j = w0 + 32 * i + lane;
+            return j < w1 ? score_key(scores[j]) : 0u;
         }
-    }
-    auto key_at = [&](int i, int j) {
-        if constexpr (R > 0) return key[i];
-        else return j < w1 ? score_key(scores[j]) : 0u;
     };
-    const int steps = R ? R : (w1 - w0 + 31) / 32;
+    // ---- all keys are in [least, end)
+    uint32_t least = 0xFFFFFFFFu, end = 0;
+#pragma unroll
+    for (int i = 0; i < (R ? R : steps); ++i) {
+        const uint32_t k = key_at(i);
+        end = max(end, k);
+        least = min(least, k ? k : 0xFFFFFFFFu);
+    }
+    least = __reduce_min_sync(QMOE_FULL_MASK, least), end = __reduce_max_sync(QMOE_FULL_MASK, end);
+    if (WARPS > 1) {
+        if (lane == 0) part_s[0][warp] = make_uint2(least, end);
+        __syncthreads();
+        const uint2 p = lane < WARPS ? part_s[0][lane] : make_uint2(0xFFFFFFFFu, 0u);
+        least = __reduce_min_sync(QMOE_FULL_MASK, p.x), end = __reduce_max_sync(QMOE_FULL_MASK, p.y);
+    }
+    ++end;
+    // ---- at least `want` keys are >= least, fewer are >= end
+    bool exact = false;         // as many as are wanted are >= least: none of the others
+    for (int turn = 0; end - least > 1 && !exact; turn ^= 1) {
+        const uint32_t span = end - least, q = span >= 4 ? span >> 2 : 1;
+        const uint32_t p1 = least + q, p2 = min(p1 + q, end), p3 = min(p2 + q, end);
+        int n1 = 0, n2 = 0, n3 = 0;
+#pragma unroll
+        for (int i = 0; i < (R ? R : steps); ++i) {
+            const uint32_t k = key_at(i);
+            n1 += k >= p1, n2 += k >= p2, n3 += k >= p3;
+        }
+        if constexpr (R > 0) {
+            // (a warp's counts are at most 512: ten bits)
+            const uint32_t n = __reduce_add_sync(QMOE_FULL_MASK, (uint32_t)(n1 | n2 << 10 | n3 << 20));
+            n1 = (int)(n & 1023u), n2 = (int)(n >> 10 & 1023u), n3 = (int)(n >> 20);
+        } else {
+            n1 = warp_sum_int(n1), n2 = warp_sum_int(n2), n3 = warp_sum_int(n3);
+        }
+        if (WARPS > 1) {
+            // 21 bits each (a list chooses from at most 2^21 - 1 blocks, kMostBlocks)
+            if (lane == 0) count_s[turn][warp] = (unsigned long long)n1 | (unsigned long long)n2 << 21 | (unsigned long long)n3 << 42;
+            __syncthreads();
+            const unsigned long long v = lane < WARPS ? count_s[turn][lane] : 0ull;
+            n1 = (int)__reduce_add_sync(QMOE_FULL_MASK, (uint32_t)(v & 0x1FFFFFu));
+            n2 = (int)__reduce_add_sync(QMOE_FULL_MASK, (uint32_t)(v >> 21 & 0x1FFFFFu));
+            n3 = (int)__reduce_add_sync(QMOE_FULL_MASK, (uint32_t)(v >> 42));
+        }
+        // (p3 >= p2 >= p1, counts the other way; a p at end counts none)
+        if (n3 >= want) least = p3, exact = n3 == want;
+        else if (n2 >= want) least = p2, exact = n2 == want, end = p3;
+        else if (n1 >= want) least = p1, exact = n1 == want, end = p2;
+        else end = p1;
+    }
+    // ---- the blocks above `cut`, and `room` of those at it
+    const uint32_t cut = least;
     int above = 0, equal = 0;
 #pragma unroll
     for (int i = 0; i < (R ? R : steps); ++i) {
-        const uint32_t k = key_at(i, w0 + 32 * i + lane);
+        const uint32_t k = key_at(i);
         above += k > cut, equal += k == cut;
     }
     above = (int)__reduce_add_sync(QMOE_FULL_MASK, (unsigned)above), equal = (int)__reduce_add_sync(QMOE_FULL_MASK, (unsigned)equal);
-    if (lane == 0) sh.above[warp] = above, sh.equal[warp] = equal;
-    __syncthreads();
-    int all_above = 0, above_before = 0, equal_before = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        const int x = sh.above[w], y = sh.equal[w];
-        all_above += x;
-        if (w < warp) above_before += x, equal_before += y;
+    int all_above = above, above_before = 0, equal_before = 0;
+    if (WARPS > 1) {
+        __syncthreads();
+        if (lane == 0) part_s[1][warp] = make_uint2((unsigned)above, (unsigned)equal);
+        __syncthreads();
+        const uint2 p = lane < WARPS ? part_s[1][lane] : make_uint2(0u, 0u);
+        all_above = (int)__reduce_add_sync(QMOE_FULL_MASK, p.x);
+        above_before = (int)__reduce_add_sync(QMOE_FULL_MASK, lane < warp ? p.x : 0u);
+        equal_before = (int)__reduce_add_sync(QMOE_FULL_MASK, lane < warp ? p.y : 0u);
     }
-    const int room = want - all_above;          // of the equal ones
+    const int room = want - all_above;
     const unsigned below = (1u << lane) - 1;
 #pragma unroll
     for (int i = 0; i < (R ? R : steps); ++i) {
-        const int j = w0 + 32 * i + lane;
-        const uint32_t k = key_at(i, j);
+        const uint32_t k = key_at(i);
         const unsigned hit = __ballot_sync(QMOE_FULL_MASK, k >= cut);
         if (hit == 0) continue;
         const unsigned over = __ballot_sync(QMOE_FULL_MASK, k > cut), same = hit & ~over;
         const int n_same = equal_before + __popc(same & below);
-        if (k > cut || (k == cut && n_same < room)) sel[a.first + above_before + __popc(over & below) + min(n_same, room)] = j;
+        if (k > cut || (k == cut && n_same < room)) sel[a.first + above_before + __popc(over & below) + min(n_same, room)] = w0 + 32 * i + lane;
         above_before += __popc(over), equal_before += __popc(same);
     }
 }
@@ -557,6 +523,8 @@ extern "C" int kv4_select_blocks(const kv4_bounds* bounds, const void* q, int n_
     if (B < 0 || n_q_tokens < 0 || max_kv < 0 || max_kv > 0x7FFFFFFF - 127 || max_blocks < 0 || n_q_heads < n_kv || n_q_heads % n_kv)
         return qmoe::fail(QMOE_EINVAL, "kv4_select_blocks: bad sizes (n_q_heads must be a multiple of n_kv_heads)");
     if (n_q_heads / n_kv > 128) return qmoe::fail(QMOE_EUNSUPPORTED, "kv4_select_blocks: more than 128 query heads per kv head");
+    if ((int64_t)max_kv > (int64_t)kMostBlocks * bounds->page_size)
+        return qmoe::fail(QMOE_EUNSUPPORTED, "kv4_select_blocks: max_kv above 2^20 pages");
     if (top < 1 || top > 65536 || first < 0 || last < 0 || (int64_t)first + last > top)
         return qmoe::fail(QMOE_EINVAL, "kv4_select_blocks: need 1 <= top <= 65536 and first + last <= top");
     if (B == 0 || n_q_tokens == 0) return QMOE_OK;
@@ -578,22 +546,23 @@ extern "C" int kv4_select_blocks(const kv4_bounds* bounds, const void* q, int n_
     const int64_t chunks = (row + chunk - 1) / chunk, blocks = chunks * n_q_tokens;
     if (blocks > 0x7FFFFFFFLL || (int64_t)n_q_tokens * n_kv > 0x7FFFFFFFLL)
         return qmoe::fail(QMOE_EINVAL, "kv4_select_blocks: too many query tokens in one call");
-    const unsigned lists = (unsigned)(n_q_tokens * n_kv);
+    const unsigned lists = (unsigned)(n_q_tokens * n_kv), by_warps = (lists + kPickThreads / 32 - 1) / (kPickThreads / 32);
+    const char* who = "kv4_select_blocks";
     if (row <= top) {
-        pick_kernel<128, 0><<<lists, 128, 0, st>>>(a);      // every block that is there
-        return qmoe::launch_check("kv4_select_blocks");
+        pick_kernel<1, 0><<<by_warps, kPickThreads, 0, st>>>(a);      // every block that is there
+        return qmoe::launch_check(who);
     }
     if (!workspace || !kv4::aligned16(workspace)) return qmoe::fail(QMOE_EINVAL, "kv4_select_blocks: workspace NULL or not 16-byte aligned");
-    const char* who = "kv4_select_blocks";
     const unsigned whole_blocks = (lists + kWholeThreads / 32 - 1) / (kWholeThreads / 32);
     const bool d128 = bounds->head_dim == 128;
     if (d128) whole_kernel<128><<<whole_blocks, kWholeThreads, 0, st>>>(a);
     else whole_kernel<64><<<whole_blocks, kWholeThreads, 0, st>>>(a);
     if ((rc = qmoe::launch_check(who))) return rc;
     if ((rc = kv4::launch_dependent(d128 ? score_kernel<128> : score_kernel<64>, dim3((unsigned)blocks), kScoreThreads, 0, st, who, a, (int)chunks))) return rc;
-    if (row <= 512) return kv4::launch_dependent(pick_kernel<128, 4>, dim3(lists), 128, 0, st, who, a);
-    if (row <= 2048) return kv4::launch_dependent(pick_kernel<256, 8>, dim3(lists), 256, 0, st, who, a);
-    if (row <= 8192) return kv4::launch_dependent(pick_kernel<512, 16>, dim3(lists), 512, 0, st, who, a);
-    if (row <= 16384) return kv4::launch_dependent(pick_kernel<1024, 16>, dim3(lists), 1024, 0, st, who, a);
-    return kv4::launch_dependent(pick_kernel<1024, 0>, dim3(lists), 1024, 0, st, who, a);
+    const int64_t most = ((int64_t)max_kv + bounds->page_size - 1) / bounds->page_size - first - last;      // blocks a list chooses from
+    if (most <= 128) return kv4::launch_dependent(pick_kernel<1, 4>, dim3(by_warps), kPickThreads, 0, st, who, a);
+    if (most <= 512) return kv4::launch_dependent(pick_kernel<1, 16>, dim3(by_warps), kPickThreads, 0, st, who, a);
+    if (most <= 2048) return kv4::launch_dependent(pick_kernel<8, 8>, dim3(lists), 256, 0, st, who, a);
+    if (most <= 8192) return kv4::launch_dependent(pick_kernel<32, 8>, dim3(lists), 1024, 0, st, who, a);
+    return kv4::launch_dependent(pick_kernel<32, 0>, dim3(lists), 1024, 0, st, who, a);
 }

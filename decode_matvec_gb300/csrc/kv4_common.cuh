@@ -25,16 +25,24 @@ __device__ __forceinline__ unsigned char* head_ptr(const CacheView& c, int page,
     return c.pages + (uint64_t)page * c.page_bytes + (uint64_t)h * c.head_bytes;
 }
 
-// The request that query token t belongs to (q_start[b] <= t < q_start[b + 1]), or -1.  In a decode step it is t itself.
-__device__ __forceinline__ int request_of(const int32_t* q_start, int B, int t) {
-    if (t < B && q_start[t] == t && q_start[t + 1] == t + 1) return t;
+// The request that query token t belongs to (q_start[b] <= t < q_start[b + 1]), or -1; with q_start[b + 1] and kv_len[b].  In a
+// decode step it is t itself: that is looked at first, in one go.
+__device__ __forceinline__ int request_of(const int32_t* q_start, const int32_t* kv_len, int B, int t, int* end, int* kv) {
+    if (t < B) {
+        const int s = q_start[t];
+        *end = q_start[t + 1], *kv = kv_len[t];
+        if (s == t && *end == t + 1) return t;
+    }
     int lo = 0, hi = B;         // the last b with q_start[b] <= t is in [lo - 1, hi - 1]
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (q_start[mid] <= t) lo = mid + 1;
         else hi = mid;
     }
-    return lo > 0 && t < q_start[lo] ? lo - 1 : -1;
+    *end = q_start[lo];
+    if (lo == 0 || t >= *end) return -1;
+    *kv = kv_len[lo - 1];
+    return lo - 1;
 }
 
 // Checks a descriptor and fills the view; `who` names the call in the message.

@@ -31,7 +31,7 @@ struct NormArgs {
     uint16_t* y;
     uint8_t* codes;
     float* scales;
-    int64_t x_stride, res_stride, res_out_stride, y_stride;
+    int x_stride, res_stride, res_out_stride, y_stride;
     int T, n;
     int row_scale;     // one scale a row (0: one for each 128 values)
     float eps;
@@ -93,19 +93,35 @@ struct Values<1> {
     __device__ __forceinline__ float2 squares(float2 sum) const { return make_float2(fmaf(v, v, sum.x), sum.y); }
 };
 
-template <int V>
-__device__ __forceinline__ Values<V> load_bf16(const uint16_t* p) {
-    Values<V> v;
-    if constexpr (V == 8) {
-        const uint4 w = *(const uint4*)p;
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// The same as they are loaded.
+template <typename X, int V>
+struct Raw {
+    uint32_t w[V * sizeof(X) / 4];
+    __device__ __forceinline__ void load(const X* p) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v.p[i] = make_float2(bf16_lo(u[i]), bf16_hi(u[i]));
-    } else {
-        v.v = bf16_to_f32(*p);
+        for (int i = 0; i < (int)(V * sizeof(X) / 16); ++i) {
+            const uint4 x = ((const uint4*)p)[i];
+            w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+        }
     }
-    return v;
-}
+    __device__ __forceinline__ Values<V> values() const {
+        Values<V> v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v.p[i] = sizeof(X) == 4 ? make_float2(__uint_as_float(w[sizeof(X) == 4 ? 2 * i : 0]), __uint_as_float(w[sizeof(X) == 4 ? 2 * i + 1 : 0]))
+                                    : make_float2(bf16_lo(w[sizeof(X) == 4 ? 0 : i]), bf16_hi(w[sizeof(X) == 4 ? 0 : i]));
+        return v;
+    }
+};
+template <typename X>
+struct Raw<X, 1> {
+    X w;
+    __device__ __forceinline__ void load(const X* p) { w = *p; }
+    __device__ __forceinline__ Values<1> values() const {
+        if constexpr (sizeof(X) == 4) return Values<1>{w};
+        else return Values<1>{bf16_to_f32(w)};
+    }
+};
 
 template <int V>
 __device__ __forceinline__ void store_bf16(uint16_t* p, const Values<V>& v) {
@@ -113,18 +129,6 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, const Values<V>& v) {
         *(uint4*)p = make_uint4(pack_bf16(v.p[0].x, v.p[0].y), pack_bf16(v.p[1].x, v.p[1].y), pack_bf16(v.p[2].x, v.p[2].y), pack_bf16(v.p[3].x, v.p[3].y));
     else
         *p = (uint16_t)pack_bf16(v.v, 0.f);
-}
-
-template <typename X, int V>
-__device__ __forceinline__ Values<V> load_x(const X* p) {
-    if constexpr (sizeof(X) == 2) {
-        return load_bf16<V>((const uint16_t*)p);
-    } else if constexpr (V == 8) {
-        const float4 a = ((const float4*)p)[0], b = ((const float4*)p)[1];
-        return Values<V>{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
-    } else {
-        return Values<V>{*(const float*)p};
-    }
 }
 
 // Reduction over the W warps of a row (slot: this row's places in shared memory).
@@ -177,49 +181,61 @@ __device__ __forceinline__ float store_codes(uint8_t* dst, const Values<8>& y, f
     return s;
 }
 
-// K steps of V values a lane, W warps a row.
+// K steps of V values a lane, W warps a row.  With many rows a lane has up to eight steps, all loads under way at once: one warp
+// for a row of 2048, whose sum needs no barrier, and few instructions beside the values' own.  With few rows a lane has one.
 template <typename X, int V, int K>
-__global__ void __launch_bounds__(1024) norm_kernel(NormArgs a, int W) {
+__global__ void __launch_bounds__(K == 8 ? 512 : 1024) norm_kernel(NormArgs a, int W, int rows) {
     __shared__ float sum_s[32], max_s[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = W == 1 ? warp : warp / W, in_row = warp - row * W;
-    const int rows = (blockDim.x >> 5) / W;
-    const int64_t t = (int64_t)blockIdx.x * rows + row;
-    const bool on = t < a.T;
-    const int c0 = in_row * 32 + lane, step = W * 32, chunks = on ? a.n / V : 0;
-    const X* x = (const X*)a.x + t * a.x_stride;
+    const int64_t t64 = (int64_t)blockIdx.x * rows + row;
+    const bool on = t64 < a.T;
+    const int t = on ? (int)t64 : 0, c0 = in_row * 32 + lane, step = W * 32, chunks = on ? a.n / V : 0;
     Values<V> h[K];
+    {
+        Raw<X, V> x[K];
+        Raw<uint16_t, V> r[K];
+        const X* xp = (const X*)a.x + (int64_t)t * a.x_stride + c0 * V;
+        const uint16_t* rp = a.residual + (int64_t)t * a.res_stride + c0 * V;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        h[k] = Values<V>{};
-        if (c0 + k * step < chunks) h[k] = load_x<X, V>(x + (c0 + k * step) * V);
+        for (int k = 0; k < K; ++k)
+            if (c0 + k * step < chunks) x[k].load(xp + k * step * V);
+        if (a.residual) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (c0 + k * step < chunks) r[k].load(rp + k * step * V);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            h[k] = Values<V>{};
+            if (c0 + k * step < chunks) {
+                h[k] = x[k].values();
+                if (a.residual) h[k].add(r[k].values());
+            }
+        }
     }
     if (a.residual) {
-        const uint16_t* r = a.residual + t * a.res_stride;
-        uint16_t* ro = a.residual_out + t * a.res_out_stride;
-        Values<V> v[K];
+        uint16_t* ro = a.residual_out + (int64_t)t * a.res_out_stride + c0 * V;
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (c0 + k * step < chunks) v[k] = load_bf16<V>(r + (c0 + k * step) * V);
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (c0 + k * step < chunks) {
-                h[k].add(v[k]);
-                store_bf16<V>(ro + (c0 + k * step) * V, h[k]);
-            }
+            if (c0 + k * step < chunks) store_bf16<V>(ro + k * step * V, h[k]);
     }
     float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) ss = h[k].squares(ss);
     const float sum = row_reduce<false>(ss.x + ss.y, W, sum_s + row * W, in_row, lane);
-    const float r = rsqrtf(__fdividef(sum, (float)a.n) + a.eps);
+    const float f = rsqrtf(__fdividef(sum, (float)a.n) + a.eps);
     float big = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int c = c0 + k * step;
         if (c < chunks) {
-            h[k].times(r);
-            if (a.weight) h[k].times(load_bf16<V>(a.weight + c * V));
-            if (a.y) store_bf16<V>(a.y + t * a.y_stride + c * V, h[k]);
+            h[k].times(f);
+            if (a.weight) {
+                Raw<uint16_t, V> w;
+                w.load(a.weight + c * V);
+                h[k].times(w.values());
+            }
+            if (a.y) store_bf16<V>(a.y + (int64_t)t * a.y_stride + c * V, h[k]);
         }
         if constexpr (V == 8) {
             if (a.codes) {
@@ -230,8 +246,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a, int W) {
 #pragma unroll
                     for (int d = 8; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(QMOE_FULL_MASK, m, d));
                     if (c < chunks) {
-                        const float s = store_codes(a.codes + t * a.n + c * V, h[k], m);
-                        if ((lane & 15) == 0) a.scales[t * ((a.n + 127) >> 7) + (c >> 4)] = s;
+                        const float s = store_codes(a.codes + (int64_t)t * a.n + c * V, h[k], m);
+                        if ((lane & 15) == 0) a.scales[(int64_t)t * ((a.n + 127) >> 7) + (c >> 4)] = s;
                     }
                 }
             }
@@ -243,31 +259,27 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a, int W) {
             if (on && c0 == 0) a.scales[t] = big * (1.f / 448.f);
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (c0 + k * step < chunks) store_codes(a.codes + t * a.n + (c0 + k * step) * V, h[k], big);
+                if (c0 + k * step < chunks) store_codes(a.codes + (int64_t)t * a.n + (c0 + k * step) * V, h[k], big);
         }
     }
 }
 
 constexpr int kNormMaxWidth = 32768;
 
+template <typename X, int V, int K>
+int launch_norm_steps(const NormArgs& a, cudaStream_t st) {
+    const int chunks = a.n / V, W = (chunks + 32 * K - 1) / (32 * K), rows = std::max(1, (K == 8 ? 4 : 8) / W);
+    norm_kernel<X, V, K><<<(unsigned)(((int64_t)a.T + rows - 1) / rows), rows * W * 32, 0, st>>>(a, W, rows);
+    return qmoe::launch_check("add_rms_norm");
+}
+
 template <typename X, int V>
 int launch_norm(const NormArgs& a, cudaStream_t st) {
-    // as many threads as a row has steps, up to 512 (more steps a thread then), and rows side by side in a block of 256
-    const int chunks = a.n / V, most = V == 8 ? 4 : 32;
-    int K = 1;
-    while (K < most && (chunks + K - 1) / K > 512) K *= 2;
-    const int W = (chunks + 32 * K - 1) / (32 * K), rows = std::max(1, 8 / W);
-    const unsigned blocks = (unsigned)(((int64_t)a.T + rows - 1) / rows);
-    const int threads = rows * W * 32;
-    if (K == 1) norm_kernel<X, V, 1><<<blocks, threads, 0, st>>>(a, W);
-    else if (K == 2) norm_kernel<X, V, 2><<<blocks, threads, 0, st>>>(a, W);
-    else if (K == 4) norm_kernel<X, V, 4><<<blocks, threads, 0, st>>>(a, W);
-    if constexpr (V == 1) {
-        if (K == 8) norm_kernel<X, V, 8><<<blocks, threads, 0, st>>>(a, W);
-        else if (K == 16) norm_kernel<X, V, 16><<<blocks, threads, 0, st>>>(a, W);
-        else if (K == 32) norm_kernel<X, V, 32><<<blocks, threads, 0, st>>>(a, W);
-    }
-    return qmoe::launch_check("add_rms_norm");
+    const int chunks = a.n / V;
+    if (V == 8 ? a.T >= 8 * qmoe::sm_count() && chunks > 32 : chunks > 1024 && chunks <= 4096) return launch_norm_steps<X, V, 8>(a, st);
+    if (chunks <= 512) return launch_norm_steps<X, V, 1>(a, st);
+    if (V == 8 || chunks <= 1024) return chunks <= 1024 ? launch_norm_steps<X, V, 2>(a, st) : launch_norm_steps<X, V, V == 8 ? 4 : 2>(a, st);
+    return launch_norm_steps<X, V, V == 8 ? 4 : 32>(a, st);
 }
 
 // ---------------------------------------------------------------- choice of experts
@@ -917,6 +929,8 @@ __global__ void __launch_bounds__(kTokenWarps * 32, R <= 16 ? 8 : R <= 32 ? 6 : 
     constexpr int V = 16 / (int)sizeof(X);
     __shared__ uint32_t key_s[kTokenWarps][kWideMost];
     __shared__ int id_s[kTokenWarps][kWideMost];
+    __shared__ float value_s[kTokenWarps][R / 8][2][128];
+    __shared__ int count_s[kTokenWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * kTokenWarps + warp;
     if (t >= a.T) return;
@@ -970,12 +984,17 @@ __global__ void __launch_bounds__(kTokenWarps * 32, R <= 16 ? 8 : R <= 32 ? 6 : 
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float s = a.sigmoid ? sigmoid_near(c[i + j]) : c[i + j] * inv_z;
-                c[i + j] = expert(i + j) < a.E ? fmaxf(s + bias[j], -INFINITY) : -INFINITY;
+                c[i + j] = fmaxf(s + bias[j], -INFINITY);
             }
+        }
+        if (a.E < 32 * R) {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                if (expert(i) >= a.E) c[i] = -INFINITY;
         }
     }
     // ---- the lanes' largest values, and the `rounds`-th of them
-    constexpr int CHUNK = R < 8 ? R : 8;
+    constexpr int CHUNK = 8;
     float chunk[R / CHUNK], mine = -INFINITY;
 #pragma unroll
     for (int i = 0; i < R / CHUNK; ++i) {
@@ -992,22 +1011,33 @@ __global__ void __launch_bounds__(kTokenWarps * 32, R <= 16 ? 8 : R <= 32 ? 6 : 
         if (lane == w) head = 0;
     }
     const float from = value_of(bound);
-    int n = 0;
+    // a lane's chunks that reach it go through shared memory, so that the code that looks at one is there once
+    uint32_t hits = 0;
 #pragma unroll
     for (int i = 0; i < R / CHUNK; ++i) {
-        if (!__any_sync(QMOE_FULL_MASK, chunk[i] >= from)) continue;
+        if (chunk[i] >= from) {
+            hits |= 1u << i;
 #pragma unroll
+            for (int j = 0; j < CHUNK; j += 4)
+                *(float4*)&value_s[warp][i][j / 4][lane * 4] = make_float4(c[i * CHUNK + j], c[i * CHUNK + j + 1], c[i * CHUNK + j + 2], c[i * CHUNK + j + 3]);
+        }
+    }
+    if (lane == 0) count_s[warp] = 0;
+    __syncwarp();
+    for (; hits; hits &= hits - 1) {
+        const int i = __ffs(hits) - 1;
+#pragma unroll 1
         for (int j = 0; j < CHUNK; ++j) {
+            const float v = value_s[warp][i][j >> 2][lane * 4 + (j & 3)];
             const int e = expert(i * CHUNK + j);
-            const bool in = c[i * CHUNK + j] >= from && e < a.E;
-            const unsigned who = __ballot_sync(QMOE_FULL_MASK, in);
-            if (who == 0) continue;
-            const int at = n + __popc(who & ((1u << lane) - 1));
-            if (in && at < kWideMost) key_s[warp][at] = key_of(c[i * CHUNK + j]), id_s[warp][at] = e;
-            n += __popc(who);
+            if (v >= from && e < a.E) {
+                const int at = atomicAdd(&count_s[warp], 1);      // (their order does not matter)
+                if (at < kWideMost) key_s[warp][at] = key_of(v), id_s[warp][at] = e;
+            }
         }
     }
     __syncwarp();
+    const int n = count_s[warp];
     bool again = n > kWideMost;
     uint32_t mk = 0;
     int at = 0;
@@ -1104,8 +1134,10 @@ extern "C" int add_rms_norm(const void* x, int x_is_f32, int64_t x_stride, const
     if (!x || (!y && !codes)) return qmoe::fail(QMOE_EINVAL, "add_rms_norm: NULL pointer");
     if (T > 1 && (x_stride < n || (residual && (residual_stride < n || residual_out_stride < n)) || (y && y_stride < n)))
         return qmoe::fail(QMOE_EINVAL, "add_rms_norm: a row stride is smaller than the row");
+    if (T == 1) x_stride = residual_stride = residual_out_stride = y_stride = 0;      // (not used)
     const int64_t strides = x_stride | (residual ? residual_stride | residual_out_stride : 0) | (y ? y_stride : 0);
-    const bool wide = n % 8 == 0 && (T == 1 || strides % 8 == 0) && aligned(x, 16) && aligned(residual, 16) && aligned(residual_out, 16) &&
+    if (strides > 0x7FFFFFFF) return qmoe::fail(QMOE_EINVAL, "add_rms_norm: a row stride of 2^31 or more");
+    const bool wide = n % 8 == 0 && strides % 8 == 0 && aligned(x, 16) && aligned(residual, 16) && aligned(residual_out, 16) &&
                       aligned(weight, 16) && aligned(y, 16);
     if (!aligned(x, x_is_f32 ? 4 : 2) || !aligned(residual, 2) || !aligned(residual_out, 2) || !aligned(weight, 2) || !aligned(y, 2) ||
         !aligned(scales, 4))
@@ -1113,7 +1145,7 @@ extern "C" int add_rms_norm(const void* x, int x_is_f32, int64_t x_stride, const
     if (codes && (!wide || !aligned(codes, 8)))
         return qmoe::fail(QMOE_EUNSUPPORTED, "add_rms_norm: codes need a row width and strides that are multiples of 8 and 16-byte aligned pointers");
     NormArgs a{x, (const uint16_t*)residual, (uint16_t*)residual_out, (const uint16_t*)weight, (uint16_t*)y, (uint8_t*)codes, scales,
-               x_stride, residual_stride, residual_out_stride, y_stride, T, n, scale_group == 0, eps};
+               (int)x_stride, (int)residual_stride, (int)residual_out_stride, (int)y_stride, T, n, scale_group == 0, eps};
     cudaStream_t st = (cudaStream_t)stream;
     if (wide) return x_is_f32 ? launch_norm<float, 8>(a, st) : launch_norm<uint16_t, 8>(a, st);
     return x_is_f32 ? launch_norm<float, 1>(a, st) : launch_norm<uint16_t, 1>(a, st);

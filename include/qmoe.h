@@ -648,7 +648,7 @@ int qk_norm_rope(const void* qkv, int64_t row_stride, int T, int n_q_heads, int 
  *  y         device out bf16 rows, or NULL when codes are given; may be x (bf16, the same stride).
  *  codes     device out uint8 [T][n], or NULL;  scales device out fp32 [T] when scale_group is 0,
  *            [T][ceil(n / 128)] when it is 128.
- *  n         1 .. 32768;  eps positive.
+ *  n         1 .. 32768, strides below 2^31;  eps positive.
  * Other overlaps between outputs and inputs are not allowed.  A row with a NaN or an infinity gives
  * what the formula gives (NaN, or 0 for its finite values beside an infinity); squares are fp32, so rows
  * with values of 1e19 and more overflow to that too.  Rows whose width, strides and
@@ -760,13 +760,13 @@ int kv4_block_bounds(const kv4_cache* cache, const kv4_bounds* bounds, const int
  *  q, q_start, kv_len, table, max_kv  as in kv4_attention.
  *  sel     device out int32 [n_q_tokens][n_kv_heads][top]: block numbers, ascending, then -1.  A query
  *          that sees top blocks or fewer has them all.
- *  top     1 .. 65536;  first, last >= 0, first + last <= top.
+ *  top     1 .. 65536;  first, last >= 0, first + last <= top;  max_kv at most 2^20 pages.
  *  workspace  device, ws_bytes >= kv4_select_blocks_ws_size(...), 16-byte aligned (no smaller for larger
  *          n_q_tokens or max_kv).
  * Rows of sel that belong to no request are left as they are.  A block without a page in the cache has
  * score -infinity (EINVAL in the error word).  A request whose kv_len is negative (EINVAL) or above
  * max_kv (ECAPACITY) gets lists of -1.
- * Errors: EINVAL, EUNSUPPORTED (more than 128 query heads per kv head), ECAPACITY (workspace).
+ * Errors: EINVAL, EUNSUPPORTED (more than 128 query heads per kv head, a larger max_kv), ECAPACITY (workspace).
  */
 int kv4_select_blocks_ws_size(int n_q_tokens, int n_kv_heads, int page_size, int max_kv, size_t* bytes);
 int kv4_select_blocks(const kv4_bounds* bounds, const void* q, int n_q_tokens, int n_q_heads, const int32_t* q_start,
