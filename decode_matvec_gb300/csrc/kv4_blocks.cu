@@ -7,6 +7,7 @@
 #include <algorithm>
 
 #include "kv4_common.cuh"
+#include "tc_common.cuh"
 
 namespace {
 
@@ -176,7 +177,7 @@ __device__ __forceinline__ int dot4(uint32_t c, uint32_t q0, uint32_t q1, int ac
     return __dp2a_hi((int)q1, (int)c, acc);
 }
 
-constexpr int kScoreThreads = 256;
+constexpr int kScoreThreads = 128;
 
 // q as bf16, NaN as 0, infinities as the largest finite value
 __device__ __forceinline__ float query_value(uint32_t bits) {
@@ -239,77 +240,119 @@ __global__ void __launch_bounds__(kWholeThreads) whole_kernel(SelectArgs a) {
     }
 }
 
-// Lanes that take a record (hi and lo codes, 16 a lane), and records of one kv head that they take at once.
-template <int D>
-constexpr int kRecordLanes = D / 8;
+// A thread block scores some blocks of one query token for up to kScoreHeads kv heads: it copies the records (hi and lo codes) of those
+// heads of each page, which stand side by side, to shared memory, all at once and without registers, so that the blocks of a
+// multiprocessor have what its bandwidth takes under way; then groups of L lanes (16 codes of a record each) multiply kRecords records
+// of one kv head at a time with the group's summed queries, and the partial sums are added up crosswise, so that lane i ends with
+// record i (mod kRecords).  What does not depend on the queries goes ahead of the wait for them.
+constexpr int kScoreBytes = 32768, kScoreHeads = 32, kRecords = 8, kMostPages = 256;
+constexpr uint32_t kWaitLimit = 1u << 22;
 
-// Blocks of the cache that a thread block scores for every kv head.
-inline int score_chunk(int head_dim, int n_kv) {
-    const int lanes = head_dim / 8, groups = kScoreThreads / lanes;
-    return std::max(1, groups / n_kv) * lanes;
+// Pages of a thread block: what its shared memory holds, or fewer while every group of lanes still has kRecords and the blocks are
+// few (131072 tokens in pages of 16, one kv head of 64: 132 blocks 12.4 us, 264 11.8).
+inline int score_pages(int head_dim, int n_kv, int64_t row, int64_t tokens) {
+    const int heads = std::min(n_kv, kScoreHeads), parts = std::max(1, kScoreThreads / (head_dim / 8) / heads);
+    int p = std::min(kScoreBytes / (2 * head_dim) / heads, kMostPages);
+    while (p >= 2 * kRecords * parts && (row + p - 1) / p * tokens < 2 * qmoe::sm_count()) p /= 2;
+    return p;
 }
 
-// A thread block scores `chunk` blocks of one query token for every kv head.  L lanes take L records of one kv head: lane i
-// looks up the i-th one's page and step, all of them load their 16 codes of every record (L loads of 16 bytes in flight), multiply
-// them with the group's summed queries, and the L x L partial sums are added up crosswise, so that lane i ends with the i-th
-// record's.  What does not depend on the queries goes ahead of the wait for them.
 template <int D>
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int chunks) {
-    constexpr int L = kRecordLanes<D>, GROUPS = kScoreThreads / L;
+__global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int chunks, int pages) {
+    constexpr int L = D / 8, GROUPS = kScoreThreads / L, TURNS = kMostPages / kScoreThreads;
+    __shared__ alignas(128) unsigned char codes_s[kScoreBytes];
+    __shared__ int page_s[kMostPages];
+    __shared__ uint64_t full;
     kv4::depend_launch();
-    const int t = blockIdx.x / chunks, c = blockIdx.x - t * chunks;
-    const int grp = threadIdx.x / L, gl = threadIdx.x & (L - 1);
-    const int parts = max(1, GROUPS / a.n_kv);
-    const int j = (c * parts + grp / a.n_kv) * L + gl;                          // the block that this lane looks up
-    // (in a decode step token t is request t: its table entry is loaded beside the lengths that say so)
-    const int likely = t < a.B && j < a.max_blocks ? a.table[(int64_t)t * a.max_blocks + j] : -1;
+    const int tid = threadIdx.x, t = blockIdx.x / chunks, c = blockIdx.x - t * chunks;
+    const int h0 = blockIdx.y * kScoreHeads, heads = min(a.n_kv - h0, kScoreHeads);
+    const int j0 = c * pages;
+    // (in a decode step token t is request t: its table entries are loaded beside the lengths that say so)
+    int entry[TURNS];
+#pragma unroll
+    for (int i = 0; i < TURNS; ++i) {
+        const int j = j0 + i * kScoreThreads + tid;
+        entry[i] = i * kScoreThreads + tid < pages && t < a.B && j < a.max_blocks ? a.table[(int64_t)t * a.max_blocks + j] : -1;
+    }
     int b;
-    const int seen = blocks_seen(a, t, &b, c == 0 && threadIdx.x == 0);
-    // few blocks are all taken
-    if (seen <= a.top || c * parts * L >= seen || grp >= a.n_kv * parts) {      // (whole groups of lanes leave)
+    const int seen = blocks_seen(a, t, &b, c == 0 && tid == 0 && h0 == 0);
+    if (seen <= a.top || j0 >= seen) {       // few blocks are all taken
         kv4::depend_wait();
         return;
     }
-    const unsigned mask = (L == 16 ? 0xFFFFu : 0xFFu) << (threadIdx.x & 31 & ~(L - 1));
-    int page = -1;
-    if (j < seen) {
-        page = b == t ? likely : j < a.max_blocks ? a.table[(int64_t)b * a.max_blocks + j] : -1;
-        if (page < 0 || page >= a.n_pages) {
-            if (grp % a.n_kv == 0) blocks_set_error(QMOE_EINVAL);
-            page = -1;
-        }
+    if (tid == 0) {
+        qmoe_tc::mbar_init(&full, 1);
+        qmoe_tc::fence_mbar_init();
     }
-    bool waited = false;
-    for (int h = grp % a.n_kv; h < a.n_kv; h += GROUPS) {
-        const float step = page >= 0 ? a.steps[(int64_t)page * a.n_kv + h] : 0.f;
-        uint4 code[L];
+    const uint32_t slice = (uint32_t)heads * (2 * D);
+    int there = 0;
 #pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const int pg = __shfl_sync(mask, page, i, L);
-            code[i] = make_uint4(0, 0, 0, 0);
-            if (pg >= 0) code[i] = *(const uint4*)(a.codes + ((int64_t)pg * a.n_kv + h) * (2 * D) + gl * 16);
+    for (int i = 0; i < TURNS; ++i) {
+        const int at = i * kScoreThreads + tid, j = j0 + at;
+        const bool mine = at < pages && j < seen;
+        if (b != t) entry[i] = mine && j < a.max_blocks ? a.table[(int64_t)b * a.max_blocks + j] : -1;
+        if (!mine || entry[i] < 0 || entry[i] >= a.n_pages) {
+            if (mine && h0 == 0) blocks_set_error(QMOE_EINVAL);
+            entry[i] = -1;
         }
-        if (!waited) kv4::depend_wait();
-        waited = true;
-        const uint4* q = (const uint4*)(a.whole + ((int64_t)t * a.n_kv + h) * (2 * D) + gl * 16);
-        const uint4 p0 = q[0], p1 = q[1];
-        int acc[L];
+        if (at < pages) page_s[at] = entry[i];
+        there += __syncthreads_count(entry[i] >= 0);
+    }
+    if (tid == 0)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(qmoe_tc::smem_u32(&full)), "r"((uint32_t)there * slice) : "memory");
+    __syncwarp();
 #pragma unroll
-        for (int i = 0; i < L; ++i)
-            acc[i] = dot4(code[i].w, p1.z, p1.w, dot4(code[i].z, p1.x, p1.y, dot4(code[i].y, p0.z, p0.w, dot4(code[i].x, p0.x, p0.y, 0))));
-        // lane i keeps the records whose number has the lane's upper bits, and gives the others away
-#pragma unroll
-        for (int d = L / 2; d > 0; d >>= 1) {
-            const bool upper = gl & d;
-#pragma unroll
-            for (int i = 0; i < d; ++i) {
-                const int give = upper ? acc[i] : acc[i + d], keep = upper ? acc[i + d] : acc[i];
-                acc[i] = keep + __shfl_xor_sync(mask, give, d);
+    for (int i = 0; i < TURNS; ++i)
+        if (entry[i] >= 0)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             qmoe_tc::smem_u32(codes_s) + (uint32_t)(i * kScoreThreads + tid) * slice),
+                         "l"(a.codes + ((int64_t)entry[i] * a.n_kv + h0) * (2 * D)), "r"(slice), "r"(qmoe_tc::smem_u32(&full))
+                         : "memory");
+    const int grp = tid / L, gl = tid & (L - 1), rec = gl & (kRecords - 1);
+    const unsigned mask = (L == 16 ? 0xFFFFu : 0xFFu) << (tid & 31 & ~(L - 1));
+    const int parts = max(1, GROUPS / heads), part = grp / heads, span = (min(pages, seen - j0) + parts - 1) / parts;
+    const int p0 = part * span, p1 = min(min(p0 + span, pages), seen - j0);
+    kv4::depend_wait();
+    bool landed = false;
+    for (int h = grp - part * heads; h < heads && part < parts; h += GROUPS) {
+        const uint4* q = (const uint4*)(a.whole + ((int64_t)t * a.n_kv + h0 + h) * (2 * D) + gl * 16);
+        const uint4 q0 = q[0], q1 = q[1];
+        for (int p = p0; p < p1; p += kRecords) {
+            const int at = p + rec, page = at < p1 ? page_s[at] : -1;
+            const float step = page >= 0 ? a.steps[(int64_t)page * a.n_kv + h0 + h] : 0.f;
+            if (!landed && !qmoe_tc::mbar_wait(&full, 0, kWaitLimit)) {
+                blocks_set_error(QMOE_ETIMEOUT);
+                return;
             }
+            landed = true;
+            const unsigned char* from = codes_s + (uint32_t)p * slice + h * (2 * D) + gl * 16;
+            int acc[kRecords];
+#pragma unroll
+            for (int r = 0; r < kRecords; ++r) {
+                const uint4 x = p + r < p1 ? *(const uint4*)(from + r * slice) : make_uint4(0, 0, 0, 0);      // (a missing page's: whatever stands there)
+                acc[r] = dot4(x.w, q1.z, q1.w, dot4(x.z, q1.x, q1.y, dot4(x.y, q0.z, q0.w, dot4(x.x, q0.x, q0.y, 0))));
+            }
+            if (L > kRecords) {
+#pragma unroll
+                for (int r = 0; r < kRecords; ++r) acc[r] += __shfl_xor_sync(mask, acc[r], kRecords);
+            }
+            // a lane keeps the records whose number has the lane's upper bits, and gives the others away
+#pragma unroll
+            for (int d = kRecords / 2; d > 0; d >>= 1) {
+                const bool upper = gl & d;
+#pragma unroll
+                for (int r = 0; r < d; ++r) {
+                    const int give = upper ? acc[r] : acc[r + d], keep = upper ? acc[r + d] : acc[r];
+                    acc[r] = keep + __shfl_xor_sync(mask, give, d);
+                }
+            }
+            // (a step that is NaN, which kv4_block_bounds never writes, gives a score like a missing page's)
+            if (at < p1 && gl < kRecords)
+                a.scores[((int64_t)t * a.n_kv + h0 + h) * a.max_seen + j0 + at] = page >= 0 ? fmaxf(__fmul_rn((float)acc[0], step), -INFINITY) : -INFINITY;
         }
-        // (a step that is NaN, which kv4_block_bounds never writes, gives a score like a missing page's)
-        if (j < seen) a.scores[((int64_t)t * a.n_kv + h) * a.max_seen + j] = page >= 0 ? fmaxf(__fmul_rn((float)acc[0], step), -INFINITY) : -INFINITY;
     }
+    // the copies land before the block's memory goes away
+    if (!landed && !qmoe_tc::mbar_wait(&full, 0, kWaitLimit)) blocks_set_error(QMOE_ETIMEOUT);
 }
 
 // ---------------------------------------------------------------- the best blocks
@@ -542,8 +585,8 @@ extern "C" int kv4_select_blocks(const kv4_bounds* bounds, const void* q, int n_
     a.bits = 15;
     while ((1 << (15 - a.bits)) < a.group) --a.bits;
     cudaStream_t st = (cudaStream_t)stream;
-    const int chunk = score_chunk(bounds->head_dim, n_kv);
-    const int64_t chunks = (row + chunk - 1) / chunk, blocks = chunks * n_q_tokens;
+    const int pages = score_pages(bounds->head_dim, n_kv, row, n_q_tokens);
+    const int64_t chunks = (row + pages - 1) / pages, blocks = chunks * n_q_tokens;
     if (blocks > 0x7FFFFFFFLL || (int64_t)n_q_tokens * n_kv > 0x7FFFFFFFLL)
         return qmoe::fail(QMOE_EINVAL, "kv4_select_blocks: too many query tokens in one call");
     const unsigned lists = (unsigned)(n_q_tokens * n_kv), by_warps = (lists + kPickThreads / 32 - 1) / (kPickThreads / 32);
@@ -558,7 +601,7 @@ extern "C" int kv4_select_blocks(const kv4_bounds* bounds, const void* q, int n_
     if (d128) whole_kernel<128><<<whole_blocks, kWholeThreads, 0, st>>>(a);
     else whole_kernel<64><<<whole_blocks, kWholeThreads, 0, st>>>(a);
     if ((rc = qmoe::launch_check(who))) return rc;
-    if ((rc = kv4::launch_dependent(d128 ? score_kernel<128> : score_kernel<64>, dim3((unsigned)blocks), kScoreThreads, 0, st, who, a, (int)chunks))) return rc;
+    if ((rc = kv4::launch_dependent(d128 ? score_kernel<128> : score_kernel<64>, dim3((unsigned)blocks, (unsigned)((n_kv + kScoreHeads - 1) / kScoreHeads)), kScoreThreads, 0, st, who, a, (int)chunks, pages))) return rc;
     const int64_t most = ((int64_t)max_kv + bounds->page_size - 1) / bounds->page_size - first - last;      // blocks a list chooses from
     if (most <= 128) return kv4::launch_dependent(pick_kernel<1, 4>, dim3(by_warps), kPickThreads, 0, st, who, a);
     if (most <= 512) return kv4::launch_dependent(pick_kernel<1, 16>, dim3(by_warps), kPickThreads, 0, st, who, a);

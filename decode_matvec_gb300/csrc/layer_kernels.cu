@@ -43,54 +43,28 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(*(unsigned long long*)&r) : "l"(*(unsigned long long*)&a), "l"(*(unsigned long long*)&b));
-    return r;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(*(unsigned long long*)&r) : "l"(*(unsigned long long*)&a), "l"(*(unsigned long long*)&b));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(*(unsigned long long*)&r)
-        : "l"(*(unsigned long long*)&a), "l"(*(unsigned long long*)&b), "l"(*(unsigned long long*)&c));
-    return r;
-}
-
-// A lane's values of a step: eight as four pairs (16-byte accesses), or one (any width, stride and alignment).
+// A lane's values of a step: eight (16-byte accesses), or one (any width, stride and alignment).  (Packed pairs of fp32 take more
+// instructions here, for the moves that line them up: 30.7 against 25.4 million for 16384 rows of 2048.)
 template <int V>
 struct Values {
-    float2 p[4];
+    float v[V];
     __device__ __forceinline__ void add(const Values& o) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = add2(p[i], o.p[i]);
+        for (int i = 0; i < V; ++i) v[i] += o.v[i];
     }
     __device__ __forceinline__ void times(const Values& o) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = mul2(p[i], o.p[i]);
+        for (int i = 0; i < V; ++i) v[i] *= o.v[i];
     }
     __device__ __forceinline__ void times(float f) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = mul2(p[i], make_float2(f, f));
+        for (int i = 0; i < V; ++i) v[i] *= f;
     }
-    __device__ __forceinline__ float2 squares(float2 sum) const {
+    __device__ __forceinline__ float squares(float sum) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum = fma2(p[i], p[i], sum);
+        for (int i = 0; i < V; ++i) sum = fmaf(v[i], v[i], sum);
         return sum;
     }
-};
-template <>
-struct Values<1> {
-    float v;
-    __device__ __forceinline__ void add(const Values& o) { v += o.v; }
-    __device__ __forceinline__ void times(const Values& o) { v *= o.v; }
-    __device__ __forceinline__ void times(float f) { v *= f; }
-    __device__ __forceinline__ float2 squares(float2 sum) const { return make_float2(fmaf(v, v, sum.x), sum.y); }
 };
 
 // The same as they are loaded.
@@ -105,12 +79,13 @@ struct Raw {
         }
     }
     __device__ __forceinline__ Values<V> values() const {
-        Values<V> v;
+        Values<V> r;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v.p[i] = sizeof(X) == 4 ? make_float2(__uint_as_float(w[sizeof(X) == 4 ? 2 * i : 0]), __uint_as_float(w[sizeof(X) == 4 ? 2 * i + 1 : 0]))
-                                    : make_float2(bf16_lo(w[sizeof(X) == 4 ? 0 : i]), bf16_hi(w[sizeof(X) == 4 ? 0 : i]));
-        return v;
+        for (int i = 0; i < V; ++i) {
+            if constexpr (sizeof(X) == 4) r.v[i] = __uint_as_float(w[i]);
+            else r.v[i] = i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+        }
+        return r;
     }
 };
 template <typename X>
@@ -118,17 +93,17 @@ struct Raw<X, 1> {
     X w;
     __device__ __forceinline__ void load(const X* p) { w = *p; }
     __device__ __forceinline__ Values<1> values() const {
-        if constexpr (sizeof(X) == 4) return Values<1>{w};
-        else return Values<1>{bf16_to_f32(w)};
+        if constexpr (sizeof(X) == 4) return Values<1>{{w}};
+        else return Values<1>{{bf16_to_f32(w)}};
     }
 };
 
 template <int V>
 __device__ __forceinline__ void store_bf16(uint16_t* p, const Values<V>& v) {
     if constexpr (V == 8)
-        *(uint4*)p = make_uint4(pack_bf16(v.p[0].x, v.p[0].y), pack_bf16(v.p[1].x, v.p[1].y), pack_bf16(v.p[2].x, v.p[2].y), pack_bf16(v.p[3].x, v.p[3].y));
+        *(uint4*)p = make_uint4(pack_bf16(v.v[0], v.v[1]), pack_bf16(v.v[2], v.v[3]), pack_bf16(v.v[4], v.v[5]), pack_bf16(v.v[6], v.v[7]));
     else
-        *p = (uint16_t)pack_bf16(v.v, 0.f);
+        *p = (uint16_t)pack_bf16(v.v[0], 0.f);
 }
 
 // Reduction over the W warps of a row (slot: this row's places in shared memory).
@@ -154,37 +129,29 @@ __device__ __forceinline__ float row_reduce(float v, int W, float* slot, int war
 __device__ __forceinline__ float largest(const Values<8>& v) {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) asm("max.NaN.abs.f32 %0, %1, %2, %0;" : "+f"(m) : "f"(v.p[i].x), "f"(v.p[i].y));
+    for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(v.v[i]));
     return m;
 }
 
-// 8 codes of y / s for s = m / 448, which is returned.  448 / m is within two steps of the quotient's last place, before a
-// rounding to 4 bits; where it or m leaves fp32's middle range, every code is a division.
+// 8 codes of y / s for s = m / 448, which is returned.  A power of two brings m next to 1 (whatever its exponent: no value
+// overflows or loses bits on the way), and 448 / m is within two steps of the quotient's last place, before a rounding to 4 bits.
 __device__ __forceinline__ float store_codes(uint8_t* dst, const Values<8>& y, float m) {
-    const float s = m * (1.f / 448.f);
-    float2 q[4];
-    if (m >= 1e-30f && m <= 1e30f) {
-        const float inv = __fdividef(448.f, m);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = mul2(y.p[i], make_float2(inv, inv));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)      // (0 and NaN: codes 0)
-            q[i] = s > 0.f ? make_float2(__fdiv_rn(y.p[i].x, s), __fdiv_rn(y.p[i].y, s)) : make_float2(0.f, 0.f);
-    }
+    const float g = __uint_as_float(max((254u << 23) - (__float_as_uint(m) & 0x7F800000u), 1u << 23));
+    const float inv = m == 0.f ? 0.f : __fdividef(448.f, m * g);
     uint32_t w[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-        w[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(q[2 * j], __NV_SATFINITE, __NV_E4M3) |
-               (uint32_t)__nv_cvt_float2_to_fp8x2(q[2 * j + 1], __NV_SATFINITE, __NV_E4M3) << 16;
+    for (int j = 0; j < 2; ++j) {
+        const float* v = y.v + 4 * j;
+        w[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[0] * g * inv, v[1] * g * inv), __NV_SATFINITE, __NV_E4M3) |
+               (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[2] * g * inv, v[3] * g * inv), __NV_SATFINITE, __NV_E4M3) << 16;
+    }
     *(uint2*)dst = make_uint2(w[0], w[1]);
-    return s;
+    return m * (1.f / 448.f);
 }
 
-// K steps of V values a lane, W warps a row.  With many rows a lane has up to eight steps, all loads under way at once: one warp
-// for a row of 2048, whose sum needs no barrier, and few instructions beside the values' own.  With few rows a lane has one.
+// K steps of V values a lane, all loads under way at once; W warps a row.
 template <typename X, int V, int K>
-__global__ void __launch_bounds__(K == 8 ? 512 : 1024) norm_kernel(NormArgs a, int W, int rows) {
+__global__ void __launch_bounds__(1024) norm_kernel(NormArgs a, int W, int rows) {
     __shared__ float sum_s[32], max_s[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = W == 1 ? warp : warp / W, in_row = warp - row * W;
     const int64_t t64 = (int64_t)blockIdx.x * rows + row;
@@ -219,10 +186,10 @@ __global__ void __launch_bounds__(K == 8 ? 512 : 1024) norm_kernel(NormArgs a, i
         for (int k = 0; k < K; ++k)
             if (c0 + k * step < chunks) store_bf16<V>(ro + k * step * V, h[k]);
     }
-    float2 ss = make_float2(0.f, 0.f);
+    float part[2] = {0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < K; ++k) ss = h[k].squares(ss);
-    const float sum = row_reduce<false>(ss.x + ss.y, W, sum_s + row * W, in_row, lane);
+    for (int k = 0; k < K; ++k) part[k & 1] = h[k].squares(part[k & 1]);
+    const float sum = row_reduce<false>(part[0] + part[1], W, sum_s + row * W, in_row, lane);
     const float f = rsqrtf(__fdividef(sum, (float)a.n) + a.eps);
     float big = 0.f;
 #pragma unroll
@@ -268,18 +235,21 @@ constexpr int kNormMaxWidth = 32768;
 
 template <typename X, int V, int K>
 int launch_norm_steps(const NormArgs& a, cudaStream_t st) {
-    const int chunks = a.n / V, W = (chunks + 32 * K - 1) / (32 * K), rows = std::max(1, (K == 8 ? 4 : 8) / W);
+    const int W = (a.n / V + 32 * K - 1) / (32 * K), rows = std::max(1, 4 / W);
     norm_kernel<X, V, K><<<(unsigned)(((int64_t)a.T + rows - 1) / rows), rows * W * 32, 0, st>>>(a, W, rows);
     return qmoe::launch_check("add_rms_norm");
 }
 
+// Steps a lane.  With many rows two: four warps for a row of 2048, blocks of 128 threads (16384 rows of 2048 with a residual and
+// codes, us: 48.2 with one step, 47.8 with two, 47.6 with four, 53.7 with eight; 4095 of 2080 from fp32 with a scale a row: 20.8,
+// 18.3, 20.0, 22.4).  With few rows one, for the shortest chain; more where a row would take more than 16 warps.
 template <typename X, int V>
 int launch_norm(const NormArgs& a, cudaStream_t st) {
     const int chunks = a.n / V;
-    if (V == 8 ? a.T >= 8 * qmoe::sm_count() && chunks > 32 : chunks > 1024 && chunks <= 4096) return launch_norm_steps<X, V, 8>(a, st);
-    if (chunks <= 512) return launch_norm_steps<X, V, 1>(a, st);
-    if (V == 8 || chunks <= 1024) return chunks <= 1024 ? launch_norm_steps<X, V, 2>(a, st) : launch_norm_steps<X, V, V == 8 ? 4 : 2>(a, st);
-    return launch_norm_steps<X, V, V == 8 ? 4 : 32>(a, st);
+    if (chunks <= 512 && a.T < 8 * qmoe::sm_count()) return launch_norm_steps<X, V, 1>(a, st);
+    if (chunks <= 1024) return launch_norm_steps<X, V, 2>(a, st);
+    if constexpr (V == 8) return launch_norm_steps<X, V, 4>(a, st);
+    else return chunks <= 4096 ? launch_norm_steps<X, V, 8>(a, st) : launch_norm_steps<X, V, 32>(a, st);
 }
 
 // ---------------------------------------------------------------- choice of experts
