@@ -64,6 +64,16 @@ __device__ __forceinline__ bool chosen_token(const AttnArgs& a, int t, int* b, i
     return true;
 }
 
+// What its list holds: entries that are read, the query's own block (the last that it sees) and the tokens it sees of that.
+struct ChosenList {
+    int req, listed, own_blk, in_own;
+};
+__device__ __forceinline__ ChosenList list_of(const AttnArgs& a, int t) {
+    int req = 0, pos = -1, seen = 0;
+    chosen_token(a, t, &req, &pos, &seen, false);
+    return ChosenList{req, min(seen, a.top), seen - 1, pos - ((seen - 1) << a.cache.page_shift) + 1};
+}
+
 // ---------------------------------------------------------------- few query rows: one pass over the codes
 //
 // A request's rows of one kv head (query n, head g of the group: row n * group + g) are few, so the
@@ -323,8 +333,15 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
         int kv_len = 0, seen_lo = 0, seen_hi = 0;       // every row sees tokens [seen_lo, seen_hi)
         int blk_lo = 0;                                 // first block that some row sees: those before may have no page
         int held = 0, entry = -1;                       // lane i holds the entry of block held + i
-        int listed = 0, own_blk = -1, in_own = 0, req = 0;   // chosen blocks: entries read, the query's own block, what it sees of that, its request
-        int chosen = -1;                                // and the block that entry belongs to
+        // chosen blocks: the token's list; the block that entry belongs to; and the same of the 32 entries that come after those
+        // held, which are looked up while the copies before them are under way (a list's entry leads to a table's)
+        ChosenList list{}, next_list{};
+        int chosen = -1, next_chosen = -1, next_entry = -1, next_b = -1, next_kh = 0, next_blk = 0;
+        bool looked = false;
+        auto look_up = [&](const ChosenList& l, int token, int head, int blk, int* c, int* e) {
+            *c = blk + lane < l.listed ? a.sel[((int64_t)token * a.cache.n_kv_heads + head) * a.top + blk + lane] : -1;
+            *e = *c >= 0 && *c <= l.own_blk && *c < a.max_blocks ? a.table[(int64_t)l.req * a.max_blocks + *c] : -1;
+        };
         bool ok = true, fresh = true;
         int issued = 0;
         for (int u = 0; ok; ++u) {
@@ -352,11 +369,9 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
             }
             const int end = (int)min((long long)n, u1 - begin);      // of the item's tiles in this run
             const int blk0 = (t0 + tile) * per_tile;
+            const bool known = kSel && looked && next_b == b && next_kh == kh && next_blk == blk0;
             if (kSel && fresh) {
-                int pos = -1, seen = 0;
-                chosen_token(a, b, &req, &pos, &seen, false);
-                listed = min(seen, a.top);
-                own_blk = seen - 1, in_own = pos - (own_blk << a.cache.page_shift) + 1;
+                list = known ? next_list : list_of(a, b);
             } else if (fresh) {
                 const int q_len = a.q_start[b + 1] - a.q_start[b];
                 kv_len = a.kv_len[b];
@@ -367,20 +382,22 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
             if (fresh || blk0 + per_tile > held + 32) {
                 held = blk0;
                 const int blk = blk0 + lane;
-                if (kSel) {
-                    chosen = blk < listed ? a.sel[((int64_t)b * a.cache.n_kv_heads + kh) * a.top + blk] : -1;
+                if constexpr (kSel) {
+                    if (known) chosen = next_chosen, entry = next_entry;
+                    else look_up(list, b, kh, blk0, &chosen, &entry);
                     if (chosen < -1) attn_set_error(QMOE_EINVAL);
-                    entry = chosen >= 0 && chosen <= own_blk && chosen < a.max_blocks ? a.table[(int64_t)req * a.max_blocks + chosen] : -1;
-                } else
-                entry = blk < a.max_blocks && ((long long)blk << a.cache.page_shift) < kv_len ? a.table[(int64_t)b * a.max_blocks + blk] : -1;
+                    looked = false;
+                } else {
+                    entry = blk < a.max_blocks && ((long long)blk << a.cache.page_shift) < kv_len ? a.table[(int64_t)b * a.max_blocks + blk] : -1;
+                }
             }
             const int page = __shfl_sync(QMOE_FULL_MASK, entry, (blk0 - held + lane) & 31);
             bool mine = lane < per_tile && blk0 + lane >= blk_lo && ((blk0 + lane) << a.cache.page_shift) < kv_len;
             unsigned partial = 0;
             if (kSel) {
                 const int blk = __shfl_sync(QMOE_FULL_MASK, chosen, (blk0 - held + lane) & 31);
-                mine = lane < per_tile && blk0 + lane < listed && blk >= 0 && blk <= own_blk;
-                partial = __ballot_sync(QMOE_FULL_MASK, mine && blk == own_blk && in_own < 1 << a.cache.page_shift);
+                mine = lane < per_tile && blk0 + lane < list.listed && blk >= 0 && blk <= list.own_blk;
+                partial = __ballot_sync(QMOE_FULL_MASK, mine && blk == list.own_blk && list.in_own < 1 << a.cache.page_shift);
             }
             const bool good = mine && page >= 0 && page < a.cache.n_pages;
             if (mine && !good) attn_set_error(QMOE_EINVAL);
@@ -399,7 +416,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
                 if (kSel) {
                     if ((int)mask != (1 << per_tile) - 1 || partial) flags |= kEdge | (int)partial * kPartial;
                 } else if ((t0 + tile) * kTile < seen_lo || (t0 + tile + 1) * kTile > seen_hi || (int)mask != (1 << per_tile) - 1) flags |= kEdge;
-                sh.info[st] = StageInfo{b, kh, kSel ? in_own : t0 + tile, flags};
+                sh.info[st] = StageInfo{b, kh, kSel ? list.in_own : t0 + tile, flags};
                 if ((flags & (kLast | kWholeStart | kWholeEnd)) == (kLast | kWholeStart))
                     items[blockIdx.x] = SplitItem{b, kh, 0, (int)((begin + n - 1) / chunk)};
                 mbar_expect(&sh.full[st], (uint32_t)__popc(mask) * page_copy);
@@ -409,6 +426,18 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
             issued = u + 1;
             fresh = false;
             ++tile;
+            if (kSel && !looked && blk0 > held) {
+                // the item's next entries, or the next item's first
+                looked = true;
+                next_b = b, next_kh = kh, next_blk = held + 32, next_list = list;
+                if (next_blk >= min(list.listed, end * per_tile)) {
+                    next_blk = 0;
+                    if (++next_kh == a.cache.n_kv_heads) next_kh = 0, ++next_b;
+                    if (begin + n + kItemCost >= u1 || next_b >= a.n_q_tokens) next_b = -1;
+                    else if (next_b != b) next_list = list_of(a, next_b);
+                }
+                if (next_b >= 0) look_up(next_list, next_b, next_kh, next_blk, &next_chosen, &next_entry);
+            }
         }
         if (!ok) {
             // give up: report, and let the copies in flight land before the block's memory goes away
@@ -1740,7 +1769,7 @@ int launch_decode(const AttnArgs& a, void* ws, cudaStream_t st) {
     float* parts = (float*)((char*)ws + decode_records());
     decode_kernel<D, NT, kSel><<<blocks, kDecodeThreads, smem, st>>>(a, rows, 0, items, parts);
     if ((rc = qmoe::launch_check("decode_kernel"))) return rc;
-    return kv4::launch_dependent(join_kernel<D, kSel>, dim3(blocks, NT == 1 ? 8 : 16), kJoinThreads, 0, st, "join_kernel", a, items, parts, rows);
+    return kv4::launch_dependent(join_kernel<D, kSel>, dim3(blocks, kSel ? std::min(a.group, 16) : NT == 1 ? 8 : 16), kJoinThreads, 0, st, "join_kernel", a, items, parts, rows);
 }
 
 // Workspace of the tile path: the plan, then the blocks' parts.  max_pairs bounds the sum of ceil(rows / 256).
