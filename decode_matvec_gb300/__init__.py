@@ -702,12 +702,14 @@ def kv4_attention(cache: Kv4Cache, q, q_start, kv_len, table, out, workspace, ma
 # ================================================================ around attention and experts
 def _rows(t, T: int, n: int, types, name: str, dev: int) -> int:
     """Row stride of t [T, n] (values of a row contiguous)."""
-    if t.shape != (T, n) or t.dtype not in types or t.get_device() != dev:
-        _refuse(f"{name}: [{T}, {n}] of {' or '.join(str(x) for x in types)} on cuda:{dev}")
-    s0, s1 = t.stride()
-    if s1 != 1 and n > 1:
-        _refuse(f"{name}: the values of a row contiguous")
-    return s0
+    if t.dtype in types and t.get_device() == dev:
+        if t.is_contiguous() and t.numel() == T * n:
+            return n
+        if t.shape == (T, n):
+            s0, s1 = t.stride()
+            if s1 == 1 or n == 1:
+                return s0
+    _refuse(f"{name}: [{T}, {n}] of {' or '.join(str(x) for x in types)} on cuda:{dev}, the values of a row contiguous")
 
 
 _bits8 = ()          # e4m3, and its bits as 8-bit integers

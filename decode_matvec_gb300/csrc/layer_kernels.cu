@@ -266,7 +266,7 @@ int launch_norm(const NormArgs& a, cudaStream_t st) {
 // A lane holds R neighbouring experts as integer keys, and the 4 best of them sorted; among lanes with equal keys the
 // lowest has the lowest index.  A round of the choice is a reduction of the lanes' heads (one instruction), a ballot, and the
 // winner's list moving up.  Which expert a key was is looked up at the end, for all the chosen at once.  A warp takes a
-// token; above 1024 experts a block of 8 warps does, each warp's best being merged by the first.
+// token.  Above 256 experts without groups a block of 4 warps does, another way (wide_route_kernel).
 struct RouteArgs {
     const void* logits;
     const float* bias;
@@ -279,7 +279,7 @@ struct RouteArgs {
     float scale;
 };
 
-constexpr int kRouteWarps = 8;              // of a block that works on one token
+constexpr int kWideWarps = 4;               // of a block that works on one token
 constexpr int kTokenWarps = 4;              // of a block whose warps take a token each (small blocks end and begin evenly)
 constexpr float kUlp = 5.9604645e-8f;       // 2^-24
 constexpr float kLargest = 3.402823466e38f;
@@ -352,6 +352,12 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Bound on a score's error: sigmoid_near's; or, with x = l - top, (2.5 |x| + 4) 2^-24 of itself from an exponential (|x| e^x <=
+// 0.37), the same of the sum (|x| weighed by the scores is at most ln E) and R / 4 + 17 additions, and 9 of a quotient and factors.
+__device__ __forceinline__ float error_bound(const RouteArgs& a, int R, float inv_z) {
+    return fmaf(a.sigmoid ? 6.f : (float)(R / 4 + 70) * inv_z, kUlp, 1e-37f);
+}
+
 // Within 6 2^-24: (1.5 |l| + 4) 2^-24 of the exponential, which the score's slope s (1 - s) makes 1.4, and 3 of the rest.
 __device__ __forceinline__ float sigmoid_near(float l) { return rcp(1.f + ex2(-kLog2e * l)); }
 
@@ -479,8 +485,8 @@ __device__ __forceinline__ unsigned long long warp_max64(unsigned long long v) {
 }
 
 struct ResolveShared {
-    double sum[kRouteWarps];
-    unsigned long long key[kRouteWarps];
+    double sum[kWideWarps];
+    unsigned long long key[kWideWarps];
 };
 
 // Sum of the row's exponentials, by NW warps that hold R experts a lane from e0 on (1 for sigmoid scores).
@@ -677,19 +683,14 @@ __device__ __forceinline__ Doubts doubts_of(const RouteArgs& a, uint32_t mk, int
     return d;
 }
 
-// R experts a lane; NW warps a token (1: kTokenWarps tokens a block).
-template <typename X, int R, int NW>
-__global__ void __launch_bounds__((NW == 1 ? kTokenWarps : kRouteWarps) * 32, NW == 1 ? (R <= 8 ? 8 : 4) : 2) route_kernel(RouteArgs a) {
-    __shared__ ResolveShared rs;
-    __shared__ float2 part_s[kRouteWarps];
-    __shared__ uint32_t key_s[NW > 1 ? kRouteWarps * 32 : 1];
-    __shared__ int id_s[NW > 1 ? kRouteWarps * 32 : 1];
-    __shared__ float2 bound_s;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = NW == 1 ? (int64_t)blockIdx.x * kTokenWarps + warp : blockIdx.x;
+// R experts a lane, a warp a token.
+template <typename X, int R>
+__global__ void __launch_bounds__(kTokenWarps * 32, R <= 8 ? 8 : 4) route_kernel(RouteArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * kTokenWarps + (threadIdx.x >> 5);
     if (t >= a.T) return;
     const X* row = (const X*)a.logits + t * a.stride;
-    const int e0 = (NW == 1 ? lane : (int)threadIdx.x) * R;
+    const int e0 = lane * R;
     float c[R];
     load_values<X, R>(row, e0, a.E, a.vec, -INFINITY, c);
 #pragma unroll
@@ -703,29 +704,15 @@ __global__ void __launch_bounds__((NW == 1 ? kTokenWarps : kRouteWarps) * 32, NW
         for (int i = 1; i < R; ++i) top = fmaxf(top, c[i]);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(QMOE_FULL_MASK, top, d));
-        const float m = top > -INFINITY ? top : 0.f;
+        if (!(top > -INFINITY)) top = 0.f;       // nothing in the row: scores 0
         float part[4] = {};
 #pragma unroll
-        for (int i = 0; i < R; ++i) part[i & 3] += ex2(kLog2e * (c[i] - m));
+        for (int i = 0; i < R; ++i) part[i & 3] += ex2(kLog2e * (c[i] - top));
         z = warp_sum((part[0] + part[1]) + (part[2] + part[3]));
-        if (NW > 1) {
-            if (lane == 0) part_s[warp] = make_float2(top, z);
-            __syncthreads();
-            const float2 p = part_s[lane & (NW - 1)];
-            top = p.x;
-#pragma unroll
-            for (int d = NW / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(QMOE_FULL_MASK, top, d));
-            z = p.x > -INFINITY ? p.y * ex2(kLog2e * (p.x - top)) : 0.f;
-#pragma unroll
-            for (int d = NW / 2; d > 0; d >>= 1) z += __shfl_xor_sync(QMOE_FULL_MASK, z, d);
-        }
-        if (!(top > -INFINITY)) top = 0.f, z = 1.f;      // nothing in the row: scores 0
+        if (!(z > 0.f)) z = 1.f;
     }
-    // ---- values, and the bound on a score's error: sigmoid_near's; or, with x = l - top, (2.5 |x| + 4) 2^-24 of itself from an
-    // exponential (|x| e^x <= 0.37), the same of the sum (|x| weighed by the scores is at most ln E) and R / 4 + 17 additions, and a
-    // quotient's 3
-    const float inv_z = rcp(z);
-    const float score_err = fmaf(a.sigmoid ? 6.f : (float)(R / 4 + 64) * inv_z, kUlp, 1e-37f);
+    // ---- values, and the bound on a score's error
+    const float inv_z = rcp(z), score_err = error_bound(a, R, inv_z), slack = by_logit ? 0.f : score_err;
     auto score_near = [&](float l) { return a.sigmoid ? sigmoid_near(l) : ex2(kLog2e * (l - top)) * inv_z; };
     if (!by_logit) {
         float bias[R];
@@ -741,85 +728,81 @@ __global__ void __launch_bounds__((NW == 1 ? kTokenWarps : kRouteWarps) * 32, NW
         for (int i = 0; i < R; ++i)
             if (e0 + i >= a.E) key[i] = 0u;
     }
-    const float slack = by_logit ? 0.f : score_err;
     best_keys<R>(key, list);
-    if constexpr (NW == 1 && R <= 32) {
-        if (a.groups > 1) {
-            // ---- groups
-            const int size = a.group_size, lanes = a.group_lanes;
-            const bool whole = lanes > 0;
-            Pair mine{0, 0};
-            if (whole) {
-                Pair p{list[0], R > 1 ? list[R > 1 ? 1 : 0] : 0u};
+    if (a.groups > 1) {
+        // ---- groups
+        const int size = a.group_size, lanes = a.group_lanes;
+        const bool whole = lanes > 0;
+        Pair mine{0, 0};
+        if (whole) {
+            Pair p{list[0], R > 1 ? list[R > 1 ? 1 : 0] : 0u};
 #pragma unroll
-                for (int d = 1; d < 32; d <<= 1)
-                    if (d < lanes) p = merge(p, Pair{__shfl_xor_sync(QMOE_FULL_MASK, p.a, d), __shfl_xor_sync(QMOE_FULL_MASK, p.b, d)});
-                mine = Pair{__shfl_sync(QMOE_FULL_MASK, p.a, lane * lanes & 31), __shfl_sync(QMOE_FULL_MASK, p.b, lane * lanes & 31)};
-            } else {
-                for (int g = 0; g < a.groups; ++g) {
-                    Pair p{0, 0};
-#pragma unroll
-                    for (int i = 0; i < R; ++i)
-                        if (e0 + i >= g * size && e0 + i < (g + 1) * size) p = merge(p, Pair{key[i], 0});
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) p = merge(p, Pair{__shfl_xor_sync(QMOE_FULL_MASK, p.a, d), __shfl_xor_sync(QMOE_FULL_MASK, p.b, d)});
-                    if (lane == g) mine = p;
-                }
-            }
-            uint32_t kept;
-            if (by_logit && a.best == 1) {
-                kept = best_groups(mine.a, a.groups, a.top_groups, lane);
-            } else {
-                float va = value_of(mine.a), vb = a.best == 2 ? value_of(mine.b) : 0.f;
-                if (by_logit) va = score_near(va), vb = score_near(vb);      // (sums of scores)
-                const bool on = lane < a.groups;
-                const float v = on ? fmaxf(va + vb, -INFINITY) : -INFINITY;
-                kept = best_groups(v, a.groups, a.top_groups, lane);
-                if (a.top_groups < a.groups) {
-                    // the last one kept and the best one dropped
-                    const float mag = fabsf(va) + fabsf(vb);
-                    const float err = on ? 2.f * score_err + (mag < kLargest ? 2.f * kUlp * mag : 0.f) : 0.f;
-                    const bool is = (kept >> lane) & 1;
-                    const float low = value_of(~__reduce_max_sync(QMOE_FULL_MASK, is ? ~key_of(v) : 0u));
-                    const float high = value_of(__reduce_max_sync(QMOE_FULL_MASK, on && !is ? key_of(v) : 0u));
-                    const float err2 = 2.f * __uint_as_float(__reduce_max_sync(QMOE_FULL_MASK, __float_as_uint(err)));
-                    // (infinite ones are equal or not, whatever the bits: NaN here)
-                    if (__builtin_expect(low - high <= err2, 0)) {
-                        const uint32_t doubt = __ballot_sync(QMOE_FULL_MASK, on && v >= high - err2 && v <= low + err2);
-                        // the experts that may be among the best of those groups
-                        uint32_t cand = 0;
-                        for (uint32_t todo = doubt; todo; todo &= todo - 1) {
-                            const int g = __ffs(todo) - 1;
-                            const uint32_t least = __shfl_sync(QMOE_FULL_MASK, a.best == 2 ? mine.b : mine.a, g);
-                            const float from = value_of(least) - (2.f * slack + 2.f * kUlp * fminf(fabsf(value_of(least)), kLargest));
-#pragma unroll
-                            for (int i = 0; i < R; ++i)
-                                if (e0 + i >= g * size && e0 + i < (g + 1) * size && (by_logit ? key[i] >= least : value_of(key[i]) >= from)) cand |= 1u << i;
-                        }
-                        const double exact = exact_groups(a, row, e0, R, top, cand, doubt);
-                        kept = best_groups((doubt >> lane) & 1 ? exact : (double)v, a.groups, a.top_groups, lane);
-                    }
-                }
-            }
-            if (whole) {
-                const bool off = !((kept >> (lane >> (31 - __clz(lanes)))) & 1);      // (lanes past the last group hold nothing)
-#pragma unroll
-                for (int i = 0; i < R; ++i) key[i] = off ? 0u : key[i];
-#pragma unroll
-                for (int i = 0; i < kDepth<R>; ++i) list[i] = off ? 0u : list[i];
-            } else {
+            for (int d = 1; d < 32; d <<= 1)
+                if (d < lanes) p = merge(p, Pair{__shfl_xor_sync(QMOE_FULL_MASK, p.a, d), __shfl_xor_sync(QMOE_FULL_MASK, p.b, d)});
+            mine = Pair{__shfl_sync(QMOE_FULL_MASK, p.a, lane * lanes & 31), __shfl_sync(QMOE_FULL_MASK, p.b, lane * lanes & 31)};
+        } else {
+            for (int g = 0; g < a.groups; ++g) {
+                Pair p{0, 0};
 #pragma unroll
                 for (int i = 0; i < R; ++i)
-                    if (e0 + i < a.E && !((kept >> ((e0 + i) / size)) & 1)) key[i] = 0u;
-                best_keys<R>(key, list);
+                    if (e0 + i >= g * size && e0 + i < (g + 1) * size) p = merge(p, Pair{key[i], 0});
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) p = merge(p, Pair{__shfl_xor_sync(QMOE_FULL_MASK, p.a, d), __shfl_xor_sync(QMOE_FULL_MASK, p.b, d)});
+                if (lane == g) mine = p;
             }
+        }
+        uint32_t kept;
+        if (by_logit && a.best == 1) {
+            kept = best_groups(mine.a, a.groups, a.top_groups, lane);
+        } else {
+            float va = value_of(mine.a), vb = a.best == 2 ? value_of(mine.b) : 0.f;
+            if (by_logit) va = score_near(va), vb = score_near(vb);      // (sums of scores)
+            const bool on = lane < a.groups;
+            const float v = on ? fmaxf(va + vb, -INFINITY) : -INFINITY;
+            kept = best_groups(v, a.groups, a.top_groups, lane);
+            if (a.top_groups < a.groups) {
+                // the last one kept and the best one dropped
+                const float mag = fabsf(va) + fabsf(vb);
+                const float err = on ? 2.f * score_err + (mag < kLargest ? 2.f * kUlp * mag : 0.f) : 0.f;
+                const bool is = (kept >> lane) & 1;
+                const float low = value_of(~__reduce_max_sync(QMOE_FULL_MASK, is ? ~key_of(v) : 0u));
+                const float high = value_of(__reduce_max_sync(QMOE_FULL_MASK, on && !is ? key_of(v) : 0u));
+                const float err2 = 2.f * __uint_as_float(__reduce_max_sync(QMOE_FULL_MASK, __float_as_uint(err)));
+                // (infinite ones are equal or not, whatever the bits: NaN here)
+                if (__builtin_expect(low - high <= err2, 0)) {
+                    const uint32_t doubt = __ballot_sync(QMOE_FULL_MASK, on && v >= high - err2 && v <= low + err2);
+                    // the experts that may be among the best of those groups
+                    uint32_t cand = 0;
+                    for (uint32_t todo = doubt; todo; todo &= todo - 1) {
+                        const int g = __ffs(todo) - 1;
+                        const uint32_t least = __shfl_sync(QMOE_FULL_MASK, a.best == 2 ? mine.b : mine.a, g);
+                        const float from = value_of(least) - (2.f * slack + 2.f * kUlp * fminf(fabsf(value_of(least)), kLargest));
+#pragma unroll
+                        for (int i = 0; i < R; ++i)
+                            if (e0 + i >= g * size && e0 + i < (g + 1) * size && (by_logit ? key[i] >= least : value_of(key[i]) >= from)) cand |= 1u << i;
+                    }
+                    const double exact = exact_groups(a, row, e0, R, top, cand, doubt);
+                    kept = best_groups((doubt >> lane) & 1 ? exact : (double)v, a.groups, a.top_groups, lane);
+                }
+            }
+        }
+        if (whole) {
+            const bool off = !((kept >> (lane >> (31 - __clz(lanes)))) & 1);      // (lanes past the last group hold nothing)
+#pragma unroll
+            for (int i = 0; i < R; ++i) key[i] = off ? 0u : key[i];
+#pragma unroll
+            for (int i = 0; i < kDepth<R>; ++i) list[i] = off ? 0u : list[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                if (e0 + i < a.E && !((kept >> ((e0 + i) / size)) & 1)) key[i] = 0u;
+            best_keys<R>(key, list);
         }
     }
     // ---- the k best, and the next one where the values are not exact
     const int rounds = min(a.k + (by_logit ? 0 : 1), 32);
     uint32_t mk;
-    int at;
-    int from;
+    int at, from;
     const bool had = list[0] != 0;
     choose(list, rounds, lane, &mk, &from);
     if (__builtin_expect(ran_out<R>(key, list, had, rounds, mk), 0)) {
@@ -830,141 +813,116 @@ __global__ void __launch_bounds__((NW == 1 ? kTokenWarps : kRouteWarps) * 32, NW
     } else {
         at = which<R>(key, mk, from, lane);
     }
-    if constexpr (NW > 1) {
-        key_s[warp * 32 + lane] = lane < rounds ? mk : 0u;
-        id_s[warp * 32 + lane] = lane < rounds && mk ? warp * 32 * R + at : 0;
-        __syncthreads();
-        if (warp == 0) {
-            // the warps' lists one behind the other, eight entries a lane: lower lanes hold lower experts among equal keys
-            uint32_t keys[8], sorted[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sorted[i] = keys[i] = key_s[lane * 8 + i];      // (a part of a warp's list: in order already)
-            choose(sorted, rounds, lane, &mk, &from);
-            at = id_s[which<8>(keys, mk, from, lane)];
-        }
-    }
     // ---- the chosen ones' logits, and neighbours that are too near to tell
-    bool again = false;       // ... among more experts than the list holds
-    float l = -INFINITY, last = 0.f;
-    if (NW == 1 || warp == 0) {
-        const bool in_list = lane < rounds && mk;
-        if (!in_list) at = 0;
-        if (in_list) l = logit(row, at);
-        if (!by_logit) {
-            const Doubts d = doubts_of(a, mk, at, l, slack, lane);
-            if (__builtin_expect(d.any || a.k == 32, 0)) {
-                last = d.last;
-                // experts outside the list that may belong into it: a block decides all of its doubts together
-                again = NW > 1;
-                if (NW == 1) {
-                    int may = 0;
+    const bool in_list = lane < rounds && mk;
+    if (!in_list) at = 0;
+    float l = in_list ? logit(row, at) : -INFINITY;
+    if (!by_logit) {
+        const Doubts d = doubts_of(a, mk, at, l, slack, lane);
+        if (__builtin_expect(d.any || a.k == 32, 0)) {
+            // experts outside the list that may belong into it: values down to the last one's less the errors
+            uint32_t cand = 0;
 #pragma unroll
-                    for (int i = 0; i < R; ++i) may += key[i] && !(value_of(key[i]) < d.least);
-                    again = warp_sum_int(may) > __popc(__ballot_sync(QMOE_FULL_MASK, in_list && !(value_of(mk) < d.least)));
-                    if (!again && d.any) {
-                        const double z64 = exact_sum<X, 1>(a, row, e0, R, top, nullptr);
-                        at = exact_order(a, row, __popc(__ballot_sync(QMOE_FULL_MASK, in_list)), value_of(mk), at, d.mine, top, z64);
-                        if (in_list) l = logit(row, at);
-                    }
-                }
+            for (int i = 0; i < R; ++i)
+                if (key[i] && !(value_of(key[i]) < d.least)) cand |= 1u << i;
+            if (warp_sum_int(__popc(cand)) > __popc(__ballot_sync(QMOE_FULL_MASK, in_list && !(value_of(mk) < d.least)))) {
+                at = exact_choice<X, 1>(a, row, e0, R, top, cand, nullptr);
+                if (lane < a.k) l = logit(row, at);
+            } else if (d.any) {
+                const double z64 = exact_sum<X, 1>(a, row, e0, R, top, nullptr);
+                at = exact_order(a, row, __popc(__ballot_sync(QMOE_FULL_MASK, in_list)), value_of(mk), at, d.mine, top, z64);
+                if (in_list) l = logit(row, at);
             }
         }
     }
-    if (NW > 1 && !by_logit) {
-        if (warp == 0 && lane == 0) bound_s = make_float2(again ? 1.f : 0.f, last);
-        __syncthreads();
-        again = bound_s.x != 0.f, last = bound_s.y;
-    }
-    if (__builtin_expect(again, 0)) {
-        // what may be among the chosen: values down to the k-th's less the errors
-        const float least = last - (2.f * slack + 4.f * kUlp * fminf(fabsf(last), kLargest));
-        using Bits = std::conditional_t<(R > 32), unsigned long long, uint32_t>;
-        Bits cand = 0;
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            if (key[i] && !(value_of(key[i]) < least)) cand |= (Bits)1 << i;
-        at = exact_choice<X, NW, Bits>(a, row, e0, R, top, cand, &rs);
-        if (lane < a.k) l = logit(row, at);
-    }
-    if (NW == 1 || warp == 0) write_route(a, t, at, l, top, z, lane);
+    write_route(a, t, at, l, top, z, lane);
 }
 
-// Many experts without groups: a warp a token, 32 R experts in loads that stand side by side.  The `rounds`-th largest of the
-// lanes' maxima bounds the values to look at from below; the few that reach it are put side by side in shared memory, and
-// the rounds go over those, by key and index.
+// Many experts without groups: a block of 4 warps a token, R values a thread in loads that stand side by side.  In each warp
+// the `rounds`-th largest of the lanes' maxima bounds the values to look at from below, and the largest of the warps' bounds
+// does for all; the few values that reach it are put side by side in shared memory, and the first warp's rounds go over
+// those, by key and index.
 constexpr int kWideMost = 256;      // values put side by side; rows with more (many equal ones) take exact_choice
 
 template <typename X, int R>
-__global__ void __launch_bounds__(kTokenWarps * 32, R <= 16 ? 8 : R <= 32 ? 6 : 4) wide_route_kernel(RouteArgs a) {
-    constexpr int V = 16 / (int)sizeof(X);
-    __shared__ uint32_t key_s[kTokenWarps][kWideMost];
-    __shared__ int id_s[kTokenWarps][kWideMost];
-    __shared__ float value_s[kTokenWarps][R / 8][2][128];
-    __shared__ int count_s[kTokenWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = (int64_t)blockIdx.x * kTokenWarps + warp;
-    if (t >= a.T) return;
+__global__ void __launch_bounds__(kWideWarps * 32, R <= 16 ? 8 : R <= 32 ? 5 : 3) wide_route_kernel(RouteArgs a) {
+    constexpr int V = 16 / (int)sizeof(X), THREADS = kWideWarps * 32, CHUNK = R < 8 ? R : 8;
+    __shared__ ResolveShared rs;
+    __shared__ uint32_t key_s[kWideMost], bound_s[kWideWarps];
+    __shared__ int id_s[kWideMost], count_s, again_s;
+    __shared__ float2 part_s[kWideWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t t = blockIdx.x;
     const X* row = (const X*)a.logits + t * a.stride;
     // expert of value i
-    auto expert = [&](int i) { return a.vec ? (i / V) * (32 * V) + lane * V + i % V : i * 32 + lane; };
+    auto expert = [&](int i) { return a.vec ? (i / V) * (THREADS * V) + tid * V + i % V : i * THREADS + tid; };
     float c[R];
     if (a.vec) {
 #pragma unroll
         for (int i = 0; i < R; i += V) {
             float v[V];
-            load_values<X, V>(row, i * 32 + lane * V, a.E, 1, -INFINITY, v);
+            load_values<X, V>(row, expert(i), a.E, 1, -INFINITY, v);
 #pragma unroll
-            for (int j = 0; j < V; ++j) c[i + j] = clean(v[j]);
+            for (int j = 0; j < V; ++j)
+                if (i + j < R) c[i + j] = clean(v[j]);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < R; ++i) c[i] = i * 32 + lane < a.E ? logit(row, i * 32 + lane) : -INFINITY;
+        for (int i = 0; i < R; ++i) c[i] = i * THREADS + tid < a.E ? logit(row, i * THREADS + tid) : -INFINITY;
     }
+    if (tid == 0) count_s = 0;
     const bool by_logit = !a.bias;
-    float top = 0.f, z = 1.f, inv_z = 1.f, slack = 0.f;
+    float top = 0.f, z = 1.f, inv_z = 1.f, scale = 1.f;
     if (!a.sigmoid && !(by_logit && a.renorm)) {
-        top = c[0];
+        // a warp's exponentials are by its own largest logit until the block's is known
+        float mine = c[0];
 #pragma unroll
-        for (int i = 1; i < R; ++i) top = fmaxf(top, c[i]);
+        for (int i = 1; i < R; ++i) mine = fmaxf(mine, c[i]);
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(QMOE_FULL_MASK, top, d));
-        if (!(top > -INFINITY)) top = 0.f;       // nothing in the row: scores 0
+        for (int d = 16; d > 0; d >>= 1) mine = fmaxf(mine, __shfl_xor_sync(QMOE_FULL_MASK, mine, d));
+        const float by = mine > -INFINITY ? mine : 0.f;
         float part[4] = {};
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const float e = ex2(kLog2e * (c[i] - top));
+            const float e = ex2(kLog2e * (c[i] - by));
             part[i & 3] += e;
             if (!by_logit) c[i] = e;
         }
-        z = warp_sum((part[0] + part[1]) + (part[2] + part[3]));
+        const float sum = warp_sum((part[0] + part[1]) + (part[2] + part[3]));
+        if (lane == 0) part_s[warp] = make_float2(mine, sum);
+        __syncthreads();
+        const float2 p0 = part_s[0], p1 = part_s[1], p2 = part_s[2], p3 = part_s[3];
+        top = fmaxf(fmaxf(p0.x, p1.x), fmaxf(p2.x, p3.x));
+        if (!(top > -INFINITY)) top = 0.f;       // nothing in the row: scores 0
+        z = fmaf(p0.y, ex2(kLog2e * (p0.x - top)), p1.y * ex2(kLog2e * (p1.x - top))) + fmaf(p2.y, ex2(kLog2e * (p2.x - top)), p3.y * ex2(kLog2e * (p3.x - top)));
         if (!(z > 0.f)) z = 1.f;
-        inv_z = rcp(z);
+        inv_z = rcp(z), scale = mine > -INFINITY ? ex2(kLog2e * (by - top)) * inv_z : 0.f;
     }
+    const float slack = by_logit ? 0.f : error_bound(a, R, inv_z);
     if (!by_logit) {
-        slack = fmaf(a.sigmoid ? 6.f : (float)(R / 4 + 64) * inv_z, kUlp, 1e-37f);      // (as in route_kernel)
+        if (a.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < R; i += V) {
-            float bias[V];
+            for (int i = 0; i < R; ++i) c[i] = sigmoid_near(c[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < R; i += 4) {
+            float bias[4];
             if (a.vec && a.vec_bias) {
-                load_values<float, V>(a.bias, i * 32 + lane * V, a.E, 1, 0.f, bias);
+                load_values<float, 4>(a.bias, expert(i), a.E, 1, 0.f, bias);
             } else {
 #pragma unroll
-                for (int j = 0; j < V; ++j) bias[j] = expert(i + j) < a.E ? a.bias[expert(i + j)] : 0.f;
+                for (int j = 0; j < 4; ++j) bias[j] = expert(i + j) < a.E ? a.bias[expert(i + j)] : 0.f;
             }
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float s = a.sigmoid ? sigmoid_near(c[i + j]) : c[i + j] * inv_z;
-                c[i + j] = fmaxf(s + bias[j], -INFINITY);
-            }
+            for (int j = 0; j < 4; ++j) c[i + j] = fmaxf(fmaf(c[i + j], scale, bias[j]), -INFINITY);
         }
-        if (a.E < 32 * R) {
+        if (a.E < THREADS * R) {
 #pragma unroll
             for (int i = 0; i < R; ++i)
                 if (expert(i) >= a.E) c[i] = -INFINITY;
         }
     }
     // ---- the lanes' largest values, and the `rounds`-th of them
-    constexpr int CHUNK = 8;
     float chunk[R / CHUNK], mine = -INFINITY;
 #pragma unroll
     for (int i = 0; i < R / CHUNK; ++i) {
@@ -980,108 +938,102 @@ __global__ void __launch_bounds__(kTokenWarps * 32, R <= 16 ? 8 : R <= 32 ? 6 : 
         const int w = __ffs(__ballot_sync(QMOE_FULL_MASK, head == bound)) - 1;
         if (lane == w) head = 0;
     }
+    if (lane == 0) bound_s[warp] = bound;
+    __syncthreads();
+    bound = max(max(bound_s[0], bound_s[1]), max(bound_s[2], bound_s[3]));
     const float from = value_of(bound);
-    // a lane's chunks that reach it go through shared memory, so that the code that looks at one is there once
-    uint32_t hits = 0;
 #pragma unroll
     for (int i = 0; i < R / CHUNK; ++i) {
         if (chunk[i] >= from) {
-            hits |= 1u << i;
 #pragma unroll
-            for (int j = 0; j < CHUNK; j += 4)
-                *(float4*)&value_s[warp][i][j / 4][lane * 4] = make_float4(c[i * CHUNK + j], c[i * CHUNK + j + 1], c[i * CHUNK + j + 2], c[i * CHUNK + j + 3]);
-        }
-    }
-    if (lane == 0) count_s[warp] = 0;
-    __syncwarp();
-    for (; hits; hits &= hits - 1) {
-        const int i = __ffs(hits) - 1;
-#pragma unroll 1
-        for (int j = 0; j < CHUNK; ++j) {
-            const float v = value_s[warp][i][j >> 2][lane * 4 + (j & 3)];
-            const int e = expert(i * CHUNK + j);
-            if (v >= from && e < a.E) {
-                const int at = atomicAdd(&count_s[warp], 1);      // (their order does not matter)
-                if (at < kWideMost) key_s[warp][at] = key_of(v), id_s[warp][at] = e;
-            }
-        }
-    }
-    __syncwarp();
-    const int n = count_s[warp];
-    bool again = n > kWideMost;
-    uint32_t mk = 0;
-    int at = 0;
-    float l = -INFINITY;
-    if (!again) {
-        constexpr int MOST = kWideMost / 32;
-        uint32_t key[MOST];
-        int id[MOST];
-        const int mine_n = (n + 31) / 32;
-#pragma unroll
-        for (int i = 0; i < MOST; ++i) {
-            key[i] = 0, id[i] = 0;
-            if (i * 32 + lane < n) key[i] = key_s[warp][i * 32 + lane], id[i] = id_s[warp][i * 32 + lane];
-        }
-        for (int j = 0; j < rounds; ++j) {
-            uint32_t best = key[0];
-            int e = id[0];
-            if (mine_n > 1) {
-#pragma unroll
-                for (int i = 1; i < MOST; ++i)
-                    if (key[i] > best || (key[i] == best && id[i] < e)) best = key[i], e = id[i];
-            }
-            const uint32_t m = __reduce_max_sync(QMOE_FULL_MASK, best);
-            const int first = (int)__reduce_min_sync(QMOE_FULL_MASK, best == m ? (unsigned)e : 0xFFFFFFFFu);
-            if (lane == j) mk = m, at = first;
-#pragma unroll
-            for (int i = 0; i < MOST; ++i) {
-                if (i > 0 && mine_n == 1) break;
-                if (key[i] == m && id[i] == first) key[i] = 0;
-            }
-        }
-        const bool in_list = lane < rounds && mk;
-        if (!in_list) at = 0;
-        if (in_list) l = logit(row, at);
-        if (!by_logit) {
-            const Doubts d = doubts_of(a, mk, at, l, slack, lane);
-            if (__builtin_expect(d.any || a.k == 32, 0)) {
-                int may = 0;
-#pragma unroll
-                for (int i = 0; i < R; ++i) may += expert(i) < a.E && !(c[i] < d.least);
-                again = warp_sum_int(may) > __popc(__ballot_sync(QMOE_FULL_MASK, in_list && !(value_of(mk) < d.least)));
-                if (!again && d.any) {
-                    const double z64 = exact_sum<X, 1>(a, row, lane * R, R, top, nullptr);
-                    at = exact_order(a, row, __popc(__ballot_sync(QMOE_FULL_MASK, in_list)), value_of(mk), at, d.mine, top, z64);
-                    if (in_list) l = logit(row, at);
+            for (int j = 0; j < CHUNK; ++j) {
+                const int e = expert(i * CHUNK + j);
+                if (c[i * CHUNK + j] >= from && e < a.E) {
+                    const int at = atomicAdd(&count_s, 1);      // (their order does not matter)
+                    if (at < kWideMost) key_s[at] = key_of(c[i * CHUNK + j]), id_s[at] = e;
                 }
             }
         }
     }
-    if (__builtin_expect(again, 0)) {
-        using Bits = std::conditional_t<(R > 32), unsigned long long, uint32_t>;
-        const int have = min(max(a.E - lane * R, 0), R);      // all of the row, R neighbouring experts a lane
-        const Bits cand = have == 0 ? 0 : ~(Bits)0 >> (8 * sizeof(Bits) - have);
-        at = exact_choice<X, 1, Bits>(a, row, lane * R, R, top, cand, nullptr);
-        if (lane < a.k) l = logit(row, at);
+    __syncthreads();
+    bool again = false;
+    int at = 0;
+    float l = -INFINITY;
+    if (warp == 0) {
+        const int n = count_s;
+        again = n > kWideMost;
+        if (!again) {
+            constexpr int MOST = kWideMost / 32;
+            uint32_t key[MOST], mk = 0;
+            int id[MOST];
+            const int mine_n = (n + 31) / 32;
+#pragma unroll
+            for (int i = 0; i < MOST; ++i) {
+                key[i] = 0, id[i] = 0;
+                if (i * 32 + lane < n) key[i] = key_s[i * 32 + lane], id[i] = id_s[i * 32 + lane];
+            }
+            for (int j = 0; j < rounds; ++j) {
+                uint32_t best = key[0];
+                int e = id[0];
+                if (mine_n > 1) {
+#pragma unroll
+                    for (int i = 1; i < MOST; ++i)
+                        if (key[i] > best || (key[i] == best && id[i] < e)) best = key[i], e = id[i];
+                }
+                const uint32_t m = __reduce_max_sync(QMOE_FULL_MASK, best);
+                const int first = (int)__reduce_min_sync(QMOE_FULL_MASK, best == m ? (unsigned)e : 0xFFFFFFFFu);
+                if (lane == j) mk = m, at = first;
+#pragma unroll
+                for (int i = 0; i < MOST; ++i) {
+                    if (i > 0 && mine_n == 1) break;
+                    if (key[i] == m && id[i] == first) key[i] = 0;
+                }
+            }
+            const bool in_list = lane < rounds && mk;
+            if (!in_list) at = 0;
+            if (in_list) l = logit(row, at);
+            if (!by_logit) {
+                again = doubts_of(a, mk, at, l, slack, lane).any;
+                if (a.k == 32) {
+                    // the list has no entry for the next one: the largest that is left, or what none of the others reaches
+                    uint32_t rest = 0;
+#pragma unroll
+                    for (int i = 0; i < MOST; ++i) rest = max(rest, key[i]);
+                    rest = __reduce_max_sync(QMOE_FULL_MASK, rest);
+                    const float last = value_of(__shfl_sync(QMOE_FULL_MASK, mk, 31)), next = rest ? value_of(rest) : from;
+                    again |= !(last - next > 2.f * slack + 2.f * kUlp * fmaxf(fabsf(last), fabsf(next)));
+                }
+            }
+        }
+        if (lane == 0) again_s = again;
     }
-    write_route(a, t, at, l, top, z, lane);
+    if (by_logit ? count_s > kWideMost : true) {
+        __syncthreads();
+        if (__builtin_expect(again_s, 0)) {
+            using Bits = std::conditional_t<(R > 32), unsigned long long, uint32_t>;
+            const int have = min(max(a.E - tid * R, 0), R);      // all of the row, R neighbouring experts a thread
+            const Bits cand = have == 0 ? 0 : ~(Bits)0 >> (8 * sizeof(Bits) - have);
+            at = exact_choice<X, kWideWarps>(a, row, tid * R, R, top, cand, &rs);
+            if (lane < a.k) l = logit(row, at);
+        }
+    }
+    if (warp == 0) write_route(a, t, at, l, top, z, lane);
 }
 
 template <typename X>
 int launch_route(const RouteArgs& a, cudaStream_t st) {
-    const unsigned per_warp = (unsigned)((a.T + kTokenWarps - 1) / kTokenWarps);
-    constexpr int threads = kTokenWarps * 32;
-    if (a.E <= 32) route_kernel<X, 1, 1><<<per_warp, threads, 0, st>>>(a);
-    else if (a.E <= 64) route_kernel<X, 2, 1><<<per_warp, threads, 0, st>>>(a);
-    else if (a.E <= 128) route_kernel<X, 4, 1><<<per_warp, threads, 0, st>>>(a);
-    else if (a.E <= 256) route_kernel<X, 8, 1><<<per_warp, threads, 0, st>>>(a);
-    else if (a.groups > 1 && a.E <= 512) route_kernel<X, 16, 1><<<per_warp, threads, 0, st>>>(a);
-    else if (a.groups > 1) route_kernel<X, 32, 1><<<per_warp, threads, 0, st>>>(a);
-    else if (a.E <= 512) wide_route_kernel<X, 16><<<per_warp, threads, 0, st>>>(a);
-    else if (a.E <= 1024) wide_route_kernel<X, 32><<<per_warp, threads, 0, st>>>(a);
-    else if (a.E <= 2048) wide_route_kernel<X, 64><<<per_warp, threads, 0, st>>>(a);
-    else if (a.E <= 4096) route_kernel<X, 16, kRouteWarps><<<(unsigned)a.T, kRouteWarps * 32, 0, st>>>(a);
-    else route_kernel<X, 32, kRouteWarps><<<(unsigned)a.T, kRouteWarps * 32, 0, st>>>(a);
+    const unsigned per_warp = (unsigned)((a.T + kTokenWarps - 1) / kTokenWarps), tokens = (unsigned)a.T;
+    constexpr int threads = kTokenWarps * 32, wide = kWideWarps * 32;
+    if (a.E <= 32) route_kernel<X, 1><<<per_warp, threads, 0, st>>>(a);
+    else if (a.E <= 64) route_kernel<X, 2><<<per_warp, threads, 0, st>>>(a);
+    else if (a.E <= 128) route_kernel<X, 4><<<per_warp, threads, 0, st>>>(a);
+    else if (a.E <= 256) route_kernel<X, 8><<<per_warp, threads, 0, st>>>(a);
+    else if (a.groups > 1 && a.E <= 512) route_kernel<X, 16><<<per_warp, threads, 0, st>>>(a);
+    else if (a.groups > 1) route_kernel<X, 32><<<per_warp, threads, 0, st>>>(a);
+    else if (a.E <= 1024) wide_route_kernel<X, 8><<<tokens, wide, 0, st>>>(a);
+    else if (a.E <= 2048) wide_route_kernel<X, 16><<<tokens, wide, 0, st>>>(a);
+    else if (a.E <= 4096) wide_route_kernel<X, 32><<<tokens, wide, 0, st>>>(a);
+    else wide_route_kernel<X, 64><<<tokens, wide, 0, st>>>(a);
     return qmoe::launch_check("qmoe_route_scored");
 }
 
