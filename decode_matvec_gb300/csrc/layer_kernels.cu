@@ -845,7 +845,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32, R <= 8 ? 8 : 4) route_kernel
 constexpr int kWideMost = 256;      // values put side by side; rows with more (many equal ones) take exact_choice
 
 template <typename X, int R>
-__global__ void __launch_bounds__(kWideWarps * 32, R <= 16 ? 8 : R <= 32 ? 5 : 3) wide_route_kernel(RouteArgs a) {
+__global__ void __launch_bounds__(kWideWarps * 32, R <= 16 ? 10 : R <= 32 ? 5 : 3) wide_route_kernel(RouteArgs a) {
     constexpr int V = 16 / (int)sizeof(X), THREADS = kWideWarps * 32, CHUNK = R < 8 ? R : 8;
     __shared__ ResolveShared rs;
     __shared__ uint32_t key_s[kWideMost], bound_s[kWideWarps];
