@@ -134,10 +134,11 @@ __device__ __forceinline__ float largest(const Values<8>& v) {
 }
 
 // 8 codes of y / s for s = m / 448, which is returned.  A power of two brings m next to 1 (whatever its exponent: no value
-// overflows or loses bits on the way), and 448 / m is within two steps of the quotient's last place, before a rounding to 4 bits.
+// overflows or loses bits on the way); 448 / m is correctly rounded, as an error of it would move all the run's codes next to the middle
+// of two values.
 __device__ __forceinline__ float store_codes(uint8_t* dst, const Values<8>& y, float m) {
     const float g = __uint_as_float(max((254u << 23) - (__float_as_uint(m) & 0x7F800000u), 1u << 23));
-    const float inv = m == 0.f ? 0.f : __fdividef(448.f, m * g);
+    const float inv = m == 0.f ? 0.f : __fdiv_rn(448.f, m * g);
     uint32_t w[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -354,8 +355,9 @@ __device__ __forceinline__ float rcp(float x) {
 }
 // Bound on a score's error: sigmoid_near's; or, with x = l - top, (2.5 |x| + 4) 2^-24 of itself from an exponential (|x| e^x <=
 // 0.37), the same of the sum (|x| weighed by the scores is at most ln E) and R / 4 + 17 additions, and 9 of a quotient and factors.
+__device__ __forceinline__ float sum_error(int R) { return (float)(R / 4 + 70) * kUlp; }      // (of itself)
 __device__ __forceinline__ float error_bound(const RouteArgs& a, int R, float inv_z) {
-    return fmaf(a.sigmoid ? 6.f : (float)(R / 4 + 70) * inv_z, kUlp, 1e-37f);
+    return (a.sigmoid ? 6.f * kUlp : sum_error(R) * inv_z) + 1e-37f;
 }
 
 // Within 6 2^-24: (1.5 |l| + 4) 2^-24 of the exponential, which the score's slope s (1 - s) makes 1.4, and 3 of the rest.
@@ -602,22 +604,38 @@ __device__ __noinline__ int exact_choice(const RouteArgs& a, const X* row, int e
     return got;
 }
 
-// The list of lanes 0 .. n - 1 in the order of its values, those of lanes with `near` in 64 bits.
+// The list of lanes 0 .. n - 1 in the order of its values, those of lanes with `near` from scores in 64 bits.  The softmax's sum stays
+// the fp32 one (256 exponentials in fp64 take 3 us here, 2048 some 22), within `error` of itself: that moves the difference of two
+// values by so much of their scores' difference, which is no more than their biases'.  -1 where that still leaves a doubt.
 template <typename X>
-__device__ __noinline__ int exact_order(const RouteArgs& a, const X* row, int n, float value, int at, bool near, float top, double z) {
+__device__ __noinline__ int exact_order(const RouteArgs& a, const X* row, int n, float value, int mine, bool near, float top, float z, float error) {
     const int lane = threadIdx.x & 31;
-    const unsigned long long c = key_of(near ? exact_value(a, row, at, top, z) : (double)value);
-    int rank = 0, got = at;
-    for (int j = 0; j < n; ++j) {
-        const unsigned long long o = __shfl_sync(QMOE_FULL_MASK, c, j);
-        const int e = __shfl_sync(QMOE_FULL_MASK, at, j);
-        rank += o > c || (o == c && e < at);
+    double c = (double)value, p = 0.0;
+    if (near) {
+        const double l = logit(row, mine);
+        p = l > -INFINITY ? a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / (double)z : 0.0;
+        c = p + (double)a.bias[mine];
     }
+    const unsigned long long key = key_of(c);
+    int rank = 0, from = lane;
     for (int j = 0; j < n; ++j) {
-        const int r = __shfl_sync(QMOE_FULL_MASK, rank, j), e = __shfl_sync(QMOE_FULL_MASK, at, j);
-        if (r == lane) got = e;
+        const unsigned long long o = __shfl_sync(QMOE_FULL_MASK, key, j);
+        const int e = __shfl_sync(QMOE_FULL_MASK, mine, j);      // (outside the condition: every lane takes part)
+        rank += o > key || (o == key && e < mine);
     }
-    return got;
+    for (int j = 0; j < n; ++j)
+        if (__shfl_sync(QMOE_FULL_MASK, rank, j) == lane) from = j;
+    // neighbours in the new order (the same logit and bias give the same bits; infinite values are equal or not)
+    bool sure = true;
+    if (!a.sigmoid) {
+        c = __shfl_sync(QMOE_FULL_MASK, c, from), p = __shfl_sync(QMOE_FULL_MASK, p, from);
+        near = __shfl_sync(QMOE_FULL_MASK, (int)near, from) != 0;
+        const double o = __shfl_down_sync(QMOE_FULL_MASK, c, 1), q = __shfl_down_sync(QMOE_FULL_MASK, p, 1);
+        const bool both = __shfl_down_sync(QMOE_FULL_MASK, (int)near, 1) != 0 && near && lane + 1 < n;
+        sure = !both || (o == c && q == p) || c - o > fabs(q - p) * (double)error + 4e-16 * (fabs(o) + fabs(c));
+    }
+    const int got = __shfl_sync(QMOE_FULL_MASK, mine, from);
+    return __all_sync(QMOE_FULL_MASK, sure) ? got : -1;
 }
 
 // Gates of the experts that lanes 0 .. k - 1 hold (l: their logits), and the outputs of token t.  Renormalised weights are taken
@@ -825,14 +843,13 @@ __global__ void __launch_bounds__(kTokenWarps * 32, R <= 8 ? 8 : 4) route_kernel
 #pragma unroll
             for (int i = 0; i < R; ++i)
                 if (key[i] && !(value_of(key[i]) < d.least)) cand |= 1u << i;
-            if (warp_sum_int(__popc(cand)) > __popc(__ballot_sync(QMOE_FULL_MASK, in_list && !(value_of(mk) < d.least)))) {
-                at = exact_choice<X, 1>(a, row, e0, R, top, cand, nullptr);
-                if (lane < a.k) l = logit(row, at);
-            } else if (d.any) {
-                const double z64 = exact_sum<X, 1>(a, row, e0, R, top, nullptr);
-                at = exact_order(a, row, __popc(__ballot_sync(QMOE_FULL_MASK, in_list)), value_of(mk), at, d.mine, top, z64);
-                if (in_list) l = logit(row, at);
+            bool again = warp_sum_int(__popc(cand)) > __popc(__ballot_sync(QMOE_FULL_MASK, in_list && !(value_of(mk) < d.least)));
+            if (!again && d.any) {
+                at = exact_order(a, row, __popc(__ballot_sync(QMOE_FULL_MASK, in_list)), value_of(mk), at, d.mine, top, z, sum_error(R));
+                again = at < 0;
             }
+            if (again) at = exact_choice<X, 1>(a, row, e0, R, top, cand, nullptr);
+            if (lane < a.k) l = logit(row, at);
         }
     }
     write_route(a, t, at, l, top, z, lane);
@@ -941,7 +958,8 @@ __global__ void __launch_bounds__(kWideWarps * 32, R <= 16 ? 10 : R <= 32 ? 5 : 
     if (lane == 0) bound_s[warp] = bound;
     __syncthreads();
     bound = max(max(bound_s[0], bound_s[1]), max(bound_s[2], bound_s[3]));
-    const float from = value_of(bound);
+    // (less the errors, as doubts_of takes off the last one chosen: what may belong to the chosen is in the list)
+    const float reach = value_of(bound), from = by_logit ? reach : reach - (2.f * slack + 4.f * kUlp * fminf(fabsf(reach), kLargest));
 #pragma unroll
     for (int i = 0; i < R / CHUNK; ++i) {
         if (chunk[i] >= from) {
@@ -993,15 +1011,17 @@ __global__ void __launch_bounds__(kWideWarps * 32, R <= 16 ? 10 : R <= 32 ? 5 : 
             if (!in_list) at = 0;
             if (in_list) l = logit(row, at);
             if (!by_logit) {
-                again = doubts_of(a, mk, at, l, slack, lane).any;
-                if (a.k == 32) {
-                    // the list has no entry for the next one: the largest that is left, or what none of the others reaches
-                    uint32_t rest = 0;
+                const Doubts d = doubts_of(a, mk, at, l, slack, lane);
+                if (__builtin_expect(d.any || a.k == 32, 0)) {
+                    uint32_t rest = 0;      // the largest that is left
 #pragma unroll
                     for (int i = 0; i < MOST; ++i) rest = max(rest, key[i]);
-                    rest = __reduce_max_sync(QMOE_FULL_MASK, rest);
-                    const float last = value_of(__shfl_sync(QMOE_FULL_MASK, mk, 31)), next = rest ? value_of(rest) : from;
-                    again |= !(last - next > 2.f * slack + 2.f * kUlp * fmaxf(fabsf(last), fabsf(next)));
+                    again = __any_sync(QMOE_FULL_MASK, rest && !(value_of(rest) < d.least));
+                    if (!again && d.any) {
+                        at = exact_order(a, row, __popc(__ballot_sync(QMOE_FULL_MASK, in_list)), value_of(mk), at, d.mine, top, z, sum_error(R));
+                        again = at < 0;
+                        if (in_list && !again) l = logit(row, at);
+                    }
                 }
             }
         }
