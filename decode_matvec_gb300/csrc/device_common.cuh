@@ -70,6 +70,33 @@ constexpr int kPlanMaxE = 8192;
 // Records phase event i on st when the measurement hook is set.
 void phase_event(int i, cudaStream_t st);
 
+// Programmatic dependent launch: a kernel begins while the one before it in the stream still runs.  It waits (depend_wait) before it
+// touches what earlier kernels read or wrote, and lets the next one begin (depend_launch) after that, so that whatever begins has all
+// but its immediate predecessor behind it.
+__device__ __forceinline__ void depend_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void depend_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename T>
+struct Same {
+    using type = T;
+};
+
+// Launches a kernel that may start while the one before it in the stream still runs (it waits itself, by depend_wait).
+template <typename... Args>
+inline int launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t st, const char* who, typename Same<Args>::type... args) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return qmoe::cuda_check(cudaLaunchKernelEx(&cfg, kernel, args...), who);
+}
+
 }  // namespace qmoe
 
 // ---------------------------------------------------------------- numerics

@@ -304,6 +304,7 @@ __global__ void __launch_bounds__(kDecodeThreads, NT <= 2 ? 3 : 2)
     }
     long long chunk = 1, u0, u1;
     Found f;
+    if (kSel) depend_wait();
     depend_launch();
     if (direct) {
         // a block an item: few tiles each, and nothing to join
@@ -1761,14 +1762,21 @@ int launch_decode(const AttnArgs& a, void* ws, cudaStream_t st) {
     // 4 8.7 / 9.2, 5 9.5 / 9.0.  More items cross later (8 requests of 32/8 heads: 6 9.6 / 10.6, 8 11.2 / 10.9; 32 of them:
     // 16 21.0 / 23.3), which is not counted on: the bound is the longest request's, and the others may be short.
     if (tiles <= 4 && n_items <= (long long)decode_fit(rows)) {
+        if (kSel)
+            return kv4::launch_dependent(decode_kernel<D, NT, kSel>, dim3((unsigned)n_items), kDecodeThreads, smem, st, "decode_kernel", a, rows, 1, nullptr, nullptr);
         decode_kernel<D, NT, kSel><<<(unsigned)n_items, kDecodeThreads, smem, st>>>(a, rows, 1, nullptr, nullptr);
         return qmoe::launch_check("decode_kernel");
     }
     const unsigned blocks = (unsigned)std::min((long long)decode_fit(rows), n_items * std::max(1LL, tiles));
     SplitItem* items = (SplitItem*)ws;
     float* parts = (float*)((char*)ws + decode_records());
-    decode_kernel<D, NT, kSel><<<blocks, kDecodeThreads, smem, st>>>(a, rows, 0, items, parts);
-    if ((rc = qmoe::launch_check("decode_kernel"))) return rc;
+    if (kSel) {
+        rc = kv4::launch_dependent(decode_kernel<D, NT, kSel>, dim3(blocks), kDecodeThreads, smem, st, "decode_kernel", a, rows, 0, items, parts);
+    } else {
+        decode_kernel<D, NT, kSel><<<blocks, kDecodeThreads, smem, st>>>(a, rows, 0, items, parts);
+        rc = qmoe::launch_check("decode_kernel");
+    }
+    if (rc) return rc;
     return kv4::launch_dependent(join_kernel<D, kSel>, dim3(blocks, kSel ? std::min(a.group, 16) : NT == 1 ? 8 : 16), kJoinThreads, 0, st, "join_kernel", a, items, parts, rows);
 }
 

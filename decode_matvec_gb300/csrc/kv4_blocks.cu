@@ -48,6 +48,8 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(BoundsArgs a, in
     constexpr int D = L * 8, ROWS = kBoundsThreads / L, STEPS = 64 / ROWS, WARPS = kBoundsThreads / 32;
     __shared__ float lo_s[WARPS][D], hi_s[WARPS][D], big_s[WARPS];
     __shared__ int ends[kBoundsThreads], n_ends;
+    kv4::depend_wait();
+    kv4::depend_launch();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gl = lane & (L - 1), row = tid / L;
     const int h = blockIdx.y, shift = a.cache.page_shift, P = 1 << shift;
     const int64_t t = (int64_t)blockIdx.x * span + tid;
@@ -192,6 +194,7 @@ constexpr int kWholeThreads = 128;
 template <int D>
 __global__ void __launch_bounds__(kWholeThreads) whole_kernel(SelectArgs a) {
     constexpr int V = D / 32;
+    kv4::depend_wait();        // (before the scores' kernel may begin: that reads what earlier calls wrote without waiting)
     kv4::depend_launch();
     const int64_t i = (int64_t)blockIdx.x * (kWholeThreads / 32) + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
@@ -384,6 +387,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? kPickThreads : WARPS * 32) pick_k
     int b, seen = -1;
     if (t < a.n) seen = blocks_seen(a, t, &b, a.max_seen <= a.top && tid == 0 && list == (int64_t)t * a.n_kv);
     kv4::depend_wait();        // (before any return: what follows the call waits for this kernel alone)
+    kv4::depend_launch();
     if (seen < 0) return;
     int32_t* sel = a.sel + list * a.top;
     if (seen <= a.top) {
@@ -542,9 +546,8 @@ extern "C" int kv4_block_bounds(const kv4_cache* cache, const kv4_bounds* bounds
     const int64_t share = (int64_t)n * cache->n_kv_heads / ((int64_t)qmoe::sm_count() * 16);
     const int span = (int)std::min<int64_t>(std::max<int64_t>(share, 1), cache->page_size);
     const dim3 grid((unsigned)(((int64_t)n + span - 1) / span), (unsigned)cache->n_kv_heads);
-    if (cache->head_dim == 128) bounds_kernel<16><<<grid, kBoundsThreads, 0, (cudaStream_t)stream>>>(a, span);
-    else bounds_kernel<8><<<grid, kBoundsThreads, 0, (cudaStream_t)stream>>>(a, span);
-    return qmoe::launch_check("kv4_block_bounds");
+    return kv4::launch_dependent(cache->head_dim == 128 ? bounds_kernel<16> : bounds_kernel<8>, grid, kBoundsThreads, 0, (cudaStream_t)stream,
+                                 "kv4_block_bounds", a, span);
 }
 
 extern "C" int kv4_select_blocks_ws_size(int n_q_tokens, int n_kv_heads, int page_size, int max_kv, size_t* bytes) {
@@ -592,15 +595,14 @@ extern "C" int kv4_select_blocks(const kv4_bounds* bounds, const void* q, int n_
     const unsigned lists = (unsigned)(n_q_tokens * n_kv), by_warps = (lists + kPickThreads / 32 - 1) / (kPickThreads / 32);
     const char* who = "kv4_select_blocks";
     if (row <= top) {
+        // (launched plainly: it reads the lengths ahead of its wait, which only a kernel behind score_kernel may)
         pick_kernel<1, 0><<<by_warps, kPickThreads, 0, st>>>(a);      // every block that is there
         return qmoe::launch_check(who);
     }
     if (!workspace || !kv4::aligned16(workspace)) return qmoe::fail(QMOE_EINVAL, "kv4_select_blocks: workspace NULL or not 16-byte aligned");
     const unsigned whole_blocks = (lists + kWholeThreads / 32 - 1) / (kWholeThreads / 32);
     const bool d128 = bounds->head_dim == 128;
-    if (d128) whole_kernel<128><<<whole_blocks, kWholeThreads, 0, st>>>(a);
-    else whole_kernel<64><<<whole_blocks, kWholeThreads, 0, st>>>(a);
-    if ((rc = qmoe::launch_check(who))) return rc;
+    if ((rc = kv4::launch_dependent(d128 ? whole_kernel<128> : whole_kernel<64>, dim3(whole_blocks), kWholeThreads, 0, st, who, a))) return rc;
     if ((rc = kv4::launch_dependent(d128 ? score_kernel<128> : score_kernel<64>, dim3((unsigned)blocks, (unsigned)((n_kv + kScoreHeads - 1) / kScoreHeads)), kScoreThreads, 0, st, who, a, (int)chunks, pages))) return rc;
     const int64_t most = ((int64_t)max_kv + bounds->page_size - 1) / bounds->page_size - first - last;      // blocks a list chooses from
     if (most <= 128) return kv4::launch_dependent(pick_kernel<1, 4>, dim3(by_warps), kPickThreads, 0, st, who, a);

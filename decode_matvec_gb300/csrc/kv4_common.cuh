@@ -65,31 +65,10 @@ inline int view_of(const kv4_cache* c, const char* who, CacheView* v) {
     return QMOE_OK;
 }
 
-// Programmatic dependent launch: the kernels of a call overlap each other's launches.
-__device__ __forceinline__ void depend_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void depend_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+using qmoe::depend_launch;
+using qmoe::depend_wait;
+using qmoe::launch_dependent;
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
-
-template <typename T>
-struct Same {
-    using type = T;
-};
-
-// Launches a kernel that may start while the one before it in the stream still runs (it waits itself, by depend_wait).
-template <typename... Args>
-inline int launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, int smem, cudaStream_t st, const char* who, typename Same<Args>::type... args) {
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return qmoe::cuda_check(cudaLaunchKernelEx(&cfg, kernel, args...), who);
-}
 
 }  // namespace kv4

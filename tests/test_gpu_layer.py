@@ -648,3 +648,88 @@ def test_a_step_of_all_of_them_on_another_stream_and_in_a_graph():
         for a, b in zip(results(held), wanted[i]):
             assert torch.equal(a, b)
     ok()
+
+
+def test_calls_behind_copies_and_other_streams():
+    """Each call right behind a copy of its inputs, and behind another stream's work, in a stream and in a graph: it waits for them."""
+    g = torch.Generator(DEV).manual_seed(2)
+    B, hq, hkv, D, P, top, E, n = 3, 4, 2, 64, 16, 3, 64, 256
+    i32 = dict(dtype=torch.int32, device=DEV)
+    lens = torch.tensor([100, 7, 160], **i32)
+    table = torch.randperm(40, generator=g, device=DEV)[:33].int().view(B, 11).contiguous()
+    q_start = torch.arange(B + 1, **i32)
+    slots = (torch.gather(table, 1, ((lens - 1) // P).long()[:, None])[:, 0] * P + (lens - 1) % P).int()
+
+    def inputs(seed):
+        g = torch.Generator(DEV).manual_seed(seed)
+        u = torch.randint(0, 256, (40, hkv * P * D), generator=g, device=DEV, dtype=torch.uint8)
+        s = torch.stack([torch.full((40, hkv, 2 * P), 0.1, device=DEV), torch.full((40, hkv, 2 * P), -0.7, device=DEV)], -1).to(torch.float16)
+        pages = torch.cat([u.view(40, hkv, P * D), s.view(torch.uint8).view(40, hkv, P * 8)], -1).reshape(40, -1).contiguous()
+        return dict(x=torch.randn((700, n), generator=g, device=DEV), logits=torch.randn((600, E), generator=g, device=DEV), pages=pages,
+                    q=torch.randn((B, hq, D), generator=g, device=DEV).to(torch.bfloat16), kv_len=lens.clone(), slots=slots.clone())
+
+    def state():
+        s = {k: torch.zeros_like(v) for k, v in inputs(0).items()}
+        s["kv_len"].fill_(1)
+        s["cache"] = Q.Kv4Cache(s["pages"], P, hkv, D)
+        s.update(bounds=Q.Kv4Bounds.empty(s["cache"]), y=torch.zeros((700, n), dtype=torch.bfloat16, device=DEV), ids=torch.zeros((600, 4), **i32),
+                 gates=torch.zeros((600, 4), device=DEV), sel=torch.zeros((B, hkv, top), **i32), att=torch.zeros((B, hq, D), dtype=torch.bfloat16, device=DEV),
+                 ws=torch.empty(max(Q.kv4_select_blocks_ws_size(B, hkv, P, 176), Q.kv4_attention_blocks_ws_size(B, hq, hkv, D, P, top)), dtype=torch.uint8, device=DEV))
+        return s
+
+    def calls(s, src, other):
+        """Copies of the inputs (each an async memory copy) with the calls right behind them; the cache's pages come by another stream."""
+        here = torch.cuda.current_stream()
+        other.wait_stream(here)
+        with torch.cuda.stream(other):
+            s["pages"].copy_(src["pages"])
+        s["x"].copy_(src["x"])
+        Q.add_rms_norm(s["x"], None, 1e-5, s["y"])
+        s["logits"].copy_(src["logits"])
+        Q.qmoe_route_scored(s["logits"], 4, s["ids"], s["gates"], sigmoid=True, n_groups=4, top_groups=2, group_best=2, renormalise=True)
+        s["slots"].copy_(src["slots"])
+        here.wait_stream(other)
+        Q.kv4_block_bounds(s["cache"], s["bounds"], s["slots"])
+        s["q"].copy_(src["q"])
+        s["kv_len"].copy_(src["kv_len"])
+        Q.kv4_select_blocks(s["bounds"], s["q"], q_start, s["kv_len"], table, s["sel"], s["ws"], 176)
+        Q.kv4_attention_blocks(s["cache"], s["q"], q_start, s["kv_len"], table, s["sel"], s["att"], s["ws"], D ** -0.5)
+
+    names = ("y", "ids", "gates", "sel", "att")
+    s, src, other = state(), inputs(0), torch.cuda.Stream()
+    wanted = []
+    for seed in (5, 6, 7):
+        for k, v in inputs(seed).items():
+            src[k].copy_(v)
+        torch.cuda.synchronize()
+        calls(s, src, other)
+        torch.cuda.synchronize()
+        wanted.append([s[k].clone() for k in names] + [s["bounds"].codes.clone(), s["bounds"].steps.clone()])
+        # against the oracle, for what a missing wait would show
+        check_norm(f64(s["y"]), Y.add_norm(f64(src["x"]), None, None, 1e-5)[1])
+        assert np.array_equal(s["ids"].cpu().numpy(), Y.route(f64(src["logits"]), 4, True, None, 4, 2, 2, True)[0])
+        ref = Y.select(f64(src["q"]), np.arange(B + 1), lens.cpu().numpy(), table.cpu().numpy(), s["bounds"].codes.cpu().numpy(), f64(s["bounds"].steps), P, top, 1, 1,
+                       np.zeros((B, hkv, top), int), 176)
+        assert np.array_equal(s["sel"].cpu().numpy(), ref)
+        check(f64(s["att"]), *Y.attention_blocks(f64(src["q"]), np.arange(B + 1), lens.cpu().numpy(), table.cpu().numpy(), src["pages"].cpu().numpy(), P, hkv, ref, D ** -0.5))
+    ok()
+    held, side = state(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            calls(held, src, other)
+    torch.cuda.synchronize()
+    for i, seed in enumerate((5, 6, 7)):
+        for k, v in inputs(seed).items():
+            src[k].copy_(v)
+        torch.cuda.synchronize()
+        for _ in range(3):          # (back to back: a replay begins where the one before it still ends)
+            graph.replay()
+        torch.cuda.synchronize()
+        # the bounds' other blocks are as they were, and those that were written are the same
+        for a, b in zip([held[k] for k in names], wanted[i]):
+            assert torch.equal(a, b)
+        page = (slots // P).long()
+        assert torch.equal(held["bounds"].codes[page], wanted[i][-2][page]) and torch.equal(held["bounds"].steps[page], wanted[i][-1][page])
+    ok()
