@@ -52,7 +52,7 @@ __device__ __forceinline__ int first_seen(const AttnArgs& a, int pos) { return a
 // Whether query token t can be run: its request, its position, and the blocks that it sees.
 __device__ __forceinline__ bool chosen_token(const AttnArgs& a, int t, int* b, int* pos, int* seen, bool report) {
     int end, n;
-    *b = kv4::request_of(a.q_start, a.kv_len, a.B, t, &end, &n);
+    *b = kv4::request_of<false>(a.q_start, a.kv_len, a.B, t, &end, &n);
     if (*b < 0) return false;
     if (n < 0 || n > kMaxKv) {
         if (report) attn_set_error(QMOE_EINVAL);

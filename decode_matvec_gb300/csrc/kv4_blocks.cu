@@ -163,7 +163,7 @@ struct SelectArgs {
 // Blocks that query token t sees (-1: the token belongs to no request), and its request.
 __device__ __forceinline__ int blocks_seen(const SelectArgs& a, int t, int* b, bool report) {
     int end, kv;
-    *b = kv4::request_of(a.q_start, a.kv_len, a.B, t, &end, &kv);
+    *b = kv4::request_of<true>(a.q_start, a.kv_len, a.B, t, &end, &kv);
     if (*b < 0) return -1;
     if (kv < 0 || kv > a.max_kv) {
         if (report) blocks_set_error(kv < 0 ? QMOE_EINVAL : QMOE_ECAPACITY);
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int 
 #pragma unroll
     for (int i = 0; i < TURNS; ++i) {
         const int j = j0 + i * kScoreThreads + tid;
-        entry[i] = i * kScoreThreads + tid < pages && t < a.B && j < a.max_blocks ? a.table[(int64_t)t * a.max_blocks + j] : -1;
+        entry[i] = i * kScoreThreads + tid < pages && t < a.B && j < a.max_blocks ? __ldcg(a.table + (int64_t)t * a.max_blocks + j) : -1;
     }
     int b;
     const int seen = blocks_seen(a, t, &b, c == 0 && tid == 0 && h0 == 0);
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int 
     for (int i = 0; i < TURNS; ++i) {
         const int at = i * kScoreThreads + tid, j = j0 + at;
         const bool mine = at < pages && j < seen;
-        if (b != t) entry[i] = mine && j < a.max_blocks ? a.table[(int64_t)b * a.max_blocks + j] : -1;
+        if (b != t) entry[i] = mine && j < a.max_blocks ? __ldcg(a.table + (int64_t)b * a.max_blocks + j) : -1;
         if (!mine || entry[i] < 0 || entry[i] >= a.n_pages) {
             if (mine && h0 == 0) blocks_set_error(QMOE_EINVAL);
             entry[i] = -1;

@@ -25,23 +25,30 @@ __device__ __forceinline__ unsigned char* head_ptr(const CacheView& c, int page,
     return c.pages + (uint64_t)page * c.page_bytes + (uint64_t)h * c.head_bytes;
 }
 
+// An int32, past the first-level cache where a kernel reads it ahead of its depend_wait.
+template <bool kAhead>
+__device__ __forceinline__ int load_i32(const int32_t* p) {
+    return kAhead ? __ldcg(p) : *p;
+}
+
 // The request that query token t belongs to (q_start[b] <= t < q_start[b + 1]), or -1; with q_start[b + 1] and kv_len[b].  In a
 // decode step it is t itself: that is looked at first, in one go.
+template <bool kAhead>
 __device__ __forceinline__ int request_of(const int32_t* q_start, const int32_t* kv_len, int B, int t, int* end, int* kv) {
     if (t < B) {
-        const int s = q_start[t];
-        *end = q_start[t + 1], *kv = kv_len[t];
+        const int s = load_i32<kAhead>(q_start + t);
+        *end = load_i32<kAhead>(q_start + t + 1), *kv = load_i32<kAhead>(kv_len + t);
         if (s == t && *end == t + 1) return t;
     }
     int lo = 0, hi = B;         // the last b with q_start[b] <= t is in [lo - 1, hi - 1]
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (q_start[mid] <= t) lo = mid + 1;
+        if (load_i32<kAhead>(q_start + mid) <= t) lo = mid + 1;
         else hi = mid;
     }
-    *end = q_start[lo];
+    *end = load_i32<kAhead>(q_start + lo);
     if (lo == 0 || t >= *end) return -1;
-    *kv = kv_len[lo - 1];
+    *kv = load_i32<kAhead>(kv_len + lo - 1);
     return lo - 1;
 }
 

@@ -147,7 +147,7 @@ __device__ __forceinline__ float largest(const Values<8>& v) {
 // overflows or loses bits on the way); 448 / m is correctly rounded, as an error of it would move all the run's codes next to the middle
 // of two values.
 __device__ __forceinline__ float store_codes(uint8_t* dst, const Values<8>& y, float m) {
-    const float g = __uint_as_float(max((254u << 23) - (__float_as_uint(m) & 0x7F800000u), 1u << 23));
+    const float g = __int_as_float(max((254 << 23) - (int)(__float_as_uint(m) & 0x7F800000u), 1 << 23));
     const float inv = m == 0.f ? 0.f : __fdiv_rn(448.f, m * g);
     uint32_t w[2];
 #pragma unroll
@@ -626,6 +626,7 @@ __device__ __noinline__ int exact_order(const RouteArgs& a, const X* row, int n,
         const double l = logit(row, mine);
         p = l > -INFINITY ? a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / (double)z : 0.0;
         c = p + (double)a.bias[mine];
+        if (c != c) c = -INFINITY;
     }
     const unsigned long long key = key_of(c);
     int rank = 0, from = lane;

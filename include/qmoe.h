@@ -650,8 +650,8 @@ int qk_norm_rope(const void* qkv, int64_t row_stride, int T, int n_q_heads, int 
  *            [T][ceil(n / 128)] when it is 128.
  *  n         1 .. 32768, strides below 2^31;  eps positive.
  * Other overlaps between outputs and inputs are not allowed.  A row with a NaN or an infinity gives
- * what the formula gives (NaN, or 0 for its finite values beside an infinity); squares are fp32, so rows
- * with values of 1e19 and more overflow to that too.  Rows whose width, strides and
+ * what the formula gives (NaN, in the codes and scales too, or 0 for its finite values beside an
+ * infinity); squares are fp32, so rows with values of 1e19 and more overflow to that too.  Rows whose width, strides and
  * addresses allow 16-byte accesses take fewer instructions; the others are as exact.
  * Errors: EINVAL (sizes, strides below n, NULL, alignment to the type), EUNSUPPORTED (codes with n
  * or a stride that is no multiple of 8, or pointers not 16-byte aligned (codes 8); another scale_group).
@@ -741,8 +741,8 @@ typedef struct {
 /*
  * Bring the bounds up to date after tokens were written to the cache at slots (device int32 [n], -1
  * skips): the bounds of each page among them, over its tokens up to the last written one, are made
- * from the cache.  slots as kv4_block_tables gives them: the tokens of a page next to each other and
- * in order.  Errors: EINVAL (other sizes than the cache's); on the device EINVAL (a slot outside the
+ * from the cache.  slots as kv4_block_tables gives them: the tokens of a page next to each other, in
+ * order and without a gap (else the page's bounds are those up to one of its written tokens).  Errors: EINVAL (other sizes than the cache's); on the device EINVAL (a slot outside the
  * cache: skipped).
  */
 int kv4_block_bounds(const kv4_cache* cache, const kv4_bounds* bounds, const int32_t* slots, int n, void* stream);
@@ -762,7 +762,7 @@ int kv4_block_bounds(const kv4_cache* cache, const kv4_bounds* bounds, const int
  *          that sees top blocks or fewer has them all.
  *  top     1 .. 65536;  first, last >= 0, first + last <= top;  max_kv at most 2^20 pages.
  *  workspace  device, ws_bytes >= kv4_select_blocks_ws_size(...), 16-byte aligned (no smaller for larger
- *          n_q_tokens or max_kv).
+ *          n_q_tokens or max_kv); not shared by calls that may run at the same time.
  * Rows of sel that belong to no request are left as they are.  A block without a page in the cache has
  * score -infinity (EINVAL in the error word).  A request whose kv_len is negative (EINVAL) or above
  * max_kv (ECAPACITY) gets lists of -1.
@@ -779,7 +779,8 @@ int kv4_select_blocks(const kv4_bounds* bounds, const void* q, int n_q_tokens, i
  *  sel     device int32 [n_q_tokens][n_kv_heads][top], as kv4_select_blocks writes it.  Of a query that
  *          sees nb blocks the first min(top, nb) entries are read; -1, and a block that the query does not
  *          see, name no tokens.  A block listed twice counts twice.
- *  workspace  device, ws_bytes >= kv4_attention_blocks_ws_size(...), 16-byte aligned.
+ *  workspace  device, ws_bytes >= kv4_attention_blocks_ws_size(...), 16-byte aligned; not shared by
+ *          calls that may run at the same time.
  * The other arguments, the arithmetic (that of requests with few query rows) and the rows that are left as they are: as in
  * kv4_attention with causal.
  * Errors: EINVAL, EUNSUPPORTED (head_dim, more than 32 query heads per kv head), ECAPACITY; on the

@@ -733,3 +733,103 @@ def test_calls_behind_copies_and_other_streams():
         page = (slots // P).long()
         assert torch.equal(held["bounds"].codes[page], wanted[i][-2][page]) and torch.equal(held["bounds"].steps[page], wanted[i][-1][page])
     ok()
+
+
+# ------------------------------------------------------------------ calls at the edges of what is allowed
+def test_norm_of_a_tensor_with_itself_and_of_values_that_overflow():
+    r = np.random.RandomState(21)
+    T, n = 5, 512
+    xt, x = bf(r.randn(T, n))
+    both = xt.clone()
+    y = torch.empty_like(xt)
+    Q.add_rms_norm(both, None, 1e-5, y, residual=both)          # x is its own residual, written in place
+    ok()
+    check_norm(f64(y), Y.add_norm(x, x, None, 1e-5)[1])
+    assert torch.equal(both, (2 * xt.float()).to(torch.bfloat16))
+    # outputs that pass fp32: the scale is infinite, finite values have code 0
+    w = torch.full((n,), 3e38, dtype=torch.bfloat16, device=DEV)
+    x = torch.ones((1, n), device=DEV)
+    x[0, 100:] = 1e-12
+    codes, scales = torch.empty((1, n), dtype=torch.uint8, device=DEV), torch.empty((1, 4), device=DEV)
+    Q.add_rms_norm(x, w, 1e-30, y[:1], codes=codes, scales=scales)
+    ok()
+    assert np.isinf(f64(y)[0, :100]).all() and np.isfinite(f64(y)[0, 100:]).all() and np.isinf(f64(scales)[0, 0]) and np.isfinite(f64(scales)[0, 1:]).all()
+    c = codes.cpu().numpy()[0]
+    assert ((c[:100] & 0x7F) == 0x7F).all() and (c[100:128] & 0x7F == 0).all() and (c[128:] == 0x7E).all()
+
+
+def test_route_with_biases_that_are_no_numbers():
+    r = np.random.RandomState(22)
+    for E in (6, 40, 300, 2048):
+        bias = 0.1 * r.randn(E)
+        bias[:3] = np.nan
+        bias[3] = -np.inf
+        k = min(E, 32)
+        for sigmoid in (False, True):
+            check_route(r.randn(4, E), k, sigmoid=sigmoid, bias=bias, renormalise=True)
+        if E == 6:
+            check_route(r.randn(4, E), 2, sigmoid=True, bias=bias, n_groups=3, top_groups=2, group_best=2)
+
+
+def test_two_calls_at_once_on_two_streams():
+    """The calls have no state of their own: with outputs and workspaces apart, two streams do not disturb each other."""
+    r = np.random.RandomState(23)
+    P, hq, hkv, D, top = 16, 8, 2, 128, 6
+    sets = []
+    for i in range(2):
+        old, new = [900 + 50 * i, 300, 40], [1, 1, 1]
+        pages, table, kv, slots = paged(r, old, new, hkv, D, P)
+        qt, q = bf(r.randn(3, hq, D))
+        cache = cache_of(pages, P, hkv, D)
+        b = Q.Kv4Bounds.empty(cache)
+        every = np.concatenate([table[j, p // P] * P + p % P for j in range(3) for p in [np.arange(kv[j])]])
+        Q.kv4_block_bounds(cache, b, ints(every))
+        s = dict(q=qt, cache=cache, b=b, qs=ints(np.arange(4)), kv=ints(kv), table=ints(table), sel=torch.zeros((3, hkv, top), dtype=torch.int32, device=DEV),
+                 out=torch.zeros_like(qt), ws=torch.empty(1 << 20, dtype=torch.uint8, device=DEV), ws2=torch.empty(8 << 20, dtype=torch.uint8, device=DEV),
+                 x=torch.randn((2000, 512), device=DEV), y=torch.zeros((2000, 512), dtype=torch.bfloat16, device=DEV), max_kv=int(kv.max()))
+        s["stream"] = torch.cuda.Stream()
+        sets.append(s)
+
+    def run(s):
+        Q.add_rms_norm(s["x"], None, 1e-5, s["y"])
+        Q.kv4_select_blocks(s["b"], s["q"], s["qs"], s["kv"], s["table"], s["sel"], s["ws"], s["max_kv"])
+        Q.kv4_attention_blocks(s["cache"], s["q"], s["qs"], s["kv"], s["table"], s["sel"], s["out"], s["ws2"], D ** -0.5)
+    wanted = []
+    for s in sets:
+        run(s)
+        torch.cuda.synchronize()
+        wanted.append([s[k].clone() for k in ("y", "sel", "out")])
+    for _ in range(20):
+        for s in sets:
+            with torch.cuda.stream(s["stream"]):
+                for k in ("y", "sel", "out"):
+                    s[k].zero_()
+                run(s)
+    torch.cuda.synchronize()
+    ok()
+    for s, w in zip(sets, wanted):
+        for k, v in zip(("y", "sel", "out"), w):
+            assert torch.equal(s[k], v)
+
+
+@pytest.mark.parametrize("n", [1, 300])
+def test_calls_on_no_rows_and_on_rows_of_no_request(n):
+    i32 = dict(dtype=torch.int32, device=DEV)
+    cache = Q.Kv4Cache.empty(4, 16, 2, 64)
+    b = Q.Kv4Bounds.empty(cache)
+    q = torch.zeros((n, 4, 64), dtype=torch.bfloat16, device=DEV)
+    sel, out = torch.full((n, 2, 3), -7, **i32), torch.full_like(q, 5.0)
+    ws = torch.empty(8 << 20, dtype=torch.uint8, device=DEV)
+    none = torch.zeros((0, 5), **i32)
+    zero = torch.zeros(1, **i32)
+    Q.kv4_select_blocks(b, q, zero, zero[:0], none, sel, ws, 100)                    # no requests
+    Q.kv4_attention_blocks(cache, q, zero, zero[:0], none, sel, out, ws, 0.125)
+    one = torch.zeros((1, 5), **i32)
+    Q.kv4_select_blocks(b, q, torch.zeros(2, **i32), zero, one, sel, ws, 100)        # one, without queries
+    Q.kv4_attention_blocks(cache, q, torch.zeros(2, **i32), zero, one, sel, out, ws, 0.125)
+    ok()
+    assert bool((sel == -7).all()) and bool((out == 5).all())
+    Q.add_rms_norm(torch.zeros((0, 64), device=DEV), None, 1e-5, torch.zeros((0, 64), dtype=torch.bfloat16, device=DEV))
+    Q.qmoe_route_scored(torch.zeros((0, 64), device=DEV), 2, torch.zeros((0, 2), **i32), torch.zeros((0, 2), device=DEV))
+    Q.kv4_block_bounds(cache, b, zero[:0])
+    ok()
