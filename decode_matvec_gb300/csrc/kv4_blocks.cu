@@ -40,7 +40,9 @@ struct BoundsArgs {
 
 // A thread block takes `span` tokens of one kv head and bounds the block of each that is the last new one of its block.
 // L = head_dim / 8 lanes hold a row of codes (a word, 8 channels, a lane); the rows of a block are dealt out over the four
-// warps, all of a lane's loads in flight together, and joined in shared memory, where a thread takes a channel.
+// warps, all of a lane's loads in flight together, and joined in shared memory, where a thread takes a channel.  The instructions bound
+// it: 8 of a word's codes made fp32 values, exactly, and compared twice (16 prompts of 777 to 2048 tokens, 8 heads of 128, pages of 64:
+// 9.4 us for 12 MB, 2300 instructions a block and head, 62 % of the issue slots; 10.2 us without the packed arithmetic).
 constexpr int kBoundsThreads = 128;
 
 template <int L>
@@ -188,7 +190,8 @@ __device__ __forceinline__ float query_value(uint32_t bits) {
 }
 
 // The queries of one token and kv head as whole numbers: sums over the group of the positive parts, then of the negative
-// ones, 16 bits each.  A warp takes a (token, kv head), a lane D / 32 channels.
+// ones, 16 bits each.  A warp takes a (token, kv head), a lane D / 32 channels.  A kernel of its own: made again in every thread
+// block of the scores they cost 21.9 us for 64 requests of up to 32768 tokens instead of 19.4.  One chain of loads bounds it.
 constexpr int kWholeThreads = 128;
 
 template <int D>
@@ -247,7 +250,9 @@ __global__ void __launch_bounds__(kWholeThreads) whole_kernel(SelectArgs a) {
 // heads of each page, which stand side by side, to shared memory, all at once and without registers, so that the blocks of a
 // multiprocessor have what its bandwidth takes under way; then groups of L lanes (16 codes of a record each) multiply kRecords records
 // of one kv head at a time with the group's summed queries, and the partial sums are added up crosswise, so that lane i ends with
-// record i (mod kRecords).  What does not depend on the queries goes ahead of the wait for them.
+// record i (mod kRecords).  What does not depend on the queries goes ahead of the wait for them.  The latency table - copy - product
+// bounds it: 64 requests of up to 32768 tokens, 8 kv heads of 128, pages of 64, 37 MB, take 19.6 us with whole_kernel and pick_kernel (this one
+// alone, cold caches, 12.8: 42 % of the copy rate), and 21 to 23 where the records go through registers.
 constexpr int kScoreBytes = 32768, kScoreHeads = 32, kRecords = 8, kMostPages = 256;
 constexpr uint32_t kWaitLimit = 1u << 22;
 
@@ -364,7 +369,9 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int 
 // registers as integer keys, warp w those of the w-th equal run.  The key of the last one taken is found between the
 // smallest and the largest by trying three keys at a time (a count each, all three in one word), until as many are above
 // one of them as are wanted or nothing is left between; then every warp writes the blocks of its run that are above it, and the
-// first ones at it.
+// first ones at it.  Some ten rounds one after the other, each a count and its sum, bound it: about 5 us for 512 lists of up to 512 scores.  Tries
+// that are not a quarter apart as keys (as values; where the counts so far point to) take longer: 64 requests' choice 20.3 to 20.5 us
+// instead of 19.6, and 13.5 to 15.1 instead of 11.8 for 8192 scores a list.
 constexpr int kMostBlocks = 1 << 20;      // of a request
 constexpr int kPickThreads = 128;        // of a block whose warps make a list each
 

@@ -160,7 +160,9 @@ __device__ __forceinline__ float store_codes(uint8_t* dst, const Values<8>& y, f
     return m * (1.f / 448.f);
 }
 
-// K steps of V values a lane, all loads under way at once; W warps a row.
+// K steps of V values a lane, all loads under way at once; W warps a row.  Bound by memory: 16384 rows of 2048 bf16 with a residual, bf16
+// and 8-bit outputs take 48 us for 303 MB, 6.3 TB/s, 93 % of a copy's rate; 32 rows from fp32 2.1 us, one launch.  A persistent grid
+// that loads the next row ahead holds fewer rows in flight (53.8 us).
 template <typename X, int V, int K>
 __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a, int W, int rows) {
     __shared__ float sum_s[32], max_s[32];
@@ -713,7 +715,9 @@ __device__ __forceinline__ Doubts doubts_of(const RouteArgs& a, uint32_t mk, int
     return d;
 }
 
-// R experts a lane, a warp a token.
+// R experts a lane, a warp a token.  Instructions bound it, and the latency of a round (a reduction, a ballot, a list that moves up): 16383
+// tokens of 256 experts in 8 groups, the best 8 by sigmoid scores and a bias, 16.3 us and 830 instructions a token, 67 % of
+// the issue slots; 32 tokens 3.6 to 4.2 us.  A warp that goes on to another token with its logits loaded ahead took 19 us.
 template <typename X, int R>
 __global__ void __launch_bounds__(kTokenWarps * 32, R <= 8 ? 8 : 4) route_kernel(RouteArgs a) {
     qmoe::depend_wait();
@@ -872,7 +876,8 @@ __global__ void __launch_bounds__(kTokenWarps * 32, R <= 8 ? 8 : 4) route_kernel
 // Many experts without groups: a block of 4 warps a token, R values a thread in loads that stand side by side.  In each warp
 // the `rounds`-th largest of the lanes' maxima bounds the values to look at from below, and the largest of the warps' bounds
 // does for all; the few values that reach it are put side by side in shared memory, and the first warp's rounds go over
-// those, by key and index.
+// those, by key and index.  The three barriers of a row bound it: 4096 tokens of 2048 fp32 logits, 2 by softmax and a bias, 17.6 us, 1.9 TB/s,
+// 46 % of the issue slots (a warp a token 21 to 23 us).
 constexpr int kWideMost = 256;      // values put side by side; rows with more (many equal ones) take exact_choice
 
 template <typename X, int R>
