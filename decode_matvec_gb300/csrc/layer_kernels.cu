@@ -116,24 +116,35 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, const Values<V>& v) {
         *p = (uint16_t)pack_bf16(v.v[0], 0.f);
 }
 
-// Reduction over the W warps of a row (slot: this row's places in shared memory).
+// Sum and largest of a row's values, over its W warps (slot: this row's places in shared memory).
 template <bool kMax>
-__device__ __forceinline__ float row_reduce(float v, int W, float* slot, int warp_in_row, int lane) {
+__device__ __forceinline__ float2 row_reduce(float sum, float big, int W, float2* slot, int warp_in_row, int lane) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
-        const float o = __shfl_xor_sync(QMOE_FULL_MASK, v, d);
-        v = kMax ? max_nan(v, o) : v + o;
+        sum += __shfl_xor_sync(QMOE_FULL_MASK, sum, d);
+        if (kMax) big = max_nan(big, __shfl_xor_sync(QMOE_FULL_MASK, big, d));
     }
-    if (W == 1) return v;
-    if (lane == 0) slot[warp_in_row] = v;
+    if (W == 1) return make_float2(sum, big);
+    if (lane == 0) slot[warp_in_row] = make_float2(sum, big);
     __syncthreads();
-    v = lane < W ? slot[lane] : 0.f;
+    if (W <= 8) {
+        float2 all = slot[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) {
+            if (i >= W) break;
+            const float2 o = slot[i];
+            all.x += o.x;
+            if (kMax) all.y = max_nan(all.y, o.y);
+        }
+        return all;
+    }
+    float2 all = lane < W ? slot[lane] : make_float2(0.f, 0.f);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
-        const float o = __shfl_xor_sync(QMOE_FULL_MASK, v, d);
-        v = kMax ? max_nan(v, o) : v + o;
+        all.x += __shfl_xor_sync(QMOE_FULL_MASK, all.x, d);
+        if (kMax) all.y = max_nan(all.y, __shfl_xor_sync(QMOE_FULL_MASK, all.y, d));
     }
-    return v;
+    return all;
 }
 
 __device__ __forceinline__ float largest(const Values<8>& v) {
@@ -143,29 +154,33 @@ __device__ __forceinline__ float largest(const Values<8>& v) {
     return m;
 }
 
-// 8 codes of y / s for s = m / 448, which is returned.  A power of two brings m next to 1 (whatever its exponent: no value
-// overflows or loses bits on the way); 448 / m is correctly rounded, as an error of it would move all the run's codes next to the middle
-// of two values.
-__device__ __forceinline__ float store_codes(uint8_t* dst, const Values<8>& y, float m) {
-    const float g = __int_as_float(max((254 << 23) - (int)(__float_as_uint(m) & 0x7F800000u), 1 << 23));
-    const float inv = m == 0.f ? 0.f : __fdiv_rn(448.f, m * g);
+// 8 codes of v / s for s = m / 448, m = max |v| > 0.  448 / m is in two floats, as an error of it would move all the run's codes next to
+// the middle of two values.  Where m is far from 1 a power of two brings the values near it first.
+__device__ __forceinline__ void store_codes(uint8_t* dst, Values<8> v, float m) {
+    if (__builtin_expect(!(m > 1e-30f && m < 1e30f), 0)) {
+        const float g = __int_as_float(max((254 << 23) - (int)(__float_as_uint(m) & 0x7F800000u), 1 << 23));
+        v.times(g), m *= g;
+    }
+    const float inv = __fdividef(448.f, m), rest = fmaf(-inv, m, 448.f) * inv * (1.f / 448.f);
+    auto quotient = [&](float x) { return fmaf(x, inv, x * rest); };
     uint32_t w[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        const float* v = y.v + 4 * j;
-        w[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[0] * g * inv, v[1] * g * inv), __NV_SATFINITE, __NV_E4M3) |
-               (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[2] * g * inv, v[3] * g * inv), __NV_SATFINITE, __NV_E4M3) << 16;
+        const float* x = v.v + 4 * j;
+        w[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(quotient(x[0]), quotient(x[1])), __NV_SATFINITE, __NV_E4M3) |
+               (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(quotient(x[2]), quotient(x[3])), __NV_SATFINITE, __NV_E4M3) << 16;
     }
     *(uint2*)dst = make_uint2(w[0], w[1]);
-    return m * (1.f / 448.f);
 }
 
 // K steps of V values a lane, all loads under way at once; W warps a row.  Bound by memory: 16384 rows of 2048 bf16 with a residual, bf16
-// and 8-bit outputs take 48 us for 303 MB, 6.3 TB/s, 93 % of a copy's rate; 32 rows from fp32 2.1 us, one launch.  A persistent grid
+// and 8-bit outputs take 46.8 us for 303 MB, 6.5 TB/s, 95 % of a copy's rate; 32 rows from fp32 2.1 us, one launch.  A persistent grid
 // that loads the next row ahead holds fewer rows in flight (53.8 us).
+// v = h w, y = v f with f = 1 / sqrt(mean(h^2) + eps): codes are those of v relative to max |v|, without f and its roundings, and a row's largest
+// v is found in the same exchange as its sum.
 template <typename X, int V, int K>
 __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a, int W, int rows) {
-    __shared__ float sum_s[32], max_s[32];
+    __shared__ float2 row_s[32];
     qmoe::depend_wait();
     qmoe::depend_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = W == 1 ? warp : warp / W, in_row = warp - row * W;
@@ -204,45 +219,62 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a, int W, int rows)
     float part[2] = {0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < K; ++k) part[k & 1] = h[k].squares(part[k & 1]);
-    const float sum = row_reduce<false>(part[0] + part[1], W, sum_s + row * W, in_row, lane);
-    const float f = rsqrtf(__fdividef(sum, (float)a.n) + a.eps);
-    float big = 0.f;
+    if (a.weight) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-        const int c = c0 + k * step;
-        if (c < chunks) {
-            h[k].times(f);
-            if (a.weight) {
+        for (int k = 0; k < K; ++k) {
+            if (c0 + k * step < chunks) {
                 Raw<uint16_t, V> w;
-                w.load(a.weight + c * V);
+                w.load(a.weight + (c0 + k * step) * V);
                 h[k].times(w.values());
-            }
-            if (a.y) store_bf16<V>(a.y + (int64_t)t * a.y_stride + c * V, h[k]);
-        }
-        if constexpr (V == 8) {
-            if (a.codes) {
-                float m = largest(h[k]);
-                if (a.row_scale) {
-                    big = max_nan(big, m);
-                } else {       // 16 lanes hold 128 values
-#pragma unroll
-                    for (int d = 8; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(QMOE_FULL_MASK, m, d));
-                    if (c < chunks) {
-                        const float s = store_codes(a.codes + (int64_t)t * a.n + c * V, h[k], m);
-                        if ((lane & 15) == 0) a.scales[(int64_t)t * ((a.n + 127) >> 7) + (c >> 4)] = s;
-                    }
-                }
             }
         }
     }
+    float big[K] = {};
     if constexpr (V == 8) {
-        if (a.codes && a.row_scale) {
-            big = row_reduce<true>(big, W, max_s + row * W, in_row, lane);
-            if (on && c0 == 0) a.scales[t] = big * (1.f / 448.f);
+        if (a.codes) {
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (c0 + k * step < chunks) store_codes(a.codes + (int64_t)t * a.n + (c0 + k * step) * V, h[k], big);
+            for (int k = 0; k < K; ++k) {
+                big[k] = largest(h[k]);
+                if (a.row_scale) {
+                    if (k) big[0] = max_nan(big[0], big[k]);
+                    continue;
+                }
+#pragma unroll
+                for (int d = 8; d > 0; d >>= 1) big[k] = max_nan(big[k], __shfl_xor_sync(QMOE_FULL_MASK, big[k], d));      // (16 lanes hold 128 values)
+            }
         }
+    }
+    const float2 all = V == 8 && a.codes && a.row_scale ? row_reduce<true>(part[0] + part[1], big[0], W, row_s + row * W, in_row, lane)
+                                                        : row_reduce<false>(part[0] + part[1], 0.f, W, row_s + row * W, in_row, lane);
+    const float f = rsqrtf(__fdividef(all.x, (float)a.n) + a.eps);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = c0 + k * step;
+        if (c >= chunks) break;
+        if constexpr (V == 8) {
+            if (a.codes) {
+                const float m = a.row_scale ? all.y : big[k], top = m * f;
+                store_codes(a.codes + (int64_t)t * a.n + c * V, h[k], m);
+                if (a.row_scale) {
+                    if (c == 0) a.scales[t] = top * (1.f / 448.f);
+                } else if ((lane & 15) == 0) {
+                    a.scales[(int64_t)t * ((a.n + 127) >> 7) + (c >> 4)] = top * (1.f / 448.f);
+                }
+                h[k].times(f);
+                if (__builtin_expect(!(top > 0.f && top < INFINITY), 0)) {
+                    // no scale: 0 where all y are 0, and for finite y beside infinite ones; the rest NaN
+                    uint32_t w[2] = {0, 0};
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (top != 0.f && !(top == INFINITY && fabsf(h[k].v[i]) < INFINITY)) w[i >> 2] |= 0x7Fu << 8 * (i & 3);
+                    *(uint2*)(a.codes + (int64_t)t * a.n + c * V) = make_uint2(w[0], w[1]);
+                }
+                if (a.y) store_bf16<V>(a.y + (int64_t)t * a.y_stride + c * V, h[k]);
+                continue;
+            }
+        }
+        h[k].times(f);
+        if (a.y) store_bf16<V>(a.y + (int64_t)t * a.y_stride + c * V, h[k]);
     }
 }
 
@@ -254,13 +286,14 @@ int launch_norm_steps(const NormArgs& a, cudaStream_t st) {
     return launch_rows(norm_kernel<X, V, K>, a.T, (unsigned)(((int64_t)a.T + rows - 1) / rows), rows * W * 32, st, "add_rms_norm", a, W, rows);
 }
 
-// Steps a lane.  With many rows two: four warps for a row of 2048, blocks of 128 threads (16384 rows of 2048 with a residual and
-// codes, us: 48.2 with one step, 47.8 with two, 47.6 with four, 53.7 with eight; 4095 of 2080 from fp32 with a scale a row: 20.8,
-// 18.3, 20.0, 22.4).  With few rows one, for the shortest chain; more where a row would take more than 16 warps.
+// Steps a lane.  With many rows two, or three where that leaves fewer lanes idle (16384 rows of 2048 with a residual and codes, us, with one
+// to four steps: 50.2, 46.8, 46.9, 47.7; 4095 of 2080 from fp32 with a scale a row: 18.9, 17.7, 17.3, 19.6).  With few rows one, for the
+// shortest chain; more where a row would take more than 16 warps.
 template <typename X, int V>
 int launch_norm(const NormArgs& a, cudaStream_t st) {
     const int chunks = a.n / V;
     if (chunks <= 512 && a.T < 8 * qmoe::sm_count()) return launch_norm_steps<X, V, 1>(a, st);
+    if (chunks <= 1024 && V == 8 && (chunks + 95) / 96 * 3 < (chunks + 63) / 64 * 2) return launch_norm_steps<X, V, V == 8 ? 3 : 2>(a, st);
     if (chunks <= 1024) return launch_norm_steps<X, V, 2>(a, st);
     if constexpr (V == 8) return launch_norm_steps<X, V, 4>(a, st);
     else return chunks <= 4096 ? launch_norm_steps<X, V, 8>(a, st) : launch_norm_steps<X, V, 32>(a, st);

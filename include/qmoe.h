@@ -637,7 +637,7 @@ int qk_norm_rope(const void* qkv, int64_t row_stride, int T, int n_q_heads, int 
 /*
  * Norm of whole rows, with the residual's addition before it:
  *   h = x + residual,  residual_out = bf16(h),  y = h / sqrt(mean(h^2) + eps) * weight,
- * in fp32 (the norm is that of the unrounded h), each output rounded once.  In 8 bits: codes are
+ * in fp32 (the norm is that of the unrounded h; the products h weight come first), each output rounded once.  In 8 bits: codes are
  * e4m3 values of y / s (y before its rounding to bf16), nearest even, with s = max |y| / 448 over the
  * row or over each 128 values of it (the last run of a row may be shorter); s is 0 and the codes 0
  * where all y are 0.

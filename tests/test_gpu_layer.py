@@ -833,3 +833,31 @@ def test_calls_on_no_rows_and_on_rows_of_no_request(n):
     Q.qmoe_route_scored(torch.zeros((0, 64), device=DEV), 2, torch.zeros((0, 2), **i32), torch.zeros((0, 2), device=DEV))
     Q.kv4_block_bounds(cache, b, zero[:0])
     ok()
+
+
+@pytest.mark.parametrize("n", [256, 264, 2048, 2080])
+def test_codes_of_rows_whose_outputs_vanish(n):
+    # an infinite value makes all other outputs of its row 0; so does a row without a value, or a weight of 0
+    x = torch.randn((300, n), device=DEV, generator=torch.Generator(DEV).manual_seed(4))
+    x[0, 9] = float("inf")
+    x[1, 9] = float("nan")
+    x[2] = 0
+    x[3, 128:] = 0
+    w = torch.ones(n, dtype=torch.bfloat16, device=DEV)
+    w[:128] = 0
+    groups = (n + 127) // 128
+    for weight in (None, w):
+        for g in (1, groups):
+            codes, scales = torch.empty((300, n), dtype=torch.uint8, device=DEV), torch.empty((300, g), device=DEV)
+            Q.add_rms_norm(x, weight, 1e-5, codes=codes, scales=scales)
+            ok()
+            c, s = codes.cpu().numpy() & 0x7F, f64(scales)
+            if g == 1:
+                assert (c[0] == 0x7F).all() and np.isnan(s[0]).all()
+            else:
+                assert (c[0, :128] == 0x7F).all() and np.isnan(s[0, 0]) and not c[0, 128:].any() and not s[0, 1:].any()
+                assert not c[3, 128:].any() and not s[3, 1:].any()
+                if weight is not None:
+                    assert not c[4:, :128].any() and not s[4:, 0].any()
+            assert (c[1] == 0x7F).all() and np.isnan(s[1]).all() and not c[2].any() and not s[2].any()
+            assert ((c[4:].reshape(296, -1) == 0x7E).any(1)).all() and not (c[4:] == 0x7F).any()
