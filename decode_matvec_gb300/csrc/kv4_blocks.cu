@@ -191,7 +191,7 @@ __device__ __forceinline__ float query_value(uint32_t bits) {
 
 // The queries of one token and kv head as whole numbers: sums over the group of the positive parts, then of the negative
 // ones, 16 bits each.  A warp takes a (token, kv head), a lane D / 32 channels.  A kernel of its own: made again in every thread
-// block of the scores they cost 21.9 us for 64 requests of up to 32768 tokens instead of 19.4.  One chain of loads bounds it.
+// block of the scores they cost 2.5 us more for 64 requests of up to 32768 tokens.  One chain of loads bounds it, 2.5 us.
 constexpr int kWholeThreads = 128;
 
 template <int D>
@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(kWholeThreads) whole_kernel(SelectArgs a) {
 // multiprocessor have what its bandwidth takes under way; then groups of L lanes (16 codes of a record each) multiply kRecords records
 // of one kv head at a time with the group's summed queries, and the partial sums are added up crosswise, so that lane i ends with
 // record i (mod kRecords).  What does not depend on the queries goes ahead of the wait for them.  The latency table - copy - product
-// bounds it: 64 requests of up to 32768 tokens, 8 kv heads of 128, pages of 64, 37 MB, take 19.6 us with whole_kernel and pick_kernel (this one
-// alone, cold caches, 12.8: 42 % of the copy rate), and 21 to 23 where the records go through registers.
+// bounds it: 64 requests of up to 32768 tokens, 8 kv heads of 128, pages of 64, 37 MB, take 10.9 us behind whole_kernel's 2.5 (cold caches, 12.8: 42 % of the copy rate), 1.5 to 3 more where the records go
+// through registers.
 constexpr int kScoreBytes = 32768, kScoreHeads = 32, kRecords = 8, kMostPages = 256;
 constexpr uint32_t kWaitLimit = 1u << 22;
 
@@ -368,10 +368,10 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, int 
 // The list of one (token, kv head) is made by a warp (up to 1024 blocks to choose from) or a thread block.  Scores are kept in
 // registers as integer keys, warp w those of the w-th equal run.  The key of the last one taken is found between the
 // smallest and the largest by trying three keys at a time (a count each, all three in one word), until as many are above
-// one of them as are wanted or nothing is left between; then every warp writes the blocks of its run that are above it, and the
-// first ones at it.  Some ten rounds one after the other, each a count and its sum, bound it: about 5 us for 512 lists of up to 512 scores.  Tries
-// that are not a quarter apart as keys (as values; where the counts so far point to) take longer: 64 requests' choice 20.3 to 20.5 us
-// instead of 19.6, and 13.5 to 15.1 instead of 11.8 for 8192 scores a list.
+// one of them as are wanted, or no more than 32 are left between: those are counted against each other.  Then every warp writes the
+// blocks of its run that are above it, and the first ones at it.  Rounds one after the other, each a count and its sum, bound it: 64 requests' choice takes
+// 13.4 us without this kernel and 17.7 with it (20.1 where the tries go on to the last key), 4 lists of 8192 scores 4.4 and 10.4 (11.5).
+// Tries that are not a quarter apart as keys (as values; where the counts so far point to) take longer.
 constexpr int kMostBlocks = 1 << 20;      // of a request
 constexpr int kPickThreads = 128;        // of a block whose warps make a list each
 
@@ -386,6 +386,9 @@ template <int WARPS, int R>
 __global__ void __launch_bounds__(WARPS == 1 ? kPickThreads : WARPS * 32) pick_kernel(SelectArgs a) {
     __shared__ uint2 part_s[2][WARPS];
     __shared__ unsigned long long count_s[2][WARPS];
+    constexpr int LISTS = WARPS == 1 ? kPickThreads / 32 : 1;
+    __shared__ alignas(16) uint32_t left_s[LISTS][32];
+    __shared__ int n_left_s[LISTS];
     const int lane = threadIdx.x & 31, warp = WARPS == 1 ? 0 : threadIdx.x >> 5;
     const int64_t list = WARPS == 1 ? (int64_t)blockIdx.x * (kPickThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
     const int tid = warp * 32 + lane;
@@ -408,6 +411,12 @@ __global__ void __launch_bounds__(WARPS == 1 ? kPickThreads : WARPS * 32) pick_k
     if (want == 0) return;
     const int per = R ? R * 32 : ((hi - lo + WARPS - 1) / WARPS + 31) & ~31;
     const int w0 = min(lo + warp * per, hi), w1 = min(w0 + per, hi), steps = R ? R : (w1 - w0 + 31) / 32;
+    uint32_t* left = left_s[WARPS == 1 ? threadIdx.x >> 5 : 0];
+    int* n_left = &n_left_s[WARPS == 1 ? threadIdx.x >> 5 : 0];
+    if (warp == 0) {
+        left[lane] = 0;
+        if (lane == 0) *n_left = 0;
+    }
     uint32_t key[R ? R : 1];
     if constexpr (R > 0) {
 #pragma unroll
@@ -440,9 +449,9 @@ __global__ void __launch_bounds__(WARPS == 1 ? kPickThreads : WARPS * 32) pick_k
         least = __reduce_min_sync(QMOE_FULL_MASK, p.x), end = __reduce_max_sync(QMOE_FULL_MASK, p.y);
     }
     ++end;
-    // ---- at least `want` keys are >= least, fewer are >= end
-    bool exact = false;         // as many as are wanted are >= least: none of the others
-    for (int turn = 0; end - least > 1 && !exact; turn ^= 1) {
+    // ---- `from` keys are >= least, at least as many as are wanted; `above_end` are >= end, fewer
+    int from = hi - lo, above_end = 0;
+    for (int turn = 0; end - least > 1 && from > want && from - above_end > 32; turn ^= 1) {
         const uint32_t span = end - least, q = span >= 4 ? span >> 2 : 1;
         const uint32_t p1 = least + q, p2 = min(p1 + q, end), p3 = min(p2 + q, end);
         int n1 = 0, n2 = 0, n3 = 0;
@@ -468,13 +477,55 @@ __global__ void __launch_bounds__(WARPS == 1 ? kPickThreads : WARPS * 32) pick_k
             n3 = (int)__reduce_add_sync(QMOE_FULL_MASK, (uint32_t)(v >> 42));
         }
         // (p3 >= p2 >= p1, counts the other way; a p at end counts none)
-        if (n3 >= want) least = p3, exact = n3 == want;
-        else if (n2 >= want) least = p2, exact = n2 == want, end = p3;
-        else if (n1 >= want) least = p1, exact = n1 == want, end = p2;
-        else end = p1;
+        if (n3 >= want) least = p3, from = n3;
+        else if (n2 >= want) least = p2, from = n2, end = p3, above_end = n3;
+        else if (n1 >= want) least = p1, from = n1, end = p2, above_end = n2;
+        else end = p1, above_end = n1;
+    }
+    uint32_t cut = least;
+    if (end - least > 1 && from > want) {
+        // ---- at most 32 are between: side by side, a lane each, which counts the larger ones
+        if (WARPS == 1) __syncwarp();
+#pragma unroll
+        for (int i = 0; i < (R ? R : steps); ++i) {
+            const uint32_t k = key_at(i);
+            if (k >= least && k < end) left[atomicAdd(n_left, 1)] = k;
+        }
+        if (WARPS == 1) __syncwarp();
+        else __syncthreads();
+        const int between = from - above_end;
+        const uint32_t mine = left[lane];
+        int larger = 0;
+        for (int j = 0; j < between; j += 4) {
+            const uint4 o = *(const uint4*)(left + j);
+            larger += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+        }
+        cut = __reduce_min_sync(QMOE_FULL_MASK, lane < between && above_end + larger < want ? mine : 0xFFFFFFFFu);
+        from = above_end + __popc(__ballot_sync(QMOE_FULL_MASK, lane < between && mine >= cut));
+    }
+    const unsigned below = (1u << lane) - 1;
+    if (from == want) {
+        // ---- the blocks from `cut` on, all of them
+        int before = 0;
+        if (WARPS > 1) {
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < (R ? R : steps); ++i) n += key_at(i) >= cut;
+            n = (int)__reduce_add_sync(QMOE_FULL_MASK, (unsigned)n);
+            if (lane == 0) part_s[1][warp] = make_uint2((unsigned)n, 0u);
+            __syncthreads();
+            before = (int)__reduce_add_sync(QMOE_FULL_MASK, lane < warp ? part_s[1][lane].x : 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < (R ? R : steps); ++i) {
+            const bool in = key_at(i) >= cut;
+            const unsigned hit = __ballot_sync(QMOE_FULL_MASK, in);
+            if (in) sel[a.first + before + __popc(hit & below)] = w0 + 32 * i + lane;
+            before += __popc(hit);
+        }
+        return;
     }
     // ---- the blocks above `cut`, and `room` of those at it
-    const uint32_t cut = least;
     int above = 0, equal = 0;
 #pragma unroll
     for (int i = 0; i < (R ? R : steps); ++i) {
@@ -493,7 +544,6 @@ __global__ void __launch_bounds__(WARPS == 1 ? kPickThreads : WARPS * 32) pick_k
         equal_before = (int)__reduce_add_sync(QMOE_FULL_MASK, lane < warp ? p.y : 0u);
     }
     const int room = want - all_above;
-    const unsigned below = (1u << lane) - 1;
 #pragma unroll
     for (int i = 0; i < (R ? R : steps); ++i) {
         const uint32_t k = key_at(i);
@@ -613,6 +663,9 @@ extern "C" int kv4_select_blocks(const kv4_bounds* bounds, const void* q, int n_
     if ((rc = kv4::launch_dependent(d128 ? score_kernel<128> : score_kernel<64>, dim3((unsigned)blocks, (unsigned)((n_kv + kScoreHeads - 1) / kScoreHeads)), kScoreThreads, 0, st, who, a, (int)chunks, pages))) return rc;
     const int64_t most = ((int64_t)max_kv + bounds->page_size - 1) / bounds->page_size - first - last;      // blocks a list chooses from
     if (most <= 128) return kv4::launch_dependent(pick_kernel<1, 4>, dim3(by_warps), kPickThreads, 0, st, who, a);
+    // (few lists by four warps each, for the shorter chain; us of a whole call of 4, 16, 64 and 256 requests with 8 kv heads, four warps a
+    // list: 6.9, 8.7, 17.8, 39.7; one: 8.1, 9.7, 17.7, 39.1)
+    if (most <= 512 && lists <= 2 * (unsigned)qmoe::sm_count()) return kv4::launch_dependent(pick_kernel<4, 4>, dim3(lists), 128, 0, st, who, a);
     if (most <= 512) return kv4::launch_dependent(pick_kernel<1, 16>, dim3(by_warps), kPickThreads, 0, st, who, a);
     if (most <= 2048) return kv4::launch_dependent(pick_kernel<8, 8>, dim3(lists), 256, 0, st, who, a);
     if (most <= 8192) return kv4::launch_dependent(pick_kernel<32, 8>, dim3(lists), 1024, 0, st, who, a);

@@ -861,3 +861,31 @@ def test_codes_of_rows_whose_outputs_vanish(n):
                     assert not c[4:, :128].any() and not s[4:, 0].any()
             assert (c[1] == 0x7F).all() and np.isnan(s[1]).all() and not c[2].any() and not s[2].any()
             assert ((c[4:].reshape(296, -1) == 0x7E).any(1)).all() and not (c[4:] == 0x7F).any()
+
+
+@pytest.mark.parametrize("B,n_kv,page,lens,top", [
+    (3, 1, 16, 8000, 33), (40, 8, 16, 2100, 9), (2, 2, 16, 8190, 300), (1, 1, 16, 120000, 128), (2, 1, 16, 33000, 40), (45, 8, 64, 32000, 64)])
+def test_select_blocks_by_every_split_of_a_list(B, n_kv, page, lens, top):
+    # lists of few distinct scores (whole tiers of equal ones at the last place taken), of distinct ones, and of one score alone
+    r = np.random.RandomState(B + page + top)
+    D, blocks = 64, (lens + page - 1) // page
+    n_pages = max(512, blocks)
+    table = np.stack([r.permutation(n_pages)[:blocks] for _ in range(B)]).astype(np.int32)
+    kv = r.randint(lens // 2, lens + 1, B).astype(np.int32)
+    kv[0] = lens
+    q = r.randn(B, n_kv, D)
+    qt, q = bf(q)
+    for kind in range(3):
+        codes = r.randint(-127, 128, (n_pages, n_kv, 2, D)) if kind < 2 else np.ones((n_pages, n_kv, 2, D))
+        if kind == 1:
+            codes[:] = codes[:3][r.randint(0, 3, n_pages)]
+        codes = np.sort(codes, 2)[:, :, ::-1].astype(np.int8)
+        steps = np.full((n_pages, n_kv), 0.125, np.float32)
+        bounds = Q.Kv4Bounds(torch.tensor(codes.copy(), device=DEV), torch.tensor(steps, device=DEV), page)
+        ws = torch.empty(Q.kv4_select_blocks_ws_size(B, n_kv, page, lens), dtype=torch.uint8, device=DEV)
+        sel = torch.full((B, n_kv, top), -7, dtype=torch.int32, device=DEV)
+        Q.kv4_select_blocks(bounds, qt, torch.arange(B + 1, dtype=torch.int32, device=DEV), torch.tensor(kv, device=DEV),
+                            torch.tensor(table, device=DEV), sel, ws, lens)
+        ok()
+        want = Y.select(q, np.arange(B + 1), kv, table, codes, steps, page, top, 1, 1, np.full((B, n_kv, top), -7), lens)
+        assert np.array_equal(sel.cpu().numpy(), want)
