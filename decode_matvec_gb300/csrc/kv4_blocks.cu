@@ -15,17 +15,12 @@ __device__ int g_kv4_blocks_error;
 
 __device__ __forceinline__ void blocks_set_error(int code) { atomicCAS(&g_kv4_blocks_error, 0, code); }
 
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+// Half-precision factors, one rounding to fp32: a's lower and upper halves times b's lower half, plus c.
+__device__ __forceinline__ float2 fma_halves(uint32_t a, uint32_t b, float c) {
     float2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(*(unsigned long long*)&r) : "l"(*(unsigned long long*)&a), "l"(*(unsigned long long*)&b));
-    return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(*(unsigned long long*)&r)
-        : "l"(*(unsigned long long*)&a), "l"(*(unsigned long long*)&b), "l"(*(unsigned long long*)&c));
+    asm("{\n .reg .b16 al, ah, bl, bh;\n mov.b32 {al, ah}, %2;\n mov.b32 {bl, bh}, %3;\n fma.rn.f32.f16 %0, al, bl, %4;\n fma.rn.f32.f16 %1, ah, bl, %4;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(a), "r"(b), "f"(c));
     return r;
 }
 
@@ -42,7 +37,8 @@ struct BoundsArgs {
 // L = head_dim / 8 lanes hold a row of codes (a word, 8 channels, a lane); the rows of a block are dealt out over the four
 // warps, all of a lane's loads in flight together, and joined in shared memory, where a thread takes a channel.  The instructions bound
 // it: 8 of a word's codes made fp32 values, exactly, and compared twice (16 prompts of 777 to 2048 tokens, 8 heads of 128, pages of 64:
-// 9.4 us for 12 MB, 2300 instructions a block and head, 62 % of the issue slots; 10.2 us without the packed arithmetic).
+// 8.1 us for 12 MB, 2000 instructions a block and head, 61 % of the issue slots; 9.4 us with codes made fp32 and packed fp32 arithmetic,
+// 2300 instructions).
 constexpr int kBoundsThreads = 128;
 
 template <int L>
@@ -82,8 +78,8 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(BoundsArgs a, in
                 w[k] = words[r * L + gl], sz[k] = pairs[r];
             }
         }
-        // Rows past the block's end repeat a row of it.  A code is a float's low bits above 2^23, where it stands in its
-        // half of the word: 16^i u, which a scale of s 16^-i makes the same product, exactly.
+        // Rows past the block's end repeat a row of it.  A code in the lowest bits of a half is u 2^-24 as a subnormal half, four bits up
+        // 16 times that: s u + z comes out 2^-24 or 2^-20 of itself, with the same rounding, and is brought back at the end.
         float lo[8], hi[8];
 #pragma unroll
         for (int c = 0; c < 8; ++c) lo[c] = INFINITY, hi[c] = -INFINITY;
@@ -93,15 +89,11 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(BoundsArgs a, in
             float v[2][8];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const float2 p = __half22float2(sz[k + x]);
-                const float2 z = make_float2(p.y, p.y);
+                const float z0 = __high2float(sz[k + x]) * (1.f / (1 << 24)), z1 = z0 * 16.f;
+                const uint32_t s = *(const uint32_t*)&sz[k + x];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float one = p.x * (1.f / (float)(1 << 4 * i));
-                    const float2 u = add2(make_float2(__uint_as_float((w[k + x] & 15u << 4 * i) | 0x4B000000u),
-                                                      __uint_as_float((w[k + x] >> 16 & 15u << 4 * i) | 0x4B000000u)),
-                                          make_float2(-8388608.f, -8388608.f));
-                    const float2 r = fma2(make_float2(one, one), u, z);
+                    const float2 r = fma_halves((w[k + x] >> (i & 2) * 4) & (i & 1 ? 0x00F000F0u : 0x000F000Fu), s, i & 1 ? z1 : z0);
                     v[x][2 * i] = r.x, v[x][2 * i + 1] = r.y;
                 }
             }
@@ -115,6 +107,8 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(BoundsArgs a, in
                 lo[c] = fminf(lo[c], __shfl_xor_sync(QMOE_FULL_MASK, lo[c], d));
                 hi[c] = fmaxf(hi[c], __shfl_xor_sync(QMOE_FULL_MASK, hi[c], d));
             }
+            const float up = c >> 1 & 1 ? (float)(1 << 20) : (float)(1 << 24);
+            lo[c] *= up, hi[c] *= up;
         }
         if (lane < L) {
 #pragma unroll
