@@ -332,11 +332,12 @@ constexpr float kUlp = 5.9604645e-8f;       // 2^-24
 constexpr float kLargest = 3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// fp32 -> integer of the same order (-0 as 0); 0 stands for no value.
-__device__ __forceinline__ uint32_t key_of(float v) {
-    const uint32_t u = __float_as_uint(v + 0.f);
+// fp32 -> integer of the same order (-0 as 0; key_of_sum: there is none); 0 stands for no value.
+__device__ __forceinline__ uint32_t key_of_sum(float v) {
+    const uint32_t u = __float_as_uint(v);
     return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ uint32_t key_of(float v) { return key_of_sum(v + 0.f); }
 __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
@@ -449,16 +450,19 @@ __device__ __forceinline__ void best_keys(const uint32_t (&key)[R], uint32_t (&l
 // The `rounds` best of all lanes' lists: lane j gets the j-th one's key and the lane that held it.
 template <int N>
 __device__ __forceinline__ void choose(uint32_t (&list)[N], int rounds, int lane, uint32_t* my_key, int* my_lane) {
-    *my_key = 0, *my_lane = 0;
+    const unsigned below = (1u << lane) - 1;
+    unsigned mine_held = 1;
+    *my_key = 0;
     for (int j = 0; j < rounds; ++j) {
         const uint32_t m = __reduce_max_sync(QMOE_FULL_MASK, list[0]);
-        const int w = __ffs(__ballot_sync(QMOE_FULL_MASK, list[0] == m)) - 1;
-        if (lane == j) *my_key = m, *my_lane = w;
-        const bool mine = lane == w;
+        const unsigned held = __ballot_sync(QMOE_FULL_MASK, list[0] == m);
+        if (lane == j) *my_key = m, mine_held = held;
+        const bool mine = list[0] == m && !(held & below);
 #pragma unroll
         for (int i = 0; i + 1 < N; ++i) list[i] = mine ? list[i + 1] : list[i];
         list[N - 1] = mine ? 0u : list[N - 1];
     }
+    *my_lane = __ffs(mine_held) - 1;
 }
 
 // Whether a lane's list (`had`: it was not empty) ran out while it held another of the `rounds` best.
@@ -514,7 +518,22 @@ struct Pair {
 };
 __device__ __forceinline__ Pair merge(Pair x, Pair y) { return Pair{max(x.a, y.a), max(min(x.a, y.a), max(x.b, y.b))}; }
 
-// Which groups are kept (bit g of the result), from values that lane g holds for g < groups.
+// Which groups are kept (bit g of the result), from keys that lane g holds for g < groups (others 0); the last one kept and the
+// best one dropped.
+__device__ __forceinline__ uint32_t best_groups(uint32_t key, int top, int lane, uint32_t* last, uint32_t* next) {
+    const unsigned below = (1u << lane) - 1;
+    uint32_t kept = 0, m = 0;
+    for (int j = 0; j < top; ++j) {
+        m = __reduce_max_sync(QMOE_FULL_MASK, key);
+        const unsigned held = __ballot_sync(QMOE_FULL_MASK, key == m);
+        kept |= held & (0u - held);
+        if (key == m && !(held & below)) key = 0;
+    }
+    *last = m, *next = __reduce_max_sync(QMOE_FULL_MASK, key);
+    return kept;
+}
+
+// The same from values, by comparing each with each.
 template <typename F>
 __device__ __forceinline__ uint32_t best_groups(F v, int groups, int top, int lane) {
     int rank = 0;
@@ -749,7 +768,7 @@ __device__ __forceinline__ Doubts doubts_of(const RouteArgs& a, uint32_t mk, int
 }
 
 // R experts a lane, a warp a token.  Instructions bound it, and the latency of a round (a reduction, a ballot, a list that moves up): 16383
-// tokens of 256 experts in 8 groups, the best 8 by sigmoid scores and a bias, 16.3 us and 830 instructions a token, 67 % of
+// tokens of 256 experts in 8 groups, the best 8 by sigmoid scores and a bias, 16.0 us and 790 instructions a token, 61 to 67 % of
 // the issue slots; 32 tokens 3.6 to 4.2 us.  A warp that goes on to another token with its logits loaded ahead took 19 us.
 template <typename X, int R>
 __global__ void __launch_bounds__(kTokenWarps * 32, R <= 8 ? 8 : 4) route_kernel(RouteArgs a) {
@@ -787,11 +806,14 @@ __global__ void __launch_bounds__(kTokenWarps * 32, R <= 8 ? 8 : 4) route_kernel
         float bias[R];
         load_values<float, R>(a.bias, e0, a.E, a.vec_bias, 0.f, bias);
 #pragma unroll
-        for (int i = 0; i < R; ++i) c[i] = fmaxf(score_near(c[i]) + bias[i], -INFINITY);      // (an infinite bias may give NaN)
+        for (int i = 0; i < R; ++i) c[i] = fmaxf(score_near(c[i]) + bias[i], -INFINITY);      // (an infinite bias may give NaN; never -0)
+    } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i) c[i] += 0.f;
     }
     uint32_t key[R], list[kDepth<R>];
 #pragma unroll
-    for (int i = 0; i < R; ++i) key[i] = key_of(c[i]);
+    for (int i = 0; i < R; ++i) key[i] = key_of_sum(c[i]);
     if (e0 + R > a.E) {
 #pragma unroll
         for (int i = 0; i < R; ++i)
@@ -820,22 +842,20 @@ __global__ void __launch_bounds__(kTokenWarps * 32, R <= 8 ? 8 : 4) route_kernel
                 if (lane == g) mine = p;
             }
         }
-        uint32_t kept;
+        const bool on = lane < a.groups;
+        uint32_t kept, last, next;
         if (by_logit && a.best == 1) {
-            kept = best_groups(mine.a, a.groups, a.top_groups, lane);
+            kept = best_groups(on ? mine.a : 0u, a.top_groups, lane, &last, &next);
         } else {
             float va = value_of(mine.a), vb = a.best == 2 ? value_of(mine.b) : 0.f;
             if (by_logit) va = score_near(va), vb = score_near(vb);      // (sums of scores)
-            const bool on = lane < a.groups;
             const float v = on ? fmaxf(va + vb, -INFINITY) : -INFINITY;
-            kept = best_groups(v, a.groups, a.top_groups, lane);
+            kept = best_groups(on ? key_of(v) : 0u, a.top_groups, lane, &last, &next);
             if (a.top_groups < a.groups) {
                 // the last one kept and the best one dropped
                 const float mag = fabsf(va) + fabsf(vb);
                 const float err = on ? 2.f * score_err + (mag < kLargest ? 2.f * kUlp * mag : 0.f) : 0.f;
-                const bool is = (kept >> lane) & 1;
-                const float low = value_of(~__reduce_max_sync(QMOE_FULL_MASK, is ? ~key_of(v) : 0u));
-                const float high = value_of(__reduce_max_sync(QMOE_FULL_MASK, on && !is ? key_of(v) : 0u));
+                const float low = value_of(last), high = value_of(next);
                 const float err2 = 2.f * __uint_as_float(__reduce_max_sync(QMOE_FULL_MASK, __float_as_uint(err)));
                 // (infinite ones are equal or not, whatever the bits: NaN here)
                 if (__builtin_expect(low - high <= err2, 0)) {
