@@ -37,7 +37,7 @@ struct BoundsArgs {
 // L = head_dim / 8 lanes hold a row of codes (a word, 8 channels, a lane); the rows of a block are dealt out over the four
 // warps, all of a lane's loads in flight together, and joined in shared memory, where a thread takes a channel.  The instructions bound
 // it: 8 of a word's codes made fp32 values, exactly, and compared twice (16 prompts of 777 to 2048 tokens, 8 heads of 128, pages of 64:
-// 8.1 us for 12 MB, 2000 instructions a block and head, 61 % of the issue slots; 9.4 us with codes made fp32 and packed fp32 arithmetic,
+// 8.1 us for 12 MB, 2000 instructions a block and head, 60 % of the issue slots; 9.4 us with codes made fp32 and packed fp32 arithmetic,
 // 2300 instructions).
 constexpr int kBoundsThreads = 128;
 
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kWholeThreads) whole_kernel(SelectArgs a) {
 // multiprocessor have what its bandwidth takes under way; then groups of L lanes (16 codes of a record each) multiply kRecords records
 // of one kv head at a time with the group's summed queries, and the partial sums are added up crosswise, so that lane i ends with
 // record i (mod kRecords).  What does not depend on the queries goes ahead of the wait for them.  The latency table - copy - product
-// bounds it: 64 requests of up to 32768 tokens, 8 kv heads of 128, pages of 64, 37 MB, take 10.9 us behind whole_kernel's 2.5 (cold caches, 12.8: 42 % of the copy rate), 1.5 to 3 more where the records go
+// bounds it: 64 requests of up to 32768 tokens, 8 kv heads of 128, pages of 64, 37 MB, take 10.9 us behind whole_kernel's 2.5 (cold caches, 13 to 15: 40 % of the copy rate), 1.5 to 3 more where the records go
 // through registers.
 constexpr int kScoreBytes = 32768, kScoreHeads = 32, kRecords = 8, kMostPages = 256;
 constexpr uint32_t kWaitLimit = 1u << 22;

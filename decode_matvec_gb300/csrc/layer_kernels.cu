@@ -768,8 +768,8 @@ __device__ __forceinline__ Doubts doubts_of(const RouteArgs& a, uint32_t mk, int
 }
 
 // R experts a lane, a warp a token.  Instructions bound it, and the latency of a round (a reduction, a ballot, a list that moves up): 16383
-// tokens of 256 experts in 8 groups, the best 8 by sigmoid scores and a bias, 16.0 us and 790 instructions a token, 61 to 67 % of
-// the issue slots; 32 tokens 3.6 to 4.2 us.  A warp that goes on to another token with its logits loaded ahead took 19 us.
+// tokens of 256 experts in 8 groups, the best 8 by sigmoid scores and a bias, 16.0 us and 790 instructions a token, 66 % of the
+// issue slots; 32 tokens 3.6 to 4.2 us.  A warp that goes on to another token with its logits loaded ahead took 19 us.
 template <typename X, int R>
 __global__ void __launch_bounds__(kTokenWarps * 32, R <= 8 ? 8 : 4) route_kernel(RouteArgs a) {
     qmoe::depend_wait();
@@ -929,8 +929,8 @@ __global__ void __launch_bounds__(kTokenWarps * 32, R <= 8 ? 8 : 4) route_kernel
 // Many experts without groups: a block of 4 warps a token, R values a thread in loads that stand side by side.  In each warp
 // the `rounds`-th largest of the lanes' maxima bounds the values to look at from below, and the largest of the warps' bounds
 // does for all; the few values that reach it are put side by side in shared memory, and the first warp's rounds go over
-// those, by key and index.  The three barriers of a row bound it: 4096 tokens of 2048 fp32 logits, 2 by softmax and a bias, 17.6 us, 1.9 TB/s,
-// 46 % of the issue slots (a warp a token 21 to 23 us).
+// those, by key and index.  The three barriers of a row bound it: 4096 tokens of 2048 fp32 logits, 2 by softmax and a bias, 17.2 us, 2 TB/s,
+// 51 % of the issue slots (a warp a token 21 to 23 us).
 constexpr int kWideMost = 256;      // values put side by side; rows with more (many equal ones) take exact_choice
 
 template <typename X, int R>
@@ -963,6 +963,25 @@ __global__ void __launch_bounds__(kWideWarps * 32, R <= 16 ? 10 : R <= 32 ? 5 : 
     }
     if (tid == 0) count_s = 0;
     const bool by_logit = !a.bias;
+    // the bias, where registers hold it as well: behind the barrier of the sum it would be waited for (18.0 -> 17.5 us)
+    constexpr bool kAhead = R <= 16;
+    const bool vec_bias = a.vec && a.vec_bias;
+    float bias[kAhead ? R : 4];
+    auto load_bias = [&](int i, float* to) {
+        float v[4];
+        if (vec_bias) {
+            load_values<float, 4>(a.bias, expert(i), a.E, 1, 0.f, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = expert(i + j) < a.E ? a.bias[expert(i + j)] : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) to[j] = v[j];
+    };
+    if (kAhead && !by_logit) {
+#pragma unroll
+        for (int i = 0; i < R; i += 4) load_bias(i, bias + (kAhead ? i : 0));
+    }
     float top = 0.f, z = 1.f, inv_z = 1.f, scale = 1.f;
     if (!a.sigmoid && !(by_logit && a.renorm)) {
         // a warp's exponentials are by its own largest logit until the block's is known
@@ -997,15 +1016,10 @@ __global__ void __launch_bounds__(kWideWarps * 32, R <= 16 ? 10 : R <= 32 ? 5 : 
         }
 #pragma unroll
         for (int i = 0; i < R; i += 4) {
-            float bias[4];
-            if (a.vec && a.vec_bias) {
-                load_values<float, 4>(a.bias, expert(i), a.E, 1, 0.f, bias);
-            } else {
+            if (!kAhead) load_bias(i, bias);
+            const float* add = bias + (kAhead ? i : 0);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) bias[j] = expert(i + j) < a.E ? a.bias[expert(i + j)] : 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) c[i + j] = fmaxf(fmaf(c[i + j], scale, bias[j]), -INFINITY);
+            for (int j = 0; j < 4; ++j) c[i + j] = fmaxf(fmaf(c[i + j], scale, add[j]), -INFINITY);
         }
         if (a.E < THREADS * R) {
 #pragma unroll
