@@ -864,7 +864,8 @@ def test_codes_of_rows_whose_outputs_vanish(n):
 
 
 @pytest.mark.parametrize("B,n_kv,page,lens,top", [
-    (3, 1, 16, 8000, 33), (40, 8, 16, 2100, 9), (2, 2, 16, 8190, 300), (1, 1, 16, 120000, 128), (2, 1, 16, 33000, 40), (45, 8, 64, 32000, 64)])
+    (3, 1, 16, 8000, 33), (40, 8, 16, 2100, 9), (2, 2, 16, 8190, 300), (1, 1, 16, 120000, 128), (2, 1, 16, 33000, 40), (45, 8, 64, 32000, 64),
+    (1, 1, 16, 200000, 64), (2, 1, 16, 300000, 9000)])
 def test_select_blocks_by_every_split_of_a_list(B, n_kv, page, lens, top):
     # lists of few distinct scores (whole tiers of equal ones at the last place taken), of distinct ones, and of one score alone
     r = np.random.RandomState(B + page + top)
