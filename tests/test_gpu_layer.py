@@ -890,3 +890,13 @@ def test_select_blocks_by_every_split_of_a_list(B, n_kv, page, lens, top):
         ok()
         want = Y.select(q, np.arange(B + 1), kv, table, codes, steps, page, top, 1, 1, np.full((B, n_kv, top), -7), lens)
         assert np.array_equal(sel.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("E", [7, 256, 2000])
+def test_renormalised_gate_of_one_expert_is_the_scale(E, sigmoid):
+    logits = 30 * torch.randn((777, E), device=DEV, generator=torch.Generator(DEV).manual_seed(5))
+    ids, gates = torch.empty((777, 1), dtype=torch.int32, device=DEV), torch.empty((777, 1), device=DEV)
+    Q.qmoe_route_scored(logits, 1, ids, gates, sigmoid=sigmoid, renormalise=True, scale=2.5)
+    ok()
+    assert torch.equal(ids[:, 0].long(), logits.argmax(1)) and bool((gates == 2.5).all())
