@@ -742,12 +742,16 @@ __device__ __forceinline__ void write_route(const RouteArgs& a, int64_t t, int i
 }
 
 // Which of the list that the lanes hold, largest first, are too near to tell apart (key mk of expert at, whose logit is l; one
-// entry more than are chosen, where there is one).
+// entry more than are chosen, where there is one).  Two neighbours of the same logit and bias are no doubt; where they are the last one
+// chosen and the one behind it, what stands behind both may still be larger than they are, and only what equals them may not.
 struct Doubts {
     bool any;        // some two neighbours
+    bool behind;     // what is behind the list has to be looked at
     bool mine;       // this lane's entry is one of such a pair, or equal to one that is
     float last;      // value of the last one chosen
     float least;     // what is below that for certain
+    int last_id;     // the last one chosen
+    float last_l, last_bias;
 };
 __device__ __forceinline__ Doubts doubts_of(const RouteArgs& a, uint32_t mk, int at, float l, float slack, int lane) {
     const float v = value_of(mk);
@@ -760,14 +764,22 @@ __device__ __forceinline__ Doubts doubts_of(const RouteArgs& a, uint32_t mk, int
         near = fabsf(v) < INFINITY && nv > -INFINITY ? v - nv <= 2.f * slack + kUlp * (fabsf(v) + fabsf(nv)) : v == nv;
         if (near) doubt = !(l == nl && a.bias[at] == a.bias[nat]);
     }
-    Doubts d{__any_sync(QMOE_FULL_MASK, doubt) != 0, false, 0.f, 0.f};
-    if (d.any || a.k == 32) {
-        const unsigned pairs = __ballot_sync(QMOE_FULL_MASK, near);
+    const unsigned pairs = __ballot_sync(QMOE_FULL_MASK, near);
+    Doubts d{__any_sync(QMOE_FULL_MASK, doubt) != 0, false, false, 0.f, 0.f, 0, 0.f, 0.f};
+    d.behind = d.any || a.k == 32 || (pairs >> (a.k - 1) & 1);
+    if (d.behind) {
         d.mine = ((pairs | pairs << 1) >> lane & 1) != 0;
         d.last = value_of(__shfl_sync(QMOE_FULL_MASK, mk, a.k - 1));
         d.least = d.last - (2.f * slack + 4.f * kUlp * fminf(fabsf(d.last), kLargest));
+        d.last_id = __shfl_sync(QMOE_FULL_MASK, at, a.k - 1), d.last_l = __shfl_sync(QMOE_FULL_MASK, l, a.k - 1);
+        d.last_bias = a.bias[d.last_id];
     }
     return d;
+}
+// Whether expert e, behind the list, equals the last one chosen and comes after it.  (With doubts in the list that one's place is open.)
+template <typename X>
+__device__ __forceinline__ bool comes_after(const RouteArgs& a, const X* row, const Doubts& d, int e) {
+    return !d.any && e >= d.last_id && logit(row, e) == d.last_l && a.bias[e] == d.last_bias;
 }
 
 // R experts a lane, a warp a token.  Instructions bound it, and the latency of a round (a reduction, a ballot, a list that moves up): 16383
@@ -911,13 +923,19 @@ __global__ void __launch_bounds__(kTokenWarps * 32, R <= 8 ? 8 : 4) route_kernel
     float l = in_list ? logit(row, at) : -INFINITY;
     if (!by_logit) {
         const Doubts d = doubts_of(a, mk, at, l, slack, lane);
-        if (__builtin_expect(d.any || a.k == 32, 0)) {
+        if (__builtin_expect(d.behind, 0)) {
             // experts outside the list that may belong into it: values down to the last one's less the errors
-            uint32_t cand = 0;
+            uint32_t cand = 0, open = 0;
 #pragma unroll
             for (int i = 0; i < R; ++i)
                 if (key[i] && !(value_of(key[i]) < d.least)) cand |= 1u << i;
-            bool again = warp_sum_int(__popc(cand)) > __popc(__ballot_sync(QMOE_FULL_MASK, in_list && !(value_of(mk) < d.least)));
+            for (uint32_t todo = cand; todo; todo &= todo - 1) {
+                const int i = __ffs((int)todo) - 1;
+                if (!comes_after(a, row, d, e0 + i)) open |= 1u << i;
+            }
+            const bool listed = in_list && !(value_of(mk) < d.least) && !comes_after(a, row, d, at);
+            __syncwarp();
+            bool again = warp_sum_int(__popc(open)) > __popc(__ballot_sync(QMOE_FULL_MASK, listed));
             if (!again && d.any) {
                 at = exact_order(a, row, __popc(__ballot_sync(QMOE_FULL_MASK, in_list)), value_of(mk), at, d.mine, top, z, sum_error(R));
                 again = at < 0;
@@ -1103,11 +1121,12 @@ __global__ void __launch_bounds__(kWideWarps * 32, R <= 16 ? 10 : R <= 32 ? 5 : 
             if (in_list) l = logit(row, at);
             if (!by_logit) {
                 const Doubts d = doubts_of(a, mk, at, l, slack, lane);
-                if (__builtin_expect(d.any || a.k == 32, 0)) {
-                    uint32_t rest = 0;      // the largest that is left
+                if (__builtin_expect(d.behind, 0)) {
+                    bool open = false;      // something that is left may belong to the chosen
 #pragma unroll
-                    for (int i = 0; i < MOST; ++i) rest = max(rest, key[i]);
-                    again = __any_sync(QMOE_FULL_MASK, rest && !(value_of(rest) < d.least));
+                    for (int i = 0; i < MOST; ++i)
+                        if (key[i] && !(value_of(key[i]) < d.least) && !comes_after(a, row, d, id[i])) open = true;
+                    again = __any_sync(QMOE_FULL_MASK, open);
                     if (!again && d.any) {
                         at = exact_order(a, row, __popc(__ballot_sync(QMOE_FULL_MASK, in_list)), value_of(mk), at, d.mine, top, z, sum_error(R));
                         again = at < 0;
