@@ -745,41 +745,52 @@ __device__ __forceinline__ void write_route(const RouteArgs& a, int64_t t, int i
 // entry more than are chosen, where there is one).  Two neighbours of the same logit and bias are no doubt; where they are the last one
 // chosen and the one behind it, what stands behind both may still be larger than they are, and only what equals them may not.
 struct Doubts {
+    bool behind;     // some two neighbours, or what is behind the list has to be looked at (else nothing below is set)
     bool any;        // some two neighbours
-    bool behind;     // what is behind the list has to be looked at
     bool mine;       // this lane's entry is one of such a pair, or equal to one that is
     float last;      // value of the last one chosen
     float least;     // what is below that for certain
     int last_id;     // the last one chosen
-    float last_l, last_bias;
 };
 __device__ __forceinline__ Doubts doubts_of(const RouteArgs& a, uint32_t mk, int at, float l, float slack, int lane) {
     const float v = value_of(mk);
     const uint32_t nk = __shfl_down_sync(QMOE_FULL_MASK, mk, 1);
     const int nat = __shfl_down_sync(QMOE_FULL_MASK, at, 1);
     const float nl = __shfl_down_sync(QMOE_FULL_MASK, l, 1);
-    bool near = false, doubt = false;
+    bool near = false, doubt = false, ask = false;
     if (lane < a.k && lane < 31 && mk && nk) {
         const float nv = value_of(nk);
         near = fabsf(v) < INFINITY && nv > -INFINITY ? v - nv <= 2.f * slack + kUlp * (fabsf(v) + fabsf(nv)) : v == nv;
-        if (near) doubt = !(l == nl && a.bias[at] == a.bias[nat]);
+        if (near) doubt = !(l == nl && a.bias[at] == a.bias[nat]), ask = doubt || lane == a.k - 1;
     }
-    const unsigned pairs = __ballot_sync(QMOE_FULL_MASK, near);
-    Doubts d{__any_sync(QMOE_FULL_MASK, doubt) != 0, false, false, 0.f, 0.f, 0, 0.f, 0.f};
-    d.behind = d.any || a.k == 32 || (pairs >> (a.k - 1) & 1);
-    if (d.behind) {
+    Doubts d{};
+    d.behind = __any_sync(QMOE_FULL_MASK, ask) || a.k == 32;
+    if (__builtin_expect(d.behind, 0)) {
+        const unsigned pairs = __ballot_sync(QMOE_FULL_MASK, near);
+        d.any = __any_sync(QMOE_FULL_MASK, doubt) != 0;
         d.mine = ((pairs | pairs << 1) >> lane & 1) != 0;
         d.last = value_of(__shfl_sync(QMOE_FULL_MASK, mk, a.k - 1));
         d.least = d.last - (2.f * slack + 4.f * kUlp * fminf(fabsf(d.last), kLargest));
-        d.last_id = __shfl_sync(QMOE_FULL_MASK, at, a.k - 1), d.last_l = __shfl_sync(QMOE_FULL_MASK, l, a.k - 1);
-        d.last_bias = a.bias[d.last_id];
+        d.last_id = __shfl_sync(QMOE_FULL_MASK, at, a.k - 1);
     }
     return d;
 }
-// Whether expert e, behind the list, equals the last one chosen and comes after it.  (With doubts in the list that one's place is open.)
+// Whether expert e equals the last one chosen and comes after it.  (With doubts in the list that one's place is open.)
 template <typename X>
-__device__ __forceinline__ bool comes_after(const RouteArgs& a, const X* row, const Doubts& d, int e) {
-    return !d.any && e >= d.last_id && logit(row, e) == d.last_l && a.bias[e] == d.last_bias;
+__device__ __forceinline__ bool comes_after(const RouteArgs& a, const X* row, int last, int e) {
+    return e >= last && logit(row, e) == logit(row, last) && a.bias[e] == a.bias[last];
+}
+// The experts that do not, of those that a lane names (bit i: e0 + i).  Out of line, and behind a count that most rows end with: 16383
+// tokens of 256 experts take 16.3 us without a look behind the list, 16.4 so and 16.7 with this in line and a second vote.
+template <typename X>
+__device__ __noinline__ uint32_t others(const RouteArgs& a, const X* row, int e0, uint32_t cand, int last) {
+    uint32_t open = cand;
+    for (uint32_t todo = cand; todo; todo &= todo - 1) {
+        const int i = __ffs((int)todo) - 1;
+        if (comes_after(a, row, last, e0 + i)) open &= ~(1u << i);
+    }
+    __syncwarp();
+    return open;
 }
 
 // R experts a lane, a warp a token.  Instructions bound it, and the latency of a round (a reduction, a ballot, a list that moves up): 16383
@@ -925,17 +936,15 @@ __global__ void __launch_bounds__(kTokenWarps * 32, R <= 8 ? 8 : 4) route_kernel
         const Doubts d = doubts_of(a, mk, at, l, slack, lane);
         if (__builtin_expect(d.behind, 0)) {
             // experts outside the list that may belong into it: values down to the last one's less the errors
-            uint32_t cand = 0, open = 0;
+            uint32_t cand = 0;
 #pragma unroll
             for (int i = 0; i < R; ++i)
                 if (key[i] && !(value_of(key[i]) < d.least)) cand |= 1u << i;
-            for (uint32_t todo = cand; todo; todo &= todo - 1) {
-                const int i = __ffs((int)todo) - 1;
-                if (!comes_after(a, row, d, e0 + i)) open |= 1u << i;
-            }
-            const bool listed = in_list && !(value_of(mk) < d.least) && !comes_after(a, row, d, at);
-            __syncwarp();
-            bool again = warp_sum_int(__popc(open)) > __popc(__ballot_sync(QMOE_FULL_MASK, listed));
+            const bool listed = in_list && !(value_of(mk) < d.least);
+            bool again = warp_sum_int(__popc(cand)) > __popc(__ballot_sync(QMOE_FULL_MASK, listed));
+            if (again && !d.any)
+                again = warp_sum_int(__popc(others(a, row, e0, cand, d.last_id))) >
+                        __popc(__ballot_sync(QMOE_FULL_MASK, listed && !comes_after(a, row, d.last_id, at)));
             if (!again && d.any) {
                 at = exact_order(a, row, __popc(__ballot_sync(QMOE_FULL_MASK, in_list)), value_of(mk), at, d.mine, top, z, sum_error(R));
                 again = at < 0;
@@ -1125,7 +1134,7 @@ __global__ void __launch_bounds__(kWideWarps * 32, R <= 16 ? 10 : R <= 32 ? 5 : 
                     bool open = false;      // something that is left may belong to the chosen
 #pragma unroll
                     for (int i = 0; i < MOST; ++i)
-                        if (key[i] && !(value_of(key[i]) < d.least) && !comes_after(a, row, d, id[i])) open = true;
+                        if (key[i] && !(value_of(key[i]) < d.least) && !(!d.any && comes_after(a, row, d.last_id, id[i]))) open = true;
                     again = __any_sync(QMOE_FULL_MASK, open);
                     if (!again && d.any) {
                         at = exact_order(a, row, __popc(__ballot_sync(QMOE_FULL_MASK, in_list)), value_of(mk), at, d.mine, top, z, sum_error(R));
