@@ -742,7 +742,8 @@ __device__ __forceinline__ void write_route(const RouteArgs& a, int64_t t, int i
 }
 
 // Which of the list that the lanes hold, largest first, are too near to tell apart (key mk of expert at, whose logit is l; one
-// entry more than are chosen, where there is one).  Two neighbours of the same logit and bias are no doubt; where they are the last one
+// entry more than are chosen, where there is one).  Two neighbours of the same logit and bias are no doubt if they stand by index (the
+// scores of one logit may differ in their last bits from warp to warp of wide_route_kernel, whose factors do).  Where they are the last one
 // chosen and the one behind it, what stands behind both may still be larger than they are, and only what equals them may not.
 struct Doubts {
     bool behind;     // some two neighbours, or what is behind the list has to be looked at (else nothing below is set)
@@ -761,7 +762,7 @@ __device__ __forceinline__ Doubts doubts_of(const RouteArgs& a, uint32_t mk, int
     if (lane < a.k && lane < 31 && mk && nk) {
         const float nv = value_of(nk);
         near = fabsf(v) < INFINITY && nv > -INFINITY ? v - nv <= 2.f * slack + kUlp * (fabsf(v) + fabsf(nv)) : v == nv;
-        if (near) doubt = !(l == nl && a.bias[at] == a.bias[nat]), ask = doubt || lane == a.k - 1;
+        if (near) doubt = !(l == nl && a.bias[at] == a.bias[nat] && at < nat), ask = doubt || lane == a.k - 1;
     }
     Doubts d{};
     d.behind = __any_sync(QMOE_FULL_MASK, ask) || a.k == 32;
@@ -1103,33 +1104,47 @@ __global__ void __launch_bounds__(kWideWarps * 32, R <= 16 ? 10 : R <= 32 ? 5 : 
             uint32_t key[MOST], mk = 0;
             int id[MOST];
             const int mine_n = (n + 31) / 32;
+            bool in_list = false;
+            auto take = [&]() {
+                for (int j = 0; j < rounds; ++j) {
+                    uint32_t best = key[0];
+                    int e = id[0];
+                    if (mine_n > 1) {
+#pragma unroll
+                        for (int i = 1; i < MOST; ++i)
+                            if (key[i] > best || (key[i] == best && id[i] < e)) best = key[i], e = id[i];
+                    }
+                    const uint32_t m = __reduce_max_sync(QMOE_FULL_MASK, best);
+                    const int first = (int)__reduce_min_sync(QMOE_FULL_MASK, best == m ? (unsigned)e : 0xFFFFFFFFu);
+                    if (lane == j) mk = m, at = first;
+#pragma unroll
+                    for (int i = 0; i < MOST; ++i) {
+                        if (i > 0 && mine_n == 1) break;
+                        if (key[i] == m && id[i] == first) key[i] = 0;
+                    }
+                }
+                in_list = lane < rounds && mk;
+                if (!in_list) at = 0;
+                l = in_list ? logit(row, at) : -INFINITY;
+            };
 #pragma unroll
             for (int i = 0; i < MOST; ++i) {
                 key[i] = 0, id[i] = 0;
                 if (i * 32 + lane < n) key[i] = key_s[i * 32 + lane], id[i] = id_s[i * 32 + lane];
             }
-            for (int j = 0; j < rounds; ++j) {
-                uint32_t best = key[0];
-                int e = id[0];
-                if (mine_n > 1) {
-#pragma unroll
-                    for (int i = 1; i < MOST; ++i)
-                        if (key[i] > best || (key[i] == best && id[i] < e)) best = key[i], e = id[i];
-                }
-                const uint32_t m = __reduce_max_sync(QMOE_FULL_MASK, best);
-                const int first = (int)__reduce_min_sync(QMOE_FULL_MASK, best == m ? (unsigned)e : 0xFFFFFFFFu);
-                if (lane == j) mk = m, at = first;
-#pragma unroll
-                for (int i = 0; i < MOST; ++i) {
-                    if (i > 0 && mine_n == 1) break;
-                    if (key[i] == m && id[i] == first) key[i] = 0;
-                }
-            }
-            const bool in_list = lane < rounds && mk;
-            if (!in_list) at = 0;
-            if (in_list) l = logit(row, at);
+            take();
             if (!by_logit) {
-                const Doubts d = doubts_of(a, mk, at, l, slack, lane);
+                Doubts d = doubts_of(a, mk, at, l, slack, lane);
+                if (__builtin_expect(d.behind && !a.sigmoid, 0)) {
+                    // the listed values again, each by the block's largest logit and sum alone: what has the same logit and bias has the same
+                    // bits, whichever warp it came from, and stands by index (what is not in the list is smaller for certain)
+#pragma unroll
+                    for (int i = 0; i < MOST; ++i)
+                        if (i * 32 + lane < n) key[i] = key_of(fmaxf(fmaf(ex2(kLog2e * (logit(row, id[i]) - top)), inv_z, a.bias[id[i]]), -INFINITY));
+                    mk = 0;
+                    take();
+                    d = doubts_of(a, mk, at, l, slack, lane);
+                }
                 if (__builtin_expect(d.behind, 0)) {
                     bool open = false;      // something that is left may belong to the chosen
 #pragma unroll

@@ -2,6 +2,9 @@
 import numpy as np
 import pytest
 
+import synth
+
+from test_gpu_kv4 import bits
 from test_gpu_layer import check_route
 
 torch = pytest.importorskip("torch")
@@ -44,3 +47,14 @@ def test_route_equal_values_at_the_border_hide_no_better_one(E, groups):
     check_route(l, min(4, E // groups), False, sigmoid=True, bias=np.full(E, 0.25), **kw)
     l[:, 0] = 1.0
     check_route(l, min(4, E // groups), False, bias=np.where(np.arange(E) == 0, -1.0, 0.25), **kw)
+
+
+# ------------------------------------------------------------------ router: the same logit in several warps
+@pytest.mark.parametrize("E,T", [(257, 150), (300, 150), (512, 150), (1000, 100), (2048, 100), (4100, 60), (8192, 60)])
+@pytest.mark.parametrize("k", [1, 2, 8, 31, 32])
+def test_route_equal_logits_go_to_the_lower_expert_in_a_softmax_of_many(E, T, k):
+    r = np.random.RandomState(E + k)
+    l = synth.bf16_to_f64(bits(r.randn(T, E) * 2))             # bf16 logits repeat, and their largest differ from part to part
+    check_route(l, k, False, bias=np.zeros(E))
+    check_route(l, k, True, pad=3, bias=0.001 * r.randint(-1, 2, E), renormalise=True)
+    check_route(np.round(l[:40]), k, False, bias=0.25 * r.randint(0, 2, E))
