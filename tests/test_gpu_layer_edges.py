@@ -1,11 +1,12 @@
-"""GPU parity of the scored router with the float64 oracle where equal values meet."""
+"""GPU parity of the scored router and the row norm with the float64 oracle: equal values, and every form of their kernels."""
 import numpy as np
 import pytest
 
 import synth
+from oracle import layer as Y
 
-from test_gpu_kv4 import bits
-from test_gpu_layer import check_route
+from test_gpu_kv4 import bits, ok
+from test_gpu_layer import DEV, U32, check_norm, check_route, f64, norm_inputs, norm_tolerance
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -58,3 +59,43 @@ def test_route_equal_logits_go_to_the_lower_expert_in_a_softmax_of_many(E, T, k)
     check_route(l, k, False, bias=np.zeros(E))
     check_route(l, k, True, pad=3, bias=0.001 * r.randint(-1, 2, E), renormalise=True)
     check_route(np.round(l[:40]), k, False, bias=0.25 * r.randint(0, 2, E))
+
+
+# ------------------------------------------------------------------ row norm: one to four steps a lane, one to 32 warps a row
+@pytest.mark.parametrize("T,n", [(1300, 2048), (1300, 2080), (1300, 520), (1300, 1032), (1217, 4096), (2, 5136), (5, 5376), (3, 8192), (1300, 8192), (2, 16392), (3, 24584)])
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("f32", [False, True])
+def test_norm_in_8_bits_of_many_and_of_wide_rows(T, n, group, f32):
+    xt, x, rt, res, wt, w = norm_inputs(T, n, f32, True, n + T)
+    groups, width = (-(-n // 128), 128) if group else (1, n)
+
+    def call():
+        y, out = torch.full((T, n), 3.0, dtype=torch.bfloat16, device=DEV), torch.full((T, n), 3.0, dtype=torch.bfloat16, device=DEV)
+        codes, scales = torch.full((T, n), 0xAA, dtype=torch.uint8, device=DEV), torch.full((T, groups), -1.0, device=DEV)
+        Q.add_rms_norm(xt, wt, 1e-5, y, residual=rt, residual_out=out, codes=codes, scales=scales)
+        ok()
+        return y, out, codes, scales
+    y, out, codes, scales = call()
+    ref = Y.add_norm(x, res, w, 1e-5)[1]
+    check_norm(f64(y), ref)
+    assert torch.equal(out, (xt.float() + rt.float()).to(torch.bfloat16))
+    got, c = f64(scales), Y.e4m3(codes.cpu().numpy())
+    s = Y.scales(ref, group)
+    # the largest |y| with norm_tolerance's error, and a quotient
+    assert (np.abs(got - s) <= 64 * U32 * s).all()
+    unit = np.repeat(got, width, 1)[:, :n]
+    # half a step of 3 fraction bits, or of the smallest step 2^-9 s; the reciprocal's and the value's own fp32 errors
+    assert (np.abs(c * unit - ref) <= 2.0 ** -4 * np.abs(ref) * (1 + 2.0 ** -16) + 2.0 ** -10 * unit + norm_tolerance(ref, n)).all()
+    assert all((np.abs(c[:, i:i + width]).max(1) == 448).all() for i in range(0, n, width))
+    for a, b in zip(call(), (y, out, codes, scales)):          # the same bits again
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,n", [(1300, 129), (1300, 1001), (2, 1025), (3, 4096), (2, 4099), (1300, 4097)])
+def test_norm_of_many_and_of_wide_rows_without_wide_loads(T, n):
+    xt, x, rt, res, wt, w = norm_inputs(T, n + 1, False, True, n)          # rows begin at odd places
+    y, out = (torch.full((T, n), 3.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    Q.add_rms_norm(xt[:, 1:], wt[1:].clone(), 1e-5, y, residual=rt[:, :n], residual_out=out)
+    ok()
+    check_norm(f64(y), Y.add_norm(x[:, 1:], res[:, :n], w[1:], 1e-5)[1])
+    assert torch.equal(out, (xt[:, 1:].float() + rt[:, :n].float()).to(torch.bfloat16))
