@@ -1176,7 +1176,7 @@ __global__ void __launch_bounds__(kWideWarps * 32, R <= 16 ? 10 : R <= 32 ? 5 : 
 
 template <typename X>
 int launch_route(const RouteArgs& a, cudaStream_t st) {
-    const unsigned per_warp = (unsigned)((a.T + kTokenWarps - 1) / kTokenWarps), tokens = (unsigned)a.T;
+    const unsigned per_warp = ((unsigned)a.T + kTokenWarps - 1) / kTokenWarps, tokens = (unsigned)a.T;      // (T may be the largest int)
     constexpr int threads = kTokenWarps * 32, wide = kWideWarps * 32;
     auto launch = [&](void (*kernel)(RouteArgs), unsigned blocks, int n) { return launch_rows(kernel, a.T, blocks, n, st, "qmoe_route_scored", a); };
     if (a.E <= 32) return launch(route_kernel<X, 1>, per_warp, threads);

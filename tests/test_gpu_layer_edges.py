@@ -99,3 +99,16 @@ def test_norm_of_many_and_of_wide_rows_without_wide_loads(T, n):
     ok()
     check_norm(f64(y), Y.add_norm(x[:, 1:], res[:, :n], w[1:], 1e-5)[1])
     assert torch.equal(out, (xt[:, 1:].float() + rt[:, :n].float()).to(torch.bfloat16))
+
+
+# ------------------------------------------------------------------ as many rows as an int holds
+def test_route_of_the_largest_number_of_tokens():
+    T = 2 ** 31 - 1
+    logits = torch.zeros((T, 1), dtype=torch.bfloat16, device=DEV)
+    ids, gates = torch.full((T, 1), -9, dtype=torch.int32, device=DEV), torch.zeros((T, 1), device=DEV)
+    Q.qmoe_route_scored(logits, 1, ids, gates, sigmoid=True, scale=3.0)
+    ok()
+    assert ids.max().item() == 0 == ids.min().item()
+    assert gates.max().item() == 1.5 == gates.min().item()          # 3 / (1 + e^0)
+    del logits, ids, gates
+    torch.cuda.empty_cache()
