@@ -462,7 +462,8 @@ __global__ void __launch_bounds__(WARPS == 1 ? kPickThreads : WARPS * 32) pick_k
             n1 = warp_sum_int(n1), n2 = warp_sum_int(n2), n3 = warp_sum_int(n3);
         }
         if (WARPS > 1) {
-            // 21 bits each (a list chooses from at most 2^21 - 1 blocks, kMostBlocks)
+            // 21 bits each: a list chooses from at most kMostBlocks blocks
+            static_assert(kMostBlocks < 1 << 21, "a count has 21 bits");
             if (lane == 0) count_s[turn][warp] = (unsigned long long)n1 | (unsigned long long)n2 << 21 | (unsigned long long)n3 << 42;
             __syncthreads();
             const unsigned long long v = lane < WARPS ? count_s[turn][lane] : 0ull;
