@@ -742,8 +742,10 @@ typedef struct {
  * Bring the bounds up to date after tokens were written to the cache at slots (device int32 [n], -1
  * skips): the bounds of each page among them, over its tokens up to the last written one, are made
  * from the cache.  slots as kv4_block_tables gives them: the tokens of a page next to each other, in
- * order and without a gap (else the page's bounds are those up to one of its written tokens).  Errors: EINVAL (other sizes than the cache's); on the device EINVAL (a slot outside the
- * cache: skipped).
+ * order and without a gap.  A page whose tokens stand otherwise (or in two calls that run at the same
+ * time) gets a mix of what each run of them gives, which bounds nothing, until a call brings it up to
+ * date from its last token; the other pages are not touched by that.
+ * Errors: EINVAL (other sizes than the cache's); on the device EINVAL (a slot outside the cache: skipped).
  */
 int kv4_block_bounds(const kv4_cache* cache, const kv4_bounds* bounds, const int32_t* slots, int n, void* stream);
 
@@ -757,7 +759,8 @@ int kv4_block_bounds(const kv4_cache* cache, const kv4_bounds* bounds, const int
  * times the power of two that brings the group's largest magnitude into [2^(b-1), 2^b), rounded
  * (nearest even) and kept within +-(2^b - 1), with b = 15 - ceil(log2(heads per kv head)); NaN is read as 0, an infinity as the largest
  * finite value.  The sum is exact; it is rounded once to fp32, and so is its product with step.
- *  q, q_start, kv_len, table, max_kv  as in kv4_attention.
+ *  q, q_start, kv_len, table, max_kv  as in kv4_attention (a q_start out of order is not looked for here: a
+ *          row is of the request whose range holds it).
  *  sel     device out int32 [n_q_tokens][n_kv_heads][top]: block numbers, ascending, then -1.  A query
  *          that sees top blocks or fewer has them all.
  *  top     1 .. 65536;  first, last >= 0, first + last <= top;  max_kv at most 2^20 pages.
@@ -782,7 +785,7 @@ int kv4_select_blocks(const kv4_bounds* bounds, const void* q, int n_q_tokens, i
  *  workspace  device, ws_bytes >= kv4_attention_blocks_ws_size(...), 16-byte aligned; not shared by
  *          calls that may run at the same time.
  * The other arguments, the arithmetic (that of requests with few query rows) and the rows that are left as they are: as in
- * kv4_attention with causal.
+ * kv4_attention with causal; a q_start out of order is not looked for, as in kv4_select_blocks.
  * Errors: EINVAL, EUNSUPPORTED (head_dim, more than 32 query heads per kv head), ECAPACITY; on the
  * device EINVAL (a listed block without a page in the cache: its tokens are not seen; an entry below -1; a
  * kv_len that is negative or above 2^31 - 128: its rows are skipped).
