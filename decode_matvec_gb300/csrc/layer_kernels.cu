@@ -795,7 +795,7 @@ __device__ __noinline__ uint32_t others(const RouteArgs& a, const X* row, int e0
 }
 
 // R experts a lane, a warp a token.  Instructions bound it, and the latency of a round (a reduction, a ballot, a list that moves up): 16383
-// tokens of 256 experts in 8 groups, the best 8 by sigmoid scores and a bias, 16.3 us and 790 instructions a token, 66 % of the
+// tokens of 256 experts in 8 groups, the best 8 by sigmoid scores and a bias, 16.4 us and 795 instructions a token, 65 % of the
 // issue slots; 32 tokens 3.6 to 4.2 us.  A warp that goes on to another token with its logits loaded ahead took 19 us.
 template <typename X, int R>
 __global__ void __launch_bounds__(kTokenWarps * 32, R <= 8 ? 8 : 4) route_kernel(RouteArgs a) {
@@ -960,7 +960,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32, R <= 8 ? 8 : 4) route_kernel
 // Many experts without groups: a block of 4 warps a token, R values a thread in loads that stand side by side.  In each warp
 // the `rounds`-th largest of the lanes' maxima bounds the values to look at from below, and the largest of the warps' bounds
 // does for all; the few values that reach it are put side by side in shared memory, and the first warp's rounds go over
-// those, by key and index.  The three barriers of a row bound it: 4096 tokens of 2048 fp32 logits, 2 by softmax and a bias, 17.5 us, 1.9 TB/s,
+// those, by key and index.  The three barriers of a row bound it: 4096 tokens of 2048 fp32 logits, 2 by softmax and a bias, 17.7 us, 1.9 TB/s,
 // 51 % of the issue slots (a warp a token 21 to 23 us).
 constexpr int kWideMost = 256;      // values put side by side; rows with more (many equal ones) take exact_choice
 
