@@ -1,11 +1,13 @@
-"""GPU parity of the scored router and the row norm with the float64 oracle: equal values, and every form of their kernels."""
+"""GPU parity with the float64 oracle: the scored router where equal values meet, every form of the row norm, and the example's steps over
+chosen blocks."""
 import numpy as np
 import pytest
 
 import synth
 from oracle import layer as Y
 
-from test_gpu_kv4 import bits, ok
+from test_gpu_decoder_layer import _example
+from test_gpu_kv4 import bits, check, ok
 from test_gpu_layer import DEV, U32, check_norm, check_route, f64, norm_inputs, norm_tolerance
 
 torch = pytest.importorskip("torch")
@@ -48,6 +50,24 @@ def test_route_equal_values_at_the_border_hide_no_better_one(E, groups):
     check_route(l, min(4, E // groups), False, sigmoid=True, bias=np.full(E, 0.25), **kw)
     l[:, 0] = 1.0
     check_route(l, min(4, E // groups), False, bias=np.where(np.arange(E) == 0, -1.0, 0.25), **kw)
+
+
+@pytest.mark.parametrize("E", [3, 256, 300, 2048])
+def test_route_repeated_logits_of_saturated_and_of_peaked_rows(E):
+    r = np.random.RandomState(E)
+    k = min(8, E - 1)
+    check_route(r.uniform(12, 30, (40, E)), k, False, sigmoid=True, bias=np.zeros(E))
+    l = np.round(2 * r.randn(40, E))
+    l[np.arange(40), r.randint(0, E, 40)] = 60                  # one score next to 1, the others far below its rounding
+    check_route(l, 1, False, bias=np.zeros(E))
+    check_route(l, k, False, bias=np.zeros(E), renormalise=True)
+    check_route(l, k, False, bias=np.full(E, 0.125))
+    l[:] = 0.5                                                  # all the same
+    check_route(l[:3], k, False, bias=np.zeros(E))
+    check_route(l[:3], k, False, sigmoid=True, bias=0.5 * r.randint(0, 2, E))
+    l[:, E // 2:] = -np.inf                                     # masked experts, fewer than k left
+    check_route(l[:3], max(1, k), False, bias=np.zeros(E))
+    check_route(l[:3], min(32, E), False, sigmoid=True, bias=np.where(np.arange(E) % 3, 0.0, -np.inf), renormalise=True)
 
 
 # ------------------------------------------------------------------ router: the same logit in several warps
@@ -112,3 +132,39 @@ def test_route_of_the_largest_number_of_tokens():
     assert gates.max().item() == 1.5 == gates.min().item()          # 3 / (1 + e^0)
     del logits, ids, gates
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ the example's layer for long contexts
+def test_steps_attend_to_the_blocks_that_the_oracle_chooses():
+    """Decode steps of the small layer, eager and replayed: the lists and the attention over them against the float64 restatement."""
+    ex, top = _example(), 2
+    prompts, P, hkv, D = [70, 1, 33], 16, 2, 64
+    layer = ex.Layer(4, hkv, D, 4, 256, 2, n_pages=64, page_size=P, max_blocks=16, max_batch=3, top_blocks=top)
+    g = torch.Generator("cuda").manual_seed(5)
+
+    def tokens(n):
+        return torch.randn((n, layer.d), generator=g, device="cuda").to(torch.bfloat16)
+    ex.Step(layer, prompts, 80)(tokens(sum(prompts)))
+    step, x = ex.Step(layer, [1] * 3, 80), tokens(3)
+
+    def look():
+        torch.cuda.synchronize()
+        assert ex.Q.qmoe_check_status() == ex.Q.QMOE_OK
+        kv, table = step.kv_len.cpu().numpy(), layer.table.cpu().numpy()
+        ref = Y.select(f64(step.q), np.arange(4), kv, table, layer.bounds.codes.cpu().numpy(), f64(layer.bounds.steps), P, top, 1, 1, np.zeros((3, hkv, top), int), 80)
+        assert np.array_equal(step.sel.cpu().numpy(), ref)
+        check(f64(step.att), *Y.attention_blocks(f64(step.q), np.arange(4), kv, table, layer.cache.pages.cpu().numpy(), P, hkv, ref, D ** -0.5))
+        return kv.tolist()
+    step(x)
+    assert look() == [71, 2, 34]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step(x)
+    torch.cuda.current_stream().wait_stream(stream)
+    for i in range(4):
+        x.copy_(tokens(3))
+        graph.replay()
+        assert look() == [72 + i, 3 + i, 35 + i]
